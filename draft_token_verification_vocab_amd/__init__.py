@@ -9,6 +9,7 @@ of the computation runs in the library's kernels; there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -18,7 +19,7 @@ import torch
 
 __all__ = [
     "SpecVerifyError", "lib_path", "load", "verify", "av_score", "av_score_stats", "av_update",
-    "row_stats",
+    "row_stats", "row_topk",
     "workspace_bytes", "draft_stats_bytes", "MODE_LOSSLESS", "MODE_FLY",
 ]
 
@@ -98,6 +99,11 @@ _SIGNATURES = {
     "spec_ngram_propose": (ctypes.c_int32, [_P, _P, ctypes.c_int32, ctypes.c_int64,
                                             ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _P, _P,
                                             _P, _P, _P]),
+    "spec_row_topk_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int32,
+                                                        ctypes.c_int32, ctypes.c_int32]),
+    "spec_row_topk": (ctypes.c_int32, [_P, ctypes.c_int64, ctypes.c_int32, ctypes.c_int64,
+                                       ctypes.c_int32, ctypes.c_float, ctypes.c_int32, _P, _P, _P,
+                                       _P, ctypes.c_size_t, _P]),
     "spec_status_string": (ctypes.c_char_p, [ctypes.c_int32]),
 }
 
@@ -703,4 +709,48 @@ def ngram_propose(context: torch.Tensor, lengths: torch.Tensor, n_min: int, n_ma
                                      int(n_max), int(K), _ptr(res["draft"]),
                                      _ptr(res["draft_len"]), _ptr(res["match_pos"]),
                                      _ptr(res["match_n"]), _stream(dev)), "spec_ngram_propose")
+    return res
+
+
+# ---------------------------------------------------------------------------
+# Draft-model calls: top-logit lists, distillation, beam search
+# ---------------------------------------------------------------------------
+@contextlib.contextmanager
+def _on(device: torch.device):
+    """The device current for a call's launches, as the library expects."""
+    if device.index == torch.cuda.current_device():
+        yield
+    else:
+        with torch.cuda.device(device):
+            yield
+
+
+def row_topk(logits: torch.Tensor, k: int, *, temperature: float = 1.0,
+             vocab: Optional[int] = None, lse: bool = True,
+             workspace: Optional[torch.Tensor] = None) -> dict:
+    """The k largest logits of each row of a [..., S] tensor (first V columns)
+    in decreasing order, equal values by lowest id: values (float32 [..., k]),
+    ids (int32 [..., k]; -inf and -1 past a row's visible entries) and lse
+    (float32 [...], ln sum e^(l/T) over the whole row; lse=False leaves it out)."""
+    _need_cuda(logits, "logits")
+    S = logits.shape[-1]
+    V = S if vocab is None else int(vocab)
+    k = int(k)
+    lead, dev, dt = logits.shape[:-1], logits.device, _dtype_code(logits)
+    rows = logits.numel() // S if S else 0
+    L = load()
+    res = {"values": torch.empty(lead + (max(k, 0),), dtype=torch.float32, device=dev),
+           "ids": torch.empty(lead + (max(k, 0),), dtype=torch.int32, device=dev)}
+    if lse:
+        res["lse"] = torch.empty(lead, dtype=torch.float32, device=dev)
+    if workspace is None:
+        n = L.spec_row_topk_workspace_bytes(rows, V, dt, k)
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+    else:
+        _need_cuda(workspace, "workspace", dev)
+    with _on(dev):
+        _check(L.spec_row_topk(_ptr(logits), rows, V, S, dt, float(temperature), k,
+                               _ptr(res["values"]), _ptr(res["ids"]), _ptr(res.get("lse")),
+                               _ptr(workspace), 0 if workspace is None else _nbytes(workspace),
+                               _stream(dev)), "spec_row_topk")
     return res

@@ -16,7 +16,8 @@ ROOT = os.path.dirname(HERE)
 LIB_NAME = "libspecverify.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 SOURCES = [os.path.join(HERE, "csrc", "specverify.hip"),
-           os.path.join(HERE, "csrc", "specverify_noalloc.hip")]
+           os.path.join(HERE, "csrc", "specverify_noalloc.hip"),
+           os.path.join(HERE, "csrc", "specverify_draft.hip")]
 ARCH = os.environ.get("SPECVERIFY_ARCH", "gfx950")
 
 

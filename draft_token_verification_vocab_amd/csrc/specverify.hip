@@ -11,6 +11,7 @@
 #include "sv_av.hpp"
 #include "sv_common.hpp"
 #include "sv_finish.hpp"
+#include "sv_host.hpp"
 #include "sv_next.hpp"
 #include "sv_rowstats.hpp"
 #include "sv_step.hpp"
@@ -45,10 +46,6 @@ constexpr int kDiagMaxBins = 64;
 // Prompt lookup: one workgroup per sequence.
 constexpr int kNgramBlock = 256;
 constexpr int kNgramUnroll = 8;
-
-size_t align_up(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
-
-int elem_size(int32_t dtype) { return dtype == SPEC_DTYPE_F32 ? 4 : 2; }
 
 int race_segments(int32_t B, int32_t V) {
     if (B <= 0) return 1;
@@ -100,18 +97,6 @@ DraftStats draft_stats_view(void *p, size_t n) {
                       reinterpret_cast<float *>(c + 16 * n), reinterpret_cast<float *>(c + 20 * n)};
 }
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-spec_status check_logits_shape(int32_t V, int64_t stride, int32_t dtype, float temperature) {
-    if (dtype != SPEC_DTYPE_F32 && dtype != SPEC_DTYPE_BF16) return SPEC_ERR_ARG;
-    if (V < 2 || stride < V) return SPEC_ERR_ARG;
-    if ((stride * elem_size(dtype)) % 16 != 0) return SPEC_ERR_ARG;
-    // rows are addressed with 32-bit byte offsets
-    if (static_cast<int64_t>(V) * elem_size(dtype) > INT32_MAX) return SPEC_ERR_UNSUPPORTED;
-    if (!(temperature >= 1e-4f && temperature <= 1e4f)) return SPEC_ERR_ARG;
-    return SPEC_OK;
-}
-
 spec_status check_params(const spec_params *p) {
     if (!p) return SPEC_ERR_ARG;
     if (p->batch < 0 || p->num_draft < 1 || p->reserved != 0) return SPEC_ERR_ARG;
@@ -121,10 +106,6 @@ spec_status check_params(const spec_params *p) {
     // all row indices and b*(K+1)+j products must fit in int32
     if (static_cast<int64_t>(p->batch) * (2 * p->num_draft + 1) > INT32_MAX) return SPEC_ERR_UNSUPPORTED;
     return SPEC_OK;
-}
-
-spec_status launch_status() {
-    return hipGetLastError() == hipSuccess ? SPEC_OK : SPEC_ERR_HIP;
 }
 
 // ---------------------------------------------------------------------------
@@ -176,8 +157,6 @@ RowGroup empty_group() {
     g.rows_per_seq = 1;
     return g;
 }
-
-float log2e_over(float temperature) { return kLog2e / temperature; }
 
 }  // namespace
 

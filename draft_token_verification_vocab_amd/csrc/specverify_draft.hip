@@ -1,0 +1,173 @@
+// specverify_draft.hip -- host side of the draft-model calls declared in
+// include/specverify.h: listing rows' top logits.  Argument validation,
+// workspace layout, kernel selection and launches on the caller's stream.  No
+// allocation, no synchronisation.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstddef>
+#include <cstdint>
+
+#include "specverify.h"
+#include "sv_common.hpp"
+#include "sv_host.hpp"
+#include "sv_topk.hpp"
+
+namespace {
+
+using namespace sv;
+
+// A grid's threads must stay below 2^32.
+bool grid_fits(int64_t blocks, int block) {
+    return blocks <= (int64_t{1} << 32) / block - 1 && blocks <= INT32_MAX;
+}
+
+// How the rows of a listing are cut into workgroups.
+//   Many rows: a workgroup per row (the row pass's shapes), as long as the
+// chunk maxima of a row fit its LDS (kWideChunks chunks: V <= 294912 in
+// bfloat16, 131072 in float32), else as many equal segments as that takes.
+//   Few rows: smaller workgroups, each row cut into segments until the GPU is
+// filled or a segment is one chunk.
+constexpr int kFillRows = 256;     // compute units
+constexpr int kSplitBlocks = 1024; // workgroups to aim for with few rows
+constexpr int kMaxMerge = 4096;    // keys one merge holds in LDS
+constexpr int kMaxListSegs = 64;   // one lane per segment in a merge
+constexpr int kSplitBlock = 256;
+constexpr int kMergeBlock = 256;
+
+template <typename T>
+struct WideShape;
+template <>
+struct WideShape<uint16_t> {
+    static constexpr int block = 768, unroll = 2, chunks = 24;
+};
+template <>
+struct WideShape<float> {
+    static constexpr int block = 512, unroll = 4, chunks = 16;
+};
+
+struct ListPlan {
+    bool wide;
+    int segs, seg_vecs, chunks;
+    size_t list, seg_lse, total;  // workspace offsets
+};
+
+// lists: joined by one merge, each of k keys per segment (a row's own, or
+// those of a sequence's beams).  keep_lists: the lists go to the workspace
+// even with one segment per row.
+template <typename T>
+ListPlan plan_lists_t(int64_t rows, int32_t V, int32_t k, int32_t lists, bool keep_lists) {
+    using S = WideShape<T>;
+    constexpr int epv = 16 / sizeof(T);
+    constexpr int wide_chunk = S::block * S::unroll, split_chunk = kSplitBlock * S::unroll;
+    const int nvec = (V + epv - 1) / epv;
+    const int need = (nvec + wide_chunk * S::chunks - 1) / (wide_chunk * S::chunks);
+    const int most = kMaxMerge / (lists * k) < kMaxListSegs ? kMaxMerge / (lists * k) : kMaxListSegs;
+    ListPlan p{};
+    int64_t want = rows > 0 ? (kSplitBlocks + rows - 1) / rows : 1;
+    const int by_len = (nvec + split_chunk - 1) / split_chunk;
+    if (want > by_len) want = by_len;
+    if (want > most) want = most;
+    p.wide = rows >= kFillRows || want < 2;
+    p.segs = p.wide ? need : static_cast<int>(want);
+    // a split segment holds at most kWideChunks of the wide shape's bytes
+    const int chunk = p.wide ? wide_chunk : split_chunk;
+    int per = ((nvec + p.segs - 1) / p.segs + chunk - 1) / chunk;
+    if (!p.wide && per > 2 * S::chunks) {  // too long for a split segment's LDS
+        p.wide = true;
+        p.segs = need;
+        per = ((nvec + p.segs - 1) / p.segs + wide_chunk - 1) / wide_chunk;
+    }
+    p.chunks = per;
+    p.seg_vecs = per * (p.wide ? wide_chunk : split_chunk);
+    p.segs = (nvec + p.seg_vecs - 1) / p.seg_vecs;
+    if (p.segs > 1 || keep_lists) {
+        const size_t n = static_cast<size_t>(rows) * p.segs;
+        p.list = 0;
+        p.seg_lse = align_up(8 * n * static_cast<size_t>(k));
+        p.total = align_up(p.seg_lse + 8 * n);
+    }
+    return p;
+}
+
+ListPlan plan_lists(int64_t rows, int32_t V, int32_t dtype, int32_t k, int32_t lists,
+                    bool keep_lists) {
+    return dtype == SPEC_DTYPE_BF16 ? plan_lists_t<uint16_t>(rows, V, k, lists, keep_lists)
+                                    : plan_lists_t<float>(rows, V, k, lists, keep_lists);
+}
+
+template <typename T>
+void launch_lists_t(const ListPlan &p, const TopkArgs &a, int64_t rows, hipStream_t st) {
+    using S = WideShape<T>;
+    const dim3 grid(static_cast<unsigned>(rows * p.segs));
+    const size_t cell = sizeof(typename ChunkMax<T>::type);
+    if (p.wide)
+        topk_rows_kernel<T, S::block, S::unroll>
+            <<<grid, dim3(S::block), p.chunks * S::block * cell, st>>>(a);
+    else
+        topk_rows_kernel<T, kSplitBlock, S::unroll>
+            <<<grid, dim3(kSplitBlock), p.chunks * kSplitBlock * cell, st>>>(a);
+}
+
+void launch_lists(const ListPlan &p, const TopkArgs &a, int64_t rows, int32_t dtype,
+                  hipStream_t st) {
+    if (dtype == SPEC_DTYPE_BF16)
+        launch_lists_t<uint16_t>(p, a, rows, st);
+    else
+        launch_lists_t<float>(p, a, rows, st);
+}
+
+constexpr int32_t kMaxListVocab = 1 << 20;
+
+}  // namespace
+
+extern "C" {
+
+size_t spec_row_topk_workspace_bytes(int64_t rows, int32_t vocab, int32_t dtype, int32_t k) {
+    if (rows < 1 || vocab < 2 || vocab > kMaxListVocab || k < 1 || k > kTopkMax ||
+        (dtype != SPEC_DTYPE_F32 && dtype != SPEC_DTYPE_BF16))
+        return 0;
+    return plan_lists(rows, vocab, dtype, k, 1, false).total;
+}
+
+spec_status spec_row_topk(const void *logits, int64_t rows, int32_t vocab, int64_t row_stride,
+                          int32_t dtype, float temperature, int32_t k, float *values,
+                          int32_t *ids, float *lse, void *workspace, size_t workspace_bytes,
+                          void *stream) {
+    spec_status s = check_logits_shape(vocab, row_stride, dtype, temperature);
+    if (s != SPEC_OK) return s;
+    if (rows < 0 || k < 1) return SPEC_ERR_ARG;
+    if (k > kTopkMax || vocab > kMaxListVocab) return SPEC_ERR_UNSUPPORTED;
+    if (rows == 0) return SPEC_OK;
+    if (!logits || !aligned16(logits) || !values || !ids) return SPEC_ERR_ARG;
+    if (rows > INT32_MAX) return SPEC_ERR_UNSUPPORTED;
+    const ListPlan p = plan_lists(rows, vocab, dtype, k, 1, false);
+    if (!grid_fits(rows * p.segs, 1024)) return SPEC_ERR_UNSUPPORTED;
+    if (p.total && (!workspace || workspace_bytes < p.total)) return SPEC_ERR_WORKSPACE;
+    if (p.total && !aligned16(workspace)) return SPEC_ERR_ARG;
+    TopkArgs a{};
+    a.base = logits;
+    a.stride = row_stride;
+    a.V = vocab;
+    a.k = k;
+    a.segs = p.segs;
+    a.seg_vecs = p.seg_vecs;
+    a.c = log2e_over(temperature);
+    a.inv_t = 1.0 / static_cast<double>(temperature);
+    a.values = values;
+    a.ids = ids;
+    a.lse = lse;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (p.segs > 1) {
+        char *w = static_cast<char *>(workspace);
+        a.list = reinterpret_cast<unsigned long long *>(w + p.list);
+        a.seg_lse = reinterpret_cast<double *>(w + p.seg_lse);
+    }
+    launch_lists(p, a, rows, dtype, st);
+    if ((s = launch_status()) != SPEC_OK || p.segs == 1) return s;
+    topk_merge_kernel<kMergeBlock><<<dim3(static_cast<unsigned>(rows)), dim3(kMergeBlock),
+                                     sizeof(unsigned long long) * p.segs * k, st>>>(a);
+    return launch_status();
+}
+
+}  // extern "C"

@@ -1,0 +1,113 @@
+// sv_stream.hpp -- the walk over one logits row (or a segment of it) that the
+// draft-model kernels share: a workgroup reads the row's 16-byte vectors in
+// chunks of UNROLL vectors a thread, one chunk ahead of the arithmetic, and
+// hands every chunk to a functor.
+#pragma once
+
+#include "sv_common.hpp"
+
+namespace sv {
+
+// Logits at or below this are masked: probability zero, never listed.  The
+// value that replaces them where arithmetic must stay finite lies below it
+// and survives a rounding to bfloat16 (it is Elem<>::pad_word).
+constexpr float kMasked = kNoMax;
+
+// consume(buf, it): buf holds the thread's vectors of chunk `it`, vector u at
+// index it*UNROLL*BLOCK + u*BLOCK + tid of the segment [vbeg, vend); vectors
+// past the segment and entries past V are padding.  Threads without a vector
+// in the last chunk are not called for it.
+//
+// The loads are the row pass's: buffer-addressed non-temporal 16-byte loads
+// over the segment's full vectors, the next chunk issued before this chunk's
+// arithmetic, a ragged last vector read element by element.
+template <typename T, int BLOCK, int UNROLL, typename F>
+__device__ __forceinline__ void stream_vectors(const T *row, int vbeg, int vend, int V, int tid,
+                                               F &&consume) {
+    using E = Elem<T>;
+    constexpr int kChunk = UNROLL * BLOCK;
+    const int nfull = V / E::kPerVec;
+    const int nv = vend - vbeg;                            // vectors of the segment
+    const int nf = (vend < nfull ? vend : nfull) - vbeg;   // full ones among them
+    const int nit = nf / kChunk;
+    const buf_rsrc rs = make_rsrc(reinterpret_cast<const uint4 *>(row) + vbeg,
+                                  static_cast<uint32_t>(nf) * 16u);
+    const uint32_t pad = E::pad_word();
+    auto load_chunk = [&](uint4 (&buf)[UNROLL], int it) {
+        const uint32_t soff = static_cast<uint32_t>(it) * (kChunk * 16u);
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u)
+            buf[u] = load_stream_buf(rs, static_cast<uint32_t>(tid + u * BLOCK) * 16u, soff);
+    };
+    uint4 a[UNROLL], b[UNROLL];
+    if (nit > 0) {
+        load_chunk(a, 0);
+        for (int it = 0; it + 1 < nit; ++it) {
+            load_chunk(b, it + 1);
+            consume(a, it);
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u) a[u] = b[u];
+        }
+    }
+    const int v = nit * kChunk + tid;
+    const bool tail = v < nv;
+    if (tail) {
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) {
+            const int vi = v + u * BLOCK;
+            b[u] = make_uint4(pad, pad, pad, pad);
+            if (vi < nf)
+                b[u] = load_stream_buf(rs, static_cast<uint32_t>(vi) * 16u, 0u);
+            else if (vi < nv)
+                b[u] = E::partial(row, nfull, V);
+        }
+    }
+    if (nit > 0) consume(a, nit - 1);
+    if (tail) consume(b, nit);
+}
+
+// One thread's running maximum m and sum of 2^((x - m)*c) over the chunks it
+// is given (an online softmax in base 2).  The difference is formed before the
+// product, so the largest term is exactly 1 however large the logits are.
+// Sums within a thread are float: a few tens of chunk sums of one sign.
+struct OnlineSum {
+    float m = kMasked, s = 0.f;
+    // x: the chunk's N logits, cm their maximum.  NaN entries count as masked.
+    template <int N>
+    __device__ __forceinline__ void add(const float (&x)[N], float cm, float c) {
+        if (cm > m) {
+            s *= hw_exp2((m - cm) * c);
+            m = cm;
+        }
+        float s4[4];
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const float e = hw_exp2((x[k] - m) * c);
+            s4[k & 3] = k < 4 ? e : s4[k & 3] + e;
+        }
+        float cs = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+        if (!(cs == cs)) {  // a NaN entry: the chunk again without it
+            cs = 0.f;
+#pragma unroll
+            for (int k = 0; k < N; ++k) cs += x[k] > kMasked ? hw_exp2((x[k] - m) * c) : 0.f;
+        }
+        s += cs;
+    }
+    // The sum relative to another maximum M >= m.
+    __device__ __forceinline__ float at(float M, float c) const {
+        return s * hw_exp2((m - M) * c);
+    }
+};
+
+// Largest of a chunk's logits in a chain of three-input maxima (NaN entries
+// are passed over).
+template <int N>
+__device__ __forceinline__ float chunk_max(const float (&x)[N]) {
+    float cm = max3f(x[0], x[1], x[2]);
+#pragma unroll
+    for (int k = 3; k + 1 < N; k += 2) cm = max3f(cm, x[k], x[k + 1]);
+    if (N % 2 == 0) cm = max3f(cm, x[N - 1], x[N - 1]);
+    return cm;
+}
+
+}  // namespace sv

@@ -1,0 +1,359 @@
+// sv_topk.hpp -- the k largest logits of each row, in decreasing order with
+// equal values by lowest id, and the row's log-normaliser, in one pass.
+//
+// A logit and its id make one 64-bit key: the ordered bits of the value above
+// the complement of the id, so that "larger key" is "earlier in the list" and
+// no two keys are equal.
+//
+// One workgroup streams a row (or a segment of it).  The pass keeps, beside
+// the online softmax, only each thread's maximum of every chunk (16 logits),
+// in LDS.  The k-th largest of the threads' own maxima is then a lower bound
+// tau of the k-th largest logit: k threads hold a logit that large.  Few
+// chunks reach tau (about k), so they are read again, their logits at or
+// above tau are collected and sorted.  A row whose collection overflows (many
+// equal logits) is settled by a radix selection over the keys instead, which
+// reads the row once per key byte.
+#pragma once
+
+#include "sv_stream.hpp"
+
+namespace sv {
+
+constexpr int kTopkMax = 128;        // longest list
+constexpr int kTopkCollect = 1024;   // logits one workgroup can collect
+
+struct TopkArgs {
+    const void *base;
+    int64_t stride;          // elements between consecutive rows
+    int32_t V;
+    int32_t k;
+    int32_t segs;            // segments (workgroups) per row
+    int32_t seg_vecs;        // 16-byte vectors per segment
+    float c;                 // log2(e) / T
+    float pad_;
+    double inv_t;            // 1 / T
+    // one segment: the caller's outputs (lse nullable)
+    float *values;           // [rows][k]
+    int32_t *ids;            // [rows][k]
+    float *lse;              // [rows]
+    // lists for a merge: keys in decreasing order, 0 after the last
+    unsigned long long *list;  // [rows][segs][k], null: write the outputs above
+    double *seg_lse;           // [rows][segs] ln sum e^(l/T), -inf when all is masked
+    // rows that take no part (beam selection), both nullable
+    const uint8_t *ended;    // [rows]
+    const float *scores;     // [rows]: -inf takes no part
+};
+
+template <typename T>
+struct ChunkMax;  // how a chunk's maximum is kept in LDS (exactly)
+template <>
+struct ChunkMax<uint16_t> {
+    using type = uint16_t;
+    __device__ static uint16_t put(float m) {
+        return static_cast<uint16_t>(__float_as_uint(m) >> 16);
+    }
+    __device__ static float get(uint16_t v) {
+        return __uint_as_float(static_cast<uint32_t>(v) << 16);
+    }
+};
+template <>
+struct ChunkMax<float> {
+    using type = float;
+    __device__ static float put(float m) { return m; }
+    __device__ static float get(float v) { return v; }
+};
+
+__device__ __forceinline__ uint64_t topk_key(float x, int id) {
+    return (static_cast<uint64_t>(ordered_bits(x + 0.0f)) << 32) |
+           static_cast<uint32_t>(~static_cast<uint32_t>(id));
+}
+__device__ __forceinline__ float key_value(uint64_t key) {
+    return from_ordered_bits(static_cast<uint32_t>(key >> 32));
+}
+__device__ __forceinline__ int key_id(uint64_t key) {
+    return static_cast<int>(~static_cast<uint32_t>(key));
+}
+
+// Sorts n2 (a power of two) keys in LDS in decreasing order.
+template <int BLOCK>
+__device__ void sort_keys(unsigned long long *key, int n2, int tid) {
+    for (int size = 2; size <= n2; size *= 2) {
+        for (int step = size / 2; step > 0; step /= 2) {
+            __syncthreads();
+            for (int p = tid; p < n2 / 2; p += BLOCK) {
+                const int i = 2 * p - (p & (step - 1));
+                const int j = i + step;
+                const unsigned long long a = key[i], b = key[j];
+                const bool up = (i & size) == 0;  // this run decreases
+                if (up ? a < b : a > b) {
+                    key[i] = b;
+                    key[j] = a;
+                }
+            }
+        }
+    }
+    __syncthreads();
+}
+
+// The exact k-th largest key of a segment's visible logits (0 when there are
+// at most k) by radix selection, eight key bits a pass over the segment.
+template <typename T, int BLOCK>
+__device__ __attribute__((noinline)) uint64_t radix_kth(const T *row, int ebeg, int eend, int k,
+                                                        unsigned int *hist, int tid) {
+    __shared__ uint64_t sh_prefix;
+    __shared__ int sh_left;
+    uint64_t prefix = 0, mask = 0;
+    int left = k;
+    for (int shift = 56; shift >= 0; shift -= 8) {
+        for (int i = tid; i < 256; i += BLOCK) hist[i] = 0;
+        __syncthreads();
+        for (int i = ebeg + tid; i < eend; i += BLOCK) {
+            const float x = Elem<T>::at(row, i);
+            const uint64_t key = topk_key(x, i);
+            if (x > kMasked && (key & mask) == prefix) {
+                const int bin = static_cast<int>((key >> shift) & 255u);
+                // lanes that share the first lane's bin count once together
+                const int lead = __builtin_amdgcn_readfirstlane(bin);
+                const uint64_t same = __ballot(bin == lead);
+                if (bin != lead)
+                    atomicAdd(&hist[bin], 1u);
+                else if ((threadIdx.x & (kWave - 1)) ==
+                         static_cast<unsigned>(__ffsll(static_cast<long long>(same)) - 1))
+                    atomicAdd(&hist[lead], static_cast<unsigned>(__popcll(same)));
+            }
+        }
+        __syncthreads();
+        if (tid == 0) {
+            int bin = 255, n = left;
+            while (bin >= 0 && static_cast<int>(hist[bin]) < n) n -= static_cast<int>(hist[bin--]);
+            sh_left = bin < 0 ? 0 : n;
+            sh_prefix = bin < 0 ? 0 : prefix | (static_cast<uint64_t>(bin) << shift);
+        }
+        __syncthreads();
+        left = sh_left;
+        prefix = sh_prefix;
+        mask |= 0xFFull << shift;
+        __syncthreads();  // read before the next pass writes them
+        if (left == 0) return 0;  // fewer than k: every visible logit is listed
+    }
+    return prefix;
+}
+
+template <typename T, int BLOCK, int UNROLL>
+__global__ __launch_bounds__(BLOCK) void topk_rows_kernel(TopkArgs a) {
+    using E = Elem<T>;
+    using M16 = ChunkMax<T>;
+    constexpr int EPV = E::kPerVec;
+    constexpr int N = UNROLL * EPV;
+    constexpr int NW = BLOCK / kWave;
+    constexpr int kChunk = UNROLL * BLOCK;
+    extern __shared__ __align__(16) unsigned char dyn[];
+    typename M16::type *cmax = reinterpret_cast<typename M16::type *>(dyn);  // [chunk][BLOCK]
+    __shared__ unsigned long long sh_key[kTopkCollect];
+    __shared__ uint32_t sh_m[BLOCK];
+    __shared__ uint32_t sh_wm[NW];
+    __shared__ double sh_s[NW];
+    __shared__ uint32_t sh_tau;
+    __shared__ int sh_n;
+
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), wv = tid / kWave;
+    const int64_t row = blockIdx.x / a.segs;
+    const int seg = static_cast<int>(blockIdx.x - row * a.segs);
+    if (a.ended && a.ended[row]) return;
+    if (a.scores && !(a.scores[row] > -__builtin_inff())) return;
+    const T *rp = static_cast<const T *>(a.base) + row * a.stride;
+    const int V = a.V, k = a.k;
+    const float c = a.c;
+    const int nvec = (V + EPV - 1) / EPV;
+    const int vbeg = seg * a.seg_vecs;
+    const int vend = vbeg + a.seg_vecs < nvec ? vbeg + a.seg_vecs : nvec;
+
+    OnlineSum acc;
+    stream_vectors<T, BLOCK, UNROLL>(rp, vbeg, vend, V, tid,
+                                     [&](const uint4 (&buf)[UNROLL], int it) {
+        float x[N];
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) E::unpack(buf[u], x + u * EPV);
+        const float cm = chunk_max(x);
+        cmax[it * BLOCK + tid] = M16::put(cm);
+        acc.add(x, cm, c);
+    });
+
+    // Row (segment) maximum and normaliser.
+    const uint32_t om = ordered_bits(acc.m + 0.0f);
+    sh_m[tid] = om;
+    const uint32_t wm = wave_max_u32(om);
+    if (lane == 0) sh_wm[wv] = wm;
+    if (tid == 0) sh_n = 0;
+    __syncthreads();
+    uint32_t bm = sh_wm[0];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) bm = sh_wm[w] > bm ? sh_wm[w] : bm;
+    const float M = from_ordered_bits(bm);
+    const float ws = wave_sum_f32(acc.at(M, c));
+    if (lane == 0) sh_s[wv] = static_cast<double>(ws);
+
+    // tau: a value that at least k threads' maxima reach (all visible logits
+    // when fewer than k threads hold one).  The first wave builds it bit by
+    // bit from the top, and stops as soon as few more than k threads reach it.
+    const uint32_t masked = ordered_bits(kMasked);
+    if (wv == 0) {
+        uint32_t key[NW];
+        int seen = 0;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            key[w] = sh_m[w * kWave + lane];
+            seen += __popcll(__ballot(key[w] > masked));
+        }
+        uint32_t tau = 0;
+        if (seen >= k) {
+            const int enough = k + k / 4 + 4;
+            for (int bit = 31; bit >= 0; --bit) {
+                const uint32_t trial = tau | (1u << bit);
+                int n = 0;
+#pragma unroll
+                for (int w = 0; w < NW; ++w) n += __popcll(__ballot(key[w] >= trial));
+                if (n >= k) {
+                    tau = trial;
+                    if (n <= enough) break;
+                }
+            }
+        }
+        if (lane == 0) sh_tau = tau > masked ? tau : masked + 1u;
+    }
+    __syncthreads();
+    const uint32_t tau = sh_tau;
+
+    // Collect the logits at or above tau from the chunks that hold one.
+    if (om >= tau) {
+        const int nv = vend - vbeg;
+        for (int it = 0; it * kChunk + tid < nv; ++it) {
+            const float cm = M16::get(cmax[it * BLOCK + tid]);
+            if (!(cm > kMasked) || ordered_bits(cm + 0.0f) < tau) continue;
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u) {
+                const int vi = vbeg + it * kChunk + u * BLOCK + tid;
+                if (vi >= vend) continue;
+                const uint4 v = (vi + 1) * EPV <= V
+                                    ? reinterpret_cast<const uint4 *>(rp)[vi]
+                                    : E::partial(rp, vi, V);
+                float x[EPV];
+                E::unpack(v, x);
+#pragma unroll
+                for (int e = 0; e < EPV; ++e) {
+                    if (x[e] > kMasked && ordered_bits(x[e] + 0.0f) >= tau) {
+                        const int o = atomicAdd(&sh_n, 1);
+                        if (o < kTopkCollect) sh_key[o] = topk_key(x[e], vi * EPV + e);
+                    }
+                }
+            }
+        }
+    }
+    __syncthreads();
+    int n = sh_n;
+    if (n > kTopkCollect) {
+        // Too many logits reach tau: the k-th key itself, then exactly the
+        // keys at or above it.
+        const int ebeg = vbeg * EPV, eend = vend * EPV < V ? vend * EPV : V;
+        const uint64_t kth = radix_kth<T, BLOCK>(rp, ebeg, eend, k,
+                                                 reinterpret_cast<unsigned int *>(sh_key), tid);
+        if (tid == 0) sh_n = 0;
+        __syncthreads();
+        for (int i = ebeg + tid; i < eend; i += BLOCK) {
+            const float x = E::at(rp, i);
+            const uint64_t key = topk_key(x, i);
+            if (x > kMasked && key >= kth) {
+                const int o = atomicAdd(&sh_n, 1);
+                if (o < kTopkCollect) sh_key[o] = key;
+            }
+        }
+        __syncthreads();
+        n = sh_n;
+    }
+    int n2 = 2;
+    while (n2 < n) n2 *= 2;
+    for (int i = n + tid; i < n2; i += BLOCK) sh_key[i] = 0;
+    sort_keys<BLOCK>(sh_key, n2, tid);
+
+    double r = 0.0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) r += sh_s[w];
+    if (a.list) {
+        unsigned long long *dst = a.list + static_cast<int64_t>(blockIdx.x) * k;
+        for (int i = tid; i < k; i += BLOCK) dst[i] = i < n ? sh_key[i] : 0ull;
+        if (tid == 0)
+            a.seg_lse[blockIdx.x] = bm > masked ? static_cast<double>(M) * a.inv_t + log(r)
+                                                : -__builtin_inf();
+        return;
+    }
+    for (int i = tid; i < k; i += BLOCK) {
+        a.values[row * k + i] = i < n ? key_value(sh_key[i]) : -__builtin_inff();
+        a.ids[row * k + i] = i < n ? key_id(sh_key[i]) : -1;
+    }
+    if (a.lse && tid == 0)
+        a.lse[row] = bm > masked
+                         ? static_cast<float>(static_cast<double>(M) * a.inv_t + log(r))
+                         : -__builtin_inff();
+}
+
+// ln of a sum of e^x over a row's segments: lanes hold segment lane's x.
+__device__ __forceinline__ double wave_log_sum(double x, int lane, int segs) {
+    double m = lane < segs ? x : -__builtin_inf();
+    double top = -__builtin_inf();
+    for (int s = 0; s < segs; ++s) {  // at most 64, usually a few
+        const double o = __shfl(m, s, kWave);
+        top = o > top ? o : top;
+    }
+    if (!(top > -__builtin_inf())) return top;
+    const double e = lane < segs ? exp(m - top) : 0.0;
+    return top + log(wave_sum_f64(e));
+}
+
+// Joins the segments' lists of one row: a key's place is the number of keys
+// above it, found in each sorted list by bisection.
+template <int BLOCK>
+__global__ __launch_bounds__(BLOCK) void topk_merge_kernel(TopkArgs a) {
+    extern __shared__ __align__(16) unsigned char dyn[];
+    unsigned long long *key = reinterpret_cast<unsigned long long *>(dyn);  // [segs][k]
+    __shared__ int sh_n;
+    const int tid = threadIdx.x, k = a.k, total = a.segs * a.k;
+    const int64_t row = blockIdx.x;
+    if (tid == 0) sh_n = 0;
+    for (int i = tid; i < total; i += BLOCK) key[i] = a.list[row * total + i];
+    __syncthreads();
+    for (int i = tid; i < total; i += BLOCK) {
+        const unsigned long long x = key[i];
+        if (x == 0) continue;
+        atomicAdd(&sh_n, 1);
+        int rank = i % k;
+        const int own = i / k;
+        for (int s = 0; s < a.segs && rank < k; ++s) {
+            if (s == own) continue;
+            int lo = 0, hi = k;  // keys of list s above x
+            while (lo < hi) {
+                const int mid = (lo + hi) / 2;
+                if (key[s * k + mid] > x)
+                    lo = mid + 1;
+                else
+                    hi = mid;
+            }
+            rank += lo;
+        }
+        if (rank < k) {
+            a.values[row * k + rank] = key_value(x);
+            a.ids[row * k + rank] = key_id(x);
+        }
+    }
+    __syncthreads();
+    for (int i = sh_n + tid; i < k; i += BLOCK) {
+        a.values[row * k + i] = -__builtin_inff();
+        a.ids[row * k + i] = -1;
+    }
+    if (a.lse && tid < kWave) {
+        const double x = tid < a.segs ? a.seg_lse[row * a.segs + tid] : -__builtin_inf();
+        const double l = wave_log_sum(x, tid, a.segs);
+        if (tid == 0) a.lse[row] = static_cast<float>(l);
+    }
+}
+
+}  // namespace sv

@@ -422,6 +422,34 @@ spec_status spec_row_stats(const void *logits, int64_t rows, int32_t vocab, int6
                            int32_t *argmax, float *qmax, float *feat, void *stream);
 
 /*
+ * Draft-model calls
+ * -----------------
+ * What a draft model needs beside verification: listing a row's top logits
+ * (the target's, recorded for training), the distillation loss on such a list
+ * with its gradient, and drafting by beam search.  Logits are rows as above,
+ * and in these calls an entry at or below -1e30 (-inf, the types' lowest
+ * values), or a quiet NaN, is masked: it has probability zero and is never
+ * listed or chosen.  A row may be masked throughout.  vocab <= 2^20, else
+ * SPEC_ERR_UNSUPPORTED.
+ */
+
+/*
+ * spec_row_topk -- the k largest logits of each row in decreasing order,
+ * equal values by lowest id.  values (device float [rows][k]) and ids (device
+ * int32 [rows][k]) are required; a row with fewer than k visible entries is
+ * filled up with (-inf, -1).  lse (device float [rows], nullable): ln sum
+ * e^(l/T) over the whole row, -inf when it is masked throughout.  One pass over the
+ * rows.  1 <= k <= 128.  workspace: device, spec_row_topk_workspace_bytes,
+ * 16-byte aligned (a size of 0 needs none); its contents on entry do not
+ * matter.
+ */
+size_t spec_row_topk_workspace_bytes(int64_t rows, int32_t vocab, int32_t dtype, int32_t k);
+spec_status spec_row_topk(const void *logits, int64_t rows, int32_t vocab, int64_t row_stride,
+                          int32_t dtype, float temperature, int32_t k, float *values,
+                          int32_t *ids, float *lse, void *workspace, size_t workspace_bytes,
+                          void *stream);
+
+/*
  * spec_read_probe -- a measurement aid, not part of verification: streams
  * `rows` rows of `row_bytes` bytes each (consecutive rows `row_stride_bytes`
  * apart) with the same loads, workgroup shape and one-workgroup-per-row grid
