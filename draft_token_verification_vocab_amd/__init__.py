@@ -19,7 +19,7 @@ import torch
 
 __all__ = [
     "SpecVerifyError", "lib_path", "load", "verify", "av_score", "av_score_stats", "av_update",
-    "row_stats", "row_topk",
+    "row_stats", "row_topk", "distill_loss", "distill_grad", "distill_step",
     "workspace_bytes", "draft_stats_bytes", "MODE_LOSSLESS", "MODE_FLY",
 ]
 
@@ -53,6 +53,12 @@ class _VerifyOut(ctypes.Structure):
                 ("target_argmax", ctypes.c_void_p), ("draft_lse", ctypes.c_void_p),
                 ("draft_qmax", ctypes.c_void_p), ("draft_feat", ctypes.c_void_p),
                 ("draft_stats_out", ctypes.c_void_p), ("boundary", ctypes.c_void_p)]
+
+
+class _DistillParams(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("vocab", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("row_stride", ctypes.c_int64), ("k", ctypes.c_int32),
+                ("temperature", ctypes.c_float), ("reserved", ctypes.c_int64)]
 
 
 # Every symbol the header declares, with its ctypes signature.
@@ -104,6 +110,13 @@ _SIGNATURES = {
     "spec_row_topk": (ctypes.c_int32, [_P, ctypes.c_int64, ctypes.c_int32, ctypes.c_int64,
                                        ctypes.c_int32, ctypes.c_float, ctypes.c_int32, _P, _P, _P,
                                        _P, ctypes.c_size_t, _P]),
+    "spec_distill_state_bytes": (ctypes.c_size_t, [ctypes.c_int64]),
+    "spec_distill_loss": (ctypes.c_int32, [_P, _P, _P, _P, _P, ctypes.POINTER(_DistillParams), _P,
+                                           _P, _P]),
+    "spec_distill_grad": (ctypes.c_int32, [_P, _P, _P, _P, _P, ctypes.POINTER(_DistillParams), _P,
+                                           _P]),
+    "spec_distill_step": (ctypes.c_int32, [_P, _P, _P, _P, _P, _P, ctypes.POINTER(_DistillParams),
+                                           _P, _P, _P]),
     "spec_status_string": (ctypes.c_char_p, [ctypes.c_int32]),
 }
 
@@ -754,3 +767,83 @@ def row_topk(logits: torch.Tensor, k: int, *, temperature: float = 1.0,
                                _ptr(workspace), 0 if workspace is None else _nbytes(workspace),
                                _stream(dev)), "spec_row_topk")
     return res
+
+
+def _distill_args(student, ids, logits, lse, keep, grad_loss, temperature, vocab, out):
+    """The checked shapes of a distillation call: (params, rows, device)."""
+    _need_cuda(student, "student")
+    S = student.shape[-1]
+    lead, dev, k = tuple(student.shape[:-1]), student.device, ids.shape[-1]
+    rows = student.numel() // S if S else 0
+    _need_cuda(ids, "ids", dev, torch.int32, lead + (k,))
+    _need_cuda(logits, "logits", dev, torch.float32, lead + (k,))
+    for t, name, dt in ((lse, "lse", torch.float32), (keep, "keep", torch.uint8),
+                        (grad_loss, "grad_loss", torch.float32)):
+        if t is not None:
+            _need_cuda(t, name, dev, dt, lead)
+    if out is not None:
+        _need_cuda(out, "out", dev, student.dtype, student.shape)
+    return _DistillParams(rows, S if vocab is None else int(vocab), _dtype_code(student), S, k,
+                          float(temperature), 0), rows, dev
+
+
+def distill_loss(student: torch.Tensor, ids: torch.Tensor, logits: torch.Tensor,
+                 lse: Optional[torch.Tensor] = None, *, temperature: float = 1.0,
+                 vocab: Optional[int] = None, keep: Optional[torch.Tensor] = None,
+                 state: bool = True):
+    """Distillation loss of each row of student [..., S] (first V columns) from
+    a teacher's listed logits (ids int32 and logits float32 [..., k], as
+    row_topk gives them).  lse (float32 [...]): the teacher's log-normaliser
+    at the same temperature, for a bucket over the unlisted ids; None: the list
+    is a distribution of its own.  keep (uint8 [...]): rows to train on.
+    Returns (loss [...], state): the state is what distill_grad takes
+    (state=False: None)."""
+    p, rows, dev = _distill_args(student, ids, logits, lse, keep, None, temperature, vocab, None)
+    L = load()
+    loss = torch.empty(student.shape[:-1], dtype=torch.float32, device=dev)
+    saved = None
+    if state:
+        saved = torch.empty(L.spec_distill_state_bytes(rows), dtype=torch.uint8, device=dev)
+    with _on(dev):
+        _check(L.spec_distill_loss(_ptr(student), _ptr(ids), _ptr(logits), _ptr(lse), _ptr(keep),
+                                   ctypes.byref(p), _ptr(loss), _ptr(saved), _stream(dev)),
+               "spec_distill_loss")
+    return loss, saved
+
+
+def distill_grad(student: torch.Tensor, ids: torch.Tensor, logits: torch.Tensor,
+                 state: torch.Tensor, grad_loss: Optional[torch.Tensor] = None, *,
+                 temperature: float = 1.0, vocab: Optional[int] = None,
+                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of sum(grad_loss * loss) (grad_loss float32 [...], None: ones)
+    with respect to the student's logits, in their dtype and shape, from the
+    state of the distill_loss call with the same arguments.  out may be the
+    student tensor itself."""
+    p, rows, dev = _distill_args(student, ids, logits, None, None, grad_loss, temperature, vocab,
+                                 out)
+    L = load()
+    _need_cuda(state, "state", dev, nbytes=L.spec_distill_state_bytes(rows))
+    grad = torch.empty_like(student) if out is None else out
+    with _on(dev):
+        _check(L.spec_distill_grad(_ptr(student), _ptr(ids), _ptr(logits), _ptr(state),
+                                   _ptr(grad_loss), ctypes.byref(p), _ptr(grad), _stream(dev)),
+               "spec_distill_grad")
+    return grad
+
+
+def distill_step(student: torch.Tensor, ids: torch.Tensor, logits: torch.Tensor,
+                 lse: Optional[torch.Tensor] = None, grad_loss: Optional[torch.Tensor] = None, *,
+                 temperature: float = 1.0, vocab: Optional[int] = None,
+                 keep: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
+    """Loss and gradient in one call, where the upstream gradient is known
+    beforehand (1/N for a mean over N rows): the (loss, gradient) of
+    distill_loss and distill_grad."""
+    p, rows, dev = _distill_args(student, ids, logits, lse, keep, grad_loss, temperature, vocab,
+                                 out)
+    loss = torch.empty(student.shape[:-1], dtype=torch.float32, device=dev)
+    grad = torch.empty_like(student) if out is None else out
+    with _on(dev):
+        _check(load().spec_distill_step(_ptr(student), _ptr(ids), _ptr(logits), _ptr(lse),
+                                        _ptr(keep), _ptr(grad_loss), ctypes.byref(p), _ptr(loss),
+                                        _ptr(grad), _stream(dev)), "spec_distill_step")
+    return loss, grad

@@ -1,5 +1,6 @@
 // specverify_draft.hip -- host side of the draft-model calls declared in
-// include/specverify.h: listing rows' top logits.  Argument validation,
+// include/specverify.h: listing rows' top logits and distillation from such
+// lists.  Argument validation,
 // workspace layout, kernel selection and launches on the caller's stream.  No
 // allocation, no synchronisation.
 #include <hip/hip_runtime.h>
@@ -10,6 +11,7 @@
 
 #include "specverify.h"
 #include "sv_common.hpp"
+#include "sv_distill.hpp"
 #include "sv_host.hpp"
 #include "sv_topk.hpp"
 
@@ -119,6 +121,56 @@ void launch_lists(const ListPlan &p, const TopkArgs &a, int64_t rows, int32_t dt
 
 constexpr int32_t kMaxListVocab = 1 << 20;
 
+// Distillation: a workgroup per row (the row pass's shapes); the gradient on
+// its own is cut into segments of kGradVecs vectors.
+constexpr int kGradBlock = 256;
+constexpr int kGradVecs = 4096;
+
+spec_status check_distill(const void *student, const int32_t *ids, const float *logits,
+                          const spec_distill_params *p) {
+    if (!p) return SPEC_ERR_ARG;
+    const spec_status s = check_logits_shape(p->vocab, p->row_stride, p->dtype, p->temperature);
+    if (s != SPEC_OK) return s;
+    if (p->rows < 0 || p->k < 1 || p->reserved != 0) return SPEC_ERR_ARG;
+    if (p->k > kDistillMax || p->vocab > kMaxListVocab) return SPEC_ERR_UNSUPPORTED;
+    if (p->rows == 0) return SPEC_OK;
+    if (!student || !aligned16(student) || !ids || !logits) return SPEC_ERR_ARG;
+    if (p->row_stride * elem_size(p->dtype) > INT32_MAX ||
+        !grid_fits(p->rows * ((p->row_stride + kGradVecs - 1) / kGradVecs), 1024))
+        return SPEC_ERR_UNSUPPORTED;
+    return SPEC_OK;
+}
+
+DistillArgs distill_args(const void *student, const int32_t *ids, const float *logits,
+                         const spec_distill_params *p) {
+    DistillArgs a{};
+    a.student = student;
+    a.ids = ids;
+    a.logits = logits;
+    a.stride = p->row_stride;
+    a.V = p->vocab;
+    a.k = p->k;
+    a.c = log2e_over(p->temperature);
+    a.inv_t = 1.0 / static_cast<double>(p->temperature);
+    return a;
+}
+
+template <typename T, bool GRAD>
+void launch_distill_t(const DistillArgs &a, int64_t rows, hipStream_t st) {
+    using S = WideShape<T>;
+    const size_t map = a.V <= kListMapVocab ? 4 * static_cast<size_t>((a.V + 31) / 32) : 0;
+    distill_rows_kernel<T, S::block, S::unroll, GRAD>
+        <<<dim3(static_cast<unsigned>(rows)), dim3(S::block), map, st>>>(a);
+}
+
+template <bool GRAD>
+void launch_distill(const DistillArgs &a, const spec_distill_params *p, hipStream_t st) {
+    if (p->dtype == SPEC_DTYPE_BF16)
+        launch_distill_t<uint16_t, GRAD>(a, p->rows, st);
+    else
+        launch_distill_t<float, GRAD>(a, p->rows, st);
+}
+
 }  // namespace
 
 extern "C" {
@@ -167,6 +219,65 @@ spec_status spec_row_topk(const void *logits, int64_t rows, int32_t vocab, int64
     if ((s = launch_status()) != SPEC_OK || p.segs == 1) return s;
     topk_merge_kernel<kMergeBlock><<<dim3(static_cast<unsigned>(rows)), dim3(kMergeBlock),
                                      sizeof(unsigned long long) * p.segs * k, st>>>(a);
+    return launch_status();
+}
+
+size_t spec_distill_state_bytes(int64_t rows) {
+    return rows < 1 ? 0 : sizeof(DistillRow) * static_cast<size_t>(rows);
+}
+
+spec_status spec_distill_loss(const void *student, const int32_t *ids, const float *logits,
+                              const float *lse, const uint8_t *keep,
+                              const spec_distill_params *params, float *loss, void *state,
+                              void *stream) {
+    const spec_status s = check_distill(student, ids, logits, params);
+    if (s != SPEC_OK || params->rows == 0) return s;
+    if (!loss || !aligned16(state)) return SPEC_ERR_ARG;
+    DistillArgs a = distill_args(student, ids, logits, params);
+    a.lse = lse;
+    a.keep = keep;
+    a.loss = loss;
+    a.state = static_cast<DistillRow *>(state);
+    launch_distill<false>(a, params, static_cast<hipStream_t>(stream));
+    return launch_status();
+}
+
+spec_status spec_distill_grad(const void *student, const int32_t *ids, const float *logits,
+                              const void *state, const float *grad_loss,
+                              const spec_distill_params *params, void *grad, void *stream) {
+    const spec_status s = check_distill(student, ids, logits, params);
+    if (s != SPEC_OK || params->rows == 0) return s;
+    if (!state || !aligned16(state) || !grad || !aligned16(grad)) return SPEC_ERR_ARG;
+    DistillArgs a = distill_args(student, ids, logits, params);
+    a.state = const_cast<DistillRow *>(static_cast<const DistillRow *>(state));
+    a.grad_loss = grad_loss;
+    a.grad = grad;
+    a.seg_vecs = kGradVecs;
+    const int64_t vecs = params->row_stride * elem_size(params->dtype) / 16;
+    const int segs = static_cast<int>((vecs + kGradVecs - 1) / kGradVecs);
+    const dim3 grid(static_cast<unsigned>(params->rows * segs));
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (params->dtype == SPEC_DTYPE_BF16)
+        distill_grad_kernel<uint16_t, kGradBlock><<<grid, dim3(kGradBlock), 0, st>>>(a, segs);
+    else
+        distill_grad_kernel<float, kGradBlock><<<grid, dim3(kGradBlock), 0, st>>>(a, segs);
+    return launch_status();
+}
+
+spec_status spec_distill_step(const void *student, const int32_t *ids, const float *logits,
+                              const float *lse, const uint8_t *keep, const float *grad_loss,
+                              const spec_distill_params *params, float *loss, void *grad,
+                              void *stream) {
+    const spec_status s = check_distill(student, ids, logits, params);
+    if (s != SPEC_OK || params->rows == 0) return s;
+    if (!loss || !grad || !aligned16(grad)) return SPEC_ERR_ARG;
+    DistillArgs a = distill_args(student, ids, logits, params);
+    a.lse = lse;
+    a.keep = keep;
+    a.grad_loss = grad_loss;
+    a.loss = loss;
+    a.grad = grad;
+    launch_distill<true>(a, params, static_cast<hipStream_t>(stream));
     return launch_status();
 }
 

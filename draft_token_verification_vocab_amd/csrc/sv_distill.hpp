@@ -1,0 +1,399 @@
+// sv_distill.hpp -- distillation of a draft (student) model from a teacher's
+// listed top logits: the loss per row and its gradient.
+//
+// With z = s/T, q = softmax(z) over the whole vocabulary, and the list's
+// masses p_i = e^(t_i/T - L) (L the teacher's log-normaliser, or the list's
+// own), P = sum p_i, r = max(0, 1 - P) the teacher's mass outside the list
+// (0 with the list's own normaliser) and rho = sum of q outside the list:
+//   loss      = sum_i p_i (ln p_i - ln q_i) + r (ln r - ln rho)
+//   dloss/ds_j = (1/T) (q_j (P + r) - sum of p_i listed at j)   j in the list
+//              = (1/T) q_j (P + r - r / rho)                   j outside it
+// rho is summed over the entries outside the list themselves, with a maximum
+// of their own: formed as one minus the list's share it would vanish in
+// rounding, or the entries underflow, as soon as the student is sure.  So the
+// stream leaves the listed entries out, and the list (at most 128 entries) is
+// settled in double by one wave.
+//
+// Outside the list the gradient is one factor per row times 2^((s_j - M) c),
+// M the largest logit outside the list; that factor's difference is taken in
+// double.
+#pragma once
+
+#include "sv_stream.hpp"
+#include "sv_topk.hpp"
+
+namespace sv {
+
+constexpr int kDistillMax = kTopkMax;         // longest list
+constexpr int kListMapVocab = 1 << 18;        // ids the list's bitmap in LDS covers
+
+// What the gradient needs of a row's forward pass.
+struct DistillRow {
+    double lse;    // student: ln sum e^z
+    double norm;   // teacher: L
+    double mass;   // P + r, or -1 for a row that is left out
+    double coef;   // mass * e^(M/T - lse) - r / sum_{outside} 2^((s - M) c)
+    float m;       // M
+    int32_t pad_;
+};
+static_assert(sizeof(DistillRow) == 40, "spec_distill_state_bytes");
+
+struct DistillArgs {
+    const void *student;
+    const int32_t *ids;       // [rows][k]
+    const float *logits;      // [rows][k]
+    const float *lse;         // [rows] or null: the list's own normaliser
+    const uint8_t *keep;      // [rows] or null
+    const float *grad_loss;   // [rows] or null (= 1)
+    float *loss;              // [rows]
+    DistillRow *state;        // [rows] or null
+    void *grad;               // rows of row_stride, or null
+    int64_t stride;
+    int32_t V;
+    int32_t k;
+    float c;                  // log2(e) / T
+    int32_t seg_vecs;         // gradient pass: vectors per workgroup
+    double inv_t;
+};
+
+// Four bytes of two bfloat16, rounded to nearest even.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+    const bf2 v = {static_cast<__bf16>(lo), static_cast<__bf16>(hi)};
+    uint32_t r;
+    __builtin_memcpy(&r, &v, 4);
+    return r;
+}
+
+template <typename T>
+struct GradOut;
+template <>
+struct GradOut<uint16_t> {
+    __device__ static uint4 pack(const float *x) {
+        return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                          pack_bf16(x[6], x[7]));
+    }
+    __device__ static uint16_t one(float x) { return static_cast<uint16_t>(pack_bf16(x, 0.f)); }
+};
+template <>
+struct GradOut<float> {
+    __device__ static uint4 pack(const float *x) {
+        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                          __float_as_uint(x[3]));
+    }
+    __device__ static float one(float x) { return x; }
+};
+
+__device__ __forceinline__ void store_stream(uint4 *p, const uint4 &v) {
+    const v4u32 r = {v.x, v.y, v.z, v.w};
+    __builtin_nontemporal_store(r, reinterpret_cast<v4u32 *>(p));
+}
+
+// Entry vectors of a row: one vector with the ragged one read element-wise.
+template <typename T>
+__device__ __forceinline__ uint4 load_vector(const T *row, int vi, int V) {
+    return (vi + 1) * Elem<T>::kPerVec <= V ? load_stream(reinterpret_cast<const uint4 *>(row) + vi)
+                                            : Elem<T>::partial(row, vi, V);
+}
+
+// Gradients of a vector outside the list: G * 2^((x - M) c), 0 where masked.
+template <typename T>
+__device__ __forceinline__ uint4 outside_grad(const uint4 &v, float M, float c, float G) {
+    constexpr int EPV = Elem<T>::kPerVec;
+    float x[EPV];
+    Elem<T>::unpack(v, x);
+#pragma unroll
+    for (int e = 0; e < EPV; ++e)
+        x[e] = G * hw_exp2((fmaxf(x[e], 2.0f * kMasked) - M) * c);  // a NaN becomes masked
+    return GradOut<T>::pack(x);
+}
+
+// The list of a row in LDS.
+struct ListShared {
+    int id[kDistillMax];       // -1: not a listed entry
+    float s[kDistillMax];      // the student's logit there (-inf when masked)
+    float t[kDistillMax];      // the teacher's
+    double p[kDistillMax];     // masses
+    float g[kDistillMax];      // gradients (the first of equal ids)
+    int first[kDistillMax];    // nonzero: the first entry with this id
+    int dup;                   // some id is listed twice
+};
+
+// Entry i of the list; call by threads i < k.
+template <typename T>
+__device__ __forceinline__ void load_list(const DistillArgs &a, int64_t row, const T *rp, int i,
+                                          ListShared &l) {
+    const int id = a.ids[row * a.k + i];
+    const float t = a.logits[row * a.k + i];
+    const bool valid = id >= 0 && id < a.V && t > kMasked;
+    float s = -__builtin_inff();
+    if (valid) {
+        s = Elem<T>::at(rp, id);
+        if (!(s > kMasked)) s = -__builtin_inff();
+    }
+    l.id[i] = valid ? id : -1;
+    l.t[i] = t;
+    l.s[i] = s;
+    l.first[i] = valid;
+}
+
+// first[] when some id is listed twice; call by threads i < k after load_list.
+__device__ __forceinline__ void mark_first(int i, ListShared &l) {
+    for (int j = 0; j < i; ++j)
+        if (l.id[j] == l.id[i]) l.first[i] = 0;
+}
+
+// Gradient at the listed id i (the first of equal ids): its own share less the
+// teacher's masses listed there.
+__device__ __forceinline__ float listed_grad(int i, int k, const ListShared &l, double lse,
+                                             double mass, double inv_t, double g) {
+    double p = l.p[i];
+    if (l.dup)
+        for (int j = i + 1; j < k; ++j)
+            if (l.id[j] == l.id[i]) p += l.p[j];
+    const double q = exp(static_cast<double>(l.s[i]) * inv_t - lse);
+    return static_cast<float>((q * mass - p) * inv_t * g);
+}
+
+// One wave: the row's loss and gradient state from the list and the sum S of
+// 2^((s - M) c) outside it (M <= kMasked: nothing visible there).
+__device__ __forceinline__ DistillRow settle_row(const DistillArgs &a, int64_t row, int lane,
+                                                 ListShared &l, float M, double S, float *loss) {
+    const double inf = __builtin_inf();
+    const double it = a.inv_t;
+    const bool outside = M > kMasked;
+    const double rest = outside ? static_cast<double>(M) * it + log(S) : -inf;
+    double t[2], z[2];
+    bool first[2];
+    double tm = -inf, zm = rest;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int i = lane + h * kWave;
+        const bool in = i < a.k && l.id[i] >= 0;
+        t[h] = in ? static_cast<double>(l.t[i]) * it : -inf;
+        z[h] = in ? static_cast<double>(l.s[i]) * it : -inf;
+        first[h] = in && l.first[i];
+        tm = fmax(tm, t[h]);
+        zm = fmax(zm, z[h]);
+    }
+#pragma unroll
+    for (int o = 1; o < kWave; o *= 2) {
+        tm = fmax(tm, __shfl_xor(tm, o, kWave));
+        zm = fmax(zm, __shfl_xor(zm, o, kWave));
+    }
+    DistillRow r{};
+    r.mass = -1.0;
+    r.m = M;
+    *loss = 0.f;
+    if (!(tm > -inf) || !(zm > -inf)) return r;  // nothing listed, or nothing visible
+    double zs = 0.0, ts = 0.0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (first[h]) zs += exp(z[h] - zm);
+        ts += exp(t[h] - tm);
+    }
+    const double total = wave_sum_f64(zs) + (outside ? exp(rest - zm) : 0.0);
+    r.lse = zm + log(total);
+    r.norm = a.lse ? static_cast<double>(a.lse[row]) : tm + log(wave_sum_f64(ts));
+    double ps = 0.0, ls = 0.0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const double lp = t[h] - r.norm, p = exp(lp);
+        if (lane + h * kWave < a.k) l.p[lane + h * kWave] = p;
+        ps += p;
+        if (p > 0.0) ls += p * (lp - (z[h] - r.lse));
+    }
+    const double P = wave_sum_f64(ps);
+    const double left = a.lse && outside ? fmax(0.0, 1.0 - P) : 0.0;
+    double total_loss = wave_sum_f64(ls);
+    if (left > 0.0) total_loss += left * (log(left) - (rest - r.lse));
+    *loss = static_cast<float>(total_loss);
+    r.mass = P + left;
+    r.coef = outside ? r.mass * exp(static_cast<double>(M) * it - r.lse) - left / S : 0.0;
+    return r;
+}
+
+// One workgroup per row: the loss, and with GRAD the gradient, for which the
+// row is read a second time.
+template <typename T, int BLOCK, int UNROLL, bool GRAD>
+__global__ __launch_bounds__(BLOCK) void distill_rows_kernel(DistillArgs a) {
+    using E = Elem<T>;
+    constexpr int EPV = E::kPerVec;
+    constexpr int N = UNROLL * EPV;
+    constexpr int NW = BLOCK / kWave;
+    constexpr int kChunk = UNROLL * BLOCK;
+    extern __shared__ __align__(16) unsigned char dyn[];
+    uint32_t *map = reinterpret_cast<uint32_t *>(dyn);  // one bit per id (V <= kListMapVocab)
+    __shared__ ListShared list;
+    __shared__ unsigned long long sh_chunks[BLOCK];  // chunks (mod 64) holding a listed entry
+    __shared__ uint32_t sh_wm[NW];
+    __shared__ double sh_s[NW];
+    __shared__ DistillRow sh_row;
+
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), wv = tid / kWave;
+    const int64_t row = blockIdx.x;
+    const T *rp = static_cast<const T *>(a.student) + row * a.stride;
+    T *gp = static_cast<T *>(a.grad) + row * a.stride;
+    const int V = a.V;
+    const float c = a.c;
+    const int nvec = (V + EPV - 1) / EPV;
+    const int out_vecs = static_cast<int>(a.stride / EPV);  // the row with its padding
+    const bool kept = !a.keep || a.keep[row];
+    const bool mapped = V <= kListMapVocab;
+
+    if (kept) {
+        sh_chunks[tid] = 0;
+        if (mapped)
+            for (int i = tid; i < (V + 31) / 32; i += BLOCK) map[i] = 0;
+        if (tid == 0) list.dup = 0;
+        if (tid < a.k) load_list<T>(a, row, rp, tid, list);
+        __syncthreads();
+        if (tid < a.k && list.id[tid] >= 0) {
+            const int id = list.id[tid];
+            const int w = id / EPV, it = w / kChunk, owner = (w % kChunk) % BLOCK;
+            atomicOr(&sh_chunks[owner], 1ull << (it & 63));
+            bool again = false;
+            if (mapped)
+                again = (atomicOr(&map[id >> 5], 1u << (id & 31)) >> (id & 31)) & 1u;
+            else
+                for (int j = 0; j < tid; ++j) again = again || list.id[j] == id;
+            if (again) list.dup = 1;
+        }
+        __syncthreads();
+        if (list.dup && tid < a.k && list.id[tid] >= 0) mark_first(tid, list);
+        const unsigned long long mine = sh_chunks[tid];
+
+        OnlineSum acc;
+        stream_vectors<T, BLOCK, UNROLL>(rp, 0, nvec, V, tid,
+                                         [&](const uint4 (&buf)[UNROLL], int it) {
+            float x[N];
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u) E::unpack(buf[u], x + u * EPV);
+            if ((mine >> (it & 63)) & 1ull) {  // leave the listed entries out
+#pragma unroll
+                for (int u = 0; u < UNROLL; ++u) {
+                    const int vi = it * kChunk + u * BLOCK + tid;
+                    uint32_t bits = 0;
+                    if (mapped) {
+                        if (vi < nvec) bits = map[vi * EPV >> 5] >> (vi * EPV & 31);
+                    } else {
+                        for (int j = 0; j < a.k; ++j) {
+                            const int e = list.id[j] - vi * EPV;
+                            if (e >= 0 && e < EPV) bits |= 1u << e;
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < EPV; ++e)
+                        if ((bits >> e) & 1u) x[u * EPV + e] = 2.0f * kMasked;
+                }
+            }
+            acc.add(x, chunk_max(x), c);
+        });
+
+        const uint32_t wm = wave_max_u32(ordered_bits(acc.m + 0.0f));
+        if (lane == 0) sh_wm[wv] = wm;
+        __syncthreads();
+        uint32_t bm = sh_wm[0];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) bm = sh_wm[w] > bm ? sh_wm[w] : bm;
+        const float M = from_ordered_bits(bm);
+        const float ws = wave_sum_f32(acc.at(M, c));
+        if (lane == 0) sh_s[wv] = static_cast<double>(ws);
+        __syncthreads();
+        if (wv == 0) {
+            double S = 0.0;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) S += sh_s[w];
+            float loss;
+            const DistillRow r = settle_row(a, row, lane, list, M, S, &loss);
+            if (lane == 0) {
+                sh_row = r;
+                a.loss[row] = loss;
+                if (a.state) a.state[row] = r;
+            }
+        }
+    } else if (tid == 0) {
+        DistillRow r{};
+        r.mass = -1.0;
+        sh_row = r;
+        a.loss[row] = 0.f;
+        if (a.state) a.state[row] = r;
+    }
+    if (!GRAD) return;
+
+    __syncthreads();
+    const DistillRow r = sh_row;
+    uint4 *out = reinterpret_cast<uint4 *>(gp);
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    if (r.mass < 0.0) {
+        for (int i = tid; i < out_vecs; i += BLOCK) store_stream(out + i, zero);
+        return;
+    }
+    const double g = a.grad_loss ? static_cast<double>(a.grad_loss[row]) : 1.0;
+    const float G = static_cast<float>(r.coef * a.inv_t * g);
+    for (int i = tid; i < nvec; i += BLOCK)
+        store_stream(out + i, outside_grad<T>(load_vector(rp, i, V), r.m, c, G));
+    for (int i = nvec + tid; i < out_vecs; i += BLOCK) store_stream(out + i, zero);
+    // the listed entries over what the stream wrote there, once it is written
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (tid < a.k && list.id[tid] >= 0 && list.first[tid])
+        gp[list.id[tid]] = GradOut<T>::one(listed_grad(tid, a.k, list, r.lse, r.mass, a.inv_t, g));
+}
+
+// The gradient alone, from the forward pass's state: every workgroup writes
+// seg_vecs vectors of a row.
+template <typename T, int BLOCK>
+__global__ __launch_bounds__(BLOCK) void distill_grad_kernel(DistillArgs a, int32_t segs) {
+    constexpr int EPV = Elem<T>::kPerVec;
+    __shared__ ListShared list;
+    const int tid = threadIdx.x;
+    const int64_t row = blockIdx.x / segs;
+    const int seg = static_cast<int>(blockIdx.x - row * segs);
+    const T *rp = static_cast<const T *>(a.student) + row * a.stride;
+    T *gp = static_cast<T *>(a.grad) + row * a.stride;
+    const int V = a.V;
+    const int nvec = (V + EPV - 1) / EPV;
+    const int out_vecs = static_cast<int>(a.stride / EPV);
+    const int vbeg = seg * a.seg_vecs;
+    const int vend = vbeg + a.seg_vecs < out_vecs ? vbeg + a.seg_vecs : out_vecs;
+    uint4 *out = reinterpret_cast<uint4 *>(gp);
+    const DistillRow r = a.state[row];
+    if (r.mass < 0.0) {
+        for (int i = vbeg + tid; i < vend; i += BLOCK) store_stream(out + i, make_uint4(0, 0, 0, 0));
+        return;
+    }
+    if (tid == 0) list.dup = 0;
+    if (tid < a.k) {
+        load_list<T>(a, row, rp, tid, list);
+        list.p[tid] = list.id[tid] >= 0
+                          ? exp(static_cast<double>(list.t[tid]) * a.inv_t - r.norm)
+                          : 0.0;
+    }
+    __syncthreads();
+    if (tid < a.k && list.id[tid] >= 0) {
+        for (int j = 0; j < tid; ++j)
+            if (list.id[j] == list.id[tid]) {
+                list.first[tid] = 0;
+                list.dup = 1;
+            }
+    }
+    __syncthreads();
+    const double g = a.grad_loss ? static_cast<double>(a.grad_loss[row]) : 1.0;
+    const float G = static_cast<float>(r.coef * a.inv_t * g);
+    for (int i = vbeg + tid; i < vend; i += BLOCK) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (i < nvec) v = outside_grad<T>(load_vector(rp, i, V), r.m, a.c, G);
+        store_stream(out + i, v);
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (tid < a.k && list.id[tid] >= 0 && list.first[tid]) {
+        const int w = list.id[tid] / EPV;
+        if (w >= vbeg && w < vend)
+            gp[list.id[tid]] =
+                GradOut<T>::one(listed_grad(tid, a.k, list, r.lse, r.mass, a.inv_t, g));
+    }
+}
+
+}  // namespace sv

@@ -450,6 +450,70 @@ spec_status spec_row_topk(const void *logits, int64_t rows, int32_t vocab, int64
                           void *stream);
 
 /*
+ * Distillation from a teacher's listed top logits.  For each row, with
+ * z = s/T, q = softmax(z) over the student's whole row, the listed masses
+ * p_i = e^(t_i/T - L), P = sum p_i, r = max(0, 1 - P) and rho the sum of q
+ * outside the list:
+ *   loss      = sum_i p_i (ln p_i - ln q_i) + r (ln r - ln rho)
+ *   dloss/ds_j = (1/T) (q_j (P + r) - the p_i listed at j)    j in the list
+ *              = (1/T) q_j (P + r - r/rho)                    j outside it
+ * lse (device float [rows], spec_row_topk's or spec_verify's target_lse at
+ * the same temperature) is the teacher's log-normaliser L: the loss is then
+ * the divergence over the listed ids and one bucket for the rest.  With lse
+ * NULL, L is the list's own normaliser and r = 0.
+ *   ids, logits  device, int32 and float [rows][k]: the teacher's list, in any
+ *                order.  An entry whose id lies outside [0, vocab) or whose
+ *                logit is masked is not listed; an id listed twice has both
+ *                masses.
+ *   keep         device uint8 [rows] or NULL: rows with 0 (padding) are left
+ *                out: not read, loss 0, gradient 0.  So are rows that list
+ *                nothing and rows whose student logits are all masked.
+ * A listed id that the student masks makes the loss +inf (its q is 0).  Where
+ * the student has nothing visible outside the list, the bucket for the rest
+ * is left out (r = 0).
+ * Losses are per row; a mean over N rows is grad_loss = 1/N.  The gradient is
+ * of the temperature-scaled loss as written: a factor T^2, where wanted,
+ * belongs in grad_loss too.
+ */
+typedef struct spec_distill_params {
+    int64_t rows;       /* R >= 0                                             */
+    int32_t vocab;      /* V, 2 <= V <= 2^20                                  */
+    int32_t dtype;      /* of the student's logits and their gradient         */
+    int64_t row_stride; /* elements between consecutive rows, >= V            */
+    int32_t k;          /* entries per list, 1 <= k <= 128                    */
+    float temperature;  /* T, 1e-4 <= T <= 1e4                                */
+    int64_t reserved;   /* must be 0                                          */
+} spec_distill_params;
+
+/* Bytes of the state spec_distill_loss leaves for spec_distill_grad (40 per
+ * row; device, 16-byte aligned, owned by the caller). */
+size_t spec_distill_state_bytes(int64_t rows);
+
+/* spec_distill_loss -- loss: device float [rows].  state: device or NULL
+ * (no gradient wanted). */
+spec_status spec_distill_loss(const void *student, const int32_t *ids, const float *logits,
+                              const float *lse, const uint8_t *keep,
+                              const spec_distill_params *params, float *loss, void *state,
+                              void *stream);
+
+/* spec_distill_grad -- the gradient of sum_r grad_loss[r] * loss[r] with
+ * respect to the student's logits, from the same arguments as the
+ * spec_distill_loss call that filled state.  grad_loss: device float [rows]
+ * or NULL (= 1).  grad: device, rows of vocab elements of the student's dtype
+ * and row_stride; entries between vocab and row_stride become 0.  grad may be
+ * student itself (same address): the gradient then replaces the logits. */
+spec_status spec_distill_grad(const void *student, const int32_t *ids, const float *logits,
+                              const void *state, const float *grad_loss,
+                              const spec_distill_params *params, void *grad, void *stream);
+
+/* spec_distill_step -- loss and gradient in one call, for an upstream gradient
+ * known beforehand: the results of spec_distill_loss and spec_distill_grad. */
+spec_status spec_distill_step(const void *student, const int32_t *ids, const float *logits,
+                              const float *lse, const uint8_t *keep, const float *grad_loss,
+                              const spec_distill_params *params, float *loss, void *grad,
+                              void *stream);
+
+/*
  * spec_read_probe -- a measurement aid, not part of verification: streams
  * `rows` rows of `row_bytes` bytes each (consecutive rows `row_stride_bytes`
  * apart) with the same loads, workgroup shape and one-workgroup-per-row grid
