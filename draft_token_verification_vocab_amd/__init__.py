@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -20,6 +21,7 @@ import torch
 __all__ = [
     "SpecVerifyError", "lib_path", "load", "verify", "av_score", "av_score_stats", "av_update",
     "row_stats", "row_topk", "distill_loss", "distill_grad", "distill_step",
+    "beam_select", "beam_reorder",
     "workspace_bytes", "draft_stats_bytes", "MODE_LOSSLESS", "MODE_FLY",
 ]
 
@@ -59,6 +61,12 @@ class _DistillParams(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("vocab", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("row_stride", ctypes.c_int64), ("k", ctypes.c_int32),
                 ("temperature", ctypes.c_float), ("reserved", ctypes.c_int64)]
+
+
+class _BeamState(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p),
+                ("position_bytes", ctypes.c_int64), ("segments", ctypes.c_int32),
+                ("positions", ctypes.c_int32)]
 
 
 # Every symbol the header declares, with its ctypes signature.
@@ -117,6 +125,13 @@ _SIGNATURES = {
                                            _P]),
     "spec_distill_step": (ctypes.c_int32, [_P, _P, _P, _P, _P, _P, ctypes.POINTER(_DistillParams),
                                            _P, _P, _P]),
+    "spec_beam_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32] * 5),
+    "spec_beam_select": (ctypes.c_int32, [_P, ctypes.c_int64, _P, _P, ctypes.c_int32,
+                                          ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                                          ctypes.c_float, ctypes.c_int32, ctypes.c_int32, _P, _P,
+                                          _P, _P, _P, ctypes.c_size_t, _P]),
+    "spec_beam_reorder": (ctypes.c_int32, [_P, _P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                                           ctypes.POINTER(_BeamState), ctypes.c_int32, _P]),
     "spec_status_string": (ctypes.c_char_p, [ctypes.c_int32]),
 }
 
@@ -847,3 +862,84 @@ def distill_step(student: torch.Tensor, ids: torch.Tensor, logits: torch.Tensor,
                                         _ptr(keep), _ptr(grad_loss), ctypes.byref(p), _ptr(loss),
                                         _ptr(grad), _stream(dev)), "spec_distill_step")
     return loss, grad
+
+
+def beam_select(logits: torch.Tensor, scores: torch.Tensor, num_out: int, *,
+                temperature: float = 1.0, vocab: Optional[int] = None,
+                ended: Optional[torch.Tensor] = None, eos: int = -1,
+                workspace: Optional[torch.Tensor] = None) -> dict:
+    """One beam-search step: the num_out best continuations of each sequence
+    over its beams and the vocabulary, from logits [B, W, S] (first V columns),
+    scores float32 [B, W] (-inf: a beam that takes no part) and ended uint8
+    [B, W] (beams that stay as they are).  Returns scores (float32), parents
+    and tokens (int32) and ended (uint8), each [B, num_out], best first; -inf,
+    -1, -1 and 0 past the last continuation."""
+    _need_cuda(logits, "logits")
+    B, W, S = logits.shape
+    V = S if vocab is None else int(vocab)
+    n, dev, dt = int(num_out), logits.device, _dtype_code(logits)
+    _need_cuda(scores, "scores", dev, torch.float32, (B, W))
+    if ended is not None:
+        _need_cuda(ended, "ended", dev, torch.uint8, (B, W))
+    L = load()
+    shape = (B, max(n, 0))
+    res = {"scores": torch.empty(shape, dtype=torch.float32, device=dev),
+           "parents": torch.empty(shape, dtype=torch.int32, device=dev),
+           "tokens": torch.empty(shape, dtype=torch.int32, device=dev),
+           "ended": torch.empty(shape, dtype=torch.uint8, device=dev)}
+    if workspace is None:
+        need = L.spec_beam_workspace_bytes(B, W, V, dt, n)
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    else:
+        _need_cuda(workspace, "workspace", dev)
+    with _on(dev):
+        _check(L.spec_beam_select(_ptr(logits), S, _ptr(scores), _ptr(ended), B, W, V, dt,
+                                  float(temperature), n, int(eos), _ptr(res["scores"]),
+                                  _ptr(res["parents"]), _ptr(res["tokens"]), _ptr(res["ended"]),
+                                  _ptr(workspace), _nbytes(workspace), _stream(dev)),
+               "spec_beam_select")
+    return res
+
+
+def beam_reorder(parents: torch.Tensor, states, outs=None, *,
+                 lengths: Optional[torch.Tensor] = None, position_dim: int = 3) -> list:
+    """Move the beams' states behind their parents (int32 [B, n], as
+    beam_select gives them): out[b, i] = state[b, parents[b, i]] for every
+    tensor [B, W, ...] of states; a parent outside the beams leaves its row.
+    outs: tensors [B, n, ...] to write, None: in place (n = W).  lengths
+    (int32 [B]): only that many positions, along dimension position_dim of
+    every state, are moved.  Returns the list of tensors written."""
+    _need_cuda(parents, "parents", dtype=torch.int32)
+    B, n = parents.shape
+    dev = parents.device
+    states = list(states)
+    outs = states if outs is None else list(outs)
+    if len(states) != len(outs):
+        raise ValueError("%d states, but %d outs" % (len(states), len(outs)))
+    if lengths is not None:
+        _need_cuda(lengths, "lengths", dev, torch.int32, (B,))
+    W = states[0].shape[1] if states and states[0].dim() > 1 else n
+    table, used = (_BeamState * max(len(states), 1))(), 0
+    for i, (src, dst) in enumerate(zip(states, outs)):
+        shape = tuple(src.shape)
+        if len(shape) < 2 or shape[:2] != (B, W):
+            raise ValueError("states[%d] must have shape (%d, %d, ...), not %s" % (i, B, W, shape))
+        _need_cuda(src, "states[%d]" % i, dev)
+        _need_cuda(dst, "outs[%d]" % i, dev, src.dtype, (B, n) + shape[2:])
+        if lengths is not None and not 2 <= position_dim < len(shape):
+            raise ValueError("position_dim %d is no dimension of states[%d]'s beams"
+                             % (position_dim, i))
+        row = math.prod(shape[2:])
+        if row == 0 or B == 0:
+            continue
+        s = table[used]
+        used += 1
+        s.src, s.dst = src.data_ptr(), dst.data_ptr()
+        s.segments, s.positions = 1, 1
+        if lengths is not None:
+            s.segments, s.positions = math.prod(shape[2:position_dim]), shape[position_dim]
+        s.position_bytes = row // (s.segments * s.positions) * src.element_size()
+    with _on(dev):
+        _check(load().spec_beam_reorder(_ptr(parents), _ptr(lengths), B, W, n, table, used,
+                                        _stream(dev)), "spec_beam_reorder")
+    return outs

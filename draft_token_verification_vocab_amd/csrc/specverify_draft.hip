@@ -1,6 +1,6 @@
 // specverify_draft.hip -- host side of the draft-model calls declared in
-// include/specverify.h: listing rows' top logits and distillation from such
-// lists.  Argument validation,
+// include/specverify.h: listing rows' top logits, distillation from such
+// lists, beam selection and the reordering of beam states.  Argument validation,
 // workspace layout, kernel selection and launches on the caller's stream.  No
 // allocation, no synchronisation.
 #include <hip/hip_runtime.h>
@@ -10,6 +10,7 @@
 #include <cstdint>
 
 #include "specverify.h"
+#include "sv_beam.hpp"
 #include "sv_common.hpp"
 #include "sv_distill.hpp"
 #include "sv_host.hpp"
@@ -163,6 +164,36 @@ void launch_distill_t(const DistillArgs &a, int64_t rows, hipStream_t st) {
         <<<dim3(static_cast<unsigned>(rows)), dim3(S::block), map, st>>>(a);
 }
 
+// Beam selection: lists a merge can hold.
+constexpr int kBeamMergeBlock = 512;
+constexpr int kMaxBeamKeys = 512;  // num_beams * num_out
+static_assert(kMaxBeamKeys * 8 <= kMaxMerge, "eight segments a row, enough for 2^20 floats");
+
+spec_status check_beam(int32_t batch, int32_t beams, int32_t vocab, int32_t dtype,
+                       int32_t num_out) {
+    if (batch < 0 || beams < 1 || num_out < 1 || vocab < 2) return SPEC_ERR_ARG;
+    if (dtype != SPEC_DTYPE_F32 && dtype != SPEC_DTYPE_BF16) return SPEC_ERR_ARG;
+    if (beams > kMaxBeams || num_out > kMaxBeamOut || beams * num_out > kMaxBeamKeys ||
+        vocab > kMaxListVocab)
+        return SPEC_ERR_UNSUPPORTED;
+    return SPEC_OK;
+}
+
+// Reordering: workgroups of kReorderBlock threads, kReorderUnroll units each.
+constexpr int kReorderBlock = 256;
+constexpr int kReorderUnroll = 4;
+
+template <int BYTES>
+void launch_reorder(const ReorderArgs &a, int group, uint32_t blocks, hipStream_t st) {
+    const dim3 grid(blocks), block(kReorderBlock);
+    if (group == 8)
+        beam_reorder_kernel<BYTES, 8, kReorderBlock, kReorderUnroll><<<grid, block, 0, st>>>(a);
+    else if (group == 16)
+        beam_reorder_kernel<BYTES, 16, kReorderBlock, kReorderUnroll><<<grid, block, 0, st>>>(a);
+    else
+        beam_reorder_kernel<BYTES, 32, kReorderBlock, kReorderUnroll><<<grid, block, 0, st>>>(a);
+}
+
 template <bool GRAD>
 void launch_distill(const DistillArgs &a, const spec_distill_params *p, hipStream_t st) {
     if (p->dtype == SPEC_DTYPE_BF16)
@@ -279,6 +310,143 @@ spec_status spec_distill_step(const void *student, const int32_t *ids, const flo
     a.grad = grad;
     launch_distill<true>(a, params, static_cast<hipStream_t>(stream));
     return launch_status();
+}
+
+size_t spec_beam_workspace_bytes(int32_t batch, int32_t num_beams, int32_t vocab, int32_t dtype,
+                                 int32_t num_out) {
+    if (check_beam(batch, num_beams, vocab, dtype, num_out) != SPEC_OK || batch == 0) return 0;
+    return plan_lists(static_cast<int64_t>(batch) * num_beams, vocab, dtype, num_out, num_beams,
+                      true).total;
+}
+
+spec_status spec_beam_select(const void *logits, int64_t row_stride, const float *scores,
+                             const uint8_t *ended, int32_t batch, int32_t num_beams,
+                             int32_t vocab, int32_t dtype, float temperature, int32_t num_out,
+                             int32_t eos, float *out_scores, int32_t *parents, int32_t *tokens,
+                             uint8_t *ended_out, void *workspace, size_t workspace_bytes,
+                             void *stream) {
+    spec_status s = check_logits_shape(vocab, row_stride, dtype, temperature);
+    if (s != SPEC_OK) return s;
+    if ((s = check_beam(batch, num_beams, vocab, dtype, num_out)) != SPEC_OK) return s;
+    if (batch == 0) return SPEC_OK;
+    if (!logits || !aligned16(logits) || !scores || !out_scores || !parents || !tokens)
+        return SPEC_ERR_ARG;
+    const int64_t rows = static_cast<int64_t>(batch) * num_beams;
+    const ListPlan p = plan_lists(rows, vocab, dtype, num_out, num_beams, true);
+    if (!grid_fits(rows * p.segs, 1024)) return SPEC_ERR_UNSUPPORTED;
+    if (!workspace || workspace_bytes < p.total) return SPEC_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return SPEC_ERR_ARG;
+    char *w = static_cast<char *>(workspace);
+    TopkArgs t{};
+    t.base = logits;
+    t.stride = row_stride;
+    t.V = vocab;
+    t.k = num_out;
+    t.segs = p.segs;
+    t.seg_vecs = p.seg_vecs;
+    t.c = log2e_over(temperature);
+    t.inv_t = 1.0 / static_cast<double>(temperature);
+    t.list = reinterpret_cast<unsigned long long *>(w + p.list);
+    t.seg_lse = reinterpret_cast<double *>(w + p.seg_lse);
+    t.ended = ended;
+    t.scores = scores;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    launch_lists(p, t, rows, dtype, st);
+    if ((s = launch_status()) != SPEC_OK) return s;
+    BeamArgs a{};
+    a.base = logits;
+    a.scores = scores;
+    a.ended = ended;
+    a.list = t.list;
+    a.seg_lse = t.seg_lse;
+    a.out_scores = out_scores;
+    a.parents = parents;
+    a.tokens = tokens;
+    a.ended_out = ended_out;
+    a.stride = row_stride;
+    a.V = vocab;
+    a.W = num_beams;
+    a.n = num_out;
+    a.segs = p.segs;
+    a.eos = eos;
+    a.inv_t = t.inv_t;
+    const size_t keys = sizeof(double) * num_beams * p.segs * num_out;
+    if (dtype == SPEC_DTYPE_BF16)
+        beam_merge_kernel<uint16_t, kBeamMergeBlock>
+            <<<dim3(batch), dim3(kBeamMergeBlock), keys, st>>>(a);
+    else
+        beam_merge_kernel<float, kBeamMergeBlock>
+            <<<dim3(batch), dim3(kBeamMergeBlock), keys, st>>>(a);
+    return launch_status();
+}
+
+spec_status spec_beam_reorder(const int32_t *parents, const int32_t *lengths, int32_t batch,
+                              int32_t num_beams, int32_t num_out, const spec_beam_state *states,
+                              int32_t num_states, void *stream) {
+    if (batch < 0 || num_beams < 1 || num_out < 1 || num_states < 0) return SPEC_ERR_ARG;
+    if (num_beams > kMaxBeams || num_out > kMaxBeamOut) return SPEC_ERR_UNSUPPORTED;
+    if (batch == 0 || num_states == 0) return SPEC_OK;
+    if (!parents || !states) return SPEC_ERR_ARG;
+    // every state is checked before anything is enqueued
+    uintptr_t low_bits = 0;
+    bool in_place = false;
+    for (int i = 0; i < num_states; ++i) {
+        const spec_beam_state &s = states[i];
+        if (!s.src || !s.dst || s.segments < 1 || s.positions < 0 || s.position_bytes < 1)
+            return SPEC_ERR_ARG;
+        if (s.position_bytes > INT32_MAX ||
+            s.segments > (int64_t{1} << 44) / (s.position_bytes * (int64_t{s.positions} + 1)))
+            return SPEC_ERR_UNSUPPORTED;
+        const int64_t beam = s.position_bytes * s.positions * s.segments;
+        const char *src = static_cast<const char *>(s.src), *dst = static_cast<char *>(s.dst);
+        if (src == dst ? num_out != num_beams
+                       : src < dst + beam * num_out * batch && dst < src + beam * num_beams * batch)
+            return SPEC_ERR_ARG;  // in place means beam for beam
+        in_place = in_place || src == dst;
+        low_bits |= reinterpret_cast<uintptr_t>(src) | reinterpret_cast<uintptr_t>(dst) |
+                    static_cast<uintptr_t>(s.position_bytes);
+    }
+    const int unit = low_bits % 16 == 0 ? 16 : low_bits % 4 == 0 ? 4 : 1;
+    const int group = !in_place || num_out <= 8 ? 8 : num_out <= 16 ? 16 : 32;
+    const int64_t chunk_bytes = static_cast<int64_t>(unit) * kReorderBlock * kReorderUnroll;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    int64_t all = 0;
+    for (int i = 0; i < num_states; ++i)
+        all += (states[i].position_bytes * states[i].positions + chunk_bytes - 1) / chunk_bytes *
+               states[i].segments * batch;
+    if (!grid_fits(all, 1024)) return SPEC_ERR_UNSUPPORTED;
+    for (int from = 0; from < num_states; from += kMaxReorder) {
+        ReorderArgs a{};
+        a.parents = parents;
+        a.lengths = lengths;
+        a.W = num_beams;
+        a.n = num_out;
+        uint32_t blocks = 0;
+        for (int i = from; i < num_states && i < from + kMaxReorder; ++i) {
+            const spec_beam_state &s = states[i];
+            if (s.positions == 0) continue;
+            ReorderState &r = a.st[a.count++];
+            r.src = static_cast<const char *>(s.src);
+            r.dst = static_cast<char *>(s.dst);
+            r.pos_bytes = s.position_bytes;
+            r.segments = s.segments;
+            r.positions = s.positions;
+            r.chunks = static_cast<int32_t>((s.position_bytes * s.positions + chunk_bytes - 1) /
+                                            chunk_bytes);
+            r.first = blocks;
+            blocks += static_cast<uint32_t>(r.chunks) * s.segments * batch;
+        }
+        if (blocks == 0) continue;
+        if (unit == 16)
+            launch_reorder<16>(a, group, blocks, st);
+        else if (unit == 4)
+            launch_reorder<4>(a, group, blocks, st);
+        else
+            launch_reorder<1>(a, group, blocks, st);
+        const spec_status s = launch_status();
+        if (s != SPEC_OK) return s;
+    }
+    return SPEC_OK;
 }
 
 }  // extern "C"

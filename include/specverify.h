@@ -514,6 +514,64 @@ spec_status spec_distill_step(const void *student, const int32_t *ids, const flo
                               void *stream);
 
 /*
+ * spec_beam_select -- one step of beam search for each sequence: of every
+ * beam w's continuation by every visible token x, with the score
+ *   scores[b][w] + l(x)/T - ln sum_x' e^(l(x')/T),
+ * the num_out best in decreasing order (equal scores: lower beam first, then
+ * the larger logit, then the lower token).  The order is that of the scores in
+ * double precision, not of the rounded sums: where beams nearly tie, their
+ * normalisers are computed again in double.
+ *   logits    device, [B][W] rows.
+ *   scores    device float [B][W]: finite, or -inf for a beam that takes no
+ *             part (all but the first in a search's first step); its logits
+ *             are not read.
+ *   ended     device uint8 [B][W] or NULL: a beam with a nonzero entry has
+ *             ended; its logits are not read, and its one continuation is the
+ *             token eos at an unchanged score.
+ *   eos       the token that ends a beam (a value outside [0, vocab) when
+ *             none does).
+ * Outputs, all [B][num_out]: out_scores (device float), parents and tokens
+ * (device int32), and ended_out (device uint8, nullable: 1 where the parent
+ * had ended or the token is eos).  With fewer continuations the rest is filled
+ * with -inf, -1, -1 and 0.  num_beams <= 32, num_out <= 64, num_beams *
+ * num_out <= 512, else SPEC_ERR_UNSUPPORTED.  workspace: device,
+ * spec_beam_workspace_bytes, 16-byte aligned; its contents on entry do not
+ * matter.
+ */
+size_t spec_beam_workspace_bytes(int32_t batch, int32_t num_beams, int32_t vocab, int32_t dtype,
+                                 int32_t num_out);
+spec_status spec_beam_select(const void *logits, int64_t row_stride, const float *scores,
+                             const uint8_t *ended, int32_t batch, int32_t num_beams,
+                             int32_t vocab, int32_t dtype, float temperature, int32_t num_out,
+                             int32_t eos, float *out_scores, int32_t *parents, int32_t *tokens,
+                             uint8_t *ended_out, void *workspace, size_t workspace_bytes,
+                             void *stream);
+
+/*
+ * spec_beam_reorder -- moves the beams' states (caches, histories) behind
+ * their chosen parents: for each state, dst[b][i] = src[b][parents[b][i]].
+ * A state is an array [B][beams][segments][positions][position_bytes]:
+ * num_beams beams in src, num_out in dst.  Only the first lengths[b] positions
+ * of every segment are moved (device int32 [B], clamped to [0, positions];
+ * NULL: all); later positions of dst, and the rows of a parent outside
+ * [0, num_beams), are left as they are.  A state may be reordered in place
+ * (dst == src, num_out == num_beams); buffers that overlap otherwise are
+ * refused, and no two states of a call may share memory.  parents: device
+ * int32 [B][num_out].  num_beams <= 32, num_out <= 64.  One launch moves up to
+ * 32 states.
+ */
+typedef struct spec_beam_state {
+    const void *src;
+    void *dst;
+    int64_t position_bytes; /* >= 1 */
+    int32_t segments;       /* parts of a beam's state that each hold positions, >= 1 */
+    int32_t positions;      /* allocated per segment, >= 0 */
+} spec_beam_state;
+spec_status spec_beam_reorder(const int32_t *parents, const int32_t *lengths, int32_t batch,
+                              int32_t num_beams, int32_t num_out, const spec_beam_state *states,
+                              int32_t num_states, void *stream);
+
+/*
  * spec_read_probe -- a measurement aid, not part of verification: streams
  * `rows` rows of `row_bytes` bytes each (consecutive rows `row_stride_bytes`
  * apart) with the same loads, workgroup shape and one-workgroup-per-row grid

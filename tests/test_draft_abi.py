@@ -80,3 +80,63 @@ def test_distill_validates_on_host(L):
     assert step(g=None) == -1 and step(g=P(8)) == -1
     assert L.spec_distill_state_bytes(7) == 280 and L.spec_distill_state_bytes(0) == 0
     assert L.spec_distill_state_bytes(-1) == 0
+
+
+@host_only
+def test_beam_select_validates_on_host(L):
+    P = ctypes.c_void_p
+    a, big = P(16), 1 << 30
+
+    def call(logits=a, S=1024, scores=a, B=4, W=4, V=1024, dt=1, T=1.0, n=8, out=a, par=a, tok=a,
+             ws=a, size=big):
+        return L.spec_beam_select(logits, S, scores, None, B, W, V, dt, T, n, 2, out, par, tok,
+                                  None, ws, size, None)
+    assert call(B=0, logits=None, scores=None, out=None, ws=None) == 0
+    for kw in (dict(B=-1), dict(W=0), dict(n=0), dict(V=1), dict(S=1000), dict(S=1028),
+               dict(dt=7), dict(T=0.0), dict(T=float("inf")), dict(logits=None),
+               dict(logits=P(8)), dict(scores=None), dict(out=None), dict(par=None),
+               dict(tok=None), dict(ws=P(8))):
+        assert call(**kw) == -1, kw
+    for kw in (dict(W=33), dict(n=65), dict(W=32, n=17), dict(V=(1 << 20) + 8, S=(1 << 20) + 8),
+               dict(B=1 << 30, W=32)):
+        assert call(**kw) == -2, kw
+    need = L.spec_beam_workspace_bytes(4, 4, 1024, 1, 8)
+    assert need > 0
+    assert call(ws=None) == -3 and call(size=need - 1) == -3
+    assert L.spec_beam_workspace_bytes(4, 33, 1024, 1, 8) == 0
+    assert L.spec_beam_workspace_bytes(0, 4, 1024, 1, 8) == 0
+
+
+@host_only
+def test_beam_reorder_validates_on_host(L):
+    P = ctypes.c_void_p
+    a = P(16)
+
+    def call(B=2, W=4, n=4, par=a, count=1, states=True, **kw):
+        base = dict(src=1 << 20, dst=1 << 30, position_bytes=16, segments=2, positions=8)
+        base.update(kw)
+        st = (sv._BeamState * 1)(sv._BeamState(**base))
+        return L.spec_beam_reorder(par, None, B, W, n, st if states else None, count, None)
+    assert call(B=0, par=None) == 0 and call(count=0, par=None, states=False) == 0
+    for kw in (dict(B=-1), dict(W=0), dict(n=0), dict(count=-1), dict(par=None),
+               dict(states=False), dict(src=None), dict(dst=None), dict(position_bytes=0),
+               dict(segments=0), dict(positions=-1),
+               dict(dst=1 << 20, n=3),                     # in place means beam for beam
+               dict(dst=(1 << 20) + 16),                   # other overlaps
+               dict(src=(1 << 30) + 2 * 4 * 256 - 16)):
+        assert call(**kw) == -1, kw
+    for kw in (dict(W=33), dict(n=65), dict(position_bytes=1 << 31),
+               dict(position_bytes=1 << 30, positions=1 << 30, segments=1 << 10),
+               dict(B=1 << 30, dst=1 << 60)):
+        assert call(**kw) == -2, kw
+
+
+def test_binding_refuses_host_tensors_and_wrong_shapes():
+    f, i = torch.zeros(2, 3, 8), torch.zeros(2, 3, 4, dtype=torch.int32)
+    for call in (lambda: sv.row_topk(f, 2), lambda: sv.distill_loss(f, i, i.float()),
+                 lambda: sv.distill_step(f, i, i.float()),
+                 lambda: sv.distill_grad(f, i, i.float(), torch.zeros(240, dtype=torch.uint8)),
+                 lambda: sv.beam_select(f, torch.zeros(2, 3), 2),
+                 lambda: sv.beam_reorder(torch.zeros(2, 3, dtype=torch.int32), [f])):
+        with pytest.raises(ValueError, match="GPU tensor"):
+            call()

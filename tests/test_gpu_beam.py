@@ -1,0 +1,255 @@
+"""Beam selection and reordering on the GPU against their 64-bit definitions:
+choices and moved bytes exactly, scores within the bound of their arithmetic."""
+import numpy as np
+import pytest
+import torch
+
+import draft_token_verification_vocab_amd as sv
+from oracle import draft_ref as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def select(x, scores, n, dtype="f32", T=1.0, ended=None, eos=-1, stride=None):
+    """One call against the oracle; returns its host arrays."""
+    B, W, V = x.shape
+    per = 8 if dtype == "bf16" else 4
+    S = stride or -(-V // per) * per
+    T = float(np.float32(T))
+    t = torch.full((B, W, S), float("nan"), dtype=DT[dtype])
+    t[..., :V] = torch.from_numpy(x).to(DT[dtype])
+    e = None if ended is None else torch.from_numpy(ended).to(DEV)
+    r = sv.beam_select(t.to(DEV), torch.from_numpy(scores).to(DEV), n, temperature=T, vocab=V,
+                       ended=e, eos=eos)
+    torch.cuda.synchronize()
+    r = {k: v.cpu().numpy() for k, v in r.items()}
+    want = ref.beam_select(t[..., :V].float().numpy(), scores.astype(np.float64), n, T, ended, eos)
+    assert np.array_equal(r["parents"], want[1])
+    assert np.array_equal(r["tokens"], want[2])
+    assert np.array_equal(r["ended"], want[3])
+    there = np.isfinite(want[0])
+    assert np.array_equal(r["scores"][~there], want[0][~there].astype(np.float32))
+    # a normaliser's float sums (7.1e-6, at the kernel) and half a step of the result
+    tol = 7.1e-6 + np.abs(want[0][there]) * 2.0 ** -24
+    assert (np.abs(r["scores"][there] - want[0][there]) <= tol).all()
+    return r
+
+
+def beams(B, W, V, seed, scale=4.0):
+    rng = np.random.default_rng(seed)
+    x = (scale * rng.standard_normal((B, W, V))).astype(np.float32)
+    scores = -np.sort(5.0 + 3.0 * rng.random((B, W)), axis=1).astype(np.float32)
+    return x, scores, rng
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,W,V,n", [
+    (1, 1, 2, 1), (2, 3, 5, 4), (3, 2, 9, 30), (1, 4, 1000, 8), (5, 5, 4099, 10),
+    (2, 32, 700, 16), (3, 8, 3001, 64), (40, 8, 1500, 16), (1, 4, 32000, 8), (64, 4, 2003, 4),
+    (1, 16, 50257, 32), (2, 2, 128256, 4), (260, 1, 777, 5)])
+def test_selection(B, W, V, n, dtype):
+    x, scores, _ = beams(B, W, V, B + 100 * W + V + n)
+    select(x, scores, n, dtype)
+
+
+@pytest.mark.parametrize("V,W,n,dtype", [(300001, 2, 8, "bf16"), (1 << 20, 32, 16, "f32"),
+                                        (140001, 270, 1, "f32")])
+def test_rows_of_several_segments(V, W, n, dtype):
+    B = 1
+    if W > 32:
+        B, W = W, 1
+    g = torch.Generator(device=DEV).manual_seed(V)
+    per = 8 if dtype == "bf16" else 4
+    S = -(-V // per) * per
+    t = (4 * torch.randn(B, W, S, generator=g, device=DEV)).to(DT[dtype])
+    scores = -8 - 2 * torch.rand(B, W, generator=g, device=DEV)
+    r = sv.beam_select(t, scores, n, vocab=V)
+    lp = torch.log_softmax(t[..., :V].double(), -1) + scores.double()[..., None]
+    best = torch.topk(lp.reshape(B, W * V), n)
+    assert torch.equal(r["parents"], (best.indices // V).int())
+    assert torch.equal(r["tokens"], (best.indices % V).int())
+    assert ((r["scores"] - best.values).abs() <= 7.1e-6 + best.values.abs() * 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("T", [1e-4, 0.7, 3.0, 1e4])
+def test_temperatures_and_strides(T):
+    x, scores, _ = beams(3, 4, 2001, 5)
+    if T == 1e4:  # nearly flat rows: logits far apart, so that scores differ
+        x *= 1e4
+    for dtype in ("bf16", "f32"):
+        select(x, scores, 8, dtype, T, stride=2048)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_ended_beams_and_beams_that_take_no_part(dtype):
+    x, scores, rng = beams(12, 4, 900, 9)
+    ended = (rng.random((12, 4)) < 0.4).astype(np.uint8)
+    ended[0], ended[1] = 1, 0
+    scores[2, 1:] = -np.inf                    # a first step
+    scores[3] = -np.inf                        # nothing left
+    scores[4, 0] = np.nan
+    x[:, :, 7] += 9.0                          # eos among the best
+    x[2, 1:] = np.nan                          # logits that are not read
+    x[5][ended[5] != 0] = np.nan
+    r = select(x, scores, 9, dtype, ended=ended, eos=7)
+    assert (r["parents"][3] == -1).all() and (r["ended"][0, :4] == 1).all()
+    assert (r["tokens"] == 7).sum() > 12
+    assert (r["parents"][2][:9] <= 0).all() or ended[2].any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_masks_that_leave_little_or_nothing(dtype):
+    x, scores, rng = beams(6, 3, 1200, 13)
+    low = float(torch.finfo(DT[dtype]).min)
+    x[0] = -np.inf
+    x[1, 0], x[1, 1] = low, np.nan             # one beam left
+    x[2, :, 4:] = -np.inf                      # 12 continuations in all
+    x[3, 0, 1:] = -np.inf                      # one continuation: probability 1
+    x[4] = np.where(rng.random((3, 1200)) < 0.9, -2e30, x[4])
+    r = select(x, scores, 16, dtype)
+    assert (r["parents"][0] == -1).all() and (r["parents"][1] == 2).all()
+    assert (r["parents"][2][12:] == -1).all() and (r["parents"][2][:12] >= 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_equal_scores(dtype):
+    x = np.zeros((3, 4, 513), np.float32)      # all continuations equal
+    scores = np.full((3, 4), -2.0, np.float32)
+    x[1] = np.random.default_rng(1).integers(0, 3, (1, 513)).astype(np.float32)  # equal beams
+    scores[2, 2] = -1.0
+    r = select(x, scores, 20, dtype)
+    assert (r["parents"][0] == 0).all() and r["tokens"][0].tolist() == list(range(20))
+    assert (r["parents"][2] == 2).all()
+
+
+@pytest.mark.parametrize("V", [4000, 40000])
+def test_near_ties_are_decided_by_the_exact_scores(V):
+    """Beams whose rows hold the same logits in another order, but for one that
+    moves the normaliser by 1e-9 to 1e-6: float sums would order them at
+    random, the gaps in double are a million times a double sum's error."""
+    B, W = 48, 4
+    rng = np.random.default_rng(V)
+    x = np.empty((B, W, V), np.float32)
+    for b in range(B):
+        base = rng.standard_normal(V).astype(np.float32)
+        total = np.exp(base.astype(np.float64)).sum()
+        for w in range(W):
+            row = base.copy()
+            gap = 10.0 ** rng.uniform(-9, -6) * (w + 1)
+            # one entry's weight grows by gap * total
+            i = int(rng.integers(V))
+            row[i] = np.log(np.exp(np.float64(row[i])) + gap * total)
+            x[b, w] = row[rng.permutation(V)]
+    top = x.max(axis=2, keepdims=True)
+    x = np.where(x == top, np.float32(6.0), x)  # equal largest logits
+    scores = np.full((B, W), -3.0, np.float32)
+    r = select(x, scores, 6)
+    assert len(np.unique(r["parents"][:, 0])) == W
+
+
+def test_workspace_is_reused_and_calls_agree():
+    x, scores, _ = beams(8, 4, 5003, 21)
+    t = torch.zeros(8, 4, 5004)
+    t[..., :5003] = torch.from_numpy(x)
+    t, s = t.to(DEV), torch.from_numpy(scores).to(DEV)
+    n = sv.load().spec_beam_workspace_bytes(8, 4, 5003, sv.DTYPE_F32, 8)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device=DEV)
+    a = sv.beam_select(t, s, 8, vocab=5003)
+    for _ in range(2):
+        b = sv.beam_select(t, s, 8, vocab=5003, workspace=ws)
+        assert all(torch.equal(a[k], b[k]) for k in a)
+    with pytest.raises(sv.SpecVerifyError):
+        sv.beam_select(t, s, 8, vocab=5003, workspace=ws[:n - 256])
+
+
+# ---------------------------------------------------------------------------
+# Reordering
+# ---------------------------------------------------------------------------
+def reorder_check(parents, shape, dtype, lengths=None, n=None, position_dim=3, count=2):
+    B, W = shape[:2]
+    n = n or W
+    g = torch.Generator().manual_seed(sum(shape))
+    if dtype.is_floating_point:
+        src = [torch.randn(shape, generator=g).to(dtype) for _ in range(count)]
+    else:
+        src = [torch.randint(0, 127, shape, generator=g).to(dtype) for _ in range(count)]
+    dst = [torch.full((B, n) + tuple(shape[2:]), 5).to(dtype) for _ in range(count)]
+    p = torch.tensor(parents, dtype=torch.int32)
+    le = None if lengths is None else torch.tensor(lengths, dtype=torch.int32)
+
+    def want(s, d):
+        s5, d5 = s, d
+        if le is None:
+            s5, d5 = s.reshape(B, W, 1, -1), d.reshape(B, n, 1, -1)
+        else:
+            lead = int(np.prod(shape[2:position_dim]))
+            s5 = s.reshape((B, W, lead) + tuple(shape[position_dim:]))
+            d5 = d.reshape((B, n, lead) + tuple(shape[position_dim:]))
+        to = torch.float64 if dtype.is_floating_point else torch.int64
+        out = ref.beam_reorder(p.numpy(), s5.to(to).numpy(), d5.to(to).numpy(), lengths)
+        return torch.from_numpy(out).reshape(d.shape).to(dtype)
+    gp, gl = p.to(DEV), None if le is None else le.to(DEV)
+    gs, gd = [s.to(DEV) for s in src], [d.to(DEV) for d in dst]
+    out = sv.beam_reorder(gp, gs, gd, lengths=gl, position_dim=position_dim)
+    assert all(a is b for a, b in zip(out, gd))
+    for s, d, a, b in zip(src, dst, gs, gd):
+        assert torch.equal(b.cpu(), want(s, d))
+        assert torch.equal(a.cpu(), s)
+    if n == W:
+        sv.beam_reorder(gp, gs, lengths=gl, position_dim=position_dim)
+        for s, a in zip(src, gs):
+            assert torch.equal(a.cpu(), want(s, s))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32, torch.int32, torch.uint8])
+@pytest.mark.parametrize("W", [1, 2, 4, 7, 8, 9, 16, 17, 32])
+def test_reorder(W, dtype):
+    rng = np.random.default_rng(W)
+    parents = rng.integers(0, W, (3, W))
+    parents[1] = np.roll(np.arange(W), 1)      # a cycle
+    if W > 1:
+        parents[2, 0], parents[2, 1] = -1, W   # rows that stay
+    reorder_check(parents, (3, W, 2, 9, 8), dtype, lengths=[0, 9, 5])
+    reorder_check(parents, (3, W, 2, 9, 5), dtype, lengths=[100, -3, 1])
+    reorder_check(parents, (3, W, 37), dtype)
+
+
+def test_reorder_to_more_and_fewer_beams():
+    reorder_check([[0] * 6, [0] * 6], (2, 1, 2, 40, 16), torch.bfloat16, lengths=[40, 7], n=6)
+    reorder_check([[3, 1], [2, 2]], (2, 4, 33, 7), torch.float32, n=2)
+    reorder_check(np.arange(64).reshape(1, 64) % 32, (1, 32, 3, 5, 4), torch.int32, n=64)
+
+
+def test_reorder_other_position_dimensions_and_many_states():
+    reorder_check([[1, 0]], (1, 2, 6, 3), torch.float32, lengths=[4], position_dim=2)
+    reorder_check([[1, 1], [0, 0]], (2, 2, 2, 3, 7, 4), torch.bfloat16, lengths=[3, 7],
+                  position_dim=4)
+    reorder_check([[1, 0, 0]], (1, 3, 2, 50, 8), torch.bfloat16, lengths=[33], count=70)
+
+
+def test_reorder_odd_addresses_and_empty_states():
+    p = torch.tensor([[1, 0]], dtype=torch.int32, device=DEV)
+    raw = torch.arange(2 * 333 + 1, device=DEV).to(torch.uint8)
+    s = raw[1:].view(1, 2, 333)                # one byte past an allocation's start
+    out = torch.zeros(1, 2, 333, dtype=torch.uint8, device=DEV)
+    sv.beam_reorder(p, [s], [out])
+    assert torch.equal(out, s.flip(1))
+    e = torch.zeros(1, 2, 4, 0, 8, device=DEV)
+    assert sv.beam_reorder(p, [e], lengths=torch.tensor([3], dtype=torch.int32, device=DEV))
+    assert sv.beam_reorder(p, []) == []
+    assert sv.beam_reorder(p[:0], [torch.zeros(0, 2, 5, device=DEV)])
+
+
+def test_reorder_large_state_in_place():
+    # beams of 1.2e9 bytes: offsets pass 2^32
+    s = torch.empty(1, 4, 2, 600_000_016, dtype=torch.uint8, device=DEV)
+    for w in range(4):
+        s[0, w] = w + 1
+    s[0, :, 1, -1] = torch.tensor([11, 12, 13, 14], dtype=torch.uint8, device=DEV)
+    p = torch.tensor([[3, 0, 0, 2]], dtype=torch.int32, device=DEV)
+    sv.beam_reorder(p, [s])
+    for w, v in enumerate((4, 1, 1, 3)):
+        assert s[0, w, 1, -1].item() == v + 10
+        assert s[0, w, 0].min().item() == v and s[0, w, 1, :-1].max().item() == v
