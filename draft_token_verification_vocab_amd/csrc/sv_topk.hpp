@@ -10,7 +10,7 @@
 // in LDS.  The k-th largest of the threads' own maxima is then a lower bound
 // tau of the k-th largest logit: k threads hold a logit that large.  Few
 // chunks reach tau (about k), so they are read again, their logits at or
-// above tau are collected and sorted.  A row whose collection overflows (many
+// above tau are collected and placed by counting.  A row whose collection overflows (many
 // equal logits) is settled by a radix selection over the keys instead, which
 // reads the row once per key byte.
 #pragma once
@@ -21,6 +21,8 @@ namespace sv {
 
 constexpr int kTopkMax = 128;        // longest list
 constexpr int kTopkCollect = 1024;   // logits one workgroup can collect
+constexpr int kTopkChunks = 1024;    // chunks it can note
+constexpr int kRankKeys = 256;       // collected keys placed by counting
 
 struct TopkArgs {
     const void *base;
@@ -151,10 +153,12 @@ __global__ __launch_bounds__(BLOCK) void topk_rows_kernel(TopkArgs a) {
     typename M16::type *cmax = reinterpret_cast<typename M16::type *>(dyn);  // [chunk][BLOCK]
     __shared__ unsigned long long sh_key[kTopkCollect];
     __shared__ uint32_t sh_m[BLOCK];
-    __shared__ uint32_t sh_wm[NW];
+    __shared__ uint16_t sh_item[kTopkChunks];
+    __shared__ uint32_t sh_wm[NW], sh_wl[NW];
     __shared__ double sh_s[NW];
     __shared__ uint32_t sh_tau;
-    __shared__ int sh_n;
+    __shared__ int sh_n, sh_items;
+    static_assert(BLOCK <= 1024, "a noted chunk is its index and its thread in 16 bits");
 
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wv = tid / kWave;
     const int64_t row = blockIdx.x / a.segs;
@@ -179,24 +183,32 @@ __global__ __launch_bounds__(BLOCK) void topk_rows_kernel(TopkArgs a) {
         acc.add(x, cm, c);
     });
 
-    // Row (segment) maximum and normaliser.
+    // Segment maximum, smallest visible thread maximum, and the normaliser.
+    const uint32_t masked = ordered_bits(kMasked);
     const uint32_t om = ordered_bits(acc.m + 0.0f);
     sh_m[tid] = om;
     const uint32_t wm = wave_max_u32(om);
-    if (lane == 0) sh_wm[wv] = wm;
-    if (tid == 0) sh_n = 0;
+    const uint32_t wl = wave_max_u32(om > masked ? ~om : 0u);
+    if (lane == 0) {
+        sh_wm[wv] = wm;
+        sh_wl[wv] = wl;
+    }
+    if (tid == 0) sh_n = sh_items = 0;
     __syncthreads();
-    uint32_t bm = sh_wm[0];
+    uint32_t bm = sh_wm[0], bl = sh_wl[0];
 #pragma unroll
-    for (int w = 1; w < NW; ++w) bm = sh_wm[w] > bm ? sh_wm[w] : bm;
+    for (int w = 1; w < NW; ++w) {
+        bm = sh_wm[w] > bm ? sh_wm[w] : bm;
+        bl = sh_wl[w] > bl ? sh_wl[w] : bl;
+    }
     const float M = from_ordered_bits(bm);
     const float ws = wave_sum_f32(acc.at(M, c));
     if (lane == 0) sh_s[wv] = static_cast<double>(ws);
 
     // tau: a value that at least k threads' maxima reach (all visible logits
     // when fewer than k threads hold one).  The first wave builds it bit by
-    // bit from the top, and stops as soon as few more than k threads reach it.
-    const uint32_t masked = ordered_bits(kMasked);
+    // bit below the bits that all visible maxima share, and stops as soon as
+    // few more than k threads reach it.
     if (wv == 0) {
         uint32_t key[NW];
         int seen = 0;
@@ -208,7 +220,10 @@ __global__ __launch_bounds__(BLOCK) void topk_rows_kernel(TopkArgs a) {
         uint32_t tau = 0;
         if (seen >= k) {
             const int enough = k + k / 4 + 4;
-            for (int bit = 31; bit >= 0; --bit) {
+            const uint32_t differ = bm ^ ~bl;
+            int bit = 31 - __clz(static_cast<int>(differ));
+            tau = differ == 0 ? bm : bm & ~((2u << bit) - 1u);
+            for (; bit >= 0; --bit) {
                 const uint32_t trial = tau | (1u << bit);
                 int n = 0;
 #pragma unroll
@@ -224,33 +239,41 @@ __global__ __launch_bounds__(BLOCK) void topk_rows_kernel(TopkArgs a) {
     __syncthreads();
     const uint32_t tau = sh_tau;
 
-    // Collect the logits at or above tau from the chunks that hold one.
+    // Note the chunks that hold a logit at or above tau, then read all of them
+    // together, a vector per thread (one memory latency, whatever the chunks'
+    // owners), and collect those logits.
+    const int nv = vend - vbeg;
     if (om >= tau) {
-        const int nv = vend - vbeg;
         for (int it = 0; it * kChunk + tid < nv; ++it) {
             const float cm = M16::get(cmax[it * BLOCK + tid]);
-            if (!(cm > kMasked) || ordered_bits(cm + 0.0f) < tau) continue;
+            if (cm > kMasked && ordered_bits(cm + 0.0f) >= tau) {
+                const int o = atomicAdd(&sh_items, 1);
+                if (o < kTopkChunks) sh_item[o] = static_cast<uint16_t>(it * 1024 + tid);
+            }
+        }
+    }
+    __syncthreads();
+    const int items = sh_items;
+    if (items <= kTopkChunks) {
+        for (int j = tid; j < items * UNROLL; j += BLOCK) {
+            const int item = sh_item[j / UNROLL];
+            const int vi = vbeg + (item >> 10) * kChunk + (j % UNROLL) * BLOCK + (item & 1023);
+            if (vi >= vend) continue;
+            const uint4 v = (vi + 1) * EPV <= V ? reinterpret_cast<const uint4 *>(rp)[vi]
+                                                : E::partial(rp, vi, V);
+            float x[EPV];
+            E::unpack(v, x);
 #pragma unroll
-            for (int u = 0; u < UNROLL; ++u) {
-                const int vi = vbeg + it * kChunk + u * BLOCK + tid;
-                if (vi >= vend) continue;
-                const uint4 v = (vi + 1) * EPV <= V
-                                    ? reinterpret_cast<const uint4 *>(rp)[vi]
-                                    : E::partial(rp, vi, V);
-                float x[EPV];
-                E::unpack(v, x);
-#pragma unroll
-                for (int e = 0; e < EPV; ++e) {
-                    if (x[e] > kMasked && ordered_bits(x[e] + 0.0f) >= tau) {
-                        const int o = atomicAdd(&sh_n, 1);
-                        if (o < kTopkCollect) sh_key[o] = topk_key(x[e], vi * EPV + e);
-                    }
+            for (int e = 0; e < EPV; ++e) {
+                if (x[e] > kMasked && ordered_bits(x[e] + 0.0f) >= tau) {
+                    const int o = atomicAdd(&sh_n, 1);
+                    if (o < kTopkCollect) sh_key[o] = topk_key(x[e], vi * EPV + e);
                 }
             }
         }
     }
     __syncthreads();
-    int n = sh_n;
+    int n = items <= kTopkChunks ? sh_n : kTopkCollect + 1;
     if (n > kTopkCollect) {
         // Too many logits reach tau: the k-th key itself, then exactly the
         // keys at or above it.
@@ -270,30 +293,46 @@ __global__ __launch_bounds__(BLOCK) void topk_rows_kernel(TopkArgs a) {
         __syncthreads();
         n = sh_n;
     }
-    int n2 = 2;
-    while (n2 < n) n2 *= 2;
-    for (int i = n + tid; i < n2; i += BLOCK) sh_key[i] = 0;
-    sort_keys<BLOCK>(sh_key, n2, tid);
 
-    double r = 0.0;
+    // Places: up to kRankKeys keys are counted against all others, a thread
+    // each; more are sorted first.
+    unsigned long long *list = a.list ? a.list + static_cast<int64_t>(blockIdx.x) * k : nullptr;
+    auto put = [&](int rank, uint64_t key) {
+        if (list) {
+            list[rank] = key;
+        } else {
+            a.values[row * k + rank] = key ? key_value(key) : -__builtin_inff();
+            a.ids[row * k + rank] = key ? key_id(key) : -1;
+        }
+    };
+    if (n <= kRankKeys) {
+        if (tid < n) {
+            const uint64_t mine = sh_key[tid];
+            int rank = 0;
+#pragma unroll 4
+            for (int j = 0; j < n; ++j) rank += sh_key[j] > mine;
+            if (rank < k) put(rank, mine);
+        }
+    } else {
+        int n2 = 2 * kRankKeys;
+        while (n2 < n) n2 *= 2;
+        for (int i = n + tid; i < n2; i += BLOCK) sh_key[i] = 0;
+        sort_keys<BLOCK>(sh_key, n2, tid);
+        for (int i = tid; i < k && i < n; i += BLOCK) put(i, sh_key[i]);
+    }
+    for (int i = n + tid; i < k; i += BLOCK) put(i, 0);
+
+    if (tid == BLOCK - 1 && (a.list || a.lse)) {
+        double r = 0.0;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) r += sh_s[w];
-    if (a.list) {
-        unsigned long long *dst = a.list + static_cast<int64_t>(blockIdx.x) * k;
-        for (int i = tid; i < k; i += BLOCK) dst[i] = i < n ? sh_key[i] : 0ull;
-        if (tid == 0)
-            a.seg_lse[blockIdx.x] = bm > masked ? static_cast<double>(M) * a.inv_t + log(r)
-                                                : -__builtin_inf();
-        return;
+        for (int w = 0; w < NW; ++w) r += sh_s[w];
+        const double l = bm > masked ? static_cast<double>(M) * a.inv_t + log(r)
+                                     : -__builtin_inf();
+        if (a.list)
+            a.seg_lse[blockIdx.x] = l;
+        else
+            a.lse[row] = static_cast<float>(l);
     }
-    for (int i = tid; i < k; i += BLOCK) {
-        a.values[row * k + i] = i < n ? key_value(sh_key[i]) : -__builtin_inff();
-        a.ids[row * k + i] = i < n ? key_id(sh_key[i]) : -1;
-    }
-    if (a.lse && tid == 0)
-        a.lse[row] = bm > masked
-                         ? static_cast<float>(static_cast<double>(M) * a.inv_t + log(r))
-                         : -__builtin_inff();
 }
 
 // ln of a sum of e^x over a row's segments: lanes hold segment lane's x.
