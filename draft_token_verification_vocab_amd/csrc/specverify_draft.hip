@@ -26,15 +26,13 @@ bool grid_fits(int64_t blocks, int block) {
 }
 
 // How the rows of a listing are cut into workgroups.
-//   Many rows: a workgroup per row (the row pass's shapes), as long as the
-// chunk maxima of a row fit its LDS (kWideChunks chunks: V <= 294912 in
-// bfloat16, 131072 in float32), else as many equal segments as that takes.
+//   Many rows: a workgroup per row (the row pass's shapes).
 //   Few rows: smaller workgroups, each row cut into segments until the GPU is
 // filled or a segment is one chunk.
-constexpr int kFillRows = 256;     // compute units
-constexpr int kSplitBlocks = 1024; // workgroups to aim for with few rows
-constexpr int kMaxMerge = 4096;    // keys one merge holds in LDS
-constexpr int kMaxListSegs = 64;   // one lane per segment in a merge
+constexpr int kFillRows = 256;      // compute units
+constexpr int kSplitBlocks = 1024;  // workgroups to aim for with few rows
+constexpr int kMaxMerge = 4096;     // keys one merge holds in LDS
+constexpr int kMaxListSegs = 64;    // one lane per segment in a merge
 constexpr int kSplitBlock = 256;
 constexpr int kMergeBlock = 256;
 
@@ -42,16 +40,16 @@ template <typename T>
 struct WideShape;
 template <>
 struct WideShape<uint16_t> {
-    static constexpr int block = 768, unroll = 2, chunks = 24;
+    static constexpr int block = 768, unroll = 2;
 };
 template <>
 struct WideShape<float> {
-    static constexpr int block = 512, unroll = 4, chunks = 16;
+    static constexpr int block = 512, unroll = 4;
 };
 
 struct ListPlan {
     bool wide;
-    int segs, seg_vecs, chunks;
+    int segs, seg_vecs;
     size_t list, seg_lse, total;  // workspace offsets
 };
 
@@ -62,27 +60,17 @@ template <typename T>
 ListPlan plan_lists_t(int64_t rows, int32_t V, int32_t k, int32_t lists, bool keep_lists) {
     using S = WideShape<T>;
     constexpr int epv = 16 / sizeof(T);
-    constexpr int wide_chunk = S::block * S::unroll, split_chunk = kSplitBlock * S::unroll;
+    constexpr int chunk = kSplitBlock * S::unroll;
     const int nvec = (V + epv - 1) / epv;
-    const int need = (nvec + wide_chunk * S::chunks - 1) / (wide_chunk * S::chunks);
+    const int by_len = (nvec + chunk - 1) / chunk;
     const int most = kMaxMerge / (lists * k) < kMaxListSegs ? kMaxMerge / (lists * k) : kMaxListSegs;
     ListPlan p{};
     int64_t want = rows > 0 ? (kSplitBlocks + rows - 1) / rows : 1;
-    const int by_len = (nvec + split_chunk - 1) / split_chunk;
     if (want > by_len) want = by_len;
     if (want > most) want = most;
     p.wide = rows >= kFillRows || want < 2;
-    p.segs = p.wide ? need : static_cast<int>(want);
-    // a split segment holds at most kWideChunks of the wide shape's bytes
-    const int chunk = p.wide ? wide_chunk : split_chunk;
-    int per = ((nvec + p.segs - 1) / p.segs + chunk - 1) / chunk;
-    if (!p.wide && per > 2 * S::chunks) {  // too long for a split segment's LDS
-        p.wide = true;
-        p.segs = need;
-        per = ((nvec + p.segs - 1) / p.segs + wide_chunk - 1) / wide_chunk;
-    }
-    p.chunks = per;
-    p.seg_vecs = per * (p.wide ? wide_chunk : split_chunk);
+    p.segs = p.wide ? 1 : static_cast<int>(want);
+    p.seg_vecs = p.wide ? nvec : ((nvec + p.segs - 1) / p.segs + chunk - 1) / chunk * chunk;
     p.segs = (nvec + p.seg_vecs - 1) / p.seg_vecs;
     if (p.segs > 1 || keep_lists) {
         const size_t n = static_cast<size_t>(rows) * p.segs;
@@ -103,13 +91,10 @@ template <typename T>
 void launch_lists_t(const ListPlan &p, const TopkArgs &a, int64_t rows, hipStream_t st) {
     using S = WideShape<T>;
     const dim3 grid(static_cast<unsigned>(rows * p.segs));
-    const size_t cell = sizeof(typename ChunkMax<T>::type);
     if (p.wide)
-        topk_rows_kernel<T, S::block, S::unroll>
-            <<<grid, dim3(S::block), p.chunks * S::block * cell, st>>>(a);
+        topk_rows_kernel<T, S::block, S::unroll><<<grid, dim3(S::block), 0, st>>>(a);
     else
-        topk_rows_kernel<T, kSplitBlock, S::unroll>
-            <<<grid, dim3(kSplitBlock), p.chunks * kSplitBlock * cell, st>>>(a);
+        topk_rows_kernel<T, kSplitBlock, S::unroll><<<grid, dim3(kSplitBlock), 0, st>>>(a);
 }
 
 void launch_lists(const ListPlan &p, const TopkArgs &a, int64_t rows, int32_t dtype,
@@ -167,7 +152,7 @@ void launch_distill_t(const DistillArgs &a, int64_t rows, hipStream_t st) {
 // Beam selection: lists a merge can hold.
 constexpr int kBeamMergeBlock = 512;
 constexpr int kMaxBeamKeys = 512;  // num_beams * num_out
-static_assert(kMaxBeamKeys * 8 <= kMaxMerge, "eight segments a row, enough for 2^20 floats");
+static_assert(kMaxBeamKeys <= kMaxMerge, "a merge holds the lists of a sequence's beams");
 
 spec_status check_beam(int32_t batch, int32_t beams, int32_t vocab, int32_t dtype,
                        int32_t num_out) {

@@ -5,14 +5,15 @@
 // the complement of the id, so that "larger key" is "earlier in the list" and
 // no two keys are equal.
 //
-// One workgroup streams a row (or a segment of it).  The pass keeps, beside
-// the online softmax, only each thread's maximum of every chunk (16 logits),
-// in LDS.  The k-th largest of the threads' own maxima is then a lower bound
-// tau of the k-th largest logit: k threads hold a logit that large.  Few
-// chunks reach tau (about k), so they are read again, their logits at or
-// above tau are collected and placed by counting.  A row whose collection overflows (many
-// equal logits) is settled by a radix selection over the keys instead, which
-// reads the row once per key byte.
+// One workgroup streams a row (or a segment of it).  A thread keeps, beside
+// the online softmax, only which of its chunks (16 logits) holds its maximum
+// and the largest maximum of its other chunks.  The k-th largest of the
+// threads' maxima is then a lower bound tau of the k-th largest logit: k
+// threads hold a logit that large.  Few chunks can reach tau (about k, and all
+// chunks of the few threads whose second chunk does), so those are read again,
+// their logits at or above tau are collected and placed by counting.  A row
+// whose collection overflows (many equal logits) is settled by a radix
+// selection over the keys instead, which reads the row once per key byte.
 #pragma once
 
 #include "sv_stream.hpp"
@@ -44,25 +45,6 @@ struct TopkArgs {
     // rows that take no part (beam selection), both nullable
     const uint8_t *ended;    // [rows]
     const float *scores;     // [rows]: -inf takes no part
-};
-
-template <typename T>
-struct ChunkMax;  // how a chunk's maximum is kept in LDS (exactly)
-template <>
-struct ChunkMax<uint16_t> {
-    using type = uint16_t;
-    __device__ static uint16_t put(float m) {
-        return static_cast<uint16_t>(__float_as_uint(m) >> 16);
-    }
-    __device__ static float get(uint16_t v) {
-        return __uint_as_float(static_cast<uint32_t>(v) << 16);
-    }
-};
-template <>
-struct ChunkMax<float> {
-    using type = float;
-    __device__ static float put(float m) { return m; }
-    __device__ static float get(float v) { return v; }
 };
 
 __device__ __forceinline__ uint64_t topk_key(float x, int id) {
@@ -144,21 +126,18 @@ __device__ __attribute__((noinline)) uint64_t radix_kth(const T *row, int ebeg, 
 template <typename T, int BLOCK, int UNROLL>
 __global__ __launch_bounds__(BLOCK) void topk_rows_kernel(TopkArgs a) {
     using E = Elem<T>;
-    using M16 = ChunkMax<T>;
     constexpr int EPV = E::kPerVec;
     constexpr int N = UNROLL * EPV;
     constexpr int NW = BLOCK / kWave;
     constexpr int kChunk = UNROLL * BLOCK;
-    extern __shared__ __align__(16) unsigned char dyn[];
-    typename M16::type *cmax = reinterpret_cast<typename M16::type *>(dyn);  // [chunk][BLOCK]
     __shared__ unsigned long long sh_key[kTopkCollect];
     __shared__ uint32_t sh_m[BLOCK];
-    __shared__ uint16_t sh_item[kTopkChunks];
+    __shared__ int sh_item[kTopkChunks];
     __shared__ uint32_t sh_wm[NW], sh_wl[NW];
     __shared__ double sh_s[NW];
     __shared__ uint32_t sh_tau;
     __shared__ int sh_n, sh_items;
-    static_assert(BLOCK <= 1024, "a noted chunk is its index and its thread in 16 bits");
+    static_assert(BLOCK <= 1024, "a noted chunk is its index and its thread");
 
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wv = tid / kWave;
     const int64_t row = blockIdx.x / a.segs;
@@ -173,13 +152,17 @@ __global__ __launch_bounds__(BLOCK) void topk_rows_kernel(TopkArgs a) {
     const int vend = vbeg + a.seg_vecs < nvec ? vbeg + a.seg_vecs : nvec;
 
     OnlineSum acc;
+    int best = 0;          // the chunk that holds the thread's maximum
+    float m2 = kMasked;    // the largest maximum of its other chunks
     stream_vectors<T, BLOCK, UNROLL>(rp, vbeg, vend, V, tid,
                                      [&](const uint4 (&buf)[UNROLL], int it) {
         float x[N];
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) E::unpack(buf[u], x + u * EPV);
         const float cm = chunk_max(x);
-        cmax[it * BLOCK + tid] = M16::put(cm);
+        m2 = __builtin_amdgcn_fmed3f(m2, cm, acc.m);  // m2 <= acc.m: the smaller of acc.m and
+                                                      // cm, unless both lie below m2 or above
+        best = cm > acc.m ? it : best;
         acc.add(x, cm, c);
     });
 
@@ -239,18 +222,17 @@ __global__ __launch_bounds__(BLOCK) void topk_rows_kernel(TopkArgs a) {
     __syncthreads();
     const uint32_t tau = sh_tau;
 
-    // Note the chunks that hold a logit at or above tau, then read all of them
-    // together, a vector per thread (one memory latency, whatever the chunks'
-    // owners), and collect those logits.
-    const int nv = vend - vbeg;
+    // Note the chunks that can hold a logit at or above tau: a thread's best
+    // chunk, or all its chunks when a second one reaches tau.  Then read all
+    // of them together, a vector per thread (one memory latency, whatever the
+    // chunks' owners), and collect those logits.
     if (om >= tau) {
-        for (int it = 0; it * kChunk + tid < nv; ++it) {
-            const float cm = M16::get(cmax[it * BLOCK + tid]);
-            if (cm > kMasked && ordered_bits(cm + 0.0f) >= tau) {
-                const int o = atomicAdd(&sh_items, 1);
-                if (o < kTopkChunks) sh_item[o] = static_cast<uint16_t>(it * 1024 + tid);
-            }
-        }
+        const bool one = ordered_bits(m2 + 0.0f) < tau;
+        const int last = (vend - vbeg - 1 - tid) / kChunk;
+        const int from = one ? best : 0, to = one ? best : last;
+        int o = atomicAdd(&sh_items, to - from + 1);
+        for (int it = from; it <= to; ++it, ++o)
+            if (o < kTopkChunks) sh_item[o] = it * 1024 + tid;
     }
     __syncthreads();
     const int items = sh_items;
