@@ -63,7 +63,8 @@ ListPlan plan_lists_t(int64_t rows, int32_t V, int32_t k, int32_t lists, bool ke
     constexpr int chunk = kSplitBlock * S::unroll;
     const int nvec = (V + epv - 1) / epv;
     const int by_len = (nvec + chunk - 1) / chunk;
-    const int most = kMaxMerge / (lists * k) < kMaxListSegs ? kMaxMerge / (lists * k) : kMaxListSegs;
+    const int fit = (keep_lists ? kMaxBeamKeys : kMaxMerge) / (lists * k);
+    const int most = fit < kMaxListSegs ? fit : kMaxListSegs;
     ListPlan p{};
     int64_t want = rows > 0 ? (kSplitBlocks + rows - 1) / rows : 1;
     if (want > by_len) want = by_len;
@@ -85,6 +86,13 @@ ListPlan plan_lists(int64_t rows, int32_t V, int32_t dtype, int32_t k, int32_t l
                     bool keep_lists) {
     return dtype == SPEC_DTYPE_BF16 ? plan_lists_t<uint16_t>(rows, V, k, lists, keep_lists)
                                     : plan_lists_t<float>(rows, V, k, lists, keep_lists);
+}
+
+// Vectors in one chunk of the plan's workgroups.
+int chunk_vecs(const ListPlan &p, int32_t dtype) {
+    if (dtype == SPEC_DTYPE_BF16)
+        return (p.wide ? WideShape<uint16_t>::block : kSplitBlock) * WideShape<uint16_t>::unroll;
+    return (p.wide ? WideShape<float>::block : kSplitBlock) * WideShape<float>::unroll;
 }
 
 template <typename T>
@@ -149,10 +157,25 @@ void launch_distill_t(const DistillArgs &a, int64_t rows, hipStream_t st) {
         <<<dim3(static_cast<unsigned>(rows)), dim3(S::block), map, st>>>(a);
 }
 
-// Beam selection: lists a merge can hold.
+// Beam selection.
 constexpr int kBeamMergeBlock = 512;
-constexpr int kMaxBeamKeys = 512;  // num_beams * num_out
-static_assert(kMaxBeamKeys <= kMaxMerge, "a merge holds the lists of a sequence's beams");
+
+// Bound on how far the listing's float sums can move the difference of two
+// beams' log-normalisers.  A term's exponent d = (l - max) log2(e)/T is off by
+// a half step (2^-24 of |d|) each for the difference and the product, and by
+// the constant's own error; the terms' mean |d| is at most log2 V.  exp2 is
+// off by one step, and every addition that a term goes through by half a step:
+// 5 in its chunk, one per chunk of its thread, 6 across the wave.
+double near_bound(const ListPlan &p, int32_t V, int32_t dtype, float temperature) {
+    const double h = 0x1p-24;
+    const double exact = kLog2eD / static_cast<double>(temperature);
+    const double constant = std::fabs(static_cast<double>(log2e_over(temperature)) / exact - 1.0);
+    const int chunk = chunk_vecs(p, dtype);
+    const double adds = 11 + (p.seg_vecs + chunk - 1) / chunk;
+    const double one = kLn2 * std::log2(static_cast<double>(V)) * (2 * h + constant) + 2 * h +
+                       adds * h;
+    return 2.0 * one * 1.0001;  // the products of the errors
+}
 
 spec_status check_beam(int32_t batch, int32_t beams, int32_t vocab, int32_t dtype,
                        int32_t num_out) {
@@ -355,13 +378,13 @@ spec_status spec_beam_select(const void *logits, int64_t row_stride, const float
     a.segs = p.segs;
     a.eos = eos;
     a.inv_t = t.inv_t;
-    const size_t keys = sizeof(double) * num_beams * p.segs * num_out;
+    a.near = near_bound(p, vocab, dtype, temperature);
     if (dtype == SPEC_DTYPE_BF16)
         beam_merge_kernel<uint16_t, kBeamMergeBlock>
-            <<<dim3(batch), dim3(kBeamMergeBlock), keys, st>>>(a);
+            <<<dim3(batch), dim3(kBeamMergeBlock), 0, st>>>(a);
     else
         beam_merge_kernel<float, kBeamMergeBlock>
-            <<<dim3(batch), dim3(kBeamMergeBlock), keys, st>>>(a);
+            <<<dim3(batch), dim3(kBeamMergeBlock), 0, st>>>(a);
     return launch_status();
 }
 

@@ -10,7 +10,7 @@
 //
 // The listing's log-normalisers come from float sums.  Where two continuations
 // of different beams that compete for a place lie closer than those sums'
-// error, the merge computes the normalisers of the beams concerned again in
+// error bound, the merge computes the normalisers of the beams concerned again in
 // double and places the continuations anew, so the choice is that of the exact
 // scores.
 #pragma once
@@ -22,12 +22,8 @@ namespace sv {
 constexpr int kMaxBeams = 32;
 constexpr int kMaxBeamOut = 64;
 
-// Bound on the error of the difference of two beams' log-normalisers.  Each
-// is off by at most (V <= 2^20, mean exponent |d| <= 20): four half steps of
-// |d| ln 2 (difference, log2(e), its division by T, product), one step of exp2
-// and half a step for each of at most 60 additions a term goes through:
-// (4 * 20 * 0.7 + 2 + 60) * 2^-24 = 7.1e-6.
-constexpr double kNearBeam = 1.5e-5;
+// Keys one merge takes: beams x segments x num_out.
+constexpr int kMaxBeamKeys = 512;
 
 struct BeamArgs {
     const void *base;                // logits, [B][W] rows
@@ -47,16 +43,49 @@ struct BeamArgs {
     int32_t eos;
     int32_t pad_;
     double inv_t;
+    double near;  // scores of two beams closer than this are compared exactly
 };
+
+// 2^d in double, d <= 0: the Taylor series of e^(f ln 2) for the fraction f in
+// [-1/2, 1/2], cut where the next term is below 2^-52.
+__device__ __forceinline__ double exp2_f64(double d) {
+    const double n = __builtin_rint(d);
+    const double f = (d - n) * kLn2;
+    double p = 1.0 / 479001600.0;  // 1 / 12!
+    p = fma(p, f, 1.0 / 39916800.0);
+    p = fma(p, f, 1.0 / 3628800.0);
+    p = fma(p, f, 1.0 / 362880.0);
+    p = fma(p, f, 1.0 / 40320.0);
+    p = fma(p, f, 1.0 / 5040.0);
+    p = fma(p, f, 1.0 / 720.0);
+    p = fma(p, f, 1.0 / 120.0);
+    p = fma(p, f, 1.0 / 24.0);
+    p = fma(p, f, 1.0 / 6.0);
+    p = fma(p, f, 0.5);
+    p = fma(p, f, 1.0);
+    p = fma(p, f, 1.0);
+    return ldexp(p, static_cast<int>(n));
+}
 
 // ln sum e^(l/T) of a row in double, given its largest visible logit M.
 template <typename T, int BLOCK>
 __device__ __attribute__((noinline)) double exact_normaliser(const T *row, int V, float M,
                                                             double inv_t, double *sh, int tid) {
+    using E = Elem<T>;
+    constexpr int EPV = E::kPerVec;
+    const int nvec = (V + EPV - 1) / EPV;
+    const double c = inv_t * kLog2eD;
     double s = 0.0;
-    for (int i = tid; i < V; i += BLOCK) {
-        const float x = Elem<T>::at(row, i);
-        if (x > kMasked) s += exp((static_cast<double>(x) - static_cast<double>(M)) * inv_t);
+    for (int i = tid; i < nvec; i += BLOCK) {
+        const uint4 v = (i + 1) * EPV <= V ? reinterpret_cast<const uint4 *>(row)[i]
+                                           : E::partial(row, i, V);
+        float x[EPV];
+        E::unpack(v, x);
+#pragma unroll
+        for (int e = 0; e < EPV; ++e) {
+            const double t = exp2_f64((static_cast<double>(x[e]) - static_cast<double>(M)) * c);
+            s += x[e] > kMasked ? t : 0.0;
+        }
     }
     s = wave_sum_f64(s);
     __syncthreads();  // sh is free
@@ -68,140 +97,167 @@ __device__ __attribute__((noinline)) double exact_normaliser(const T *row, int V
     return static_cast<double>(M) * inv_t + log(t);
 }
 
-// One workgroup per sequence.
+// One workgroup per sequence.  The segments' lists of a beam are joined first
+// (whole keys, counted); then every continuation's place among the other
+// beams' sorted scores is found by bisection, by as many lanes as there are
+// for each.
 template <typename T, int BLOCK>
 __global__ __launch_bounds__(BLOCK) void beam_merge_kernel(BeamArgs a) {
-    extern __shared__ __align__(16) unsigned char dyn[];
-    double *key = reinterpret_cast<double *>(dyn);  // [W][segs][n], -inf: no continuation
+    static_assert(BLOCK >= kMaxBeamKeys, "a thread per key");
+    __shared__ unsigned long long sh_in[kMaxBeamKeys];   // [W][segs][n]
+    __shared__ unsigned long long sh_key[kMaxBeamKeys];  // [W][n], 0 after the last
+    __shared__ double sh_score[kMaxBeamKeys];            // [W][n], -inf after the last
     __shared__ double sh_lse[kMaxBeams], sh_red[BLOCK / kWave];
+    __shared__ float sh_prior[kMaxBeams];                // -inf: takes no part
+    __shared__ int sh_ended[kMaxBeams];
     __shared__ int sh_pick[kMaxBeamOut];
-    __shared__ unsigned int sh_near[(4096 + 31) / 32];
     __shared__ unsigned int sh_again;  // beams whose normaliser is needed in double
     __shared__ int sh_count;
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wv = tid / kWave;
     const int b = blockIdx.x, W = a.W, n = a.n, segs = a.segs;
-    const int per = segs * n, total = W * per;
-    const unsigned long long *list = a.list + static_cast<int64_t>(b) * total;
+    const int per = segs * n, total = W * n;
     const double inf = __builtin_inf();
 
-    if (tid == 0) {
-        sh_again = 0;
-        sh_count = 0;
+    // The lists of beams that take no part, or have ended, were not written.
+    if (tid < W * per) {
+        const unsigned long long k = a.list[static_cast<int64_t>(b) * W * per + tid];
+        (segs == 1 ? sh_key : sh_in)[tid] = k;
     }
-    for (int i = tid; i < (total + 31) / 32; i += BLOCK) sh_near[i] = 0;
-    for (int w = wv; w < W; w += BLOCK / kWave) {
-        const double x = lane < segs ? a.seg_lse[(static_cast<int64_t>(b) * W + w) * segs + lane]
-                                     : -inf;
-        const double l = wave_log_sum(x, lane, segs);
-        if (lane == 0) sh_lse[w] = l;
+    if (tid < W) {
+        const float s = a.scores[static_cast<int64_t>(b) * W + tid];
+        sh_prior[tid] = s > -__builtin_inff() ? s : -__builtin_inff();
+        sh_ended[tid] = a.ended ? a.ended[static_cast<int64_t>(b) * W + tid] != 0 : 0;
+    }
+    for (int q = wv; q < W; q += BLOCK / kWave) {
+        const int64_t at = (static_cast<int64_t>(b) * W + q) * segs;
+        if (segs == 1) {
+            if (lane == 0) sh_lse[q] = a.seg_lse[at];
+        } else {
+            const double l = wave_log_sum(lane < segs ? a.seg_lse[at + lane] : -inf, lane, segs);
+            if (lane == 0) sh_lse[q] = l;
+        }
+    }
+    if (tid == 0) sh_again = 0;
+    if (segs > 1) {
+        if (tid < total) sh_key[tid] = 0;
+        __syncthreads();
+        int share = 1;
+        while (share < kWave && W * per * share * 2 <= BLOCK) share *= 2;
+        const int at = tid / share, w = at / per;
+        const unsigned long long mine = at < W * per ? sh_in[at] : 0;
+        int rank = 0;
+        if (mine)
+#pragma unroll 4
+            for (int j = tid & (share - 1); j < per; j += share)
+                rank += sh_in[w * per + j] > mine;
+        for (int o = 1; o < share; o *= 2) rank += __shfl_xor(rank, o, kWave);
+        if (mine && (tid & (share - 1)) == 0 && rank < n) sh_key[w * n + rank] = mine;
     }
     __syncthreads();
 
-    // Scores of the continuations.  A beam that has ended continues once, as
-    // it is; a beam of score -inf (or NaN) has none.
-    auto score_all = [&]() {
-        for (int i = tid; i < total; i += BLOCK) {
-            const int w = i / per;
-            const int64_t bw = static_cast<int64_t>(b) * W + w;
-            const float s = a.scores[bw];
-            double x = -inf;
-            if (s > -__builtin_inff()) {
-                if (a.ended && a.ended[bw])
-                    x = i == w * per ? static_cast<double>(s) : -inf;
-                else if (const unsigned long long k = list[i])
-                    x = static_cast<double>(s) +
-                        (static_cast<double>(key_value(k)) * a.inv_t - sh_lse[w]);
-            }
-            key[i] = x;
+    // Scores of the continuations, sorted within each beam.  A beam that has
+    // ended continues once, as it is.
+    auto score = [&]() {
+        if (tid >= total) return;
+        const int w = tid / n;
+        const double s = static_cast<double>(sh_prior[w]);
+        const unsigned long long key = sh_key[tid];
+        double x = -inf;
+        if (s > -inf) {
+            if (sh_ended[w])
+                x = tid == w * n ? s : -inf;
+            else if (key)
+                x = s + (static_cast<double>(key_value(key)) * a.inv_t - sh_lse[w]);
         }
+        sh_score[tid] = x;
     };
 
-    // Places by bisection in every other list.  tol > 0 also notes the
-    // continuations within tol of one of another beam.
-    auto place_all = [&](double tol) {
-        for (int i = tid; i < total; i += BLOCK) {
-            const double x = key[i];
-            if (!(x > -inf)) continue;
-            const int own = i / n, w = i / per;
-            int rank = i - own * n;
-            bool near = false;
-            for (int l = 0; l < W * segs; ++l) {
-                if (l == own) continue;
-                const double *o = key + l * n;
-                const bool other = l / segs != w;
-                const double slack = other ? tol : 0.0;
-                int lo = 0, hi = n;  // entries above x + slack
+    // Places among all continuations.  near > 0 also finds those within it of
+    // a continuation of another beam; returns whether this lane's is one.
+    int share = 1;
+    while (share < kWave && share < W && total * share * 2 <= BLOCK) share *= 2;
+    auto place = [&](double near) {
+        const int at = tid / share;
+        if (tid == 0) sh_count = 0;
+        __syncthreads();
+        const double x = at < total ? sh_score[at] : -inf;
+        const int own = at / n;
+        int rank = 0, close = 0;
+        if (x > -inf) {
+            for (int q = tid & (share - 1); q < W; q += share) {
+                if (q == own) {
+                    rank += at - own * n;
+                    continue;
+                }
+                const double *o = sh_score + q * n;
+                int lo = 0, hi = n;  // scores above x + near
                 while (lo < hi) {
                     const int mid = (lo + hi) / 2;
-                    if (o[mid] > x + slack)
+                    if (o[mid] > x + near)
                         lo = mid + 1;
                     else
                         hi = mid;
                 }
                 rank += lo;
-                for (; lo < n && o[lo] >= x - slack && o[lo] > -inf; ++lo) {
-                    near = near || (other && tol > 0.0);
-                    rank += o[lo] > x || (o[lo] == x && l < own);
+                for (; lo < n && o[lo] >= x - near && o[lo] > -inf; ++lo) {
+                    close = 1;
+                    rank += o[lo] > x || (o[lo] == x && q < own);
                 }
             }
-            if (near) atomicOr(&sh_near[i >> 5], 1u << (i & 31));
-            atomicAdd(&sh_count, 1);
-            if (rank < n) sh_pick[rank] = i;
         }
+        for (int o = 1; o < share; o *= 2) {
+            rank += __shfl_xor(rank, o, kWave);
+            close |= __shfl_xor(close, o, kWave);
+        }
+        const bool there = x > -inf && (tid & (share - 1)) == 0;
+        if (there && rank < n) sh_pick[rank] = at;
+        const uint64_t votes = __ballot(there);
+        if (lane == 0 && votes) atomicAdd(&sh_count, __popcll(votes));
+        __syncthreads();
+        return close != 0 && there;
     };
 
-    score_all();
-    __syncthreads();
-    place_all(kNearBeam);
-    __syncthreads();
-    // A near continuation matters when it is chosen or could be.
-    const double worst = sh_count >= n ? key[sh_pick[n - 1]] : -inf;
-    for (int i = tid; i < total; i += BLOCK) {
-        if (!((sh_near[i >> 5] >> (i & 31)) & 1u) || key[i] < worst - kNearBeam) continue;
-        const int w = i / per;
-        if (!(a.ended && a.ended[static_cast<int64_t>(b) * W + w])) atomicOr(&sh_again, 1u << w);
+    score();
+    if (place(a.near)) {
+        // a near continuation matters when it is chosen or could be
+        const int at = tid / share;
+        const double worst = sh_count >= n ? sh_score[sh_pick[n - 1]] : -inf;
+        if (sh_score[at] >= worst - a.near && !sh_ended[at / n]) atomicOr(&sh_again, 1u << (at / n));
     }
     __syncthreads();
     unsigned int again = sh_again;
     if (again) {
         while (again) {
-            const int w = __ffs(static_cast<int>(again)) - 1;
+            const int q = __ffs(static_cast<int>(again)) - 1;
             again &= again - 1;
-            const int64_t bw = static_cast<int64_t>(b) * W + w;
-            float M = -__builtin_inff();
-            for (int s = 0; s < segs; ++s) {
-                const unsigned long long k = list[w * per + s * n];
-                if (k) M = fmaxf(M, key_value(k));
-            }
-            const double l = exact_normaliser<T, BLOCK>(
-                static_cast<const T *>(a.base) + bw * a.stride, a.V, M, a.inv_t, sh_red, tid);
-            if (tid == 0) sh_lse[w] = l;
+            const T *row = static_cast<const T *>(a.base) +
+                           (static_cast<int64_t>(b) * W + q) * a.stride;
+            const double l = exact_normaliser<T, BLOCK>(row, a.V, key_value(sh_key[q * n]),
+                                                        a.inv_t, sh_red, tid);
+            if (tid == 0) sh_lse[q] = l;
         }
-        if (tid == 0) sh_count = 0;
         __syncthreads();
-        score_all();
-        __syncthreads();
-        place_all(0.0);
-        __syncthreads();
+        score();
+        place(0.0);
     }
 
     const int count = sh_count;
-    for (int i = tid; i < n; i += BLOCK) {
-        const int64_t o = static_cast<int64_t>(b) * n + i;
-        if (i >= count) {
-            a.out_scores[o] = -__builtin_inff();
-            a.parents[o] = -1;
-            a.tokens[o] = -1;
-            if (a.ended_out) a.ended_out[o] = 0;
-            continue;
+    if (tid < n) {
+        const int64_t o = static_cast<int64_t>(b) * n + tid;
+        float s = -__builtin_inff();
+        int parent = -1, token = -1, over = 0;
+        if (tid < count) {
+            const int at = sh_pick[tid];
+            parent = at / n;
+            over = sh_ended[parent];
+            token = over ? a.eos : key_id(sh_key[at]);
+            over |= token == a.eos;
+            s = static_cast<float>(sh_score[at]);
         }
-        const int at = sh_pick[i], w = at / per;
-        const bool over = a.ended && a.ended[static_cast<int64_t>(b) * W + w];
-        const int token = over ? a.eos : key_id(list[at]);
-        a.out_scores[o] = static_cast<float>(key[at]);
-        a.parents[o] = w;
+        a.out_scores[o] = s;
+        a.parents[o] = parent;
         a.tokens[o] = token;
-        if (a.ended_out) a.ended_out[o] = over || token == a.eos;
+        if (a.ended_out) a.ended_out[o] = static_cast<uint8_t>(over);
     }
 }
 

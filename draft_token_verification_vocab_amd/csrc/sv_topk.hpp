@@ -6,13 +6,13 @@
 // no two keys are equal.
 //
 // One workgroup streams a row (or a segment of it).  A thread keeps, beside
-// the online softmax, only which of its chunks (16 logits) holds its maximum
-// and the largest maximum of its other chunks.  The k-th largest of the
-// threads' maxima is then a lower bound tau of the k-th largest logit: k
-// threads hold a logit that large.  Few chunks can reach tau (about k, and all
-// chunks of the few threads whose second chunk does), so those are read again,
-// their logits at or above tau are collected and placed by counting.  A row
-// whose collection overflows (many equal logits) is settled by a radix
+// the online softmax, its chunk (16 logits) with the largest maximum in LDS,
+// which chunk comes second, and the second and third largest maximum.  The
+// k-th largest of the threads' maxima is then a lower bound tau of the k-th
+// largest logit: k threads hold a logit that large.  The logits at or above
+// tau lie in about k best chunks, the few second chunks that reach tau (read
+// again), and all chunks of the very few threads with a third one; they are
+// collected and placed by counting.  A row whose collection overflows (many equal logits) is settled by a radix
 // selection over the keys instead, which reads the row once per key byte.
 #pragma once
 
@@ -130,6 +130,7 @@ __global__ __launch_bounds__(BLOCK) void topk_rows_kernel(TopkArgs a) {
     constexpr int N = UNROLL * EPV;
     constexpr int NW = BLOCK / kWave;
     constexpr int kChunk = UNROLL * BLOCK;
+    __shared__ uint4 sh_saved[UNROLL][BLOCK];  // the threads' best chunks
     __shared__ unsigned long long sh_key[kTopkCollect];
     __shared__ uint32_t sh_m[BLOCK];
     __shared__ int sh_item[kTopkChunks];
@@ -152,17 +153,23 @@ __global__ __launch_bounds__(BLOCK) void topk_rows_kernel(TopkArgs a) {
     const int vend = vbeg + a.seg_vecs < nvec ? vbeg + a.seg_vecs : nvec;
 
     OnlineSum acc;
-    int best = 0;          // the chunk that holds the thread's maximum
-    float m2 = kMasked;    // the largest maximum of its other chunks
+    int best = 0, second = 0;             // the chunks with the thread's largest maxima
+    float m2 = kMasked, m3 = kMasked;     // the second and third largest chunk maximum
     stream_vectors<T, BLOCK, UNROLL>(rp, vbeg, vend, V, tid,
                                      [&](const uint4 (&buf)[UNROLL], int it) {
         float x[N];
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) E::unpack(buf[u], x + u * EPV);
         const float cm = chunk_max(x);
-        m2 = __builtin_amdgcn_fmed3f(m2, cm, acc.m);  // m2 <= acc.m: the smaller of acc.m and
-                                                      // cm, unless both lie below m2 or above
-        best = cm > acc.m ? it : best;
+        // acc.m >= m2 >= m3: the new second and third largest are medians
+        m3 = __builtin_amdgcn_fmed3f(m3, cm, m2);
+        second = cm > acc.m ? best : (cm > m2 ? it : second);
+        m2 = __builtin_amdgcn_fmed3f(m2, cm, acc.m);
+        if (cm > acc.m) {
+            best = it;
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u) sh_saved[u][tid] = buf[u];
+        }
         acc.add(x, cm, c);
     });
 
@@ -222,39 +229,51 @@ __global__ __launch_bounds__(BLOCK) void topk_rows_kernel(TopkArgs a) {
     __syncthreads();
     const uint32_t tau = sh_tau;
 
-    // Note the chunks that can hold a logit at or above tau: a thread's best
-    // chunk, or all its chunks when a second one reaches tau.  Then read all
-    // of them together, a vector per thread (one memory latency, whatever the
-    // chunks' owners), and collect those logits.
-    if (om >= tau) {
-        const bool one = ordered_bits(m2 + 0.0f) < tau;
-        const int last = (vend - vbeg - 1 - tid) / kChunk;
-        const int from = one ? best : 0, to = one ? best : last;
-        int o = atomicAdd(&sh_items, to - from + 1);
-        for (int it = from; it <= to; ++it, ++o)
-            if (o < kTopkChunks) sh_item[o] = it * 1024 + tid;
-    }
-    __syncthreads();
-    const int items = sh_items;
-    if (items <= kTopkChunks) {
-        for (int j = tid; j < items * UNROLL; j += BLOCK) {
-            const int item = sh_item[j / UNROLL];
-            const int vi = vbeg + (item >> 10) * kChunk + (j % UNROLL) * BLOCK + (item & 1023);
-            if (vi >= vend) continue;
-            const uint4 v = (vi + 1) * EPV <= V ? reinterpret_cast<const uint4 *>(rp)[vi]
-                                                : E::partial(rp, vi, V);
-            float x[EPV];
-            E::unpack(v, x);
+    // Collect the logits at or above tau: those of a thread's best chunk from
+    // LDS, and of its second chunk, or all its chunks when a third reaches
+    // tau, from the row again, noted first and then read together, a vector
+    // per thread (one memory latency, whatever the chunks' owners).
+    auto collect = [&](const uint4 &v, int vi) {
+        float x[EPV];
+        E::unpack(v, x);
+        uint32_t hit = 0;
 #pragma unroll
-            for (int e = 0; e < EPV; ++e) {
-                if (x[e] > kMasked && ordered_bits(x[e] + 0.0f) >= tau) {
-                    const int o = atomicAdd(&sh_n, 1);
-                    if (o < kTopkCollect) sh_key[o] = topk_key(x[e], vi * EPV + e);
-                }
-            }
+        for (int e = 0; e < EPV; ++e)
+            hit |= (x[e] > kMasked && ordered_bits(x[e] + 0.0f) >= tau) ? 1u << e : 0u;
+        if (hit == 0) return;
+        int o = atomicAdd(&sh_n, __popc(hit));
+#pragma unroll
+        for (int e = 0; e < EPV; ++e) {
+            if (((hit >> e) & 1u) && o < kTopkCollect) sh_key[o] = topk_key(x[e], vi * EPV + e);
+            o += (hit >> e) & 1u;
+        }
+    };
+    if (om >= tau) {
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u)
+            collect(sh_saved[u][tid], vbeg + best * kChunk + u * BLOCK + tid);
+        if (ordered_bits(m2 + 0.0f) >= tau) {
+            const bool two = ordered_bits(m3 + 0.0f) < tau;
+            const int from = two ? second : 0;
+            const int to = two ? second : (vend - vbeg - 1 - tid) / kChunk;
+            int o = atomicAdd(&sh_items, to - from + 1);
+            for (int it = from; it <= to; ++it, ++o)
+                if (o < kTopkChunks) sh_item[o] = it == best ? -1 : it * 1024 + tid;
         }
     }
     __syncthreads();
+    const int items = sh_items;
+    if (items > 0) {  // the same for every thread
+        for (int j = tid; j < items * UNROLL && items <= kTopkChunks; j += BLOCK) {
+            const int item = sh_item[j / UNROLL];
+            const int vi = vbeg + (item >> 10) * kChunk + (j % UNROLL) * BLOCK + (item & 1023);
+            if (item < 0 || vi >= vend) continue;
+            collect((vi + 1) * EPV <= V ? reinterpret_cast<const uint4 *>(rp)[vi]
+                                        : E::partial(rp, vi, V),
+                    vi);
+        }
+        __syncthreads();
+    }
     int n = items <= kTopkChunks ? sh_n : kTopkCollect + 1;
     if (n > kTopkCollect) {
         // Too many logits reach tau: the k-th key itself, then exactly the
@@ -288,13 +307,16 @@ __global__ __launch_bounds__(BLOCK) void topk_rows_kernel(TopkArgs a) {
         }
     };
     if (n <= kRankKeys) {
-        if (tid < n) {
-            const uint64_t mine = sh_key[tid];
-            int rank = 0;
+        // as many lanes per key as the workgroup has, each against its share
+        int share = 1;
+        while (share < 16 && n * share * 2 <= BLOCK) share *= 2;
+        const int at = tid / share;
+        const uint64_t mine = at < n ? sh_key[at] : 0;
+        int rank = 0;
 #pragma unroll 4
-            for (int j = 0; j < n; ++j) rank += sh_key[j] > mine;
-            if (rank < k) put(rank, mine);
-        }
+        for (int j = tid & (share - 1); j < n; j += share) rank += sh_key[j] > mine;
+        for (int o = 1; o < share; o *= 2) rank += __shfl_xor(rank, o, kWave);
+        if (at < n && (tid & (share - 1)) == 0 && rank < k) put(rank, mine);
     } else {
         int n2 = 2 * kRankKeys;
         while (n2 < n) n2 *= 2;
