@@ -9,7 +9,6 @@ of the computation runs in the library's kernels; there is no fallback.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -743,14 +742,21 @@ def ngram_propose(context: torch.Tensor, lengths: torch.Tensor, n_min: int, n_ma
 # ---------------------------------------------------------------------------
 # Draft-model calls: top-logit lists, distillation, beam search
 # ---------------------------------------------------------------------------
-@contextlib.contextmanager
-def _on(device: torch.device):
-    """The device current for a call's launches, as the library expects."""
-    if device.index == torch.cuda.current_device():
-        yield
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _enqueue(what: str, dev: torch.device, fn, *args):
+    """Call the library with dev current, as its launches expect, on dev's
+    current stream (the last argument)."""
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    if dev.index == torch.cuda.current_device():
+        status = fn(*args, stream)
     else:
-        with torch.cuda.device(device):
-            yield
+        with torch.cuda.device(dev):
+            status = fn(*args, stream)
+    if status:
+        _check(status, what)
 
 
 def row_topk(logits: torch.Tensor, k: int, *, temperature: float = 1.0,
@@ -776,11 +782,9 @@ def row_topk(logits: torch.Tensor, k: int, *, temperature: float = 1.0,
         workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
     else:
         _need_cuda(workspace, "workspace", dev)
-    with _on(dev):
-        _check(L.spec_row_topk(_ptr(logits), rows, V, S, dt, float(temperature), k,
-                               _ptr(res["values"]), _ptr(res["ids"]), _ptr(res.get("lse")),
-                               _ptr(workspace), 0 if workspace is None else _nbytes(workspace),
-                               _stream(dev)), "spec_row_topk")
+    _enqueue("spec_row_topk", dev, L.spec_row_topk, logits.data_ptr(), rows, V, S, dt, temperature,
+             k, res["values"].data_ptr(), res["ids"].data_ptr(), _addr(res.get("lse")),
+             _addr(workspace), 0 if workspace is None else _nbytes(workspace))
     return res
 
 
@@ -819,10 +823,9 @@ def distill_loss(student: torch.Tensor, ids: torch.Tensor, logits: torch.Tensor,
     saved = None
     if state:
         saved = torch.empty(L.spec_distill_state_bytes(rows), dtype=torch.uint8, device=dev)
-    with _on(dev):
-        _check(L.spec_distill_loss(_ptr(student), _ptr(ids), _ptr(logits), _ptr(lse), _ptr(keep),
-                                   ctypes.byref(p), _ptr(loss), _ptr(saved), _stream(dev)),
-               "spec_distill_loss")
+    _enqueue("spec_distill_loss", dev, L.spec_distill_loss, student.data_ptr(), ids.data_ptr(),
+             logits.data_ptr(), _addr(lse), _addr(keep), ctypes.byref(p), loss.data_ptr(),
+             _addr(saved))
     return loss, saved
 
 
@@ -839,10 +842,9 @@ def distill_grad(student: torch.Tensor, ids: torch.Tensor, logits: torch.Tensor,
     L = load()
     _need_cuda(state, "state", dev, nbytes=L.spec_distill_state_bytes(rows))
     grad = torch.empty_like(student) if out is None else out
-    with _on(dev):
-        _check(L.spec_distill_grad(_ptr(student), _ptr(ids), _ptr(logits), _ptr(state),
-                                   _ptr(grad_loss), ctypes.byref(p), _ptr(grad), _stream(dev)),
-               "spec_distill_grad")
+    _enqueue("spec_distill_grad", dev, L.spec_distill_grad, student.data_ptr(), ids.data_ptr(),
+             logits.data_ptr(), state.data_ptr(), _addr(grad_loss), ctypes.byref(p),
+             grad.data_ptr())
     return grad
 
 
@@ -857,10 +859,9 @@ def distill_step(student: torch.Tensor, ids: torch.Tensor, logits: torch.Tensor,
                                  out)
     loss = torch.empty(student.shape[:-1], dtype=torch.float32, device=dev)
     grad = torch.empty_like(student) if out is None else out
-    with _on(dev):
-        _check(load().spec_distill_step(_ptr(student), _ptr(ids), _ptr(logits), _ptr(lse),
-                                        _ptr(keep), _ptr(grad_loss), ctypes.byref(p), _ptr(loss),
-                                        _ptr(grad), _stream(dev)), "spec_distill_step")
+    _enqueue("spec_distill_step", dev, load().spec_distill_step, student.data_ptr(),
+             ids.data_ptr(), logits.data_ptr(), _addr(lse), _addr(keep), _addr(grad_loss),
+             ctypes.byref(p), loss.data_ptr(), grad.data_ptr())
     return loss, grad
 
 
@@ -892,12 +893,10 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, num_out: int, *,
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
     else:
         _need_cuda(workspace, "workspace", dev)
-    with _on(dev):
-        _check(L.spec_beam_select(_ptr(logits), S, _ptr(scores), _ptr(ended), B, W, V, dt,
-                                  float(temperature), n, int(eos), _ptr(res["scores"]),
-                                  _ptr(res["parents"]), _ptr(res["tokens"]), _ptr(res["ended"]),
-                                  _ptr(workspace), _nbytes(workspace), _stream(dev)),
-               "spec_beam_select")
+    _enqueue("spec_beam_select", dev, L.spec_beam_select, logits.data_ptr(), S, scores.data_ptr(),
+             _addr(ended), B, W, V, dt, temperature, n, eos, res["scores"].data_ptr(),
+             res["parents"].data_ptr(), res["tokens"].data_ptr(), res["ended"].data_ptr(),
+             workspace.data_ptr(), _nbytes(workspace))
     return res
 
 
@@ -919,27 +918,33 @@ def beam_reorder(parents: torch.Tensor, states, outs=None, *,
     if lengths is not None:
         _need_cuda(lengths, "lengths", dev, torch.int32, (B,))
     W = states[0].shape[1] if states and states[0].dim() > 1 else n
-    table, used = (_BeamState * max(len(states), 1))(), 0
+    if lengths is not None and position_dim < 2:
+        raise ValueError("position_dim %d is no dimension of a beam's state" % position_dim)
+    table, used, shape = (_BeamState * max(len(states), 1))(), 0, None
     for i, (src, dst) in enumerate(zip(states, outs)):
-        shape = tuple(src.shape)
-        if len(shape) < 2 or shape[:2] != (B, W):
-            raise ValueError("states[%d] must have shape (%d, %d, ...), not %s" % (i, B, W, shape))
+        if src.shape != shape:
+            shape = src.shape
+            if len(shape) < 2 or shape[:2] != (B, W):
+                raise ValueError("states[%d] must have shape (%d, %d, ...), not %s"
+                                 % (i, B, W, tuple(shape)))
+            if lengths is not None and position_dim >= len(shape):
+                raise ValueError("states[%d] has no dimension %d" % (i, position_dim))
+            out_shape = (B, n) + shape[2:]
+            row, seg, pos = math.prod(shape[2:]), 1, 1
+            if lengths is not None:
+                seg, pos = math.prod(shape[2:position_dim]), shape[position_dim]
         _need_cuda(src, "states[%d]" % i, dev)
-        _need_cuda(dst, "outs[%d]" % i, dev, src.dtype, (B, n) + shape[2:])
-        if lengths is not None and not 2 <= position_dim < len(shape):
-            raise ValueError("position_dim %d is no dimension of states[%d]'s beams"
-                             % (position_dim, i))
-        row = math.prod(shape[2:])
+        if dst is not src:
+            _need_cuda(dst, "outs[%d]" % i, dev, src.dtype, out_shape)
+        elif n != W:
+            raise ValueError("%d beams cannot be reordered in place to %d" % (W, n))
         if row == 0 or B == 0:
             continue
         s = table[used]
         used += 1
         s.src, s.dst = src.data_ptr(), dst.data_ptr()
-        s.segments, s.positions = 1, 1
-        if lengths is not None:
-            s.segments, s.positions = math.prod(shape[2:position_dim]), shape[position_dim]
-        s.position_bytes = row // (s.segments * s.positions) * src.element_size()
-    with _on(dev):
-        _check(load().spec_beam_reorder(_ptr(parents), _ptr(lengths), B, W, n, table, used,
-                                        _stream(dev)), "spec_beam_reorder")
+        s.position_bytes = row // (seg * pos) * src.element_size()
+        s.segments, s.positions = seg, pos
+    _enqueue("spec_beam_reorder", dev, load().spec_beam_reorder, parents.data_ptr(),
+             _addr(lengths), B, W, n, table, used)
     return outs
