@@ -112,11 +112,9 @@ _SIGNATURES = {
     "spec_ngram_propose": (ctypes.c_int32, [_P, _P, ctypes.c_int32, ctypes.c_int64,
                                             ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _P, _P,
                                             _P, _P, _P]),
-    "spec_row_topk_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int32,
-                                                        ctypes.c_int32, ctypes.c_int32]),
     "spec_row_topk": (ctypes.c_int32, [_P, ctypes.c_int64, ctypes.c_int32, ctypes.c_int64,
                                        ctypes.c_int32, ctypes.c_float, ctypes.c_int32, _P, _P, _P,
-                                       _P, ctypes.c_size_t, _P]),
+                                       _P]),
     "spec_distill_state_bytes": (ctypes.c_size_t, [ctypes.c_int64]),
     "spec_distill_loss": (ctypes.c_int32, [_P, _P, _P, _P, _P, ctypes.POINTER(_DistillParams), _P,
                                            _P, _P]),
@@ -760,8 +758,7 @@ def _enqueue(what: str, dev: torch.device, fn, *args):
 
 
 def row_topk(logits: torch.Tensor, k: int, *, temperature: float = 1.0,
-             vocab: Optional[int] = None, lse: bool = True,
-             workspace: Optional[torch.Tensor] = None) -> dict:
+             vocab: Optional[int] = None, lse: bool = True) -> dict:
     """The k largest logits of each row of a [..., S] tensor (first V columns)
     in decreasing order, equal values by lowest id: values (float32 [..., k]),
     ids (int32 [..., k]; -inf and -1 past a row's visible entries) and lse
@@ -772,19 +769,12 @@ def row_topk(logits: torch.Tensor, k: int, *, temperature: float = 1.0,
     k = int(k)
     lead, dev, dt = logits.shape[:-1], logits.device, _dtype_code(logits)
     rows = logits.numel() // S if S else 0
-    L = load()
     res = {"values": torch.empty(lead + (max(k, 0),), dtype=torch.float32, device=dev),
            "ids": torch.empty(lead + (max(k, 0),), dtype=torch.int32, device=dev)}
     if lse:
         res["lse"] = torch.empty(lead, dtype=torch.float32, device=dev)
-    if workspace is None:
-        n = L.spec_row_topk_workspace_bytes(rows, V, dt, k)
-        workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
-    else:
-        _need_cuda(workspace, "workspace", dev)
-    _enqueue("spec_row_topk", dev, L.spec_row_topk, logits.data_ptr(), rows, V, S, dt, temperature,
-             k, res["values"].data_ptr(), res["ids"].data_ptr(), _addr(res.get("lse")),
-             _addr(workspace), 0 if workspace is None else _nbytes(workspace))
+    _enqueue("spec_row_topk", dev, load().spec_row_topk, logits.data_ptr(), rows, V, S, dt, temperature,
+             k, res["values"].data_ptr(), res["ids"].data_ptr(), _addr(res.get("lse")))
     return res
 
 

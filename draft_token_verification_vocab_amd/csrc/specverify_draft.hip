@@ -25,17 +25,8 @@ bool grid_fits(int64_t blocks, int block) {
     return blocks <= (int64_t{1} << 32) / block - 1 && blocks <= INT32_MAX;
 }
 
-// How the rows of a listing are cut into workgroups.
-//   Many rows: a workgroup per row (the row pass's shapes).
-//   Few rows: smaller workgroups, each row cut into segments until the GPU is
-// filled or a segment is one chunk.
-constexpr int kFillRows = 256;      // compute units
-constexpr int kSplitBlocks = 1024;  // workgroups to aim for with few rows
-constexpr int kMaxMerge = 4096;     // keys one merge holds in LDS
-constexpr int kMaxListSegs = 64;    // one lane per segment in a merge
-constexpr int kSplitBlock = 256;
-constexpr int kMergeBlock = 256;
-
+// Workgroup shapes: the row pass's for a workgroup per row (several rows share
+// a compute unit), smaller ones for a row cut into segments.
 template <typename T>
 struct WideShape;
 template <>
@@ -46,71 +37,38 @@ template <>
 struct WideShape<float> {
     static constexpr int block = 512, unroll = 4;
 };
-
-struct ListPlan {
-    bool wide;
-    int segs, seg_vecs;
-    size_t list, seg_lse, total;  // workspace offsets
-};
-
-// lists: joined by one merge, each of k keys per segment (a row's own, or
-// those of a sequence's beams).  keep_lists: the lists go to the workspace
-// even with one segment per row.
-template <typename T>
-ListPlan plan_lists_t(int64_t rows, int32_t V, int32_t k, int32_t lists, bool keep_lists) {
-    using S = WideShape<T>;
-    constexpr int epv = 16 / sizeof(T);
-    constexpr int chunk = kSplitBlock * S::unroll;
-    const int nvec = (V + epv - 1) / epv;
-    const int by_len = (nvec + chunk - 1) / chunk;
-    const int fit = (keep_lists ? kMaxBeamKeys : kMaxMerge) / (lists * k);
-    const int most = fit < kMaxListSegs ? fit : kMaxListSegs;
-    ListPlan p{};
-    int64_t want = rows > 0 ? (kSplitBlocks + rows - 1) / rows : 1;
-    if (want > by_len) want = by_len;
-    if (want > most) want = most;
-    p.wide = rows >= kFillRows || want < 2;
-    p.segs = p.wide ? 1 : static_cast<int>(want);
-    p.seg_vecs = p.wide ? nvec : ((nvec + p.segs - 1) / p.segs + chunk - 1) / chunk * chunk;
-    p.segs = (nvec + p.seg_vecs - 1) / p.seg_vecs;
-    if (p.segs > 1 || keep_lists) {
-        const size_t n = static_cast<size_t>(rows) * p.segs;
-        p.list = 0;
-        p.seg_lse = align_up(8 * n * static_cast<size_t>(k));
-        p.total = align_up(p.seg_lse + 8 * n);
-    }
-    return p;
-}
-
-ListPlan plan_lists(int64_t rows, int32_t V, int32_t dtype, int32_t k, int32_t lists,
-                    bool keep_lists) {
-    return dtype == SPEC_DTYPE_BF16 ? plan_lists_t<uint16_t>(rows, V, k, lists, keep_lists)
-                                    : plan_lists_t<float>(rows, V, k, lists, keep_lists);
-}
-
-// Vectors in one chunk of the plan's workgroups.
-int chunk_vecs(const ListPlan &p, int32_t dtype) {
-    if (dtype == SPEC_DTYPE_BF16)
-        return (p.wide ? WideShape<uint16_t>::block : kSplitBlock) * WideShape<uint16_t>::unroll;
-    return (p.wide ? WideShape<float>::block : kSplitBlock) * WideShape<float>::unroll;
-}
+constexpr int kSplitBlock = 256;
 
 template <typename T>
-void launch_lists_t(const ListPlan &p, const TopkArgs &a, int64_t rows, hipStream_t st) {
+void launch_topk_t(const TopkArgs &a, int64_t rows, hipStream_t st) {
     using S = WideShape<T>;
-    const dim3 grid(static_cast<unsigned>(rows * p.segs));
-    if (p.wide)
+    const dim3 grid(static_cast<unsigned>(rows * a.segs));
+    if (a.segs == 1)
         topk_rows_kernel<T, S::block, S::unroll><<<grid, dim3(S::block), 0, st>>>(a);
     else
         topk_rows_kernel<T, kSplitBlock, S::unroll><<<grid, dim3(kSplitBlock), 0, st>>>(a);
 }
 
-void launch_lists(const ListPlan &p, const TopkArgs &a, int64_t rows, int32_t dtype,
-                  hipStream_t st) {
+void launch_topk(const TopkArgs &a, int64_t rows, int32_t dtype, hipStream_t st) {
     if (dtype == SPEC_DTYPE_BF16)
-        launch_lists_t<uint16_t>(p, a, rows, st);
+        launch_topk_t<uint16_t>(a, rows, st);
     else
-        launch_lists_t<float>(p, a, rows, st);
+        launch_topk_t<float>(a, rows, st);
+}
+
+TopkArgs topk_args(const void *logits, int64_t row_stride, int32_t V, int32_t dtype,
+                   float temperature, int32_t k) {
+    TopkArgs a{};
+    a.base = logits;
+    a.stride = row_stride;
+    a.V = V;
+    a.k = k;
+    a.segs = 1;
+    const int per = 16 / elem_size(dtype);
+    a.seg_vecs = (V + per - 1) / per;
+    a.c = log2e_over(temperature);
+    a.inv_t = 1.0 / static_cast<double>(temperature);
+    return a;
 }
 
 constexpr int32_t kMaxListVocab = 1 << 20;
@@ -160,18 +118,62 @@ void launch_distill_t(const DistillArgs &a, int64_t rows, hipStream_t st) {
 // Beam selection.
 constexpr int kBeamMergeBlock = 512;
 
+// How a beam selection's rows are cut into workgroups, and its workspace.  A
+// row's listing keeps a compute unit's vector units busy (256 KB take 12 us
+// there), so few rows are cut into segments, as long as the merge can take
+// their lists: one sequence of four beams of 128256 bfloat16 logits 16.6 us
+// against 19.0, of 2^20 logits 23 against 72; 240 rows lose by it (23.0 against
+// 20.9).
+constexpr int kSplitRows = 64;       // rows below which they are cut
+constexpr int kSplitBlocks = 1024;   // workgroups to aim for
+constexpr int kMaxSegs = 64;         // one lane per segment in the merge
+struct BeamPlan {
+    int segs, seg_vecs, chunk_vecs;
+    size_t list, seg_lse, total;  // workspace offsets
+};
+
+template <typename T>
+BeamPlan plan_beam_t(int64_t rows, int32_t V, int32_t beams, int32_t n) {
+    using S = WideShape<T>;
+    constexpr int per = 16 / sizeof(T), split_chunk = kSplitBlock * S::unroll;
+    const int nvec = (V + per - 1) / per;
+    BeamPlan p{1, nvec, S::block * S::unroll, 0, 0, 0};
+    if (rows <= kSplitRows) {
+        int64_t want = (kSplitBlocks + rows - 1) / rows;
+        const int by_len = (nvec + split_chunk - 1) / split_chunk;
+        const int fit = kMaxBeamKeys / (beams * n);
+        if (want > by_len) want = by_len;
+        if (want > fit) want = fit;
+        if (want > kMaxSegs) want = kMaxSegs;
+        if (want > 1) {
+            const int chunks = (by_len + static_cast<int>(want) - 1) / static_cast<int>(want);
+            p.chunk_vecs = split_chunk;
+            p.seg_vecs = chunks * split_chunk;
+            p.segs = (nvec + p.seg_vecs - 1) / p.seg_vecs;
+        }
+    }
+    const size_t lists = static_cast<size_t>(rows) * p.segs;
+    p.seg_lse = align_up(8 * lists * static_cast<size_t>(n));
+    p.total = align_up(p.seg_lse + 8 * lists);
+    return p;
+}
+
+BeamPlan plan_beam(int64_t rows, int32_t V, int32_t dtype, int32_t beams, int32_t n) {
+    return dtype == SPEC_DTYPE_BF16 ? plan_beam_t<uint16_t>(rows, V, beams, n)
+                                    : plan_beam_t<float>(rows, V, beams, n);
+}
+
 // Bound on how far the listing's float sums can move the difference of two
 // beams' log-normalisers.  A term's exponent d = (l - max) log2(e)/T is off by
 // a half step (2^-24 of |d|) each for the difference and the product, and by
 // the constant's own error; the terms' mean |d| is at most log2 V.  exp2 is
 // off by one step, and every addition that a term goes through by half a step:
 // 5 in its chunk, one per chunk of its thread, 6 across the wave.
-double near_bound(const ListPlan &p, int32_t V, int32_t dtype, float temperature) {
+double near_bound(const BeamPlan &p, int32_t V, float temperature) {
     const double h = 0x1p-24;
     const double exact = kLog2eD / static_cast<double>(temperature);
     const double constant = std::fabs(static_cast<double>(log2e_over(temperature)) / exact - 1.0);
-    const int chunk = chunk_vecs(p, dtype);
-    const double adds = 11 + (p.seg_vecs + chunk - 1) / chunk;
+    const double adds = 11 + (p.seg_vecs + p.chunk_vecs - 1) / p.chunk_vecs;
     const double one = kLn2 * std::log2(static_cast<double>(V)) * (2 * h + constant) + 2 * h +
                        adds * h;
     return 2.0 * one * 1.0001;  // the products of the errors
@@ -214,50 +216,21 @@ void launch_distill(const DistillArgs &a, const spec_distill_params *p, hipStrea
 
 extern "C" {
 
-size_t spec_row_topk_workspace_bytes(int64_t rows, int32_t vocab, int32_t dtype, int32_t k) {
-    if (rows < 1 || vocab < 2 || vocab > kMaxListVocab || k < 1 || k > kTopkMax ||
-        (dtype != SPEC_DTYPE_F32 && dtype != SPEC_DTYPE_BF16))
-        return 0;
-    return plan_lists(rows, vocab, dtype, k, 1, false).total;
-}
-
 spec_status spec_row_topk(const void *logits, int64_t rows, int32_t vocab, int64_t row_stride,
                           int32_t dtype, float temperature, int32_t k, float *values,
-                          int32_t *ids, float *lse, void *workspace, size_t workspace_bytes,
-                          void *stream) {
-    spec_status s = check_logits_shape(vocab, row_stride, dtype, temperature);
+                          int32_t *ids, float *lse, void *stream) {
+    const spec_status s = check_logits_shape(vocab, row_stride, dtype, temperature);
     if (s != SPEC_OK) return s;
     if (rows < 0 || k < 1) return SPEC_ERR_ARG;
-    if (k > kTopkMax || vocab > kMaxListVocab) return SPEC_ERR_UNSUPPORTED;
+    if (k > kTopkMax || vocab > kMaxListVocab || !grid_fits(rows, 1024))
+        return SPEC_ERR_UNSUPPORTED;
     if (rows == 0) return SPEC_OK;
     if (!logits || !aligned16(logits) || !values || !ids) return SPEC_ERR_ARG;
-    if (rows > INT32_MAX) return SPEC_ERR_UNSUPPORTED;
-    const ListPlan p = plan_lists(rows, vocab, dtype, k, 1, false);
-    if (!grid_fits(rows * p.segs, 1024)) return SPEC_ERR_UNSUPPORTED;
-    if (p.total && (!workspace || workspace_bytes < p.total)) return SPEC_ERR_WORKSPACE;
-    if (p.total && !aligned16(workspace)) return SPEC_ERR_ARG;
-    TopkArgs a{};
-    a.base = logits;
-    a.stride = row_stride;
-    a.V = vocab;
-    a.k = k;
-    a.segs = p.segs;
-    a.seg_vecs = p.seg_vecs;
-    a.c = log2e_over(temperature);
-    a.inv_t = 1.0 / static_cast<double>(temperature);
+    TopkArgs a = topk_args(logits, row_stride, vocab, dtype, temperature, k);
     a.values = values;
     a.ids = ids;
     a.lse = lse;
-    hipStream_t st = static_cast<hipStream_t>(stream);
-    if (p.segs > 1) {
-        char *w = static_cast<char *>(workspace);
-        a.list = reinterpret_cast<unsigned long long *>(w + p.list);
-        a.seg_lse = reinterpret_cast<double *>(w + p.seg_lse);
-    }
-    launch_lists(p, a, rows, dtype, st);
-    if ((s = launch_status()) != SPEC_OK || p.segs == 1) return s;
-    topk_merge_kernel<kMergeBlock><<<dim3(static_cast<unsigned>(rows)), dim3(kMergeBlock),
-                                     sizeof(unsigned long long) * p.segs * k, st>>>(a);
+    launch_topk(a, rows, dtype, static_cast<hipStream_t>(stream));
     return launch_status();
 }
 
@@ -323,8 +296,8 @@ spec_status spec_distill_step(const void *student, const int32_t *ids, const flo
 size_t spec_beam_workspace_bytes(int32_t batch, int32_t num_beams, int32_t vocab, int32_t dtype,
                                  int32_t num_out) {
     if (check_beam(batch, num_beams, vocab, dtype, num_out) != SPEC_OK || batch == 0) return 0;
-    return plan_lists(static_cast<int64_t>(batch) * num_beams, vocab, dtype, num_out, num_beams,
-                      true).total;
+    return plan_beam(static_cast<int64_t>(batch) * num_beams, vocab, dtype, num_beams, num_out)
+        .total;
 }
 
 spec_status spec_beam_select(const void *logits, int64_t row_stride, const float *scores,
@@ -340,26 +313,20 @@ spec_status spec_beam_select(const void *logits, int64_t row_stride, const float
     if (!logits || !aligned16(logits) || !scores || !out_scores || !parents || !tokens)
         return SPEC_ERR_ARG;
     const int64_t rows = static_cast<int64_t>(batch) * num_beams;
-    const ListPlan p = plan_lists(rows, vocab, dtype, num_out, num_beams, true);
+    const BeamPlan p = plan_beam(rows, vocab, dtype, num_beams, num_out);
     if (!grid_fits(rows * p.segs, 1024)) return SPEC_ERR_UNSUPPORTED;
     if (!workspace || workspace_bytes < p.total) return SPEC_ERR_WORKSPACE;
     if (!aligned16(workspace)) return SPEC_ERR_ARG;
     char *w = static_cast<char *>(workspace);
-    TopkArgs t{};
-    t.base = logits;
-    t.stride = row_stride;
-    t.V = vocab;
-    t.k = num_out;
+    TopkArgs t = topk_args(logits, row_stride, vocab, dtype, temperature, num_out);
     t.segs = p.segs;
     t.seg_vecs = p.seg_vecs;
-    t.c = log2e_over(temperature);
-    t.inv_t = 1.0 / static_cast<double>(temperature);
     t.list = reinterpret_cast<unsigned long long *>(w + p.list);
     t.seg_lse = reinterpret_cast<double *>(w + p.seg_lse);
     t.ended = ended;
     t.scores = scores;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    launch_lists(p, t, rows, dtype, st);
+    launch_topk(t, rows, dtype, st);
     if ((s = launch_status()) != SPEC_OK) return s;
     BeamArgs a{};
     a.base = logits;
@@ -378,7 +345,7 @@ spec_status spec_beam_select(const void *logits, int64_t row_stride, const float
     a.segs = p.segs;
     a.eos = eos;
     a.inv_t = t.inv_t;
-    a.near = near_bound(p, vocab, dtype, temperature);
+    a.near = near_bound(p, vocab, temperature);
     if (dtype == SPEC_DTYPE_BF16)
         beam_merge_kernel<uint16_t, kBeamMergeBlock>
             <<<dim3(batch), dim3(kBeamMergeBlock), 0, st>>>(a);

@@ -97,6 +97,19 @@ __device__ __attribute__((noinline)) double exact_normaliser(const T *row, int V
     return static_cast<double>(M) * inv_t + log(t);
 }
 
+// ln of a sum of e^x over a row's segments: lanes hold segment lane's x.
+__device__ __forceinline__ double wave_log_sum(double x, int lane, int segs) {
+    double m = lane < segs ? x : -__builtin_inf();
+    double top = -__builtin_inf();
+    for (int s = 0; s < segs; ++s) {  // at most 64, usually a few
+        const double o = __shfl(m, s, kWave);
+        top = o > top ? o : top;
+    }
+    if (!(top > -__builtin_inf())) return top;
+    const double e = lane < segs ? exp(m - top) : 0.0;
+    return top + log(wave_sum_f64(e));
+}
+
 // One workgroup per sequence.  The segments' lists of a beam are joined first
 // (whole keys, counted); then every continuation's place among the other
 // beams' sorted scores is found by bisection, by as many lanes as there are

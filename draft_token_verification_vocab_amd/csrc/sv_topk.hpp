@@ -5,7 +5,7 @@
 // the complement of the id, so that "larger key" is "earlier in the list" and
 // no two keys are equal.
 //
-// One workgroup streams a row (or a segment of it).  A thread keeps, beside
+// One workgroup streams a row (beam selection with few rows: a segment of it).  A thread keeps, beside
 // the online softmax, its chunk (16 logits) with the largest maximum in LDS,
 // which chunk comes second, and the second and third largest maximum.  The
 // k-th largest of the threads' maxima is then a lower bound tau of the k-th
@@ -30,17 +30,17 @@ struct TopkArgs {
     int64_t stride;          // elements between consecutive rows
     int32_t V;
     int32_t k;
-    int32_t segs;            // segments (workgroups) per row
+    int32_t segs;            // segments (workgroups) per row, 1 without a list
     int32_t seg_vecs;        // 16-byte vectors per segment
     float c;                 // log2(e) / T
     float pad_;
     double inv_t;            // 1 / T
-    // one segment: the caller's outputs (lse nullable)
+    // the caller's outputs (lse nullable)
     float *values;           // [rows][k]
     int32_t *ids;            // [rows][k]
     float *lse;              // [rows]
-    // lists for a merge: keys in decreasing order, 0 after the last
-    unsigned long long *list;  // [rows][segs][k], null: write the outputs above
+    // or lists for the beam merge: keys in decreasing order, 0 after the last
+    unsigned long long *list;  // [rows][segs][k]
     double *seg_lse;           // [rows][segs] ln sum e^(l/T), -inf when all is masked
     // rows that take no part (beam selection), both nullable
     const uint8_t *ended;    // [rows]
@@ -336,66 +336,6 @@ __global__ __launch_bounds__(BLOCK) void topk_rows_kernel(TopkArgs a) {
             a.seg_lse[blockIdx.x] = l;
         else
             a.lse[row] = static_cast<float>(l);
-    }
-}
-
-// ln of a sum of e^x over a row's segments: lanes hold segment lane's x.
-__device__ __forceinline__ double wave_log_sum(double x, int lane, int segs) {
-    double m = lane < segs ? x : -__builtin_inf();
-    double top = -__builtin_inf();
-    for (int s = 0; s < segs; ++s) {  // at most 64, usually a few
-        const double o = __shfl(m, s, kWave);
-        top = o > top ? o : top;
-    }
-    if (!(top > -__builtin_inf())) return top;
-    const double e = lane < segs ? exp(m - top) : 0.0;
-    return top + log(wave_sum_f64(e));
-}
-
-// Joins the segments' lists of one row: a key's place is the number of keys
-// above it, found in each sorted list by bisection.
-template <int BLOCK>
-__global__ __launch_bounds__(BLOCK) void topk_merge_kernel(TopkArgs a) {
-    extern __shared__ __align__(16) unsigned char dyn[];
-    unsigned long long *key = reinterpret_cast<unsigned long long *>(dyn);  // [segs][k]
-    __shared__ int sh_n;
-    const int tid = threadIdx.x, k = a.k, total = a.segs * a.k;
-    const int64_t row = blockIdx.x;
-    if (tid == 0) sh_n = 0;
-    for (int i = tid; i < total; i += BLOCK) key[i] = a.list[row * total + i];
-    __syncthreads();
-    for (int i = tid; i < total; i += BLOCK) {
-        const unsigned long long x = key[i];
-        if (x == 0) continue;
-        atomicAdd(&sh_n, 1);
-        int rank = i % k;
-        const int own = i / k;
-        for (int s = 0; s < a.segs && rank < k; ++s) {
-            if (s == own) continue;
-            int lo = 0, hi = k;  // keys of list s above x
-            while (lo < hi) {
-                const int mid = (lo + hi) / 2;
-                if (key[s * k + mid] > x)
-                    lo = mid + 1;
-                else
-                    hi = mid;
-            }
-            rank += lo;
-        }
-        if (rank < k) {
-            a.values[row * k + rank] = key_value(x);
-            a.ids[row * k + rank] = key_id(x);
-        }
-    }
-    __syncthreads();
-    for (int i = sh_n + tid; i < k; i += BLOCK) {
-        a.values[row * k + i] = -__builtin_inff();
-        a.ids[row * k + i] = -1;
-    }
-    if (a.lse && tid < kWave) {
-        const double x = tid < a.segs ? a.seg_lse[row * a.segs + tid] : -__builtin_inf();
-        const double l = wave_log_sum(x, tid, a.segs);
-        if (tid == 0) a.lse[row] = static_cast<float>(l);
     }
 }
 

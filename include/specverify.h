@@ -439,15 +439,11 @@ spec_status spec_row_stats(const void *logits, int64_t rows, int32_t vocab, int6
  * int32 [rows][k]) are required; a row with fewer than k visible entries is
  * filled up with (-inf, -1).  lse (device float [rows], nullable): ln sum
  * e^(l/T) over the whole row, -inf when it is masked throughout.  One pass over the
- * rows.  1 <= k <= 128.  workspace: device, spec_row_topk_workspace_bytes,
- * 16-byte aligned (a size of 0 needs none); its contents on entry do not
- * matter.
+ * rows, no workspace.  1 <= k <= 128.
  */
-size_t spec_row_topk_workspace_bytes(int64_t rows, int32_t vocab, int32_t dtype, int32_t k);
 spec_status spec_row_topk(const void *logits, int64_t rows, int32_t vocab, int64_t row_stride,
                           int32_t dtype, float temperature, int32_t k, float *values,
-                          int32_t *ids, float *lse, void *workspace, size_t workspace_bytes,
-                          void *stream);
+                          int32_t *ids, float *lse, void *stream);
 
 /*
  * Distillation from a teacher's listed top logits.  For each row, with

@@ -59,7 +59,7 @@ def test_random_rows(rows, V, k, dtype):
 
 @pytest.mark.parametrize("rows,V,dtype", [(1, 300001, "bf16"), (260, 300001, "bf16"),
                                           (258, 140001, "f32"), (2, 1 << 20, "bf16")])
-def test_rows_of_more_than_one_workgroup(rows, V, dtype):
+def test_long_rows(rows, V, dtype):
     g = torch.Generator().manual_seed(rows + V)
     x = 4.0 * torch.randn(rows, V, generator=g)
     per = 8 if dtype == "bf16" else 4
