@@ -164,17 +164,17 @@ BeamPlan plan_beam(int64_t rows, int32_t V, int32_t dtype, int32_t beams, int32_
 }
 
 // Bound on how far the listing's float sums can move the difference of two
-// beams' log-normalisers.  A term's exponent d = (l - max) log2(e)/T is off by
-// a half step (2^-24 of |d|) each for the difference and the product, and by
-// the constant's own error; the terms' mean |d| is at most log2 V.  exp2 is
-// off by one step, and every addition that a term goes through by half a step:
-// 5 in its chunk, one per chunk of its thread, 6 across the wave.
+// beams' log-normalisers.  A term's exponent d = l log2(e)/T - n is off by half
+// a step (2^-24 of |d|) and by the constant's own error; the terms' mean |d|
+// is at most log2 V + 1.  exp2 is off by one step, and every addition that a
+// term goes through by half a step: 5 in its chunk, one per chunk of its
+// thread, 6 across the wave.
 double near_bound(const BeamPlan &p, int32_t V, float temperature) {
     const double h = 0x1p-24;
     const double exact = kLog2eD / static_cast<double>(temperature);
     const double constant = std::fabs(static_cast<double>(log2e_over(temperature)) / exact - 1.0);
     const double adds = 11 + (p.seg_vecs + p.chunk_vecs - 1) / p.chunk_vecs;
-    const double one = kLn2 * std::log2(static_cast<double>(V)) * (2 * h + constant) + 2 * h +
+    const double one = kLn2 * (std::log2(static_cast<double>(V)) + 1.0) * (h + constant) + 2 * h +
                        adds * h;
     return 2.0 * one * 1.0001;  // the products of the errors
 }

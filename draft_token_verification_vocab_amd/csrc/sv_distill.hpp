@@ -263,7 +263,7 @@ __global__ __launch_bounds__(BLOCK) void distill_rows_kernel(DistillArgs a) {
         if (list.dup && tid < a.k && list.id[tid] >= 0) mark_first(tid, list);
         const unsigned long long mine = sh_chunks[tid];
 
-        OnlineSum acc;
+        OnlineSum acc(c);
         stream_vectors<T, BLOCK, UNROLL>(rp, 0, nvec, V, tid,
                                          [&](const uint4 (&buf)[UNROLL], int it) {
             float x[N];
@@ -304,6 +304,7 @@ __global__ __launch_bounds__(BLOCK) void distill_rows_kernel(DistillArgs a) {
             double S = 0.0;
 #pragma unroll
             for (int w = 0; w < NW; ++w) S += sh_s[w];
+            S = OnlineSum::from_max(S, M, c);
             float loss;
             const DistillRow r = settle_row(a, row, lane, list, M, S, &loss);
             if (lane == 0) {

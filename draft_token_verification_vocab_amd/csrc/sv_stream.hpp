@@ -66,36 +66,70 @@ __device__ __forceinline__ void stream_vectors(const T *row, int vbeg, int vend,
     if (tail) consume(b, nit);
 }
 
-// One thread's running maximum m and sum of 2^((x - m)*c) over the chunks it
-// is given (an online softmax in base 2).  The difference is formed before the
-// product, so the largest term is exactly 1 however large the logits are.
-// Sums within a thread are float: a few tens of chunk sums of one sign.
+// One thread's running maximum m and sum of 2^(x*c - n) over the chunks it is
+// given (an online softmax in base 2).  The reference n is m*c rounded up to
+// an integer: a term's exponent is then one fused product, rounded once, and a
+// rescaling to another reference is an exact power of two.  Sums within a
+// thread are float: a few tens of chunk sums of one sign.
+//
+// Beyond |m*c| = 2^30 neighbouring floats differ by 128 or more in the
+// exponent, so only logits equal to the maximum count; there the rounding of
+// m*c itself would be large, and a power of two takes the place of c that
+// keeps those apart and makes m's own term exactly 1.
 struct OnlineSum {
-    float m = kMasked, s = 0.f;
+    float m = kMasked, n, slope, s = 0.f;
+    bool far = false;  // |m*c| >= kFar
+    static constexpr float kFar = 0x1p30f;
+    __device__ __forceinline__ explicit OnlineSum(float c) : n(mul_rn(kMasked, c)), slope(c) {}
+
     // x: the chunk's N logits, cm their maximum.  NaN entries count as masked.
     template <int N>
     __device__ __forceinline__ void add(const float (&x)[N], float cm, float c) {
         if (cm > m) {
-            s *= hw_exp2((m - cm) * c);
+            const float mc = mul_rn(cm, c);
+            float to = ceilf(mc), k = c;
+            const bool was_far = far;
+            far = fabsf(mc) >= kFar;
+            if (far) {
+                k = ldexpf(1.0f, 31 - ilogbf(cm));
+                to = cm * k;
+            }
+            s = far || was_far || n - to < -300.f ? 0.f : ldexpf(s, static_cast<int>(n - to));
             m = cm;
+            n = to;
+            slope = k;
         }
         float s4[4];
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-            const float e = hw_exp2((x[k] - m) * c);
+            const float e = hw_exp2(fmaf(x[k], slope, -n));
             s4[k & 3] = k < 4 ? e : s4[k & 3] + e;
         }
         float cs = (s4[0] + s4[1]) + (s4[2] + s4[3]);
         if (!(cs == cs)) {  // a NaN entry: the chunk again without it
             cs = 0.f;
 #pragma unroll
-            for (int k = 0; k < N; ++k) cs += x[k] > kMasked ? hw_exp2((x[k] - m) * c) : 0.f;
+            for (int k = 0; k < N; ++k)
+                cs += x[k] > kMasked ? hw_exp2(fmaf(x[k], slope, -n)) : 0.f;
         }
         s += cs;
     }
-    // The sum relative to another maximum M >= m.
+    // The reference that a maximum M has.
+    __device__ __forceinline__ static float reference(float M, float c) {
+        return ceilf(mul_rn(M, c));
+    }
+    // The thread's sum relative to the reference of a maximum M >= m.
     __device__ __forceinline__ float at(float M, float c) const {
-        return s * hw_exp2((m - M) * c);
+        if (m == M) return s;
+        const float d = n - reference(M, c);
+        return far || fabsf(mul_rn(M, c)) >= kFar || d < -300.f ? 0.f
+                                                                : ldexpf(s, static_cast<int>(d));
+    }
+    // From r, the sum of the threads' at(M): the sum of 2^((x - M)*c).
+    __device__ __forceinline__ static double from_max(double r, float M, float c) {
+        if (fabsf(mul_rn(M, c)) >= kFar) return r;
+        return r * exp2(static_cast<double>(reference(M, c)) -
+                        static_cast<double>(M) * static_cast<double>(c));
     }
 };
 

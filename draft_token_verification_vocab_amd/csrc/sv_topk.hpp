@@ -152,7 +152,7 @@ __global__ __launch_bounds__(BLOCK) void topk_rows_kernel(TopkArgs a) {
     const int vbeg = seg * a.seg_vecs;
     const int vend = vbeg + a.seg_vecs < nvec ? vbeg + a.seg_vecs : nvec;
 
-    OnlineSum acc;
+    OnlineSum acc(c);
     int best = 0, second = 0;             // the chunks with the thread's largest maxima
     float m2 = kMasked, m3 = kMasked;     // the second and third largest chunk maximum
     stream_vectors<T, BLOCK, UNROLL>(rp, vbeg, vend, V, tid,
@@ -330,7 +330,8 @@ __global__ __launch_bounds__(BLOCK) void topk_rows_kernel(TopkArgs a) {
         double r = 0.0;
 #pragma unroll
         for (int w = 0; w < NW; ++w) r += sh_s[w];
-        const double l = bm > masked ? static_cast<double>(M) * a.inv_t + log(r)
+        const double l = bm > masked ? static_cast<double>(M) * a.inv_t +
+                                           log(OnlineSum::from_max(r, M, c))
                                      : -__builtin_inf();
         if (a.list)
             a.seg_lse[blockIdx.x] = l;

@@ -15,13 +15,13 @@ DT = {"bf16": torch.bfloat16, "f32": torch.float32}
 
 
 def lse_tolerance(V, lse):
-    """The float32 row pass: each term's exponent d = (l - max) log2(e)/T is off
-    by four half steps of |d| (the difference, the constant log2(e), its
-    division by T, the product), and the terms' mean |d| is at most log2 V; exp2 by one
-    step, sums by half a step per addition a term goes through (4 chains, the
+    """The float32 row pass: each term's exponent d = l log2(e)/T - n is off by
+    three half steps of |d| (the constant log2(e), its division by T, the fused
+    product), and the terms' mean |d| is at most log2 V + 1; exp2 by one step,
+    sums by half a step per addition a term goes through (4 chains, the
     thread's chunks, 6 wave steps), the result by half a step."""
     h = 2.0 ** -24
-    return (math.log(2) * 4 * h * math.log2(max(V, 2)) + 2 * h + (16 + V / 4096) * h +
+    return (math.log(2) * 3 * h * (math.log2(max(V, 2)) + 1) + 2 * h + (16 + V / 4096) * h +
             abs(lse) * h)
 
 
