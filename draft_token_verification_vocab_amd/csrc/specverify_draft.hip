@@ -77,6 +77,7 @@ constexpr int32_t kMaxListVocab = 1 << 20;
 // its own is cut into segments of kGradVecs vectors.
 constexpr int kGradBlock = 256;
 constexpr int kGradVecs = 4096;
+constexpr int kGradUnroll = 4;
 
 spec_status check_distill(const void *student, const int32_t *ids, const float *logits,
                           const spec_distill_params *p) {
@@ -107,12 +108,34 @@ DistillArgs distill_args(const void *student, const int32_t *ids, const float *l
     return a;
 }
 
-template <typename T, bool GRAD>
-void launch_distill_t(const DistillArgs &a, int64_t rows, hipStream_t st) {
+// Rows that are read again at once stay in the 256 MB last-level cache when
+// the student's logits fit it.
+constexpr int64_t kCacheBytes = int64_t{192} << 20;
+
+size_t map_bytes(const DistillArgs &a) {
+    return a.V <= kListMapVocab ? 4 * static_cast<size_t>((a.V + 31) / 32) : 0;
+}
+
+template <typename T>
+void launch_loss_t(const DistillArgs &a, int64_t rows, hipStream_t st) {
     using S = WideShape<T>;
-    const size_t map = a.V <= kListMapVocab ? 4 * static_cast<size_t>((a.V + 31) / 32) : 0;
-    distill_rows_kernel<T, S::block, S::unroll, GRAD>
-        <<<dim3(static_cast<unsigned>(rows)), dim3(S::block), map, st>>>(a);
+    const dim3 grid(static_cast<unsigned>(rows)), block(S::block);
+    if (a.state && rows * a.V * static_cast<int64_t>(sizeof(T)) <= kCacheBytes)
+        distill_rows_kernel<T, S::block, S::unroll, true>
+            <<<grid, block, map_bytes(a), st>>>(a);
+    else
+        distill_rows_kernel<T, S::block, S::unroll, false>
+            <<<grid, block, map_bytes(a), st>>>(a);
+}
+
+template <typename T>
+void launch_step_t(const DistillArgs &a, int64_t rows, hipStream_t st) {
+    constexpr int per = 16 / sizeof(T);
+    const dim3 grid(static_cast<unsigned>(rows));
+    if ((a.V + per - 1) / per <= 4096)
+        distill_held_kernel<T, 256, 8><<<grid, dim3(256), map_bytes(a), st>>>(a);
+    else
+        distill_held_kernel<T, 512, 12><<<grid, dim3(512), map_bytes(a), st>>>(a);
 }
 
 // Beam selection.
@@ -204,14 +227,6 @@ void launch_reorder(const ReorderArgs &a, int group, uint32_t blocks, hipStream_
         beam_reorder_kernel<BYTES, 32, kReorderBlock, kReorderUnroll><<<grid, block, 0, st>>>(a);
 }
 
-template <bool GRAD>
-void launch_distill(const DistillArgs &a, const spec_distill_params *p, hipStream_t st) {
-    if (p->dtype == SPEC_DTYPE_BF16)
-        launch_distill_t<uint16_t, GRAD>(a, p->rows, st);
-    else
-        launch_distill_t<float, GRAD>(a, p->rows, st);
-}
-
 }  // namespace
 
 extern "C" {
@@ -250,7 +265,11 @@ spec_status spec_distill_loss(const void *student, const int32_t *ids, const flo
     a.keep = keep;
     a.loss = loss;
     a.state = static_cast<DistillRow *>(state);
-    launch_distill<false>(a, params, static_cast<hipStream_t>(stream));
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (params->dtype == SPEC_DTYPE_BF16)
+        launch_loss_t<uint16_t>(a, params->rows, st);
+    else
+        launch_loss_t<float>(a, params->rows, st);
     return launch_status();
 }
 
@@ -270,9 +289,9 @@ spec_status spec_distill_grad(const void *student, const int32_t *ids, const flo
     const dim3 grid(static_cast<unsigned>(params->rows * segs));
     hipStream_t st = static_cast<hipStream_t>(stream);
     if (params->dtype == SPEC_DTYPE_BF16)
-        distill_grad_kernel<uint16_t, kGradBlock><<<grid, dim3(kGradBlock), 0, st>>>(a, segs);
+        distill_grad_kernel<uint16_t, kGradBlock, kGradUnroll><<<grid, dim3(kGradBlock), 0, st>>>(a, segs);
     else
-        distill_grad_kernel<float, kGradBlock><<<grid, dim3(kGradBlock), 0, st>>>(a, segs);
+        distill_grad_kernel<float, kGradBlock, kGradUnroll><<<grid, dim3(kGradBlock), 0, st>>>(a, segs);
     return launch_status();
 }
 
@@ -289,7 +308,11 @@ spec_status spec_distill_step(const void *student, const int32_t *ids, const flo
     a.grad_loss = grad_loss;
     a.loss = loss;
     a.grad = grad;
-    launch_distill<true>(a, params, static_cast<hipStream_t>(stream));
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (params->dtype == SPEC_DTYPE_BF16)
+        launch_step_t<uint16_t>(a, params->rows, st);
+    else
+        launch_step_t<float>(a, params->rows, st);
     return launch_status();
 }
 

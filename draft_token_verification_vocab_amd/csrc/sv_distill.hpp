@@ -89,13 +89,6 @@ __device__ __forceinline__ void store_stream(uint4 *p, const uint4 &v) {
     __builtin_nontemporal_store(r, reinterpret_cast<v4u32 *>(p));
 }
 
-// Entry vectors of a row: one vector with the ragged one read element-wise.
-template <typename T>
-__device__ __forceinline__ uint4 load_vector(const T *row, int vi, int V) {
-    return (vi + 1) * Elem<T>::kPerVec <= V ? load_stream(reinterpret_cast<const uint4 *>(row) + vi)
-                                            : Elem<T>::partial(row, vi, V);
-}
-
 // Gradients of a vector outside the list: G * 2^((x - M) c), 0 where masked.
 template <typename T>
 __device__ __forceinline__ uint4 outside_grad(const uint4 &v, float M, float c, float G) {
@@ -119,25 +112,29 @@ struct ListShared {
     int dup;                   // some id is listed twice
 };
 
-// Entry i of the list; call by threads i < k.
-template <typename T>
-__device__ __forceinline__ void load_list(const DistillArgs &a, int64_t row, const T *rp, int i,
-                                          ListShared &l) {
-    const int id = a.ids[row * a.k + i];
-    const float t = a.logits[row * a.k + i];
-    const bool valid = id >= 0 && id < a.V && t > kMasked;
-    float s = -__builtin_inff();
-    if (valid) {
-        s = Elem<T>::at(rp, id);
-        if (!(s > kMasked)) s = -__builtin_inff();
+// One entry of a row's list on its way to LDS.
+struct ListEntry {
+    int id = -1;     // -1: not a listed entry
+    float t = 0.f;
+    float s = 0.f;
+    __device__ __forceinline__ void fetch(const DistillArgs &a, int64_t row, int i) {
+        id = a.ids[row * a.k + i];
+        t = a.logits[row * a.k + i];
     }
-    l.id[i] = valid ? id : -1;
-    l.t[i] = t;
-    l.s[i] = s;
-    l.first[i] = valid;
-}
+    template <typename T>
+    __device__ __forceinline__ void gather(const DistillArgs &a, const T *rp) {
+        if (!(id >= 0 && id < a.V && t > kMasked)) id = -1;
+        s = id >= 0 ? Elem<T>::at(rp, id) : 0.f;
+    }
+    __device__ __forceinline__ void put(ListShared &l, int i) const {
+        l.id[i] = id;
+        l.t[i] = t;
+        l.s[i] = s > kMasked ? s : -__builtin_inff();
+        l.first[i] = id >= 0;
+    }
+};
 
-// first[] when some id is listed twice; call by threads i < k after load_list.
+// first[] when some id is listed twice; call by threads i < k.
 __device__ __forceinline__ void mark_first(int i, ListShared &l) {
     for (int j = 0; j < i; ++j)
         if (l.id[j] == l.id[i]) l.first[i] = 0;
@@ -213,138 +210,292 @@ __device__ __forceinline__ DistillRow settle_row(const DistillArgs &a, int64_t r
     return r;
 }
 
-// One workgroup per row: the loss, and with GRAD the gradient, for which the
-// row is read a second time.
-template <typename T, int BLOCK, int UNROLL, bool GRAD>
-__global__ __launch_bounds__(BLOCK) void distill_rows_kernel(DistillArgs a) {
-    using E = Elem<T>;
-    constexpr int EPV = E::kPerVec;
-    constexpr int N = UNROLL * EPV;
-    constexpr int NW = BLOCK / kWave;
+// What a workgroup holds of its row besides the list.  The bitmap of listed ids
+// (one bit per id, V <= kListMapVocab) is dynamic.
+template <int BLOCK>
+struct DistillShared {
+    ListShared list;
+    unsigned long long chunks[BLOCK];  // chunks (mod 64) of a thread with a listed entry
+    uint32_t wm[BLOCK / kWave];
+    double s[BLOCK / kWave];
+    DistillRow row;
+};
+
+// Puts a row's list (entry tid of it in the threads below k) in LDS, with the
+// bitmap and each thread's chunks (of UNROLL vectors a thread) that hold a
+// listed entry.  Returns the thread's.
+template <typename T, int BLOCK, int UNROLL>
+__device__ __forceinline__ unsigned long long prepare_list(const DistillArgs &a,
+                                                           const ListEntry &entry, int tid,
+                                                           DistillShared<BLOCK> &sh,
+                                                           uint32_t *map) {
+    constexpr int EPV = Elem<T>::kPerVec;
     constexpr int kChunk = UNROLL * BLOCK;
-    extern __shared__ __align__(16) unsigned char dyn[];
-    uint32_t *map = reinterpret_cast<uint32_t *>(dyn);  // one bit per id (V <= kListMapVocab)
-    __shared__ ListShared list;
-    __shared__ unsigned long long sh_chunks[BLOCK];  // chunks (mod 64) holding a listed entry
-    __shared__ uint32_t sh_wm[NW];
-    __shared__ double sh_s[NW];
-    __shared__ DistillRow sh_row;
-
-    const int tid = threadIdx.x, lane = tid & (kWave - 1), wv = tid / kWave;
-    const int64_t row = blockIdx.x;
-    const T *rp = static_cast<const T *>(a.student) + row * a.stride;
-    T *gp = static_cast<T *>(a.grad) + row * a.stride;
-    const int V = a.V;
-    const float c = a.c;
-    const int nvec = (V + EPV - 1) / EPV;
-    const int out_vecs = static_cast<int>(a.stride / EPV);  // the row with its padding
-    const bool kept = !a.keep || a.keep[row];
-    const bool mapped = V <= kListMapVocab;
-
-    if (kept) {
-        sh_chunks[tid] = 0;
-        if (mapped)
-            for (int i = tid; i < (V + 31) / 32; i += BLOCK) map[i] = 0;
-        if (tid == 0) list.dup = 0;
-        if (tid < a.k) load_list<T>(a, row, rp, tid, list);
-        __syncthreads();
-        if (tid < a.k && list.id[tid] >= 0) {
-            const int id = list.id[tid];
-            const int w = id / EPV, it = w / kChunk, owner = (w % kChunk) % BLOCK;
-            atomicOr(&sh_chunks[owner], 1ull << (it & 63));
-            bool again = false;
-            if (mapped)
-                again = (atomicOr(&map[id >> 5], 1u << (id & 31)) >> (id & 31)) & 1u;
-            else
-                for (int j = 0; j < tid; ++j) again = again || list.id[j] == id;
-            if (again) list.dup = 1;
-        }
-        __syncthreads();
-        if (list.dup && tid < a.k && list.id[tid] >= 0) mark_first(tid, list);
-        const unsigned long long mine = sh_chunks[tid];
-
-        OnlineSum acc(c);
-        stream_vectors<T, BLOCK, UNROLL>(rp, 0, nvec, V, tid,
-                                         [&](const uint4 (&buf)[UNROLL], int it) {
-            float x[N];
-#pragma unroll
-            for (int u = 0; u < UNROLL; ++u) E::unpack(buf[u], x + u * EPV);
-            if ((mine >> (it & 63)) & 1ull) {  // leave the listed entries out
-#pragma unroll
-                for (int u = 0; u < UNROLL; ++u) {
-                    const int vi = it * kChunk + u * BLOCK + tid;
-                    uint32_t bits = 0;
-                    if (mapped) {
-                        if (vi < nvec) bits = map[vi * EPV >> 5] >> (vi * EPV & 31);
-                    } else {
-                        for (int j = 0; j < a.k; ++j) {
-                            const int e = list.id[j] - vi * EPV;
-                            if (e >= 0 && e < EPV) bits |= 1u << e;
-                        }
-                    }
-#pragma unroll
-                    for (int e = 0; e < EPV; ++e)
-                        if ((bits >> e) & 1u) x[u * EPV + e] = 2.0f * kMasked;
-                }
-            }
-            acc.add(x, chunk_max(x), c);
-        });
-
-        const uint32_t wm = wave_max_u32(ordered_bits(acc.m + 0.0f));
-        if (lane == 0) sh_wm[wv] = wm;
-        __syncthreads();
-        uint32_t bm = sh_wm[0];
-#pragma unroll
-        for (int w = 1; w < NW; ++w) bm = sh_wm[w] > bm ? sh_wm[w] : bm;
-        const float M = from_ordered_bits(bm);
-        const float ws = wave_sum_f32(acc.at(M, c));
-        if (lane == 0) sh_s[wv] = static_cast<double>(ws);
-        __syncthreads();
-        if (wv == 0) {
-            double S = 0.0;
-#pragma unroll
-            for (int w = 0; w < NW; ++w) S += sh_s[w];
-            S = OnlineSum::from_max(S, M, c);
-            float loss;
-            const DistillRow r = settle_row(a, row, lane, list, M, S, &loss);
-            if (lane == 0) {
-                sh_row = r;
-                a.loss[row] = loss;
-                if (a.state) a.state[row] = r;
-            }
-        }
-    } else if (tid == 0) {
-        DistillRow r{};
-        r.mass = -1.0;
-        sh_row = r;
-        a.loss[row] = 0.f;
-        if (a.state) a.state[row] = r;
-    }
-    if (!GRAD) return;
-
+    ListShared &list = sh.list;
+    const bool mapped = a.V <= kListMapVocab;
+    sh.chunks[tid] = 0;
+    if (mapped)
+        for (int i = tid; i < (a.V + 31) / 32; i += BLOCK) map[i] = 0;
+    if (tid == 0) list.dup = 0;
+    if (tid < a.k) entry.put(list, tid);
     __syncthreads();
-    const DistillRow r = sh_row;
-    uint4 *out = reinterpret_cast<uint4 *>(gp);
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    if (r.mass < 0.0) {
-        for (int i = tid; i < out_vecs; i += BLOCK) store_stream(out + i, zero);
-        return;
+    if (tid < a.k && list.id[tid] >= 0) {
+        const int id = list.id[tid];
+        const int w = id / EPV, it = w / kChunk, owner = (w % kChunk) % BLOCK;
+        atomicOr(&sh.chunks[owner], 1ull << (it & 63));
+        bool again = false;
+        if (mapped)
+            again = (atomicOr(&map[id >> 5], 1u << (id & 31)) >> (id & 31)) & 1u;
+        else
+            for (int j = 0; j < tid; ++j) again = again || list.id[j] == id;
+        if (again) list.dup = 1;
     }
-    const double g = a.grad_loss ? static_cast<double>(a.grad_loss[row]) : 1.0;
-    const float G = static_cast<float>(r.coef * a.inv_t * g);
-    for (int i = tid; i < nvec; i += BLOCK)
-        store_stream(out + i, outside_grad<T>(load_vector(rp, i, V), r.m, c, G));
-    for (int i = nvec + tid; i < out_vecs; i += BLOCK) store_stream(out + i, zero);
-    // the listed entries over what the stream wrote there, once it is written
+    __syncthreads();
+    if (list.dup && tid < a.k && list.id[tid] >= 0) mark_first(tid, list);
+    return sh.chunks[tid];
+}
+
+// Masks the listed entries among a vector's.
+template <typename T>
+__device__ __forceinline__ void leave_out_listed(const DistillArgs &a, const ListShared &list,
+                                                 const uint32_t *map, int vi, int nvec,
+                                                 float *x) {
+    constexpr int EPV = Elem<T>::kPerVec;
+    uint32_t bits = 0;
+    if (a.V <= kListMapVocab) {
+        if (vi < nvec) bits = map[vi * EPV >> 5] >> (vi * EPV & 31);
+    } else {
+        for (int j = 0; j < a.k; ++j) {
+            const int e = list.id[j] - vi * EPV;
+            if (e >= 0 && e < EPV) bits |= 1u << e;
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < EPV; ++e)
+        if ((bits >> e) & 1u) x[e] = 2.0f * kMasked;
+}
+
+// The row's results from the threads' sums, in sh.row; ends with a barrier.
+template <int BLOCK>
+__device__ __forceinline__ void finish_row(const DistillArgs &a, int64_t row,
+                                           const OnlineSum &acc, int tid,
+                                           DistillShared<BLOCK> &sh) {
+    constexpr int NW = BLOCK / kWave;
+    const int lane = tid & (kWave - 1), wv = tid / kWave;
+    const uint32_t wm = wave_max_u32(ordered_bits(acc.m + 0.0f));
+    if (lane == 0) sh.wm[wv] = wm;
+    __syncthreads();
+    uint32_t bm = sh.wm[0];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) bm = sh.wm[w] > bm ? sh.wm[w] : bm;
+    const float M = from_ordered_bits(bm);
+    const float ws = wave_sum_f32(acc.at(M, a.c));
+    if (lane == 0) sh.s[wv] = static_cast<double>(ws);
+    __syncthreads();
+    if (wv == 0) {
+        double S = 0.0;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) S += sh.s[w];
+        float loss;
+        const DistillRow r =
+            settle_row(a, row, lane, sh.list, M, OnlineSum::from_max(S, M, a.c), &loss);
+        if (lane == 0) {
+            sh.row = r;
+            a.loss[row] = loss;
+            if (a.state) a.state[row] = r;
+        }
+    }
+    __syncthreads();
+}
+
+// A row that is left out, or whose loss has no gradient.
+__device__ __forceinline__ void skip_row(const DistillArgs &a, int64_t row) {
+    DistillRow r{};
+    r.mass = -1.0;
+    a.loss[row] = 0.f;
+    if (a.state) a.state[row] = r;
+}
+
+template <int BLOCK>
+__device__ __forceinline__ void zero_vectors(uint4 *out, int from, int to, int tid) {
+    for (int i = from + tid; i < to; i += BLOCK) store_stream(out + i, make_uint4(0, 0, 0, 0));
+}
+
+// The gradients of the listed entries, over what the stream wrote there, once
+// that is written.
+template <typename T>
+__device__ __forceinline__ void patch_listed(const DistillArgs &a, const DistillRow &r, double g,
+                                             int tid, const ListShared &list, T *gp) {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     if (tid < a.k && list.id[tid] >= 0 && list.first[tid])
         gp[list.id[tid]] = GradOut<T>::one(listed_grad(tid, a.k, list, r.lse, r.mass, a.inv_t, g));
 }
 
+// The loss, a workgroup per row.  KEEP: the row is read again soon.
+template <typename T, int BLOCK, int UNROLL, bool KEEP>
+__global__ __launch_bounds__(BLOCK) void distill_rows_kernel(DistillArgs a) {
+    using E = Elem<T>;
+    constexpr int EPV = E::kPerVec;
+    constexpr int N = UNROLL * EPV;
+    extern __shared__ __align__(16) unsigned char dyn[];
+    uint32_t *map = reinterpret_cast<uint32_t *>(dyn);
+    __shared__ DistillShared<BLOCK> sh;
+
+    const int tid = threadIdx.x;
+    const int64_t row = blockIdx.x;
+    const T *rp = static_cast<const T *>(a.student) + row * a.stride;
+    const int V = a.V;
+    const int nvec = (V + EPV - 1) / EPV;
+    if (a.keep && !a.keep[row]) {
+        if (tid == 0) skip_row(a, row);
+        return;
+    }
+    ListEntry entry;
+    if (tid < a.k) {
+        entry.fetch(a, row, tid);
+        entry.gather<T>(a, rp);
+    }
+    const unsigned long long mine = prepare_list<T, BLOCK, UNROLL>(a, entry, tid, sh, map);
+    OnlineSum acc(a.c);
+    stream_vectors<T, BLOCK, UNROLL, KEEP>(rp, 0, nvec, V, tid,
+                                           [&](const uint4 (&buf)[UNROLL], int it) {
+        float x[N];
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) E::unpack(buf[u], x + u * EPV);
+        if ((mine >> (it & 63)) & 1ull) {
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u)
+                leave_out_listed<T>(a, sh.list, map, (it * UNROLL + u) * BLOCK + tid, nvec,
+                                    x + u * EPV);
+        }
+        acc.add(x, chunk_max(x), a.c);
+    });
+    finish_row<BLOCK>(a, row, acc, tid, sh);
+}
+
+// Loss and gradient of a row whose first BLOCK*NV vectors are read once: a
+// thread holds its NV of them in registers from the read to the gradient.
+// What lies beyond is read twice, the first time without the non-temporal
+// hint, so that the second read comes from the last-level cache.
+//
+// The bound is memory: with all of the row read twice, 2048 rows of 128256
+// bfloat16 logits took 245 us, the fabric's rate for their 1.6 GB.  512 threads
+// at 128 registers (two workgroups per compute unit, which cover each other's
+// waits) hold 12 vectors each, 38 % of such a row: 213 us.  16 vectors hold
+// more and gain nothing (216), in float32 they spill (2048 rows of 32000: 115 us
+// against 96).  A whole row in one workgroup of 1024 threads, alone on its
+// compute unit, took 257 us.  Rows of up to 4096 vectors take 256 threads with
+// 8 (4000 bfloat16 logits: 20 us against 36 with 512 threads).
+template <typename T, int BLOCK, int NV>
+__global__ __launch_bounds__(BLOCK, 4) void distill_held_kernel(DistillArgs a) {
+    using E = Elem<T>;
+    constexpr int EPV = E::kPerVec;
+    constexpr int UNROLL = 16 / EPV;  // 16 logits a chunk, as in the stream
+    constexpr int N = UNROLL * EPV;
+    constexpr int kHeld = BLOCK * NV;
+    static_assert(NV % UNROLL == 0, "whole chunks");
+    extern __shared__ __align__(16) unsigned char dyn[];
+    uint32_t *map = reinterpret_cast<uint32_t *>(dyn);
+    __shared__ DistillShared<BLOCK> sh;
+
+    const int tid = threadIdx.x;
+    const int64_t row = blockIdx.x;
+    const T *rp = static_cast<const T *>(a.student) + row * a.stride;
+    T *gp = static_cast<T *>(a.grad) + row * a.stride;
+    const int V = a.V;
+    const int nfull = V / EPV, nvec = (V + EPV - 1) / EPV;
+    const int out_vecs = static_cast<int>(a.stride / EPV);
+    uint4 *out = reinterpret_cast<uint4 *>(gp);
+    if (a.keep && !a.keep[row]) {
+        if (tid == 0) skip_row(a, row);
+        zero_vectors<BLOCK>(out, 0, out_vecs, tid);
+        return;
+    }
+    ListEntry entry;
+    if (tid < a.k) {
+        entry.fetch(a, row, tid);
+        entry.gather<T>(a, rp);
+    }
+    // Vector u*BLOCK + tid; past the full ones the last full one stands in
+    // until the ragged vector or padding takes its place below.
+    const buf_rsrc rs = make_rsrc(rp, static_cast<uint32_t>(nfull) * 16u);
+    uint4 v[NV];
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        if (u * BLOCK < nfull) {
+            const int vi = u * BLOCK + tid;
+            v[u] = load_row_buf<false>(rs, static_cast<uint32_t>(vi < nfull ? vi : nfull - 1) * 16u,
+                                       0u);
+        }
+    }
+    const unsigned long long mine = prepare_list<T, BLOCK, UNROLL>(a, entry, tid, sh, map);
+    const uint32_t pad = E::pad_word();
+    OnlineSum acc(a.c);
+#pragma unroll
+    for (int it = 0; it < NV / UNROLL; ++it) {
+        if (it * UNROLL * BLOCK >= nvec) break;
+        float x[N];
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) {
+            const int w = it * UNROLL + u, vi = w * BLOCK + tid;
+            if ((w + 1) * BLOCK > nfull) {  // the same for every thread
+                if (vi >= nvec || w * BLOCK >= nvec)
+                    v[w] = make_uint4(pad, pad, pad, pad);
+                else if (vi >= nfull)
+                    v[w] = E::partial(rp, nfull, V);
+            }
+            E::unpack(v[w], x + u * EPV);
+            if ((mine >> it) & 1ull) leave_out_listed<T>(a, sh.list, map, vi, nvec, x + u * EPV);
+        }
+        acc.add(x, chunk_max(x), a.c);
+    }
+    if (nvec > kHeld) {
+        stream_vectors<T, BLOCK, UNROLL, true>(rp, kHeld, nvec, V, tid,
+                                               [&](const uint4 (&buf)[UNROLL], int it) {
+            it += NV / UNROLL;
+            float x[N];
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u) E::unpack(buf[u], x + u * EPV);
+            if ((mine >> (it & 63)) & 1ull) {
+#pragma unroll
+                for (int u = 0; u < UNROLL; ++u)
+                    leave_out_listed<T>(a, sh.list, map, (it * UNROLL + u) * BLOCK + tid, nvec,
+                                        x + u * EPV);
+            }
+            acc.add(x, chunk_max(x), a.c);
+        });
+    }
+    finish_row<BLOCK>(a, row, acc, tid, sh);
+    const DistillRow r = sh.row;
+    if (r.mass < 0.0) {
+        zero_vectors<BLOCK>(out, 0, out_vecs, tid);
+        return;
+    }
+    const double g = a.grad_loss ? static_cast<double>(a.grad_loss[row]) : 1.0;
+    const float G = static_cast<float>(r.coef * a.inv_t * g);
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        const int vi = u * BLOCK + tid;
+        if (vi < nvec) store_stream(out + vi, outside_grad<T>(v[u], r.m, a.c, G));
+    }
+    if (nvec > kHeld) {
+        stream_vectors<T, BLOCK, UNROLL>(rp, kHeld, nvec, V, tid,
+                                         [&](const uint4 (&buf)[UNROLL], int it) {
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u) {
+                const int vi = kHeld + (it * UNROLL + u) * BLOCK + tid;
+                if (vi < nvec) store_stream(out + vi, outside_grad<T>(buf[u], r.m, a.c, G));
+            }
+        });
+    }
+    zero_vectors<BLOCK>(out, nvec, out_vecs, tid);
+    patch_listed<T>(a, r, g, tid, sh.list, gp);
+}
+
 // The gradient alone, from the forward pass's state: every workgroup writes
 // seg_vecs vectors of a row.
-template <typename T, int BLOCK>
+template <typename T, int BLOCK, int UNROLL>
 __global__ __launch_bounds__(BLOCK) void distill_grad_kernel(DistillArgs a, int32_t segs) {
     constexpr int EPV = Elem<T>::kPerVec;
     __shared__ ListShared list;
@@ -361,12 +512,15 @@ __global__ __launch_bounds__(BLOCK) void distill_grad_kernel(DistillArgs a, int3
     uint4 *out = reinterpret_cast<uint4 *>(gp);
     const DistillRow r = a.state[row];
     if (r.mass < 0.0) {
-        for (int i = vbeg + tid; i < vend; i += BLOCK) store_stream(out + i, make_uint4(0, 0, 0, 0));
+        zero_vectors<BLOCK>(out, vbeg, vend, tid);
         return;
     }
     if (tid == 0) list.dup = 0;
     if (tid < a.k) {
-        load_list<T>(a, row, rp, tid, list);
+        ListEntry entry;
+        entry.fetch(a, row, tid);
+        entry.gather<T>(a, rp);
+        entry.put(list, tid);
         list.p[tid] = list.id[tid] >= 0
                           ? exp(static_cast<double>(list.t[tid]) * a.inv_t - r.norm)
                           : 0.0;
@@ -382,11 +536,17 @@ __global__ __launch_bounds__(BLOCK) void distill_grad_kernel(DistillArgs a, int3
     __syncthreads();
     const double g = a.grad_loss ? static_cast<double>(a.grad_loss[row]) : 1.0;
     const float G = static_cast<float>(r.coef * a.inv_t * g);
-    for (int i = vbeg + tid; i < vend; i += BLOCK) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (i < nvec) v = outside_grad<T>(load_vector(rp, i, V), r.m, a.c, G);
-        store_stream(out + i, v);
-    }
+    const int vlast = vend < nvec ? vend : nvec;
+    if (vbeg < vlast)
+        stream_vectors<T, BLOCK, UNROLL>(rp, vbeg, vlast, V, tid,
+                                         [&](const uint4 (&buf)[UNROLL], int it) {
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u) {
+                const int vi = vbeg + (it * UNROLL + u) * BLOCK + tid;
+                if (vi < vlast) store_stream(out + vi, outside_grad<T>(buf[u], r.m, a.c, G));
+            }
+        });
+    zero_vectors<BLOCK>(out, vbeg > nvec ? vbeg : nvec, vend, tid);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     if (tid < a.k && list.id[tid] >= 0 && list.first[tid]) {

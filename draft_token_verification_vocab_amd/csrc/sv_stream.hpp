@@ -13,6 +13,14 @@ namespace sv {
 // and survives a rounding to bfloat16 (it is Elem<>::pad_word).
 constexpr float kMasked = kNoMax;
 
+// A 16-byte buffer load with (KEEP = false) or without the non-temporal hint.
+template <bool KEEP>
+__device__ __forceinline__ uint4 load_row_buf(buf_rsrc r, uint32_t voff, uint32_t soff) {
+    const v4u32 v = __builtin_amdgcn_raw_buffer_load_b128(
+        r, static_cast<int>(voff), static_cast<int>(soff), KEEP ? 0 : kCachePolicyNT);
+    return make_uint4(v.x, v.y, v.z, v.w);
+}
+
 // consume(buf, it): buf holds the thread's vectors of chunk `it`, vector u at
 // index it*UNROLL*BLOCK + u*BLOCK + tid of the segment [vbeg, vend); vectors
 // past the segment and entries past V are padding.  Threads without a vector
@@ -20,8 +28,10 @@ constexpr float kMasked = kNoMax;
 //
 // The loads are the row pass's: buffer-addressed non-temporal 16-byte loads
 // over the segment's full vectors, the next chunk issued before this chunk's
-// arithmetic, a ragged last vector read element by element.
-template <typename T, int BLOCK, int UNROLL, typename F>
+// arithmetic, a ragged last vector read element by element.  KEEP: without the
+// non-temporal hint, for rows that are read again soon (the hint keeps them
+// out of the caches).
+template <typename T, int BLOCK, int UNROLL, bool KEEP = false, typename F>
 __device__ __forceinline__ void stream_vectors(const T *row, int vbeg, int vend, int V, int tid,
                                                F &&consume) {
     using E = Elem<T>;
@@ -37,7 +47,7 @@ __device__ __forceinline__ void stream_vectors(const T *row, int vbeg, int vend,
         const uint32_t soff = static_cast<uint32_t>(it) * (kChunk * 16u);
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u)
-            buf[u] = load_stream_buf(rs, static_cast<uint32_t>(tid + u * BLOCK) * 16u, soff);
+            buf[u] = load_row_buf<KEEP>(rs, static_cast<uint32_t>(tid + u * BLOCK) * 16u, soff);
     };
     uint4 a[UNROLL], b[UNROLL];
     if (nit > 0) {
@@ -57,7 +67,7 @@ __device__ __forceinline__ void stream_vectors(const T *row, int vbeg, int vend,
             const int vi = v + u * BLOCK;
             b[u] = make_uint4(pad, pad, pad, pad);
             if (vi < nf)
-                b[u] = load_stream_buf(rs, static_cast<uint32_t>(vi) * 16u, 0u);
+                b[u] = load_row_buf<KEEP>(rs, static_cast<uint32_t>(vi) * 16u, 0u);
             else if (vi < nv)
                 b[u] = E::partial(row, nfull, V);
         }

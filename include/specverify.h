@@ -503,7 +503,8 @@ spec_status spec_distill_grad(const void *student, const int32_t *ids, const flo
                               const spec_distill_params *params, void *grad, void *stream);
 
 /* spec_distill_step -- loss and gradient in one call, for an upstream gradient
- * known beforehand: the results of spec_distill_loss and spec_distill_grad. */
+ * known beforehand: the results of spec_distill_loss and spec_distill_grad up
+ * to the rounding of the rows' sums. */
 spec_status spec_distill_step(const void *student, const int32_t *ids, const float *logits,
                               const float *lse, const uint8_t *keep, const float *grad_loss,
                               const spec_distill_params *params, float *loss, void *grad,
