@@ -276,9 +276,10 @@ __global__ __launch_bounds__(BLOCK) void beam_merge_kernel(BeamArgs a) {
 
 // ---------------------------------------------------------------------------
 // Reordering of states: dst[b][i] = src[b][parents[b][i]], the used positions
-// of every segment.  A thread takes one unit (16, 4 or 1 bytes) of a sequence,
-// reads it from all the parents and only then writes the rows, so a state may
-// be reordered in place: no other thread touches that unit.
+// of every segment.  A thread takes one unit (16, 4 or 1 bytes) of a sequence: it
+// reads each parent that has children once and writes the children's rows.  In
+// place it reads all the parents before it writes, and no other thread touches
+// that unit, so nothing is overwritten that is still needed.
 // ---------------------------------------------------------------------------
 constexpr int kMaxReorder = 32;  // states per launch
 
@@ -317,8 +318,13 @@ struct ReorderUnit<1> {
     using type = uint8_t;
 };
 
-// GROUP rows are in flight at once; in place that is all of them (n <= GROUP).
-template <int BYTES, int GROUP, int BLOCK, int UNROLL>
+template <typename U>
+__device__ __forceinline__ U load_unit(const char *p, int64_t i) {
+    return __builtin_nontemporal_load(reinterpret_cast<const U *>(p) + i);
+}
+
+// GROUP parents are in flight at once; in place that is all of them (W <= GROUP).
+template <int BYTES, int GROUP, int BLOCK>
 __global__ __launch_bounds__(BLOCK) void beam_reorder_kernel(ReorderArgs a) {
     using U = typename ReorderUnit<BYTES>::type;
     int t = 0;
@@ -331,29 +337,35 @@ __global__ __launch_bounds__(BLOCK) void beam_reorder_kernel(ReorderArgs a) {
     const int b = static_cast<int>(at / s.segments);
     const int used = a.lengths ? clamp_len(a.lengths[b], s.positions) : s.positions;
     const int64_t units = used * s.pos_bytes / BYTES;
+    const int64_t i = static_cast<int64_t>(chunk) * BLOCK + threadIdx.x;
+    if (i - threadIdx.x >= units) return;
     const int64_t seg_bytes = s.positions * s.pos_bytes;
     const int64_t beam_bytes = seg_bytes * s.segments;
     const char *src = s.src + static_cast<int64_t>(b) * a.W * beam_bytes + seg * seg_bytes;
     char *dst = s.dst + static_cast<int64_t>(b) * a.n * beam_bytes + seg * seg_bytes;
-    const bool in_place = s.src == s.dst;
-    const int32_t *par = a.parents + static_cast<int64_t>(b) * a.n;
-    int64_t i = static_cast<int64_t>(chunk) * (BLOCK * UNROLL) + threadIdx.x;
-    for (int u = 0; u < UNROLL; ++u, i += BLOCK) {
-        if (i >= units) return;
-        for (int g = 0; g < a.n; g += GROUP) {
-            U v[GROUP];
+
+    // kids[w]: the rows that take parent w; in place a row that keeps its own
+    // beam is not moved.
+    const int lane = threadIdx.x & (kWave - 1);
+    int mine = lane < a.n ? a.parents[static_cast<int64_t>(b) * a.n + lane] : -1;
+    if (s.src == s.dst && mine == lane) mine = -1;
+    for (int g = 0; g < a.W; g += GROUP) {
+        uint64_t kids[GROUP];
 #pragma unroll
-            for (int k = 0; k < GROUP; ++k) {
-                const int p = g + k < a.n ? par[g + k] : -1;
-                v[k] = U{};
-                if (p >= 0 && p < a.W && !(in_place && p == g + k))
-                    v[k] = reinterpret_cast<const U *>(src + p * beam_bytes)[i];
-            }
+        for (int k = 0; k < GROUP; ++k) kids[k] = g + k < a.W ? __ballot(mine == g + k) : 0;
+        if (i >= units) continue;
+        U v[GROUP];
 #pragma unroll
-            for (int k = 0; k < GROUP; ++k) {
-                const int p = g + k < a.n ? par[g + k] : -1;
-                if (p >= 0 && p < a.W && !(in_place && p == g + k))
-                    reinterpret_cast<U *>(dst + (g + k) * beam_bytes)[i] = v[k];
+        for (int k = 0; k < GROUP; ++k) {
+            v[k] = U{};
+            if (kids[k]) v[k] = load_unit<U>(src + (g + k) * beam_bytes, i);
+        }
+#pragma unroll
+        for (int k = 0; k < GROUP; ++k) {
+            for (uint64_t m = kids[k]; m; m &= m - 1) {
+                const int child = __ffsll(static_cast<long long>(m)) - 1;
+                __builtin_nontemporal_store(v[k],
+                                            reinterpret_cast<U *>(dst + child * beam_bytes) + i);
             }
         }
     }
