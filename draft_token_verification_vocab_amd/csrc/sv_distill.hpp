@@ -112,25 +112,28 @@ struct ListShared {
     int dup;                   // some id is listed twice
 };
 
-// One entry of a row's list on its way to LDS.
+// One entry of a row's list on its way to LDS, in steps, so that its loads lie
+// among the row's without a wait of their own.
 struct ListEntry {
     int id = -1;     // -1: not a listed entry
     float t = 0.f;
-    float s = 0.f;
     __device__ __forceinline__ void fetch(const DistillArgs &a, int64_t row, int i) {
         id = a.ids[row * a.k + i];
         t = a.logits[row * a.k + i];
     }
-    template <typename T>
-    __device__ __forceinline__ void gather(const DistillArgs &a, const T *rp) {
+    __device__ __forceinline__ void put(const DistillArgs &a, ListShared &l, int i) {
         if (!(id >= 0 && id < a.V && t > kMasked)) id = -1;
-        s = id >= 0 ? Elem<T>::at(rp, id) : 0.f;
-    }
-    __device__ __forceinline__ void put(ListShared &l, int i) const {
         l.id[i] = id;
         l.t[i] = t;
-        l.s[i] = s > kMasked ? s : -__builtin_inff();
         l.first[i] = id >= 0;
+    }
+    // The student's logit there, to be put in l.s by the same thread.
+    template <typename T>
+    __device__ __forceinline__ float gather(const T *rp) const {
+        return id >= 0 ? Elem<T>::at(rp, id) : 0.f;
+    }
+    __device__ __forceinline__ static float seen(float s) {
+        return s > kMasked ? s : -__builtin_inff();
     }
 };
 
@@ -223,10 +226,10 @@ struct DistillShared {
 
 // Puts a row's list (entry tid of it in the threads below k) in LDS, with the
 // bitmap and each thread's chunks (of UNROLL vectors a thread) that hold a
-// listed entry.  Returns the thread's.
+// listed entry.  Returns the thread's.  The student's logits there (l.s) follow.
 template <typename T, int BLOCK, int UNROLL>
 __device__ __forceinline__ unsigned long long prepare_list(const DistillArgs &a,
-                                                           const ListEntry &entry, int tid,
+                                                           ListEntry &entry, int tid,
                                                            DistillShared<BLOCK> &sh,
                                                            uint32_t *map) {
     constexpr int EPV = Elem<T>::kPerVec;
@@ -237,7 +240,7 @@ __device__ __forceinline__ unsigned long long prepare_list(const DistillArgs &a,
     if (mapped)
         for (int i = tid; i < (a.V + 31) / 32; i += BLOCK) map[i] = 0;
     if (tid == 0) list.dup = 0;
-    if (tid < a.k) entry.put(list, tid);
+    if (tid < a.k) entry.put(a, list, tid);
     __syncthreads();
     if (tid < a.k && list.id[tid] >= 0) {
         const int id = list.id[tid];
@@ -352,25 +355,29 @@ __global__ __launch_bounds__(BLOCK) void distill_rows_kernel(DistillArgs a) {
         return;
     }
     ListEntry entry;
-    if (tid < a.k) {
-        entry.fetch(a, row, tid);
-        entry.gather<T>(a, rp);
-    }
-    const unsigned long long mine = prepare_list<T, BLOCK, UNROLL>(a, entry, tid, sh, map);
+    if (tid < a.k) entry.fetch(a, row, tid);
+    unsigned long long mine = 0;
+    float at_id = 0.f;
     OnlineSum acc(a.c);
-    stream_vectors<T, BLOCK, UNROLL, KEEP>(rp, 0, nvec, V, tid,
-                                           [&](const uint4 (&buf)[UNROLL], int it) {
-        float x[N];
+    stream_vectors<T, BLOCK, UNROLL, KEEP>(
+        rp, 0, nvec, V, tid,
+        [&](const uint4 (&buf)[UNROLL], int it) {
+            float x[N];
 #pragma unroll
-        for (int u = 0; u < UNROLL; ++u) E::unpack(buf[u], x + u * EPV);
-        if ((mine >> (it & 63)) & 1ull) {
+            for (int u = 0; u < UNROLL; ++u) E::unpack(buf[u], x + u * EPV);
+            if ((mine >> (it & 63)) & 1ull) {
 #pragma unroll
-            for (int u = 0; u < UNROLL; ++u)
-                leave_out_listed<T>(a, sh.list, map, (it * UNROLL + u) * BLOCK + tid, nvec,
-                                    x + u * EPV);
-        }
-        acc.add(x, chunk_max(x), a.c);
-    });
+                for (int u = 0; u < UNROLL; ++u)
+                    leave_out_listed<T>(a, sh.list, map, (it * UNROLL + u) * BLOCK + tid, nvec,
+                                        x + u * EPV);
+            }
+            acc.add(x, chunk_max(x), a.c);
+        },
+        [&]() {
+            mine = prepare_list<T, BLOCK, UNROLL>(a, entry, tid, sh, map);
+            at_id = entry.gather(rp);
+        });
+    if (tid < a.k) sh.list.s[tid] = ListEntry::seen(at_id);
     finish_row<BLOCK>(a, row, acc, tid, sh);
 }
 
@@ -413,10 +420,7 @@ __global__ __launch_bounds__(BLOCK, 4) void distill_held_kernel(DistillArgs a) {
         return;
     }
     ListEntry entry;
-    if (tid < a.k) {
-        entry.fetch(a, row, tid);
-        entry.gather<T>(a, rp);
-    }
+    if (tid < a.k) entry.fetch(a, row, tid);
     // Vector u*BLOCK + tid; past the full ones the last full one stands in
     // until the ragged vector or padding takes its place below.
     const buf_rsrc rs = make_rsrc(rp, static_cast<uint32_t>(nfull) * 16u);
@@ -430,6 +434,7 @@ __global__ __launch_bounds__(BLOCK, 4) void distill_held_kernel(DistillArgs a) {
         }
     }
     const unsigned long long mine = prepare_list<T, BLOCK, UNROLL>(a, entry, tid, sh, map);
+    const float at_id = entry.gather(rp);
     const uint32_t pad = E::pad_word();
     OnlineSum acc(a.c);
 #pragma unroll
@@ -466,6 +471,7 @@ __global__ __launch_bounds__(BLOCK, 4) void distill_held_kernel(DistillArgs a) {
             acc.add(x, chunk_max(x), a.c);
         });
     }
+    if (tid < a.k) sh.list.s[tid] = ListEntry::seen(at_id);
     finish_row<BLOCK>(a, row, acc, tid, sh);
     const DistillRow r = sh.row;
     if (r.mass < 0.0) {
@@ -519,8 +525,8 @@ __global__ __launch_bounds__(BLOCK) void distill_grad_kernel(DistillArgs a, int3
     if (tid < a.k) {
         ListEntry entry;
         entry.fetch(a, row, tid);
-        entry.gather<T>(a, rp);
-        entry.put(list, tid);
+        entry.put(a, list, tid);
+        list.s[tid] = ListEntry::seen(entry.gather(rp));
         list.p[tid] = list.id[tid] >= 0
                           ? exp(static_cast<double>(list.t[tid]) * a.inv_t - r.norm)
                           : 0.0;

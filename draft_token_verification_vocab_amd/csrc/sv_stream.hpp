@@ -30,10 +30,15 @@ __device__ __forceinline__ uint4 load_row_buf(buf_rsrc r, uint32_t voff, uint32_
 // over the segment's full vectors, the next chunk issued before this chunk's
 // arithmetic, a ragged last vector read element by element.  KEEP: without the
 // non-temporal hint, for rows that are read again soon (the hint keeps them
-// out of the caches).
-template <typename T, int BLOCK, int UNROLL, bool KEEP = false, typename F>
+// out of the caches).  first(): called once, after the first chunk's loads are
+// issued and before any is consumed.
+struct NoPrologue {
+    __device__ __forceinline__ void operator()() const {}
+};
+template <typename T, int BLOCK, int UNROLL, bool KEEP = false, typename F,
+          typename P = NoPrologue>
 __device__ __forceinline__ void stream_vectors(const T *row, int vbeg, int vend, int V, int tid,
-                                               F &&consume) {
+                                               F &&consume, P &&first = P{}) {
     using E = Elem<T>;
     constexpr int kChunk = UNROLL * BLOCK;
     const int nfull = V / E::kPerVec;
@@ -50,8 +55,9 @@ __device__ __forceinline__ void stream_vectors(const T *row, int vbeg, int vend,
             buf[u] = load_row_buf<KEEP>(rs, static_cast<uint32_t>(tid + u * BLOCK) * 16u, soff);
     };
     uint4 a[UNROLL], b[UNROLL];
+    if (nit > 0) load_chunk(a, 0);
+    first();
     if (nit > 0) {
-        load_chunk(a, 0);
         for (int it = 0; it + 1 < nit; ++it) {
             load_chunk(b, it + 1);
             consume(a, it);
