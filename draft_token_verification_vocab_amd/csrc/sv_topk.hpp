@@ -185,12 +185,9 @@ __global__ __launch_bounds__(BLOCK) void topk_rows_kernel(TopkArgs a) {
     }
     if (tid == 0) sh_n = sh_items = 0;
     __syncthreads();
-    uint32_t bm = sh_wm[0], bl = sh_wl[0];
+    uint32_t bm = sh_wm[0];
 #pragma unroll
-    for (int w = 1; w < NW; ++w) {
-        bm = sh_wm[w] > bm ? sh_wm[w] : bm;
-        bl = sh_wl[w] > bl ? sh_wl[w] : bl;
-    }
+    for (int w = 1; w < NW; ++w) bm = sh_wm[w] > bm ? sh_wm[w] : bm;
     const float M = from_ordered_bits(bm);
     const float ws = wave_sum_f32(acc.at(M, c));
     if (lane == 0) sh_s[wv] = static_cast<double>(ws);
@@ -200,11 +197,12 @@ __global__ __launch_bounds__(BLOCK) void topk_rows_kernel(TopkArgs a) {
     // bit below the bits that all visible maxima share, and stops as soon as
     // few more than k threads reach it.
     if (wv == 0) {
-        uint32_t key[NW];
+        uint32_t key[NW], bl = 0;
         int seen = 0;
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
             key[w] = sh_m[w * kWave + lane];
+            bl = sh_wl[w] > bl ? sh_wl[w] : bl;
             seen += __popcll(__ballot(key[w] > masked));
         }
         uint32_t tau = 0;
@@ -233,27 +231,24 @@ __global__ __launch_bounds__(BLOCK) void topk_rows_kernel(TopkArgs a) {
     // LDS, and of its second chunk, or all its chunks when a third reaches
     // tau, from the row again, noted first and then read together, a vector
     // per thread (one memory latency, whatever the chunks' owners).
-    auto collect = [&](const uint4 &v, int vi) {
-        float x[EPV];
-        E::unpack(v, x);
+    const float least = from_ordered_bits(tau);  // above kMasked
+    if (om >= tau) {
         uint32_t hit = 0;
 #pragma unroll
-        for (int e = 0; e < EPV; ++e)
-            hit |= (x[e] > kMasked && ordered_bits(x[e] + 0.0f) >= tau) ? 1u << e : 0u;
-        if (hit == 0) return;
-        int o = atomicAdd(&sh_n, __popc(hit));
+        for (int u = 0; u < UNROLL; ++u) {
+            float x[EPV];
+            E::unpack(sh_saved[u][tid], x);
 #pragma unroll
-        for (int e = 0; e < EPV; ++e) {
-            if (((hit >> e) & 1u) && o < kTopkCollect) sh_key[o] = topk_key(x[e], vi * EPV + e);
-            o += (hit >> e) & 1u;
+            for (int e = 0; e < EPV; ++e) hit |= x[e] >= least ? 1u << (u * EPV + e) : 0u;
         }
-    };
-    if (om >= tau) {
-#pragma unroll
-        for (int u = 0; u < UNROLL; ++u)
-            collect(sh_saved[u][tid], vbeg + best * kChunk + u * BLOCK + tid);
-        if (ordered_bits(m2 + 0.0f) >= tau) {
-            const bool two = ordered_bits(m3 + 0.0f) < tau;
+        int o = atomicAdd(&sh_n, __popc(hit));
+        for (; hit && o < kTopkCollect; hit &= hit - 1, ++o) {  // one or two, mostly
+            const int q = __ffs(static_cast<int>(hit)) - 1, u = q / EPV, e = q % EPV;
+            const float x = E::at(reinterpret_cast<const T *>(&sh_saved[u][tid]), e);
+            sh_key[o] = topk_key(x, (vbeg + best * kChunk + u * BLOCK + tid) * EPV + e);
+        }
+        if (m2 >= least) {
+            const bool two = !(m3 >= least);
             const int from = two ? second : 0;
             const int to = two ? second : (vend - vbeg - 1 - tid) / kChunk;
             int o = atomicAdd(&sh_items, to - from + 1);
@@ -268,9 +263,16 @@ __global__ __launch_bounds__(BLOCK) void topk_rows_kernel(TopkArgs a) {
             const int item = sh_item[j / UNROLL];
             const int vi = vbeg + (item >> 10) * kChunk + (j % UNROLL) * BLOCK + (item & 1023);
             if (item < 0 || vi >= vend) continue;
-            collect((vi + 1) * EPV <= V ? reinterpret_cast<const uint4 *>(rp)[vi]
-                                        : E::partial(rp, vi, V),
-                    vi);
+            const uint4 v = (vi + 1) * EPV <= V ? reinterpret_cast<const uint4 *>(rp)[vi]
+                                                : E::partial(rp, vi, V);
+            float x[EPV];
+            E::unpack(v, x);
+#pragma unroll
+            for (int e = 0; e < EPV; ++e) {
+                if (!(x[e] >= least)) continue;
+                const int o = atomicAdd(&sh_n, 1);
+                if (o < kTopkCollect) sh_key[o] = topk_key(x[e], vi * EPV + e);
+            }
         }
         __syncthreads();
     }
