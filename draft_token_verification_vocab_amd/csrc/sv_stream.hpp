@@ -54,32 +54,45 @@ __device__ __forceinline__ void stream_vectors(const T *row, int vbeg, int vend,
         for (int u = 0; u < UNROLL; ++u)
             buf[u] = load_row_buf<KEEP>(rs, static_cast<uint32_t>(tid + u * BLOCK) * 16u, soff);
     };
-    uint4 a[UNROLL], b[UNROLL];
-    if (nit > 0) load_chunk(a, 0);
-    first();
-    if (nit > 0) {
-        for (int it = 0; it + 1 < nit; ++it) {
-            load_chunk(b, it + 1);
-            consume(a, it);
-#pragma unroll
-            for (int u = 0; u < UNROLL; ++u) a[u] = b[u];
-        }
-    }
+    // The last, partly filled chunk (index nit).
     const int v = nit * kChunk + tid;
     const bool tail = v < nv;
-    if (tail) {
+    auto load_tail = [&](uint4 (&buf)[UNROLL]) {
+        if (!tail) return;
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
             const int vi = v + u * BLOCK;
-            b[u] = make_uint4(pad, pad, pad, pad);
+            buf[u] = make_uint4(pad, pad, pad, pad);
             if (vi < nf)
-                b[u] = load_row_buf<KEEP>(rs, static_cast<uint32_t>(vi) * 16u, 0u);
+                buf[u] = load_row_buf<KEEP>(rs, static_cast<uint32_t>(vi) * 16u, 0u);
             else if (vi < nv)
-                b[u] = E::partial(row, nfull, V);
+                buf[u] = E::partial(row, nfull, V);
         }
+    };
+    // Two register buffers take turns: the loads of a chunk are in flight
+    // while the wait for the one before it runs (a single prefetch buffer that
+    // is copied over makes each wave drain its loads once a chunk).
+    uint4 a[UNROLL], b[UNROLL];
+    if (nit > 0) load_chunk(a, 0);
+    first();
+    int it = 0;
+    for (; it + 3 <= nit; it += 2) {
+        load_chunk(b, it + 1);
+        consume(a, it);
+        load_chunk(a, it + 2);
+        consume(b, it + 1);
     }
-    if (nit > 0) consume(a, nit - 1);
-    if (tail) consume(b, nit);
+    if (it + 2 == nit) {
+        load_chunk(b, it + 1);
+        consume(a, it);
+        load_tail(a);
+        consume(b, it + 1);
+        if (tail) consume(a, nit);
+    } else {
+        load_tail(b);
+        if (nit > 0) consume(a, it);
+        if (tail) consume(b, nit);
+    }
 }
 
 // One thread's running maximum m and sum of 2^(x*c - n) over the chunks it is
@@ -93,10 +106,11 @@ __device__ __forceinline__ void stream_vectors(const T *row, int vbeg, int vend,
 // m*c itself would be large, and a power of two takes the place of c that
 // keeps those apart and makes m's own term exactly 1.
 struct OnlineSum {
-    float m = kMasked, n, slope, s = 0.f;
-    bool far = false;  // |m*c| >= kFar
+    float m = kMasked;
+    float n = -kMasked;  // until a visible logit comes every term is 2^-huge = 0
+    float slope, s = 0.f;
     static constexpr float kFar = 0x1p30f;
-    __device__ __forceinline__ explicit OnlineSum(float c) : n(mul_rn(kMasked, c)), slope(c) {}
+    __device__ __forceinline__ explicit OnlineSum(float c) : slope(c) {}
 
     // x: the chunk's N logits, cm their maximum.  NaN entries count as masked.
     template <int N>
@@ -104,13 +118,14 @@ struct OnlineSum {
         if (cm > m) {
             const float mc = mul_rn(cm, c);
             float to = ceilf(mc), k = c;
-            const bool was_far = far;
-            far = fabsf(mc) >= kFar;
-            if (far) {
-                k = ldexpf(1.0f, 31 - ilogbf(cm));
+            if (slope != c) s = 0.f;
+            if (fabsf(mc) >= kFar) {
+                // 2^(31 - exponent of cm)
+                k = __uint_as_float((285u - (__float_as_uint(cm) >> 23 & 255u)) << 23);
                 to = cm * k;
+                s = 0.f;
             }
-            s = far || was_far || n - to < -300.f ? 0.f : ldexpf(s, static_cast<int>(n - to));
+            s = ldexpf(s, static_cast<int>(n - to));
             m = cm;
             n = to;
             slope = k;
@@ -137,9 +152,7 @@ struct OnlineSum {
     // The thread's sum relative to the reference of a maximum M >= m.
     __device__ __forceinline__ float at(float M, float c) const {
         if (m == M) return s;
-        const float d = n - reference(M, c);
-        return far || fabsf(mul_rn(M, c)) >= kFar || d < -300.f ? 0.f
-                                                                : ldexpf(s, static_cast<int>(d));
+        return slope != c ? 0.f : ldexpf(s, static_cast<int>(n - reference(M, c)));
     }
     // From r, the sum of the threads' at(M): the sum of 2^((x - M)*c).
     __device__ __forceinline__ static double from_max(double r, float M, float c) {
