@@ -135,7 +135,7 @@ void launch_step_t(const DistillArgs &a, int64_t rows, hipStream_t st) {
     if ((a.V + per - 1) / per <= 4096)
         distill_held_kernel<T, 256, 8><<<grid, dim3(256), map_bytes(a), st>>>(a);
     else
-        distill_held_kernel<T, 512, 12><<<grid, dim3(512), map_bytes(a), st>>>(a);
+        distill_held_kernel<T, 512, sizeof(T) == 2 ? 12 : 8><<<grid, dim3(512), map_bytes(a), st>>>(a);
 }
 
 // Beam selection.

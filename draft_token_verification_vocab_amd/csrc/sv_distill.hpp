@@ -389,11 +389,12 @@ __global__ __launch_bounds__(BLOCK) void distill_rows_kernel(DistillArgs a) {
 // The bound is memory: with all of the row read twice, 2048 rows of 128256
 // bfloat16 logits took 245 us, the fabric's rate for their 1.6 GB.  512 threads
 // at 128 registers (two workgroups per compute unit, which cover each other's
-// waits) hold 12 vectors each, 38 % of such a row: 213 us.  16 vectors hold
-// more and gain nothing (216), in float32 they spill (2048 rows of 32000: 115 us
-// against 96).  A whole row in one workgroup of 1024 threads, alone on its
-// compute unit, took 257 us.  Rows of up to 4096 vectors take 256 threads with
-// 8 (4000 bfloat16 logits: 20 us against 36 with 512 threads).
+// waits) hold 12 vectors each, 38 % of such a row: 202 to 207 us, what a copy
+// of the same bytes takes (8 vectors: 214, 16: 211).  In float32 they hold 8
+// (2048 rows of 32000: 98 us; 12 spill: 123).  A whole row in one workgroup of
+// 1024 threads, alone on its compute unit, took 257 us.  Rows of up to 4096
+// vectors take 256 threads with 8 (2048 rows of 4000 bfloat16 logits: 21 us
+// against 36 with 512 threads).
 template <typename T, int BLOCK, int NV>
 __global__ __launch_bounds__(BLOCK, 4) void distill_held_kernel(DistillArgs a) {
     using E = Elem<T>;
