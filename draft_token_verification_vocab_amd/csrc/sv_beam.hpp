@@ -30,7 +30,7 @@ struct BeamArgs {
     const float *scores;             // [B][W]
     const uint8_t *ended;            // [B][W] or null
     const unsigned long long *list;  // [B][W][segs][n]
-    const double *seg_lse;           // [B][W][segs]
+    const double *seg_lse;           // [B][W][segs], relative to the segment's maximum
     float *out_scores;               // [B][n]
     int32_t *parents;                // [B][n]
     int32_t *tokens;                 // [B][n]
@@ -67,7 +67,7 @@ __device__ __forceinline__ double exp2_f64(double d) {
     return ldexp(p, static_cast<int>(n));
 }
 
-// ln sum e^(l/T) of a row in double, given its largest visible logit M.
+// ln sum e^((l - M)/T) of a row in double, M its largest visible logit.
 template <typename T, int BLOCK>
 __device__ __attribute__((noinline)) double exact_normaliser(const T *row, int V, float M,
                                                             double inv_t, double *sh, int tid) {
@@ -94,20 +94,7 @@ __device__ __attribute__((noinline)) double exact_normaliser(const T *row, int V
     double t = 0.0;
 #pragma unroll
     for (int w = 0; w < BLOCK / kWave; ++w) t += sh[w];
-    return static_cast<double>(M) * inv_t + log(t);
-}
-
-// ln of a sum of e^x over a row's segments: lanes hold segment lane's x.
-__device__ __forceinline__ double wave_log_sum(double x, int lane, int segs) {
-    double m = lane < segs ? x : -__builtin_inf();
-    double top = -__builtin_inf();
-    for (int s = 0; s < segs; ++s) {  // at most 64, usually a few
-        const double o = __shfl(m, s, kWave);
-        top = o > top ? o : top;
-    }
-    if (!(top > -__builtin_inf())) return top;
-    const double e = lane < segs ? exp(m - top) : 0.0;
-    return top + log(wave_sum_f64(e));
+    return log(t);
 }
 
 // One workgroup per sequence.  The segments' lists of a beam are joined first
@@ -120,6 +107,7 @@ __global__ __launch_bounds__(BLOCK) void beam_merge_kernel(BeamArgs a) {
     __shared__ unsigned long long sh_in[kMaxBeamKeys];   // [W][segs][n]
     __shared__ unsigned long long sh_key[kMaxBeamKeys];  // [W][n], 0 after the last
     __shared__ double sh_score[kMaxBeamKeys];            // [W][n], -inf after the last
+    // ln sum e^((l - M)/T) of each beam, M its largest logit (its first key's)
     __shared__ double sh_lse[kMaxBeams], sh_red[BLOCK / kWave];
     __shared__ float sh_prior[kMaxBeams];                // -inf: takes no part
     __shared__ int sh_ended[kMaxBeams];
@@ -141,19 +129,22 @@ __global__ __launch_bounds__(BLOCK) void beam_merge_kernel(BeamArgs a) {
         sh_prior[tid] = s > -__builtin_inff() ? s : -__builtin_inff();
         sh_ended[tid] = a.ended ? a.ended[static_cast<int64_t>(b) * W + tid] != 0 : 0;
     }
-    for (int q = wv; q < W; q += BLOCK / kWave) {
-        const int64_t at = (static_cast<int64_t>(b) * W + q) * segs;
-        if (segs == 1) {
-            if (lane == 0) sh_lse[q] = a.seg_lse[at];
-        } else {
-            const double l = wave_log_sum(lane < segs ? a.seg_lse[at + lane] : -inf, lane, segs);
-            if (lane == 0) sh_lse[q] = l;
-        }
-    }
+    if (segs == 1 && tid < W) sh_lse[tid] = a.seg_lse[static_cast<int64_t>(b) * W + tid];
     if (tid == 0) sh_again = 0;
     if (segs > 1) {
         if (tid < total) sh_key[tid] = 0;
         __syncthreads();
+        for (int q = wv; q < W; q += BLOCK / kWave) {
+            const bool there = lane < segs && sh_in[(q * segs + lane) * n] != 0;
+            const float m = there ? key_value(sh_in[(q * segs + lane) * n]) : -__builtin_inff();
+            const float M = wave_max_f32(m);
+            const double e =
+                there ? exp((static_cast<double>(m) - static_cast<double>(M)) * a.inv_t +
+                            a.seg_lse[(static_cast<int64_t>(b) * W + q) * segs + lane])
+                      : 0.0;
+            const double t = wave_sum_f64(e);
+            if (lane == 0) sh_lse[q] = log(t);
+        }
         int share = 1;
         while (share < kWave && W * per * share * 2 <= BLOCK) share *= 2;
         const int at = tid / share, w = at / per;
@@ -180,7 +171,10 @@ __global__ __launch_bounds__(BLOCK) void beam_merge_kernel(BeamArgs a) {
             if (sh_ended[w])
                 x = tid == w * n ? s : -inf;
             else if (key)
-                x = s + (static_cast<double>(key_value(key)) * a.inv_t - sh_lse[w]);
+                x = s + ((static_cast<double>(key_value(key)) -
+                          static_cast<double>(key_value(sh_key[w * n]))) *
+                             a.inv_t -
+                         sh_lse[w]);
         }
         sh_score[tid] = x;
     };

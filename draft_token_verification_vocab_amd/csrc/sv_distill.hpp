@@ -27,16 +27,27 @@ namespace sv {
 constexpr int kDistillMax = kTopkMax;         // longest list
 constexpr int kListMapVocab = 1 << 18;        // ids the list's bitmap in LDS covers
 
-// What the gradient needs of a row's forward pass.
+// What the gradient needs of a row's forward pass.  Normalisers are kept
+// relative to a logit, so that they lose nothing however large l/T is.
 struct DistillRow {
-    double lse;    // student: ln sum e^z
-    double norm;   // teacher: L
+    double lse;    // student: ln sum e^((s - top)/T)
+    double norm;   // teacher: ln p_i = (t_i - t_top)/T - norm
     double mass;   // P + r, or -1 for a row that is left out
-    double coef;   // mass * e^(M/T - lse) - r / sum_{outside} 2^((s - M) c)
-    float m;       // M
+    double coef;   // (P + r) e^((m - top)/T - lse) - r / sum_{outside} 2^((s - m) c)
+    float top;     // the largest of the student's logits
+    float t_top;   // the largest listed logit (0 with the teacher's normaliser)
+    float m;       // M, the largest logit outside the list
     int32_t pad_;
 };
-static_assert(sizeof(DistillRow) == 40, "spec_distill_state_bytes");
+static_assert(sizeof(DistillRow) == 48, "spec_distill_state_bytes");
+
+// ln q and ln p of a logit, in double.
+__device__ __forceinline__ double log_q(const DistillRow &r, float s, double inv_t) {
+    return (static_cast<double>(s) - static_cast<double>(r.top)) * inv_t - r.lse;
+}
+__device__ __forceinline__ double log_p(const DistillRow &r, float t, double inv_t) {
+    return (static_cast<double>(t) - static_cast<double>(r.t_top)) * inv_t - r.norm;
+}
 
 struct DistillArgs {
     const void *student;
@@ -145,63 +156,62 @@ __device__ __forceinline__ void mark_first(int i, ListShared &l) {
 
 // Gradient at the listed id i (the first of equal ids): its own share less the
 // teacher's masses listed there.
-__device__ __forceinline__ float listed_grad(int i, int k, const ListShared &l, double lse,
-                                             double mass, double inv_t, double g) {
+__device__ __forceinline__ float listed_grad(int i, int k, const ListShared &l,
+                                             const DistillRow &r, double inv_t, double g) {
     double p = l.p[i];
     if (l.dup)
         for (int j = i + 1; j < k; ++j)
             if (l.id[j] == l.id[i]) p += l.p[j];
-    const double q = exp(static_cast<double>(l.s[i]) * inv_t - lse);
-    return static_cast<float>((q * mass - p) * inv_t * g);
+    return static_cast<float>((exp(log_q(r, l.s[i], inv_t)) * r.mass - p) * inv_t * g);
 }
 
 // One wave: the row's loss and gradient state from the list and the sum S of
 // 2^((s - M) c) outside it (M <= kMasked: nothing visible there).
 __device__ __forceinline__ DistillRow settle_row(const DistillArgs &a, int64_t row, int lane,
                                                  ListShared &l, float M, double S, float *loss) {
-    const double inf = __builtin_inf();
+    const float inf = __builtin_inff();
     const double it = a.inv_t;
     const bool outside = M > kMasked;
-    const double rest = outside ? static_cast<double>(M) * it + log(S) : -inf;
-    double t[2], z[2];
+    float t[2], s[2];
     bool first[2];
-    double tm = -inf, zm = rest;
+    float tm = -inf, sm = outside ? M : -inf;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int i = lane + h * kWave;
         const bool in = i < a.k && l.id[i] >= 0;
-        t[h] = in ? static_cast<double>(l.t[i]) * it : -inf;
-        z[h] = in ? static_cast<double>(l.s[i]) * it : -inf;
+        t[h] = in ? l.t[i] : -inf;
+        s[h] = in ? l.s[i] : -inf;
         first[h] = in && l.first[i];
-        tm = fmax(tm, t[h]);
-        zm = fmax(zm, z[h]);
+        tm = fmaxf(tm, t[h]);
+        sm = fmaxf(sm, s[h]);
     }
-#pragma unroll
-    for (int o = 1; o < kWave; o *= 2) {
-        tm = fmax(tm, __shfl_xor(tm, o, kWave));
-        zm = fmax(zm, __shfl_xor(zm, o, kWave));
-    }
+    tm = wave_max_f32(tm);
+    sm = wave_max_f32(sm);
     DistillRow r{};
     r.mass = -1.0;
     r.m = M;
     *loss = 0.f;
-    if (!(tm > -inf) || !(zm > -inf)) return r;  // nothing listed, or nothing visible
+    if (!(tm > -inf) || !(sm > -inf)) return r;  // nothing listed, or nothing visible
+    r.top = sm;
+    r.t_top = a.lse ? 0.f : tm;
     double zs = 0.0, ts = 0.0;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        if (first[h]) zs += exp(z[h] - zm);
-        ts += exp(t[h] - tm);
+        if (first[h]) zs += exp(log_q(r, s[h], it));
+        ts += exp((static_cast<double>(t[h]) - static_cast<double>(tm)) * it);
     }
-    const double total = wave_sum_f64(zs) + (outside ? exp(rest - zm) : 0.0);
-    r.lse = zm + log(total);
-    r.norm = a.lse ? static_cast<double>(a.lse[row]) : tm + log(wave_sum_f64(ts));
+    // log_q and log_p of the row so far are without their normalisers (0)
+    const double rest = outside ? log_q(r, M, it) + log(S) : -static_cast<double>(inf);
+    const double total = wave_sum_f64(zs) + (outside ? exp(rest) : 0.0);
+    r.lse = log(total);
+    r.norm = a.lse ? static_cast<double>(a.lse[row]) : log(wave_sum_f64(ts));
     double ps = 0.0, ls = 0.0;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const double lp = t[h] - r.norm, p = exp(lp);
+        const double lp = log_p(r, t[h], it), p = exp(lp);
         if (lane + h * kWave < a.k) l.p[lane + h * kWave] = p;
         ps += p;
-        if (p > 0.0) ls += p * (lp - (z[h] - r.lse));
+        if (p > 0.0) ls += p * (lp - log_q(r, s[h], it));
     }
     const double P = wave_sum_f64(ps);
     const double left = a.lse && outside ? fmax(0.0, 1.0 - P) : 0.0;
@@ -209,7 +219,7 @@ __device__ __forceinline__ DistillRow settle_row(const DistillArgs &a, int64_t r
     if (left > 0.0) total_loss += left * (log(left) - (rest - r.lse));
     *loss = static_cast<float>(total_loss);
     r.mass = P + left;
-    r.coef = outside ? r.mass * exp(static_cast<double>(M) * it - r.lse) - left / S : 0.0;
+    r.coef = outside ? (r.mass * exp(rest - r.lse) - left) / S : 0.0;
     return r;
 }
 
@@ -332,7 +342,7 @@ __device__ __forceinline__ void patch_listed(const DistillArgs &a, const Distill
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     if (tid < a.k && list.id[tid] >= 0 && list.first[tid])
-        gp[list.id[tid]] = GradOut<T>::one(listed_grad(tid, a.k, list, r.lse, r.mass, a.inv_t, g));
+        gp[list.id[tid]] = GradOut<T>::one(listed_grad(tid, a.k, list, r, a.inv_t, g));
 }
 
 // The loss, a workgroup per row.  KEEP: the row is read again soon.
@@ -529,7 +539,7 @@ __global__ __launch_bounds__(BLOCK) void distill_grad_kernel(DistillArgs a, int3
         entry.put(a, list, tid);
         list.s[tid] = ListEntry::seen(entry.gather(rp));
         list.p[tid] = list.id[tid] >= 0
-                          ? exp(static_cast<double>(list.t[tid]) * a.inv_t - r.norm)
+                          ? exp(log_p(r, list.t[tid], a.inv_t))
                           : 0.0;
     }
     __syncthreads();
@@ -560,7 +570,7 @@ __global__ __launch_bounds__(BLOCK) void distill_grad_kernel(DistillArgs a, int3
         const int w = list.id[tid] / EPV;
         if (w >= vbeg && w < vend)
             gp[list.id[tid]] =
-                GradOut<T>::one(listed_grad(tid, a.k, list, r.lse, r.mass, a.inv_t, g));
+                GradOut<T>::one(listed_grad(tid, a.k, list, r, a.inv_t, g));
     }
 }
 

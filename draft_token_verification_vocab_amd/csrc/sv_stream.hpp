@@ -162,6 +162,11 @@ struct OnlineSum {
     }
 };
 
+// Largest float over the wave.
+__device__ __forceinline__ float wave_max_f32(float x) {
+    return from_ordered_bits(wave_max_u32(ordered_bits(x)));
+}
+
 // Largest of a chunk's logits in a chain of three-input maxima (NaN entries
 // are passed over).
 template <int N>

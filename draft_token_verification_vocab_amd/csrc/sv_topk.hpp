@@ -41,7 +41,7 @@ struct TopkArgs {
     float *lse;              // [rows]
     // or lists for the beam merge: keys in decreasing order, 0 after the last
     unsigned long long *list;  // [rows][segs][k]
-    double *seg_lse;           // [rows][segs] ln sum e^(l/T), -inf when all is masked
+    double *seg_lse;           // [rows][segs] ln sum e^((l - max)/T), -inf when all is masked
     // rows that take no part (beam selection), both nullable
     const uint8_t *ended;    // [rows]
     const float *scores;     // [rows]: -inf takes no part
@@ -332,13 +332,11 @@ __global__ __launch_bounds__(BLOCK) void topk_rows_kernel(TopkArgs a) {
         double r = 0.0;
 #pragma unroll
         for (int w = 0; w < NW; ++w) r += sh_s[w];
-        const double l = bm > masked ? static_cast<double>(M) * a.inv_t +
-                                           log(OnlineSum::from_max(r, M, c))
-                                     : -__builtin_inf();
+        const double l = bm > masked ? log(OnlineSum::from_max(r, M, c)) : -__builtin_inf();
         if (a.list)
             a.seg_lse[blockIdx.x] = l;
         else
-            a.lse[row] = static_cast<float>(l);
+            a.lse[row] = static_cast<float>(static_cast<double>(M) * a.inv_t + l);
     }
 }
 

@@ -481,7 +481,7 @@ typedef struct spec_distill_params {
     int64_t reserved;   /* must be 0                                          */
 } spec_distill_params;
 
-/* Bytes of the state spec_distill_loss leaves for spec_distill_grad (40 per
+/* Bytes of the state spec_distill_loss leaves for spec_distill_grad (48 per
  * row; device, 16-byte aligned, owned by the caller). */
 size_t spec_distill_state_bytes(int64_t rows);
 

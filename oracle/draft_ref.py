@@ -56,10 +56,15 @@ def distill(student, ids, logits, lse, T=1.0, keep=None, grad_loss=None):
         if not listed or not seen.any():
             continue
         at = np.array([i for i, _ in listed])
-        t = np.array([v for _, v in listed]) / T
-        norm = log_sum_exp(t, np.ones(len(t), bool)) if lse is None else float(lse[r])
+        # relative to the largest logits, so that nothing is lost however large l/T
+        t = np.array([v for _, v in listed])
+        if lse is None:
+            t = (t - t.max()) / T
+            norm = log_sum_exp(t, np.ones(len(t), bool))
+        else:
+            t, norm = t / T, float(lse[r])
         p = np.exp(t - norm)
-        z = np.where(seen, x[r], 0.0) / T
+        z = (np.where(seen, x[r], 0.0) - x[r][seen].max()) / T
         log_total = log_sum_exp(z, seen)
         log_q = np.where(seen, z - log_total, -np.inf)
         q = np.exp(log_q)
@@ -103,7 +108,7 @@ def beam_select(x, scores, n, T=1.0, ended=None, eos=-1):
             seen = visible(x[b, w])
             if not seen.any():
                 continue
-            z = np.where(seen, x[b, w], 0.0) / T
+            z = (np.where(seen, x[b, w], 0.0) - x[b, w][seen].max()) / T
             norm = log_sum_exp(z, seen)
             at = np.flatnonzero(seen)
             order = at[np.argsort(-x[b, w][at], kind="stable")][:n]

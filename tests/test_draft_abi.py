@@ -71,7 +71,7 @@ def test_distill_validates_on_host(L):
     assert loss(state=P(8)) == -1
     assert grad(state=None) == -1 and grad(state=P(8)) == -1 and grad(out=P(8)) == -1
     assert step(g=None) == -1 and step(g=P(8)) == -1
-    assert L.spec_distill_state_bytes(7) == 280 and L.spec_distill_state_bytes(0) == 0
+    assert L.spec_distill_state_bytes(7) == 7 * 48 and L.spec_distill_state_bytes(0) == 0
     assert L.spec_distill_state_bytes(-1) == 0
 
 

@@ -149,6 +149,18 @@ def test_near_ties_are_decided_by_the_exact_scores(V):
     assert len(np.unique(r["parents"][:, 0])) == W
 
 
+@pytest.mark.parametrize("T", [1.0, 1e-4])
+def test_huge_logits(T):
+    # l / T beyond a double's whole numbers: differences are formed first
+    x, scores, rng = beams(3, 4, 9001, 15)
+    x[:, 1:] += 7e11
+    x[0, 2] *= 1e20
+    x[1, 3] -= 3e12
+    for V in (900, 9001):
+        select(x[..., :V], scores, 6, T=T)
+        select(x[..., :V], scores, 6, "bf16", T=T)
+
+
 def test_workspace_is_reused_and_calls_agree():
     x, scores, _ = beams(8, 4, 5003, 21)
     t = torch.zeros(8, 4, 5004)

@@ -39,12 +39,13 @@ def bounds(x, ids, logits, lse, T, keep, grad_loss, loss, grad, dtype):
         if (keep is not None and not keep[r]) or not listed or not seen.any():
             continue
         at = np.array([i for i, _ in listed])
-        t = np.array([v for _, v in listed], np.float64) / T
+        t = np.array([v for _, v in listed], np.float64)
+        t = t / T if lse is not None else (t - t.max()) / T
         norm = ref.log_sum_exp(t, np.ones(len(t), bool)) if lse is None else float(lse[r])
         P = np.exp(t - norm).sum()
         rest = max(0.0, 1.0 - P) if lse is not None else 0.0
         mass = P + rest
-        z = np.where(seen, x[r], 0.0) / T
+        z = (np.where(seen, x[r], 0.0) - x[r][seen].max()) / T
         q = np.where(seen, np.exp(z - ref.log_sum_exp(z, seen)), 0.0)
         outside = seen.copy()
         outside[at] = False
@@ -230,3 +231,16 @@ def test_leading_dimensions_and_no_rows():
     none = [a[:0] for a in t]
     loss0, grad0 = sv.distill_step(*none)
     assert loss0.shape == (0,) and grad0.shape == (0, 500)
+
+
+@pytest.mark.parametrize("T", [1.0, 1e-4])
+def test_huge_logits(T):
+    # |l| / T beyond 2^30: only the largest unlisted logits have a share of rho
+    x, ids, logits, lse, rng = batch(3, 1000, 6, 41)
+    top = [i for i in range(1000) if i not in set(ids[0])][:3]
+    x[0, top[:2]] = 4e11
+    x[1] = -6e11
+    x[1, ids[1]] = -6e11
+    x[2] *= 1e10
+    l, g, _ = check(x, ids, logits, None, T=T)
+    assert np.isfinite(g).all()

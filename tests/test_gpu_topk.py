@@ -137,3 +137,15 @@ def test_many_rows_beyond_32_bit_offsets():
     assert np.array_equal(r["ids"][at].cpu().numpy(), ids)
     assert np.array_equal(r["values"][at].cpu().numpy(), values.astype(np.float32))
     assert r["ids"][1].tolist() == [0, 1, 2, 3, 4]
+
+
+def test_huge_logits():
+    # |l| / T beyond 2^30: only the largest logits count
+    x = np.full((4, 3000), -5.0, np.float32)
+    x[0, [5, 2999]] = 3e12
+    x[1] = -np.linspace(2e29, 9e29, 3000)
+    x[2, ::7] = 1.5e9
+    x[3, 100:] = -7e11
+    check(x, 9, "f32")
+    check(x, 9, "f32", T=1e-4)
+    check(x[:, :2990], 9, "bf16", T=3.0)
