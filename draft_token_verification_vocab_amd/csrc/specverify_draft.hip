@@ -25,28 +25,41 @@ bool grid_fits(int64_t blocks, int block) {
     return blocks <= (int64_t{1} << 32) / block - 1 && blocks <= INT32_MAX;
 }
 
-// Workgroup shapes: the row pass's for a workgroup per row (several rows share
-// a compute unit), smaller ones for a row cut into segments.
+// Workgroup shapes, a workgroup per row.  Long rows take the row pass's shapes.
+// Rows of up to 128 KB take 256 threads: a row's fixed work (barriers, the
+// list's selection or the loss) weighs more there, and more of the smaller
+// workgroups share a compute unit.  2500 rows, us at 256 threads against the
+// long rows' shape, top 16 (loss): 4000 bfloat16 logits 14 (14) against 39
+// (30), 32000 31 (32) against 46 (42), 50264 44 (46) against 51 (51), 128256
+// 101 (104) against 99 (100); 32000 float32 51 (52) against 56 (64), 50264 81
+// (84) against 79 (81).  Beam rows that are cut into segments take 256 too.
 template <typename T>
-struct WideShape;
+struct LongShape;
 template <>
-struct WideShape<uint16_t> {
+struct LongShape<uint16_t> {
     static constexpr int block = 768, unroll = 2;
 };
 template <>
-struct WideShape<float> {
+struct LongShape<float> {
     static constexpr int block = 512, unroll = 4;
 };
-constexpr int kSplitBlock = 256;
+constexpr int kShortBlock = 256;
+constexpr int kShortVecs = 8192;  // 16-byte vectors
+
+template <typename T>
+int row_vecs(int32_t V) {
+    constexpr int per = 16 / sizeof(T);
+    return (V + per - 1) / per;
+}
 
 template <typename T>
 void launch_topk_t(const TopkArgs &a, int64_t rows, hipStream_t st) {
-    using S = WideShape<T>;
+    using S = LongShape<T>;
     const dim3 grid(static_cast<unsigned>(rows * a.segs));
-    if (a.segs == 1)
+    if (a.segs == 1 && row_vecs<T>(a.V) > kShortVecs)
         topk_rows_kernel<T, S::block, S::unroll><<<grid, dim3(S::block), 0, st>>>(a);
     else
-        topk_rows_kernel<T, kSplitBlock, S::unroll><<<grid, dim3(kSplitBlock), 0, st>>>(a);
+        topk_rows_kernel<T, kShortBlock, S::unroll><<<grid, dim3(kShortBlock), 0, st>>>(a);
 }
 
 void launch_topk(const TopkArgs &a, int64_t rows, int32_t dtype, hipStream_t st) {
@@ -64,8 +77,7 @@ TopkArgs topk_args(const void *logits, int64_t row_stride, int32_t V, int32_t dt
     a.V = V;
     a.k = k;
     a.segs = 1;
-    const int per = 16 / elem_size(dtype);
-    a.seg_vecs = (V + per - 1) / per;
+    a.seg_vecs = dtype == SPEC_DTYPE_BF16 ? row_vecs<uint16_t>(V) : row_vecs<float>(V);
     a.c = log2e_over(temperature);
     a.inv_t = 1.0 / static_cast<double>(temperature);
     return a;
@@ -118,21 +130,30 @@ size_t map_bytes(const DistillArgs &a) {
 
 template <typename T>
 void launch_loss_t(const DistillArgs &a, int64_t rows, hipStream_t st) {
-    using S = WideShape<T>;
-    const dim3 grid(static_cast<unsigned>(rows)), block(S::block);
-    if (a.state && rows * a.V * static_cast<int64_t>(sizeof(T)) <= kCacheBytes)
-        distill_rows_kernel<T, S::block, S::unroll, true>
-            <<<grid, block, map_bytes(a), st>>>(a);
-    else
-        distill_rows_kernel<T, S::block, S::unroll, false>
-            <<<grid, block, map_bytes(a), st>>>(a);
+    using S = LongShape<T>;
+    const dim3 grid(static_cast<unsigned>(rows));
+    const bool again = a.state && rows * a.V * static_cast<int64_t>(sizeof(T)) <= kCacheBytes;
+    if (row_vecs<T>(a.V) > kShortVecs) {
+        if (again)
+            distill_rows_kernel<T, S::block, S::unroll, true>
+                <<<grid, dim3(S::block), map_bytes(a), st>>>(a);
+        else
+            distill_rows_kernel<T, S::block, S::unroll, false>
+                <<<grid, dim3(S::block), map_bytes(a), st>>>(a);
+    } else {
+        if (again)
+            distill_rows_kernel<T, kShortBlock, S::unroll, true>
+                <<<grid, dim3(kShortBlock), map_bytes(a), st>>>(a);
+        else
+            distill_rows_kernel<T, kShortBlock, S::unroll, false>
+                <<<grid, dim3(kShortBlock), map_bytes(a), st>>>(a);
+    }
 }
 
 template <typename T>
 void launch_step_t(const DistillArgs &a, int64_t rows, hipStream_t st) {
-    constexpr int per = 16 / sizeof(T);
     const dim3 grid(static_cast<unsigned>(rows));
-    if ((a.V + per - 1) / per <= 4096)
+    if (row_vecs<T>(a.V) <= 4096)
         distill_held_kernel<T, 256, 8><<<grid, dim3(256), map_bytes(a), st>>>(a);
     else
         distill_held_kernel<T, 512, sizeof(T) == 2 ? 12 : 8><<<grid, dim3(512), map_bytes(a), st>>>(a);
@@ -142,12 +163,13 @@ void launch_step_t(const DistillArgs &a, int64_t rows, hipStream_t st) {
 constexpr int kBeamMergeBlock = 512;
 
 // How a beam selection's rows are cut into workgroups, and its workspace.  A
-// row's listing keeps a compute unit's vector units busy (256 KB take 12 us
-// there), so few rows are cut into segments, as long as the merge can take
-// their lists: one sequence of four beams of 128256 bfloat16 logits 16.6 us
-// against 19.0, of 2^20 logits 23 against 72; 240 rows lose by it (23.0 against
-// 20.9).
-constexpr int kSplitRows = 64;       // rows below which they are cut
+// row's listing keeps a compute unit's vector units busy (256 KB take 10 us
+// there), so a few long rows are cut into segments, as far as the merge can
+// take their lists: one sequence of four beams of 128256 bfloat16 logits 13.2 us
+// against 16.4, eight of eight beams 14.6 against 17.6.  Rows of 128 KB lose by
+// it (10.8 against 10.4), and so do 240 rows (21.5 against 19.0).
+constexpr int kSplitRows = 64;       // most rows that are cut
+constexpr int kSplitVecs = 12288;    // 16-byte vectors of the shortest that are
 constexpr int kSplitBlocks = 1024;   // workgroups to aim for
 constexpr int kMaxSegs = 64;         // one lane per segment in the merge
 struct BeamPlan {
@@ -157,11 +179,11 @@ struct BeamPlan {
 
 template <typename T>
 BeamPlan plan_beam_t(int64_t rows, int32_t V, int32_t beams, int32_t n) {
-    using S = WideShape<T>;
-    constexpr int per = 16 / sizeof(T), split_chunk = kSplitBlock * S::unroll;
-    const int nvec = (V + per - 1) / per;
-    BeamPlan p{1, nvec, S::block * S::unroll, 0, 0, 0};
-    if (rows <= kSplitRows) {
+    using S = LongShape<T>;
+    constexpr int split_chunk = kShortBlock * S::unroll;
+    const int nvec = row_vecs<T>(V);
+    BeamPlan p{1, nvec, (nvec > kShortVecs ? S::block : kShortBlock) * S::unroll, 0, 0, 0};
+    if (rows <= kSplitRows && nvec >= kSplitVecs) {
         int64_t want = (kSplitBlocks + rows - 1) / rows;
         const int by_len = (nvec + split_chunk - 1) / split_chunk;
         const int fit = kMaxBeamKeys / (beams * n);

@@ -48,7 +48,8 @@ def beams(B, W, V, seed, scale=4.0):
 @pytest.mark.parametrize("B,W,V,n", [
     (1, 1, 2, 1), (2, 3, 5, 4), (3, 2, 9, 30), (1, 4, 1000, 8), (5, 5, 4099, 10),
     (2, 32, 700, 16), (3, 8, 3001, 64), (40, 8, 1500, 16), (1, 4, 32000, 8), (64, 4, 2003, 4),
-    (1, 16, 50257, 32), (2, 2, 128256, 4), (260, 1, 777, 5)])
+    (1, 16, 50257, 32), (2, 2, 128256, 4), (260, 1, 777, 5), (2, 8, 98304, 16),
+    (1, 3, 150001, 10), (8, 8, 98310, 8)])
 def test_selection(B, W, V, n, dtype):
     x, scores, _ = beams(B, W, V, B + 100 * W + V + n)
     select(x, scores, n, dtype)
@@ -124,12 +125,12 @@ def test_equal_scores(dtype):
     assert (r["parents"][2] == 2).all()
 
 
-@pytest.mark.parametrize("V", [4000, 40000])
-def test_near_ties_are_decided_by_the_exact_scores(V):
+@pytest.mark.parametrize("V,B", [(4000, 48), (40000, 48), (100000, 12)])
+def test_near_ties_are_decided_by_the_exact_scores(V, B):
     """Beams whose rows hold the same logits in another order, but for one that
     moves the normaliser by 1e-9 to 1e-6: float sums would order them at
     random, the gaps in double are a million times a double sum's error."""
-    B, W = 48, 4
+    W = 4
     rng = np.random.default_rng(V)
     x = np.empty((B, W, V), np.float32)
     for b in range(B):
@@ -152,11 +153,11 @@ def test_near_ties_are_decided_by_the_exact_scores(V):
 @pytest.mark.parametrize("T", [1.0, 1e-4])
 def test_huge_logits(T):
     # l / T beyond a double's whole numbers: differences are formed first
-    x, scores, rng = beams(3, 4, 9001, 15)
+    x, scores, rng = beams(3, 4, 100001, 15)
     x[:, 1:] += 7e11
     x[0, 2] *= 1e20
     x[1, 3] -= 3e12
-    for V in (900, 9001):
+    for V in (900, 100001):
         select(x[..., :V], scores, 6, T=T)
         select(x[..., :V], scores, 6, "bf16", T=T)
 
