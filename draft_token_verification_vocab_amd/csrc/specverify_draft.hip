@@ -52,21 +52,22 @@ int row_vecs(int32_t V) {
     return (V + per - 1) / per;
 }
 
-template <typename T>
+template <typename T, bool LSE>
 void launch_topk_t(const TopkArgs &a, int64_t rows, hipStream_t st) {
     using S = LongShape<T>;
     const dim3 grid(static_cast<unsigned>(rows * a.segs));
     if (a.segs == 1 && row_vecs<T>(a.V) > kShortVecs)
-        topk_rows_kernel<T, S::block, S::unroll><<<grid, dim3(S::block), 0, st>>>(a);
+        topk_rows_kernel<T, S::block, S::unroll, LSE><<<grid, dim3(S::block), 0, st>>>(a);
     else
-        topk_rows_kernel<T, kShortBlock, S::unroll><<<grid, dim3(kShortBlock), 0, st>>>(a);
+        topk_rows_kernel<T, kShortBlock, S::unroll, LSE><<<grid, dim3(kShortBlock), 0, st>>>(a);
 }
 
 void launch_topk(const TopkArgs &a, int64_t rows, int32_t dtype, hipStream_t st) {
+    const bool lse = a.list || a.lse;
     if (dtype == SPEC_DTYPE_BF16)
-        launch_topk_t<uint16_t>(a, rows, st);
+        lse ? launch_topk_t<uint16_t, true>(a, rows, st) : launch_topk_t<uint16_t, false>(a, rows, st);
     else
-        launch_topk_t<float>(a, rows, st);
+        lse ? launch_topk_t<float, true>(a, rows, st) : launch_topk_t<float, false>(a, rows, st);
 }
 
 TopkArgs topk_args(const void *logits, int64_t row_stride, int32_t V, int32_t dtype,

@@ -123,7 +123,8 @@ __device__ __attribute__((noinline)) uint64_t radix_kth(const T *row, int ebeg, 
     return prefix;
 }
 
-template <typename T, int BLOCK, int UNROLL>
+// LSE: with the log-normaliser (else a third of the arithmetic is left out).
+template <typename T, int BLOCK, int UNROLL, bool LSE>
 __global__ __launch_bounds__(BLOCK) void topk_rows_kernel(TopkArgs a) {
     using E = Elem<T>;
     constexpr int EPV = E::kPerVec;
@@ -170,7 +171,10 @@ __global__ __launch_bounds__(BLOCK) void topk_rows_kernel(TopkArgs a) {
 #pragma unroll
             for (int u = 0; u < UNROLL; ++u) sh_saved[u][tid] = buf[u];
         }
-        acc.add(x, cm, c);
+        if (LSE)
+            acc.add(x, cm, c);
+        else
+            acc.m = cm > acc.m ? cm : acc.m;
     });
 
     // Segment maximum, smallest visible thread maximum, and the normaliser.
@@ -189,8 +193,10 @@ __global__ __launch_bounds__(BLOCK) void topk_rows_kernel(TopkArgs a) {
 #pragma unroll
     for (int w = 1; w < NW; ++w) bm = sh_wm[w] > bm ? sh_wm[w] : bm;
     const float M = from_ordered_bits(bm);
-    const float ws = wave_sum_f32(acc.at(M, c));
-    if (lane == 0) sh_s[wv] = static_cast<double>(ws);
+    if (LSE) {
+        const float ws = wave_sum_f32(acc.at(M, c));
+        if (lane == 0) sh_s[wv] = static_cast<double>(ws);
+    }
 
     // tau: a value that at least k threads' maxima reach (all visible logits
     // when fewer than k threads hold one).  The first wave builds it bit by
@@ -328,7 +334,7 @@ __global__ __launch_bounds__(BLOCK) void topk_rows_kernel(TopkArgs a) {
     }
     for (int i = n + tid; i < k; i += BLOCK) put(i, 0);
 
-    if (tid == BLOCK - 1 && (a.list || a.lse)) {
+    if (LSE && tid == BLOCK - 1) {
         double r = 0.0;
 #pragma unroll
         for (int w = 0; w < NW; ++w) r += sh_s[w];

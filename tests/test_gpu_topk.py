@@ -45,6 +45,9 @@ def check(x, k, dtype, T=1.0, stride=None):
     assert np.array_equal(got["values"], values.astype(np.float32))
     for a, b in zip(got["lse"], lse):
         assert a == b or abs(a - b) <= lse_tolerance(V, b), (a, b)
+    alone = sv.row_topk(t.to(DEV), k, temperature=T, vocab=V, lse=False)
+    assert set(alone) == {"values", "ids"} and torch.equal(alone["ids"], r["ids"])
+    assert torch.equal(alone["values"], r["values"])
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
