@@ -1,6 +1,7 @@
 /*
  * specverify.h -- C ABI of an MI355X (gfx950) library for batched
- * speculative-decoding verification over full-vocabulary logits.
+ * speculative-decoding verification over full-vocabulary logits, and for what
+ * a draft model needs beside it (top-logit lists, distillation, beam search).
  *
  * The method comes from three pages:
  *   [SD]  "Speculative Decoding: как черновая модель ускоряет генерацию LLM
