@@ -107,6 +107,13 @@ spec_status check_distill(const void *student, const int32_t *ids, const float *
     return SPEC_OK;
 }
 
+// The gradient replaces the logits exactly, or shares no memory with them.
+bool overlaps_partly(const void *student, const void *grad, const spec_distill_params *p) {
+    const int64_t bytes = p->rows * p->row_stride * elem_size(p->dtype);
+    const char *s = static_cast<const char *>(student), *g = static_cast<const char *>(grad);
+    return s != g && s < g + bytes && g < s + bytes;
+}
+
 DistillArgs distill_args(const void *student, const int32_t *ids, const float *logits,
                          const spec_distill_params *p) {
     DistillArgs a{};
@@ -235,6 +242,11 @@ spec_status check_beam(int32_t batch, int32_t beams, int32_t vocab, int32_t dtyp
     return SPEC_OK;
 }
 
+struct Span {
+    const char *from, *to;
+    bool meets(const Span &o) const { return from < o.to && o.from < to; }
+};
+
 // Reordering: a unit per thread.  More units a thread only queue up behind
 // each other (2.1 GB of caches, eight beams: 386 us, with two a thread 415, with
 // four 428, with eight 439).
@@ -302,7 +314,9 @@ spec_status spec_distill_grad(const void *student, const int32_t *ids, const flo
                               const spec_distill_params *params, void *grad, void *stream) {
     const spec_status s = check_distill(student, ids, logits, params);
     if (s != SPEC_OK || params->rows == 0) return s;
-    if (!state || !aligned16(state) || !grad || !aligned16(grad)) return SPEC_ERR_ARG;
+    if (!state || !aligned16(state) || !grad || !aligned16(grad) ||
+        overlaps_partly(student, grad, params))
+        return SPEC_ERR_ARG;
     DistillArgs a = distill_args(student, ids, logits, params);
     a.state = const_cast<DistillRow *>(static_cast<const DistillRow *>(state));
     a.grad_loss = grad_loss;
@@ -325,7 +339,8 @@ spec_status spec_distill_step(const void *student, const int32_t *ids, const flo
                               void *stream) {
     const spec_status s = check_distill(student, ids, logits, params);
     if (s != SPEC_OK || params->rows == 0) return s;
-    if (!loss || !grad || !aligned16(grad)) return SPEC_ERR_ARG;
+    if (!loss || !grad || !aligned16(grad) || overlaps_partly(student, grad, params))
+        return SPEC_ERR_ARG;
     DistillArgs a = distill_args(student, ids, logits, params);
     a.lse = lse;
     a.keep = keep;
@@ -420,10 +435,20 @@ spec_status spec_beam_reorder(const int32_t *parents, const int32_t *lengths, in
             s.segments > (int64_t{1} << 44) / (s.position_bytes * (int64_t{s.positions} + 1)))
             return SPEC_ERR_UNSUPPORTED;
         const int64_t beam = s.position_bytes * s.positions * s.segments;
+        if (beam > (int64_t{1} << 54) / batch) return SPEC_ERR_UNSUPPORTED;
         const char *src = static_cast<const char *>(s.src), *dst = static_cast<char *>(s.dst);
-        if (src == dst ? num_out != num_beams
-                       : src < dst + beam * num_out * batch && dst < src + beam * num_beams * batch)
+        const Span from{src, src + beam * num_beams * batch}, to{dst, dst + beam * num_out * batch};
+        if (src == dst ? num_out != num_beams : from.meets(to))
             return SPEC_ERR_ARG;  // in place means beam for beam
+        for (int j = 0; j < i; ++j) {  // what one state writes no other state holds
+            const spec_beam_state &o = states[j];
+            const int64_t other = o.position_bytes * o.positions * o.segments;
+            const char *osrc = static_cast<const char *>(o.src);
+            const char *odst = static_cast<char *>(o.dst);
+            const Span ofrom{osrc, osrc + other * num_beams * batch};
+            const Span oto{odst, odst + other * num_out * batch};
+            if (to.meets(oto) || to.meets(ofrom) || from.meets(oto)) return SPEC_ERR_ARG;
+        }
         in_place = in_place || src == dst;
         low_bits |= reinterpret_cast<uintptr_t>(src) | reinterpret_cast<uintptr_t>(dst) |
                     static_cast<uintptr_t>(s.position_bytes);
@@ -433,7 +458,7 @@ spec_status spec_beam_reorder(const int32_t *parents, const int32_t *lengths, in
     const int64_t chunk_bytes = static_cast<int64_t>(unit) * kReorderBlock;
     hipStream_t st = static_cast<hipStream_t>(stream);
     int64_t all = 0;
-    for (int i = 0; i < num_states; ++i)
+    for (int i = 0; i < num_states && all < (int64_t{1} << 40); ++i)
         all += (states[i].position_bytes * states[i].positions + chunk_bytes - 1) / chunk_bytes *
                states[i].segments * batch;
     if (!grid_fits(all, kReorderBlock)) return SPEC_ERR_UNSUPPORTED;

@@ -498,7 +498,8 @@ spec_status spec_distill_loss(const void *student, const int32_t *ids, const flo
  * spec_distill_loss call that filled state.  grad_loss: device float [rows]
  * or NULL (= 1).  grad: device, rows of vocab elements of the student's dtype
  * and row_stride; entries between vocab and row_stride become 0.  grad may be
- * student itself (same address): the gradient then replaces the logits. */
+ * student itself (same address): the gradient then replaces the logits; any
+ * other overlap is refused. */
 spec_status spec_distill_grad(const void *student, const int32_t *ids, const float *logits,
                               const void *state, const float *grad_loss,
                               const spec_distill_params *params, void *grad, void *stream);
@@ -532,7 +533,8 @@ spec_status spec_distill_step(const void *student, const int32_t *ids, const flo
  * (device int32), and ended_out (device uint8, nullable: 1 where the parent
  * had ended or the token is eos).  With fewer continuations the rest is filled
  * with -inf, -1, -1 and 0.  num_beams <= 32, num_out <= 64, num_beams *
- * num_out <= 512, else SPEC_ERR_UNSUPPORTED.  workspace: device,
+ * num_out <= 512, else SPEC_ERR_UNSUPPORTED.  Outputs share no memory with
+ * inputs.  workspace: device,
  * spec_beam_workspace_bytes, 16-byte aligned; its contents on entry do not
  * matter.
  */
@@ -554,7 +556,8 @@ spec_status spec_beam_select(const void *logits, int64_t row_stride, const float
  * NULL: all); later positions of dst, and the rows of a parent outside
  * [0, num_beams), are left as they are.  A state may be reordered in place
  * (dst == src, num_out == num_beams); buffers that overlap otherwise are
- * refused, and no two states of a call may share memory.  parents: device
+ * refused, also between the states of a call (two may share a src that none
+ * writes).  parents: device
  * int32 [B][num_out].  num_beams <= 32, num_out <= 64.  One launch moves up to
  * 32 states.
  */

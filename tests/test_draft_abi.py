@@ -71,6 +71,10 @@ def test_distill_validates_on_host(L):
     assert loss(state=P(8)) == -1
     assert grad(state=None) == -1 and grad(state=P(8)) == -1 and grad(out=P(8)) == -1
     assert step(g=None) == -1 and step(g=P(8)) == -1
+    # the gradient replaces the logits exactly or not at all (4 rows of 2048 bytes)
+    base = P(1 << 20)
+    for g in ((1 << 20) + 16, (1 << 20) - 16, (1 << 20) + 8176):
+        assert step(student=base, g=P(g)) == -1 and grad(student=base, out=P(g)) == -1
     assert L.spec_distill_state_bytes(7) == 7 * 48 and L.spec_distill_state_bytes(0) == 0
     assert L.spec_distill_state_bytes(-1) == 0
 
@@ -118,6 +122,14 @@ def test_beam_reorder_validates_on_host(L):
                dict(dst=(1 << 20) + 16),                   # other overlaps
                dict(src=(1 << 30) + 2 * 4 * 256 - 16)):
         assert call(**kw) == -1, kw
+    # two states: a dst twice, or one state's dst in the other's src
+    def two(a, b):
+        st = (sv._BeamState * 2)(*[sv._BeamState(s, d, 16, 2, 8) for s, d in (a, b)])
+        return L.spec_beam_reorder(P(16), None, 2, 4, 4, st, 2, None)
+    x, y, z = 1 << 20, 1 << 21, 1 << 22
+    for pair in (((x, x), (x, x)), ((x, y), (z, y)), ((x, y), (y, z)), ((y, z), (x, y)),
+                 ((x, y), (z, y + 2032)), ((x, x), (x + 16, z))):
+        assert two(*pair) == -1, pair
     for kw in (dict(W=33), dict(n=65), dict(position_bytes=1 << 31),
                dict(position_bytes=1 << 30, positions=1 << 30, segments=1 << 10),
                dict(B=1 << 30, dst=1 << 60)):
