@@ -46,27 +46,6 @@ struct BeamArgs {
     double near;  // scores of two beams closer than this are compared exactly
 };
 
-// 2^d in double, d <= 0: the Taylor series of e^(f ln 2) for the fraction f in
-// [-1/2, 1/2], cut where the next term is below 2^-52.
-__device__ __forceinline__ double exp2_f64(double d) {
-    const double n = __builtin_rint(d);
-    const double f = (d - n) * kLn2;
-    double p = 1.0 / 479001600.0;  // 1 / 12!
-    p = fma(p, f, 1.0 / 39916800.0);
-    p = fma(p, f, 1.0 / 3628800.0);
-    p = fma(p, f, 1.0 / 362880.0);
-    p = fma(p, f, 1.0 / 40320.0);
-    p = fma(p, f, 1.0 / 5040.0);
-    p = fma(p, f, 1.0 / 720.0);
-    p = fma(p, f, 1.0 / 120.0);
-    p = fma(p, f, 1.0 / 24.0);
-    p = fma(p, f, 1.0 / 6.0);
-    p = fma(p, f, 0.5);
-    p = fma(p, f, 1.0);
-    p = fma(p, f, 1.0);
-    return ldexp(p, static_cast<int>(n));
-}
-
 // ln sum e^((l - M)/T) of a row in double, M its largest visible logit.
 template <typename T, int BLOCK>
 __device__ __attribute__((noinline)) double exact_normaliser(const T *row, int V, float M,
@@ -94,7 +73,7 @@ __device__ __attribute__((noinline)) double exact_normaliser(const T *row, int V
     double t = 0.0;
 #pragma unroll
     for (int w = 0; w < BLOCK / kWave; ++w) t += sh[w];
-    return log(t);
+    return log_f64(t);
 }
 
 // One workgroup per sequence.  The segments' lists of a beam are joined first
@@ -144,11 +123,11 @@ __global__ __launch_bounds__(BLOCK) void beam_merge_kernel(BeamArgs a) {
             const float m = there ? key_value(sh_in[(q * segs + lane) * n]) : -__builtin_inff();
             const float M = wave_max_f32(m);
             const double e =
-                there ? exp((static_cast<double>(m) - static_cast<double>(M)) * a.inv_t +
+                there ? exp_f64((static_cast<double>(m) - static_cast<double>(M)) * a.inv_t +
                             a.seg_lse[(static_cast<int64_t>(b) * W + q) * segs + lane])
                       : 0.0;
             const double t = wave_sum_f64(e);
-            if (lane == 0) sh_lse[q] = log(t);
+            if (lane == 0) sh_lse[q] = log_f64(t);
         }
         int share = 1;
         while (share < kWave && W * per * share * 2 <= BLOCK) share *= 2;

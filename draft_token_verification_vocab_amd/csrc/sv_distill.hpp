@@ -162,7 +162,7 @@ __device__ __forceinline__ float listed_grad(int i, int k, const ListShared &l,
     if (l.dup)
         for (int j = i + 1; j < k; ++j)
             if (l.id[j] == l.id[i]) p += l.p[j];
-    return static_cast<float>((exp(log_q(r, l.s[i], inv_t)) * r.mass - p) * inv_t * g);
+    return static_cast<float>((exp_f64(log_q(r, l.s[i], inv_t)) * r.mass - p) * inv_t * g);
 }
 
 // One wave: the row's loss and gradient state from the list and the sum S of
@@ -197,18 +197,18 @@ __device__ __forceinline__ DistillRow settle_row(const DistillArgs &a, int64_t r
     double zs = 0.0, ts = 0.0;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        if (first[h]) zs += exp(log_q(r, s[h], it));
-        ts += exp((static_cast<double>(t[h]) - static_cast<double>(tm)) * it);
+        if (first[h]) zs += exp_f64(log_q(r, s[h], it));
+        ts += exp_f64((static_cast<double>(t[h]) - static_cast<double>(tm)) * it);
     }
     // log_q and log_p of the row so far are without their normalisers (0)
-    const double rest = outside ? log_q(r, M, it) + log(S) : -static_cast<double>(inf);
-    const double total = wave_sum_f64(zs) + (outside ? exp(rest) : 0.0);
-    r.lse = log(total);
-    r.norm = a.lse ? static_cast<double>(a.lse[row]) : log(wave_sum_f64(ts));
+    const double rest = outside ? log_q(r, M, it) + log_f64(S) : -static_cast<double>(inf);
+    const double total = wave_sum_f64(zs) + (outside ? exp_f64(rest) : 0.0);
+    r.lse = log_f64(total);
+    r.norm = a.lse ? static_cast<double>(a.lse[row]) : log_f64(wave_sum_f64(ts));
     double ps = 0.0, ls = 0.0;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const double lp = log_p(r, t[h], it), p = exp(lp);
+        const double lp = log_p(r, t[h], it), p = exp_f64(lp);
         if (lane + h * kWave < a.k) l.p[lane + h * kWave] = p;
         ps += p;
         if (p > 0.0) ls += p * (lp - log_q(r, s[h], it));
@@ -216,10 +216,10 @@ __device__ __forceinline__ DistillRow settle_row(const DistillArgs &a, int64_t r
     const double P = wave_sum_f64(ps);
     const double left = a.lse && outside ? fmax(0.0, 1.0 - P) : 0.0;
     double total_loss = wave_sum_f64(ls);
-    if (left > 0.0) total_loss += left * (log(left) - (rest - r.lse));
+    if (left > 0.0) total_loss += left * (log_f64(left) - (rest - r.lse));
     *loss = static_cast<float>(total_loss);
     r.mass = P + left;
-    r.coef = outside ? (r.mass * exp(rest - r.lse) - left) / S : 0.0;
+    r.coef = outside ? (r.mass * exp_f64(rest - r.lse) - left) / S : 0.0;
     return r;
 }
 
@@ -311,7 +311,8 @@ __device__ __forceinline__ void finish_row(const DistillArgs &a, int64_t row,
         for (int w = 0; w < NW; ++w) S += sh.s[w];
         float loss;
         const DistillRow r =
-            settle_row(a, row, lane, sh.list, M, OnlineSum::from_max(S, M, a.c), &loss);
+            settle_row(a, row, lane, sh.list, M,
+                       S * exp2_f64(-OnlineSum::above_max(M, a.c)), &loss);
         if (lane == 0) {
             sh.row = r;
             a.loss[row] = loss;
@@ -544,7 +545,7 @@ __global__ __launch_bounds__(BLOCK) void distill_grad_kernel(DistillArgs a, int3
         entry.put(a, list, tid);
         list.s[tid] = ListEntry::seen(entry.gather(rp));
         list.p[tid] = list.id[tid] >= 0
-                          ? exp(log_p(r, list.t[tid], a.inv_t))
+                          ? exp_f64(log_p(r, list.t[tid], a.inv_t))
                           : 0.0;
     }
     __syncthreads();

@@ -95,6 +95,40 @@ __device__ __forceinline__ void stream_vectors(const T *row, int vbeg, int vend,
     }
 }
 
+// Double-precision exponential and logarithm of the kernels' finishes.  They
+// stand on every row's way to its result, in one wave; with the library's, which
+// branch for every range, a listing of 2304 rows took 97.3 us instead of 96.2,
+// loss and gradient of 2048 rows 214 instead of 208.
+// 2^d: the Taylor series of e^(f ln 2) for the fraction f in [-1/2, 1/2], cut
+// where the next term is below 2^-52.
+__device__ __forceinline__ double exp2_f64(double d) {
+    d = d < -1100.0 ? -1100.0 : d;  // -inf too: 0
+    const double n = __builtin_rint(d);
+    const double f = (d - n) * kLn2;
+    double p = 1.0 / 479001600.0;  // 1 / 12!
+    p = fma(p, f, 1.0 / 39916800.0);
+    p = fma(p, f, 1.0 / 3628800.0);
+    p = fma(p, f, 1.0 / 362880.0);
+    p = fma(p, f, 1.0 / 40320.0);
+    p = fma(p, f, 1.0 / 5040.0);
+    p = fma(p, f, 1.0 / 720.0);
+    p = fma(p, f, 1.0 / 120.0);
+    p = fma(p, f, 1.0 / 24.0);
+    p = fma(p, f, 1.0 / 6.0);
+    p = fma(p, f, 0.5);
+    p = fma(p, f, 1.0);
+    p = fma(p, f, 1.0);
+    return ldexp(p, static_cast<int>(n));
+}
+__device__ __forceinline__ double exp_f64(double x) { return exp2_f64(x * kLog2eD); }
+// ln x of a normal float's size: the hardware's log2 L, off by some 1e-6, and
+// the rest of ln x = L ln 2 + ln(x 2^-L) as a two-term series.
+__device__ __forceinline__ double log_f64(double x) {
+    const double L = static_cast<double>(hw_log2(static_cast<float>(x)));
+    const double d = fma(x, exp2_f64(-L), -1.0);
+    return fma(L, kLn2, d - 0.5 * d * d);
+}
+
 // One thread's running maximum m and sum of 2^(x*c - n) over the chunks it is
 // given (an online softmax in base 2).  The reference n is m*c rounded up to
 // an integer: a term's exponent is then one fused product, rounded once, and a
@@ -154,11 +188,12 @@ struct OnlineSum {
         if (m == M) return s;
         return slope != c ? 0.f : ldexpf(s, static_cast<int>(n - reference(M, c)));
     }
-    // From r, the sum of the threads' at(M): the sum of 2^((x - M)*c).
-    __device__ __forceinline__ static double from_max(double r, float M, float c) {
-        if (fabsf(mul_rn(M, c)) >= kFar) return r;
-        return r * exp2(static_cast<double>(reference(M, c)) -
-                        static_cast<double>(M) * static_cast<double>(c));
+    // The sum of the threads' at(M) is 2^above_max times the sum of
+    // 2^((x - M)*c).
+    __device__ __forceinline__ static double above_max(float M, float c) {
+        if (fabsf(mul_rn(M, c)) >= kFar) return 0.0;
+        return static_cast<double>(M) * static_cast<double>(c) -
+               static_cast<double>(reference(M, c));
     }
 };
 

@@ -346,7 +346,8 @@ __global__ __launch_bounds__(BLOCK) void topk_rows_kernel(TopkArgs a) {
         double r = 0.0;
 #pragma unroll
         for (int w = 0; w < NW; ++w) r += sh_s[w];
-        const double l = bm > masked ? log(OnlineSum::from_max(r, M, c)) : -__builtin_inf();
+        const double l = bm > masked ? log_f64(r) - OnlineSum::above_max(M, c) * kLn2
+                                     : -__builtin_inf();
         if (a.list)
             a.seg_lse[blockIdx.x] = l;
         else
