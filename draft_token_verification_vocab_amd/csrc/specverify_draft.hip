@@ -168,7 +168,7 @@ void launch_step_t(const DistillArgs &a, int64_t rows, hipStream_t st) {
 }
 
 // Beam selection.
-constexpr int kBeamMergeBlock = 512;
+constexpr int kBeamMergeBlock = 1024;
 
 // How a beam selection's rows are cut into workgroups, and its workspace.  A
 // row's listing keeps a compute unit's vector units busy (256 KB take 10 us
@@ -181,16 +181,15 @@ constexpr int kSplitVecs = 12288;    // 16-byte vectors of the shortest that are
 constexpr int kSplitBlocks = 1024;   // workgroups to aim for
 constexpr int kMaxSegs = 64;         // one lane per segment in the merge
 struct BeamPlan {
-    int segs, seg_vecs, chunk_vecs;
+    int segs, seg_vecs;
     size_t list, seg_lse, total;  // workspace offsets
 };
 
 template <typename T>
 BeamPlan plan_beam_t(int64_t rows, int32_t V, int32_t beams, int32_t n) {
-    using S = LongShape<T>;
-    constexpr int split_chunk = kShortBlock * S::unroll;
+    constexpr int split_chunk = kShortBlock * LongShape<T>::unroll;
     const int nvec = row_vecs<T>(V);
-    BeamPlan p{1, nvec, (nvec > kShortVecs ? S::block : kShortBlock) * S::unroll, 0, 0, 0};
+    BeamPlan p{1, nvec, 0, 0, 0};
     if (rows <= kSplitRows && nvec >= kSplitVecs) {
         int64_t want = (kSplitBlocks + rows - 1) / rows;
         const int by_len = (nvec + split_chunk - 1) / split_chunk;
@@ -200,7 +199,6 @@ BeamPlan plan_beam_t(int64_t rows, int32_t V, int32_t beams, int32_t n) {
         if (want > kMaxSegs) want = kMaxSegs;
         if (want > 1) {
             const int chunks = (by_len + static_cast<int>(want) - 1) / static_cast<int>(want);
-            p.chunk_vecs = split_chunk;
             p.seg_vecs = chunks * split_chunk;
             p.segs = (nvec + p.seg_vecs - 1) / p.seg_vecs;
         }
@@ -219,16 +217,14 @@ BeamPlan plan_beam(int64_t rows, int32_t V, int32_t dtype, int32_t beams, int32_
 // Bound on how far the listing's float sums can move the difference of two
 // beams' log-normalisers.  A term's exponent d = l log2(e)/T - n is off by half
 // a step (2^-24 of |d|) and by the constant's own error; the terms' mean |d|
-// is at most log2 V + 1.  exp2 is off by one step, and every addition that a
-// term goes through by half a step: 5 in its chunk, one per chunk of its
-// thread, 6 across the wave.
-double near_bound(const BeamPlan &p, int32_t V, float temperature) {
+// is at most log2 V + 1.  exp2 is off by one step, and the five float additions
+// that a term goes through in its chunk by half a step each; beyond the chunk
+// the sums are double.
+double near_bound(int32_t V, float temperature) {
     const double h = 0x1p-24;
     const double exact = kLog2eD / static_cast<double>(temperature);
     const double constant = std::fabs(static_cast<double>(log2e_over(temperature)) / exact - 1.0);
-    const double adds = 11 + (p.seg_vecs + p.chunk_vecs - 1) / p.chunk_vecs;
-    const double one = kLn2 * (std::log2(static_cast<double>(V)) + 1.0) * (h + constant) + 2 * h +
-                       adds * h;
+    const double one = kLn2 * (std::log2(static_cast<double>(V)) + 1.0) * (h + constant) + 7 * h;
     return 2.0 * one * 1.0001;  // the products of the errors
 }
 
@@ -407,7 +403,7 @@ spec_status spec_beam_select(const void *logits, int64_t row_stride, const float
     a.segs = p.segs;
     a.eos = eos;
     a.inv_t = t.inv_t;
-    a.near = near_bound(p, vocab, temperature);
+    a.near = near_bound(vocab, temperature);
     if (dtype == SPEC_DTYPE_BF16)
         beam_merge_kernel<uint16_t, kBeamMergeBlock>
             <<<dim3(batch), dim3(kBeamMergeBlock), 0, st>>>(a);

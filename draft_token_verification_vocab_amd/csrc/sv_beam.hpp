@@ -83,8 +83,8 @@ __device__ __attribute__((noinline)) double exact_normaliser(const T *row, int V
 // 128 of eight with 16 out (counting every continuation against all others took
 // 7.6 there and 19 with eight segments a row: comparisons of doubles are slow).
 // Two beams that nearly tie are read again, 32 us for each row of 152064 in
-// double; of calls with 128 sequences of eight beams 8 % have such a pair, with
-// 64 of four 1 %.
+// double: 9 of 200 inputs of 128 sequences with eight beams had such a pair, 1 of
+// 200 of 64 with four.
 template <typename T, int BLOCK>
 __global__ __launch_bounds__(BLOCK) void beam_merge_kernel(BeamArgs a) {
     static_assert(BLOCK >= kMaxBeamKeys, "a thread per key");

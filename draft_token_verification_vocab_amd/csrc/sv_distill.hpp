@@ -302,8 +302,8 @@ __device__ __forceinline__ void finish_row(const DistillArgs &a, int64_t row,
 #pragma unroll
     for (int w = 1; w < NW; ++w) bm = sh.wm[w] > bm ? sh.wm[w] : bm;
     const float M = from_ordered_bits(bm);
-    const float ws = wave_sum_f32(acc.at(M, a.c));
-    if (lane == 0) sh.s[wv] = static_cast<double>(ws);
+    const double ws = wave_sum_f64(acc.at(M, a.c));
+    if (lane == 0) sh.s[wv] = ws;
     __syncthreads();
     if (wv == 0) {
         double S = 0.0;

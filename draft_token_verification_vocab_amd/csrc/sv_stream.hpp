@@ -132,8 +132,10 @@ __device__ __forceinline__ double log_f64(double x) {
 // One thread's running maximum m and sum of 2^(x*c - n) over the chunks it is
 // given (an online softmax in base 2).  The reference n is m*c rounded up to
 // an integer: a term's exponent is then one fused product, rounded once, and a
-// rescaling to another reference is an exact power of two.  Sums within a
-// thread are float: a few tens of chunk sums of one sign.
+// rescaling to another reference is an exact power of two.  A chunk's terms are
+// added in float, the chunks in double: that costs nothing measurable (97.1 us
+// and 97.5 for 2304 rows) and halves the error that beam selection has to allow
+// for.
 //
 // Beyond |m*c| = 2^30 neighbouring floats differ by 128 or more in the
 // exponent, so only logits equal to the maximum count; there the rounding of
@@ -142,7 +144,8 @@ __device__ __forceinline__ double log_f64(double x) {
 struct OnlineSum {
     float m = kMasked;
     float n = -kMasked;  // until a visible logit comes every term is 2^-huge = 0
-    float slope, s = 0.f;
+    float slope;
+    double s = 0.0;
     static constexpr float kFar = 0x1p30f;
     __device__ __forceinline__ explicit OnlineSum(float c) : slope(c) {}
 
@@ -152,14 +155,14 @@ struct OnlineSum {
         if (cm > m) {
             const float mc = mul_rn(cm, c);
             float to = ceilf(mc), k = c;
-            if (slope != c) s = 0.f;
+            if (slope != c) s = 0.0;
             if (fabsf(mc) >= kFar) {
                 // 2^(31 - exponent of cm)
                 k = __uint_as_float((285u - (__float_as_uint(cm) >> 23 & 255u)) << 23);
                 to = cm * k;
-                s = 0.f;
+                s = 0.0;
             }
-            s = ldexpf(s, static_cast<int>(n - to));
+            s = ldexp(s, static_cast<int>(n - to));
             m = cm;
             n = to;
             slope = k;
@@ -177,16 +180,16 @@ struct OnlineSum {
             for (int k = 0; k < N; ++k)
                 cs += x[k] > kMasked ? hw_exp2(fmaf(x[k], slope, -n)) : 0.f;
         }
-        s += cs;
+        s += static_cast<double>(cs);
     }
     // The reference that a maximum M has.
     __device__ __forceinline__ static float reference(float M, float c) {
         return ceilf(mul_rn(M, c));
     }
     // The thread's sum relative to the reference of a maximum M >= m.
-    __device__ __forceinline__ float at(float M, float c) const {
+    __device__ __forceinline__ double at(float M, float c) const {
         if (m == M) return s;
-        return slope != c ? 0.f : ldexpf(s, static_cast<int>(n - reference(M, c)));
+        return slope != c ? 0.0 : ldexp(s, static_cast<int>(n - reference(M, c)));
     }
     // The sum of the threads' at(M) is 2^above_max times the sum of
     // 2^((x - M)*c).

@@ -202,8 +202,8 @@ __global__ __launch_bounds__(BLOCK) void topk_rows_kernel(TopkArgs a) {
     for (int w = 1; w < NW; ++w) bm = sh_wm[w] > bm ? sh_wm[w] : bm;
     const float M = from_ordered_bits(bm);
     if (LSE) {
-        const float ws = wave_sum_f32(acc.at(M, c));
-        if (lane == 0) sh_s[wv] = static_cast<double>(ws);
+        const double ws = wave_sum_f64(acc.at(M, c));
+        if (lane == 0) sh_s[wv] = ws;
     }
 
     // tau: a value that at least k threads' maxima reach (all visible logits

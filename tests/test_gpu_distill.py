@@ -18,10 +18,10 @@ H = 2.0 ** -24  # half a float32 step, relative
 def sum_error(V):
     """Relative error of the sum over the unlisted entries: every exponent d is
     off by three half steps of |d| (log2(e), its division by T, the fused
-    product) and the terms' mean |d| is at most log2 V + 1; exp2 by one step; half
-    a step per addition a term goes through (4 chains, the thread's chunks, 6
-    wave steps)."""
-    return math.log(2) * 3 * H * (math.log2(max(V, 2)) + 1) + 2 * H + (16 + V / 4096) * H
+    product) and the terms' mean |d| is at most log2 V + 1; exp2 by one step; the
+    five additions within a chunk by half a step each (beyond it the sums are
+    double)."""
+    return math.log(2) * 3 * H * (math.log2(max(V, 2)) + 1) + 7 * H
 
 
 def bounds(x, ids, logits, lse, T, keep, grad_loss, loss, grad, dtype):

@@ -18,10 +18,10 @@ def lse_tolerance(V, lse):
     """The float32 row pass: each term's exponent d = l log2(e)/T - n is off by
     three half steps of |d| (the constant log2(e), its division by T, the fused
     product), and the terms' mean |d| is at most log2 V + 1; exp2 by one step,
-    sums by half a step per addition a term goes through (4 chains, the
-    thread's chunks, 6 wave steps), the result by half a step."""
+    the five additions within a chunk by half a step each (beyond it the sums
+    are double), the result by half a step."""
     h = 2.0 ** -24
-    return (math.log(2) * 3 * h * (math.log2(max(V, 2)) + 1) + 2 * h + (16 + V / 4096) * h +
+    return (math.log(2) * 3 * h * (math.log2(max(V, 2)) + 1) + 7 * h +
             abs(lse) * h)
 
 
