@@ -12,8 +12,8 @@
 // largest logit: k threads hold a logit that large.  The logits at or above
 // tau lie in about k best chunks, the few second chunks that reach tau (read
 // again), and all chunks of the very few threads with a third one; they are
-// collected and placed by counting.  A row whose collection overflows (many equal logits) is settled by a radix
-// selection over the keys instead, which reads the row once per key byte.
+// collected and placed by counting.  A row whose collection overflows (many
+// equal logits) is settled by further passes (collect_ties).
 //
 // Bound: vector issue and memory alike (8.7 instructions per logit, one of them
 // the quarter-rate exp2: 77 % busy).  2304 rows of 128256 bfloat16 logits, k = 64:
@@ -87,48 +87,122 @@ __device__ void sort_keys(unsigned long long *key, int n2, int tid) {
     __syncthreads();
 }
 
-// The exact k-th largest key of a segment's visible logits (0 when there are
-// at most k) by radix selection, eight key bits a pass over the segment.
+// Collects exactly the segment's k first keys where more logits than can be
+// collected reach the bound `lo` (at least k do; `hi` is the maximum; both as
+// ordered bits): equal values, mostly.  Passes over the segment narrow [lo, hi]
+// to the k-th largest value, 256 bins at a time (none when it is the maximum
+// itself, as in a constant or clamped row); a last pass takes the values above
+// it, and of those equal to it the first ids, counted tile by tile in id order.
+// 2304 rows of 128256 bfloat16 logits, short bursts: 138 us when all are
+// constant, 155 when clamped, 92 to 100 when none is (3700 with a radix
+// selection over whole keys instead).
 template <typename T, int BLOCK>
-__device__ __attribute__((noinline)) uint64_t radix_kth(const T *row, int ebeg, int eend, int k,
-                                                        unsigned int *hist, int tid) {
-    __shared__ uint64_t sh_prefix;
-    __shared__ int sh_left;
-    uint64_t prefix = 0, mask = 0;
-    int left = k;
-    for (int shift = 56; shift >= 0; shift -= 8) {
+__device__ __attribute__((noinline)) int collect_ties(const T *row, int vbeg, int vend, int V,
+                                                      int k, uint32_t lo, uint32_t hi,
+                                                      unsigned long long *keys, int *hist,
+                                                      int tid) {
+    using E = Elem<T>;
+    constexpr int EPV = E::kPerVec;
+    constexpr int NW = BLOCK / kWave;
+    __shared__ uint32_t sh_lo, sh_hi;
+    __shared__ int sh_above, sh_n, sh_wave[NW];
+    const int lane = tid & (kWave - 1), wv = tid / kWave;
+    auto load = [&](int vi, uint32_t (&key)[EPV]) {  // ordered bits, 0 past the end
+        float x[EPV];
+        E::unpack(vi < vend ? ((vi + 1) * EPV <= V ? reinterpret_cast<const uint4 *>(row)[vi]
+                                                   : E::partial(row, vi, V))
+                            : make_uint4(E::pad_word(), E::pad_word(), E::pad_word(),
+                                         E::pad_word()),
+                  x);
+#pragma unroll
+        for (int e = 0; e < EPV; ++e) key[e] = x[e] > kMasked ? ordered_bits(x[e] + 0.0f) : 0u;
+    };
+    int above = 0;  // logits above hi
+    while (lo < hi) {
+        const int width = 32 - __clz(static_cast<int>(hi - lo));
+        const int shift = width > 8 ? width - 8 : 0;
         for (int i = tid; i < 256; i += BLOCK) hist[i] = 0;
         __syncthreads();
-        for (int i = ebeg + tid; i < eend; i += BLOCK) {
-            const float x = Elem<T>::at(row, i);
-            const uint64_t key = topk_key(x, i);
-            if (x > kMasked && (key & mask) == prefix) {
-                const int bin = static_cast<int>((key >> shift) & 255u);
+        for (int vi = vbeg + tid; vi < vend; vi += BLOCK) {
+            uint32_t key[EPV];
+            load(vi, key);
+#pragma unroll
+            for (int e = 0; e < EPV; ++e) {
+                if (key[e] < lo || key[e] > hi) continue;
                 // lanes that share the first lane's bin count once together
+                const int bin = static_cast<int>((key[e] - lo) >> shift);
                 const int lead = __builtin_amdgcn_readfirstlane(bin);
                 const uint64_t same = __ballot(bin == lead);
                 if (bin != lead)
-                    atomicAdd(&hist[bin], 1u);
-                else if ((threadIdx.x & (kWave - 1)) ==
-                         static_cast<unsigned>(__ffsll(static_cast<long long>(same)) - 1))
-                    atomicAdd(&hist[lead], static_cast<unsigned>(__popcll(same)));
+                    atomicAdd(&hist[bin], 1);
+                else if (lane == __ffsll(static_cast<long long>(same)) - 1)
+                    atomicAdd(&hist[lead], __popcll(same));
             }
         }
         __syncthreads();
         if (tid == 0) {
-            int bin = 255, n = left;
-            while (bin >= 0 && static_cast<int>(hist[bin]) < n) n -= static_cast<int>(hist[bin--]);
-            sh_left = bin < 0 ? 0 : n;
-            sh_prefix = bin < 0 ? 0 : prefix | (static_cast<uint64_t>(bin) << shift);
+            int bin = static_cast<int>((hi - lo) >> shift), n = above;
+            while (bin > 0 && n + hist[bin] < k) n += hist[bin--];
+            const uint32_t from = lo + (static_cast<uint32_t>(bin) << shift);
+            const uint32_t to = from + ((1u << shift) - 1u);
+            sh_above = n;
+            sh_lo = from;
+            sh_hi = to < hi ? to : hi;
         }
         __syncthreads();
-        left = sh_left;
-        prefix = sh_prefix;
-        mask |= 0xFFull << shift;
+        above = sh_above;
+        lo = sh_lo;
+        hi = sh_hi;
         __syncthreads();  // read before the next pass writes them
-        if (left == 0) return 0;  // fewer than k: every visible logit is listed
     }
-    return prefix;
+    // keys above lo, and the first `left` equal to it
+    int left = k - above;
+    if (tid == 0) sh_n = 0;
+    __syncthreads();
+    for (int tile = vbeg; tile < vend; tile += BLOCK) {
+        const int vi = tile + tid;
+        uint32_t key[EPV];
+        load(vi, key);
+        int equal = 0;
+#pragma unroll
+        for (int e = 0; e < EPV; ++e) {
+            equal += key[e] == lo;
+            if (key[e] > lo)
+                keys[atomicAdd(&sh_n, 1)] = (static_cast<uint64_t>(key[e]) << 32) |
+                                            static_cast<uint32_t>(~(vi * EPV + e));
+        }
+        if (left <= 0) {  // the same for every thread
+            if (above == 0) break;
+            continue;
+        }
+        int upto = equal;         // within the wave, this lane included
+#pragma unroll
+        for (int o = 1; o < kWave; o *= 2) {
+            const int below = __shfl_up(upto, o, kWave);
+            if (lane >= o) upto += below;
+        }
+        if (lane == kWave - 1) sh_wave[wv] = upto;
+        __syncthreads();
+        int before = upto - equal, total = 0;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            before += w < wv ? sh_wave[w] : 0;
+            total += sh_wave[w];
+        }
+        if (equal != 0 && before < left) {
+#pragma unroll
+            for (int e = 0; e < EPV; ++e) {
+                if (key[e] != lo || before >= left) continue;
+                ++before;
+                keys[atomicAdd(&sh_n, 1)] = (static_cast<uint64_t>(key[e]) << 32) |
+                                            static_cast<uint32_t>(~(vi * EPV + e));
+            }
+        }
+        left -= total;
+        __syncthreads();  // sh_wave is free
+    }
+    __syncthreads();
+    return sh_n;
 }
 
 // LSE: with the log-normaliser (else a third of the arithmetic is left out).
@@ -291,25 +365,8 @@ __global__ __launch_bounds__(BLOCK) void topk_rows_kernel(TopkArgs a) {
         __syncthreads();
     }
     int n = items <= kTopkChunks ? sh_n : kTopkCollect + 1;
-    if (n > kTopkCollect) {
-        // Too many logits reach tau: the k-th key itself, then exactly the
-        // keys at or above it.
-        const int ebeg = vbeg * EPV, eend = vend * EPV < V ? vend * EPV : V;
-        const uint64_t kth = radix_kth<T, BLOCK>(rp, ebeg, eend, k,
-                                                 reinterpret_cast<unsigned int *>(sh_key), tid);
-        if (tid == 0) sh_n = 0;
-        __syncthreads();
-        for (int i = ebeg + tid; i < eend; i += BLOCK) {
-            const float x = E::at(rp, i);
-            const uint64_t key = topk_key(x, i);
-            if (x > kMasked && key >= kth) {
-                const int o = atomicAdd(&sh_n, 1);
-                if (o < kTopkCollect) sh_key[o] = key;
-            }
-        }
-        __syncthreads();
-        n = sh_n;
-    }
+    if (n > kTopkCollect)  // too many logits reach tau
+        n = collect_ties<T, BLOCK>(rp, vbeg, vend, V, k, tau, bm, sh_key, sh_item, tid);
 
     // Places: up to kRankKeys keys are counted against all others, a thread
     // each; more are sorted first.

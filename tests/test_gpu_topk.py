@@ -101,6 +101,24 @@ def test_equal_values_are_listed_by_lowest_id(rows, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [70001, 9000])
+def test_rows_that_collect_too_many(V, dtype):
+    rng = np.random.default_rng(V)
+    x = (4.0 * rng.standard_normal((8, V))).astype(np.float32)
+    x[0] = np.minimum(x[0], 6.0)                     # clamped: thousands at the maximum
+    x[1] = -np.sort(-x[1])                           # decreasing
+    x[2] = np.sort(x[2])                             # increasing
+    x[3] = np.round(x[3])                            # a few dozen values
+    x[4] = np.where(rng.random(V) < 0.3, 2.0, -1e9)  # one value and a far one
+    x[4, 77] = 3.0
+    x[5] = np.where(np.arange(V) >= V - 1500, 1.0, -np.inf)   # equal, at the end
+    x[6] = 5.0 + rng.integers(0, 3, V) * 2.0 ** -5
+    x[7] = np.float32(1.0) + rng.integers(0, 40, V).astype(np.float32) * np.float32(2.0 ** -23)
+    for k in (1, 13, 128):
+        check(x, k, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("rows", [3, 256])
 def test_masked_entries_are_never_listed(rows, dtype):
     rng = np.random.default_rng(rows + 1)
