@@ -32,7 +32,11 @@ bool grid_fits(int64_t blocks, int block) {
 // long rows' shape, top 16 (loss): 4000 bfloat16 logits 14 (14) against 39
 // (30), 32000 31 (32) against 46 (42), 50264 44 (46) against 51 (51), 128256
 // 101 (104) against 99 (100); 32000 float32 51 (52) against 56 (64), 50264 81
-// (84) against 79 (81).  Beam rows that are cut into segments take 256 too.
+// (84) against 79 (81).  With at most a row per compute unit there is nothing to
+// share it with, and rows above 32 KB take the long shape: 32 rows of 50264
+// bfloat16 logits 9.1 (8.1) against 10.3 (10.6) at 256 threads, of 32000 float32
+// 8.3 (8.0) against 9.2 (9.9); of 4000 bfloat16 6.1 (5.6) at 256 against 7.6
+// (5.7).  Beam rows that are cut into segments take 256 too.
 template <typename T>
 struct LongShape;
 template <>
@@ -44,7 +48,7 @@ struct LongShape<float> {
     static constexpr int block = 512, unroll = 4;
 };
 constexpr int kShortBlock = 256;
-constexpr int kShortVecs = 8192;  // 16-byte vectors
+constexpr int kUnits = 256;  // compute units
 
 template <typename T>
 int row_vecs(int32_t V) {
@@ -52,11 +56,16 @@ int row_vecs(int32_t V) {
     return (V + per - 1) / per;
 }
 
+template <typename T>
+bool long_shape(int64_t rows, int32_t V) {
+    return row_vecs<T>(V) > (rows <= kUnits ? 2048 : 8192);
+}
+
 template <typename T, bool LSE>
 void launch_topk_t(const TopkArgs &a, int64_t rows, hipStream_t st) {
     using S = LongShape<T>;
     const dim3 grid(static_cast<unsigned>(rows * a.segs));
-    if (a.segs == 1 && row_vecs<T>(a.V) > kShortVecs)
+    if (a.segs == 1 && long_shape<T>(rows, a.V))
         topk_rows_kernel<T, S::block, S::unroll, LSE><<<grid, dim3(S::block), 0, st>>>(a);
     else
         topk_rows_kernel<T, kShortBlock, S::unroll, LSE><<<grid, dim3(kShortBlock), 0, st>>>(a);
@@ -141,7 +150,7 @@ void launch_loss_t(const DistillArgs &a, int64_t rows, hipStream_t st) {
     using S = LongShape<T>;
     const dim3 grid(static_cast<unsigned>(rows));
     const bool again = a.state && rows * a.V * static_cast<int64_t>(sizeof(T)) <= kCacheBytes;
-    if (row_vecs<T>(a.V) > kShortVecs) {
+    if (long_shape<T>(rows, a.V)) {
         if (again)
             distill_rows_kernel<T, S::block, S::unroll, true>
                 <<<grid, dim3(S::block), map_bytes(a), st>>>(a);
@@ -158,10 +167,16 @@ void launch_loss_t(const DistillArgs &a, int64_t rows, hipStream_t st) {
     }
 }
 
+// With at most a row per compute unit, 1024 threads share the one row (us against
+// the shapes below: one row of 32000 bfloat16 logits 9.1 to 12.2, 250 rows of
+// 128256 29.4 to 31.2, 32 rows of 32000 float32 10.3 to 11.9).
 template <typename T>
 void launch_step_t(const DistillArgs &a, int64_t rows, hipStream_t st) {
     const dim3 grid(static_cast<unsigned>(rows));
-    if (row_vecs<T>(a.V) <= 4096)
+    const int nvec = row_vecs<T>(a.V);
+    if (rows <= kUnits && nvec > 2048)
+        distill_held_kernel<T, 1024, 8><<<grid, dim3(1024), map_bytes(a), st>>>(a);
+    else if (nvec <= 4096)
         distill_held_kernel<T, 256, 8><<<grid, dim3(256), map_bytes(a), st>>>(a);
     else
         distill_held_kernel<T, 512, sizeof(T) == 2 ? 12 : 8><<<grid, dim3(512), map_bytes(a), st>>>(a);
