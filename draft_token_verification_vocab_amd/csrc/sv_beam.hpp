@@ -51,8 +51,8 @@ struct BeamArgs {
 // 32 doubles, one per pair of LDS banks, times the Taylor series of 2^(f/32) cut
 // where the next term is below 2^-52.  Masked logits count 2^-1000 beside the
 // maximum's 1.  Bound by issue of double-precision instructions: 25 us for 152064
-bfloat16 logits, 27 in float32 (31 and 33 with the series of twelve terms that
-needs no table; the next vector's load ahead of the sums gained nothing).
+// bfloat16 logits, 27 in float32 (31 and 33 with the series of twelve terms that
+// needs no table; the next vector's load ahead of the sums gained nothing).
 template <typename T, int BLOCK>
 __device__ __attribute__((noinline)) double exact_normaliser(const T *row, int V, float M,
                                                             double inv_t, double *sh, int tid) {
