@@ -140,6 +140,17 @@ def test_loss_and_gradient(R, V, k, T, dtype, rest):
     check(x, ids, logits, lse if rest else None, dtype=dtype, T=T, grad_loss=g)
 
 
+# More rows than compute units take other workgroups than few rows of the same length.
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("R,V,k", [(260, 5003, 8), (258, 34001, 20), (257, 70001, 64)])
+def test_more_rows_than_compute_units(R, V, k, dtype):
+    x, ids, logits, lse, rng = batch(R, V, k, R + V, 1.3)
+    keep = (rng.random(R) < 0.9).astype(np.uint8)
+    x[3] = -np.inf
+    check(x, ids, logits, lse, dtype=dtype, T=1.3, grad_loss=rng.random(R).astype(np.float32),
+          keep=keep)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_padded_rows_and_strides(dtype):
     x, ids, logits, lse, rng = batch(9, 3001, 16, 3)
