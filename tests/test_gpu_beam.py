@@ -273,3 +273,25 @@ def test_reorder_large_state_in_place():
     for w, v in enumerate((4, 1, 1, 3)):
         assert s[0, w, 1, -1].item() == v + 10
         assert s[0, w, 0].min().item() == v and s[0, w, 1, :-1].max().item() == v
+
+
+@pytest.mark.parametrize("V,T", [(5003, 0.7), (98317, 1.0), (200003, 1.6)])
+def test_near_ties_of_rows_with_masked_logits(V, T):
+    """As above, a third of each row masked in three ways: what the exact sums
+    count for masked logits has to stay below any gap."""
+    W = 3
+    rng = np.random.default_rng(V + 1)
+    base = rng.standard_normal(V).astype(np.float32)
+    base[: V // 3] = np.resize(np.float32([-np.inf, np.nan, -2e30]), V // 3)
+    base[-1] = 6.0
+    total = np.exp(base[V // 3:].astype(np.float64) / T).sum()
+    x = np.empty((1, W, V), np.float32)
+    for w in range(W):
+        row = base.copy()
+        i = int(rng.integers(V // 3, V - 1))
+        row[i] = T * np.log(np.exp(np.float64(row[i]) / T) + 1e-7 * (w + 1) * total)
+        x[0, w] = row[rng.permutation(V)]
+    for order in ([0, 1, 2], [2, 0, 1]):
+        r = select(np.ascontiguousarray(x[:, order]), np.full((1, W), -3.0, np.float32), 5, T=T)
+        # the lightest row's maximum comes first
+        assert list(r["parents"][0, :W]) == list(np.argsort(order))
