@@ -776,7 +776,9 @@ def row_topk(logits: torch.Tensor, k: int, *, temperature: float = 1.0,
     """The k largest logits of each row of a [..., S] tensor (first V columns)
     in decreasing order, equal values by lowest id: values (float32 [..., k]),
     ids (int32 [..., k]; -inf and -1 past a row's visible entries) and lse
-    (float32 [...], ln sum e^(l/T) over the whole row; lse=False leaves it out)."""
+    (float32 [...], ln sum e^(l/T) over the whole row; lse=False leaves it out).
+    The list holds at any temperature, its lse at this one only: distil at the
+    temperature that the lse was taken at."""
     _need_cuda(logits, "logits")
     S = logits.shape[-1]
     V = S if vocab is None else int(vocab)
@@ -817,7 +819,8 @@ def distill_loss(student: torch.Tensor, ids: torch.Tensor, logits: torch.Tensor,
     """Distillation loss of each row of student [..., S] (first V columns) from
     a teacher's listed logits (ids int32 and logits float32 [..., k], as
     row_topk gives them).  lse (float32 [...]): the teacher's log-normaliser
-    at the same temperature, for a bucket over the unlisted ids; None: the list
+    at the same temperature (another one's trains towards wrong masses, and
+    nothing can tell), for a bucket over the unlisted ids; None: the list
     is a distribution of its own.  keep (uint8 [...]): rows to train on.
     Returns (loss [...], state): the state is what distill_grad takes
     (state=False: None)."""

@@ -439,8 +439,9 @@ spec_status spec_row_stats(const void *logits, int64_t rows, int32_t vocab, int6
  * equal values by lowest id.  values (device float [rows][k]) and ids (device
  * int32 [rows][k]) are required; a row with fewer than k visible entries is
  * filled up with (-inf, -1).  lse (device float [rows], nullable): ln sum
- * e^(l/T) over the whole row, -inf when it is masked throughout.  One pass over the
- * rows, no workspace.  1 <= k <= 128.
+ * e^(l/T) over the whole row, -inf when it is masked throughout; it is the
+ * normaliser at this T only.  One pass over the rows, no workspace.
+ * 1 <= k <= 128.
  */
 spec_status spec_row_topk(const void *logits, int64_t rows, int32_t vocab, int64_t row_stride,
                           int32_t dtype, float temperature, int32_t k, float *values,
