@@ -274,6 +274,47 @@ void launch_reorder(const ReorderArgs &a, int group, uint32_t blocks, hipStream_
         beam_reorder_kernel<BYTES, 32, kReorderBlock><<<grid, block, 0, st>>>(a);
 }
 
+// Bytes that a thread takes of each beam: the widest access that the bits of
+// the addresses and of the positions' sizes allow.
+int reorder_unit(uint64_t bits) { return bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 1; }
+
+uint64_t reorder_bits(const spec_beam_state &s) {
+    return reinterpret_cast<uintptr_t>(s.src) | reinterpret_cast<uintptr_t>(s.dst) |
+           static_cast<uint64_t>(s.position_bytes);
+}
+
+// Workgroups per segment of a state, and for the state.
+int64_t reorder_chunks(const spec_beam_state &s, int unit) {
+    const int64_t chunk = static_cast<int64_t>(unit) * kReorderBlock;
+    return (s.position_bytes * s.positions + chunk - 1) / chunk;
+}
+int64_t reorder_blocks(const spec_beam_state &s, int unit, int32_t batch) {
+    return reorder_chunks(s, unit) * s.segments * batch;
+}
+
+void launch_reorder(const ReorderArgs &a, int unit, int group, int64_t blocks, hipStream_t st) {
+    if (unit == 16)
+        launch_reorder<16>(a, group, static_cast<uint32_t>(blocks), st);
+    else if (unit == 4)
+        launch_reorder<4>(a, group, static_cast<uint32_t>(blocks), st);
+    else
+        launch_reorder<1>(a, group, static_cast<uint32_t>(blocks), st);
+}
+
+// States of different units go in a launch per unit, so that an odd one among
+// them leaves the others' accesses wide, or all in one launch in the unit that
+// they share.  Each further launch costs the host 2.8 us, so little work stays
+// together (us, four beams, 16-byte caches and a history in 4-byte units, 4096
+// workgroups in the shared unit: 17.5 apart, 14.7 together; 16384: 24 and 38;
+// 65536: 81 and 140; with flags in single bytes 262144: 84 and 490).  With more
+// than 12 beams 4-byte units keep as many bytes in flight as memory takes (65536
+// workgroups, in place: 12 beams 229 and 243, 14 beams 282 and 265, 32 beams
+// 648 and 598).
+constexpr int64_t kOneUnitWork = 49152;  // workgroups times beams
+bool reorder_together(int64_t blocks, int common, int32_t beams) {
+    return blocks * beams <= kOneUnitWork || (common == 4 && beams > 12);
+}
+
 }  // namespace
 
 extern "C" {
@@ -436,7 +477,7 @@ spec_status spec_beam_reorder(const int32_t *parents, const int32_t *lengths, in
     if (batch == 0 || num_states == 0) return SPEC_OK;
     if (!parents || !states) return SPEC_ERR_ARG;
     // every state is checked before anything is enqueued
-    uintptr_t low_bits = 0;
+    uint64_t bits = 0;
     bool in_place = false;
     for (int i = 0; i < num_states; ++i) {
         const spec_beam_state &s = states[i];
@@ -460,49 +501,53 @@ spec_status spec_beam_reorder(const int32_t *parents, const int32_t *lengths, in
             const Span oto{odst, odst + other * num_out * batch};
             if (to.meets(oto) || to.meets(ofrom) || from.meets(oto)) return SPEC_ERR_ARG;
         }
+        if (!grid_fits(reorder_blocks(s, reorder_unit(reorder_bits(s)), batch), kReorderBlock))
+            return SPEC_ERR_UNSUPPORTED;  // a launch takes whole states
         in_place = in_place || src == dst;
-        low_bits |= reinterpret_cast<uintptr_t>(src) | reinterpret_cast<uintptr_t>(dst) |
-                    static_cast<uintptr_t>(s.position_bytes);
+        bits |= reorder_bits(s);
     }
-    const int unit = low_bits % 16 == 0 ? 16 : low_bits % 4 == 0 ? 4 : 1;
     const int group = !in_place || num_beams <= 8 ? 8 : num_beams <= 16 ? 16 : 32;
-    const int64_t chunk_bytes = static_cast<int64_t>(unit) * kReorderBlock;
     hipStream_t st = static_cast<hipStream_t>(stream);
+    const int common = reorder_unit(bits);
     int64_t all = 0;
-    for (int i = 0; i < num_states && all < (int64_t{1} << 40); ++i)
-        all += (states[i].position_bytes * states[i].positions + chunk_bytes - 1) / chunk_bytes *
-               states[i].segments * batch;
-    if (!grid_fits(all, kReorderBlock)) return SPEC_ERR_UNSUPPORTED;
-    for (int from = 0; from < num_states; from += kMaxReorder) {
+    for (int i = 0; i < num_states && all <= kOneUnitWork; ++i)
+        all += reorder_blocks(states[i], common, batch);
+    const bool together = reorder_together(all, common, num_beams);
+    for (const int unit : {16, 4, 1}) {
         ReorderArgs a{};
         a.parents = parents;
         a.lengths = lengths;
         a.W = num_beams;
         a.n = num_out;
-        uint32_t blocks = 0;
-        for (int i = from; i < num_states && i < from + kMaxReorder; ++i) {
+        int64_t blocks = 0;
+        for (int i = 0; i < num_states; ++i) {
             const spec_beam_state &s = states[i];
-            if (s.positions == 0) continue;
+            const bool shared =
+                together && grid_fits(reorder_blocks(s, common, batch), kReorderBlock);
+            if (unit != (shared ? common : reorder_unit(reorder_bits(s)))) continue;
+            const int64_t more = reorder_blocks(s, unit, batch);
+            if (more == 0) continue;
+            if (a.count == kMaxReorder || !grid_fits(blocks + more, kReorderBlock)) {
+                launch_reorder(a, unit, group, blocks, st);
+                const spec_status r = launch_status();
+                if (r != SPEC_OK) return r;
+                a.count = 0;
+                blocks = 0;
+            }
             ReorderState &r = a.st[a.count++];
             r.src = static_cast<const char *>(s.src);
             r.dst = static_cast<char *>(s.dst);
             r.pos_bytes = s.position_bytes;
             r.segments = s.segments;
             r.positions = s.positions;
-            r.chunks = static_cast<int32_t>((s.position_bytes * s.positions + chunk_bytes - 1) /
-                                            chunk_bytes);
-            r.first = blocks;
-            blocks += static_cast<uint32_t>(r.chunks) * s.segments * batch;
+            r.chunks = static_cast<int32_t>(reorder_chunks(s, unit));
+            r.first = static_cast<uint32_t>(blocks);
+            blocks += more;
         }
-        if (blocks == 0) continue;
-        if (unit == 16)
-            launch_reorder<16>(a, group, blocks, st);
-        else if (unit == 4)
-            launch_reorder<4>(a, group, blocks, st);
-        else
-            launch_reorder<1>(a, group, blocks, st);
-        const spec_status s = launch_status();
-        if (s != SPEC_OK) return s;
+        if (a.count == 0) continue;
+        launch_reorder(a, unit, group, blocks, st);
+        const spec_status r = launch_status();
+        if (r != SPEC_OK) return r;
     }
     return SPEC_OK;
 }

@@ -278,7 +278,8 @@ __global__ __launch_bounds__(BLOCK) void beam_merge_kernel(BeamArgs a) {
 
 // ---------------------------------------------------------------------------
 // Reordering of states: dst[b][i] = src[b][parents[b][i]], the used positions
-// of every segment.  A thread takes one unit (16, 4 or 1 bytes) of a sequence: it
+// of every segment.  A thread takes one unit (16, 4 or 1 bytes, for all states of
+// a launch) of a sequence: it
 // reads each parent that has children once and writes the children's rows.  In
 // place it reads all the parents before it writes, and no other thread touches
 // that unit, so nothing is overwritten that is still needed.  Bound by memory:

@@ -560,7 +560,12 @@ spec_status spec_beam_select(const void *logits, int64_t row_stride, const float
  * refused, also between the states of a call (two may share a src that none
  * writes).  parents: device
  * int32 [B][num_out].  num_beams <= 32, num_out <= 64.  One launch moves up to
- * 32 states.
+ * 32 states.  A state is moved in units of 16, 4 or 1 bytes, the widest that
+ * its addresses and position_bytes are multiples of, whatever the call's other
+ * states are.  Limits, beyond which a call is refused (SPEC_ERR_UNSUPPORTED): a
+ * position of 2^31 - 1 bytes; and for a state, summed over the batch and
+ * per beam, just under 64, 16 or 4 GiB by its unit (every segment counted up
+ * to whole 4096, 1024 or 256 bytes).
  */
 typedef struct spec_beam_state {
     const void *src;

@@ -136,6 +136,28 @@ def test_beam_reorder_validates_on_host(L):
         assert call(**kw) == -2, kw
 
 
+@host_only
+def test_beam_reorder_takes_each_state_by_its_own_size(L):
+    # without a GPU a call that passes every check ends in a failed launch (-4)
+    def call(*states, B=1):
+        st = (sv._BeamState * len(states))(*[sv._BeamState(*s) for s in states])
+        return L.spec_beam_reorder(ctypes.c_void_p(16), None, B, 4, 4, st, len(states), None)
+    cache = (1 << 40, 1 << 44, 256, 2, 1 << 24)          # 8 GiB a beam, in 16-byte units
+    flags = (1 << 46, 1 << 47, 1, 1, 37)                 # 37 single bytes
+    assert call(cache) == -4 and call(flags) == -4
+    assert call(cache, flags) == -4 and call(flags, cache) == -4
+    # more workgroups in all than one launch holds, fewer in each state
+    many = [((1 << 40) + (i << 34), (1 << 45) + (i << 34), 20, 1, (1 << 31) // 20)
+            for i in range(16)]
+    assert call(*many) == -4
+    # a state that one launch cannot hold: 64 GiB, 16 GiB and 4 GiB a beam
+    for unit, positions, segments in ((16, 1 << 28, 16), (4, 1 << 28, 16), (1, 1 << 28, 16)):
+        over = (1 << 50, 1 << 54, unit, segments, positions)
+        under = (1 << 50, 1 << 54, unit, segments - 1, positions)
+        assert call(over) == -2 and call(cache, over) == -2, unit
+        assert call(under) == -4, unit
+
+
 def test_binding_refuses_host_tensors_and_wrong_shapes():
     f, i = torch.zeros(2, 3, 8), torch.zeros(2, 3, 4, dtype=torch.int32)
     for call in (lambda: sv.row_topk(f, 2), lambda: sv.distill_loss(f, i, i.float()),

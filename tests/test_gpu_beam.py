@@ -295,3 +295,59 @@ def test_near_ties_of_rows_with_masked_logits(V, T):
         r = select(np.ascontiguousarray(x[:, order]), np.full((1, W), -3.0, np.float32), 5, T=T)
         # the lightest row's maximum comes first
         assert list(r["parents"][0, :W]) == list(np.argsort(order))
+
+
+@pytest.mark.parametrize("with_lengths", [False, True])
+@pytest.mark.parametrize("W", [3, 12, 32])
+def test_reorder_states_of_different_units_in_one_call(W, with_lengths):
+    # caches in 16-byte units, histories in 4-byte ones, flags in single bytes,
+    # more than one launch of them, alternating
+    rng = np.random.default_rng(W)
+    parents = rng.integers(-1, W + 1, (2, W))
+    lengths = [11, 4] if with_lengths else None
+    g = torch.Generator().manual_seed(W)
+    shapes = [((2, W, 2, 13, 8), torch.bfloat16), ((2, W, 1, 13, 1), torch.int32),
+              ((2, W, 3, 13, 3), torch.uint8), ((2, W, 1, 13, 5), torch.bfloat16)]
+    src = [torch.randint(0, 127, shape, generator=g).to(dt)
+           for i in range(18) for shape, dt in shapes[i % 2:] + shapes[:i % 2]]
+    dst = [torch.full_like(s, 5) for s in src]
+
+    def want(s, d):
+        to = torch.float64 if s.is_floating_point() else torch.int64
+        at = s if with_lengths else s.reshape(2, W, 1, 1, -1)
+        out = ref.beam_reorder(parents, at.to(to).numpy(),
+                               d.to(to).reshape(at.shape).numpy(), lengths)
+        return torch.from_numpy(out).reshape(s.shape).to(s.dtype)
+    p = torch.tensor(parents, dtype=torch.int32, device=DEV)
+    le = torch.tensor(lengths, dtype=torch.int32, device=DEV) if with_lengths else None
+    gs, gd = [s.to(DEV) for s in src], [d.to(DEV) for d in dst]
+    sv.beam_reorder(p, gs, gd, lengths=le)
+    for s, d, a, b in zip(src, dst, gs, gd):
+        assert torch.equal(b.cpu(), want(s, d)) and torch.equal(a.cpu(), s)
+    # some in place, the others to buffers of their own
+    outs = [s if i % 3 else torch.full_like(s, 5) for i, s in enumerate(gs)]
+    sv.beam_reorder(p, gs, outs, lengths=le)
+    for i, (s, b) in enumerate(zip(src, outs)):
+        assert torch.equal(b.cpu(), want(s, s if i % 3 else torch.full_like(s, 5)))
+
+
+@pytest.mark.parametrize("W", [2, 8, 9, 16])
+def test_reorder_large_states_of_different_units_in_one_call(W):
+    # enough work for a launch per unit; bytes are checked on the GPU
+    g = torch.Generator(device=DEV).manual_seed(W)
+    p = torch.randint(0, W, (3, W), generator=g, device=DEV, dtype=torch.int32)
+    shapes = [((3, W, 2, 4001, 64), torch.bfloat16), ((3, W, 1, 4001, 1), torch.int32),
+              ((3, W, 1, 4001, 3), torch.uint8), ((3, W, 4, 4001, 16), torch.float32)]
+    src = [torch.randint(0, 127, shape, generator=g, device=DEV).to(dt) for shape, dt in shapes]
+    lengths = torch.tensor([4001, 0, 2777], dtype=torch.int32, device=DEV)
+    used = torch.arange(4001, device=DEV) < lengths[:, None]
+    for count in (2, 3, 4):
+        outs = [torch.full_like(s, 5) for s in src[:count]]
+        sv.beam_reorder(p, src[:count], outs, lengths=lengths)
+        place = [s.clone() for s in src[:count]]
+        sv.beam_reorder(p, place, lengths=lengths)
+        for s, o, q in zip(src, outs, place):
+            moved = s[torch.arange(3, device=DEV)[:, None], p.long()]
+            at = used[:, None, None, :, None]
+            assert torch.equal(o, torch.where(at, moved, torch.full_like(s, 5)))
+            assert torch.equal(q, torch.where(at, moved, s))

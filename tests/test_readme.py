@@ -12,6 +12,9 @@ from oracle import draft_ref as ref
 
 README = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")
 
+# a tree may be shipped without its documents
+pytestmark = pytest.mark.skipif(not os.path.exists(README), reason="README.md is not here")
+
 
 def example():
     with open(README, encoding="utf-8") as f:
