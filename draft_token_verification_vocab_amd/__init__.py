@@ -30,6 +30,7 @@ MODE_LOSSLESS = 0
 MODE_FLY = 1
 DTYPE_F32 = 0
 DTYPE_BF16 = 1
+_INT32_MAX = 2 ** 31 - 1
 # boundary-case bits of VerifyResult.boundary (see include/specverify.h)
 NEAR_ACCEPT = 1
 NEAR_RACE = 2
@@ -905,6 +906,18 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, num_out: int, *,
     return res
 
 
+def _positions(nbytes: int) -> int:
+    """The least number of equal positions that a run of nbytes divides into, so
+    that none passes the library's limit and each keeps the run's unit (16, 4 or
+    1 bytes).  1 (which the library refuses) where a long run has no such divisor
+    below 65536."""
+    unit = 16 if nbytes % 16 == 0 else 4 if nbytes % 4 == 0 else 1
+    for n in range(-(-nbytes // _INT32_MAX), 65536):
+        if nbytes // unit % n == 0:
+            return n
+    return 1
+
+
 def beam_reorder(parents: torch.Tensor, states, outs=None, *,
                  lengths: Optional[torch.Tensor] = None, position_dim: int = 3) -> list:
     """Move the beams' states behind their parents (int32 [B, n], as
@@ -912,7 +925,8 @@ def beam_reorder(parents: torch.Tensor, states, outs=None, *,
     tensor [B, W, ...] of states; a parent outside the beams leaves its row.
     outs: tensors [B, n, ...] to write, None: in place (n = W).  lengths
     (int32 [B]): only that many positions, along dimension position_dim of
-    every state, are moved.  Returns the list of tensors written."""
+    every state, are moved; a position of more than 2^31 - 1 bytes is refused.
+    Returns the list of tensors written."""
     _need_cuda(parents, "parents", dtype=torch.int32)
     B, n = parents.shape
     dev = parents.device
@@ -948,8 +962,12 @@ def beam_reorder(parents: torch.Tensor, states, outs=None, *,
         s = table[used]
         used += 1
         s.src, s.dst = src.data_ptr(), dst.data_ptr()
-        s.position_bytes = row // (seg * pos) * src.element_size()
-        s.segments, s.positions = seg, pos
+        nbytes = row // (seg * pos) * src.element_size()
+        if lengths is None and nbytes > _INT32_MAX:
+            s.positions = _positions(nbytes)
+            s.position_bytes, s.segments = nbytes // s.positions, seg
+        else:
+            s.position_bytes, s.segments, s.positions = nbytes, seg, pos
     _enqueue("spec_beam_reorder", dev, load().spec_beam_reorder, parents.data_ptr(),
              _addr(lengths), B, W, n, table, used)
     return outs

@@ -167,3 +167,11 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
                  lambda: sv.beam_reorder(torch.zeros(2, 3, dtype=torch.int32), [f])):
         with pytest.raises(ValueError, match="GPU tensor"):
             call()
+
+
+def test_long_runs_are_cut_into_positions_that_keep_their_unit():
+    for nbytes, unit in ((2 ** 31, 16), (2 ** 31 + 16, 16), (2 ** 33 + 48, 16), (2 ** 31 + 1, 1),
+                         (5 * 10 ** 9 + 4, 4), (2 ** 32 + 2, 1), (3 * 2 ** 34, 16)):
+        n = sv._positions(nbytes)
+        assert nbytes % n == 0 and nbytes // n <= 2 ** 31 - 1 and nbytes // n % unit == 0, nbytes
+    assert sv._positions(2147483659) == 1            # a prime past 2^31: refused by the library

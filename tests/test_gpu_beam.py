@@ -351,3 +351,22 @@ def test_reorder_large_states_of_different_units_in_one_call(W):
             at = used[:, None, None, :, None]
             assert torch.equal(o, torch.where(at, moved, torch.full_like(s, 5)))
             assert torch.equal(q, torch.where(at, moved, s))
+
+
+@pytest.mark.parametrize("shape", [(1, 2, 2, (1 << 30) + 8), (1, 2, (1 << 31) + 48),
+                                   (1, 2, 3, 715827883)])
+def test_reorder_beams_of_more_than_two_gib(shape):
+    # without lengths a beam is one run of bytes, here more than a position holds
+    # (2^31 + 16 and 2^31 + 48; 2^31 + 1, which has no factor of 16 or 4)
+    s = torch.zeros(shape, dtype=torch.uint8, device=DEV)
+    flat = s.view(2, -1)
+    ends = [0, 1, 2 ** 30 + 7, 2 ** 31 - 2, 2 ** 31 - 1, 2 ** 31, flat.shape[1] - 1]
+    for w in range(2):
+        flat[w] = w + 1
+        flat[w, ends] = torch.arange(7, dtype=torch.uint8, device=DEV) + 10 * (w + 1)
+    p = torch.tensor([[1, 1]], dtype=torch.int32, device=DEV)
+    out = torch.zeros_like(s)
+    sv.beam_reorder(p, [s], [out])
+    assert torch.equal(out.view(2, -1)[0], flat[1]) and torch.equal(out.view(2, -1)[1], flat[1])
+    sv.beam_reorder(p, [s])
+    assert torch.equal(flat[0], out.view(2, -1)[0]) and torch.equal(flat[1], out.view(2, -1)[1])
