@@ -174,11 +174,13 @@ struct OnlineSum {
             s4[k & 3] = k < 4 ? e : s4[k & 3] + e;
         }
         float cs = (s4[0] + s4[1]) + (s4[2] + s4[3]);
-        if (!(cs == cs)) {  // a NaN entry: the chunk again without it
-            cs = 0.f;
+        if (!(cs == cs)) {  // a NaN entry: the chunk again without it, added alike
 #pragma unroll
-            for (int k = 0; k < N; ++k)
-                cs += x[k] > kMasked ? hw_exp2(fmaf(x[k], slope, -n)) : 0.f;
+            for (int k = 0; k < N; ++k) {
+                const float e = x[k] > kMasked ? hw_exp2(fmaf(x[k], slope, -n)) : 0.f;
+                s4[k & 3] = k < 4 ? e : s4[k & 3] + e;
+            }
+            cs = (s4[0] + s4[1]) + (s4[2] + s4[3]);
         }
         s += static_cast<double>(cs);
     }

@@ -170,3 +170,29 @@ def test_huge_logits():
     check(x, 9, "f32")
     check(x, 9, "f32", T=1e-4)
     check(x[:, :2990], 9, "bf16", T=3.0)
+
+
+@pytest.mark.parametrize("up", [1, -1])
+def test_normaliser_of_a_chunk_with_a_nan_entry(up):
+    """One logit at 0 and fourteen whose terms are a hair more (or less) than half
+    a step of 1: added to 1 one by one, each is rounded up to a step (or lost),
+    fourteen half steps in all.  The sixteenth entry of their chunk is a NaN; the
+    chunk's sum has to stay within the five additions that a term goes through
+    in a chunk without one."""
+    h, rows, V = 2.0 ** -24, 3, 4096
+    # row 0: the 16 logits that a thread of a 4096-float row takes at once
+    block = np.arange(V).reshape(4, 256, 4)          # [vector][thread][entry]
+    x = np.full((rows, V), -np.inf, np.float32)
+    small = np.float32(-24 * math.log(2) + up * 1e-3)
+    at = [block[:, 0].ravel(), block[:, 131].ravel(), np.arange(16) * 200 + 7]
+    for r in range(rows):
+        x[r, at[r]] = small
+        x[r, at[r][0]], x[r, at[r][9]] = 0.0, np.nan
+    got = sv.row_topk(torch.from_numpy(x).to(DEV), 16)
+    torch.cuda.synchronize()
+    _, ids, lse = ref.row_topk(x, 16)
+    assert np.array_equal(got["ids"].cpu().numpy(), ids)
+    # the exponents: 0, and fourteen of 24 whose terms weigh 2^-24 each
+    tol = math.log(2) * 3 * h * 14 * 24 * 1.01 * h + 7 * h + abs(lse) * h
+    off = np.abs(got["lse"].cpu().numpy() - lse)
+    assert (off <= tol).all(), off / h
