@@ -47,27 +47,28 @@ struct BeamArgs {
 };
 
 // ln sum e^((l - M)/T) of a row in double, M its largest visible logit.  A
-// term's exponent is i + k/32 + f/32 with |f| <= 1/2: 2^(k/32) from a table of
-// 32 doubles, one per pair of LDS banks, times the Taylor series of 2^(f/32) cut
-// where the next term is below 2^-52.  Masked logits count 2^-1000 beside the
-// maximum's 1.  Bound by issue of double-precision instructions: 25 us for 152064
-// bfloat16 logits, 27 in float32 (31 and 33 with the series of twelve terms that
-// needs no table; the next vector's load ahead of the sums gained nothing).
+// term's exponent is i + k/64 + f/64 with |f| <= 1/2: 2^(k/64) from a table of
+// 64 doubles times the Taylor series of 2^(f/64) to the fifth degree, whose next
+// term is below 2^-54 (with 32 doubles it would be 2^-48.7, always to one side,
+// in the same time).  Masked logits count 2^-1000 beside the maximum's 1.  Bound
+// by issue of double-precision instructions: 25 us for 152064 bfloat16 logits, 27
+// in float32 (31 and 33 with the series of twelve terms that needs no table; the
+// next vector's load ahead of the sums gained nothing).
 template <typename T, int BLOCK>
 __device__ __attribute__((noinline)) double exact_normaliser(const T *row, int V, float M,
                                                             double inv_t, double *sh, int tid) {
     using E = Elem<T>;
     constexpr int EPV = E::kPerVec;
-    __shared__ double sh_pow[32];
+    __shared__ double sh_pow[64];
     const int nvec = (V + EPV - 1) / EPV;
-    const double c32 = inv_t * kLog2eD * 32.0;
-    const double deepest = -32000.0 / c32;  // below: 2^-1000, as good as 0
+    const double c64 = inv_t * kLog2eD * 64.0;
+    const double deepest = -64000.0 / c64;  // below: 2^-1000, as good as 0
     const double top = static_cast<double>(M);
     constexpr double kRound = 0x1.8p52;  // leaves the integer in the low word
-    constexpr double u = kLn2 / 32.0;
+    constexpr double u = kLn2 / 64.0;
     constexpr double c2 = u * u / 2.0, c3 = c2 * u / 3.0, c4 = c3 * u / 4.0, c5 = c4 * u / 5.0;
     __syncthreads();  // the table of the row before is read no more
-    if (tid < 32) sh_pow[tid] = exp2_f64(tid / 32.0);
+    if (tid < 64) sh_pow[tid] = exp2_f64(tid / 64.0);
     __syncthreads();
     double s = 0.0;
     for (int i = tid; i < nvec; i += BLOCK) {
@@ -79,15 +80,15 @@ __device__ __attribute__((noinline)) double exact_normaliser(const T *row, int V
         for (int e = 0; e < EPV; ++e) {
             const float l = x[e] > kMasked ? x[e] : -__builtin_inff();
             const double d = fmax(static_cast<double>(l) - top, deepest);
-            const double y = fma(d, c32, kRound);
-            const double f = fma(d, c32, kRound - y);
+            const double y = fma(d, c64, kRound);
+            const double f = fma(d, c64, kRound - y);
             const int n = __double2loint(y);
             double p = fma(c5, f, c4);
             p = fma(p, f, c3);
             p = fma(p, f, c2);
             p = fma(p, f, u);
-            p = fma(p, f, 1.0) * sh_pow[n & 31];
-            s += __hiloint2double(__double2hiint(p) + ((n & ~31) << 15), __double2loint(p));
+            p = fma(p, f, 1.0) * sh_pow[n & 63];
+            s += __hiloint2double(__double2hiint(p) + ((n & ~63) << 14), __double2loint(p));
         }
     }
     s = wave_sum_f64(s);

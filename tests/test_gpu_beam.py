@@ -1,5 +1,7 @@
 """Beam selection and reordering on the GPU against their 64-bit definitions:
 choices and moved bytes exactly, scores within the bound of their arithmetic."""
+from decimal import Decimal, localcontext
+
 import numpy as np
 import pytest
 import torch
@@ -370,3 +372,51 @@ def test_reorder_beams_of_more_than_two_gib(shape):
     assert torch.equal(out.view(2, -1)[0], flat[1]) and torch.equal(out.view(2, -1)[1], flat[1])
     sv.beam_reorder(p, [s])
     assert torch.equal(flat[0], out.view(2, -1)[0]) and torch.equal(flat[1], out.view(2, -1)[1])
+
+
+def hair_apart(j, ahead, parts):
+    """Two rows of float32 logits and their beams' scores, the second beam's best
+    continuation ahead of the first's by `ahead` (beyond a double's digits).
+    Sixteen of the first row's terms lie halfway between two powers of
+    2^(1/parts), the second row's on one; three small logits of the second set the distance."""
+    with localcontext() as ctx:
+        ctx.prec = 60
+
+        def total(x):
+            return sum(Decimal(float(v)).exp() for v in x)
+        step = np.log(2.0) / parts
+        k = -round(1.0 / step) - j
+        a = [np.float32(0)] + [np.float32((k + 0.5) * step)] * 16
+        b = [np.float32(0)] + [np.float32(k * step)] * 16
+        want = (total(b) / total(a)).ln() + ahead
+        score = np.nextafter(np.float32(want), np.float32(1))
+        for _ in range(4):
+            more = total(a) * (Decimal(float(score)) - ahead).exp() - total(b)
+            if more < Decimal("1e-30"):
+                break
+            v = np.float32(more.ln())
+            b.append(v if Decimal(float(v)).exp() <= more else np.nextafter(v, np.float32(-99)))
+        gap = Decimal(float(score)) - (total(b) / total(a)).ln()
+        assert abs(gap - ahead) < ahead / 1000
+    return a, b, score
+
+
+@pytest.mark.parametrize("parts", [32, 64])
+def test_beams_a_hair_apart_are_decided_by_sums_good_to_a_double(parts):
+    """1e-15 apart, nine half steps of a double near 1: the terms, their sum and
+    its logarithm are rounded by one to four of them (each step of the double
+    arithmetic emulated exactly); a term off by 2e-15 would tell."""
+    n = 12
+    x = np.full((n, 2, 128), -np.inf, np.float32)
+    scores = np.zeros((n, 2), np.float32)
+    for j in range(n):
+        first, second, scores[j, 1] = hair_apart(j, Decimal("1e-15"), parts)
+        for w, row in enumerate((first, second)):
+            x[j, w, 4 * np.arange(len(row))] = row
+    for flip in (False, True):
+        order = [1, 0] if flip else [0, 1]
+        r = sv.beam_select(torch.from_numpy(np.ascontiguousarray(x[:, order])).to(DEV),
+                           torch.from_numpy(np.ascontiguousarray(scores[:, order])).to(DEV), 2)
+        torch.cuda.synchronize()
+        assert r["parents"][:, 0].tolist() == [0 if flip else 1] * n
+        assert r["parents"][:, 1].tolist() == [1 if flip else 0] * n
