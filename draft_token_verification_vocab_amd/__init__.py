@@ -772,6 +772,11 @@ def _enqueue(what: str, dev: torch.device, fn, *args):
         _check(status, what)
 
 
+# A call writes through raw pointers; this tells autograd, which refuses to go
+# backward through values that were overwritten since it kept them.
+_overwritten = torch.autograd.graph.increment_version
+
+
 def row_topk(logits: torch.Tensor, k: int, *, temperature: float = 1.0,
              vocab: Optional[int] = None, lse: bool = True) -> dict:
     """The k largest logits of each row of a [..., S] tensor (first V columns)
@@ -824,7 +829,8 @@ def distill_loss(student: torch.Tensor, ids: torch.Tensor, logits: torch.Tensor,
     nothing can tell), for a bucket over the unlisted ids; None: the list
     is a distribution of its own.  keep (uint8 [...]): rows to train on.
     Returns (loss [...], state): the state is what distill_grad takes
-    (state=False: None)."""
+    (state=False: None).  Autograd does not record the call: the loss carries no
+    graph, and student.backward(gradient) goes on from distill_grad's result."""
     p, rows, dev = _distill_args(student, ids, logits, lse, keep, None, temperature, vocab, None)
     L = load()
     loss = torch.empty(student.shape[:-1], dtype=torch.float32, device=dev)
@@ -843,8 +849,9 @@ def distill_grad(student: torch.Tensor, ids: torch.Tensor, logits: torch.Tensor,
                  out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Gradient of sum(grad_loss * loss) (grad_loss float32 [...], None: ones)
     with respect to the student's logits, in their dtype and shape, from the
-    state of the distill_loss call with the same arguments.  out may be the
-    student tensor itself."""
+    state of the distill_loss call with the same arguments: student values,
+    list, temperature and vocab (the state does not record them, and nothing
+    can tell).  out may be the student tensor itself."""
     p, rows, dev = _distill_args(student, ids, logits, None, None, grad_loss, temperature, vocab,
                                  out)
     L = load()
@@ -853,6 +860,8 @@ def distill_grad(student: torch.Tensor, ids: torch.Tensor, logits: torch.Tensor,
     _enqueue("spec_distill_grad", dev, L.spec_distill_grad, student.data_ptr(), ids.data_ptr(),
              logits.data_ptr(), state.data_ptr(), _addr(grad_loss), ctypes.byref(p),
              grad.data_ptr())
+    if out is not None:
+        _overwritten(out)
     return grad
 
 
@@ -862,7 +871,9 @@ def distill_step(student: torch.Tensor, ids: torch.Tensor, logits: torch.Tensor,
                  keep: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
     """Loss and gradient in one call, where the upstream gradient is known
     beforehand (1/N for a mean over N rows): the (loss, gradient) of
-    distill_loss and distill_grad."""
+    distill_loss and distill_grad, neither with a graph of its own.  out may be
+    the student tensor itself: autograd then refuses a backward pass that needs
+    the logits it held."""
     p, rows, dev = _distill_args(student, ids, logits, lse, keep, grad_loss, temperature, vocab,
                                  out)
     loss = torch.empty(student.shape[:-1], dtype=torch.float32, device=dev)
@@ -870,6 +881,8 @@ def distill_step(student: torch.Tensor, ids: torch.Tensor, logits: torch.Tensor,
     _enqueue("spec_distill_step", dev, load().spec_distill_step, student.data_ptr(),
              ids.data_ptr(), logits.data_ptr(), _addr(lse), _addr(keep), _addr(grad_loss),
              ctypes.byref(p), loss.data_ptr(), grad.data_ptr())
+    if out is not None:
+        _overwritten(out)
     return loss, grad
 
 
@@ -970,4 +983,5 @@ def beam_reorder(parents: torch.Tensor, states, outs=None, *,
             s.position_bytes, s.segments, s.positions = nbytes, seg, pos
     _enqueue("spec_beam_reorder", dev, load().spec_beam_reorder, parents.data_ptr(),
              _addr(lengths), B, W, n, table, used)
+    _overwritten(outs)
     return outs

@@ -222,3 +222,31 @@ def test_refusals_of_the_binding():
     one, two = flat[:48].view(3, 4, 4), flat[4:52].view(3, 4, 4)
     with pytest.raises(sv.SpecVerifyError):
         sv.beam_reorder(p, [one], [two])                 # overlapping buffers
+
+
+def test_autograd_sees_what_the_calls_overwrite():
+    """exp keeps its result for its backward pass: once a call has written there,
+    that pass has to be refused, not to go on with other values."""
+    x = inputs(8)
+    top = sv.row_topk(x["logits"], 8, vocab=V)
+    teacher = top["ids"], top["values"]
+
+    def result(t):
+        return t.float().clone().requires_grad_().exp()
+    student = result(x["student"] / 8)
+    version = student._version
+    _, state = sv.distill_loss(student, *teacher, vocab=V)
+    sv.distill_grad(student, *teacher, state, vocab=V)
+    sv.distill_step(student, *teacher, vocab=V)
+    assert student._version == version
+    student.sum().backward()                         # nothing was written
+    writes = [lambda t: sv.distill_grad(t, *teacher, state, vocab=V, out=t),
+              lambda t: sv.distill_step(t, *teacher, vocab=V, out=t),
+              lambda t: sv.beam_reorder(torch.zeros(3, 4, dtype=torch.int32, device=DEV), [t]),
+              lambda t: sv.beam_reorder(torch.zeros(3, 4, dtype=torch.int32, device=DEV),
+                                        [torch.zeros_like(t)], [t])]
+    for write in writes:
+        student = result(x["student"] / 8)
+        write(student)
+        with pytest.raises(RuntimeError, match="inplace"):
+            student.sum().backward()
