@@ -110,7 +110,9 @@ spec_status check_distill(const void *student, const int32_t *ids, const float *
     if (p->k > kDistillMax || p->vocab > kMaxListVocab) return SPEC_ERR_UNSUPPORTED;
     if (p->rows == 0) return SPEC_OK;
     if (!student || !aligned16(student) || !ids || !logits) return SPEC_ERR_ARG;
-    if (p->row_stride * elem_size(p->dtype) > INT32_MAX ||
+    // the rows alone first: below that their products stay within 64 bits
+    if (p->row_stride > INT32_MAX || p->row_stride * elem_size(p->dtype) > INT32_MAX ||
+        !grid_fits(p->rows, 1024) ||
         !grid_fits(p->rows * ((p->row_stride + kGradVecs - 1) / kGradVecs), 1024))
         return SPEC_ERR_UNSUPPORTED;
     return SPEC_OK;

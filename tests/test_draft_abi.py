@@ -80,6 +80,19 @@ def test_distill_validates_on_host(L):
 
 
 @host_only
+def test_distill_refuses_row_counts_whose_products_pass_64_bits(L):
+    a = ctypes.c_void_p(16)
+    for rows, stride in (((1 << 62) + 1, 16384), ((1 << 63) - 1, 1 << 20), (1 << 61, 1 << 20),
+                         ((1 << 32) + 5, 1024)):
+        p = sv._DistillParams(rows=rows, vocab=1024, dtype=1, row_stride=stride, k=8,
+                              temperature=1.0, reserved=0)
+        p = ctypes.byref(p)
+        assert L.spec_distill_loss(a, a, a, None, None, p, a, a, None) == -2, rows
+        assert L.spec_distill_grad(a, a, a, a, None, p, a, None) == -2, rows
+        assert L.spec_distill_step(a, a, a, None, None, None, p, a, a, None) == -2, rows
+
+
+@host_only
 def test_beam_select_validates_on_host(L):
     P = ctypes.c_void_p
     a, big = P(16), 1 << 30
