@@ -110,10 +110,8 @@ spec_status check_distill(const void *student, const int32_t *ids, const float *
     if (p->k > kDistillMax || p->vocab > kMaxListVocab) return SPEC_ERR_UNSUPPORTED;
     if (p->rows == 0) return SPEC_OK;
     if (!student || !aligned16(student) || !ids || !logits) return SPEC_ERR_ARG;
-    // the rows alone first: below that their products stay within 64 bits
     if (p->row_stride > INT32_MAX || p->row_stride * elem_size(p->dtype) > INT32_MAX ||
-        !grid_fits(p->rows, 1024) ||
-        !grid_fits(p->rows * ((p->row_stride + kGradVecs - 1) / kGradVecs), 1024))
+        !grid_fits(p->rows, 1024))
         return SPEC_ERR_UNSUPPORTED;
     return SPEC_OK;
 }
@@ -378,6 +376,7 @@ spec_status spec_distill_grad(const void *student, const int32_t *ids, const flo
     a.seg_vecs = kGradVecs;
     const int64_t vecs = params->row_stride * elem_size(params->dtype) / 16;
     const int segs = static_cast<int>((vecs + kGradVecs - 1) / kGradVecs);
+    if (!grid_fits(params->rows * segs, kGradBlock)) return SPEC_ERR_UNSUPPORTED;
     const dim3 grid(static_cast<unsigned>(params->rows * segs));
     hipStream_t st = static_cast<hipStream_t>(stream);
     if (params->dtype == SPEC_DTYPE_BF16)

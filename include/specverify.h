@@ -441,7 +441,7 @@ spec_status spec_row_stats(const void *logits, int64_t rows, int32_t vocab, int6
  * filled up with (-inf, -1).  lse (device float [rows], nullable): ln sum
  * e^(l/T) over the whole row, -inf when it is masked throughout; it is the
  * normaliser at this T only.  One pass over the rows, no workspace.
- * 1 <= k <= 128.
+ * 1 <= k <= 128; fewer than 2^22 rows, else SPEC_ERR_UNSUPPORTED.
  */
 spec_status spec_row_topk(const void *logits, int64_t rows, int32_t vocab, int64_t row_stride,
                           int32_t dtype, float temperature, int32_t k, float *values,
@@ -474,10 +474,12 @@ spec_status spec_row_topk(const void *logits, int64_t rows, int32_t vocab, int64
  * belongs in grad_loss too.
  */
 typedef struct spec_distill_params {
-    int64_t rows;       /* R >= 0                                             */
+    int64_t rows;       /* 0 <= R < 2^22; for spec_distill_grad a row's 64 KiB */
+                        /* parts, counted over all rows, stay below 2^24 - 1  */
+                        /* (SPEC_ERR_UNSUPPORTED otherwise)                   */
     int32_t vocab;      /* V, 2 <= V <= 2^20                                  */
     int32_t dtype;      /* of the student's logits and their gradient         */
-    int64_t row_stride; /* elements between consecutive rows, >= V            */
+    int64_t row_stride; /* elements between consecutive rows, >= V; < 2 GiB   */
     int32_t k;          /* entries per list, 1 <= k <= 128                    */
     float temperature;  /* T, 1e-4 <= T <= 1e4                                */
     int64_t reserved;   /* must be 0                                          */
@@ -534,7 +536,7 @@ spec_status spec_distill_step(const void *student, const int32_t *ids, const flo
  * (device int32), and ended_out (device uint8, nullable: 1 where the parent
  * had ended or the token is eos).  With fewer continuations the rest is filled
  * with -inf, -1, -1 and 0.  num_beams <= 32, num_out <= 64, num_beams *
- * num_out <= 512, else SPEC_ERR_UNSUPPORTED.  Outputs share no memory with
+ * num_out <= 512, fewer than 2^22 rows, else SPEC_ERR_UNSUPPORTED.  Outputs share no memory with
  * inputs.  workspace: device,
  * spec_beam_workspace_bytes, 16-byte aligned; its contents on entry do not
  * matter.

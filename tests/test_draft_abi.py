@@ -93,6 +93,25 @@ def test_distill_refuses_row_counts_whose_products_pass_64_bits(L):
 
 
 @host_only
+def test_distill_takes_the_batches_that_its_launches_hold(L):
+    # without a GPU a call that passes every check ends in a failed launch (-4)
+    s, g, x = (ctypes.c_void_p(1 << n) for n in (40, 44, 46))
+
+    def calls(rows, vocab, stride, dtype):
+        p = ctypes.byref(sv._DistillParams(rows=rows, vocab=vocab, dtype=dtype, row_stride=stride,
+                                           k=8, temperature=1.0, reserved=0))
+        return (L.spec_distill_loss(s, x, x, None, None, p, x, x, None),
+                L.spec_distill_step(s, x, x, None, None, None, p, x, g, None),
+                L.spec_distill_grad(s, x, x, x, None, p, g, None))
+    for case in ((131072, 152064, 152064, 1), (1 << 21, 4100, 4104, 1), ((1 << 22) - 1, 8, 8, 0)):
+        assert calls(*case) == (-4, -4, -4), case
+    assert calls(1 << 22, 8, 8, 0) == (-2, -2, -2)
+    # rows of 512 KiB are eight parts for the gradient alone
+    assert calls((1 << 21) - 1, 131072, 131072, 0) == (-4, -4, -4)
+    assert calls(1 << 21, 131072, 131072, 0) == (-4, -4, -2)
+
+
+@host_only
 def test_beam_select_validates_on_host(L):
     P = ctypes.c_void_p
     a, big = P(16), 1 << 30

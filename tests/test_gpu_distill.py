@@ -255,3 +255,30 @@ def test_huge_logits(T):
     x[2] *= 1e10
     l, g, _ = check(x, ids, logits, None, T=T)
     assert np.isfinite(g).all()
+
+
+def test_more_rows_than_a_grid_of_row_parts():
+    # 2.1e6 rows (17 GB): the rows repeat, so every one has its first copy's results
+    R, n, V, S, k = 525 * 4000, 4000, 4100, 4104, 4
+    g = torch.Generator(device=DEV).manual_seed(5)
+    block = torch.randn(n, S, generator=g, device=DEV).to(torch.bfloat16)
+    ids = torch.randint(0, V, (n, k), generator=g, device=DEV, dtype=torch.int32)
+    logits = torch.randn(n, k, generator=g, device=DEV)
+    weight = torch.rand(n, generator=g, device=DEV)
+    one_l, state = sv.distill_loss(block, ids, logits, vocab=V)
+    one_g = sv.distill_grad(block, ids, logits, state, weight, vocab=V)
+    step_l, step_g = sv.distill_step(block, ids, logits, None, weight, vocab=V)
+    times = R // n
+    student = block.repeat(times, 1)
+    args = [t.repeat((times,) + (1,) * (t.dim() - 1)) for t in (ids, logits, weight)]
+    loss, state = sv.distill_loss(student, *args[:2], vocab=V)
+    assert torch.equal(loss.view(times, n), one_l.expand(times, n))
+    grad = sv.distill_grad(student, *args[:2], state, args[2], vocab=V)
+    for i in (0, 1, times // 2, times - 1):
+        assert torch.equal(grad[i * n:(i + 1) * n].view(torch.int16), one_g.view(torch.int16))
+    some = grad.view(times, -1)[:, ::997]
+    assert torch.equal(some, some[:1].expand_as(some))
+    loss, _ = sv.distill_step(student, *args[:2], None, args[2], vocab=V, out=grad)
+    assert torch.equal(loss.view(times, n), step_l.expand(times, n))
+    for i in (0, 1, times // 2, times - 1):
+        assert torch.equal(grad[i * n:(i + 1) * n].view(torch.int16), step_g.view(torch.int16))
