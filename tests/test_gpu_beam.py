@@ -420,3 +420,29 @@ def test_beams_a_hair_apart_are_decided_by_sums_good_to_a_double(parts):
         torch.cuda.synchronize()
         assert r["parents"][:, 0].tolist() == [0 if flip else 1] * n
         assert r["parents"][:, 1].tolist() == [1 if flip else 0] * n
+
+
+# Rows that the plan cuts, unlike most above: the workspace holds a list and a
+# normaliser per segment.
+@pytest.mark.parametrize("B,W,V,n,dtype", [(1, 4, 1 << 20, 8, "f32"), (15, 4, 140001, 1, "f32"),
+                                           (1, 2, 300001, 8, "bf16"), (2, 32, 100001, 4, "bf16"),
+                                           (1, 1, 1 << 20, 64, "bf16"), (3, 5, 98309, 20, "bf16")])
+def test_rows_that_are_cut_into_segments(B, W, V, n, dtype):
+    code = sv.DTYPE_BF16 if dtype == "bf16" else sv.DTYPE_F32
+    whole = sv.load().spec_beam_workspace_bytes(B, W, 2, code, n)
+    assert sv.load().spec_beam_workspace_bytes(B, W, V, code, n) > 2 * whole - 512
+    g = torch.Generator(device=DEV).manual_seed(V + W)
+    per = 8 if dtype == "bf16" else 4
+    S = -(-V // per) * per
+    t = (4 * torch.randn(B, W, S, generator=g, device=DEV)).to(DT[dtype])
+    t[:, W // 2, : V // 2] = float("-inf")           # segments with nothing visible
+    scores = -8 - 2 * torch.rand(B, W, generator=g, device=DEV)
+    r = sv.beam_select(t, scores, n, vocab=V)
+    lp = torch.log_softmax(t[..., :V].double(), -1) + scores.double()[..., None]
+    lp = lp.reshape(B, W * V)
+    # equal logits of a row: the lowest token first
+    best = torch.sort(lp, dim=-1, descending=True, stable=True)
+    values, at = best.values[:, :n], best.indices[:, :n]
+    assert torch.equal(r["parents"], (at // V).int())
+    assert torch.equal(r["tokens"], (at % V).int())
+    assert ((r["scores"] - values).abs() <= sum_error(V) + values.abs() * 2.0 ** -24).all()
