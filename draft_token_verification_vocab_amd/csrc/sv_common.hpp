@@ -60,7 +60,9 @@ __device__ __forceinline__ uint4 load_stream_buf(buf_rsrc r, uint32_t voff, uint
 // Maximum of three floats in one v_max3_f32.  Written as an instruction so
 // that a chain of them stays a chain: the compiler neither inserts operand
 // canonicalisations (logits enter as reinterpreted integer bits) nor reshapes
-// the chain into a tree of two-input maxima.  Operands are not NaN.
+// the chain into a tree of two-input maxima.  A quiet NaN among the operands is
+// passed over (the draft-model calls, where it masks a logit, rely on that; the
+// row pass has none); the result is a NaN when all three are.
 __device__ __forceinline__ float max3f(float a, float b, float c) {
     float r;
     asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));

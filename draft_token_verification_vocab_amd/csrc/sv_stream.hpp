@@ -208,7 +208,7 @@ __device__ __forceinline__ float wave_max_f32(float x) {
 }
 
 // Largest of a chunk's logits in a chain of three-input maxima (NaN entries
-// are passed over).
+// are passed over; a chunk of nothing else gives NaN, which no comparison takes).
 template <int N>
 __device__ __forceinline__ float chunk_max(const float (&x)[N]) {
     float cm = max3f(x[0], x[1], x[2]);

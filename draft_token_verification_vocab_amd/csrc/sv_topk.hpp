@@ -15,12 +15,12 @@
 // collected and placed by counting.  A row whose collection overflows (many
 // equal logits) is settled by further passes (collect_ties).
 //
-// Bound: vector issue and memory alike (8.7 instructions per logit, one of them
-// the quarter-rate exp2: 77 % busy).  2304 rows of 128256 bfloat16 logits, k = 64:
+// Bound: vector issue and memory alike (9.1 instructions per logit, one of them
+// the quarter-rate exp2: 79 % busy).  2304 rows of 128256 bfloat16 logits, k = 64:
 // 96 us, 6.2 TB/s; without the normaliser 90; the load-only pass over the same
-// rows takes 84.  Cutting the launch short showed 90 of 108 us in the stream;
-// keeping two register buffers in turn there gave 12 of them back.  Saving the
-// second chunks in LDS too gained nothing (115 us against 112 then).
+// rows takes 84.  Cut short after the stream the launch takes 89 to 90.  Two
+// register buffers in turn took the whole from 108 to 96 us (the stream alone
+// took 90 before, too).  Saving the second chunks in LDS too gained nothing (115 us against 112 then).
 // Few rows wait for one compute unit each: 256 KB take it 10 us.
 #pragma once
 

@@ -457,8 +457,11 @@ spec_status spec_row_topk(const void *logits, int64_t rows, int32_t vocab, int64
  *              = (1/T) q_j (P + r - r/rho)                    j outside it
  * lse (device float [rows], spec_row_topk's or spec_verify's target_lse at
  * the same temperature) is the teacher's log-normaliser L: the loss is then
- * the divergence over the listed ids and one bucket for the rest.  With lse
- * NULL, L is the list's own normaliser and r = 0.
+ * the divergence over the listed ids and one bucket for the rest.  L is a
+ * float, and its rounding is every listed mass's: |L| 2^-24 of it (2e-6 at
+ * |L| = 40, 2e-4 at 3000), and P's, so that much of r = 1 - P too.  With lse
+ * NULL, L is the list's own normaliser, taken relative to its largest logit, and
+ * r = 0.
  *   ids, logits  device, int32 and float [rows][k]: the teacher's list, in any
  *                order.  An entry whose id lies outside [0, vocab) or whose
  *                logit is masked is not listed; an id listed twice has both
@@ -475,7 +478,7 @@ spec_status spec_row_topk(const void *logits, int64_t rows, int32_t vocab, int64
  */
 typedef struct spec_distill_params {
     int64_t rows;       /* 0 <= R < 2^22; for spec_distill_grad a row's 64 KiB */
-                        /* parts, counted over all rows, stay below 2^24 - 1  */
+                        /* parts, counted over all rows, stay below 2^24      */
                         /* (SPEC_ERR_UNSUPPORTED otherwise)                   */
     int32_t vocab;      /* V, 2 <= V <= 2^20                                  */
     int32_t dtype;      /* of the student's logits and their gradient         */
@@ -536,10 +539,9 @@ spec_status spec_distill_step(const void *student, const int32_t *ids, const flo
  * (device int32), and ended_out (device uint8, nullable: 1 where the parent
  * had ended or the token is eos).  With fewer continuations the rest is filled
  * with -inf, -1, -1 and 0.  num_beams <= 32, num_out <= 64, num_beams *
- * num_out <= 512, fewer than 2^22 rows, else SPEC_ERR_UNSUPPORTED.  Outputs share no memory with
- * inputs.  workspace: device,
- * spec_beam_workspace_bytes, 16-byte aligned; its contents on entry do not
- * matter.
+ * num_out <= 512, fewer than 2^22 rows, else SPEC_ERR_UNSUPPORTED.  Outputs
+ * share no memory with inputs.  workspace: device, spec_beam_workspace_bytes,
+ * 16-byte aligned; its contents on entry do not matter.
  */
 size_t spec_beam_workspace_bytes(int32_t batch, int32_t num_beams, int32_t vocab, int32_t dtype,
                                  int32_t num_out);
