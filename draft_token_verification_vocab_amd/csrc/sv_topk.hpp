@@ -20,7 +20,8 @@
 // 96 us, 6.2 TB/s; without the normaliser 90; the load-only pass over the same
 // rows takes 84.  Cut short after the stream the launch takes 89 to 90.  Two
 // register buffers in turn took the whole from 108 to 96 us (the stream alone
-// took 90 before, too).  Saving the second chunks in LDS too gained nothing (115 us against 112 then).
+// took 90 before, too).  Saving the second chunks in LDS too gained nothing (115
+// us against 112 then).
 // Few rows wait for one compute unit each: 256 KB take it 10 us.
 #pragma once
 
