@@ -22,6 +22,8 @@ __all__ = [
     "SpecVerifyError", "lib_path", "load", "verify", "av_score", "av_score_stats", "av_update",
     "row_stats", "row_topk", "distill_loss", "distill_grad", "distill_step",
     "beam_select", "beam_reorder",
+    "tree_attention", "tree_accept", "cache_append", "cache_keep",
+    "pages_fork", "pages_release", "pages_reserve", "pages_copy",
     "workspace_bytes", "draft_stats_bytes", "MODE_LOSSLESS", "MODE_FLY",
 ]
 
@@ -30,6 +32,7 @@ MODE_LOSSLESS = 0
 MODE_FLY = 1
 DTYPE_F32 = 0
 DTYPE_BF16 = 1
+DTYPE_F16 = 2  # the paged-cache calls only
 _INT32_MAX = 2 ** 31 - 1
 # boundary-case bits of VerifyResult.boundary (see include/specverify.h)
 NEAR_ACCEPT = 1
@@ -70,8 +73,27 @@ class _BeamState(ctypes.Structure):
                 ("positions", ctypes.c_int32)]
 
 
+class _Cache(ctypes.Structure):
+    _fields_ = [("keys", ctypes.c_void_p), ("values", ctypes.c_void_p),
+                ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("slot_stride", ctypes.c_int64), ("table", ctypes.c_void_p),
+                ("lengths", ctypes.c_void_p), ("batch", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("table_width", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class _CachePools(ctypes.Structure):
+    _fields_ = [("bases", ctypes.c_void_p), ("num_pools", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("heads", ctypes.c_int32), ("page_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64),
+                ("slot_bytes", ctypes.c_int64)]
+
+
 # Every symbol the header declares, with its ctypes signature.
 _P = ctypes.c_void_p
+_I32, _I64 = ctypes.c_int32, ctypes.c_int64
 _SIGNATURES = {
     "spec_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(_Params)]),
     "spec_draft_stats_bytes": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32]),
@@ -131,6 +153,19 @@ _SIGNATURES = {
                                           _P, _P, _P, ctypes.c_size_t, _P]),
     "spec_beam_reorder": (ctypes.c_int32, [_P, _P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                                            ctypes.POINTER(_BeamState), ctypes.c_int32, _P]),
+    "spec_tree_attention_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(_Cache), _I32, _I32]),
+    "spec_tree_attention": (_I32, [ctypes.POINTER(_Cache), _P, _I64, _I64, _I64, _I32, _I32, _P, _P,
+                                   ctypes.c_float, _P, _P, _P, ctypes.c_size_t, _P]),
+    "spec_cache_append": (_I32, [ctypes.POINTER(_Cache), _P, _P, _I64, _I64, _I64, _I32, _P, _P]),
+    "spec_tree_accept": (_I32, [_P, _P, _P, _P, _I32, _I32, _P, _P, _P, _P]),
+    "spec_cache_keep": (_I32, [ctypes.POINTER(_CachePools), _P, _I32, _P, _P, _P, _I32, _I32, _P,
+                               _P]),
+    "spec_pages_fork": (_I32, [_P, _P, _P, _I32, _I32, _I32, _I32, _I32, _I32, _P, _P, _P, _P]),
+    "spec_pages_release": (_I32, [_P, _P, _I32, _I32, _I32, _I32, _P, _P]),
+    "spec_pages_reserve_workspace_bytes": (ctypes.c_size_t, [_I32, _I32]),
+    "spec_pages_reserve": (_I32, [_P, _P, _P, _I32, _I32, _I32, _I32, _P, _P, _P, _P,
+                                  ctypes.c_size_t, _P]),
+    "spec_pages_copy": (_I32, [ctypes.POINTER(_CachePools), _P, _I32, _P]),
     "spec_status_string": (ctypes.c_char_p, [ctypes.c_int32]),
 }
 
@@ -985,3 +1020,294 @@ def beam_reorder(parents: torch.Tensor, states, outs=None, *,
              _addr(lengths), B, W, n, table, used)
     _overwritten(outs)
     return outs
+
+
+# ---------------------------------------------------------------------------
+# Paged-cache calls: attention of new tokens over the pages, and their upkeep
+# ---------------------------------------------------------------------------
+_CACHE_DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
+
+
+def _strides(t):
+    """t's strides, 0 along dimensions of one element (whose strides may be anything)."""
+    return [0 if n == 1 else s for n, s in zip(t.shape, t.stride())]
+
+
+def _cache(keys, values, table, lengths):
+    """The checked _Cache of two pools [pages, heads, page, dim] and a table [B, P]."""
+    dev = keys.device
+    for t, name in ((keys, "keys"), (values, "values")):
+        if not t.is_cuda:
+            raise ValueError("%s must be a GPU tensor" % name)
+    if keys.dim() != 4 or keys.stride(3) != 1:
+        raise ValueError("keys must be [pages, heads, page, dim] with a contiguous last dimension")
+    if (values.device != dev or values.dtype != keys.dtype or values.shape != keys.shape
+            or values.stride() != keys.stride() and _strides(values) != _strides(keys)):
+        raise ValueError("values must be laid out as keys")
+    code = _CACHE_DTYPES.get(keys.dtype)
+    if code is None:
+        raise TypeError("keys and values must be float32, bfloat16 or float16, got %s" % keys.dtype)
+    if table.dim() != 2:
+        raise ValueError("table must be [B, pages of a sequence]")
+    B, P = table.shape
+    _need_cuda(table, "table", dev, torch.int32)
+    _need_cuda(lengths, "lengths", dev, torch.int32, (B,))
+    N, kv, page, D = keys.shape
+    s = _strides(keys)
+    return _Cache(keys.data_ptr(), values.data_ptr(), s[0], s[1], s[2], table.data_ptr(),
+                  lengths.data_ptr(), B, N, page, P, kv, D, code, 0)
+
+
+def _need_rows(t, name, cache, keys, heads=None):
+    """The strides of a [B, T, heads, dim] tensor with a contiguous last dimension."""
+    if not t.is_cuda or t.device != keys.device:
+        raise ValueError("%s must be on %s" % (name, keys.device))
+    if t.dtype != keys.dtype:
+        raise ValueError("%s must be %s, not %s" % (name, keys.dtype, t.dtype))
+    if (t.dim() != 4 or t.shape[0] != cache.batch or t.shape[3] != cache.dim
+            or (heads is not None and t.shape[2] != heads)):
+        raise ValueError("%s must have shape (%d, nodes, %s, %d), not %s"
+                         % (name, cache.batch, heads or "heads", cache.dim, tuple(t.shape)))
+    if t.stride(3) != 1:
+        raise ValueError("%s must have a contiguous last dimension" % name)
+    return _strides(t)
+
+
+@functools.lru_cache(maxsize=1024)
+def _tree_workspace_bytes(B: int, P: int, page: int, kv: int, dim: int, dtype: int, T: int,
+                          H: int) -> int:
+    c = _Cache(None, None, dim, dim, dim, None, None, B, 1, page, P, kv, dim, dtype, 0)
+    return int(load().spec_tree_attention_workspace_bytes(ctypes.byref(c), T, H))
+
+
+def tree_attention(q: torch.Tensor, keys: torch.Tensor, values: torch.Tensor, table: torch.Tensor,
+                   lengths: torch.Tensor, parents: Optional[torch.Tensor] = None, *,
+                   num_nodes: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                   lse: bool = False, out: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None):
+    """Attention of each sequence's new tokens (nodes) over its cached ones: q
+    [B, T, H, dim], pools keys and values [pages, heads, page, dim], whose heads
+    divide H, table int32 [B, P] of the sequences' pages (-1: none) and lengths
+    int32 [B] of cached positions.  The nodes' own keys and values are at the
+    positions behind them (cache_append).  parents int32 [B, T]: the node that a
+    node follows (-1: none), for a tree of at most 128 nodes; None: a chain.
+    Node i sees the cached positions, itself and its ancestors.  num_nodes int32
+    [B]: nodes in use; the others' outputs are 0.  scale: None is dim ** -0.5.
+    Returns out [B, T, H, dim], with lse also the log-sum-exp of the scores
+    (float32 [B, T, H], -inf where a node sees nothing).  q and the pools may be
+    strided views with contiguous last dimensions."""
+    c = _cache(keys, values, table, lengths)
+    sb, st, sh, _ = _need_rows(q, "q", c, keys)
+    B, T, H, D = q.shape
+    dev = q.device
+    if parents is not None:
+        _need_cuda(parents, "parents", dev, torch.int32, (B, T))
+    if num_nodes is not None:
+        _need_cuda(num_nodes, "num_nodes", dev, torch.int32, (B,))
+    if out is None:
+        out = torch.empty((B, T, H, D), dtype=q.dtype, device=dev)
+    else:
+        _need_cuda(out, "out", dev, q.dtype, (B, T, H, D))
+    sums = torch.empty((B, T, H), dtype=torch.float32, device=dev) if lse else None
+    if workspace is None:
+        n = _tree_workspace_bytes(B, c.table_width, c.page_size, c.kv_heads, D, c.dtype, T, H)
+        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
+    else:
+        _need_cuda(workspace, "workspace", dev)
+    _enqueue("spec_tree_attention", dev, load().spec_tree_attention, ctypes.byref(c), q.data_ptr(),
+             sb, st, sh, T, H, _addr(parents), _addr(num_nodes),
+             D ** -0.5 if scale is None else float(scale), out.data_ptr(), _addr(sums),
+             workspace.data_ptr(), _nbytes(workspace))
+    _overwritten(out)
+    return (out, sums) if lse else out
+
+
+def cache_append(k: torch.Tensor, v: torch.Tensor, keys: torch.Tensor, values: torch.Tensor,
+                 table: torch.Tensor, lengths: torch.Tensor, *,
+                 num_nodes: Optional[torch.Tensor] = None):
+    """Write the nodes' keys and values, k and v [B, T, heads, dim] (strided alike),
+    to the positions lengths[b] + j of their sequences' pages, for the first
+    num_nodes[b] nodes (None: T).  Positions without a page are left out.  Returns
+    (keys, values), the pools written."""
+    c = _cache(keys, values, table, lengths)
+    strides = _need_rows(k, "k", c, keys, c.kv_heads)
+    if _need_rows(v, "v", c, keys, c.kv_heads) != strides or v.shape != k.shape:
+        raise ValueError("v must be laid out as k")
+    if num_nodes is not None:
+        _need_cuda(num_nodes, "num_nodes", keys.device, torch.int32, (c.batch,))
+    _enqueue("spec_cache_append", keys.device, load().spec_cache_append, ctypes.byref(c),
+             k.data_ptr(), v.data_ptr(), *strides[:3], k.shape[1], _addr(num_nodes))
+    _overwritten((keys, values))
+    return keys, values
+
+
+def tree_accept(parents: torch.Tensor, tokens: torch.Tensor, chosen: torch.Tensor, *,
+                num_nodes: Optional[torch.Tensor] = None) -> dict:
+    """The path of each drafted tree that the target agrees with: from node 0 (the
+    last emitted token) to the lowest child whose token is what the target chose
+    after its parent, as long as there is one.  parents, tokens and chosen: int32
+    [B, T] (chosen: row_stats' argmax of the target's logits for greedy
+    verification, or its own samples).  Returns path (int32 [B, T], the accepted
+    nodes, then -1), count (int32 [B]) and tokens (int32 [B, T], what is emitted:
+    count tokens, the last one the target's own)."""
+    _need_cuda(tokens, "tokens", dtype=torch.int32)
+    if tokens.dim() != 2:
+        raise ValueError("tokens must be [B, nodes]")
+    B, T = tokens.shape
+    dev = tokens.device
+    _need_cuda(parents, "parents", dev, torch.int32, (B, T))
+    _need_cuda(chosen, "chosen", dev, torch.int32, (B, T))
+    if num_nodes is not None:
+        _need_cuda(num_nodes, "num_nodes", dev, torch.int32, (B,))
+    path, emitted = torch.empty((2, B, T), dtype=torch.int32, device=dev).unbind(0)
+    count = torch.empty(B, dtype=torch.int32, device=dev)
+    _enqueue("spec_tree_accept", dev, load().spec_tree_accept, parents.data_ptr(),
+             tokens.data_ptr(), chosen.data_ptr(), _addr(num_nodes), B, T, path.data_ptr(),
+             count.data_ptr(), emitted.data_ptr())
+    return {"path": path, "count": count, "tokens": emitted}
+
+
+def _pools(pools, device):
+    """The checked _CachePools of a list of tensors [pages, heads, page, dim] of one layout."""
+    first = pools[0] if pools else None
+    n = len(pools)
+    bases = (ctypes.c_void_p * max(n, 1))()
+    for i, t in enumerate(pools):
+        if not t.is_cuda or t.device != device:
+            raise ValueError("pools[%d] must be on %s" % (i, device))
+        if t.dim() != 4 or t.stride(3) != 1:
+            raise ValueError("pools[%d] must be [pages, heads, page, dim] with a contiguous last "
+                             "dimension" % i)
+        if (t.dtype != first.dtype or t.shape != first.shape
+                or t.stride() != first.stride() and _strides(t) != _strides(first)):
+            raise ValueError("pools[%d] must be laid out as pools[0]" % i)
+        bases[i] = t.data_ptr()
+    if first is None:
+        raise ValueError("pools must hold at least one tensor")
+    e = first.element_size()
+    s = _strides(first)
+    return _CachePools(ctypes.cast(bases, ctypes.c_void_p), n, first.shape[0], first.shape[2],
+                       first.shape[1], s[0] * e, s[1] * e, s[2] * e, first.shape[3] * e), bases
+
+
+def cache_keep(pools, table: torch.Tensor, lengths: torch.Tensor, path: torch.Tensor,
+               count: torch.Tensor) -> torch.Tensor:
+    """Move the accepted nodes' positions together in every pool (tensors [pages,
+    heads, page, dim] of one layout, all layers' keys and values): position
+    lengths[b] + path[b, i] to lengths[b] + i for i < count[b] (path and count as
+    tree_accept gives them).  Returns the new lengths, int32 [B]."""
+    pools = list(pools)
+    dev = table.device
+    _need_cuda(path, "path", dev, torch.int32)
+    if path.dim() != 2 or table.dim() != 2:
+        raise ValueError("path must be [B, nodes] and table [B, pages of a sequence]")
+    B, T = path.shape
+    _need_cuda(table, "table", dev, torch.int32, (B, table.shape[1]))
+    _need_cuda(lengths, "lengths", dev, torch.int32, (B,))
+    _need_cuda(count, "count", dev, torch.int32, (B,))
+    p, _bases = _pools(pools, dev)
+    new = torch.empty(B, dtype=torch.int32, device=dev)
+    _enqueue("spec_cache_keep", dev, load().spec_cache_keep, ctypes.byref(p), table.data_ptr(),
+             table.shape[1], lengths.data_ptr(), path.data_ptr(), count.data_ptr(), B, T,
+             new.data_ptr())
+    _overwritten(pools)
+    return new
+
+
+def pages_fork(table: torch.Tensor, lengths: torch.Tensor, parents: torch.Tensor,
+               refs: torch.Tensor, page_size: int, *, out: torch.Tensor) -> torch.Tensor:
+    """Fill out (int32 [B, n, P]) with rows that share their parents' pages: row
+    [b, i] lists the pages that hold row [b, parents[b, i]] of table (int32
+    [B, W, P]) up to its length (lengths int32 [B, W]), and refs (int32 [pages])
+    counts them.  What out listed before is not released.  Returns the new rows'
+    lengths, int32 [B, n]."""
+    _need_cuda(table, "table", dtype=torch.int32)
+    if table.dim() != 3 or parents.dim() != 2 or refs.dim() != 1:
+        raise ValueError("table must be [B, W, P], parents [B, n] and refs [pages]")
+    B, W, P = table.shape
+    dev, n = table.device, parents.shape[1]
+    _need_cuda(lengths, "lengths", dev, torch.int32, (B, W))
+    _need_cuda(parents, "parents", dev, torch.int32, (B, n))
+    _need_cuda(refs, "refs", dev, torch.int32)
+    _need_cuda(out, "out", dev, torch.int32, (B, n, P))
+    new = torch.empty((B, n), dtype=torch.int32, device=dev)
+    _enqueue("spec_pages_fork", dev, load().spec_pages_fork, table.data_ptr(), lengths.data_ptr(),
+             parents.data_ptr(), B, W, n, P, page_size, refs.shape[0], refs.data_ptr(),
+             out.data_ptr(), new.data_ptr())
+    _overwritten((out, refs))
+    return new
+
+
+def _table_rows(table, refs):
+    """(rows, P) of a table [..., P] beside refs [pages]."""
+    _need_cuda(table, "table", dtype=torch.int32)
+    _need_cuda(refs, "refs", table.device, torch.int32)
+    if table.dim() < 2 or refs.dim() != 1:
+        raise ValueError("table must be [..., P] and refs [pages]")
+    return math.prod(table.shape[:-1]), table.shape[-1]
+
+
+def pages_release(table: torch.Tensor, refs: torch.Tensor, page_size: int,
+                  lengths: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Drop the pages of each row of table (int32 [..., P]) behind its first lengths
+    positions (int32 [...]; None: all pages): their entries become -1 and refs
+    (int32 [pages]) goes down.  Returns table."""
+    rows, P = _table_rows(table, refs)
+    dev = table.device
+    if lengths is not None:
+        _need_cuda(lengths, "lengths", dev, torch.int32, table.shape[:-1])
+    _enqueue("spec_pages_release", dev, load().spec_pages_release, table.data_ptr(),
+             _addr(lengths), rows, P, page_size, refs.shape[0], refs.data_ptr())
+    _overwritten((table, refs))
+    return table
+
+
+@functools.lru_cache(maxsize=256)
+def _reserve_workspace_bytes(rows: int, pages: int) -> int:
+    return int(load().spec_pages_reserve_workspace_bytes(rows, pages))
+
+
+def pages_reserve(table: torch.Tensor, lengths: torch.Tensor, refs: torch.Tensor, page_size: int,
+                  new: torch.Tensor, *, workspace: Optional[torch.Tensor] = None) -> dict:
+    """Give each row of table (int32 [..., P]) pages of its own for the new
+    positions behind its lengths (both int32 [...]): free pages, lowest first, for
+    entries without one and in place of shared ones.  Returns copies (int32
+    [rows, 3]: page, its replacement, positions that pages_copy is to move; -1, -1
+    and 0 for none) and missing (int32 [1]: 0; the pages that lack, or -1 where
+    positions pass a table row, and then nothing changed)."""
+    rows, P = _table_rows(table, refs)
+    dev = table.device
+    _need_cuda(lengths, "lengths", dev, torch.int32, table.shape[:-1])
+    _need_cuda(new, "new", dev, torch.int32, table.shape[:-1])
+    copies = torch.empty((rows, 3), dtype=torch.int32, device=dev)
+    missing = torch.empty(1, dtype=torch.int32, device=dev)
+    if rows == 0:
+        missing.zero_()
+    if workspace is None:
+        n = _reserve_workspace_bytes(rows, refs.shape[0])
+        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
+    else:
+        _need_cuda(workspace, "workspace", dev)
+    _enqueue("spec_pages_reserve", dev, load().spec_pages_reserve, table.data_ptr(),
+             lengths.data_ptr(), new.data_ptr(), rows, P, page_size, refs.shape[0],
+             refs.data_ptr(), copies.data_ptr(), missing.data_ptr(), workspace.data_ptr(),
+             _nbytes(workspace))
+    _overwritten((table, refs))
+    return {"copies": copies, "missing": missing}
+
+
+def pages_copy(pools, copies: torch.Tensor) -> list:
+    """Copy pages in every pool (tensors [pages, heads, page, dim] of one layout):
+    for each row of copies (int32 [rows, 3], as pages_reserve gives them) the
+    first copies[r, 2] positions of page copies[r, 0] to page copies[r, 1].
+    Returns the pools."""
+    pools = list(pools)
+    _need_cuda(copies, "copies", dtype=torch.int32)
+    if copies.dim() != 2 or copies.shape[1] != 3:
+        raise ValueError("copies must be [rows, 3]")
+    dev = copies.device
+    p, _bases = _pools(pools, dev)
+    _enqueue("spec_pages_copy", dev, load().spec_pages_copy, ctypes.byref(p), copies.data_ptr(),
+             copies.shape[0])
+    _overwritten(pools)
+    return pools

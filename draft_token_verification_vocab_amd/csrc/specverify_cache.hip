@@ -1,0 +1,544 @@
+// specverify_cache.hip -- host side of the paged-cache calls declared in
+// include/specverify.h: tree attention, appending, accepting and keeping a
+// path, and the pages' sharing.  Argument validation, workspace layout, kernel
+// selection and launches on the caller's stream.  No allocation, no
+// synchronisation.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstddef>
+#include <cstdint>
+
+#include "specverify.h"
+#include "sv_cache.hpp"
+#include "sv_common.hpp"
+#include "sv_host.hpp"
+#include "sv_tree.hpp"
+
+namespace {
+
+using namespace sv;
+
+constexpr int kUnits = 256;            // compute units
+constexpr int kMaxChainNodes = 65536;
+constexpr int kMaxHeads = 65535;
+constexpr int kMaxRoom = 1 << 30;      // positions that a table row can hold
+constexpr int kMaxReserveRows = 65536;
+
+// A grid's threads must stay below 2^32.
+bool grid_fits(int64_t blocks, int block) {
+    return blocks <= (int64_t{1} << 32) / block - 1 && blocks <= INT32_MAX;
+}
+
+int page_shift(int32_t page_size) {
+    int s = 0;
+    while ((1 << s) < page_size) ++s;
+    return s;
+}
+
+bool page_size_ok(int32_t s) { return s >= 8 && s <= 1024 && (s & (s - 1)) == 0; }
+
+// A table row's shape, for the calls that take no pools.
+spec_status check_table(int32_t table_width, int32_t page_size, int32_t num_pages) {
+    if (table_width < 1 || num_pages < 1 || page_size < 1) return SPEC_ERR_ARG;
+    if (!page_size_ok(page_size)) return SPEC_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(table_width) * page_size > kMaxRoom) return SPEC_ERR_UNSUPPORTED;
+    return SPEC_OK;
+}
+
+bool stride_ok(int64_t bytes) { return bytes >= 0 && bytes % 16 == 0; }
+
+// Addresses [from, to).
+struct Range {
+    const char *from, *to;
+    bool meets(const Range &o) const { return from < o.to && o.from < to; }
+};
+Range range(const void *p, int64_t bytes) {
+    const char *c = static_cast<const char *>(p);
+    return Range{c, c + bytes};
+}
+
+// The largest multiple of n that fits the address arithmetic.
+constexpr int64_t kMaxStride = int64_t{1} << 40;
+
+spec_status check_cache(const spec_cache *c) {
+    if (!c || c->batch < 0 || c->reserved != 0) return SPEC_ERR_ARG;
+    if (c->dtype != SPEC_DTYPE_F32 && c->dtype != SPEC_DTYPE_BF16 && c->dtype != SPEC_DTYPE_F16)
+        return SPEC_ERR_ARG;
+    if (c->kv_heads < 1 || c->dim < 8 || c->dim % 8 != 0) return SPEC_ERR_ARG;
+    const spec_status s = check_table(c->table_width, c->page_size, c->num_pages);
+    if (s != SPEC_OK) return s;
+    const int e = elem_size(c->dtype);
+    if (c->page_stride > kMaxStride || c->head_stride > kMaxStride || c->slot_stride > kMaxStride)
+        return SPEC_ERR_UNSUPPORTED;
+    if (!stride_ok(c->page_stride * e) || !stride_ok(c->head_stride * e) ||
+        !stride_ok(c->slot_stride * e) || c->slot_stride < c->dim)
+        return SPEC_ERR_ARG;
+    if (c->dim > 256 || c->kv_heads > kMaxHeads) return SPEC_ERR_UNSUPPORTED;
+    return SPEC_OK;
+}
+
+// The bytes from a pool's base to its last element's end.
+int64_t pool_bytes(const spec_cache *c) {
+    return ((c->num_pages - 1) * c->page_stride + (c->kv_heads - 1) * c->head_stride +
+            (c->page_size - 1) * c->slot_stride + c->dim) *
+           elem_size(c->dtype);
+}
+
+bool pools_ok(const spec_cache *c) {
+    return c->keys && c->values && aligned16(c->keys) && aligned16(c->values) && c->table &&
+           c->lengths;
+}
+
+// ---------------------------------------------------------------------------
+// Tree attention
+// ---------------------------------------------------------------------------
+struct TreePlan {
+    int dp;      // dimensions, rounded up to what a kernel takes
+    int rt;      // 16-row tiles to a workgroup
+    int mtiles;
+    int slices;
+    size_t first, part, part_ml, total;  // workspace
+};
+
+spec_status check_tree(const spec_cache *c, int32_t nodes, int32_t heads, bool tree) {
+    spec_status s = check_cache(c);
+    if (s != SPEC_OK) return s;
+    if (nodes < 1 || heads < 1 || heads % c->kv_heads != 0) return SPEC_ERR_ARG;
+    if (nodes > (tree ? kMaxTreeNodes : kMaxChainNodes) || heads > kMaxHeads)
+        return SPEC_ERR_UNSUPPORTED;
+    const int64_t tiles =
+        static_cast<int64_t>(c->table_width) * c->page_size / kTreeTile + 1;
+    if (c->batch > INT32_MAX / tiles) return SPEC_ERR_UNSUPPORTED;
+    const int64_t rows = static_cast<int64_t>(c->batch) * nodes;
+    if (rows > 0 && rows > (int64_t{1} << 40) / heads) return SPEC_ERR_UNSUPPORTED;
+    if (!grid_fits(rows * heads / kTreeWaves + 1, kTreeBlock)) return SPEC_ERR_UNSUPPORTED;
+    return SPEC_OK;
+}
+
+TreePlan plan_tree(const spec_cache *c, int32_t nodes, int32_t heads) {
+    TreePlan p;
+    p.dp = c->dim <= 64 ? 64 : (c->dim <= 128 ? 128 : 256);
+    const int64_t rows = static_cast<int64_t>(nodes) * (heads / c->kv_heads);
+    p.rt = rows > 16 && p.dp <= 128 ? 2 : 1;
+    p.mtiles = static_cast<int>((rows + 16 * p.rt - 1) / (16 * p.rt));
+    const int64_t units = static_cast<int64_t>(p.mtiles) * c->kv_heads;
+    const int64_t tiles =
+        c->batch * (static_cast<int64_t>(c->table_width) * c->page_size / kTreeTile + 1);
+    int64_t slices = (4 * kUnits + units - 1) / units;
+    if (slices > tiles) slices = tiles;
+    p.slices = static_cast<int>(slices < 1 ? 1 : slices);
+    const int64_t parts = 2 * units * p.slices * 16 * p.rt;
+    p.first = 0;
+    p.part = align_up((static_cast<size_t>(c->batch) + 1) * sizeof(int32_t));
+    p.part_ml = p.part + align_up(static_cast<size_t>(parts) * c->dim * sizeof(float));
+    p.total = p.part_ml + align_up(static_cast<size_t>(parts) * 2 * sizeof(float));
+    return p;
+}
+
+template <typename T, int DP>
+void launch_tree_rt(const TreeArgs &a, const TreePlan &p, hipStream_t st) {
+    const dim3 grid(static_cast<unsigned>(p.slices * a.KV * p.mtiles));
+    if constexpr (DP <= 128) {
+        if (p.rt == 2) {
+            tree_attention_kernel<T, DP, 2><<<grid, dim3(kTreeBlock), 0, st>>>(a);
+            return;
+        }
+    }
+    tree_attention_kernel<T, DP, 1><<<grid, dim3(kTreeBlock), 0, st>>>(a);
+}
+
+template <typename T>
+void launch_tree(const TreeArgs &a, const TreePlan &p, hipStream_t st) {
+    if (p.dp == 64)
+        launch_tree_rt<T, 64>(a, p, st);
+    else if (p.dp == 128)
+        launch_tree_rt<T, 128>(a, p, st);
+    else
+        launch_tree_rt<T, 256>(a, p, st);
+}
+
+template <typename T>
+void launch_join(const TreeArgs &a, const TreePlan &p, hipStream_t st) {
+    const int64_t rows = static_cast<int64_t>(a.B) * a.T * a.H;
+    tree_join_kernel<T><<<dim3(static_cast<unsigned>((rows + kTreeWaves - 1) / kTreeWaves)),
+                          dim3(kTreeBlock), 0, st>>>(a, 16 * p.rt);
+}
+
+// ---------------------------------------------------------------------------
+// Pools
+// ---------------------------------------------------------------------------
+spec_status check_pools(const spec_cache_pools *p) {
+    if (!p || p->num_pools < 0 || p->num_pages < 1 || p->page_size < 1 || p->heads < 1 ||
+        p->slot_bytes < 1)
+        return SPEC_ERR_ARG;
+    if (p->page_stride > kMaxStride || p->head_stride > kMaxStride || p->slot_stride > kMaxStride)
+        return SPEC_ERR_UNSUPPORTED;
+    if (!stride_ok(p->page_stride) || !stride_ok(p->head_stride) || !stride_ok(p->slot_stride) ||
+        p->slot_bytes % 16 != 0 || p->slot_stride < p->slot_bytes)
+        return SPEC_ERR_ARG;
+    if (!page_size_ok(p->page_size) || p->heads > kMaxHeads || p->slot_bytes > 65536)
+        return SPEC_ERR_UNSUPPORTED;
+    if (p->num_pools > 0 && !p->bases) return SPEC_ERR_ARG;
+    for (int i = 0; i < p->num_pools; ++i)
+        if (!p->bases[i] || !aligned16(p->bases[i])) return SPEC_ERR_ARG;
+    return SPEC_OK;
+}
+
+// Pools [first, first + count) as a kernel takes them.
+PoolArgs pool_args(const spec_cache_pools *p, int first, int count) {
+    PoolArgs a{};
+    for (int i = 0; i < count; ++i) a.base[i] = static_cast<char *>(p->bases[first + i]);
+    a.page_stride = p->page_stride;
+    a.head_stride = p->head_stride;
+    a.slot_stride = p->slot_stride;
+    a.count = count;
+    a.heads = p->heads;
+    a.units = static_cast<int32_t>(p->slot_bytes / 16);
+    a.pages = p->num_pages;
+    a.shift = page_shift(p->page_size);
+    return a;
+}
+
+size_t reserve_words(int32_t num_pages) {
+    return static_cast<size_t>((num_pages + kPageChunk - 1) / kPageChunk) * (kPageChunk / kWave);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t spec_tree_attention_workspace_bytes(const spec_cache *cache, int32_t nodes,
+                                           int32_t heads) {
+    if (check_tree(cache, nodes, heads, false) != SPEC_OK || cache->batch == 0) return 0;
+    return plan_tree(cache, nodes, heads).total;
+}
+
+spec_status spec_tree_attention(const spec_cache *cache, const void *q, int64_t q_batch_stride,
+                                int64_t q_node_stride, int64_t q_head_stride, int32_t nodes,
+                                int32_t heads, const int32_t *parents, const int32_t *num_nodes,
+                                float scale, void *out, float *lse, void *workspace,
+                                size_t workspace_bytes, void *stream) {
+    const spec_status s = check_tree(cache, nodes, heads, parents != nullptr);
+    if (s != SPEC_OK) return s;
+    if (!(scale > 0.0f) || !std::isfinite(scale)) return SPEC_ERR_ARG;
+    const int e = elem_size(cache->dtype);
+    if (q_batch_stride > kMaxStride || q_node_stride > kMaxStride || q_head_stride > kMaxStride)
+        return SPEC_ERR_UNSUPPORTED;
+    if (!stride_ok(q_batch_stride * e) || !stride_ok(q_node_stride * e) ||
+        !stride_ok(q_head_stride * e))
+        return SPEC_ERR_ARG;
+    if (cache->batch == 0) return SPEC_OK;
+    if (!pools_ok(cache) || !q || !aligned16(q) || !out || !aligned16(out)) return SPEC_ERR_ARG;
+    const int64_t rows = static_cast<int64_t>(cache->batch) * nodes * heads;
+    const Range to = range(out, rows * cache->dim * e);
+    const Range sums = range(lse, lse ? rows * static_cast<int64_t>(sizeof(float)) : 0);
+    const Range in[] = {
+        range(cache->keys, pool_bytes(cache)), range(cache->values, pool_bytes(cache)),
+        range(q, ((cache->batch - 1) * q_batch_stride + (nodes - 1) * q_node_stride +
+                  (heads - 1) * q_head_stride + cache->dim) *
+                     e)};
+    for (const Range &r : in)
+        if (to.meets(r) || (lse && sums.meets(r))) return SPEC_ERR_ARG;
+    if (lse && to.meets(sums)) return SPEC_ERR_ARG;
+    const TreePlan p = plan_tree(cache, nodes, heads);
+    if (!grid_fits(static_cast<int64_t>(p.slices) * cache->kv_heads * p.mtiles, kTreeBlock))
+        return SPEC_ERR_UNSUPPORTED;
+    if (!workspace || workspace_bytes < p.total) return SPEC_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return SPEC_ERR_ARG;
+    char *w = static_cast<char *>(workspace);
+    TreeArgs a{};
+    a.keys = cache->keys;
+    a.values = cache->values;
+    a.q = q;
+    a.out = out;
+    a.lse = lse;
+    a.table = cache->table;
+    a.lengths = cache->lengths;
+    a.nodes = num_nodes;
+    a.parents = parents;
+    a.first = reinterpret_cast<int32_t *>(w + p.first);
+    a.part = reinterpret_cast<float *>(w + p.part);
+    a.part_ml = reinterpret_cast<float *>(w + p.part_ml);
+    a.page_stride = cache->page_stride;
+    a.head_stride = cache->head_stride;
+    a.slot_stride = cache->slot_stride;
+    a.q_batch = q_batch_stride;
+    a.q_node = q_node_stride;
+    a.q_head = q_head_stride;
+    a.B = cache->batch;
+    a.T = nodes;
+    a.H = heads;
+    a.KV = cache->kv_heads;
+    a.G = heads / cache->kv_heads;
+    a.D = cache->dim;
+    a.P = cache->table_width;
+    a.pages = cache->num_pages;
+    a.shift = page_shift(cache->page_size);
+    a.slices = p.slices;
+    a.mtiles = p.mtiles;
+    a.scale2 = scale * kLog2e;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (cache->dtype == SPEC_DTYPE_BF16)
+        launch_tree<__bf16>(a, p, st);
+    else if (cache->dtype == SPEC_DTYPE_F16)
+        launch_tree<_Float16>(a, p, st);
+    else
+        launch_tree<float>(a, p, st);
+    const spec_status r = launch_status();
+    if (r != SPEC_OK || p.slices == 1) return r;
+    if (cache->dtype == SPEC_DTYPE_BF16)
+        launch_join<__bf16>(a, p, st);
+    else if (cache->dtype == SPEC_DTYPE_F16)
+        launch_join<_Float16>(a, p, st);
+    else
+        launch_join<float>(a, p, st);
+    return launch_status();
+}
+
+spec_status spec_cache_append(const spec_cache *cache, const void *k, const void *v,
+                              int64_t batch_stride, int64_t node_stride, int64_t head_stride,
+                              int32_t nodes, const int32_t *num_nodes, void *stream) {
+    const spec_status s = check_cache(cache);
+    if (s != SPEC_OK) return s;
+    const int e = elem_size(cache->dtype);
+    if (nodes < 0) return SPEC_ERR_ARG;
+    if (batch_stride > kMaxStride || node_stride > kMaxStride || head_stride > kMaxStride ||
+        nodes > kMaxRoom)
+        return SPEC_ERR_UNSUPPORTED;
+    if (!stride_ok(batch_stride * e) || !stride_ok(node_stride * e) || !stride_ok(head_stride * e))
+        return SPEC_ERR_ARG;
+    if (cache->batch == 0 || nodes == 0) return SPEC_OK;
+    if (!pools_ok(cache) || !k || !v || !aligned16(k) || !aligned16(v)) return SPEC_ERR_ARG;
+    const int64_t span = ((cache->batch - 1) * batch_stride + (nodes - 1) * node_stride +
+                          (cache->kv_heads - 1) * head_stride + cache->dim) *
+                         e;
+    const Range pools[] = {range(cache->keys, pool_bytes(cache)),
+                           range(cache->values, pool_bytes(cache))};
+    for (const Range &r : pools)
+        if (r.meets(range(k, span)) || r.meets(range(v, span))) return SPEC_ERR_ARG;
+    AppendArgs a{};
+    a.k = static_cast<const char *>(k);
+    a.v = static_cast<const char *>(v);
+    a.keys = static_cast<char *>(cache->keys);
+    a.values = static_cast<char *>(cache->values);
+    a.table = cache->table;
+    a.lengths = cache->lengths;
+    a.nodes = num_nodes;
+    a.batch_stride = batch_stride * e;
+    a.node_stride = node_stride * e;
+    a.k_head_stride = head_stride * e;
+    a.page_stride = cache->page_stride * e;
+    a.head_stride = cache->head_stride * e;
+    a.slot_stride = cache->slot_stride * e;
+    a.T = nodes;
+    a.P = cache->table_width;
+    a.heads = cache->kv_heads;
+    a.units = cache->dim * e / 16;
+    a.pages = cache->num_pages;
+    a.shift = page_shift(cache->page_size);
+    const int64_t blocks =
+        (static_cast<int64_t>(nodes) * a.heads * a.units + kCacheBlock - 1) / kCacheBlock;
+    if (blocks > INT32_MAX / cache->batch || !grid_fits(blocks * cache->batch, kCacheBlock))
+        return SPEC_ERR_UNSUPPORTED;
+    a.blocks = static_cast<int32_t>(blocks);
+    cache_append_kernel<<<dim3(static_cast<unsigned>(blocks * cache->batch)), dim3(kCacheBlock),
+                          0, static_cast<hipStream_t>(stream)>>>(a);
+    return launch_status();
+}
+
+spec_status spec_tree_accept(const int32_t *parents, const int32_t *tokens,
+                             const int32_t *chosen, const int32_t *num_nodes, int32_t batch,
+                             int32_t nodes, int32_t *path, int32_t *count, int32_t *emitted,
+                             void *stream) {
+    if (batch < 0 || nodes < 1) return SPEC_ERR_ARG;
+    if (nodes > kMaxAcceptNodes) return SPEC_ERR_UNSUPPORTED;
+    if (batch == 0) return SPEC_OK;
+    if (!parents || !tokens || !chosen || !path || !count || !emitted) return SPEC_ERR_ARG;
+    AcceptArgs a{};
+    a.parents = parents;
+    a.tokens = tokens;
+    a.chosen = chosen;
+    a.nodes = num_nodes;
+    a.path = path;
+    a.count = count;
+    a.emitted = emitted;
+    a.B = batch;
+    a.T = nodes;
+    constexpr int per = kCacheBlock / kWave;
+    const int64_t blocks = (static_cast<int64_t>(batch) + per - 1) / per;
+    if (!grid_fits(blocks, kCacheBlock)) return SPEC_ERR_UNSUPPORTED;
+    tree_accept_kernel<<<dim3(static_cast<unsigned>(blocks)), dim3(kCacheBlock), 0,
+                         static_cast<hipStream_t>(stream)>>>(a);
+    return launch_status();
+}
+
+spec_status spec_cache_keep(const spec_cache_pools *pools, const int32_t *table,
+                            int32_t table_width, const int32_t *lengths, const int32_t *path,
+                            const int32_t *count, int32_t batch, int32_t nodes,
+                            int32_t *new_lengths, void *stream) {
+    spec_status s = check_pools(pools);
+    if (s != SPEC_OK) return s;
+    if ((s = check_table(table_width, pools->page_size, pools->num_pages)) != SPEC_OK) return s;
+    if (batch < 0 || nodes < 1) return SPEC_ERR_ARG;
+    if (nodes > kMaxKeepNodes) return SPEC_ERR_UNSUPPORTED;
+    if (batch == 0) return SPEC_OK;
+    if (!table || !lengths || !path || !count || !new_lengths) return SPEC_ERR_ARG;
+    const Range to = range(new_lengths, int64_t{batch} * 4);
+    if (to.meets(range(lengths, int64_t{batch} * 4)) || to.meets(range(count, int64_t{batch} * 4)) ||
+        to.meets(range(path, int64_t{batch} * nodes * 4)) ||
+        to.meets(range(table, int64_t{batch} * table_width * 4)))
+        return SPEC_ERR_ARG;
+    KeepArgs a{};
+    a.table = table;
+    a.lengths = lengths;
+    a.path = path;
+    a.count = count;
+    a.T = nodes;
+    a.P = table_width;
+    const int64_t column = static_cast<int64_t>(pools->heads) * (pools->slot_bytes / 16);
+    int step = kMaxPools;
+    const int64_t most = (int64_t{1} << 30) / batch;  // workgroups per sequence
+    while (step > 1 && column * step / kCacheBlock + 1 > most) step /= 2;
+    if (column * step / kCacheBlock + 1 > most ||
+        !grid_fits((column * step / kCacheBlock + 1) * batch, kCacheBlock))
+        return SPEC_ERR_UNSUPPORTED;
+    for (int first = 0; first == 0 || first < pools->num_pools; first += step) {
+        const int n = pools->num_pools - first < step ? pools->num_pools - first : step;
+        a.pool = pool_args(pools, first, n);
+        a.new_lengths = first == 0 ? new_lengths : nullptr;
+        a.blocks = static_cast<int32_t>((column * n + kCacheBlock - 1) / kCacheBlock);
+        if (a.blocks < 1) a.blocks = 1;  // no pools: the lengths alone
+        cache_keep_kernel<<<dim3(static_cast<unsigned>(a.blocks * batch)), dim3(kCacheBlock), 0,
+                            static_cast<hipStream_t>(stream)>>>(a);
+        if ((s = launch_status()) != SPEC_OK) return s;
+    }
+    return SPEC_OK;
+}
+
+spec_status spec_pages_fork(const int32_t *table, const int32_t *lengths, const int32_t *parents,
+                            int32_t batch, int32_t num_beams, int32_t num_out,
+                            int32_t table_width, int32_t page_size, int32_t num_pages,
+                            int32_t *refs, int32_t *out_table, int32_t *out_lengths,
+                            void *stream) {
+    const spec_status s = check_table(table_width, page_size, num_pages);
+    if (s != SPEC_OK) return s;
+    if (batch < 0 || num_beams < 1 || num_out < 1) return SPEC_ERR_ARG;
+    if (batch == 0) return SPEC_OK;
+    if (!table || !lengths || !parents || !refs || !out_table || !out_lengths) return SPEC_ERR_ARG;
+    const int64_t rows = static_cast<int64_t>(batch) * num_out;
+    const int64_t from = static_cast<int64_t>(batch) * num_beams;
+    if (!grid_fits(rows, kCacheBlock) || from > INT32_MAX) return SPEC_ERR_UNSUPPORTED;
+    const Range to[] = {range(out_table, rows * table_width * 4), range(out_lengths, rows * 4),
+                        range(refs, int64_t{num_pages} * 4)};
+    const Range in[] = {range(table, from * table_width * 4), range(lengths, from * 4),
+                        range(parents, rows * 4)};
+    for (const Range &t : to)
+        for (const Range &i : in)
+            if (t.meets(i)) return SPEC_ERR_ARG;
+    if (to[0].meets(to[1]) || to[0].meets(to[2]) || to[1].meets(to[2])) return SPEC_ERR_ARG;
+    ForkArgs a{};
+    a.table = table;
+    a.lengths = lengths;
+    a.parents = parents;
+    a.refs = refs;
+    a.out = out_table;
+    a.out_lengths = out_lengths;
+    a.W = num_beams;
+    a.n = num_out;
+    a.P = table_width;
+    a.shift = page_shift(page_size);
+    a.pages = num_pages;
+    pages_fork_kernel<<<dim3(static_cast<unsigned>(rows)), dim3(kCacheBlock), 0,
+                        static_cast<hipStream_t>(stream)>>>(a);
+    return launch_status();
+}
+
+spec_status spec_pages_release(int32_t *table, const int32_t *lengths, int32_t rows,
+                               int32_t table_width, int32_t page_size, int32_t num_pages,
+                               int32_t *refs, void *stream) {
+    const spec_status s = check_table(table_width, page_size, num_pages);
+    if (s != SPEC_OK) return s;
+    if (rows < 0) return SPEC_ERR_ARG;
+    if (rows == 0) return SPEC_OK;
+    if (!table || !refs) return SPEC_ERR_ARG;
+    if (!grid_fits(rows, kCacheBlock)) return SPEC_ERR_UNSUPPORTED;
+    ReleaseArgs a{};
+    a.table = table;
+    a.refs = refs;
+    a.lengths = lengths;
+    a.P = table_width;
+    a.shift = page_shift(page_size);
+    a.pages = num_pages;
+    pages_release_kernel<<<dim3(static_cast<unsigned>(rows)), dim3(kCacheBlock), 0,
+                           static_cast<hipStream_t>(stream)>>>(a);
+    return launch_status();
+}
+
+size_t spec_pages_reserve_workspace_bytes(int32_t rows, int32_t num_pages) {
+    if (rows < 1 || num_pages < 1 || rows > kMaxReserveRows || num_pages > kMaxReservePages)
+        return 0;
+    return align_up(reserve_words(num_pages) * 8) +
+           align_up(reserve_words(num_pages) / (kPageChunk / kWave) * 4);
+}
+
+spec_status spec_pages_reserve(int32_t *table, const int32_t *lengths,
+                               const int32_t *new_positions, int32_t rows, int32_t table_width,
+                               int32_t page_size, int32_t num_pages, int32_t *refs,
+                               int32_t *copies, int32_t *missing, void *workspace,
+                               size_t workspace_bytes, void *stream) {
+    const spec_status s = check_table(table_width, page_size, num_pages);
+    if (s != SPEC_OK) return s;
+    if (rows < 0) return SPEC_ERR_ARG;
+    if (rows > kMaxReserveRows || num_pages > kMaxReservePages) return SPEC_ERR_UNSUPPORTED;
+    if (rows == 0) return SPEC_OK;
+    if (!table || !lengths || !new_positions || !refs || !copies || !missing) return SPEC_ERR_ARG;
+    if (!workspace || workspace_bytes < spec_pages_reserve_workspace_bytes(rows, num_pages))
+        return SPEC_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return SPEC_ERR_ARG;
+    char *w = static_cast<char *>(workspace);
+    ReserveArgs a{};
+    a.table = table;
+    a.refs = refs;
+    a.copies = copies;
+    a.missing = missing;
+    a.lengths = lengths;
+    a.news = new_positions;
+    a.words = reinterpret_cast<unsigned long long *>(w);
+    a.counts = reinterpret_cast<int32_t *>(w + align_up(reserve_words(num_pages) * 8));
+    a.rows = rows;
+    a.P = table_width;
+    a.shift = page_shift(page_size);
+    a.pages = num_pages;
+    a.chunks = (num_pages + kPageChunk - 1) / kPageChunk;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    pages_free_kernel<<<dim3(static_cast<unsigned>(a.chunks)), dim3(kCacheBlock), 0, st>>>(a);
+    const spec_status r = launch_status();
+    if (r != SPEC_OK) return r;
+    pages_reserve_kernel<<<dim3(1), dim3(kReserveBlock), 0, st>>>(a);
+    return launch_status();
+}
+
+spec_status spec_pages_copy(const spec_cache_pools *pools, const int32_t *copies, int32_t rows,
+                            void *stream) {
+    spec_status s = check_pools(pools);
+    if (s != SPEC_OK) return s;
+    if (rows < 0) return SPEC_ERR_ARG;
+    if (rows == 0 || pools->num_pools == 0) return SPEC_OK;
+    if (!copies) return SPEC_ERR_ARG;
+    CopyArgs a{};
+    a.copies = copies;
+    int step = kMaxPools;
+    while (step > 1 && !grid_fits(int64_t{rows} * pools->heads * step, kCacheBlock)) step /= 2;
+    if (!grid_fits(int64_t{rows} * pools->heads * step, kCacheBlock)) return SPEC_ERR_UNSUPPORTED;
+    for (int first = 0; first < pools->num_pools; first += step) {
+        const int n = pools->num_pools - first < step ? pools->num_pools - first : step;
+        a.pool = pool_args(pools, first, n);
+        pages_copy_kernel<<<dim3(static_cast<unsigned>(rows * pools->heads * n)),
+                            dim3(kCacheBlock), 0, static_cast<hipStream_t>(stream)>>>(a);
+        if ((s = launch_status()) != SPEC_OK) return s;
+    }
+    return SPEC_OK;
+}
+
+}  // extern "C"

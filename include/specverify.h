@@ -1,7 +1,9 @@
 /*
  * specverify.h -- C ABI of an MI355X (gfx950) library for batched
  * speculative-decoding verification over full-vocabulary logits, and for what
- * a draft model needs beside it (top-logit lists, distillation, beam search).
+ * a draft model needs beside it (top-logit lists, distillation, beam search),
+ * and for the paged cache that the passes before it read (attention of a tree of
+ * new tokens, and the cache's upkeep).
  *
  * The method comes from three pages:
  *   [SD]  "Speculative Decoding: как черновая модель ускоряет генерацию LLM
@@ -70,7 +72,8 @@ typedef enum spec_status {
     SPEC_ERR_HIP = -4          /* a HIP launch reported an error              */
 } spec_status;
 
-enum { SPEC_DTYPE_F32 = 0, SPEC_DTYPE_BF16 = 1 };
+enum { SPEC_DTYPE_F32 = 0, SPEC_DTYPE_BF16 = 1,
+       SPEC_DTYPE_F16 = 2 /* the paged-cache calls only */ };
 enum { SPEC_MODE_LOSSLESS = 0, SPEC_MODE_FLY = 1 };
 
 /* Problem description.  B sequences, each with K draft tokens, K draft rows
@@ -581,6 +584,193 @@ typedef struct spec_beam_state {
 spec_status spec_beam_reorder(const int32_t *parents, const int32_t *lengths, int32_t batch,
                               int32_t num_beams, int32_t num_out, const spec_beam_state *states,
                               int32_t num_states, void *stream);
+
+/*
+ * Paged-cache calls
+ * -----------------
+ * The passes that make the logits read a cache of keys and values kept in
+ * pages: a pool holds one layer's keys (or values) as num_pages pages of
+ * kv_heads x page_size slots of dim elements, and each sequence lists its pages
+ * in a row of a table.  Position p of sequence b is slot p % page_size of page
+ * table[b][p / page_size].  A table entry outside [0, num_pages) (-1) holds
+ * nothing: its positions are not read and not written.  New tokens of a step
+ * (nodes) take the positions behind the cached ones, node j position
+ * lengths[b] + j.  Nodes form a chain (node j follows node j - 1) or a tree
+ * (parents[b][j] is the node that node j follows, -1 for none; an entry that
+ * does not precede its node counts as -1).  num_nodes (device int32 [batch] or
+ * NULL = nodes) says how many nodes a sequence uses; values are clamped to
+ * [0, nodes], and lengths to what the table row can hold.
+ *
+ * page_size is a power of two from 8 to 1024, kv_heads <= 65535, and table_width
+ * * page_size <= 2^30, else SPEC_ERR_UNSUPPORTED.
+ */
+typedef struct spec_cache {
+    void *keys;           /* device, 16-byte aligned                          */
+    void *values;         /* device, 16-byte aligned, laid out as keys        */
+    int64_t page_stride;  /* elements between pages, heads and slots; each a  */
+    int64_t head_stride;  /* multiple of 16 bytes, >= 0; a slot's elements    */
+    int64_t slot_stride;  /* are consecutive, slot_stride >= dim              */
+    const int32_t *table;   /* device [batch][table_width]                    */
+    const int32_t *lengths; /* device [batch]: cached positions               */
+    int32_t batch;        /* >= 0                                             */
+    int32_t num_pages;    /* >= 1                                             */
+    int32_t page_size;
+    int32_t table_width;  /* >= 1                                             */
+    int32_t kv_heads;     /* >= 1                                             */
+    int32_t dim;          /* a multiple of 8, 8 <= dim <= 256                 */
+    int32_t dtype;        /* SPEC_DTYPE_F32, _BF16 or _F16                    */
+    int32_t reserved;     /* must be 0                                        */
+} spec_cache;
+
+/*
+ * spec_tree_attention -- attention of the new nodes over the cache: for node i
+ * of sequence b and query head h, with g = h / (heads / kv_heads),
+ *   out = sum_p e^(s_p - lse) v_p,  s_p = scale q.k_p,  lse = ln sum_p e^s_p
+ * over key head g's cached positions and node i's own and its ancestors'
+ * positions (spec_cache_append writes them first).  Keys, values or scores of
+ * positions that a node does not see do not enter, whatever they hold.
+ *   q        device, elements of cache->dtype: node i's head h of sequence b
+ *            starts at q + b*q_batch_stride + i*q_node_stride + h*q_head_stride
+ *            (elements; multiples of 16 bytes, >= 0; q 16-byte aligned).
+ *   parents  device int32 [batch][nodes], or NULL for a chain.  A tree has at
+ *            most 128 nodes, a chain at most 65536, else SPEC_ERR_UNSUPPORTED.
+ *   scale    finite and > 0.
+ *   out      device [batch][nodes][heads][dim], cache->dtype, 16-byte aligned.
+ *   lse      device float [batch][nodes][heads] or NULL.
+ * A node that is not in use, or that sees nothing (its scores -inf throughout
+ * counts as nothing), has out 0 and lse -inf.  Sums and products are taken in
+ * 32 bits; for 16-bit types the weights are rounded to the type before their
+ * product with the values.  out and lse overlap no input.  workspace: device,
+ * spec_tree_attention_workspace_bytes (0 if the arguments are not valid),
+ * 16-byte aligned; its contents on entry do not matter.
+ */
+size_t spec_tree_attention_workspace_bytes(const spec_cache *cache, int32_t nodes, int32_t heads);
+spec_status spec_tree_attention(const spec_cache *cache, const void *q, int64_t q_batch_stride,
+                                int64_t q_node_stride, int64_t q_head_stride, int32_t nodes,
+                                int32_t heads, const int32_t *parents, const int32_t *num_nodes,
+                                float scale, void *out, float *lse, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
+/*
+ * spec_cache_append -- writes the nodes' keys and values to their positions.
+ * k, v: device, elements of cache->dtype, node j's key head h of sequence b at
+ * b*batch_stride + j*node_stride + h*head_stride of each (elements; multiples
+ * of 16 bytes, >= 0; 16-byte aligned).  Positions past the table row are
+ * dropped.  Rows of a table that share a page must not both write to it
+ * (spec_pages_reserve sees to that).
+ */
+spec_status spec_cache_append(const spec_cache *cache, const void *k, const void *v,
+                              int64_t batch_stride, int64_t node_stride, int64_t head_stride,
+                              int32_t nodes, const int32_t *num_nodes, void *stream);
+
+/*
+ * spec_tree_accept -- the path of a drafted tree that the target agrees with.
+ * Node 0 (the last emitted token) is accepted; from an accepted node i the next
+ * one is its lowest child c with tokens[b][c] == chosen[b][i], as long as there
+ * is one.  With chosen[b][i] the target's top token after node i this is strict
+ * greedy verification of a tree; with a sample from the target's distribution
+ * there, the emitted tokens are distributed as the target's own ([SD] section
+ * "Математика верификации" for the chain).
+ *   parents, tokens, chosen  device int32 [batch][nodes].
+ * Outputs (device int32): path [batch][nodes], the accepted nodes in order,
+ * ascending; count [batch], how many (0 for a sequence without nodes);
+ * emitted [batch][nodes], the accepted children's tokens and then the target's
+ * choice after the last one; path and emitted hold count[b] entries, then -1.
+ * 1 <= nodes <= 128, else SPEC_ERR_UNSUPPORTED.
+ */
+spec_status spec_tree_accept(const int32_t *parents, const int32_t *tokens,
+                             const int32_t *chosen, const int32_t *num_nodes, int32_t batch,
+                             int32_t nodes, int32_t *path, int32_t *count, int32_t *emitted,
+                             void *stream);
+
+/* Pools of one shape, for the calls that move positions or pages of all layers
+ * at once.  Sizes and strides in bytes; bases, strides and slot_bytes are
+ * multiples of 16. */
+typedef struct spec_cache_pools {
+    void *const *bases;   /* host array of num_pools device addresses         */
+    int32_t num_pools;    /* >= 0                                             */
+    int32_t num_pages;
+    int32_t page_size;
+    int32_t heads;
+    int64_t page_stride;
+    int64_t head_stride;
+    int64_t slot_stride;
+    int64_t slot_bytes;   /* <= 65536                                         */
+} spec_cache_pools;
+
+/*
+ * spec_cache_keep -- after verification: moves the accepted nodes' positions
+ * together, in every pool: position lengths[b] + path[b][i] goes to
+ * lengths[b] + i for i < count[b].  path: device int32 [batch][nodes],
+ * ascending within [0, nodes) as spec_tree_accept gives it (the first entry
+ * that is not ends the list); count: device int32 [batch].  new_lengths
+ * (device int32 [batch], apart from the inputs): lengths[b] plus the entries
+ * kept, at most what the table row can hold.  A move from or to a position without a page is left out.  Rows of a
+ * table that share a page must not both move into it.  nodes <= 1024.
+ */
+spec_status spec_cache_keep(const spec_cache_pools *pools, const int32_t *table,
+                            int32_t table_width, const int32_t *lengths, const int32_t *path,
+                            const int32_t *count, int32_t batch, int32_t nodes,
+                            int32_t *new_lengths, void *stream);
+
+/*
+ * Pages are shared by reference counts: refs (device int32 [num_pages]) holds
+ * how many table entries list a page, and a page with refs <= 0 is free.  The
+ * calls change refs in place, so calls on one refs array are to be ordered by
+ * their stream.  Table entries outside [0, num_pages) are passed over.
+ *
+ * spec_pages_fork -- new table rows that share their parents' pages, for
+ * sequences that branch: for row [b][i] of out_table [batch][num_out][width],
+ * parent w = parents[b][i] of table [batch][num_beams][width]: the entries
+ * that hold its lengths[b][w] positions, then -1; their refs go up by one each;
+ * out_lengths[b][i] = lengths[b][w].  A parent outside [0, num_beams) gives
+ * an empty row of length 0.  What out_table's rows listed before is
+ * overwritten, not released.  Outputs overlap no input.
+ */
+spec_status spec_pages_fork(const int32_t *table, const int32_t *lengths, const int32_t *parents,
+                            int32_t batch, int32_t num_beams, int32_t num_out,
+                            int32_t table_width, int32_t page_size, int32_t num_pages,
+                            int32_t *refs, int32_t *out_table, int32_t *out_lengths,
+                            void *stream);
+
+/* spec_pages_release -- drops the pages of each row of table [rows][width]
+ * behind its first lengths[row] positions (NULL: all of them): refs goes down by
+ * one (not below 0) and the entry becomes -1. */
+spec_status spec_pages_release(int32_t *table, const int32_t *lengths, int32_t rows,
+                               int32_t table_width, int32_t page_size, int32_t num_pages,
+                               int32_t *refs, void *stream);
+
+/*
+ * spec_pages_reserve -- pages for the positions lengths[r] ..
+ * lengths[r] + new_positions[r] - 1 of each row r that no other row holds:
+ *   - an entry without a page takes a free one (refs 1);
+ *   - an entry whose page is shared (refs > 1) is replaced by a free page, and
+ *     the shared one's refs goes down by one; where all of a shared page's
+ *     holders are entries of this call, the first of them keeps it;
+ *   - other entries stay.
+ * Free pages are taken lowest first, by rows in order and positions in order.
+ * copies (device int32 [rows][3]): where a replaced page holds positions below
+ * lengths[r], its index, its replacement's, and their number (for
+ * spec_pages_copy); (-1, -1, 0) otherwise.  missing (device int32 [1]): 0, or,
+ * where the free pages do not suffice, how many lack, or -1 where a row's
+ * positions pass its table row; then nothing is taken or changed and copies
+ * are (-1, -1, 0).  workspace: device, spec_pages_reserve_workspace_bytes,
+ * 16-byte aligned; its contents on entry do not matter.  rows <= 65536, else
+ * SPEC_ERR_UNSUPPORTED.
+ */
+size_t spec_pages_reserve_workspace_bytes(int32_t rows, int32_t num_pages);
+spec_status spec_pages_reserve(int32_t *table, const int32_t *lengths,
+                               const int32_t *new_positions, int32_t rows, int32_t table_width,
+                               int32_t page_size, int32_t num_pages, int32_t *refs,
+                               int32_t *copies, int32_t *missing, void *workspace,
+                               size_t workspace_bytes, void *stream);
+
+/* spec_pages_copy -- in every pool, the first copies[r][2] positions of page
+ * copies[r][0] to page copies[r][1] (device int32 [rows][3]), for all rows whose
+ * pages lie in [0, num_pages).  No page is the destination of two rows, or of
+ * one and the source of another. */
+spec_status spec_pages_copy(const spec_cache_pools *pools, const int32_t *copies, int32_t rows,
+                            void *stream);
 
 /*
  * spec_read_probe -- a measurement aid, not part of verification: streams

@@ -1,0 +1,267 @@
+"""Host-side argument checks of the paged-cache calls (every refusal happens
+before any GPU work, so no GPU is needed), and the definitions that the GPU
+results are checked against, on cases worked out by hand."""
+import ctypes
+import math
+import os
+
+import numpy as np
+import pytest
+import torch
+
+import draft_token_verification_vocab_amd as sv
+from oracle import cache_ref as ref
+
+# fake device addresses that host-side validation must reject
+host_only = pytest.mark.skipif(torch.cuda.is_available(),
+                               reason="fake device pointers: host-only validation test")
+P = ctypes.c_void_p
+FAR = 1 << 44  # an address that no fake buffer below reaches
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not os.path.exists(sv.lib_path()):
+        from draft_token_verification_vocab_amd import build
+        build.build()
+    return sv.load()
+
+
+def cache(**kw):
+    base = dict(keys=FAR, values=2 * FAR, page_stride=4096, head_stride=1024, slot_stride=64,
+                table=16, lengths=16, batch=2, num_pages=10, page_size=16, table_width=5,
+                kv_heads=4, dim=64, dtype=1, reserved=0)
+    base.update(kw)
+    return sv._Cache(*[base[n] for n, _ in sv._Cache._fields_])
+
+
+BAD_CACHE = [
+    (dict(batch=-1), -1), (dict(reserved=1), -1), (dict(dtype=3), -1), (dict(dtype=-1), -1),
+    (dict(kv_heads=0), -1), (dict(dim=0), -1), (dict(dim=4), -1), (dict(dim=60), -1),
+    (dict(dim=264, slot_stride=264), -2), (dict(num_pages=0), -1), (dict(table_width=0), -1),
+    (dict(page_size=0), -1), (dict(page_size=4), -2), (dict(page_size=12), -2),
+    (dict(page_size=2048), -2), (dict(table_width=1 << 28), -2), (dict(slot_stride=63), -1),
+    (dict(slot_stride=56), -1), (dict(page_stride=4100), -1), (dict(head_stride=-8), -1),
+    (dict(page_stride=1 << 41), -2), (dict(keys=None), -1), (dict(values=None), -1),
+    (dict(keys=FAR + 8), -1), (dict(table=None), -1), (dict(lengths=None), -1)]
+
+
+@host_only
+@pytest.mark.parametrize("kw,status", BAD_CACHE, ids=str)
+def test_bad_caches(L, kw, status):
+    c = cache(**kw)
+    assert L.spec_tree_attention(ctypes.byref(c), P(16), 1024, 512, 64, 3, 8, None, None, 1.0,
+                                 P(4 * FAR), None, P(16), 1 << 40, None) == status
+    assert L.spec_cache_append(ctypes.byref(c), P(16), P(16), 1024, 512, 64, 3, None,
+                               None) == status
+
+
+@host_only
+def test_tree_attention_validates_on_host(L):
+    def call(c=None, q=P(16), sb=1024, sn=512, sh=64, T=3, H=8, parents=None, scale=1.0,
+             out=P(4 * FAR), lse=None, ws=P(16), n=1 << 40, null=False, **kw):
+        c = cache(**kw)
+        return L.spec_tree_attention(None if null else ctypes.byref(c), q, sb, sn, sh, T, H,
+                                     parents, None, scale, out, lse, ws, n, None)
+    for kw in (dict(null=True), dict(T=0), dict(H=0), dict(H=6), dict(scale=0.0),
+               dict(scale=-1.0), dict(scale=math.nan), dict(scale=math.inf), dict(q=None),
+               dict(q=P(8)), dict(sb=1028), dict(sn=-8), dict(sh=60), dict(out=None),
+               dict(out=P(4 * FAR + 8)), dict(ws=P(8)), dict(out=P(FAR + 64)),
+               dict(out=P(2 * FAR)), dict(out=P(4096), q=P(4096)),
+               dict(lse=P(4 * FAR)), dict(lse=P(2 * FAR + 4))):
+        assert call(**kw) == -1, kw
+    for kw in (dict(T=129, parents=P(16)), dict(T=65537), dict(H=65540), dict(batch=2 ** 31 - 1),
+               dict(sb=1 << 41)):
+        assert call(**kw) == -2, kw
+    for kw in (dict(ws=None), dict(n=64)):
+        assert call(**kw) == -3, kw
+    assert call(batch=0, keys=None, values=None, table=None, lengths=None, q=None, out=None,
+                ws=None, n=0) == 0
+
+
+def test_tree_workspace(L):
+    def need(T=3, H=8, **kw):
+        return L.spec_tree_attention_workspace_bytes(ctypes.byref(cache(**kw)), T, H)
+    assert need() > 0 and need() % 256 == 0
+    assert need(batch=0) == 0 and need(T=0) == 0 and need(H=6) == 0 and need(page_size=12) == 0
+    assert L.spec_tree_attention_workspace_bytes(None, 3, 8) == 0
+
+
+@host_only
+def test_append_validates_on_host(L):
+    def call(k=P(16), v=P(16), sb=1024, sn=512, sh=64, T=3, null=False, **kw):
+        c = cache(**kw)
+        return L.spec_cache_append(None if null else ctypes.byref(c), k, v, sb, sn, sh, T, None,
+                                   None)
+    for kw in (dict(null=True), dict(k=None), dict(v=None), dict(k=P(8)), dict(v=P(24)),
+               dict(T=-1), dict(sb=4), dict(sn=-8), dict(sh=1), dict(k=P(FAR + 64)),
+               dict(v=P(2 * FAR))):
+        assert call(**kw) == -1, kw
+    assert call(T=1 << 30, batch=1 << 20) == -2
+    assert call(sn=1 << 41) == -2
+    assert call(T=0, k=None, v=None) == 0 and call(batch=0, k=None, v=None) == 0
+
+
+@host_only
+def test_accept_validates_on_host(L):
+    def call(B=2, T=4, **kw):
+        a = dict(parents=P(16), tokens=P(16), chosen=P(16), path=P(16), count=P(16), emitted=P(16))
+        a.update(kw)
+        return L.spec_tree_accept(a["parents"], a["tokens"], a["chosen"], None, B, T, a["path"],
+                                  a["count"], a["emitted"], None)
+    for name in ("parents", "tokens", "chosen", "path", "count", "emitted"):
+        assert call(**{name: None}) == -1, name
+    assert call(B=-1) == -1 and call(T=0) == -1 and call(T=129) == -2
+    assert call(B=0, parents=None) == 0
+
+
+def pools(bases=(FAR, 2 * FAR), **kw):
+    a = (ctypes.c_void_p * max(len(bases), 1))(*bases)
+    base = dict(bases=ctypes.cast(a, ctypes.c_void_p), num_pools=len(bases), num_pages=10,
+                page_size=16, heads=2, page_stride=4096, head_stride=2048, slot_stride=128,
+                slot_bytes=128)
+    base.update(kw)
+    p = sv._CachePools(*[base[n] for n, _ in sv._CachePools._fields_])
+    p.keep = a
+    return p
+
+
+BAD_POOLS = [
+    (dict(num_pools=-1), -1), (dict(num_pages=0), -1), (dict(page_size=0), -1),
+    (dict(page_size=24), -2), (dict(heads=0), -1), (dict(slot_bytes=0), -1),
+    (dict(slot_bytes=120), -1), (dict(slot_bytes=144), -1), (dict(page_stride=4104), -1),
+    (dict(head_stride=-16), -1), (dict(slot_bytes=65552, slot_stride=65552), -2),
+    (dict(page_stride=1 << 41), -2), (dict(bases=None), -1), (dict(bases=(FAR, None)), -1),
+    (dict(bases=(FAR + 8,)), -1), (dict(heads=65536), -2)]
+
+
+@host_only
+@pytest.mark.parametrize("kw,status", BAD_POOLS, ids=str)
+def test_bad_pools(L, kw, status):
+    if "bases" in kw and kw["bases"] is None:
+        p = pools(bases=(FAR,))
+        p.bases = None
+    else:
+        p = pools(**kw)
+    a = P(16)
+    assert L.spec_cache_keep(ctypes.byref(p), a, 5, a, a, a, 2, 4, P(4096), None) == status
+    assert L.spec_pages_copy(ctypes.byref(p), a, 3, None) == status
+
+
+@host_only
+def test_keep_and_copy_validate_on_host(L):
+    p = pools()
+
+    def keep(p=p, table=P(1 << 12), width=5, lengths=P(2 << 12), path=P(3 << 12),
+             count=P(4 << 12), B=2, T=4, new=P(5 << 12)):
+        return L.spec_cache_keep(ctypes.byref(p), table, width, lengths, path, count, B, T, new,
+                                 None)
+    for kw in (dict(table=None), dict(lengths=None), dict(path=None), dict(count=None),
+               dict(new=None), dict(B=-1), dict(T=0), dict(width=0), dict(new=P(2 << 12)),
+               dict(new=P((4 << 12) + 4)), dict(new=P((3 << 12) + 28)), dict(new=P(1 << 12))):
+        assert keep(**kw) == -1, kw
+    assert keep(T=1025) == -2 and keep(width=1 << 28) == -2
+    assert keep(B=0, table=None, new=None) == 0
+    assert L.spec_cache_keep(None, P(16), 5, P(16), P(16), P(16), 2, 4, P(64), None) == -1
+    assert L.spec_pages_copy(ctypes.byref(p), None, 3, None) == -1
+    assert L.spec_pages_copy(ctypes.byref(p), P(16), -1, None) == -1
+    assert L.spec_pages_copy(ctypes.byref(p), None, 0, None) == 0
+    assert L.spec_pages_copy(ctypes.byref(pools(bases=())), None, 3, None) in (-1, 0)
+    assert L.spec_pages_copy(None, P(16), 3, None) == -1
+
+
+@host_only
+def test_page_calls_validate_on_host(L):
+    def fork(table=P(1 << 16), lengths=P(2 << 16), parents=P(3 << 16), B=2, W=3, n=4, width=5,
+             page=16, N=10, refs=P(4 << 16), out=P(5 << 16), new=P(6 << 16)):
+        return L.spec_pages_fork(table, lengths, parents, B, W, n, width, page, N, refs, out, new,
+                                 None)
+    for kw in (dict(table=None), dict(lengths=None), dict(parents=None), dict(refs=None),
+               dict(out=None), dict(new=None), dict(B=-1), dict(W=0), dict(n=0), dict(width=0),
+               dict(page=0), dict(N=0), dict(out=P(1 << 16)), dict(out=P((1 << 16) + 8)),
+               dict(new=P(2 << 16)), dict(refs=P(3 << 16)), dict(new=P(5 << 16))):
+        assert fork(**kw) == -1, kw
+    assert fork(page=12) == -2 and fork(B=1 << 30, n=64) == -2 and fork(width=1 << 28) == -2
+    assert fork(B=0, table=None) == 0
+
+    def release(table=P(1 << 16), rows=3, width=5, page=16, N=10, refs=P(4 << 16)):
+        return L.spec_pages_release(table, None, rows, width, page, N, refs, None)
+    for kw in (dict(table=None), dict(refs=None), dict(rows=-1), dict(width=0), dict(N=0)):
+        assert release(**kw) == -1, kw
+    assert release(page=4) == -2 and release(rows=0, table=None) == 0
+
+    def reserve(table=P(1 << 16), lengths=P(16), new=P(16), rows=3, width=5, page=16, N=10,
+                refs=P(16), copies=P(16), missing=P(16), ws=P(16), n=1 << 30):
+        return L.spec_pages_reserve(table, lengths, new, rows, width, page, N, refs, copies,
+                                    missing, ws, n, None)
+    for kw in (dict(table=None), dict(lengths=None), dict(new=None), dict(refs=None),
+               dict(copies=None), dict(missing=None), dict(rows=-1), dict(width=0), dict(N=0),
+               dict(ws=P(8))):
+        assert reserve(**kw) == -1, kw
+    for kw in (dict(page=2048), dict(rows=65537), dict(N=(1 << 22) + 1)):
+        assert reserve(**kw) == -2, kw
+    assert reserve(ws=None) == -3 and reserve(n=8) == -3
+    assert reserve(rows=0, table=None, ws=None) == 0
+    need = L.spec_pages_reserve_workspace_bytes
+    assert need(3, 10) > 0 and need(3, 1 << 22) > need(3, 10)
+    assert need(0, 10) == need(3, 0) == need(65537, 10) == need(3, (1 << 22) + 1) == 0
+
+
+def test_half_floats_stay_with_the_paged_calls():
+    with pytest.raises(TypeError):
+        sv._dtype_code(torch.zeros(1, dtype=torch.float16))
+
+
+# ---------------------------------------------------------------------------
+# The definitions, by hand
+# ---------------------------------------------------------------------------
+def test_definition_of_ancestors():
+    see = ref.ancestors([-1, 0, 0, 1, 3, 9], 6)
+    assert see.astype(int).tolist() == [[1, 0, 0, 0, 0, 0], [1, 1, 0, 0, 0, 0], [1, 0, 1, 0, 0, 0],
+                                        [1, 1, 0, 1, 0, 0], [1, 1, 0, 1, 1, 0], [0, 0, 0, 0, 0, 1]]
+    assert ref.ancestors(None, 3).astype(int).tolist() == [[1, 0, 0], [1, 1, 0], [1, 1, 1]]
+
+
+def test_definition_of_attention():
+    """Two cached positions over two pages and two siblings, scores by hand."""
+    keys, values = torch.zeros(3, 1, 8, 8), torch.zeros(3, 1, 8, 8)
+    table, lengths = torch.tensor([[2, 0]]), torch.tensor([7])
+    keys[2, 0, 0, 0], values[2, 0, 0, 1] = math.log(3.0), 1.0     # position 0
+    values[2, 0, 7, 2] = 5.0                                      # node 0, position 7
+    values[0, 0, 0, 2] = 7.0                                      # node 1, position 8
+    q = torch.zeros(1, 2, 1, 8)
+    q[..., 0] = 1.0
+    out, lse, *_ = ref.tree_attention(q, keys, values, table, lengths, torch.tensor([[-1, -1]]),
+                                      scale=1.0)
+    # weights 3 and seven ones: positions 1..6 hold zeros, each node sees itself alone
+    assert np.allclose(lse[0, :, 0], math.log(10.0))
+    assert np.allclose(out[0, 0, 0, 1:3], [0.3, 0.5]) and np.allclose(out[0, 1, 0, 1:3], [0.3, 0.7])
+
+
+def test_definition_of_acceptance():
+    parents, tokens = np.array([[-1, 0, 0, 2, 2]]), np.array([[9, 4, 5, 6, 6]])
+    path, count, emitted = ref.tree_accept(parents, tokens, np.array([[5, 0, 6, 8, 0]]))
+    assert path.tolist() == [[0, 2, 3, -1, -1]] and count.tolist() == [3]
+    assert emitted.tolist() == [[5, 6, 8, -1, -1]]
+
+
+def test_definition_of_keeping():
+    pool = torch.arange(4 * 8.0).reshape(4, 1, 8, 1)
+    (got,), new = ref.cache_keep([pool], torch.tensor([[3, 1]]), torch.tensor([6]),
+                                 torch.tensor([[0, 3, 4, -1, -1]]), torch.tensor([3]))
+    want = pool.clone()
+    want[3, 0, 7], want[1, 0, 0] = pool[1, 0, 1], pool[1, 0, 2]
+    assert torch.equal(got, want) and new == [9]
+
+
+def test_definition_of_sharing():
+    table, lengths = np.array([[[4, 2, 0], [1, -1, -1]]]), np.array([[17, 3]])
+    refs = np.array([1, 1, 1, 0, 1, 0])
+    out, new, after = ref.pages_fork(table, lengths, np.array([[0, 0, 1]]), refs, 16)
+    assert out.tolist() == [[[4, 2, -1], [4, 2, -1], [1, -1, -1]]] and new.tolist() == [[17, 17, 3]]
+    assert after.tolist() == [1, 2, 3, 0, 3, 0]
+    got, refs, copies, missing = ref.pages_reserve(out[0, :2], new[0, :2], after, 16, np.array([1, 1]))
+    assert got.tolist() == [[4, 3, -1], [4, 5, -1]] and missing == 0
+    assert copies.tolist() == [[2, 3, 1], [2, 5, 1]] and refs.tolist() == [1, 2, 1, 1, 3, 1]
+    got, refs = ref.pages_release(got, refs, 16, np.array([0, 16]))
+    assert got.tolist() == [[-1] * 3, [4, -1, -1]] and refs.tolist() == [1, 2, 1, 0, 2, 0]

@@ -1,0 +1,356 @@
+"""The paged cache's upkeep on the GPU against the plain definitions: appending,
+accepting and keeping a path, and the pages' bookkeeping.  Everything here moves
+or counts, so results are equal."""
+import numpy as np
+import pytest
+import torch
+
+import draft_token_verification_vocab_amd as sv
+from oracle import cache_ref as ref
+
+pytestmark = pytest.mark.gpu
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+def bits(t):
+    return t.cpu().contiguous().view(torch.uint8)
+
+
+def same(got, want):
+    assert torch.equal(bits(got), bits(want))
+
+
+def i32(x):
+    return torch.as_tensor(np.asarray(x), dtype=torch.int32)
+
+
+def paged(g, B, N, width, page, high, holes=False):
+    """A table of pages in random order and lengths, some past what pages hold."""
+    order = torch.randperm(N, generator=g).to(torch.int32)
+    table = order[:B * width].reshape(B, width).clone()
+    if holes:
+        table[torch.rand(B, width, generator=g) < 0.2] = -1
+        table[0, 0] = N
+        table[-1, -1] = -2 ** 31
+    lengths = torch.randint(0, high + 1, (B,), generator=g).to(torch.int32)
+    return table, lengths
+
+
+def pool(g, N, kv, page, D, dt):
+    return torch.randn(N, kv, page, D, generator=g).to(dt)
+
+
+LAYOUTS = {
+    "heads": lambda t: t.cuda(),
+    "slots": lambda t: t.cuda().transpose(1, 2).contiguous().transpose(1, 2),
+    "wide": lambda t: torch.cat([t, t], dim=3).cuda()[..., :t.shape[3]],
+}
+
+
+@pytest.mark.parametrize("dt", [BF16, F16, F32])
+@pytest.mark.parametrize("layout", sorted(LAYOUTS))
+@pytest.mark.parametrize("B,T,kv,D,page,high", [
+    (1, 1, 1, 8, 8, 20), (3, 5, 2, 128, 16, 50), (2, 40, 3, 80, 8, 30), (9, 3, 8, 64, 1024, 900),
+    (2, 17, 4, 256, 32, 70)])
+def test_append(dt, layout, B, T, kv, D, page, high):
+    g = torch.Generator().manual_seed(B * 100 + T)
+    width = -(-(high + T) // page)
+    N = B * width + 3
+    table, lengths = paged(g, B, N, width, page, high, holes=width > 2)
+    keys, values = (pool(g, N, kv, page, D, dt) for _ in range(2))
+    rows = torch.randn(B, T, 3 * kv, D, generator=g).to(dt)
+    nodes = torch.randint(-1, T + 3, (B,), generator=g).to(torch.int32)
+    k, v = rows[:, :, kv:2 * kv], rows[:, :, 2 * kv:]
+    for num in (None, nodes):
+        want = ref.cache_append(k, v, keys, values, table, lengths, num)
+        dk, dv = LAYOUTS[layout](keys), LAYOUTS[layout](values)
+        r = rows.cuda()
+        got = sv.cache_append(r[:, :, kv:2 * kv], r[:, :, 2 * kv:], dk, dv, table.cuda(),
+                              lengths.cuda(), num_nodes=None if num is None else num.cuda())
+        assert got[0] is dk and got[1] is dv
+        same(dk, want[0])
+        same(dv, want[1])
+
+
+def test_append_past_the_table_and_at_bad_lengths():
+    g = torch.Generator().manual_seed(1)
+    table, _ = paged(g, 4, 12, 2, 8, 1)
+    lengths = i32([14, 16, -5, 2 ** 31 - 1])
+    keys, values = (pool(g, 12, 2, 8, 16, F32) for _ in range(2))
+    k, v = torch.randn(4, 5, 2, 16, generator=g), torch.randn(4, 5, 2, 16, generator=g)
+    want = ref.cache_append(k, v, keys, values, table, lengths)
+    dk, dv = keys.cuda(), values.cuda()
+    sv.cache_append(k.cuda(), v.cuda(), dk, dv, table.cuda(), lengths.cuda())
+    same(dk, want[0])
+    same(dv, want[1])
+
+
+@pytest.mark.parametrize("B,T", [(1, 1), (1, 5), (70, 9), (33, 64), (5, 65), (9, 128)])
+@pytest.mark.parametrize("ragged", [False, True])
+def test_accept(B, T, ragged):
+    g = torch.Generator().manual_seed(B + T)
+    at = torch.arange(T)
+    parents = (torch.rand(B, T, generator=g) * at).long().clamp(max=(at - 1).clamp(min=0))
+    parents[:, 0] = -1
+    parents[B // 2] = at - 1                                  # a chain
+    if T > 4:
+        parents[0, 3] = 4                                     # does not precede its node
+        parents[0, 4] = -9
+    tokens = torch.randint(0, 3, (B, T), generator=g)         # twins among the children
+    chosen = torch.randint(0, 3, (B, T), generator=g)
+    chosen[B // 2, :-1] = tokens[B // 2, 1:]                  # all of the chain accepted
+    nodes = torch.randint(-1, T + 2, (B,), generator=g) if ragged else None
+    want = ref.tree_accept(parents.numpy(), tokens.numpy(), chosen.numpy(), nodes)
+    r = sv.tree_accept(i32(parents).cuda(), i32(tokens).cuda(), i32(chosen).cuda(),
+                       num_nodes=None if nodes is None else i32(nodes).cuda())
+    for name, w in zip(("path", "count", "tokens"), want):
+        assert (r[name].cpu().numpy() == w).all(), name
+
+
+@pytest.mark.parametrize("dt,D", [(BF16, 128), (F32, 80), (BF16, 8)])
+@pytest.mark.parametrize("layout", sorted(LAYOUTS))
+@pytest.mark.parametrize("B,T,kv,page,high,count", [(1, 1, 1, 8, 5, 1), (4, 9, 2, 8, 40, 3),
+                                                    (3, 128, 3, 16, 90, 2), (40, 20, 2, 16, 33, 5)])
+def test_keep(dt, D, layout, B, T, kv, page, high, count):
+    g = torch.Generator().manual_seed(B * T)
+    width = -(-(high + T) // page)
+    N = B * width + 2
+    table, lengths = paged(g, B, N, width, page, high, holes=B == 4)
+    pools = [pool(g, N, kv, page, D, dt) for _ in range(count)]
+    path = torch.stack([torch.rand(T, generator=g).argsort() for _ in range(B)])
+    counts = torch.randint(0, T + 1, (B,), generator=g)
+    for b in range(B):
+        path[b, :counts[b]] = path[b, :counts[b]].sort().values
+        path[b, counts[b]:] = -1
+    path[0, 0] = 0
+    if B > 3:
+        path[1, 2:4] = T + 5       # ends the list
+        counts[1] = T
+        counts[2] = 2 ** 31 - 1    # clamped; the -1 behind the path ends it
+        counts[3] = -4
+    want, new = ref.cache_keep(pools, table, lengths, path, counts)
+    dev = [LAYOUTS[layout](p) for p in pools]
+    got = sv.cache_keep(dev, table.cuda(), lengths.cuda(), i32(path).cuda(), i32(counts).cuda())
+    assert got.tolist() == new
+    for a, w in zip(dev, want):
+        same(a, w)
+
+
+def test_keep_more_pools_than_a_launch_takes():
+    g = torch.Generator().manual_seed(3)
+    table, lengths = paged(g, 3, 20, 5, 8, 30)
+    pools = [pool(g, 20, 2, 8, 16, BF16) for _ in range(131)]
+    path, counts = i32([[0, 2, 5, -1, -1, -1], [1, 3, 4, 5, -1, -1], [0, 1, 2, 3, 4, 5]]), i32([3, 4, 6])
+    want, new = ref.cache_keep(pools, table, lengths, path, counts)
+    dev = [p.cuda() for p in pools]
+    got = sv.cache_keep(dev, table.cuda(), lengths.cuda(), path.cuda(), counts.cuda())
+    assert got.tolist() == new
+    for a, w in zip(dev, want):
+        same(a, w)
+
+
+@pytest.mark.parametrize("B,W,n,P", [(1, 1, 1, 1), (3, 4, 7, 5), (2, 8, 8, 700), (20, 5, 3, 9)])
+def test_fork_and_release(B, W, n, P):
+    rng = np.random.default_rng(B * W + P)
+    page, N = 16, 4000
+    table = rng.integers(0, N, (B, W, P))
+    table[rng.random(table.shape) < 0.1] = -1
+    table[0, 0, 0] = N
+    lengths = rng.integers(-3, P * page + 20, (B, W))
+    parents = rng.integers(-1, W + 1, (B, n))
+    refs = rng.integers(0, 4, N)
+    out, new, after = ref.pages_fork(table, lengths, parents, refs, page)
+    d_refs, d_out = i32(refs).cuda(), torch.full((B, n, P), 12345, dtype=torch.int32, device="cuda")
+    got = sv.pages_fork(i32(table).cuda(), i32(lengths).cuda(), i32(parents).cuda(), d_refs, page,
+                        out=d_out)
+    assert (got.cpu().numpy() == new).all()
+    assert (d_out.cpu().numpy() == out).all()
+    assert (d_refs.cpu().numpy() == after).all()
+    # dropping the tails, then everything, more often than there are references
+    short = rng.integers(-2, P * page + 5, B * n)
+    for cut in (short, None):
+        out, after = ref.pages_release(out.reshape(-1, P), after, page, cut)
+        r = sv.pages_release(d_out, d_refs, page,
+                             None if cut is None else i32(cut.reshape(B, n)).cuda())
+        assert r is d_out
+        assert (d_out.cpu().numpy().reshape(-1, P) == out).all()
+        assert (d_refs.cpu().numpy() == after).all()
+    t, after = ref.pages_release(table.reshape(-1, P), after, page)
+    d_table = i32(table).cuda()
+    sv.pages_release(d_table, d_refs, page)
+    assert (d_table.cpu().numpy().reshape(-1, P) == t).all()
+    assert (d_refs.cpu().numpy() == after).all()
+
+
+def reserve(table, lengths, refs, page, new, **kw):
+    t, r = i32(table).cuda(), i32(refs).cuda()
+    got = sv.pages_reserve(t, i32(lengths).cuda(), r, page, i32(new).cuda(), **kw)
+    return (t.cpu().numpy(), r.cpu().numpy(), got["copies"].cpu().numpy(), got["missing"].item())
+
+
+def check_reserve(table, lengths, refs, page, new):
+    got = reserve(table, lengths, refs, page, new)
+    want = ref.pages_reserve(np.asarray(table), np.asarray(lengths), np.asarray(refs), page,
+                             np.asarray(new))
+    assert got[3] == want[3]
+    assert (got[0] == want[0]).all()
+    assert (got[1] == want[1]).all()
+    assert (got[2] == want[2]).all()
+    return got
+
+
+def random_tables(rng, rows, P, N, page, share):
+    """Rows that hold pages up to random lengths, some of them shared by rows or
+    with holders that are not among the rows."""
+    lengths = rng.integers(0, P * page // 2 + 1, rows)
+    free = list(rng.permutation(N))
+    refs = np.zeros(N, dtype=int)
+    table = np.full((rows, P), -1)
+    for r in range(rows):
+        held = -(-int(lengths[r]) // page) + int(rng.integers(0, 2))
+        if r and rng.random() < share:      # a branch of an earlier row
+            o = int(rng.integers(0, r))
+            lengths[r], table[r] = lengths[o], table[o]
+        else:
+            for k in range(min(held, P)):
+                table[r, k] = free.pop()
+        for e in table[r][table[r] >= 0]:
+            refs[e] += 1
+    held_elsewhere = rng.random(N) < 0.3
+    refs[held_elsewhere] += 1
+    return table, lengths, refs
+
+
+@pytest.mark.parametrize("rows,P,N,page", [(1, 1, 3, 8), (4, 6, 100, 16), (50, 9, 3000, 8),
+                                           (3, 300, 2500, 8), (700, 4, 9000, 16),
+                                           (2000, 3, 9000, 8), (17, 100, 70000, 16)])
+@pytest.mark.parametrize("share", [0.0, 0.6])
+def test_reserve(rows, P, N, page, share):
+    for seed in range(4):
+        rng = np.random.default_rng(seed * 1000 + rows)
+        table, lengths, refs = random_tables(rng, rows, P, N, page, share)
+        most = [1, 5, P * page // 2, 3 * page][seed]
+        new = np.minimum(rng.integers(0, most + 1, rows), P * page - lengths)
+        check_reserve(table, lengths, refs, page, new)
+
+
+def test_reserve_settles_who_keeps_a_shared_page():
+    page = 8
+    # pages 3 (all holders here), 4 (one elsewhere), 5 (full: not written)
+    table = [[5, 3, -1], [5, 3, -1], [5, 3, -1], [5, 4, -1], [5, 4, -1]]
+    refs = [0, 0, 0, 3, 3, 5, 0, 0, 0, 0]
+    t, r, copies, missing = check_reserve(table, [12, 12, 12, 9, 9], refs, page, [1, 1, 1, 8, 1])
+    assert missing == 0
+    assert t.tolist() == [[5, 3, -1], [5, 0, -1], [5, 1, -1], [5, 2, 6], [5, 7, -1]]
+    assert r.tolist() == [1, 1, 1, 1, 1, 5, 1, 1, 0, 0]
+    assert copies.tolist() == [[-1, -1, 0], [3, 0, 4], [3, 1, 4], [4, 2, 1], [4, 7, 1]]
+
+
+def test_reserve_all_or_nothing():
+    page = 8
+    table = [[5, 3, -1], [5, 3, -1], [5, 4, -1]]
+    refs = [1, 1, 0, 2, 3, 3, 1, 0]
+    got = check_reserve(table, [12, 12, 9], refs, page, [9, 5, 1])
+    assert got[3] == 2 and got[0].tolist() == table and got[1].tolist() == refs
+    got = check_reserve(table, [12, 12, 9], refs, page, [9, 5, 16])
+    assert got[3] == -1 and got[0].tolist() == table and got[1].tolist() == refs
+    got = check_reserve(table, [12, 12, 9], refs, page, [2 ** 31 - 1, 5, 1])
+    assert got[3] == -1
+    got = check_reserve(table, [12, 30, 9], refs, page, [0, 1, 0])
+    assert got[3] == -1
+    got = check_reserve(table, [12, 12, 9], refs, page, [0, -3, 0])
+    assert got[3] == 0 and got[0].tolist() == table and got[1].tolist() == refs
+    # three pages for two that are free, then exactly enough
+    got = check_reserve(table, [12, 12, 9], refs, page, [1, 5, 1])
+    assert got[3] == 1
+    got = check_reserve(table, [12, 12, 9], refs, page, [1, 4, 1])
+    assert got[3] == 0
+
+
+def test_reserve_takes_its_workspace_as_it_is():
+    rng = np.random.default_rng(5)
+    table, lengths, refs = random_tables(rng, 30, 8, 5000, 16, 0.5)
+    new = np.minimum(rng.integers(0, 40, 30), 8 * 16 - lengths)
+    a = reserve(table, lengths, refs, 16, new)
+    n = sv._reserve_workspace_bytes(30, 5000)
+    w = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+    b = reserve(table, lengths, refs, 16, new, workspace=w)
+    for x, y in zip(a, b):
+        assert (x == y) if isinstance(x, int) else (x == y).all()
+
+
+@pytest.mark.parametrize("dt,D", [(BF16, 128), (F32, 80), (BF16, 8)])
+@pytest.mark.parametrize("layout", sorted(LAYOUTS))
+@pytest.mark.parametrize("page,kv", [(8, 1), (16, 3), (256, 2)])
+def test_copy(dt, D, layout, page, kv):
+    g = torch.Generator().manual_seed(page)
+    pools = [pool(g, 30, kv, page, D, dt) for _ in range(3)]
+    copies = i32([[0, 7, page], [0, 8, 1], [3, 9, page - 1], [-1, -1, 0], [5, 30, 4], [30, 5, 4],
+                  [4, 11, -2], [2, 12, page + 9]])
+    want = ref.pages_copy(pools, copies)
+    dev = [LAYOUTS[layout](p) for p in pools]
+    sv.pages_copy(dev, copies.cuda())
+    for a, w in zip(dev, want):
+        same(a, w)
+
+
+def test_empty_calls():
+    e = torch.empty(0, dtype=torch.int32, device="cuda")
+    refs = torch.zeros(4, dtype=torch.int32, device="cuda")
+    p = torch.zeros(4, 2, 8, 16, dtype=BF16, device="cuda")
+    rows = torch.zeros(0, 3, 2, 16, dtype=BF16, device="cuda")
+    sv.cache_append(rows, rows, p, p.clone(), e.view(0, 3), e)
+    sv.cache_append(rows.view(0, 3, 2, 16)[:, :0], rows[:, :0], p, p.clone(), e.view(0, 3), e)
+    assert sv.tree_accept(e.view(0, 3), e.view(0, 3), e.view(0, 3))["count"].shape == (0,)
+    assert sv.cache_keep([p], e.view(0, 3), e, e.view(0, 2), e).shape == (0,)
+    assert sv.pages_fork(e.view(0, 2, 3), e.view(0, 2), e.view(0, 4), refs, 8,
+                         out=e.view(0, 4, 3)).shape == (0, 4)
+    sv.pages_release(e.view(0, 3), refs, 8)
+    r = sv.pages_reserve(e.view(0, 3), e, refs, 8, e)
+    assert r["copies"].shape == (0, 3) and r["missing"].item() == 0
+    sv.pages_copy([p], e.view(0, 3))
+
+
+def test_refusals():
+    i = torch.zeros(2, 3, dtype=torch.int32, device="cuda")
+    n = torch.zeros(2, dtype=torch.int32, device="cuda")
+    refs = torch.zeros(6, dtype=torch.int32, device="cuda")
+    p = torch.zeros(6, 2, 8, 16, dtype=BF16, device="cuda")
+    rows = torch.zeros(2, 3, 2, 16, dtype=BF16, device="cuda")
+    odd = torch.zeros(6, 2, 12, 16, dtype=BF16, device="cuda")
+    thin = torch.zeros(6, 2, 8, 4, dtype=BF16, device="cuda")
+    b = torch.zeros(2, 2, 3, dtype=torch.int32, device="cuda")
+    for error, fn in (
+            (ValueError, lambda: sv.cache_append(rows, rows.float(), p, p.clone(), i, n)),
+            (ValueError, lambda: sv.cache_append(rows, rows[:, :2], p, p.clone(), i, n)),
+            (ValueError, lambda: sv.cache_append(rows[:, :, :1], rows[:, :, :1], p, p.clone(), i, n)),
+            (ValueError, lambda: sv.cache_append(rows, rows, p, p.clone(), i.long(), n)),
+            (ValueError, lambda: sv.cache_append(rows, rows, p, p[:5], i, n)),
+            (sv.SpecVerifyError, lambda: sv.cache_append(p[:2, :, :3].transpose(1, 2),
+                                                         p[:2, :, 3:6].transpose(1, 2), p,
+                                                         p.clone(), i, n)),
+            (sv.SpecVerifyError, lambda: sv.cache_append(rows, rows, odd, odd.clone(), i, n)),
+            (ValueError, lambda: sv.tree_accept(i, i, i.long())),
+            (ValueError, lambda: sv.tree_accept(i, i[:1], i)),
+            (sv.SpecVerifyError, lambda: sv.tree_accept(*[torch.zeros(1, 129, dtype=torch.int32,
+                                                                      device="cuda")] * 3)),
+            (ValueError, lambda: sv.cache_keep([], i, n, i, n)),
+            (ValueError, lambda: sv.cache_keep([p, p.float()], i, n, i, n)),
+            (ValueError, lambda: sv.cache_keep([p, p[:5]], i, n, i, n)),
+            (ValueError, lambda: sv.cache_keep([p.cpu()], i, n, i, n)),
+            (sv.SpecVerifyError, lambda: sv.cache_keep([thin], i, n, i, n)),
+            (sv.SpecVerifyError, lambda: sv.cache_keep([odd], i, n, i, n)),
+            (ValueError, lambda: sv.pages_fork(i, n, i, refs, 8, out=b)),
+            (sv.SpecVerifyError, lambda: sv.pages_fork(b, i[:, :2].contiguous(),
+                                                       i[:, :2].contiguous(), refs, 8, out=b)),
+            (sv.SpecVerifyError, lambda: sv.pages_release(i, refs, 12)),
+            (sv.SpecVerifyError, lambda: sv.pages_release(i, refs, 4)),
+            (ValueError, lambda: sv.pages_release(i, refs, 8, i)),
+            (ValueError, lambda: sv.pages_reserve(i, n, refs, 8, n.long())),
+            (sv.SpecVerifyError, lambda: sv.pages_reserve(
+                i, n, refs, 8, n, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))),
+            (ValueError, lambda: sv.pages_copy([p], i[:, :2].contiguous())),
+            (sv.SpecVerifyError, lambda: sv.pages_copy([thin], i))):
+        with pytest.raises(error):
+            fn()
+    torch.cuda.synchronize()
