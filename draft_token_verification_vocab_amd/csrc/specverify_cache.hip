@@ -96,6 +96,7 @@ bool pools_ok(const spec_cache *c) {
 struct TreePlan {
     int dp;      // dimensions, rounded up to what a kernel takes
     int rt;      // 16-row tiles to a workgroup
+    int waves;   // workgroups to a compute unit
     int mtiles;
     int slices;
     size_t first, part, part_ml, total;  // workspace
@@ -120,12 +121,18 @@ TreePlan plan_tree(const spec_cache *c, int32_t nodes, int32_t heads) {
     TreePlan p;
     p.dp = c->dim <= 64 ? 64 : (c->dim <= 128 ? 128 : 256);
     const int64_t rows = static_cast<int64_t>(nodes) * (heads / c->kv_heads);
-    p.rt = rows > 16 && p.dp <= 128 ? 2 : 1;
+    const int most = c->dtype == SPEC_DTYPE_F32 || p.dp == 256 ? 2 : 4;
+    const int64_t tiles16 = (rows + 15) / 16, splits = (tiles16 + most - 1) / most;
+    p.rt = static_cast<int>((tiles16 + splits - 1) / splits);
+    p.waves = c->dtype == SPEC_DTYPE_F32 ? 1
+              : p.dp == 64               ? tree_waves<__bf16, 64>(p.rt)
+              : p.dp == 128              ? tree_waves<__bf16, 128>(p.rt)
+                                         : tree_waves<__bf16, 256>(p.rt);
     p.mtiles = static_cast<int>((rows + 16 * p.rt - 1) / (16 * p.rt));
     const int64_t units = static_cast<int64_t>(p.mtiles) * c->kv_heads;
     const int64_t tiles =
         c->batch * (static_cast<int64_t>(c->table_width) * c->page_size / kTreeTile + 1);
-    int64_t slices = (4 * kUnits + units - 1) / units;
+    int64_t slices = (p.waves * kUnits + units - 1) / units;
     if (slices > tiles) slices = tiles;
     p.slices = static_cast<int>(slices < 1 ? 1 : slices);
     const int64_t parts = 2 * units * p.slices * 16 * p.rt;
@@ -136,33 +143,53 @@ TreePlan plan_tree(const spec_cache *c, int32_t nodes, int32_t heads) {
     return p;
 }
 
-template <typename T, int DP>
+template <typename T, int DP, bool FULL>
 void launch_tree_rt(const TreeArgs &a, const TreePlan &p, hipStream_t st) {
-    const dim3 grid(static_cast<unsigned>(p.slices * a.KV * p.mtiles));
-    if constexpr (DP <= 128) {
-        if (p.rt == 2) {
-            tree_attention_kernel<T, DP, 2><<<grid, dim3(kTreeBlock), 0, st>>>(a);
+    const dim3 grid(static_cast<unsigned>(p.slices * a.KV * p.mtiles)), block(kTreeBlock);
+    if constexpr (DP <= 128 && sizeof(T) == 2) {
+        if (p.rt == 4) {
+            tree_attention_kernel<T, DP, 4, FULL><<<grid, block, 0, st>>>(a);
+            return;
+        }
+        if (p.rt == 3) {
+            tree_attention_kernel<T, DP, 3, FULL><<<grid, block, 0, st>>>(a);
             return;
         }
     }
-    tree_attention_kernel<T, DP, 1><<<grid, dim3(kTreeBlock), 0, st>>>(a);
+    if (p.rt == 2)
+        tree_attention_kernel<T, DP, 2, FULL><<<grid, block, 0, st>>>(a);
+    else
+        tree_attention_kernel<T, DP, 1, FULL><<<grid, block, 0, st>>>(a);
+}
+
+template <typename T, int DP>
+void launch_tree_dim(const TreeArgs &a, const TreePlan &p, hipStream_t st) {
+    if (a.D == DP && a.slot_stride == DP)
+        launch_tree_rt<T, DP, true>(a, p, st);
+    else
+        launch_tree_rt<T, DP, false>(a, p, st);
 }
 
 template <typename T>
 void launch_tree(const TreeArgs &a, const TreePlan &p, hipStream_t st) {
     if (p.dp == 64)
-        launch_tree_rt<T, 64>(a, p, st);
+        launch_tree_dim<T, 64>(a, p, st);
     else if (p.dp == 128)
-        launch_tree_rt<T, 128>(a, p, st);
+        launch_tree_dim<T, 128>(a, p, st);
     else
-        launch_tree_rt<T, 256>(a, p, st);
+        launch_tree_dim<T, 256>(a, p, st);
 }
 
 template <typename T>
 void launch_join(const TreeArgs &a, const TreePlan &p, hipStream_t st) {
     const int64_t rows = static_cast<int64_t>(a.B) * a.T * a.H;
-    tree_join_kernel<T><<<dim3(static_cast<unsigned>((rows + kTreeWaves - 1) / kTreeWaves)),
-                          dim3(kTreeBlock), 0, st>>>(a, 16 * p.rt);
+    const dim3 grid(static_cast<unsigned>((rows + kTreeWaves - 1) / kTreeWaves));
+    if (p.dp == 64)
+        tree_join_kernel<T, 16><<<grid, dim3(kTreeBlock), 0, st>>>(a, 16 * p.rt);
+    else if (p.dp == 128)
+        tree_join_kernel<T, 32><<<grid, dim3(kTreeBlock), 0, st>>>(a, 16 * p.rt);
+    else
+        tree_join_kernel<T, 64><<<grid, dim3(kTreeBlock), 0, st>>>(a, 16 * p.rt);
 }
 
 // ---------------------------------------------------------------------------

@@ -46,6 +46,8 @@ constexpr int kTreeKeys = 32;                        // a wave's keys at a time
 constexpr int kTreeTile = kTreeKeys * kTreeWaves;    // the unit that is dealt out
 constexpr int kMaxTreeNodes = 128;                   // of a tree; chains may be longer
 
+typedef unsigned int v2u32 __attribute__((ext_vector_type(2)));
+typedef float v2f32 __attribute__((ext_vector_type(2)));
 typedef float v4f32 __attribute__((ext_vector_type(4)));
 typedef float v8f32 __attribute__((ext_vector_type(8)));
 typedef __bf16 v8bf16 __attribute__((ext_vector_type(8)));
@@ -137,6 +139,14 @@ template <typename T>
 __device__ __forceinline__ typename TreeElem<T>::Raw tree_load8(const T *p) {
     return *reinterpret_cast<const typename TreeElem<T>::Raw *>(p);
 }
+// Keys and values are read once, so past the caches' usual order.
+template <typename T>
+__device__ __forceinline__ typename TreeElem<T>::Raw tree_stream8(const T *p) {
+    typename TreeElem<T>::Raw r;
+    using V = decltype(r.w);
+    r.w = __builtin_nontemporal_load(reinterpret_cast<const V *>(p));
+    return r;
+}
 
 // Words of 32 bits that C elements take.
 template <typename T, int C>
@@ -148,13 +158,13 @@ template <typename T, int C>
 __device__ __forceinline__ void tree_load_row(const T *p, uint32_t *w) {
     constexpr int n = tree_words<T, C>();
     if constexpr (n == 2) {
-        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        const v2u32 v = __builtin_nontemporal_load(reinterpret_cast<const v2u32 *>(p));
         w[0] = v.x;
         w[1] = v.y;
     } else {
 #pragma unroll
         for (int i = 0; i < n / 4; ++i) {
-            const v4u32 v = reinterpret_cast<const v4u32 *>(p)[i];
+            const v4u32 v = __builtin_nontemporal_load(reinterpret_cast<const v4u32 *>(p) + i);
 #pragma unroll
             for (int k = 0; k < 4; ++k) w[4 * i + k] = v[k];
         }
@@ -180,14 +190,15 @@ __device__ __forceinline__ typename TreeElem<T>::Frag tree_column(
     }
 }
 
-// Whether a word holds an infinity or a NaN.
+// A word with its infinities and NaNs taken out.
 template <typename T>
-__device__ __forceinline__ bool tree_nonfinite(uint32_t w) {
+__device__ __forceinline__ uint32_t tree_finite(uint32_t w) {
     if constexpr (sizeof(T) == 4) {
-        return (w & 0x7F800000u) == 0x7F800000u;
+        return (w & 0x7F800000u) == 0x7F800000u ? 0u : w;
     } else {
         constexpr uint32_t e = TreeElem<T>::kExponent;
-        return (w & e) == e || ((w >> 16) & e) == e;
+        if ((w & e) == e) w &= 0xFFFF0000u;
+        return ((w >> 16) & e) == e ? w & 0xFFFFu : w;
     }
 }
 
@@ -225,65 +236,113 @@ __device__ __forceinline__ bool tree_sees(const uint64_t (*mask)[2], bool chain,
     return (mask[row_node][node >> 6] >> (node & 63)) & 1;
 }
 
+// Which of the 8 positions from node `at` on (below 0: cached ones) a row sees, a
+// bit for each; nothing where its node is -1.
+__device__ __forceinline__ uint32_t tree_sees8(const uint64_t (*mask)[2], bool chain,
+                                               int row_node, int at) {
+    if (row_node < 0) return 0;
+    // bits 0..7 of a window that begins at node `at`
+    if (chain) {
+        const int n = row_node + 1 - at;  // positions up to the row's own node
+        return n >= 8 ? 0xFFu : (n <= 0 ? 0u : (1u << n) - 1);
+    }
+    if (at <= -8) return 0xFFu;
+    const uint64_t lo = mask[row_node][0], hi = mask[row_node][1];
+    if (at < 0) return (static_cast<uint32_t>(lo << -at) | ((1u << -at) - 1)) & 0xFFu;
+    if (at >= 128) return 0;
+    const uint64_t w = at >= 64 ? hi >> (at - 64) : (lo >> at) | (at ? hi << (64 - at) : 0);
+    return static_cast<uint32_t>(w) & 0xFFu;
+}
+
+// Queries and joined sums are not needed at the same time.
 template <typename T, int DP, int R>
 struct TreeShared {
     static constexpr int kPitch = DP + 4;  // 16 rows' starts on different banks
-    float merge[kTreeWaves][16][kPitch];
+    union {
+        float merge[kTreeWaves][16][kPitch];
+        typename TreeElem<T>::Raw q[R][DP / 32][kWave];
+    };
     float ml[kTreeWaves][16 * R][2];
+    int node[16 * R];  // a row's node, -1 where it is not in use
+    int odd;           // a node's value holds an infinity or a NaN
     uint64_t mask[kMaxTreeNodes][2];
     int up[kMaxTreeNodes];
-    int scan[kTreeWaves];
-    int plan[4];
 };
 
-// Finds this slice's tiles: [start, end), the sequence that holds start and
-// that sequence's first tile.  Workgroup 0 leaves the sequences' first tiles
-// for the second launch.
-template <typename Shared>
-__device__ __forceinline__ void tree_plan(const TreeArgs &a, Shared &sh, int slice, bool leave,
-                                          int &start, int &end, int &b, int &first) {
-    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
-    int total = 0;
-    for (int pass = 0; pass < 2; ++pass) {
-        // pass 0 adds the tiles up, pass 1 finds the place
-        int per = 0;
-        if (pass == 1) {
-            per = (total + a.slices - 1) / a.slices;
-            start = slice * per;
-            end = start + per < total ? start + per : total;
-            if (tid == 0) sh.plan[0] = a.B;
-            if (leave && tid == 0) a.first[a.B] = per;
-        }
-        int base = 0;
-        for (int b0 = 0; b0 < a.B; b0 += kTreeBlock) {
-            const int i = b0 + tid;
-            const int mine = i < a.B ? tree_tiles(tree_span(a, i).keys) : 0;
-            int upto = mine;
+// The thread's index as a value the compiler knows nothing about, so that what
+// a segment's beginning and end derive from it is not kept in registers
+// throughout the loop between them.
+__device__ __forceinline__ int fresh_tid() {
+    int t = threadIdx.x;
+    asm volatile("" : "+v"(t));
+    return t;
+}
+
+__device__ __forceinline__ int tree_scan(int v, int lane) {
 #pragma unroll
-            for (int o = 1; o < kWave; o <<= 1) {
-                const int v = __shfl_up(upto, o, kWave);
-                if (lane >= o) upto += v;
-            }
-            __syncthreads();
-            if (lane == kWave - 1) sh.scan[wave] = upto;
-            __syncthreads();
-            int before = base;
-            for (int w = 0; w < wave; ++w) before += sh.scan[w];
-            before += upto - mine;
-            if (pass == 1 && i < a.B) {
-                if (leave) a.first[i] = before;
-                if (start >= before && start < before + mine) {
-                    sh.plan[0] = i;
-                    sh.plan[1] = before;
-                }
-            }
-            for (int w = 0; w < kTreeWaves; ++w) base += sh.scan[w];
-        }
-        total = base;
+    for (int o = 1; o < kWave; o <<= 1) {
+        const int u = __shfl_up(v, o, kWave);
+        if (lane >= o) v += u;
     }
-    __syncthreads();
-    b = sh.plan[0];
-    first = sh.plan[1];
+    return v;
+}
+
+struct TreePlace {
+    int start, end;  // this slice's tiles
+    int b, first;    // the sequence that holds start, and its first tile
+    TreeSpan span;   // of that sequence
+};
+
+// Finds a slice's place, in every wave for itself: a lane adds up an equal share
+// of the sequences, a scan over the lanes finds the share that holds the
+// slice's first tile, and a second one, over that share, the sequence.
+// Workgroup 0 leaves the sequences' first tiles for the second launch.
+__device__ __forceinline__ TreePlace tree_plan(const TreeArgs &a, int slice, int lane,
+                                               bool leave) {
+    const int share = (a.B + kWave - 1) / kWave;
+    int mine = 0;
+    for (int k = 0; k < share; ++k) {
+        const int i = lane * share + k;
+        if (i < a.B) mine += tree_tiles(tree_span(a, i).keys);
+    }
+    const int upto = tree_scan(mine, lane);
+    const int total = __builtin_amdgcn_readlane(upto, kWave - 1);
+    const int per = (total + a.slices - 1) / a.slices;
+    if (leave) {
+        int before = upto - mine;
+        for (int k = 0; k < share; ++k) {
+            const int i = lane * share + k;
+            if (i >= a.B) break;
+            a.first[i] = before;
+            before += tree_tiles(tree_span(a, i).keys);
+        }
+        if (lane == 0) a.first[a.B] = per;
+    }
+    TreePlace p{};
+    p.start = slice * per;
+    p.end = p.start + per < total ? p.start + per : total;
+    if (p.start >= total) return p;
+    uint64_t found = __ballot(p.start < upto);
+    const int at = __builtin_amdgcn_readfirstlane(__ffsll(static_cast<long long>(found)) - 1);
+    int before = __builtin_amdgcn_readlane(upto - mine, at);
+    for (int i0 = at * share;; i0 += kWave) {
+        const int i = i0 + lane;
+        const bool in = i < at * share + share && i < a.B;
+        const TreeSpan span = in ? tree_span(a, i) : TreeSpan{0, 0, 0};
+        const int upto_i = before + tree_scan(in ? tree_tiles(span.keys) : 0, lane);
+        found = __ballot(p.start < upto_i);
+        if (found) {
+            const int k =
+                __builtin_amdgcn_readfirstlane(__ffsll(static_cast<long long>(found)) - 1);
+            p.b = i0 + k;
+            p.span.cached = __builtin_amdgcn_readlane(span.cached, k);
+            p.span.live = __builtin_amdgcn_readlane(span.live, k);
+            p.span.keys = __builtin_amdgcn_readlane(span.keys, k);
+            p.first = __builtin_amdgcn_readlane(upto_i, k) - tree_tiles(p.span.keys);
+            return p;
+        }
+        before = __builtin_amdgcn_readlane(upto_i, kWave - 1);
+    }
 }
 
 // Ancestor masks of a tree's nodes, the node itself included, by doubling the
@@ -291,7 +350,7 @@ __device__ __forceinline__ void tree_plan(const TreeArgs &a, Shared &sh, int sli
 // its node makes it a root.
 template <typename Shared>
 __device__ __forceinline__ void tree_masks(const TreeArgs &a, Shared &sh, int b, int live) {
-    const int i = threadIdx.x;
+    const int i = fresh_tid();
     if (i < kMaxTreeNodes) {
         int up = i < live ? a.parents[static_cast<int64_t>(b) * a.T + i] : -1;
         if (up < 0 || up >= i) up = -1;
@@ -318,10 +377,22 @@ __device__ __forceinline__ void tree_masks(const TreeArgs &a, Shared &sh, int b,
     }
 }
 
-template <typename T, int DP, int R>
-__global__ __launch_bounds__(kTreeBlock) void tree_attention_kernel(TreeArgs a) {
+// Waves that a compute unit's SIMD holds, by the registers that R row tiles
+// need (an accumulator takes DP/4 of them, a block's keys and values DP/2).
+template <typename T, int DP>
+constexpr int tree_waves(int R) {
+    if (DP == 256 || sizeof(T) == 4) return 1;
+    if (DP == 64) return R <= 2 ? 4 : (R <= 4 ? 2 : 1);
+    return R == 1 ? 3 : (R <= 3 ? 2 : 1);
+}
+
+// FULL: a slot has DP elements and the next one follows it, so that the loads of
+// a block share their addresses; otherwise fewer than DP or further apart.
+template <typename T, int DP, int R, bool FULL>
+__global__ __launch_bounds__(kTreeBlock, (tree_waves<T, DP>(R))) void tree_attention_kernel(TreeArgs a) {
     using E = TreeElem<T>;
     using Frag = typename E::Frag;
+    using Raw = typename E::Raw;
     constexpr int kSteps = DP / 32;             // matrix instructions along a key's row
     constexpr int kCols = DP / 16;              // along the output's dimensions
     constexpr int kChunk = kCols < 8 ? kCols : 8;   // elements of a value load
@@ -334,19 +405,33 @@ __global__ __launch_bounds__(kTreeBlock) void tree_attention_kernel(TreeArgs a) 
     const int mt = blockIdx.x / units;
     const int slice = (blockIdx.x % units) / a.KV;
     const int h = blockIdx.x % a.KV;
-    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int i16 = lane & 15, g = lane >> 4;
     const bool chain = a.parents == nullptr;
 
-    int tile, end, b, first;
-    tree_plan(a, sh, slice, blockIdx.x == 0, tile, end, b, first);
+    TreePlace place = tree_plan(a, slice, lane, blockIdx.x == 0 && wave == 0);
+    int tile = place.start, b = place.b, first = place.first;
+    const int end = place.end;
+    TreeSpan span = place.span;
 
+    // this lane's place in a key's row and in a value's; past the row's end
+    // (D < DP) it reads its start, and a key's elements there become 0 (the
+    // queries' are 0 too); the values' dimensions there are never written
+    const int slot_mask = (1 << a.shift) - 1;
+    const int64_t slot_stride = FULL ? DP : a.slot_stride;
     const T *keys = static_cast<const T *>(a.keys) + h * a.head_stride;
     const T *values = static_cast<const T *>(a.values) + h * a.head_stride;
-    const int slot_mask = (1 << a.shift) - 1;
+    int dk[kSteps], dv[kChunks];
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) dk[s] = FULL || 32 * s + 8 * g < a.D ? 32 * s + 8 * g : 0;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+        dv[c] = c * 16 * kChunk + i16 * kChunk;
+        if (!FULL && dv[c] >= a.D) dv[c] = 0;
+    }
 
     while (tile < end) {
-        const TreeSpan span = tree_span(a, b);
         const int nt = tree_tiles(span.keys);
         const int from = tile - first;
         const int to = nt < from + end - tile ? nt : from + end - tile;
@@ -360,29 +445,76 @@ __global__ __launch_bounds__(kTreeBlock) void tree_attention_kernel(TreeArgs a) 
         if (last < span.live && keys_end > span.cached + last + 1)
             keys_end = span.cached + last + 1;
         if (dead) keys_end = 0;
-        const bool nodes_here = !dead && keys_end > span.cached;
-        if (nodes_here && !chain) tree_masks(a, sh, b, span.live);
+        if (!dead && keys_end > span.cached && !chain) tree_masks(a, sh, b, span.live);
 
-        Frag qf[R][kSteps];
-        int node[R];
+        // the queries: a row's operand in the lanes that take it
+        constexpr int kQueries = (R * kSteps * kWave + kTreeBlock - 1) / kTreeBlock;
+        Raw queries[kQueries];
+        const int qt = fresh_tid();
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int row = (mt * R + r) * 16 + i16;
-            node[r] = row / a.G;
-            const bool on = node[r] < span.live;
-            const T *q = static_cast<const T *>(a.q) + b * a.q_batch + node[r] * a.q_node +
-                         (h * a.G + row % a.G) * a.q_head;
-            if (!on) node[r] = -1;
+        for (int k = 0; k < kQueries; ++k) {
+            const int e = k * kTreeBlock + qt;
+            const int s = e / kWave % kSteps, r = e / kWave / kSteps;
+            const int row = (mt * R + r) * 16 + (qt & 15);
+            const int node = row / a.G, d = 32 * s + 8 * (qt >> 4 & 3);
+            queries[k] = Raw{};
+            if (r < R && node < span.live && d < a.D)
+                queries[k] = tree_load8<T>(static_cast<const T *>(a.q) + b * a.q_batch +
+                                           node * a.q_node + (h * a.G + row % a.G) * a.q_head + d);
+        }
+        const int mine = (mt * 16 * R + qt) / a.G;  // the node of row qt
+
+        // the pages of the keys that this lane loads at p0: keys 8(i16/4).. of the
+        // first product, keys 8g.. of the second
+        auto entry_of = [&](int p) {
+            return table[(p < span.keys ? p : span.keys - 1) >> a.shift];
+        };
+        auto is_page = [&](int e) {
+            return static_cast<uint32_t>(e) < static_cast<uint32_t>(a.pages);
+        };
+        Frag kf[2][kSteps];
+        uint32_t vw[kChunks][8][kWords];
+        auto load_keys = [&](int p0, int page) {
+            if (!is_page(page)) page = 0;
+            const T *kp = keys + page * a.page_stride +
+                          (((p0 + 8 * (i16 >> 2)) & slot_mask) + (i16 & 3)) * slot_stride;
 #pragma unroll
-            for (int s = 0; s < kSteps; ++s) {
-                typename E::Raw raw{};
-                const int d = 32 * s + 8 * g;
-                if (on && d < a.D) raw = tree_load8<T>(q + d);
-                qf[r][s] = E::frag(raw);
-            }
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s)
+                    kf[c][s] = E::frag(tree_stream8<T>(kp + 4 * c * slot_stride + dk[s]));
+        };
+        auto load_values = [&](int p0, int page) {
+            if (!is_page(page)) page = 0;
+            const T *vp = values + page * a.page_stride +
+                          ((p0 + 8 * g) & slot_mask) * slot_stride;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c)
+                    tree_load_row<T, kChunk>(vp + j * slot_stride + dv[c], vw[c][j]);
+        };
+        int p0 = from * kTreeTile + wave * kTreeKeys;
+        int page_k = -1, page_v = -1, next_k = -1, next_v = -1;
+        if (p0 < keys_end) {
+            page_k = entry_of(p0 + 8 * (i16 >> 2));
+            page_v = entry_of(p0 + 8 * g);
+            next_k = entry_of(p0 + kTreeTile + 8 * (i16 >> 2));
+            next_v = entry_of(p0 + kTreeTile + 8 * g);
+            load_keys(p0, page_k);
+            load_values(p0, page_v);
         }
 
-        float m[R], l[R];
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kQueries; ++k)
+            if (k * kTreeBlock + qt < R * kSteps * kWave)
+                (&sh.q[0][0][0])[k * kTreeBlock + qt] = queries[k];
+        if (qt < 16 * R) sh.node[qt] = mine < span.live ? mine : -1;
+        if (qt == 0) sh.odd = 0;
+        __syncthreads();
+
+        float m[R], l[R];  // a row's maximum, scaled to powers of two, and the lane's sum
         v4f32 o[R][kCols];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -392,137 +524,161 @@ __global__ __launch_bounds__(kTreeBlock) void tree_attention_kernel(TreeArgs a) 
             for (int t = 0; t < kCols; ++t) o[r][t] = v4f32{0.0f, 0.0f, 0.0f, 0.0f};
         }
 
-        for (int p0 = from * kTreeTile + wave * kTreeKeys; p0 < keys_end; p0 += kTreeTile) {
-            // the pages of the keys that this lane loads: keys 8(i16/4).. of
-            // the first product, keys 8g.. of the second
-            const int pk = p0 + 8 * (i16 >> 2), pv = p0 + 8 * g;
-            int page_k = pk < span.keys ? table[pk >> a.shift] : -1;
-            int page_v = pv < span.keys ? table[pv >> a.shift] : -1;
-            const bool held = static_cast<uint32_t>(page_v) < static_cast<uint32_t>(a.pages);
-            if (static_cast<uint32_t>(page_k) >= static_cast<uint32_t>(a.pages)) page_k = 0;
-            if (!held) page_v = 0;
-            const T *kp = keys + page_k * a.page_stride +
-                          ((pk & slot_mask) + (i16 & 3)) * a.slot_stride;
-            const T *vp = values + page_v * a.page_stride + (pv & slot_mask) * a.slot_stride;
-
-            Frag kf[2][kSteps];
+        v4f32 z[R][2];
+        auto score = [&]() {
+            asm volatile("" ::: "memory");  // the queries are read again, not kept
+            if (!FULL) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                for (int s = 0; s < kSteps; ++s) {
-                    typename E::Raw raw{};
-                    const int d = 32 * s + 8 * g;
-                    if (d < a.D) raw = tree_load8<T>(kp + 4 * c * a.slot_stride + d);
-                    kf[c][s] = E::frag(raw);
-                }
-            uint32_t vw[kChunks][8][kWords];
-#pragma unroll
-            for (int c = 0; c < kChunks; ++c)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int d = c * 16 * kChunk + i16 * kChunk;
-#pragma unroll
-                    for (int k = 0; k < kWords; ++k) vw[c][j][k] = 0;
-                    if (d < a.D) tree_load_row<T, kChunk>(vp + j * a.slot_stride + d, vw[c][j]);
-                }
-
-            // every row sees every key: only cached positions, all of them held
-            const bool plain = __all(held && p0 + kTreeKeys <= span.cached);
-            bool apart = false;  // a node's infinity or NaN, which some rows may not see
-            if (!plain) {
-                bool odd = false;
-#pragma unroll
-                for (int c = 0; c < kChunks; ++c)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const bool there = held && pv + j < span.keys;
-#pragma unroll
-                        for (int k = 0; k < kWords; ++k) {
-                            if (!there) vw[c][j][k] = 0;
-                            odd |= pv + j >= span.cached && tree_nonfinite<T>(vw[c][j][k]);
-                        }
-                    }
-                apart = __any(odd);
+                for (int s = 0; s < kSteps; ++s)
+                    if (32 * s + 8 * g >= a.D) kf[0][s] = kf[1][s] = E::frag(Raw{});
             }
-
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                v4f32 s0 = {0.0f, 0.0f, 0.0f, 0.0f}, s1 = s0;
+                z[r][0] = z[r][1] = v4f32{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int s = 0; s < kSteps; ++s) {
-                    s0 = E::mma(kf[0][s], qf[r][s], s0);
-                    s1 = E::mma(kf[1][s], qf[r][s], s1);
+                    const Frag qf = E::frag(sh.q[r][s][lane]);
+                    z[r][0] = E::mma(kf[0][s], qf, z[r][0]);
+                    z[r][1] = E::mma(kf[1][s], qf, z[r][1]);
                 }
-                float z[8] = {s0[0], s0[1], s0[2], s0[3], s1[0], s1[1], s1[2], s1[3]};
-                if (!plain) {
+            }
+        };
+        auto add_values = [&]() {
+            // a maximum that has been passed moves
+            float top[R];
+            bool behind = false;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int at = pv + j - span.cached;
-                        bool see = held && pv + j < span.keys && node[r] >= 0;
-                        if (see && at >= 0) see = tree_sees(sh.mask, chain, node[r], at);
-                        if (!see) z[j] = -__builtin_inff();
-                    }
-                }
-                float top = z[0];
+            for (int r = 0; r < R; ++r) {
+                float t = z[r][0][0];
 #pragma unroll
-                for (int j = 1; j < 8; ++j) top = fmaxf(top, z[j]);
-                top = fmaxf(m[r], across_groups_max(top));
-                const float ref = top == -__builtin_inff() ? 0.0f : top;
-                const float shift2 = ref * a.scale2;
-                if (__any(top > m[r])) {
-                    const float f = hw_exp2(m[r] * a.scale2 - shift2);
+                for (int j = 1; j < 8; ++j) t = fmaxf(t, z[r][j / 4][j % 4]);
+                top[r] = t * a.scale2;
+                behind |= top[r] > m[r];
+            }
+            if (__builtin_expect(__any(behind), 0)) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float to = fmaxf(m[r], across_groups_max(top[r]));
+                    // a row that has seen nothing keeps -inf
+                    const float f = to == -__builtin_inff() ? 1.0f : hw_exp2(m[r] - to);
                     l[r] *= f;
 #pragma unroll
                     for (int t = 0; t < kCols; ++t) o[r][t] *= f;
-                    m[r] = top;
+                    m[r] = to;
                 }
+            }
+            Frag pf[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float shift = m[r] == -__builtin_inff() ? 0.0f : m[r];
+                float w[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    z[j] = hw_exp2(__builtin_fmaf(z[j], a.scale2, -shift2));
-                    l[r] += z[j];
+                    w[j] = hw_exp2(__builtin_fmaf(z[r][j / 4][j % 4], a.scale2, -shift));
+                    l[r] += w[j];
                 }
-                const Frag pf = E::from(z);
-                if (!apart) {
+                pf[r] = E::from(w);
+            }
 #pragma unroll
-                    for (int c = 0; c < kChunks; ++c)
+            for (int c = 0; c < kChunks; ++c)
 #pragma unroll
-                        for (int t = 0; t < kChunk; ++t)
-                            o[r][c * kChunk + t] = E::mma(tree_column<T, kChunk>(vw[c], t), pf,
-                                                          o[r][c * kChunk + t]);
-                } else {
-                    // key by key, added only where the row sees it
-                    for (int key = 0; key < kTreeKeys; ++key) {
-                        const int at = p0 + key - span.cached;
-                        const bool see = p0 + key < span.keys && node[r] >= 0 &&
-                                         (at < 0 || tree_sees(sh.mask, chain, node[r], at));
+                for (int t = 0; t < kChunk; ++t) {
+                    const Frag vf = tree_column<T, kChunk>(vw[c], t);
 #pragma unroll
-                        for (int c = 0; c < kChunks; ++c) {
-                            uint32_t one[8][kWords];
+                    for (int r = 0; r < R; ++r)
+                        o[r][c * kChunk + t] = E::mma(vf, pf[r], o[r][c * kChunk + t]);
+                }
+        };
+
+        // Blocks in turn.  A block's keys are loaded while the block before is
+        // weighed and added, its values while it is scored itself: each set of
+        // registers is filled again as soon as its products are done.  page_v is
+        // the block's own entry, next_k and next_v the next one's.
+        // The loop runs while every row sees every key (only cached positions, all
+        // of them held) and a block follows, so that its loads are always in
+        // flight; the second one takes the rest: the last block, the nodes, and
+        // everything behind a page that is missing.
+        while (p0 + kTreeTile < keys_end && p0 + kTreeKeys <= span.cached &&
+               __all(is_page(page_v))) {
+            score();
+            load_keys(p0 + kTreeTile, next_k);
+            add_values();
+            p0 += kTreeTile;
+            page_v = next_v;
+            load_values(p0, page_v);
+            next_k = entry_of(p0 + kTreeTile + 8 * (i16 >> 2));
+            next_v = entry_of(p0 + kTreeTile + 8 * g);
+        }
+        while (p0 < keys_end) {
+            const int pv = p0 + 8 * g;
+            const bool held = is_page(page_v) && pv < span.keys;
+            score();
+            // a node's infinities and NaNs, which some rows do not see, are taken
+            // out here and added to the rows that do at the end
+            uint32_t odd = 0;
 #pragma unroll
-                            for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t there = held && pv + j < span.keys ? ~0u : 0u;
+                const uint32_t node = pv + j >= span.cached ? ~0u : 0u;
 #pragma unroll
-                                for (int k = 0; k < kWords; ++k)
-                                    one[j][k] = 8 * g + j == key ? vw[c][j][k] : 0u;
+                for (int c = 0; c < kChunks; ++c)
 #pragma unroll
-                            for (int t = 0; t < kChunk; ++t) {
-                                const v4f32 add = E::mma(tree_column<T, kChunk>(one, t), pf,
-                                                         v4f32{0.0f, 0.0f, 0.0f, 0.0f});
-                                if (see) o[r][c * kChunk + t] += add;
-                            }
-                        }
+                    for (int k = 0; k < kWords; ++k) {
+                        const uint32_t w = vw[c][j][k] & there;
+                        const uint32_t out = (w ^ tree_finite<T>(w)) & node;
+                        odd |= out;
+                        vw[c][j][k] = w ^ out;
                     }
-                }
+            }
+            if (odd) sh.odd = 1;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const uint32_t see =
+                    tree_sees8(sh.mask, chain, sh.node[16 * r + i16], pv - span.cached) &
+                    (held ? 0xFFu >> clamp_len(pv + 8 - span.keys, 8) : 0u);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (!(see >> j & 1)) z[r][j / 4][j % 4] = -__builtin_inff();
+            }
+            add_values();
+            p0 += kTreeTile;
+            if (p0 < keys_end) {
+                load_keys(p0, next_k);
+                page_v = next_v;
+                load_values(p0, page_v);
+                next_k = entry_of(p0 + kTreeTile + 8 * (i16 >> 2));
+                next_v = entry_of(p0 + kTreeTile + 8 * g);
             }
         }
 
+        // The infinities and NaNs among dimensions d.. of the nodes that a row
+        // sees, of this run of tiles: a weight above 0 times one is that again.
+        auto odd_values = [&](int node, int d) {
+            v4f32 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+            const int lo = from * kTreeTile > span.cached ? from * kTreeTile : span.cached;
+            for (int p = lo; p < keys_end; ++p) {
+                const int page = table[p >> a.shift];
+                if (!is_page(page) ||
+                    !tree_sees(sh.mask, chain, node, p - span.cached))
+                    continue;
+                const T *vp = values + page * a.page_stride + (p & slot_mask) * slot_stride + d;
+                for (int t = 0; t < 4; ++t) {
+                    const float v = static_cast<float>(vp[t]);
+                    if (!(__builtin_fabsf(v) < __builtin_inff())) sum[t] += v;
+                }
+            }
+            return sum;
+        };
+
         // join the four waves and leave the rows, or their part
+        const int jt = fresh_tid(), ji = jt & 15, jg = jt >> 4 & 3;
         __syncthreads();
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             l[r] = across_groups_sum(l[r]);
-            if (g == 0) {
-                sh.ml[wave][16 * r + i16][0] = m[r];
-                sh.ml[wave][16 * r + i16][1] = l[r];
+            if (jg == 0) {
+                sh.ml[wave][16 * r + ji][0] = m[r];
+                sh.ml[wave][16 * r + ji][1] = l[r];
             }
         }
         __syncthreads();
@@ -531,10 +687,10 @@ __global__ __launch_bounds__(kTreeBlock) void tree_attention_kernel(TreeArgs a) 
         for (int r = 0; r < R; ++r) {
             float top = -__builtin_inff();
 #pragma unroll
-            for (int w = 0; w < kTreeWaves; ++w) top = fmaxf(top, sh.ml[w][16 * r + i16][0]);
+            for (int w = 0; w < kTreeWaves; ++w) top = fmaxf(top, sh.ml[w][16 * r + ji][0]);
             const float ref = top == -__builtin_inff() ? 0.0f : top;
-            const float f = hw_exp2(m[r] * a.scale2 - ref * a.scale2);
-            // lane: query row i16, dimensions kChunk*(4g + e) + t of each chunk
+            const float f = hw_exp2(m[r] - ref);
+            // lane: query row ji, dimensions kChunk*(4g + e) + t of each chunk
 #pragma unroll
             for (int c = 0; c < kChunks; ++c)
 #pragma unroll
@@ -545,11 +701,11 @@ __global__ __launch_bounds__(kTreeBlock) void tree_attention_kernel(TreeArgs a) 
 #pragma unroll
                         for (int t = 0; t < 4; ++t) v[t] = o[r][c * kChunk + 4 * t4 + t][e] * f;
                         *reinterpret_cast<v4f32 *>(
-                            &sh.merge[wave][i16][c * 16 * kChunk + kChunk * (4 * g + e) +
+                            &sh.merge[wave][ji][c * 16 * kChunk + kChunk * (4 * jg + e) +
                                                  4 * t4]) = v;
                     }
             __syncthreads();
-            const int qr = tid >> 4;  // 16 threads to a row
+            const int qr = jt >> 4;  // 16 threads to a row
             const int row = (mt * R + r) * 16 + qr;
             const int nd = row / a.G;
             float rtop = -__builtin_inff(), sum = 0.0f;
@@ -557,19 +713,21 @@ __global__ __launch_bounds__(kTreeBlock) void tree_attention_kernel(TreeArgs a) 
             for (int w = 0; w < kTreeWaves; ++w) rtop = fmaxf(rtop, sh.ml[w][16 * r + qr][0]);
             const float rref = rtop == -__builtin_inff() ? 0.0f : rtop;
 #pragma unroll
-            for (int w = 0; w < kTreeWaves; ++w)
-                sum += sh.ml[w][16 * r + qr][1] *
-                       hw_exp2(sh.ml[w][16 * r + qr][0] * a.scale2 - rref * a.scale2);
+            for (int w = 0; w < kTreeWaves; ++w) {
+                const float f2 = hw_exp2(sh.ml[w][16 * r + qr][0] - rref);
+                sum += sh.ml[w][16 * r + qr][1] * f2;
+            }
             const bool on = nd < span.live;
             if (nd < a.T && (whole || on)) {
-                const float inv = whole ? (on && !(sum == 0.0f) ? 1.0f / sum : 0.0f) : 1.0f;
+                const float inv = 1.0f / sum;
                 const int64_t orow = (static_cast<int64_t>(b) * a.T + nd) * a.H + h * a.G +
                                      row % a.G;
-                for (int d = (tid & 15) * 4; d < a.D; d += 64) {
+                for (int d = (jt & 15) * 4; d < a.D; d += 64) {
                     v4f32 v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                     for (int w = 0; w < kTreeWaves; ++w)
                         v += *reinterpret_cast<const v4f32 *>(&sh.merge[w][qr][d]);
+                    if (sh.odd && on) v += odd_values(nd, d);
                     if (whole) {
                         T *out = static_cast<T *>(a.out) + orow * a.D + d;
 #pragma unroll
@@ -580,17 +738,16 @@ __global__ __launch_bounds__(kTreeBlock) void tree_attention_kernel(TreeArgs a) 
                         *reinterpret_cast<v4f32 *>(part) = v;
                     }
                 }
-                if ((tid & 15) == 0) {
+                if ((jt & 15) == 0) {
                     if (whole) {
                         if (a.lse)
                             a.lse[orow] = on && !(sum == 0.0f)
                                               ? static_cast<float>(kLn2) *
-                                                    (rref * a.scale2 + hw_log2(sum))
+                                                    (rref + hw_log2(sum))
                                               : -__builtin_inff();
                     } else {
-                        float *ml = a.part_ml + (slot * (16 * R) + 16 * r + qr) * 2;
-                        ml[0] = rtop;
-                        ml[1] = sum;
+                        *reinterpret_cast<v2f32 *>(a.part_ml + (slot * (16 * R) + 16 * r + qr) * 2) =
+                            v2f32{rtop, sum};
                     }
                 }
             }
@@ -599,11 +756,14 @@ __global__ __launch_bounds__(kTreeBlock) void tree_attention_kernel(TreeArgs a) 
         tile += to - from;
         first += nt;
         ++b;
+        if (tile < end) span = tree_span(a, b);
     }
 }
 
-// Joins the parts of a row whose sequence was cut: a wave per row.
-template <typename T>
+// Joins the parts of a row whose sequence was cut: a wave per row.  Its lanes
+// take the parts' references and sums, then 64 / L parts at a time, L lanes to
+// a part's dimensions.
+template <typename T, int L>
 __global__ __launch_bounds__(kTreeBlock) void tree_join_kernel(TreeArgs a, int rows16) {
     const int64_t row_at = static_cast<int64_t>(blockIdx.x) * kTreeWaves + threadIdx.x / kWave;
     const int lane = threadIdx.x & (kWave - 1);
@@ -611,38 +771,68 @@ __global__ __launch_bounds__(kTreeBlock) void tree_join_kernel(TreeArgs a, int r
     const int head = static_cast<int>(row_at % a.H);
     const int nd = static_cast<int>(row_at / a.H % a.T);
     const int b = static_cast<int>(row_at / a.H / a.T);
-    const TreeSpan span = tree_span(a, b);
     const int per = a.first[a.B], first = a.first[b];
+    const TreeSpan span = tree_span(a, b);
     const int w0 = first / per, w1 = (first + tree_tiles(span.keys) - 1) / per;
     if (w0 == w1) return;
     T *out = static_cast<T *>(a.out) + row_at * a.D;
+    const int d = lane % L * 4;
+    if (nd >= span.live) {
+        if (lane < L && d < a.D)
+            for (int t = 0; t < 4; ++t) out[d + t] = static_cast<T>(0.0f);
+        if (lane == 0 && a.lse) a.lse[row_at] = -__builtin_inff();
+        return;
+    }
     const int h = head / a.G;
     const int row = nd * a.G + head % a.G;
-    const int mt = row / rows16, in = row % rows16;
-    float top = -__builtin_inff(), sum = 0.0f;
-    const bool on = nd < span.live;
-    auto at = [&](int w) {
-        const int64_t wg = (static_cast<int64_t>(mt) * a.slices + w) * a.KV + h;
-        return (2 * wg + (w == w0 ? 1 : 0)) * rows16 + in;
+    const int64_t step = static_cast<int64_t>(a.KV) * 2 * rows16;  // from a slice's part to the next's
+    const int64_t at0 = (static_cast<int64_t>(row / rows16) * a.slices * a.KV + h) * 2 * rows16 +
+                        row % rows16;
+    auto at = [&](int w) { return at0 + w * step + (w == w0 ? rows16 : 0); };
+    auto ml_of = [&](int w) {
+        return w <= w1 ? *reinterpret_cast<const v2f32 *>(a.part_ml + at(w) * 2)
+                       : v2f32{-__builtin_inff(), 0.0f};
     };
-    if (on)
-        for (int w = w0; w <= w1; ++w) top = fmaxf(top, a.part_ml[at(w) * 2]);
+    float top = -__builtin_inff();
+    for (int w = w0; w <= w1; w += kWave) top = fmaxf(top, ml_of(w + lane)[0]);
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) top = fmaxf(top, __shfl_xor(top, o, kWave));
     const float ref = top == -__builtin_inff() ? 0.0f : top;
+    float sum = 0.0f;
     v4f32 v = {0.0f, 0.0f, 0.0f, 0.0f};
-    const int d = lane * 4;
-    if (on)
-        for (int w = w0; w <= w1; ++w) {
-            const float f = hw_exp2(a.part_ml[at(w) * 2] * a.scale2 - ref * a.scale2);
-            sum += f * a.part_ml[at(w) * 2 + 1];
-            if (d < a.D) v += *reinterpret_cast<const v4f32 *>(a.part + at(w) * a.D + d) * f;
+    for (int wb = w0; wb <= w1; wb += kWave) {
+        const v2f32 ml = ml_of(wb + lane);
+        const float f = hw_exp2(ml[0] - ref);
+        sum += f * ml[1];
+        const int n = w1 - wb + 1 < kWave ? w1 - wb + 1 : kWave;
+        for (int k0 = 0; k0 < n; k0 += 4 * (kWave / L)) {
+            v4f32 p[4];
+            float fk[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int k = k0 + u * (kWave / L) + lane / L;
+                fk[u] = __shfl(f, k & (kWave - 1), kWave);
+                p[u] = v4f32{0.0f, 0.0f, 0.0f, 0.0f};
+                if (k < n && d < a.D)
+                    p[u] = *reinterpret_cast<const v4f32 *>(a.part + at(wb + k) * a.D + d);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) v += p[u] * fk[u];
         }
-    const bool some = on && !(sum == 0.0f);
-    if (d < a.D) {
+    }
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) sum += __shfl_xor(sum, o, kWave);
+#pragma unroll
+    for (int o = L; o < kWave; o <<= 1)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) v[t] += __shfl_xor(v[t], o, kWave);
+    const bool some = !(sum == 0.0f);
+    if (lane < L && d < a.D) {
 #pragma unroll
         for (int t = 0; t < 4; ++t) out[d + t] = static_cast<T>(some ? v[t] / sum : 0.0f);
     }
     if (lane == 0 && a.lse)
-        a.lse[row_at] = some ? static_cast<float>(kLn2) * (ref * a.scale2 + hw_log2(sum))
+        a.lse[row_at] = some ? static_cast<float>(kLn2) * (ref + hw_log2(sum))
                              : -__builtin_inff();
 }
 

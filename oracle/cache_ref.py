@@ -59,25 +59,31 @@ def tree_attention(q, keys, values, table, lengths, parents=None, num_nodes=None
             continue
         pages = torch.tensor([e for _, e in at])
         slots = torch.tensor([p % page for p, _ in at])
-        see = np.array([[p < cached or above[i, p - cached] for p, _ in at] for i in range(n)])
+        where = np.array([p for p, _ in at])
+        see = (where < cached) | above[:, np.maximum(where - cached, 0)]
         see = torch.from_numpy(see)
+        rows = see.repeat_interleave(G, 0)  # a head's rows, node by node
         for h in range(kv):
             k, v = keys[pages, h, slots].double(), values[pages, h, slots].double()
-            for m in range(h * G, (h + 1) * G):
-                for i in range(n):
-                    on = see[i]
-                    if not on.any():
-                        continue
-                    z = scale * (k[on] @ q[b, i, m])
-                    lse[b, i, m] = torch.logsumexp(z, 0)
-                    if lse[b, i, m] == float("-inf"):
-                        continue
-                    w = torch.exp(z - lse[b, i, m])
-                    out[b, i, m] = w @ v[on]
-                    mass[b, i, m] = w @ v[on].abs()
-                    size[b, i, m] = scale * (k[on].abs() @ q[b, i, m].abs()).max()
-                    seen[b, i, m] = on.sum()
-                    high[b, m] = torch.maximum(high[b, m], v[on].abs().amax(0))
+            heads = slice(h * G, (h + 1) * G)
+            x = q[b, :n, heads].reshape(n * G, D)
+            z = (scale * (x @ k.T)).masked_fill(~rows, float("-inf"))
+            total = torch.logsumexp(z, 1)
+            w = torch.exp(z - total[:, None])
+            w[(total == float("-inf"))] = 0.0
+            # a value that is not finite reaches the rows that see it
+            odd = ~torch.isfinite(v)
+            o = w @ v.masked_fill(odd, 0.0)
+            for p in odd.any(1).nonzero()[:, 0].tolist():
+                o[rows[:, p]] += torch.where(odd[p], v[p], 0.0)
+            u = v.masked_fill(odd, 0.0).abs()
+            big = scale * (x.abs() @ k.abs().T)
+            lse[b, :n, heads] = total.view(n, G)
+            out[b, :n, heads] = o.view(n, G, D)
+            mass[b, :n, heads] = (w @ u).view(n, G, D)
+            size[b, :n, heads] = big.masked_fill(~rows, 0.0).amax(1).view(n, G)
+            seen[b, :n, heads] = rows.sum(1).view(n, G).float()
+            high[b, heads] = u.amax(0)
     return out, lse, mass, size, seen, high
 
 

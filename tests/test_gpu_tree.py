@@ -140,6 +140,21 @@ def test_against_the_definition(dt, shape, tree):
     check(c, call(on_gpu(c), lse=True))
 
 
+# rows of a key head: 16 to a tile, and every number of tiles that has a kernel
+ROWS = [(4, 4), (9, 3), (9, 4), (12, 4), (15, 4), (9, 8), (12, 8), (13, 8), (17, 8), (40, 8)]
+
+
+@pytest.mark.parametrize("dt,D", [(BF16, 128), (F16, 64), (F32, 128), (BF16, 256), (F16, 96),
+                                  (F32, 72)])
+@pytest.mark.parametrize("T,G", ROWS)
+def test_several_tiles_to_a_workgroup(dt, D, T, G):
+    """So many key heads that a workgroup walks along its keys."""
+    kv = 64
+    c = make(T * G, dt, 2, T, kv * G, kv, D, 16, 700, 1500, tree=T % 2 == 1, least=T - 2)
+    c["keys"] = c["keys"] * 1.5
+    check(c, call(on_gpu(c), lse=True))
+
+
 @pytest.mark.parametrize("dt", [BF16, F32])
 @pytest.mark.parametrize("layout,strided", [("slots", False), ("both", True), ("heads", True)])
 def test_layouts(dt, layout, strided):
@@ -211,6 +226,10 @@ def test_missing_pages_are_not_there():
     c["table"][1, 0] = -2 ** 31
     c["table"][2] = -1
     c["table"][3, 3] = 2 ** 31 - 1
+    check(c, call(on_gpu(c), lse=True))
+    # in the middle of a long walk
+    c = make(15, BF16, 1, 3, 256, 128, 64, 16, 1500, 1500)
+    c["table"][0, 20] = -1
     check(c, call(on_gpu(c), lse=True))
 
 
