@@ -95,7 +95,9 @@ bool pools_ok(const spec_cache *c) {
 // ---------------------------------------------------------------------------
 struct TreePlan {
     int dp;      // dimensions, rounded up to what a kernel takes
-    int rt;      // 16-row tiles to a workgroup
+    bool wide;   // rows shared out to the waves, else keys
+    int rt;      // 16-row tiles to a wave
+    int rows;    // of a workgroup
     int waves;   // workgroups to a compute unit
     int mtiles;
     int slices;
@@ -121,45 +123,63 @@ TreePlan plan_tree(const spec_cache *c, int32_t nodes, int32_t heads) {
     TreePlan p;
     p.dp = c->dim <= 64 ? 64 : (c->dim <= 128 ? 128 : 256);
     const int64_t rows = static_cast<int64_t>(nodes) * (heads / c->kv_heads);
-    const int most = c->dtype == SPEC_DTYPE_F32 || p.dp == 256 ? 2 : 4;
-    const int64_t tiles16 = (rows + 15) / 16, splits = (tiles16 + most - 1) / most;
-    p.rt = static_cast<int>((tiles16 + splits - 1) / splits);
-    p.waves = c->dtype == SPEC_DTYPE_F32 ? 1
-              : p.dp == 64               ? tree_waves<__bf16, 64>(p.rt)
-              : p.dp == 128              ? tree_waves<__bf16, 128>(p.rt)
-                                         : tree_waves<__bf16, 256>(p.rt);
-    p.mtiles = static_cast<int>((rows + 16 * p.rt - 1) / (16 * p.rt));
+    const int64_t tiles16 = (rows + 15) / 16;
+    const bool half = c->dtype != SPEC_DTYPE_F32;
+    p.wide = half && tiles16 > (p.dp == 256 ? 1 : 3);
+    if (p.wide) {
+        p.rt = tiles16 > 4 ? 2 : 1;
+        p.rows = 64 * p.rt;
+        p.waves = p.dp == 256 ? 1 : 2;
+    } else {
+        const int most = half ? (p.dp == 256 ? 1 : 3) : 2;
+        const int64_t splits = (tiles16 + most - 1) / most;
+        p.rt = static_cast<int>((tiles16 + splits - 1) / splits);
+        p.rows = 16 * p.rt;
+        p.waves = !half         ? 1
+                  : p.dp == 64  ? tree_waves<__bf16, 64>(p.rt)
+                  : p.dp == 128 ? tree_waves<__bf16, 128>(p.rt)
+                                : tree_waves<__bf16, 256>(p.rt);
+    }
+    p.mtiles = static_cast<int>((rows + p.rows - 1) / p.rows);
     const int64_t units = static_cast<int64_t>(p.mtiles) * c->kv_heads;
     const int64_t tiles =
         c->batch * (static_cast<int64_t>(c->table_width) * c->page_size / kTreeTile + 1);
     int64_t slices = (p.waves * kUnits + units - 1) / units;
     if (slices > tiles) slices = tiles;
     p.slices = static_cast<int>(slices < 1 ? 1 : slices);
-    const int64_t parts = 2 * units * p.slices * 16 * p.rt;
+    const int64_t parts = 2 * units * p.slices * p.rows;
     p.first = 0;
     p.part = align_up((static_cast<size_t>(c->batch) + 1) * sizeof(int32_t));
     p.part_ml = p.part + align_up(static_cast<size_t>(parts) * c->dim * sizeof(float));
-    p.total = p.part_ml + align_up(static_cast<size_t>(parts) * 2 * sizeof(float));
+    p.total = p.part_ml + align_up(static_cast<size_t>(parts) * 4 * sizeof(float));
     return p;
 }
 
 template <typename T, int DP, bool FULL>
 void launch_tree_rt(const TreeArgs &a, const TreePlan &p, hipStream_t st) {
     const dim3 grid(static_cast<unsigned>(p.slices * a.KV * p.mtiles)), block(kTreeBlock);
-    if constexpr (DP <= 128 && sizeof(T) == 2) {
-        if (p.rt == 4) {
-            tree_attention_kernel<T, DP, 4, FULL><<<grid, block, 0, st>>>(a);
+    if constexpr (sizeof(T) == 2) {
+        if (p.wide) {
+            if (p.rt == 2)
+                tree_wide_kernel<T, DP, 2, FULL><<<grid, block, 0, st>>>(a);
+            else
+                tree_wide_kernel<T, DP, 1, FULL><<<grid, block, 0, st>>>(a);
             return;
         }
-        if (p.rt == 3) {
-            tree_attention_kernel<T, DP, 3, FULL><<<grid, block, 0, st>>>(a);
+        if constexpr (DP <= 128) {
+            if (p.rt == 3) {
+                tree_attention_kernel<T, DP, 3, FULL><<<grid, block, 0, st>>>(a);
+                return;
+            }
+        }
+    }
+    if constexpr (DP <= 128 || sizeof(T) == 4) {
+        if (p.rt == 2) {
+            tree_attention_kernel<T, DP, 2, FULL><<<grid, block, 0, st>>>(a);
             return;
         }
     }
-    if (p.rt == 2)
-        tree_attention_kernel<T, DP, 2, FULL><<<grid, block, 0, st>>>(a);
-    else
-        tree_attention_kernel<T, DP, 1, FULL><<<grid, block, 0, st>>>(a);
+    tree_attention_kernel<T, DP, 1, FULL><<<grid, block, 0, st>>>(a);
 }
 
 template <typename T, int DP>
@@ -185,11 +205,11 @@ void launch_join(const TreeArgs &a, const TreePlan &p, hipStream_t st) {
     const int64_t rows = static_cast<int64_t>(a.B) * a.T * a.H;
     const dim3 grid(static_cast<unsigned>((rows + kTreeWaves - 1) / kTreeWaves));
     if (p.dp == 64)
-        tree_join_kernel<T, 16><<<grid, dim3(kTreeBlock), 0, st>>>(a, 16 * p.rt);
+        tree_join_kernel<T, 16><<<grid, dim3(kTreeBlock), 0, st>>>(a, p.rows);
     else if (p.dp == 128)
-        tree_join_kernel<T, 32><<<grid, dim3(kTreeBlock), 0, st>>>(a, 16 * p.rt);
+        tree_join_kernel<T, 32><<<grid, dim3(kTreeBlock), 0, st>>>(a, p.rows);
     else
-        tree_join_kernel<T, 64><<<grid, dim3(kTreeBlock), 0, st>>>(a, 16 * p.rt);
+        tree_join_kernel<T, 64><<<grid, dim3(kTreeBlock), 0, st>>>(a, p.rows);
 }
 
 // ---------------------------------------------------------------------------

@@ -47,7 +47,6 @@ constexpr int kTreeTile = kTreeKeys * kTreeWaves;    // the unit that is dealt o
 constexpr int kMaxTreeNodes = 128;                   // of a tree; chains may be longer
 
 typedef unsigned int v2u32 __attribute__((ext_vector_type(2)));
-typedef float v2f32 __attribute__((ext_vector_type(2)));
 typedef float v4f32 __attribute__((ext_vector_type(4)));
 typedef float v8f32 __attribute__((ext_vector_type(8)));
 typedef __bf16 v8bf16 __attribute__((ext_vector_type(8)));
@@ -64,7 +63,7 @@ struct TreeArgs {
     const int32_t *nodes;    // [B] or null (= T)
     const int32_t *parents;  // [B][T] or null (a chain)
     float *part;             // [workgroup][2][rows][D]: unfinished sums
-    float *part_ml;          // [workgroup][2][rows][2]: their maximum and sum
+    float *part_ml;          // [workgroup][2][rows][4]: reference, sum, divisor of the output
     int32_t *first;          // [B + 1]: sequences' first tiles, then the tiles per slice
     int64_t page_stride, head_stride, slot_stride;  // elements
     int64_t q_batch, q_node, q_head;                // elements
@@ -93,6 +92,10 @@ struct TreeElem16 {
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = x[j];
         return __builtin_convertvector(v, V8);
+    }
+    __device__ static __forceinline__ Frag ones() {
+        const float x[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
+        return from(x);
     }
 };
 
@@ -377,6 +380,42 @@ __device__ __forceinline__ void tree_masks(const TreeArgs &a, Shared &sh, int b,
     }
 }
 
+// Adds the infinities and NaNs among the values of nodes, between positions
+// `from` and `to`, to the rows that see them: a weight above 0 times one is that
+// again.  The workgroup's rows row0 .. row0 + rows - 1 have been written, to out
+// (whole) or to its part.
+template <typename T>
+__device__ __forceinline__ void tree_add_odd(const TreeArgs &a, const uint64_t (*mask)[2],
+                                             const TreeSpan &span, int b, int h, int from, int to,
+                                             bool whole, int64_t slot, int row0, int rows) {
+    __threadfence_block();
+    __syncthreads();
+    const int32_t *table = a.table + static_cast<int64_t>(b) * a.P;
+    for (int e = threadIdx.x; e < rows * a.D; e += kTreeBlock) {
+        const int in = e / a.D, d = e % a.D, row = row0 + in, node = row / a.G;
+        if (node >= span.live) break;
+        float sum = 0.0f;
+        for (int p = from > span.cached ? from : span.cached; p < to; ++p) {
+            const int page = table[p >> a.shift];
+            if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.pages) ||
+                !tree_sees(mask, a.parents == nullptr, node, p - span.cached))
+                continue;
+            const float v = static_cast<float>(static_cast<const T *>(
+                a.values)[page * a.page_stride + h * a.head_stride +
+                          (p & ((1 << a.shift) - 1)) * a.slot_stride + d]);
+            if (!(__builtin_fabsf(v) < __builtin_inff())) sum += v;
+        }
+        if (sum == 0.0f) continue;
+        if (whole) {
+            T *out = static_cast<T *>(a.out) +
+                     ((static_cast<int64_t>(b) * a.T + node) * a.H + h * a.G + row % a.G) * a.D + d;
+            *out = static_cast<T>(static_cast<float>(*out) + sum);
+        } else {
+            a.part[(slot * rows + in) * a.D + d] += sum;
+        }
+    }
+}
+
 // Waves that a compute unit's SIMD holds, by the registers that R row tiles
 // need (an accumulator takes DP/4 of them, a block's keys and values DP/2).
 template <typename T, int DP>
@@ -651,25 +690,6 @@ __global__ __launch_bounds__(kTreeBlock, (tree_waves<T, DP>(R))) void tree_atten
             }
         }
 
-        // The infinities and NaNs among dimensions d.. of the nodes that a row
-        // sees, of this run of tiles: a weight above 0 times one is that again.
-        auto odd_values = [&](int node, int d) {
-            v4f32 sum = {0.0f, 0.0f, 0.0f, 0.0f};
-            const int lo = from * kTreeTile > span.cached ? from * kTreeTile : span.cached;
-            for (int p = lo; p < keys_end; ++p) {
-                const int page = table[p >> a.shift];
-                if (!is_page(page) ||
-                    !tree_sees(sh.mask, chain, node, p - span.cached))
-                    continue;
-                const T *vp = values + page * a.page_stride + (p & slot_mask) * slot_stride + d;
-                for (int t = 0; t < 4; ++t) {
-                    const float v = static_cast<float>(vp[t]);
-                    if (!(__builtin_fabsf(v) < __builtin_inff())) sum[t] += v;
-                }
-            }
-            return sum;
-        };
-
         // join the four waves and leave the rows, or their part
         const int jt = fresh_tid(), ji = jt & 15, jg = jt >> 4 & 3;
         __syncthreads();
@@ -727,7 +747,6 @@ __global__ __launch_bounds__(kTreeBlock, (tree_waves<T, DP>(R))) void tree_atten
 #pragma unroll
                     for (int w = 0; w < kTreeWaves; ++w)
                         v += *reinterpret_cast<const v4f32 *>(&sh.merge[w][qr][d]);
-                    if (sh.odd && on) v += odd_values(nd, d);
                     if (whole) {
                         T *out = static_cast<T *>(a.out) + orow * a.D + d;
 #pragma unroll
@@ -746,13 +765,354 @@ __global__ __launch_bounds__(kTreeBlock, (tree_waves<T, DP>(R))) void tree_atten
                                                     (rref + hw_log2(sum))
                                               : -__builtin_inff();
                     } else {
-                        *reinterpret_cast<v2f32 *>(a.part_ml + (slot * (16 * R) + 16 * r + qr) * 2) =
-                            v2f32{rtop, sum};
+                        *reinterpret_cast<v4f32 *>(a.part_ml + (slot * (16 * R) + 16 * r + qr) * 4) =
+                            v4f32{rtop, sum, sum, 0.0f};
                     }
                 }
             }
             __syncthreads();
         }
+        if (__builtin_expect(sh.odd, 0))
+            tree_add_odd<T>(a, sh.mask, span, b, h, from * kTreeTile, keys_end, whole, slot,
+                            mt * 16 * R, 16 * R);
+        tile += to - from;
+        first += nt;
+        ++b;
+        if (tile < end) span = tree_span(a, b);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Many rows to a key head (wide trees, many heads to a key head, pieces of a
+// prompt): each of the workgroup's four waves takes R row tiles of its own, and
+// all read the same keys and values from shared memory, so that a key's bytes
+// cross the vector registers' load path once for 64 R rows.
+//
+// A tile of kTreeWideKeys keys is in shared memory while the next one is on its
+// way in registers.  Rows lie 16-byte chunk by chunk, chunk c of key k at c xor
+// tree_swizzle(k): the 16 keys that one operand of K Q^T takes, and the 16 that
+// one transposing read of V takes, then lie on different banks.  For V^T P^T
+// that read gives a lane four keys' elements of its dimension.
+//
+// The weights' reference moves only when a score passes it by 2^6: they stay
+// below 2^6 and sums of 2^30 of them far from a float's end.  As the largest
+// weight is then not exactly 1, the output is divided by the sum of the rounded
+// weights, one more matrix product with a row of ones; lse takes the sum of
+// the unrounded ones.
+// ---------------------------------------------------------------------------
+constexpr float kTreeSlack = 6.0f;
+
+template <int DP>
+constexpr int tree_wide_keys() {
+    return DP <= 128 ? 64 : 32;
+}
+
+template <int DP>
+__device__ __forceinline__ int tree_swizzle(int key) {
+    return DP >= 128 ? (key & 3) | (key >> 1 & 12) : (key >> 1 & 1) | (key >> 2 & 6);
+}
+
+typedef short v4i16 __attribute__((ext_vector_type(4)));
+
+template <int DP>
+struct TreeWideShared {
+    v4u32 tile[2][2][tree_wide_keys<DP>() * DP / 8];  // [stage][keys, values]
+    uint64_t mask[kMaxTreeNodes][2];
+    int up[kMaxTreeNodes];
+    int odd;
+};
+
+template <typename T, int DP, int R, bool FULL>
+__global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_kernel(TreeArgs a) {
+    using E = TreeElem<T>;
+    using Frag = typename E::Frag;
+    using Raw = typename E::Raw;
+    constexpr int kKeys = tree_wide_keys<DP>();
+    constexpr int kSteps = DP / 32, kCols = DP / 16, kRow = DP / 8;
+    constexpr int kLoads = kKeys * kRow / kTreeBlock;  // chunks per thread and matrix
+    constexpr int kTile = 64 * R;                      // rows of a workgroup
+    static_assert(kTreeTile % kKeys == 0, "tiles are dealt out in whole ones");
+    __shared__ TreeWideShared<DP> sh;
+
+    const int units = a.slices * a.KV;
+    const int mt = blockIdx.x / units;
+    const int slice = (blockIdx.x % units) / a.KV;
+    const int h = blockIdx.x % a.KV;
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int i16 = lane & 15, g = lane >> 4;
+    const bool chain = a.parents == nullptr;
+
+    TreePlace place = tree_plan(a, slice, lane, blockIdx.x == 0 && wave == 0);
+    int tile = place.start, b = place.b, first = place.first;
+    const int end = place.end;
+    TreeSpan span = place.span;
+
+    const int slot_mask = (1 << a.shift) - 1;
+    const int64_t slot_stride = FULL ? DP : a.slot_stride;
+    const T *keys = static_cast<const T *>(a.keys) + h * a.head_stride;
+    const T *values = static_cast<const T *>(a.values) + h * a.head_stride;
+    if (!FULL) {
+        // chunks past a row's end are never loaded
+        for (int e = tid; e < 4 * kKeys * kRow; e += kTreeBlock)
+            (&sh.tile[0][0][0])[e] = v4u32{0, 0, 0, 0};
+    }
+    // this lane's chunks of a tile: the first one's key, and its place in a row
+    const int key0 = tid / kRow;
+    constexpr int kKeyStep = kTreeBlock / kRow;
+    // and its operands' addresses: chunk 4s + g of key i16's in the instruction's
+    // order, and four dimensions of key 8g + i16/4
+    const int fk = tree_swizzle<DP>(8 * (i16 >> 2) + (i16 & 3));
+    const int fv = tree_swizzle<DP>(8 * g + (i16 >> 2));
+
+    while (tile < end) {
+        const int nt = tree_tiles(span.keys);
+        const int from = tile - first;
+        const int to = nt < from + end - tile ? nt : from + end - tile;
+        const bool whole = from == 0 && to == nt;
+        const bool dead = mt * kTile >= span.live * a.G;  // no row in use
+        const int32_t *table = a.table + static_cast<int64_t>(b) * a.P;
+        const int last = ((mt + 1) * kTile - 1) / a.G;
+        int keys_end = to * kTreeTile < span.keys ? to * kTreeTile : span.keys;
+        if (last < span.live && keys_end > span.cached + last + 1)
+            keys_end = span.cached + last + 1;
+        if (dead) keys_end = 0;
+        const int begin = from * kTreeTile;
+
+        __syncthreads();
+        if (tid == 0) sh.odd = 0;
+        if (keys_end > span.cached && !chain) tree_masks(a, sh, b, span.live);
+
+        // wave w's tile r is the workgroup's tile 4 r + w
+        Frag qf[R][kSteps];
+        int node[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int row = mt * kTile + (4 * r + wave) * 16 + i16;
+            node[r] = row / a.G;
+            if (node[r] >= span.live) node[r] = -1;
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                Raw raw{};
+                const int d = 32 * s + 8 * g;
+                if (node[r] >= 0 && (FULL || d < a.D))
+                    raw = tree_load8<T>(static_cast<const T *>(a.q) + b * a.q_batch +
+                                        node[r] * a.q_node + (h * a.G + row % a.G) * a.q_head + d);
+                qf[r][s] = E::frag(raw);
+            }
+        }
+        float m[R], l[R];
+        v4f32 n[R], o[R][kCols];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            m[r] = -__builtin_inff();
+            l[r] = 0.0f;
+            n[r] = v4f32{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int t = 0; t < kCols; ++t) o[r][t] = v4f32{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+
+        // lane k holds the table entry of key k of a tile
+        auto entry_of = [&](int p0) {
+            const int p = p0 + (lane & (kKeys - 1));
+            return table[(p < span.keys ? p : span.keys - 1) >> a.shift];
+        };
+        auto held_of = [&](int p0, int entry) {
+            return __ballot(p0 + (lane & (kKeys - 1)) < span.keys &&
+                            static_cast<uint32_t>(entry) < static_cast<uint32_t>(a.pages));
+        };
+        v4u32 kr[kLoads], vr[kLoads];
+        auto load = [&](int p0, int entry) {
+#pragma unroll
+            for (int k = 0; k < kLoads; ++k) {
+                const int key = key0 + k * kKeyStep, p = p0 + key;
+                const int c = (tid % kRow) ^ tree_swizzle<DP>(key);
+                int page = __shfl(entry, key, kWave);
+                if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.pages)) page = 0;
+                const int64_t at = page * a.page_stride + (p & slot_mask) * slot_stride + 8 * c;
+                if (FULL || 8 * c < a.D) {
+                    kr[k] = *reinterpret_cast<const v4u32 *>(keys + at);
+                    vr[k] = *reinterpret_cast<const v4u32 *>(values + at);
+                }
+            }
+        };
+        // into a stage; values of positions that are not there become 0, and of
+        // nodes lose their infinities and NaNs
+        auto store = [&](int stage, int p0, uint64_t held) {
+            if (p0 + kKeys > span.cached || ~held) {
+                uint32_t odd = 0;
+#pragma unroll
+                for (int k = 0; k < kLoads; ++k) {
+                    const int key = key0 + k * kKeyStep;
+                    const uint32_t there = held >> key & 1 ? ~0u : 0u;
+                    const uint32_t nodes = p0 + key >= span.cached ? ~0u : 0u;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t w = vr[k][i] & there;
+                        const uint32_t out = (w ^ tree_finite<T>(w)) & nodes;
+                        odd |= out;
+                        vr[k][i] = w ^ out;
+                    }
+                }
+                if (odd) sh.odd = 1;
+            }
+#pragma unroll
+            for (int k = 0; k < kLoads; ++k) {
+                const int key = key0 + k * kKeyStep;
+                if (FULL || 8 * ((tid % kRow) ^ tree_swizzle<DP>(key)) < a.D) {
+                    sh.tile[stage][0][k * kTreeBlock + tid] = kr[k];
+                    sh.tile[stage][1][k * kTreeBlock + tid] = vr[k];
+                }
+            }
+        };
+
+        int entry = 0, entry_next = 0;
+        uint64_t held = 0;
+        if (begin < keys_end) {
+            entry = entry_of(begin);
+            entry_next = entry_of(begin + kKeys);
+            held = held_of(begin, entry);
+            load(begin, entry);
+        }
+        __syncthreads();
+        if (begin < keys_end) store(0, begin, held);
+        __syncthreads();
+
+        int stage = 0;
+        for (int p0 = begin; p0 < keys_end; p0 += kKeys, stage ^= 1) {
+            const bool more = p0 + kKeys < keys_end;
+            uint64_t held_next = 0;
+            if (more) {
+                load(p0 + kKeys, entry_next);
+                held_next = held_of(p0 + kKeys, entry_next);
+                entry_next = entry_of(p0 + 2 * kKeys);
+            }
+            const bool plain = p0 + kKeys <= span.cached && ~held == 0;
+            const v4u32 *kt = sh.tile[stage][0];
+            const char *vt = reinterpret_cast<const char *>(sh.tile[stage][1]);
+#pragma unroll
+            for (int kb = 0; kb < kKeys / kTreeKeys; ++kb) {
+                v4f32 z[R][2];
+#pragma unroll
+                for (int r = 0; r < R; ++r) z[r][0] = z[r][1] = v4f32{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int key = 32 * kb + 8 * (i16 >> 2) + 4 * c + (i16 & 3);
+                        Raw raw;
+                        raw.w = kt[key * kRow + ((4 * s + g) ^ fk)];
+#pragma unroll
+                        for (int r = 0; r < R; ++r)
+                            z[r][c] = E::mma(E::frag(raw), qf[r][s], z[r][c]);
+                    }
+                if (!plain) {
+                    const int pv = p0 + 32 * kb + 8 * g;
+                    const uint32_t there = static_cast<uint32_t>(held >> (32 * kb + 8 * g)) & 0xFFu;
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        const uint32_t see =
+                            tree_sees8(sh.mask, chain, node[r], pv - span.cached) & there;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (!(see >> j & 1)) z[r][j / 4][j % 4] = -__builtin_inff();
+                    }
+                }
+                float top[R];
+                bool behind = false;
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    float t = z[r][0][0];
+#pragma unroll
+                    for (int j = 1; j < 8; ++j) t = fmaxf(t, z[r][j / 4][j % 4]);
+                    top[r] = t * a.scale2;
+                    behind |= top[r] > m[r] + kTreeSlack;
+                }
+                if (__builtin_expect(__any(behind), 0)) {
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        const float up = fmaxf(m[r], across_groups_max(top[r]));
+                        const float f = up == -__builtin_inff() ? 1.0f : hw_exp2(m[r] - up);
+                        l[r] *= f;
+                        n[r] *= f;
+#pragma unroll
+                        for (int t = 0; t < kCols; ++t) o[r][t] *= f;
+                        m[r] = up;
+                    }
+                }
+                Frag pf[R];
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float shift = m[r] == -__builtin_inff() ? 0.0f : m[r];
+                    float w[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        w[j] = hw_exp2(__builtin_fmaf(z[r][j / 4][j % 4], a.scale2, -shift));
+                        l[r] += w[j];
+                    }
+                    pf[r] = E::from(w);
+                    n[r] = E::mma(E::ones(), pf[r], n[r]);
+                }
+#pragma unroll
+                for (int t = 0; t < kCols; ++t) {
+                    v4i16 half[2];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int key = 32 * kb + 8 * g + 4 * u + (i16 >> 2);
+                        const int c = (2 * t + (i16 >> 1 & 1)) ^ fv;
+                        half[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                            (__attribute__((address_space(3))) v4i16 *)(vt + (key * kRow + c) * 16 +
+                                                                       (i16 & 1) * 8));
+                    }
+                    const Frag vf = __builtin_bit_cast(
+                        Frag, __builtin_shufflevector(half[0], half[1], 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+                    for (int r = 0; r < R; ++r) o[r][t] = E::mma(vf, pf[r], o[r][t]);
+                }
+            }
+            held = held_next;
+            if (more) store(stage ^ 1, p0 + kKeys, held);
+            __syncthreads();
+        }
+
+        // leave the rows, or their part
+        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (from == 0 ? 1 : 0);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int in = (4 * r + wave) * 16 + i16, row = mt * kTile + in;
+            const int nd = row / a.G;
+            const float sum = across_groups_sum(l[r]);
+            const bool on = node[r] >= 0, some = on && !(sum == 0.0f);
+            if (nd >= a.T || !(whole || on)) continue;
+            const int64_t orow = (static_cast<int64_t>(b) * a.T + nd) * a.H + h * a.G + row % a.G;
+            const float inv = 1.0f / n[r][0];
+#pragma unroll
+            for (int t = 0; t < kCols; ++t) {
+                const int d = 16 * t + 4 * g;
+                if (!FULL && d >= a.D) continue;
+                const v4f32 v = o[r][t];
+                if (whole) {
+                    T x[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) x[k] = static_cast<T>(some ? v[k] * inv : 0.0f);
+                    *reinterpret_cast<v2u32 *>(static_cast<T *>(a.out) + orow * a.D + d) =
+                        __builtin_bit_cast(v2u32, x);
+                } else {
+                    *reinterpret_cast<v4f32 *>(a.part + (slot * kTile + in) * a.D + d) = v;
+                }
+            }
+            if (g == 0) {
+                if (!whole)
+                    *reinterpret_cast<v4f32 *>(a.part_ml + (slot * kTile + in) * 4) =
+                        v4f32{m[r], sum, n[r][0], 0.0f};
+                else if (a.lse)
+                    a.lse[orow] = some ? static_cast<float>(kLn2) * (m[r] + hw_log2(sum))
+                                       : -__builtin_inff();
+            }
+        }
+        if (__builtin_expect(sh.odd, 0))
+            tree_add_odd<T>(a, sh.mask, span, b, h, begin, keys_end, whole, slot, mt * kTile,
+                            kTile);
         tile += to - from;
         first += nt;
         ++b;
@@ -790,20 +1150,21 @@ __global__ __launch_bounds__(kTreeBlock) void tree_join_kernel(TreeArgs a, int r
                         row % rows16;
     auto at = [&](int w) { return at0 + w * step + (w == w0 ? rows16 : 0); };
     auto ml_of = [&](int w) {
-        return w <= w1 ? *reinterpret_cast<const v2f32 *>(a.part_ml + at(w) * 2)
-                       : v2f32{-__builtin_inff(), 0.0f};
+        return w <= w1 ? *reinterpret_cast<const v4f32 *>(a.part_ml + at(w) * 4)
+                       : v4f32{-__builtin_inff(), 0.0f, 0.0f, 0.0f};
     };
     float top = -__builtin_inff();
     for (int w = w0; w <= w1; w += kWave) top = fmaxf(top, ml_of(w + lane)[0]);
 #pragma unroll
     for (int o = 1; o < kWave; o <<= 1) top = fmaxf(top, __shfl_xor(top, o, kWave));
     const float ref = top == -__builtin_inff() ? 0.0f : top;
-    float sum = 0.0f;
+    float sum = 0.0f, norm = 0.0f;
     v4f32 v = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int wb = w0; wb <= w1; wb += kWave) {
-        const v2f32 ml = ml_of(wb + lane);
+        const v4f32 ml = ml_of(wb + lane);
         const float f = hw_exp2(ml[0] - ref);
         sum += f * ml[1];
+        norm += f * ml[2];
         const int n = w1 - wb + 1 < kWave ? w1 - wb + 1 : kWave;
         for (int k0 = 0; k0 < n; k0 += 4 * (kWave / L)) {
             v4f32 p[4];
@@ -821,7 +1182,10 @@ __global__ __launch_bounds__(kTreeBlock) void tree_join_kernel(TreeArgs a, int r
         }
     }
 #pragma unroll
-    for (int o = 1; o < kWave; o <<= 1) sum += __shfl_xor(sum, o, kWave);
+    for (int o = 1; o < kWave; o <<= 1) {
+        sum += __shfl_xor(sum, o, kWave);
+        norm += __shfl_xor(norm, o, kWave);
+    }
 #pragma unroll
     for (int o = L; o < kWave; o <<= 1)
 #pragma unroll
@@ -829,7 +1193,7 @@ __global__ __launch_bounds__(kTreeBlock) void tree_join_kernel(TreeArgs a, int r
     const bool some = !(sum == 0.0f);
     if (lane < L && d < a.D) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) out[d + t] = static_cast<T>(some ? v[t] / sum : 0.0f);
+        for (int t = 0; t < 4; ++t) out[d + t] = static_cast<T>(some ? v[t] / norm : 0.0f);
     }
     if (lane == 0 && a.lse)
         a.lse[row_at] = some ? static_cast<float>(kLn2) * (ref + hw_log2(sum))
