@@ -788,8 +788,8 @@ __global__ __launch_bounds__(kTreeBlock, (tree_waves<T, DP>(R))) void tree_atten
 // all read the same keys and values from shared memory, so that a key's bytes
 // cross the vector registers' load path once for 64 R rows.
 //
-// A tile of kTreeWideKeys keys is in shared memory while the next one is on its
-// way in registers.  Rows lie 16-byte chunk by chunk, chunk c of key k at c xor
+// A tile of keys is in shared memory while the next one is on its way there,
+// past the registers.  Rows lie 16-byte chunk by chunk, chunk c of key k at c xor
 // tree_swizzle(k): the 16 keys that one operand of K Q^T takes, and the 16 that
 // one transposing read of V takes, then lie on different banks.  For V^T P^T
 // that read gives a lane four keys' elements of its dimension.
@@ -801,6 +801,19 @@ __global__ __launch_bounds__(kTreeBlock, (tree_waves<T, DP>(R))) void tree_atten
 // the unrounded ones.
 // ---------------------------------------------------------------------------
 constexpr float kTreeSlack = 6.0f;
+
+// 16 bytes a lane from memory to the wave's 1024 bytes of shared memory at lds,
+// lane by lane; lanes that are off leave their places.  The load has no
+// destination register and the compiler does not know of it, so that reading
+// another stage does not wait for it; tree_loads_done() does.  Nothing else in the
+// kernel uses m0 (shared memory needs none on this architecture).
+__device__ __forceinline__ void tree_load_lds(const void *p, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p)
+                 : "memory");
+}
+__device__ __forceinline__ void tree_loads_done() {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
 
 template <int DP>
 constexpr int tree_wide_keys() {
@@ -862,6 +875,10 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
     constexpr int kKeyStep = kTreeBlock / kRow;
     // and its operands' addresses: chunk 4s + g of key i16's in the instruction's
     // order, and four dimensions of key 8g + i16/4
+    constexpr uint32_t kStageBytes = kKeys * kRow * 16;
+    const uint32_t lds0 = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(
+        reinterpret_cast<size_t>((__attribute__((address_space(3))) v4u32 *)&sh.tile[0][0][0]) +
+        wave * kWave * 16));
     const int fk = tree_swizzle<DP>(8 * (i16 >> 2) + (i16 & 3));
     const int fv = tree_swizzle<DP>(8 * g + (i16 >> 2));
 
@@ -921,8 +938,9 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
             return __ballot(p0 + (lane & (kKeys - 1)) < span.keys &&
                             static_cast<uint32_t>(entry) < static_cast<uint32_t>(a.pages));
         };
-        v4u32 kr[kLoads], vr[kLoads];
-        auto load = [&](int p0, int entry) {
+        // a tile's keys and values on their way to a stage
+        auto load = [&](int stage, int p0, int entry) {
+            const uint32_t to_k = lds0 + stage * 2 * kStageBytes, to_v = to_k + kStageBytes;
 #pragma unroll
             for (int k = 0; k < kLoads; ++k) {
                 const int key = key0 + k * kKeyStep, p = p0 + key;
@@ -931,70 +949,41 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
                 if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.pages)) page = 0;
                 const int64_t at = page * a.page_stride + (p & slot_mask) * slot_stride + 8 * c;
                 if (FULL || 8 * c < a.D) {
-                    kr[k] = *reinterpret_cast<const v4u32 *>(keys + at);
-                    vr[k] = *reinterpret_cast<const v4u32 *>(values + at);
+                    tree_load_lds(keys + at, to_k + k * kTreeBlock * 16);
+                    tree_load_lds(values + at, to_v + k * kTreeBlock * 16);
                 }
             }
         };
-        // into a stage; values of positions that are not there become 0, and of
-        // nodes lose their infinities and NaNs
-        auto store = [&](int stage, int p0, uint64_t held) {
-            if (p0 + kKeys > span.cached || ~held) {
-                uint32_t odd = 0;
-#pragma unroll
-                for (int k = 0; k < kLoads; ++k) {
-                    const int key = key0 + k * kKeyStep;
-                    const uint32_t there = held >> key & 1 ? ~0u : 0u;
-                    const uint32_t nodes = p0 + key >= span.cached ? ~0u : 0u;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t w = vr[k][i] & there;
-                        const uint32_t out = (w ^ tree_finite<T>(w)) & nodes;
-                        odd |= out;
-                        vr[k][i] = w ^ out;
-                    }
-                }
-                if (odd) sh.odd = 1;
-            }
+        // Values of positions that are not there become 0, and of nodes lose their
+        // infinities and NaNs: each thread looks through the chunks it loaded.
+        auto clean = [&](int stage, int p0, uint64_t held) {
+            uint32_t odd = 0;
 #pragma unroll
             for (int k = 0; k < kLoads; ++k) {
                 const int key = key0 + k * kKeyStep;
-                if (FULL || 8 * ((tid % kRow) ^ tree_swizzle<DP>(key)) < a.D) {
-                    sh.tile[stage][0][k * kTreeBlock + tid] = kr[k];
-                    sh.tile[stage][1][k * kTreeBlock + tid] = vr[k];
+                const uint32_t there = held >> key & 1 ? ~0u : 0u;
+                const uint32_t nodes = p0 + key >= span.cached ? ~0u : 0u;
+                v4u32 v = sh.tile[stage][1][k * kTreeBlock + tid];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t w = v[i] & there;
+                    const uint32_t out = (w ^ tree_finite<T>(w)) & nodes;
+                    odd |= out;
+                    v[i] = w ^ out;
                 }
+                sh.tile[stage][1][k * kTreeBlock + tid] = v;
             }
+            if (odd) sh.odd = 1;
         };
-
-        int entry = 0, entry_next = 0;
-        uint64_t held = 0;
-        if (begin < keys_end) {
-            entry = entry_of(begin);
-            entry_next = entry_of(begin + kKeys);
-            held = held_of(begin, entry);
-            load(begin, entry);
-        }
-        __syncthreads();
-        if (begin < keys_end) store(0, begin, held);
-        __syncthreads();
-
-        int stage = 0;
-        for (int p0 = begin; p0 < keys_end; p0 += kKeys, stage ^= 1) {
-            const bool more = p0 + kKeys < keys_end;
-            uint64_t held_next = 0;
-            if (more) {
-                load(p0 + kKeys, entry_next);
-                held_next = held_of(p0 + kKeys, entry_next);
-                entry_next = entry_of(p0 + 2 * kKeys);
-            }
-            const bool plain = p0 + kKeys <= span.cached && ~held == 0;
+        constexpr int kBlocks = kKeys / kTreeKeys;
+        v4f32 z[kBlocks][R][2];
+        auto score = [&](int stage) {
             const v4u32 *kt = sh.tile[stage][0];
-            const char *vt = reinterpret_cast<const char *>(sh.tile[stage][1]);
 #pragma unroll
-            for (int kb = 0; kb < kKeys / kTreeKeys; ++kb) {
-                v4f32 z[R][2];
+            for (int kb = 0; kb < kBlocks; ++kb) {
 #pragma unroll
-                for (int r = 0; r < R; ++r) z[r][0] = z[r][1] = v4f32{0.0f, 0.0f, 0.0f, 0.0f};
+                for (int r = 0; r < R; ++r)
+                    z[kb][r][0] = z[kb][r][1] = v4f32{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int s = 0; s < kSteps; ++s)
 #pragma unroll
@@ -1004,42 +993,37 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
                         raw.w = kt[key * kRow + ((4 * s + g) ^ fk)];
 #pragma unroll
                         for (int r = 0; r < R; ++r)
-                            z[r][c] = E::mma(E::frag(raw), qf[r][s], z[r][c]);
+                            z[kb][r][c] = E::mma(E::frag(raw), qf[r][s], z[kb][r][c]);
                     }
-                if (!plain) {
-                    const int pv = p0 + 32 * kb + 8 * g;
-                    const uint32_t there = static_cast<uint32_t>(held >> (32 * kb + 8 * g)) & 0xFFu;
+            }
+        };
+        auto add_values = [&](int stage) {
+            const char *vt = reinterpret_cast<const char *>(sh.tile[stage][1]);
+            float top[R];
+            bool behind = false;
 #pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        const uint32_t see =
-                            tree_sees8(sh.mask, chain, node[r], pv - span.cached) & there;
+            for (int r = 0; r < R; ++r) {
+                float t = z[0][r][0][0];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            if (!(see >> j & 1)) z[r][j / 4][j % 4] = -__builtin_inff();
-                    }
-                }
-                float top[R];
-                bool behind = false;
+                for (int j = 1; j < 8 * kBlocks; ++j)
+                    t = fmaxf(t, z[j / 8][r][j / 4 % 2][j % 4]);
+                top[r] = t * a.scale2;
+                behind |= top[r] > m[r] + kTreeSlack;
+            }
+            if (__builtin_expect(__any(behind), 0)) {
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    float t = z[r][0][0];
+                    const float up = fmaxf(m[r], across_groups_max(top[r]));
+                    const float f = up == -__builtin_inff() ? 1.0f : hw_exp2(m[r] - up);
+                    l[r] *= f;
+                    n[r] *= f;
 #pragma unroll
-                    for (int j = 1; j < 8; ++j) t = fmaxf(t, z[r][j / 4][j % 4]);
-                    top[r] = t * a.scale2;
-                    behind |= top[r] > m[r] + kTreeSlack;
+                    for (int t = 0; t < kCols; ++t) o[r][t] *= f;
+                    m[r] = up;
                 }
-                if (__builtin_expect(__any(behind), 0)) {
+            }
 #pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        const float up = fmaxf(m[r], across_groups_max(top[r]));
-                        const float f = up == -__builtin_inff() ? 1.0f : hw_exp2(m[r] - up);
-                        l[r] *= f;
-                        n[r] *= f;
-#pragma unroll
-                        for (int t = 0; t < kCols; ++t) o[r][t] *= f;
-                        m[r] = up;
-                    }
-                }
+            for (int kb = 0; kb < kBlocks; ++kb) {
                 Frag pf[R];
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
@@ -1047,7 +1031,7 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
                     float w[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        w[j] = hw_exp2(__builtin_fmaf(z[r][j / 4][j % 4], a.scale2, -shift));
+                        w[j] = hw_exp2(__builtin_fmaf(z[kb][r][j / 4][j % 4], a.scale2, -shift));
                         l[r] += w[j];
                     }
                     pf[r] = E::from(w);
@@ -1070,8 +1054,60 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
                     for (int r = 0; r < R; ++r) o[r][t] = E::mma(vf, pf[r], o[r][t]);
                 }
             }
-            held = held_next;
-            if (more) store(stage ^ 1, p0 + kKeys, held);
+        };
+
+        // entry and held: the tile's own; entry_next: the following one's
+        int entry = 0, entry_next = 0, p0 = begin, stage = 0;
+        uint64_t held = 0;
+        __syncthreads();  // the stages are free
+        if (p0 < keys_end) {
+            entry = entry_of(p0);
+            entry_next = entry_of(p0 + kKeys);
+            held = held_of(p0, entry);
+            load(0, p0, entry);
+            tree_loads_done();
+        }
+        __syncthreads();
+        // while every row sees every key and a tile follows, which is on its way
+        // meanwhile; then the rest: the last tile, the nodes, and everything behind
+        // a page that is missing
+        while (p0 + kKeys < keys_end && p0 + kKeys <= span.cached && ~held == 0) {
+            load(stage ^ 1, p0 + kKeys, entry_next);
+            held = held_of(p0 + kKeys, entry_next);
+            entry_next = entry_of(p0 + 2 * kKeys);
+            score(stage);
+            add_values(stage);
+            p0 += kKeys;
+            stage ^= 1;
+            tree_loads_done();
+            __syncthreads();
+        }
+        while (p0 < keys_end) {
+            clean(stage, p0, held);
+            __syncthreads();
+            score(stage);
+#pragma unroll
+            for (int kb = 0; kb < kBlocks; ++kb) {
+                const uint32_t there = static_cast<uint32_t>(held >> (32 * kb + 8 * g)) & 0xFFu;
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const uint32_t see =
+                        tree_sees8(sh.mask, chain, node[r], p0 + 32 * kb + 8 * g - span.cached) &
+                        there;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (!(see >> j & 1)) z[kb][r][j / 4][j % 4] = -__builtin_inff();
+                }
+            }
+            add_values(stage);
+            p0 += kKeys;
+            if (p0 < keys_end) {
+                stage ^= 1;  // free since the last barrier
+                load(stage, p0, entry_next);
+                held = held_of(p0, entry_next);
+                entry_next = entry_of(p0 + kKeys);
+                tree_loads_done();
+            }
             __syncthreads();
         }
 
