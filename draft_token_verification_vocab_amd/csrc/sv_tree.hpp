@@ -801,6 +801,9 @@ __global__ __launch_bounds__(kTreeBlock, (tree_waves<T, DP>(R))) void tree_atten
 // the unrounded ones.
 // ---------------------------------------------------------------------------
 constexpr float kTreeSlack = 6.0f;
+// What may be moved past a scheduling barrier: ordinary arithmetic, which then
+// fills the time of the matrix products around it.
+constexpr int kTreeArith = 0x406;
 
 // 16 bytes a lane from memory to the wave's 1024 bytes of shared memory at lds,
 // lane by lane; lanes that are off leave their places.  The load has no
@@ -903,15 +906,16 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
         // wave w's tile r is the workgroup's tile 4 r + w
         Frag qf[R][kSteps];
         int node[R];
+        const int qt = fresh_tid();
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const int row = mt * kTile + (4 * r + wave) * 16 + i16;
+            const int row = mt * kTile + (4 * r + wave) * 16 + (qt & 15);
             node[r] = row / a.G;
             if (node[r] >= span.live) node[r] = -1;
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
                 Raw raw{};
-                const int d = 32 * s + 8 * g;
+                const int d = 32 * s + 8 * (qt >> 4 & 3);
                 if (node[r] >= 0 && (FULL || d < a.D))
                     raw = tree_load8<T>(static_cast<const T *>(a.q) + b * a.q_batch +
                                         node[r] * a.q_node + (h * a.G + row % a.G) * a.q_head + d);
@@ -941,16 +945,23 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
         // a tile's keys and values on their way to a stage
         auto load = [&](int stage, int p0, int entry) {
             const uint32_t to_k = lds0 + stage * 2 * kStageBytes, to_v = to_k + kStageBytes;
+            // lane k: where key k's row begins
+            if (static_cast<uint32_t>(entry) >= static_cast<uint32_t>(a.pages)) entry = 0;
+            const int64_t row = (entry * a.page_stride +
+                                 ((p0 + (lane & (kKeys - 1))) & slot_mask) * slot_stride) *
+                                static_cast<int64_t>(sizeof(T));
 #pragma unroll
             for (int k = 0; k < kLoads; ++k) {
-                const int key = key0 + k * kKeyStep, p = p0 + key;
+                const int key = key0 + k * kKeyStep;
                 const int c = (tid % kRow) ^ tree_swizzle<DP>(key);
-                int page = __shfl(entry, key, kWave);
-                if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.pages)) page = 0;
-                const int64_t at = page * a.page_stride + (p & slot_mask) * slot_stride + 8 * c;
+                const uint32_t lo = __shfl(static_cast<int>(row), key, kWave);
+                const uint32_t hi = __shfl(static_cast<int>(row >> 32), key, kWave);
+                const int64_t at = (static_cast<int64_t>(hi) << 32 | lo) + 16 * c;
                 if (FULL || 8 * c < a.D) {
-                    tree_load_lds(keys + at, to_k + k * kTreeBlock * 16);
-                    tree_load_lds(values + at, to_v + k * kTreeBlock * 16);
+                    tree_load_lds(reinterpret_cast<const char *>(keys) + at,
+                                  to_k + k * kTreeBlock * 16);
+                    tree_load_lds(reinterpret_cast<const char *>(values) + at,
+                                  to_v + k * kTreeBlock * 16);
                 }
             }
         };
@@ -979,22 +990,28 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
         v4f32 z[kBlocks][R][2];
         auto score = [&](int stage) {
             const v4u32 *kt = sh.tile[stage][0];
+            // operands are read kAhead products before they are needed; the
+            // barriers keep reads and products in this order
+            constexpr int kAll = kBlocks * kSteps * 2, kAhead = 4;
+            Raw kf[kAhead];
+            auto operand = [&](int i) {
+                const int c = i % 2, s = i / 2 % kSteps, kb = i / 2 / kSteps;
+                const int key = 32 * kb + 8 * (i16 >> 2) + 4 * c + (i16 & 3);
+                kf[i % kAhead].w = kt[key * kRow + ((4 * s + g) ^ fk)];
+            };
 #pragma unroll
-            for (int kb = 0; kb < kBlocks; ++kb) {
+            for (int i = 0; i < kAhead; ++i) operand(i);
+#pragma unroll
+            for (int i = 0; i < kAll; ++i) {
+                const int c = i % 2, s = i / 2 % kSteps, kb = i / 2 / kSteps;
+                __builtin_amdgcn_sched_barrier(kTreeArith);
 #pragma unroll
                 for (int r = 0; r < R; ++r)
-                    z[kb][r][0] = z[kb][r][1] = v4f32{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const int key = 32 * kb + 8 * (i16 >> 2) + 4 * c + (i16 & 3);
-                        Raw raw;
-                        raw.w = kt[key * kRow + ((4 * s + g) ^ fk)];
-#pragma unroll
-                        for (int r = 0; r < R; ++r)
-                            z[kb][r][c] = E::mma(E::frag(raw), qf[r][s], z[kb][r][c]);
-                    }
+                    z[kb][r][c] =
+                        E::mma(E::frag(kf[i % kAhead]), qf[r][s],
+                               s == 0 ? v4f32{0.0f, 0.0f, 0.0f, 0.0f} : z[kb][r][c]);
+                __builtin_amdgcn_sched_barrier(kTreeArith);
+                if (i + kAhead < kAll) operand(i + kAhead);
             }
         };
         auto add_values = [&](int stage) {
@@ -1022,37 +1039,58 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
                     m[r] = up;
                 }
             }
+            // the values' operands, read kAhead products before they are needed
+            constexpr int kAll = kBlocks * kCols, kAhead = 4;
+            Frag vf[kAhead];
+            auto operand = [&](int i) {
+                v4i16 half[2];
 #pragma unroll
-            for (int kb = 0; kb < kBlocks; ++kb) {
-                Frag pf[R];
+                for (int u = 0; u < 2; ++u) {
+                    const int key = 32 * (i / kCols) + 8 * g + 4 * u + (i16 >> 2);
+                    const int c = (2 * (i % kCols) + (i16 >> 1 & 1)) ^ fv;
+                    half[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                        (__attribute__((address_space(3))) v4i16 *)(vt + (key * kRow + c) * 16 +
+                                                                   (i16 & 1) * 8));
+                }
+                vf[i % kAhead] = __builtin_bit_cast(
+                    Frag, __builtin_shufflevector(half[0], half[1], 0, 1, 2, 3, 4, 5, 6, 7));
+            };
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) operand(i);
+            float shift[R], w[kBlocks][R][8];
+#pragma unroll
+            for (int r = 0; r < R; ++r) shift[r] = m[r] == -__builtin_inff() ? 0.0f : m[r];
+            auto weigh = [&](int kb, int j) {
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    const float shift = m[r] == -__builtin_inff() ? 0.0f : m[r];
-                    float w[8];
+                    w[kb][r][j] =
+                        hw_exp2(__builtin_fmaf(z[kb][r][j / 4][j % 4], a.scale2, -shift[r]));
+                    l[r] += w[kb][r][j];
+                }
+            };
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        w[j] = hw_exp2(__builtin_fmaf(z[kb][r][j / 4][j % 4], a.scale2, -shift));
-                        l[r] += w[j];
+            for (int j = 0; j < 8; ++j) weigh(0, j);
+            Frag pf[R];
+#pragma unroll
+            for (int i = 0; i < kAll; ++i) {
+                const int kb = i / kCols, t = i % kCols;
+                if (t == 0) {
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        pf[r] = E::from(w[kb][r]);
+                        n[r] = E::mma(E::ones(), pf[r], n[r]);
                     }
-                    pf[r] = E::from(w);
-                    n[r] = E::mma(E::ones(), pf[r], n[r]);
                 }
 #pragma unroll
-                for (int t = 0; t < kCols; ++t) {
-                    v4i16 half[2];
+                for (int r = 0; r < R; ++r) o[r][t] = E::mma(vf[i % kAhead], pf[r], o[r][t]);
+                __builtin_amdgcn_sched_barrier(kTreeArith);
+                if (i + kAhead < kAll) operand(i + kAhead);
+                // the next block's weights between this one's products
+                if (kb + 1 < kBlocks) {
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const int key = 32 * kb + 8 * g + 4 * u + (i16 >> 2);
-                        const int c = (2 * t + (i16 >> 1 & 1)) ^ fv;
-                        half[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                            (__attribute__((address_space(3))) v4i16 *)(vt + (key * kRow + c) * 16 +
-                                                                       (i16 & 1) * 8));
-                    }
-                    const Frag vf = __builtin_bit_cast(
-                        Frag, __builtin_shufflevector(half[0], half[1], 0, 1, 2, 3, 4, 5, 6, 7));
-#pragma unroll
-                    for (int r = 0; r < R; ++r) o[r][t] = E::mma(vf, pf[r], o[r][t]);
+                    for (int j = t * 8 / kCols; j < (t + 1) * 8 / kCols; ++j) weigh(kb + 1, j);
                 }
+                __builtin_amdgcn_sched_barrier(0);
             }
         };
 
@@ -1112,10 +1150,11 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
         }
 
         // leave the rows, or their part
+        const int jt = fresh_tid(), ji = jt & 15, jg = jt >> 4 & 3;
         const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (from == 0 ? 1 : 0);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const int in = (4 * r + wave) * 16 + i16, row = mt * kTile + in;
+            const int in = (4 * r + wave) * 16 + ji, row = mt * kTile + in;
             const int nd = row / a.G;
             const float sum = across_groups_sum(l[r]);
             const bool on = node[r] >= 0, some = on && !(sum == 0.0f);
@@ -1124,7 +1163,7 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
             const float inv = 1.0f / n[r][0];
 #pragma unroll
             for (int t = 0; t < kCols; ++t) {
-                const int d = 16 * t + 4 * g;
+                const int d = 16 * t + 4 * jg;
                 if (!FULL && d >= a.D) continue;
                 const v4f32 v = o[r][t];
                 if (whole) {
@@ -1137,7 +1176,7 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
                     *reinterpret_cast<v4f32 *>(a.part + (slot * kTile + in) * a.D + d) = v;
                 }
             }
-            if (g == 0) {
+            if (jg == 0) {
                 if (!whole)
                     *reinterpret_cast<v4f32 *>(a.part_ml + (slot * kTile + in) * 4) =
                         v4f32{m[r], sum, n[r][0], 0.0f};
