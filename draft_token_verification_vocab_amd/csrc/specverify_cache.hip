@@ -125,7 +125,8 @@ TreePlan plan_tree(const spec_cache *c, int32_t nodes, int32_t heads) {
     const int64_t rows = static_cast<int64_t>(nodes) * (heads / c->kv_heads);
     const int64_t tiles16 = (rows + 15) / 16;
     const bool half = c->dtype != SPEC_DTYPE_F32;
-    p.wide = half && tiles16 > (p.dp == 256 ? 1 : 3);
+    // (the first addresses a few slots by 32 bits)
+    p.wide = half && tiles16 > (p.dp == 256 ? 1 : 3) && c->slot_stride <= (1 << 24);
     if (p.wide) {
         p.rt = tiles16 > 4 ? 2 : 1;
         p.rows = 64 * p.rt;

@@ -805,13 +805,13 @@ constexpr float kTreeSlack = 6.0f;
 // fills the time of the matrix products around it.
 constexpr int kTreeArith = 0x406;
 
-// 16 bytes a lane from memory to the wave's 1024 bytes of shared memory at lds,
-// lane by lane; lanes that are off leave their places.  The load has no
+// 16 bytes a lane, at bytes behind p, to the wave's 1024 bytes of shared memory at
+// lds, lane by lane; lanes that are off leave their places.  The load has no
 // destination register and the compiler does not know of it, so that reading
 // another stage does not wait for it; tree_loads_done() does.  Nothing else in the
 // kernel uses m0 (shared memory needs none on this architecture).
-__device__ __forceinline__ void tree_load_lds(const void *p, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p)
+__device__ __forceinline__ void tree_load_lds(const void *p, uint32_t at, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(at), "s"(p)
                  : "memory");
 }
 __device__ __forceinline__ void tree_loads_done() {
@@ -875,7 +875,16 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
     }
     // this lane's chunks of a tile: the first one's key, and its place in a row
     const int key0 = tid / kRow;
-    constexpr int kKeyStep = kTreeBlock / kRow;
+    constexpr int kKeyStep = kTreeBlock / kRow, kWaveKeys = kWave / kRow;
+    static_assert(kWaveKeys <= 8, "a wave's load stays in a page");
+    // key0 lies below a load's step, so the swizzles of the two xor
+    int chunk[kLoads];
+    uint32_t lane_at[kLoads];
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) {
+        chunk[k] = (tid % kRow) ^ tree_swizzle<DP>(key0) ^ tree_swizzle<DP>(k * kKeyStep);
+        lane_at[k] = static_cast<uint32_t>((lane / kRow * slot_stride + 8 * chunk[k]) * sizeof(T));
+    }
     // and its operands' addresses: chunk 4s + g of key i16's in the instruction's
     // order, and four dimensions of key 8g + i16/4
     constexpr uint32_t kStageBytes = kKeys * kRow * 16;
@@ -942,26 +951,21 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
             return __ballot(p0 + (lane & (kKeys - 1)) < span.keys &&
                             static_cast<uint32_t>(entry) < static_cast<uint32_t>(a.pages));
         };
-        // a tile's keys and values on their way to a stage
+        // a tile's keys and values on their way to a stage.  The keys of one of a
+        // wave's loads are consecutive, at most 8 and aligned, so they share a page,
+        // and their addresses are a scalar and an offset that stays.
         auto load = [&](int stage, int p0, int entry) {
             const uint32_t to_k = lds0 + stage * 2 * kStageBytes, to_v = to_k + kStageBytes;
-            // lane k: where key k's row begins
-            if (static_cast<uint32_t>(entry) >= static_cast<uint32_t>(a.pages)) entry = 0;
-            const int64_t row = (entry * a.page_stride +
-                                 ((p0 + (lane & (kKeys - 1))) & slot_mask) * slot_stride) *
-                                static_cast<int64_t>(sizeof(T));
 #pragma unroll
             for (int k = 0; k < kLoads; ++k) {
-                const int key = key0 + k * kKeyStep;
-                const int c = (tid % kRow) ^ tree_swizzle<DP>(key);
-                const uint32_t lo = __shfl(static_cast<int>(row), key, kWave);
-                const uint32_t hi = __shfl(static_cast<int>(row >> 32), key, kWave);
-                const int64_t at = (static_cast<int64_t>(hi) << 32 | lo) + 16 * c;
-                if (FULL || 8 * c < a.D) {
-                    tree_load_lds(reinterpret_cast<const char *>(keys) + at,
-                                  to_k + k * kTreeBlock * 16);
-                    tree_load_lds(reinterpret_cast<const char *>(values) + at,
-                                  to_v + k * kTreeBlock * 16);
+                const int key = k * kKeyStep + wave * kWaveKeys;
+                int page = __builtin_amdgcn_readlane(entry, key);
+                if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.pages)) page = 0;
+                const int64_t at =
+                    page * a.page_stride + ((p0 + key) & slot_mask) * slot_stride;
+                if (FULL || 8 * chunk[k] < a.D) {
+                    tree_load_lds(keys + at, lane_at[k], to_k + k * kTreeBlock * 16);
+                    tree_load_lds(values + at, lane_at[k], to_v + k * kTreeBlock * 16);
                 }
             }
         };
@@ -987,6 +991,8 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
             if (odd) sh.odd = 1;
         };
         constexpr int kBlocks = kKeys / kTreeKeys;
+        // a wave whose rows are not in use only loads
+        const bool mine = mt * kTile + 16 * wave < span.live * a.G;
         v4f32 z[kBlocks][R][2];
         auto score = [&](int stage) {
             const v4u32 *kt = sh.tile[stage][0];
@@ -1113,8 +1119,10 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
             load(stage ^ 1, p0 + kKeys, entry_next);
             held = held_of(p0 + kKeys, entry_next);
             entry_next = entry_of(p0 + 2 * kKeys);
-            score(stage);
-            add_values(stage);
+            if (mine) {
+                score(stage);
+                add_values(stage);
+            }
             p0 += kKeys;
             stage ^= 1;
             tree_loads_done();
@@ -1123,7 +1131,7 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
         while (p0 < keys_end) {
             clean(stage, p0, held);
             __syncthreads();
-            score(stage);
+            if (mine) score(stage);
 #pragma unroll
             for (int kb = 0; kb < kBlocks; ++kb) {
                 const uint32_t there = static_cast<uint32_t>(held >> (32 * kb + 8 * g)) & 0xFFu;
@@ -1137,7 +1145,7 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
                         if (!(see >> j & 1)) z[kb][r][j / 4][j % 4] = -__builtin_inff();
                 }
             }
-            add_values(stage);
+            if (mine) add_values(stage);
             p0 += kKeys;
             if (p0 < keys_end) {
                 stage ^= 1;  // free since the last barrier
