@@ -794,11 +794,14 @@ def _beam_workspace_bytes(B: int, W: int, V: int, dtype: int, n: int) -> int:
     return int(load().spec_beam_workspace_bytes(B, W, V, dtype, n))
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _enqueue(what: str, dev: torch.device, fn, *args):
     """Call the library with dev current, as its launches expect, on dev's
     current stream (the last argument)."""
     stream = _raw_stream(dev.index)
-    if dev.index == torch.cuda.current_device():
+    if dev.index == _current_device():
         status = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -1028,46 +1031,59 @@ def beam_reorder(parents: torch.Tensor, states, outs=None, *,
 _CACHE_DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
 
 
+def _ints(t, name, index, shape):
+    """Raise unless t is a contiguous int32 tensor of this shape on GPU index."""
+    if not (t.dtype is torch.int32 and t.get_device() == index and t.shape == shape
+            and t.is_contiguous()):
+        _need_cuda(t, name, torch.device("cuda", index), torch.int32, shape)
+
+
 def _strides(t):
     """t's strides, 0 along dimensions of one element (whose strides may be anything)."""
-    return [0 if n == 1 else s for n, s in zip(t.shape, t.stride())]
+    s = t.stride()
+    return s if 1 not in t.shape else [0 if n == 1 else x for n, x in zip(t.shape, s)]
+
+
+def _same_layout(t, u):
+    return (t.dtype is u.dtype and t.shape == u.shape and t.get_device() == u.get_device()
+            and (t.stride() == u.stride() or list(_strides(t)) == list(_strides(u))))
 
 
 def _cache(keys, values, table, lengths):
-    """The checked _Cache of two pools [pages, heads, page, dim] and a table [B, P]."""
-    dev = keys.device
-    for t, name in ((keys, "keys"), (values, "values")):
-        if not t.is_cuda:
-            raise ValueError("%s must be a GPU tensor" % name)
+    """(the checked _Cache of two pools [pages, heads, page, dim] and a table [B, P],
+    the GPU's index)."""
+    index = keys.get_device()
+    if index < 0:
+        raise ValueError("keys must be a GPU tensor")
     if keys.dim() != 4 or keys.stride(3) != 1:
         raise ValueError("keys must be [pages, heads, page, dim] with a contiguous last dimension")
-    if (values.device != dev or values.dtype != keys.dtype or values.shape != keys.shape
-            or values.stride() != keys.stride() and _strides(values) != _strides(keys)):
-        raise ValueError("values must be laid out as keys")
+    if not _same_layout(values, keys):
+        raise ValueError("values must be laid out as keys, on the same device")
     code = _CACHE_DTYPES.get(keys.dtype)
     if code is None:
         raise TypeError("keys and values must be float32, bfloat16 or float16, got %s" % keys.dtype)
     if table.dim() != 2:
         raise ValueError("table must be [B, pages of a sequence]")
-    B, P = table.shape
-    _need_cuda(table, "table", dev, torch.int32)
-    _need_cuda(lengths, "lengths", dev, torch.int32, (B,))
+    B, P = shape = table.shape
+    _ints(table, "table", index, shape)
+    _ints(lengths, "lengths", index, (B,))
     N, kv, page, D = keys.shape
     s = _strides(keys)
     return _Cache(keys.data_ptr(), values.data_ptr(), s[0], s[1], s[2], table.data_ptr(),
-                  lengths.data_ptr(), B, N, page, P, kv, D, code, 0)
+                  lengths.data_ptr(), B, N, page, P, kv, D, code, 0), index
 
 
-def _need_rows(t, name, cache, keys, heads=None):
+def _need_rows(t, name, index, keys, B, heads=None):
     """The strides of a [B, T, heads, dim] tensor with a contiguous last dimension."""
-    if not t.is_cuda or t.device != keys.device:
-        raise ValueError("%s must be on %s" % (name, keys.device))
-    if t.dtype != keys.dtype:
+    if t.get_device() != index:
+        raise ValueError("%s must be on cuda:%d" % (name, index))
+    if t.dtype is not keys.dtype:
         raise ValueError("%s must be %s, not %s" % (name, keys.dtype, t.dtype))
-    if (t.dim() != 4 or t.shape[0] != cache.batch or t.shape[3] != cache.dim
-            or (heads is not None and t.shape[2] != heads)):
+    shape = t.shape
+    if (len(shape) != 4 or shape[0] != B or shape[3] != keys.shape[3]
+            or (heads is not None and shape[2] != heads)):
         raise ValueError("%s must have shape (%d, nodes, %s, %d), not %s"
-                         % (name, cache.batch, heads or "heads", cache.dim, tuple(t.shape)))
+                         % (name, B, heads or "heads", keys.shape[3], tuple(shape)))
     if t.stride(3) != 1:
         raise ValueError("%s must have a contiguous last dimension" % name)
     return _strides(t)
@@ -1075,8 +1091,9 @@ def _need_rows(t, name, cache, keys, heads=None):
 
 @functools.lru_cache(maxsize=1024)
 def _tree_workspace_bytes(B: int, P: int, page: int, kv: int, dim: int, dtype: int, T: int,
-                          H: int) -> int:
-    c = _Cache(None, None, dim, dim, dim, None, None, B, 1, page, P, kv, dim, dtype, 0)
+                          H: int, slot_stride: int = 0) -> int:
+    c = _Cache(None, None, dim, dim, slot_stride or dim, None, None, B, 1, page, P, kv, dim, dtype,
+               0)
     return int(load().spec_tree_attention_workspace_bytes(ctypes.byref(c), T, H))
 
 
@@ -1095,31 +1112,37 @@ def tree_attention(q: torch.Tensor, keys: torch.Tensor, values: torch.Tensor, ta
     [B]: nodes in use; the others' outputs are 0.  scale: None is dim ** -0.5.
     Returns out [B, T, H, dim], with lse also the log-sum-exp of the scores
     (float32 [B, T, H], -inf where a node sees nothing).  q and the pools may be
-    strided views with contiguous last dimensions."""
-    c = _cache(keys, values, table, lengths)
-    sb, st, sh, _ = _need_rows(q, "q", c, keys)
-    B, T, H, D = q.shape
-    dev = q.device
+    strided views with contiguous last dimensions.  Autograd does not record the
+    call."""
+    c, index = _cache(keys, values, table, lengths)
+    B = c.batch
+    sb, st, sh, _ = _need_rows(q, "q", index, keys, B)
+    shape = q.shape
+    _, T, H, D = shape
     if parents is not None:
-        _need_cuda(parents, "parents", dev, torch.int32, (B, T))
+        _ints(parents, "parents", index, (B, T))
     if num_nodes is not None:
-        _need_cuda(num_nodes, "num_nodes", dev, torch.int32, (B,))
+        _ints(num_nodes, "num_nodes", index, (B,))
+    dev = q.device
     if out is None:
-        out = torch.empty((B, T, H, D), dtype=q.dtype, device=dev)
+        result = q.new_empty(shape)
     else:
-        _need_cuda(out, "out", dev, q.dtype, (B, T, H, D))
-    sums = torch.empty((B, T, H), dtype=torch.float32, device=dev) if lse else None
+        _need_cuda(out, "out", dev, q.dtype, shape)
+        result = out
+    sums = lengths.new_empty((B, T, H), dtype=torch.float32) if lse else None
     if workspace is None:
-        n = _tree_workspace_bytes(B, c.table_width, c.page_size, c.kv_heads, D, c.dtype, T, H)
-        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
+        workspace = lengths.new_empty(
+            _tree_workspace_bytes(B, c.table_width, c.page_size, c.kv_heads, D, c.dtype, T, H,
+                                  c.slot_stride), dtype=torch.uint8)
     else:
         _need_cuda(workspace, "workspace", dev)
     _enqueue("spec_tree_attention", dev, load().spec_tree_attention, ctypes.byref(c), q.data_ptr(),
              sb, st, sh, T, H, _addr(parents), _addr(num_nodes),
-             D ** -0.5 if scale is None else float(scale), out.data_ptr(), _addr(sums),
+             D ** -0.5 if scale is None else float(scale), result.data_ptr(), _addr(sums),
              workspace.data_ptr(), _nbytes(workspace))
-    _overwritten(out)
-    return (out, sums) if lse else out
+    if out is not None:
+        _overwritten(out)
+    return (result, sums) if lse else result
 
 
 def cache_append(k: torch.Tensor, v: torch.Tensor, keys: torch.Tensor, values: torch.Tensor,
@@ -1129,14 +1152,15 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, keys: torch.Tensor, values: t
     to the positions lengths[b] + j of their sequences' pages, for the first
     num_nodes[b] nodes (None: T).  Positions without a page are left out.  Returns
     (keys, values), the pools written."""
-    c = _cache(keys, values, table, lengths)
-    strides = _need_rows(k, "k", c, keys, c.kv_heads)
-    if _need_rows(v, "v", c, keys, c.kv_heads) != strides or v.shape != k.shape:
+    c, index = _cache(keys, values, table, lengths)
+    strides = _need_rows(k, "k", index, keys, c.batch, c.kv_heads)
+    if not _same_layout(v, k):
         raise ValueError("v must be laid out as k")
     if num_nodes is not None:
-        _need_cuda(num_nodes, "num_nodes", keys.device, torch.int32, (c.batch,))
+        _ints(num_nodes, "num_nodes", index, (c.batch,))
     _enqueue("spec_cache_append", keys.device, load().spec_cache_append, ctypes.byref(c),
-             k.data_ptr(), v.data_ptr(), *strides[:3], k.shape[1], _addr(num_nodes))
+             k.data_ptr(), v.data_ptr(), strides[0], strides[1], strides[2], k.shape[1],
+             _addr(num_nodes))
     _overwritten((keys, values))
     return keys, values
 
@@ -1150,44 +1174,52 @@ def tree_accept(parents: torch.Tensor, tokens: torch.Tensor, chosen: torch.Tenso
     verification, or its own samples).  Returns path (int32 [B, T], the accepted
     nodes, then -1), count (int32 [B]) and tokens (int32 [B, T], what is emitted:
     count tokens, the last one the target's own)."""
-    _need_cuda(tokens, "tokens", dtype=torch.int32)
     if tokens.dim() != 2:
         raise ValueError("tokens must be [B, nodes]")
-    B, T = tokens.shape
-    dev = tokens.device
-    _need_cuda(parents, "parents", dev, torch.int32, (B, T))
-    _need_cuda(chosen, "chosen", dev, torch.int32, (B, T))
+    B, T = shape = tokens.shape
+    index = tokens.get_device()
+    if index < 0:
+        raise ValueError("tokens must be a GPU tensor")
+    _ints(tokens, "tokens", index, shape)
+    _ints(parents, "parents", index, shape)
+    _ints(chosen, "chosen", index, shape)
     if num_nodes is not None:
-        _need_cuda(num_nodes, "num_nodes", dev, torch.int32, (B,))
-    path, emitted = torch.empty((2, B, T), dtype=torch.int32, device=dev).unbind(0)
-    count = torch.empty(B, dtype=torch.int32, device=dev)
-    _enqueue("spec_tree_accept", dev, load().spec_tree_accept, parents.data_ptr(),
+        _ints(num_nodes, "num_nodes", index, (B,))
+    path, emitted, count = torch.empty_like(tokens), torch.empty_like(tokens), tokens.new_empty(B)
+    _enqueue("spec_tree_accept", tokens.device, load().spec_tree_accept, parents.data_ptr(),
              tokens.data_ptr(), chosen.data_ptr(), _addr(num_nodes), B, T, path.data_ptr(),
              count.data_ptr(), emitted.data_ptr())
     return {"path": path, "count": count, "tokens": emitted}
 
 
-def _pools(pools, device):
-    """The checked _CachePools of a list of tensors [pages, heads, page, dim] of one layout."""
-    first = pools[0] if pools else None
-    n = len(pools)
-    bases = (ctypes.c_void_p * max(n, 1))()
-    for i, t in enumerate(pools):
-        if not t.is_cuda or t.device != device:
-            raise ValueError("pools[%d] must be on %s" % (i, device))
-        if t.dim() != 4 or t.stride(3) != 1:
-            raise ValueError("pools[%d] must be [pages, heads, page, dim] with a contiguous last "
-                             "dimension" % i)
-        if (t.dtype != first.dtype or t.shape != first.shape
-                or t.stride() != first.stride() and _strides(t) != _strides(first)):
-            raise ValueError("pools[%d] must be laid out as pools[0]" % i)
-        bases[i] = t.data_ptr()
-    if first is None:
+@functools.lru_cache(maxsize=64)
+def _address_array(n: int):
+    return ctypes.c_void_p * n
+
+
+def _pools(pools, index):
+    """The checked _CachePools of a list of tensors [pages, heads, page, dim] of one
+    layout, and the addresses it points to."""
+    if not pools:
         raise ValueError("pools must hold at least one tensor")
+    first = pools[0]
+    if first.get_device() != index:
+        raise ValueError("pools[0] must be on cuda:%d" % index)
+    if first.dim() != 4 or first.stride(3) != 1:
+        raise ValueError("pools[0] must be [pages, heads, page, dim] with a contiguous last "
+                         "dimension")
+    dtype, shape, stride = first.dtype, first.shape, first.stride()
+    for i, t in enumerate(pools):
+        if not (t.dtype is dtype and t.shape == shape and t.get_device() == index
+                and t.stride() == stride) and not _same_layout(t, first):
+            raise ValueError("pools[%d] must be laid out as pools[0], on the same device" % i)
+    n = len(pools)
+    bases = _address_array(n)(*[t.data_ptr() for t in pools])
     e = first.element_size()
     s = _strides(first)
-    return _CachePools(ctypes.cast(bases, ctypes.c_void_p), n, first.shape[0], first.shape[2],
-                       first.shape[1], s[0] * e, s[1] * e, s[2] * e, first.shape[3] * e), bases
+    N, kv, page, D = shape
+    return _CachePools(ctypes.addressof(bases), n, N, page, kv, s[0] * e, s[1] * e, s[2] * e,
+                       D * e), bases
 
 
 def cache_keep(pools, table: torch.Tensor, lengths: torch.Tensor, path: torch.Tensor,
@@ -1197,21 +1229,37 @@ def cache_keep(pools, table: torch.Tensor, lengths: torch.Tensor, path: torch.Te
     lengths[b] + path[b, i] to lengths[b] + i for i < count[b] (path and count as
     tree_accept gives them).  Returns the new lengths, int32 [B]."""
     pools = list(pools)
-    dev = table.device
-    _need_cuda(path, "path", dev, torch.int32)
+    index = table.get_device()
+    if index < 0:
+        raise ValueError("table must be a GPU tensor")
     if path.dim() != 2 or table.dim() != 2:
         raise ValueError("path must be [B, nodes] and table [B, pages of a sequence]")
     B, T = path.shape
-    _need_cuda(table, "table", dev, torch.int32, (B, table.shape[1]))
-    _need_cuda(lengths, "lengths", dev, torch.int32, (B,))
-    _need_cuda(count, "count", dev, torch.int32, (B,))
-    p, _bases = _pools(pools, dev)
-    new = torch.empty(B, dtype=torch.int32, device=dev)
-    _enqueue("spec_cache_keep", dev, load().spec_cache_keep, ctypes.byref(p), table.data_ptr(),
-             table.shape[1], lengths.data_ptr(), path.data_ptr(), count.data_ptr(), B, T,
+    P = table.shape[1]
+    _ints(path, "path", index, (B, T))
+    _ints(table, "table", index, (B, P))
+    _ints(lengths, "lengths", index, (B,))
+    _ints(count, "count", index, (B,))
+    p, _bases = _pools(pools, index)
+    new = torch.empty_like(lengths)
+    _enqueue("spec_cache_keep", table.device, load().spec_cache_keep, ctypes.byref(p),
+             table.data_ptr(), P, lengths.data_ptr(), path.data_ptr(), count.data_ptr(), B, T,
              new.data_ptr())
     _overwritten(pools)
     return new
+
+
+def _table_on(table, refs, dims, what):
+    """The GPU's index of a table [..., P] with dims dimensions (0: any from two on)
+    beside refs [pages]."""
+    index = table.get_device()
+    if index < 0:
+        raise ValueError("table must be a GPU tensor")
+    if table.dim() < 2 or (dims and table.dim() != dims) or refs.dim() != 1:
+        raise ValueError("table must be %s and refs [pages]" % what)
+    _ints(table, "table", index, table.shape)
+    _ints(refs, "refs", index, refs.shape)
+    return index
 
 
 def pages_fork(table: torch.Tensor, lengths: torch.Tensor, parents: torch.Tensor,
@@ -1221,30 +1269,20 @@ def pages_fork(table: torch.Tensor, lengths: torch.Tensor, parents: torch.Tensor
     [B, W, P]) up to its length (lengths int32 [B, W]), and refs (int32 [pages])
     counts them.  What out listed before is not released.  Returns the new rows'
     lengths, int32 [B, n]."""
-    _need_cuda(table, "table", dtype=torch.int32)
-    if table.dim() != 3 or parents.dim() != 2 or refs.dim() != 1:
-        raise ValueError("table must be [B, W, P], parents [B, n] and refs [pages]")
+    index = _table_on(table, refs, 3, "[B, W, P]")
+    if parents.dim() != 2:
+        raise ValueError("parents must be [B, n]")
     B, W, P = table.shape
-    dev, n = table.device, parents.shape[1]
-    _need_cuda(lengths, "lengths", dev, torch.int32, (B, W))
-    _need_cuda(parents, "parents", dev, torch.int32, (B, n))
-    _need_cuda(refs, "refs", dev, torch.int32)
-    _need_cuda(out, "out", dev, torch.int32, (B, n, P))
-    new = torch.empty((B, n), dtype=torch.int32, device=dev)
-    _enqueue("spec_pages_fork", dev, load().spec_pages_fork, table.data_ptr(), lengths.data_ptr(),
-             parents.data_ptr(), B, W, n, P, page_size, refs.shape[0], refs.data_ptr(),
-             out.data_ptr(), new.data_ptr())
+    n = parents.shape[1]
+    _ints(lengths, "lengths", index, (B, W))
+    _ints(parents, "parents", index, (B, n))
+    _ints(out, "out", index, (B, n, P))
+    new = torch.empty_like(parents)
+    _enqueue("spec_pages_fork", table.device, load().spec_pages_fork, table.data_ptr(),
+             lengths.data_ptr(), parents.data_ptr(), B, W, n, P, page_size, refs.shape[0],
+             refs.data_ptr(), out.data_ptr(), new.data_ptr())
     _overwritten((out, refs))
     return new
-
-
-def _table_rows(table, refs):
-    """(rows, P) of a table [..., P] beside refs [pages]."""
-    _need_cuda(table, "table", dtype=torch.int32)
-    _need_cuda(refs, "refs", table.device, torch.int32)
-    if table.dim() < 2 or refs.dim() != 1:
-        raise ValueError("table must be [..., P] and refs [pages]")
-    return math.prod(table.shape[:-1]), table.shape[-1]
 
 
 def pages_release(table: torch.Tensor, refs: torch.Tensor, page_size: int,
@@ -1252,12 +1290,13 @@ def pages_release(table: torch.Tensor, refs: torch.Tensor, page_size: int,
     """Drop the pages of each row of table (int32 [..., P]) behind its first lengths
     positions (int32 [...]; None: all pages): their entries become -1 and refs
     (int32 [pages]) goes down.  Returns table."""
-    rows, P = _table_rows(table, refs)
-    dev = table.device
+    index = _table_on(table, refs, 0, "[..., P]")
+    shape = table.shape
     if lengths is not None:
-        _need_cuda(lengths, "lengths", dev, torch.int32, table.shape[:-1])
-    _enqueue("spec_pages_release", dev, load().spec_pages_release, table.data_ptr(),
-             _addr(lengths), rows, P, page_size, refs.shape[0], refs.data_ptr())
+        _ints(lengths, "lengths", index, shape[:-1])
+    _enqueue("spec_pages_release", table.device, load().spec_pages_release, table.data_ptr(),
+             _addr(lengths), math.prod(shape[:-1]), shape[-1], page_size, refs.shape[0],
+             refs.data_ptr())
     _overwritten((table, refs))
     return table
 
@@ -1275,23 +1314,21 @@ def pages_reserve(table: torch.Tensor, lengths: torch.Tensor, refs: torch.Tensor
     [rows, 3]: page, its replacement, positions that pages_copy is to move; -1, -1
     and 0 for none) and missing (int32 [1]: 0; the pages that lack, or -1 where
     positions pass a table row, and then nothing changed)."""
-    rows, P = _table_rows(table, refs)
-    dev = table.device
-    _need_cuda(lengths, "lengths", dev, torch.int32, table.shape[:-1])
-    _need_cuda(new, "new", dev, torch.int32, table.shape[:-1])
-    copies = torch.empty((rows, 3), dtype=torch.int32, device=dev)
-    missing = torch.empty(1, dtype=torch.int32, device=dev)
+    index = _table_on(table, refs, 0, "[..., P]")
+    lead, P = table.shape[:-1], table.shape[-1]
+    rows, pages = math.prod(lead), refs.shape[0]
+    _ints(lengths, "lengths", index, lead)
+    _ints(new, "new", index, lead)
+    copies, missing = refs.new_empty((rows, 3)), refs.new_empty(1)
     if rows == 0:
         missing.zero_()
     if workspace is None:
-        n = _reserve_workspace_bytes(rows, refs.shape[0])
-        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
+        workspace = refs.new_empty(_reserve_workspace_bytes(rows, pages), dtype=torch.uint8)
     else:
-        _need_cuda(workspace, "workspace", dev)
-    _enqueue("spec_pages_reserve", dev, load().spec_pages_reserve, table.data_ptr(),
-             lengths.data_ptr(), new.data_ptr(), rows, P, page_size, refs.shape[0],
-             refs.data_ptr(), copies.data_ptr(), missing.data_ptr(), workspace.data_ptr(),
-             _nbytes(workspace))
+        _need_cuda(workspace, "workspace", refs.device)
+    _enqueue("spec_pages_reserve", refs.device, load().spec_pages_reserve, table.data_ptr(),
+             lengths.data_ptr(), new.data_ptr(), rows, P, page_size, pages, refs.data_ptr(),
+             copies.data_ptr(), missing.data_ptr(), workspace.data_ptr(), _nbytes(workspace))
     _overwritten((table, refs))
     return {"copies": copies, "missing": missing}
 
@@ -1302,12 +1339,14 @@ def pages_copy(pools, copies: torch.Tensor) -> list:
     first copies[r, 2] positions of page copies[r, 0] to page copies[r, 1].
     Returns the pools."""
     pools = list(pools)
-    _need_cuda(copies, "copies", dtype=torch.int32)
+    index = copies.get_device()
+    if index < 0:
+        raise ValueError("copies must be a GPU tensor")
     if copies.dim() != 2 or copies.shape[1] != 3:
         raise ValueError("copies must be [rows, 3]")
-    dev = copies.device
-    p, _bases = _pools(pools, dev)
-    _enqueue("spec_pages_copy", dev, load().spec_pages_copy, ctypes.byref(p), copies.data_ptr(),
-             copies.shape[0])
+    _ints(copies, "copies", index, copies.shape)
+    p, _bases = _pools(pools, index)
+    _enqueue("spec_pages_copy", copies.device, load().spec_pages_copy, ctypes.byref(p),
+             copies.data_ptr(), copies.shape[0])
     _overwritten(pools)
     return pools

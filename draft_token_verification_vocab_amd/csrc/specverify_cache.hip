@@ -93,6 +93,8 @@ bool pools_ok(const spec_cache *c) {
 // ---------------------------------------------------------------------------
 // Tree attention
 // ---------------------------------------------------------------------------
+constexpr int kTreeWhole = 8;  // tiles of the longest sequence
+
 struct TreePlan {
     int dp;      // dimensions, rounded up to what a kernel takes
     bool wide;   // rows shared out to the waves, else keys
@@ -100,6 +102,7 @@ struct TreePlan {
     int rows;    // of a workgroup
     int waves;   // workgroups to a compute unit
     int mtiles;
+    bool whole;  // a slice is a sequence
     int slices;
     size_t first, part, part_ml, total;  // workspace
 };
@@ -111,7 +114,7 @@ spec_status check_tree(const spec_cache *c, int32_t nodes, int32_t heads, bool t
     if (nodes > (tree ? kMaxTreeNodes : kMaxChainNodes) || heads > kMaxHeads)
         return SPEC_ERR_UNSUPPORTED;
     const int64_t tiles =
-        static_cast<int64_t>(c->table_width) * c->page_size / kTreeTile + 1;
+        (static_cast<int64_t>(c->table_width) * c->page_size + kTreeTile - 1) / kTreeTile;
     if (c->batch > INT32_MAX / tiles) return SPEC_ERR_UNSUPPORTED;
     const int64_t rows = static_cast<int64_t>(c->batch) * nodes;
     if (rows > 0 && rows > (int64_t{1} << 40) / heads) return SPEC_ERR_UNSUPPORTED;
@@ -143,12 +146,15 @@ TreePlan plan_tree(const spec_cache *c, int32_t nodes, int32_t heads) {
     }
     p.mtiles = static_cast<int>((rows + p.rows - 1) / p.rows);
     const int64_t units = static_cast<int64_t>(p.mtiles) * c->kv_heads;
-    const int64_t tiles =
-        c->batch * (static_cast<int64_t>(c->table_width) * c->page_size / kTreeTile + 1);
+    const int64_t longest =
+        (static_cast<int64_t>(c->table_width) * c->page_size + kTreeTile - 1) / kTreeTile;
+    const int64_t tiles = c->batch * longest;
+    // short sequences are not cut: no second launch
+    p.whole = longest <= kTreeWhole;
     int64_t slices = (p.waves * kUnits + units - 1) / units;
     if (slices > tiles) slices = tiles;
-    p.slices = static_cast<int>(slices < 1 ? 1 : slices);
-    const int64_t parts = 2 * units * p.slices * p.rows;
+    p.slices = p.whole ? c->batch : static_cast<int>(slices < 1 ? 1 : slices);
+    const int64_t parts = p.whole ? 0 : 2 * units * p.slices * p.rows;
     p.first = 0;
     p.part = align_up((static_cast<size_t>(c->batch) + 1) * sizeof(int32_t));
     p.part_ml = p.part + align_up(static_cast<size_t>(parts) * c->dim * sizeof(float));
@@ -324,6 +330,7 @@ spec_status spec_tree_attention(const spec_cache *cache, const void *q, int64_t 
     a.pages = cache->num_pages;
     a.shift = page_shift(cache->page_size);
     a.slices = p.slices;
+    a.whole = p.whole;
     a.mtiles = p.mtiles;
     a.scale2 = scale * kLog2e;
     hipStream_t st = static_cast<hipStream_t>(stream);
@@ -334,7 +341,7 @@ spec_status spec_tree_attention(const spec_cache *cache, const void *q, int64_t 
     else
         launch_tree<float>(a, p, st);
     const spec_status r = launch_status();
-    if (r != SPEC_OK || p.slices == 1) return r;
+    if (r != SPEC_OK || p.whole) return r;
     if (cache->dtype == SPEC_DTYPE_BF16)
         launch_join<__bf16>(a, p, st);
     else if (cache->dtype == SPEC_DTYPE_F16)
@@ -560,9 +567,11 @@ spec_status spec_pages_reserve(int32_t *table, const int32_t *lengths,
     a.pages = num_pages;
     a.chunks = (num_pages + kPageChunk - 1) / kPageChunk;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    pages_free_kernel<<<dim3(static_cast<unsigned>(a.chunks)), dim3(kCacheBlock), 0, st>>>(a);
-    const spec_status r = launch_status();
-    if (r != SPEC_OK) return r;
+    if (a.chunks > kReserveAlone) {
+        pages_free_kernel<<<dim3(static_cast<unsigned>(a.chunks)), dim3(kCacheBlock), 0, st>>>(a);
+        const spec_status r = launch_status();
+        if (r != SPEC_OK) return r;
+    }
     pages_reserve_kernel<<<dim3(1), dim3(kReserveBlock), 0, st>>>(a);
     return launch_status();
 }

@@ -274,6 +274,7 @@ constexpr int kReserveBlock = 1024;
 constexpr int kPageChunk = 1024;         // pages to a count
 constexpr int kMaxReservePages = 1 << 22;
 constexpr int kKeeper = 1 << 30;
+constexpr int kReserveAlone = 64;  // chunks that the second launch looks through by itself
 
 struct ReserveArgs {
     int32_t *table, *refs, *copies, *missing;
@@ -326,6 +327,22 @@ __global__ __launch_bounds__(kReserveBlock) void pages_reserve_kernel(ReserveArg
     if (tid == 0) {
         sh_widest = 1;
         sh_over = 0;
+    }
+    if (a.chunks <= kReserveAlone) {
+        // a small pool needs no launch of its own: a wave to a chunk
+        for (int c = tid / kWave; c < a.chunks; c += kReserveBlock / kWave) {
+            int count = 0;
+#pragma unroll
+            for (int k = 0; k < kPageChunk / kWave; ++k) {
+                const int at = c * kPageChunk + k * kWave + lane;
+                const uint64_t w = __ballot(at < a.pages && a.refs[at] <= 0);
+                if (lane == 0) a.words[at / kWave] = w;
+                count += __popcll(w);
+            }
+            if (lane == 0) a.counts[c] = count;
+        }
+        __threadfence_block();
+        __syncthreads();
     }
     // free pages before each chunk
     int free = 0;

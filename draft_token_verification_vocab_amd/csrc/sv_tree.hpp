@@ -69,7 +69,7 @@ struct TreeArgs {
     int64_t q_batch, q_node, q_head;                // elements
     int32_t B, T, H, KV, G, D, P;
     int32_t pages, shift;    // page size 2^shift
-    int32_t slices, mtiles;
+    int32_t slices, mtiles, whole;
     float scale2;            // scale * log2(e)
 };
 
@@ -299,9 +299,17 @@ struct TreePlace {
 // Finds a slice's place, in every wave for itself: a lane adds up an equal share
 // of the sequences, a scan over the lanes finds the share that holds the
 // slice's first tile, and a second one, over that share, the sequence.
-// Workgroup 0 leaves the sequences' first tiles for the second launch.
+// Workgroup 0 leaves the sequences' first tiles for the second launch.  Where
+// sequences are not cut (whole), a slice is a sequence.
 __device__ __forceinline__ TreePlace tree_plan(const TreeArgs &a, int slice, int lane,
                                                bool leave) {
+    if (a.whole) {
+        TreePlace p{};
+        p.b = slice;
+        p.span = tree_span(a, slice);
+        p.end = tree_tiles(p.span.keys);
+        return p;
+    }
     const int share = (a.B + kWave - 1) / kWave;
     int mine = 0;
     for (int k = 0; k < share; ++k) {
