@@ -1130,16 +1130,19 @@ def tree_attention(q: torch.Tensor, keys: torch.Tensor, values: torch.Tensor, ta
         _need_cuda(out, "out", dev, q.dtype, shape)
         result = out
     sums = lengths.new_empty((B, T, H), dtype=torch.float32) if lse else None
-    if workspace is None:
-        workspace = lengths.new_empty(
-            _tree_workspace_bytes(B, c.table_width, c.page_size, c.kv_heads, D, c.dtype, T, H,
-                                  c.slot_stride), dtype=torch.uint8)
-    else:
+    room = 0
+    if workspace is not None:
         _need_cuda(workspace, "workspace", dev)
+        room = _nbytes(workspace)
+    else:
+        room = _tree_workspace_bytes(B, c.table_width, c.page_size, c.kv_heads, D, c.dtype, T, H,
+                                     c.slot_stride)
+        if room:
+            workspace = lengths.new_empty(room, dtype=torch.uint8)
     _enqueue("spec_tree_attention", dev, load().spec_tree_attention, ctypes.byref(c), q.data_ptr(),
              sb, st, sh, T, H, _addr(parents), _addr(num_nodes),
              D ** -0.5 if scale is None else float(scale), result.data_ptr(), _addr(sums),
-             workspace.data_ptr(), _nbytes(workspace))
+             _addr(workspace), room)
     if out is not None:
         _overwritten(out)
     return (result, sums) if lse else result

@@ -93,7 +93,7 @@ bool pools_ok(const spec_cache *c) {
 // ---------------------------------------------------------------------------
 // Tree attention
 // ---------------------------------------------------------------------------
-constexpr int kTreeWhole = 8;  // tiles of the longest sequence
+constexpr int kTreeWhole = 8, kTreeWholeWide = 4;  // tiles of the longest sequence
 
 struct TreePlan {
     int dp;      // dimensions, rounded up to what a kernel takes
@@ -150,7 +150,7 @@ TreePlan plan_tree(const spec_cache *c, int32_t nodes, int32_t heads) {
         (static_cast<int64_t>(c->table_width) * c->page_size + kTreeTile - 1) / kTreeTile;
     const int64_t tiles = c->batch * longest;
     // short sequences are not cut: no second launch
-    p.whole = longest <= kTreeWhole;
+    p.whole = longest <= (p.wide ? kTreeWholeWide : kTreeWhole);
     int64_t slices = (p.waves * kUnits + units - 1) / units;
     if (slices > tiles) slices = tiles;
     p.slices = p.whole ? c->batch : static_cast<int>(slices < 1 ? 1 : slices);
@@ -158,7 +158,7 @@ TreePlan plan_tree(const spec_cache *c, int32_t nodes, int32_t heads) {
     p.first = 0;
     p.part = align_up((static_cast<size_t>(c->batch) + 1) * sizeof(int32_t));
     p.part_ml = p.part + align_up(static_cast<size_t>(parts) * c->dim * sizeof(float));
-    p.total = p.part_ml + align_up(static_cast<size_t>(parts) * 4 * sizeof(float));
+    p.total = p.whole ? 0 : p.part_ml + align_up(static_cast<size_t>(parts) * 4 * sizeof(float));
     return p;
 }
 
@@ -254,8 +254,20 @@ PoolArgs pool_args(const spec_cache_pools *p, int first, int count) {
     return a;
 }
 
-size_t reserve_words(int32_t num_pages) {
-    return static_cast<size_t>((num_pages + kPageChunk - 1) / kPageChunk) * (kPageChunk / kWave);
+struct ReservePlan {
+    int chunks;
+    size_t words, before, counts, total;
+};
+
+ReservePlan plan_reserve(int32_t num_pages) {
+    ReservePlan p;
+    p.chunks = (num_pages + kPageChunk - 1) / kPageChunk;
+    const size_t n = static_cast<size_t>(p.chunks) * kChunkWords;
+    p.words = 0;
+    p.before = align_up(n * sizeof(uint64_t));
+    p.counts = p.before + align_up(n * sizeof(int32_t));
+    p.total = p.counts + align_up(p.chunks * sizeof(int32_t));
+    return p;
 }
 
 }  // namespace
@@ -298,7 +310,7 @@ spec_status spec_tree_attention(const spec_cache *cache, const void *q, int64_t 
     const TreePlan p = plan_tree(cache, nodes, heads);
     if (!grid_fits(static_cast<int64_t>(p.slices) * cache->kv_heads * p.mtiles, kTreeBlock))
         return SPEC_ERR_UNSUPPORTED;
-    if (!workspace || workspace_bytes < p.total) return SPEC_ERR_WORKSPACE;
+    if (p.total > 0 && (!workspace || workspace_bytes < p.total)) return SPEC_ERR_WORKSPACE;
     if (!aligned16(workspace)) return SPEC_ERR_ARG;
     char *w = static_cast<char *>(workspace);
     TreeArgs a{};
@@ -311,9 +323,11 @@ spec_status spec_tree_attention(const spec_cache *cache, const void *q, int64_t 
     a.lengths = cache->lengths;
     a.nodes = num_nodes;
     a.parents = parents;
-    a.first = reinterpret_cast<int32_t *>(w + p.first);
-    a.part = reinterpret_cast<float *>(w + p.part);
-    a.part_ml = reinterpret_cast<float *>(w + p.part_ml);
+    if (!p.whole) {
+        a.first = reinterpret_cast<int32_t *>(w + p.first);
+        a.part = reinterpret_cast<float *>(w + p.part);
+        a.part_ml = reinterpret_cast<float *>(w + p.part_ml);
+    }
     a.page_stride = cache->page_stride;
     a.head_stride = cache->head_stride;
     a.slot_stride = cache->slot_stride;
@@ -533,8 +547,7 @@ spec_status spec_pages_release(int32_t *table, const int32_t *lengths, int32_t r
 size_t spec_pages_reserve_workspace_bytes(int32_t rows, int32_t num_pages) {
     if (rows < 1 || num_pages < 1 || rows > kMaxReserveRows || num_pages > kMaxReservePages)
         return 0;
-    return align_up(reserve_words(num_pages) * 8) +
-           align_up(reserve_words(num_pages) / (kPageChunk / kWave) * 4);
+    return plan_reserve(num_pages).total;
 }
 
 spec_status spec_pages_reserve(int32_t *table, const int32_t *lengths,
@@ -548,7 +561,7 @@ spec_status spec_pages_reserve(int32_t *table, const int32_t *lengths,
     if (rows > kMaxReserveRows || num_pages > kMaxReservePages) return SPEC_ERR_UNSUPPORTED;
     if (rows == 0) return SPEC_OK;
     if (!table || !lengths || !new_positions || !refs || !copies || !missing) return SPEC_ERR_ARG;
-    if (!workspace || workspace_bytes < spec_pages_reserve_workspace_bytes(rows, num_pages))
+    if (!workspace || workspace_bytes < plan_reserve(num_pages).total)
         return SPEC_ERR_WORKSPACE;
     if (!aligned16(workspace)) return SPEC_ERR_ARG;
     char *w = static_cast<char *>(workspace);
@@ -559,16 +572,20 @@ spec_status spec_pages_reserve(int32_t *table, const int32_t *lengths,
     a.missing = missing;
     a.lengths = lengths;
     a.news = new_positions;
-    a.words = reinterpret_cast<unsigned long long *>(w);
-    a.counts = reinterpret_cast<int32_t *>(w + align_up(reserve_words(num_pages) * 8));
+    const ReservePlan p = plan_reserve(num_pages);
+    a.words = reinterpret_cast<unsigned long long *>(w + p.words);
+    a.before = reinterpret_cast<int32_t *>(w + p.before);
+    a.counts = reinterpret_cast<int32_t *>(w + p.counts);
     a.rows = rows;
     a.P = table_width;
     a.shift = page_shift(page_size);
     a.pages = num_pages;
-    a.chunks = (num_pages + kPageChunk - 1) / kPageChunk;
+    a.chunks = p.chunks;
     hipStream_t st = static_cast<hipStream_t>(stream);
     if (a.chunks > kReserveAlone) {
-        pages_free_kernel<<<dim3(static_cast<unsigned>(a.chunks)), dim3(kCacheBlock), 0, st>>>(a);
+        constexpr int per = kCacheBlock / kWave;
+        pages_free_kernel<<<dim3(static_cast<unsigned>((a.chunks + per - 1) / per)),
+                            dim3(kCacheBlock), 0, st>>>(a);
         const spec_status r = launch_status();
         if (r != SPEC_OK) return r;
     }

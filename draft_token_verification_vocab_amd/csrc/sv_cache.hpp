@@ -260,44 +260,62 @@ __global__ __launch_bounds__(kCacheBlock) void pages_release_kernel(ReleaseArgs 
 }
 
 // ---------------------------------------------------------------------------
-// Reserving.  The first launch writes which pages are free, 64 to a word, and
-// their number in every chunk of 1024; the second, one workgroup, finds what the
-// rows need and hands out free pages in order.
+// Reserving.  One workgroup finds what the rows need and hands out free pages in
+// order; which pages are free, 64 to a word, with the words' running counts in
+// every chunk of 1024, it looks up itself in a small pool and a launch before it
+// does in a larger one.
 //
-// Shared pages among the entries that a row is about to write are marked in the
-// table (-2 - page) while they are settled: every marked entry takes its
-// reference off; a page that has none left then has all its holders here, and
-// the lowest row among them, found by a minimum over row - 2^30 in the page's own
-// count, keeps it.
+// A row's entries that are about to be written belong to a group of lanes, as
+// many as the widest row needs.  Shared pages among them are settled in the
+// pages' own counts: every entry takes its reference off; a page that has none
+// left then has all its holders here, and the lowest row among them, found by a
+// minimum over row - 2^30, keeps it.
+//
+// Where the rows fit the workgroup, an entry to a thread (a step of decoding),
+// entries stay in registers; otherwise shared ones are marked in the table
+// (-2 - page) until they are settled.
 // ---------------------------------------------------------------------------
 constexpr int kReserveBlock = 1024;
-constexpr int kPageChunk = 1024;         // pages to a count
+constexpr int kPageChunk = 1024;                   // pages to a count
+constexpr int kChunkWords = kPageChunk / kWave;
 constexpr int kMaxReservePages = 1 << 22;
 constexpr int kKeeper = 1 << 30;
-constexpr int kReserveAlone = 64;  // chunks that the second launch looks through by itself
+constexpr int kReserveAlone = 32;  // chunks that the workgroup looks through by itself
 
 struct ReserveArgs {
     int32_t *table, *refs, *copies, *missing;
     const int32_t *lengths, *news;
-    unsigned long long *words;  // [pages / 64]
-    int32_t *counts;            // [pages / 1024]
+    unsigned long long *words;  // [chunks][16]
+    int32_t *before;            // [chunks][16]: free pages of the chunk before a word
+    int32_t *counts;            // [chunks]
     int32_t rows, P, shift, pages, chunks;
 };
 
-__global__ __launch_bounds__(kCacheBlock) void pages_free_kernel(ReserveArgs a) {
-    __shared__ int sh[kCacheBlock / kWave];
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+// One wave: a chunk's words and counts.
+__device__ __forceinline__ void chunk_words(const ReserveArgs &a, int c, int lane) {
+    int v[kChunkWords];
+#pragma unroll
+    for (int k = 0; k < kChunkWords; ++k) {
+        const int at = c * kPageChunk + k * kWave + lane;
+        v[k] = a.refs[at < a.pages ? at : a.pages - 1];
+        if (at >= a.pages) v[k] = 1;
+    }
     int free = 0;
 #pragma unroll
-    for (int k = 0; k < kPageChunk / kCacheBlock; ++k) {
-        const int at = blockIdx.x * kPageChunk + k * kCacheBlock + threadIdx.x;
-        const uint64_t w = __ballot(at < a.pages && a.refs[at] <= 0);
-        if (lane == 0) a.words[at / kWave] = w;
+    for (int k = 0; k < kChunkWords; ++k) {
+        const uint64_t w = __ballot(v[k] <= 0);
+        if (lane == 0) {
+            a.words[c * kChunkWords + k] = w;
+            a.before[c * kChunkWords + k] = free;
+        }
         free += __popcll(w);
     }
-    if (lane == 0) sh[wave] = free;
-    __syncthreads();
-    if (threadIdx.x == 0) a.counts[blockIdx.x] = sh[0] + sh[1] + sh[2] + sh[3];
+    if (lane == 0) a.counts[c] = free;
+}
+
+__global__ __launch_bounds__(kCacheBlock) void pages_free_kernel(ReserveArgs a) {
+    const int c = blockIdx.x * (kCacheBlock / kWave) + threadIdx.x / kWave;
+    if (c < a.chunks) chunk_words(a, c, threadIdx.x & (kWave - 1));
 }
 
 // Inclusive scan of v over the workgroup; the total goes to every thread.
@@ -319,6 +337,27 @@ __device__ __forceinline__ int reserve_scan(int v, int *sh, int &total) {
     return v;
 }
 
+// The free page of this rank: the chunk is the last one with no more before it,
+// likewise the word.
+__device__ __forceinline__ int free_page(const ReserveArgs &a, const int *before, int rank) {
+    int c = 0;
+    for (int step = kMaxReservePages / kPageChunk; step; step >>= 1)
+        if (c + step < a.chunks && before[c + step] <= rank) c += step;
+    rank -= before[c];
+    int w = -1, base = 0;
+#pragma unroll
+    for (int k = 0; k < kChunkWords; ++k) {
+        const int b = a.before[c * kChunkWords + k];
+        if (b <= rank) {
+            ++w;
+            base = b;
+        }
+    }
+    uint64_t bits = a.words[c * kChunkWords + w];
+    for (rank -= base; rank > 0; --rank) bits &= bits - 1;
+    return c * kPageChunk + w * kWave + __ffsll(static_cast<long long>(bits)) - 1;
+}
+
 __global__ __launch_bounds__(kReserveBlock) void pages_reserve_kernel(ReserveArgs a) {
     __shared__ int sh_before[kMaxReservePages / kPageChunk];
     __shared__ int sh_scan[kReserveBlock / kWave];
@@ -328,22 +367,33 @@ __global__ __launch_bounds__(kReserveBlock) void pages_reserve_kernel(ReserveArg
         sh_widest = 1;
         sh_over = 0;
     }
-    if (a.chunks <= kReserveAlone) {
-        // a small pool needs no launch of its own: a wave to a chunk
-        for (int c = tid / kWave; c < a.chunks; c += kReserveBlock / kWave) {
-            int count = 0;
-#pragma unroll
-            for (int k = 0; k < kPageChunk / kWave; ++k) {
-                const int at = c * kPageChunk + k * kWave + lane;
-                const uint64_t w = __ballot(at < a.pages && a.refs[at] <= 0);
-                if (lane == 0) a.words[at / kWave] = w;
-                count += __popcll(w);
-            }
-            if (lane == 0) a.counts[c] = count;
-        }
-        __threadfence_block();
-        __syncthreads();
+    const int room = a.P << a.shift, page_size = 1 << a.shift;
+    // the table entries [lo, hi) that row r is about to write (hi -1: too many)
+    auto range = [&](int r, int &lo, int &hi, int &length) {
+        lo = hi = length = 0;
+        if (r >= a.rows) return;
+        const int given = a.lengths[r], more = a.news[r] > 0 ? a.news[r] : 0;
+        length = clamp_len(given, room);
+        lo = length >> a.shift;
+        if (more > room - length || (more > 0 && given > room))
+            hi = -1;
+        else
+            hi = more == 0 ? lo : (length + more + page_size - 1) >> a.shift;
+    };
+    __syncthreads();
+    for (int r = tid; r < a.rows; r += kReserveBlock) {
+        int lo, hi, length;
+        range(r, lo, hi, length);
+        if (hi < 0)
+            atomicMax(&sh_over, 1);
+        else
+            atomicMax(&sh_widest, hi - lo);
     }
+    if (a.chunks <= kReserveAlone) {
+        for (int c = tid / kWave; c < a.chunks; c += kReserveBlock / kWave) chunk_words(a, c, lane);
+        __threadfence_block();
+    }
+    __syncthreads();
     // free pages before each chunk
     int free = 0;
     for (int c0 = 0; c0 < a.chunks; c0 += kReserveBlock) {
@@ -353,33 +403,63 @@ __global__ __launch_bounds__(kReserveBlock) void pages_reserve_kernel(ReserveArg
         if (c < a.chunks) sh_before[c] = free + upto - mine;
         free += total;
     }
-    const int room = a.P << a.shift, page_size = 1 << a.shift;
-    // the table entries [lo, hi) that row r is about to write
-    auto range = [&](int r, int &lo, int &hi, int &length) {
-        lo = hi = length = 0;
-        if (r >= a.rows) return;
-        length = clamp_len(a.lengths[r], room);
-        const int more = a.news[r] > 0 ? a.news[r] : 0;
-        lo = length >> a.shift;
-        if (more > room - length || (more > 0 && a.lengths[r] > room))
-            hi = -1;
-        else
-            hi = more == 0 ? lo : (length + more + page_size - 1) >> a.shift;
-    };
-    for (int r = tid; r < a.rows; r += kReserveBlock) {
-        int lo, hi, length;
-        range(r, lo, hi, length);
-        if (hi < 0)
-            atomicMax(&sh_over, 1);
-        else
-            atomicMax(&sh_widest, hi - lo);
-    }
-    __syncthreads();
     const bool over = sh_over != 0;
     // lanes to a row: a power of two that holds the widest range, up to a wave
     int group = 1;
     while (group < kWave && group < sh_widest) group <<= 1;
     const int in = tid & (group - 1), batch = kReserveBlock / group;
+    auto copy_of = [&](int r, int from, int to, int n) {
+        int32_t *c = a.copies + 3 * static_cast<int64_t>(r);
+        c[0] = from;
+        c[1] = to;
+        c[2] = n;
+    };
+    auto is_page = [&](int e) { return static_cast<uint32_t>(e) < static_cast<uint32_t>(a.pages); };
+
+    if (a.rows <= batch && sh_widest <= group) {
+        const int r = tid / group;
+        int lo, hi, length;
+        range(r, lo, hi, length);
+        int32_t *at = a.table + static_cast<int64_t>(r) * a.P + lo + in;
+        const bool mine = !over && lo + in < hi;
+        const int e = mine ? *at : -1;
+        const bool held = mine && is_page(e);
+        const bool shared = held && a.refs[held ? e : 0] > 1;
+        bool stays = false;
+        if (__syncthreads_or(shared)) {
+            if (shared) atomicSub(&a.refs[e], 1);
+            __syncthreads();
+            if (shared && atomicAdd(&a.refs[e], 0) <= 0) atomicMin(&a.refs[e], r - kKeeper);
+            __syncthreads();
+            if (shared) stays = atomicAdd(&a.refs[e], 0) + kKeeper == r;
+        }
+        const bool fresh = mine && (!held || (shared && !stays));
+        int total;
+        const int upto = reserve_scan(fresh, sh_scan, total);
+        const int missing = over ? -1 : (total > free ? total - free : 0);
+        if (tid == 0) a.missing[0] = missing;
+        int page = -1;
+        if (missing != 0) {
+            // nothing is taken: the references go back
+            if (stays) atomicExch(&a.refs[e], 0);
+            __syncthreads();
+            if (shared) atomicAdd(&a.refs[e], 1);
+        } else {
+            if (stays) atomicExch(&a.refs[e], 1);
+            if (fresh) {
+                page = free_page(a, sh_before, upto - 1);
+                *at = page;
+                a.refs[page] = 1;
+            }
+        }
+        if (r < a.rows && in == 0) {
+            const int n = length & (page_size - 1);
+            const bool moved = page >= 0 && held && n > 0;
+            copy_of(r, moved ? e : -1, moved ? page : -1, moved ? n : 0);
+        }
+        return;
+    }
+
     const uint64_t below = (group == kWave ? ~0ull : ((1ull << group) - 1))
                            << (lane & ~(group - 1));
     int need = 0;
@@ -394,7 +474,7 @@ __global__ __launch_bounds__(kReserveBlock) void pages_reserve_kernel(ReserveArg
             for (int i = lo + in; i < hi; i += group) {
                 const int e = row[i];
                 if (phase == 0) {
-                    if (static_cast<uint32_t>(e) < static_cast<uint32_t>(a.pages)) {
+                    if (is_page(e)) {
                         if (a.refs[e] > 1) row[i] = -2 - e;
                     } else if (e != -1) {
                         row[i] = -1;  // lists nothing
@@ -403,10 +483,7 @@ __global__ __launch_bounds__(kReserveBlock) void pages_reserve_kernel(ReserveArg
                     int *ref = &a.refs[-2 - e];
                     if (phase == 1) atomicSub(ref, 1);
                     if (phase == 2 && atomicAdd(ref, 0) <= 0) atomicMin(ref, r - kKeeper);
-                    if (phase == 3) {
-                        const int v = atomicAdd(ref, 0);
-                        need += !(v < 0 && v + kKeeper == r);
-                    }
+                    if (phase == 3) need += atomicAdd(ref, 0) + kKeeper != r;
                 } else if (phase == 3) {
                     need += e == -1;
                 }
@@ -424,21 +501,16 @@ __global__ __launch_bounds__(kReserveBlock) void pages_reserve_kernel(ReserveArg
         for (int phase = 0; phase < 2; ++phase) {
             for (int r0 = 0; r0 < a.rows; r0 += batch) {
                 const int r = r0 + tid / group;
-                if (r < a.rows && in == 0 && phase == 0) {
-                    a.copies[3 * static_cast<int64_t>(r)] = -1;
-                    a.copies[3 * static_cast<int64_t>(r) + 1] = -1;
-                    a.copies[3 * static_cast<int64_t>(r) + 2] = 0;
-                }
+                if (r < a.rows && in == 0 && phase == 0) copy_of(r, -1, -1, 0);
                 int lo, hi, length;
                 range(r, lo, hi, length);
                 int32_t *row = a.table + static_cast<int64_t>(r) * a.P;
-                for (int i = lo + in; i < hi; i += group) {
+                for (int i = lo + in; i < hi && !over; i += group) {
                     const int e = row[i];
                     if (e >= -1) continue;
                     int *ref = &a.refs[-2 - e];
                     if (phase == 0) {
-                        const int v = atomicAdd(ref, 0);
-                        if (v < 0 && v + kKeeper == r) atomicExch(ref, 0);
+                        if (atomicAdd(ref, 0) + kKeeper == r) atomicExch(ref, 0);
                     } else {
                         atomicAdd(ref, 1);
                         row[i] = -2 - e;
@@ -460,8 +532,7 @@ __global__ __launch_bounds__(kReserveBlock) void pages_reserve_kernel(ReserveArg
             e = i < hi ? row[i] : 0;
             if (e == -1) return true;
             if (e >= 0) return false;
-            const int v = atomicAdd(&a.refs[-2 - e], 0);
-            return !(v < 0 && v + kKeeper == r);
+            return atomicAdd(&a.refs[-2 - e], 0) + kKeeper != r;
         };
         int mine = 0, e;
         for (int i = lo + in; i < hi; i += group) mine += fresh(i, e);
@@ -475,23 +546,8 @@ __global__ __launch_bounds__(kReserveBlock) void pages_reserve_kernel(ReserveArg
             const bool f = fresh(i, e);
             const uint64_t who = __ballot(f) & below;
             if (f) {
-                int rank = before + done + __popcll(who & ((1ull << lane) - 1));
-                // the chunk that holds it: the last one with no more before it
-                int c = 0;
-                for (int step = 1 << 12; step; step >>= 1)
-                    if (c + step < a.chunks && sh_before[c + step] <= rank) c += step;
-                rank -= sh_before[c];
-                int page = c * kPageChunk;
-                for (int w = 0; w < kPageChunk / kWave; ++w) {
-                    uint64_t bits = a.words[c * (kPageChunk / kWave) + w];
-                    const int have = __popcll(bits);
-                    if (rank < have) {
-                        for (; rank > 0; --rank) bits &= bits - 1;
-                        page += w * kWave + __ffsll(static_cast<long long>(bits)) - 1;
-                        break;
-                    }
-                    rank -= have;
-                }
+                const int page =
+                    free_page(a, sh_before, before + done + __popcll(who & ((1ull << lane) - 1)));
                 row[i] = page;
                 a.refs[page] = 1;
                 if (e < -1 && i == lo && (length & (page_size - 1))) {
@@ -502,11 +558,7 @@ __global__ __launch_bounds__(kReserveBlock) void pages_reserve_kernel(ReserveArg
             }
             done += __popcll(who);
         }
-        if (r < a.rows && in == 0) {
-            a.copies[3 * static_cast<int64_t>(r)] = copy_from;
-            a.copies[3 * static_cast<int64_t>(r) + 1] = copy_to;
-            a.copies[3 * static_cast<int64_t>(r) + 2] = copy_n;
-        }
+        if (r < a.rows && in == 0) copy_of(r, copy_from, copy_to, copy_n);
         taken += all;
     }
     __threadfence_block();

@@ -73,6 +73,12 @@ struct TreeArgs {
     float scale2;            // scale * log2(e)
 };
 
+// Asks for every 64 bytes of the arguments at once: they come from far, and each
+// part that is first read later would be waited for again.
+__device__ __forceinline__ void tree_touch(const TreeArgs &a) {
+    asm volatile("" ::"s"(a.keys), "s"(a.parents), "s"(a.q_node), "s"(a.scale2));
+}
+
 // Types of keys and values.  Frag: a matrix operand's 8 elements along the
 // summed dimension; load8: 8 consecutive elements.
 template <typename T>
@@ -205,6 +211,13 @@ __device__ __forceinline__ uint32_t tree_finite(uint32_t w) {
     }
 }
 
+// A barrier over shared memory alone: stores to memory need not have arrived.
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 __device__ __forceinline__ float across_groups_max(float v) {
     v = fmaxf(v, __shfl_xor(v, 16, kWave));
     return fmaxf(v, __shfl_xor(v, 32, kWave));
@@ -261,12 +274,15 @@ __device__ __forceinline__ uint32_t tree_sees8(const uint64_t (*mask)[2], bool c
 template <typename T, int DP, int R>
 struct TreeShared {
     static constexpr int kPitch = DP + 4;  // 16 rows' starts on different banks
+    // row tiles that are joined at a time, by what shared memory holds beside
+    // another workgroup's
+    static constexpr int kJoin = R == 2 && DP <= 128 ? 2 : 1;
     union {
-        float merge[kTreeWaves][16][kPitch];
+        float merge[kJoin][kTreeWaves][16][kPitch];
         typename TreeElem<T>::Raw q[R][DP / 32][kWave];
     };
     float ml[kTreeWaves][16 * R][2];
-    int node[16 * R];  // a row's node, -1 where it is not in use
+    int node[16 * R];  // a row's node
     int odd;           // a node's value holds an infinity or a NaN
     uint64_t mask[kMaxTreeNodes][2];
     int up[kMaxTreeNodes];
@@ -369,7 +385,7 @@ __device__ __forceinline__ void tree_masks(const TreeArgs &a, Shared &sh, int b,
         sh.mask[i][0] = i < 64 ? 1ull << i : 0;
         sh.mask[i][1] = i < 64 ? 0 : 1ull << (i - 64);
     }
-    __syncthreads();
+    lds_barrier();
     for (int round = 1; round < live; round <<= 1) {
         uint64_t m0 = 0, m1 = 0;
         int up = -1;
@@ -378,13 +394,13 @@ __device__ __forceinline__ void tree_masks(const TreeArgs &a, Shared &sh, int b,
             m0 = sh.mask[sh.up[i]][0];
             m1 = sh.mask[sh.up[i]][1];
         }
-        __syncthreads();
+        lds_barrier();
         if (i < live) {
             sh.up[i] = up;
             sh.mask[i][0] |= m0;
             sh.mask[i][1] |= m1;
         }
-        __syncthreads();
+        lds_barrier();
     }
 }
 
@@ -448,6 +464,7 @@ __global__ __launch_bounds__(kTreeBlock, (tree_waves<T, DP>(R))) void tree_atten
     using Shared = TreeShared<T, DP, R>;
     __shared__ Shared sh;
 
+    tree_touch(a);
     const int units = a.slices * a.KV;
     const int mt = blockIdx.x / units;
     const int slice = (blockIdx.x % units) / a.KV;
@@ -492,7 +509,6 @@ __global__ __launch_bounds__(kTreeBlock, (tree_waves<T, DP>(R))) void tree_atten
         if (last < span.live && keys_end > span.cached + last + 1)
             keys_end = span.cached + last + 1;
         if (dead) keys_end = 0;
-        if (!dead && keys_end > span.cached && !chain) tree_masks(a, sh, b, span.live);
 
         // the queries: a row's operand in the lanes that take it
         constexpr int kQueries = (R * kSteps * kWave + kTreeBlock - 1) / kTreeBlock;
@@ -505,7 +521,7 @@ __global__ __launch_bounds__(kTreeBlock, (tree_waves<T, DP>(R))) void tree_atten
             const int row = (mt * R + r) * 16 + (qt & 15);
             const int node = row / a.G, d = 32 * s + 8 * (qt >> 4 & 3);
             queries[k] = Raw{};
-            if (r < R && node < span.live && d < a.D)
+            if (r < R && node < a.T && d < a.D)
                 queries[k] = tree_load8<T>(static_cast<const T *>(a.q) + b * a.q_batch +
                                            node * a.q_node + (h * a.G + row % a.G) * a.q_head + d);
         }
@@ -513,8 +529,11 @@ __global__ __launch_bounds__(kTreeBlock, (tree_waves<T, DP>(R))) void tree_atten
 
         // the pages of the keys that this lane loads at p0: keys 8(i16/4).. of the
         // first product, keys 8g.. of the second
+        // (an entry behind the sequence's end may be anything, and its page, if it is
+        // one, is read and not used)
         auto entry_of = [&](int p) {
-            return table[(p < span.keys ? p : span.keys - 1) >> a.shift];
+            const int e = p >> a.shift;
+            return table[e < a.P ? e : a.P - 1];
         };
         auto is_page = [&](int e) {
             return static_cast<uint32_t>(e) < static_cast<uint32_t>(a.pages);
@@ -552,14 +571,15 @@ __global__ __launch_bounds__(kTreeBlock, (tree_waves<T, DP>(R))) void tree_atten
             load_values(p0, page_v);
         }
 
-        __syncthreads();
+        lds_barrier();
+        if (!dead && keys_end > span.cached && !chain) tree_masks(a, sh, b, span.live);
 #pragma unroll
         for (int k = 0; k < kQueries; ++k)
             if (k * kTreeBlock + qt < R * kSteps * kWave)
                 (&sh.q[0][0][0])[k * kTreeBlock + qt] = queries[k];
-        if (qt < 16 * R) sh.node[qt] = mine < span.live ? mine : -1;
+        if (qt < 16 * R) sh.node[qt] = mine;
         if (qt == 0) sh.odd = 0;
-        __syncthreads();
+        lds_barrier();
 
         float m[R], l[R];  // a row's maximum, scaled to powers of two, and the lane's sum
         v4f32 o[R][kCols];
@@ -680,8 +700,9 @@ __global__ __launch_bounds__(kTreeBlock, (tree_waves<T, DP>(R))) void tree_atten
             if (odd) sh.odd = 1;
 #pragma unroll
             for (int r = 0; r < R; ++r) {
+                const int node = sh.node[16 * r + i16];
                 const uint32_t see =
-                    tree_sees8(sh.mask, chain, sh.node[16 * r + i16], pv - span.cached) &
+                    tree_sees8(sh.mask, chain, node < span.live ? node : -1, pv - span.cached) &
                     (held ? 0xFFu >> clamp_len(pv + 8 - span.keys, 8) : 0u);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
@@ -700,7 +721,7 @@ __global__ __launch_bounds__(kTreeBlock, (tree_waves<T, DP>(R))) void tree_atten
 
         // join the four waves and leave the rows, or their part
         const int jt = fresh_tid(), ji = jt & 15, jg = jt >> 4 & 3;
-        __syncthreads();
+        lds_barrier();
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             l[r] = across_groups_sum(l[r]);
@@ -709,76 +730,81 @@ __global__ __launch_bounds__(kTreeBlock, (tree_waves<T, DP>(R))) void tree_atten
                 sh.ml[wave][16 * r + ji][1] = l[r];
             }
         }
-        __syncthreads();
+        lds_barrier();
         const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (from == 0 ? 1 : 0);
+        constexpr int kJoin = Shared::kJoin, kPerRow = kTreeBlock / 16;  // threads to a row
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            float top = -__builtin_inff();
+        for (int r0 = 0; r0 < R; r0 += kJoin) {
 #pragma unroll
-            for (int w = 0; w < kTreeWaves; ++w) top = fmaxf(top, sh.ml[w][16 * r + ji][0]);
-            const float ref = top == -__builtin_inff() ? 0.0f : top;
-            const float f = hw_exp2(m[r] - ref);
-            // lane: query row ji, dimensions kChunk*(4g + e) + t of each chunk
+            for (int rj = 0; rj < kJoin; ++rj) {
+                const int r = r0 + rj;
+                float top = -__builtin_inff();
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c)
+                for (int w = 0; w < kTreeWaves; ++w) top = fmaxf(top, sh.ml[w][16 * r + ji][0]);
+                const float ref = top == -__builtin_inff() ? 0.0f : top;
+                const float f = hw_exp2(m[r] - ref);
+                // lane: query row ji, dimensions kChunk*(4 jg + e) + t of each chunk
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
+                for (int c = 0; c < kChunks; ++c)
 #pragma unroll
-                    for (int t4 = 0; t4 < kChunk / 4; ++t4) {
-                        v4f32 v;
+                    for (int e = 0; e < 4; ++e)
 #pragma unroll
-                        for (int t = 0; t < 4; ++t) v[t] = o[r][c * kChunk + 4 * t4 + t][e] * f;
-                        *reinterpret_cast<v4f32 *>(
-                            &sh.merge[wave][ji][c * 16 * kChunk + kChunk * (4 * jg + e) +
-                                                 4 * t4]) = v;
-                    }
-            __syncthreads();
-            const int qr = jt >> 4;  // 16 threads to a row
-            const int row = (mt * R + r) * 16 + qr;
-            const int nd = row / a.G;
-            float rtop = -__builtin_inff(), sum = 0.0f;
+                        for (int t4 = 0; t4 < kChunk / 4; ++t4) {
+                            v4f32 v;
 #pragma unroll
-            for (int w = 0; w < kTreeWaves; ++w) rtop = fmaxf(rtop, sh.ml[w][16 * r + qr][0]);
-            const float rref = rtop == -__builtin_inff() ? 0.0f : rtop;
-#pragma unroll
-            for (int w = 0; w < kTreeWaves; ++w) {
-                const float f2 = hw_exp2(sh.ml[w][16 * r + qr][0] - rref);
-                sum += sh.ml[w][16 * r + qr][1] * f2;
+                            for (int t = 0; t < 4; ++t)
+                                v[t] = o[r][c * kChunk + 4 * t4 + t][e] * f;
+                            *reinterpret_cast<v4f32 *>(
+                                &sh.merge[rj][wave][ji][c * 16 * kChunk + kChunk * (4 * jg + e) +
+                                                        4 * t4]) = v;
+                        }
             }
-            const bool on = nd < span.live;
-            if (nd < a.T && (whole || on)) {
+            lds_barrier();
+#pragma unroll
+            for (int rj = 0; rj < kJoin; ++rj) {
+                const int r = r0 + rj, qr = jt / kPerRow, in = jt % kPerRow;
+                const int row = (mt * R + r) * 16 + qr;
+                const int nd = sh.node[16 * r + qr];
+                float rtop = -__builtin_inff(), sum = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kTreeWaves; ++w) rtop = fmaxf(rtop, sh.ml[w][16 * r + qr][0]);
+                const float rref = rtop == -__builtin_inff() ? 0.0f : rtop;
+#pragma unroll
+                for (int w = 0; w < kTreeWaves; ++w)
+                    sum += sh.ml[w][16 * r + qr][1] * hw_exp2(sh.ml[w][16 * r + qr][0] - rref);
+                const bool on = nd < span.live, some = on && !(sum == 0.0f);
+                if (nd >= a.T || !(whole || on)) continue;
                 const float inv = 1.0f / sum;
-                const int64_t orow = (static_cast<int64_t>(b) * a.T + nd) * a.H + h * a.G +
-                                     row % a.G;
-                for (int d = (jt & 15) * 4; d < a.D; d += 64) {
+                const int64_t orow =
+                    (static_cast<int64_t>(b) * a.T + nd) * a.H + h * a.G + row - nd * a.G;
+                for (int d = in * 4; d < a.D; d += kPerRow * 4) {
                     v4f32 v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                     for (int w = 0; w < kTreeWaves; ++w)
-                        v += *reinterpret_cast<const v4f32 *>(&sh.merge[w][qr][d]);
+                        v += *reinterpret_cast<const v4f32 *>(&sh.merge[rj][w][qr][d]);
                     if (whole) {
                         T *out = static_cast<T *>(a.out) + orow * a.D + d;
 #pragma unroll
                         for (int t = 0; t < 4; ++t)
-                            out[t] = static_cast<T>(on && !(sum == 0.0f) ? v[t] * inv : 0.0f);
+                            out[t] = static_cast<T>(some ? v[t] * inv : 0.0f);
                     } else {
                         float *part = a.part + (slot * (16 * R) + 16 * r + qr) * a.D + d;
                         *reinterpret_cast<v4f32 *>(part) = v;
                     }
                 }
-                if ((jt & 15) == 0) {
+                if (in == 0) {
                     if (whole) {
                         if (a.lse)
-                            a.lse[orow] = on && !(sum == 0.0f)
-                                              ? static_cast<float>(kLn2) *
-                                                    (rref + hw_log2(sum))
-                                              : -__builtin_inff();
+                            a.lse[orow] = some ? static_cast<float>(kLn2) * (rref + hw_log2(sum))
+                                               : -__builtin_inff();
                     } else {
-                        *reinterpret_cast<v4f32 *>(a.part_ml + (slot * (16 * R) + 16 * r + qr) * 4) =
+                        *reinterpret_cast<v4f32 *>(a.part_ml +
+                                                   (slot * (16 * R) + 16 * r + qr) * 4) =
                             v4f32{rtop, sum, sum, 0.0f};
                     }
                 }
             }
-            __syncthreads();
+            if (r0 + kJoin < R) lds_barrier();
         }
         if (__builtin_expect(sh.odd, 0))
             tree_add_odd<T>(a, sh.mask, span, b, h, from * kTreeTile, keys_end, whole, slot,
@@ -858,6 +884,7 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
     static_assert(kTreeTile % kKeys == 0, "tiles are dealt out in whole ones");
     __shared__ TreeWideShared<DP> sh;
 
+    tree_touch(a);
     const int units = a.slices * a.KV;
     const int mt = blockIdx.x / units;
     const int slice = (blockIdx.x % units) / a.KV;
@@ -916,7 +943,7 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
         if (dead) keys_end = 0;
         const int begin = from * kTreeTile;
 
-        __syncthreads();
+        lds_barrier();
         if (tid == 0) sh.odd = 0;
         if (keys_end > span.cached && !chain) tree_masks(a, sh, b, span.live);
 
@@ -1111,7 +1138,7 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
         // entry and held: the tile's own; entry_next: the following one's
         int entry = 0, entry_next = 0, p0 = begin, stage = 0;
         uint64_t held = 0;
-        __syncthreads();  // the stages are free
+        lds_barrier();  // the stages are free
         if (p0 < keys_end) {
             entry = entry_of(p0);
             entry_next = entry_of(p0 + kKeys);
@@ -1119,7 +1146,7 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
             load(0, p0, entry);
             tree_loads_done();
         }
-        __syncthreads();
+        lds_barrier();
         // while every row sees every key and a tile follows, which is on its way
         // meanwhile; then the rest: the last tile, the nodes, and everything behind
         // a page that is missing
@@ -1134,11 +1161,11 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
             p0 += kKeys;
             stage ^= 1;
             tree_loads_done();
-            __syncthreads();
+            lds_barrier();
         }
         while (p0 < keys_end) {
             clean(stage, p0, held);
-            __syncthreads();
+            lds_barrier();
             if (mine) score(stage);
 #pragma unroll
             for (int kb = 0; kb < kBlocks; ++kb) {
@@ -1162,7 +1189,7 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
                 entry_next = entry_of(p0 + kKeys);
                 tree_loads_done();
             }
-            __syncthreads();
+            lds_barrier();
         }
 
         // leave the rows, or their part
@@ -1216,6 +1243,7 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
 // a part's dimensions.
 template <typename T, int L>
 __global__ __launch_bounds__(kTreeBlock) void tree_join_kernel(TreeArgs a, int rows16) {
+    tree_touch(a);
     const int64_t row_at = static_cast<int64_t>(blockIdx.x) * kTreeWaves + threadIdx.x / kWave;
     const int lane = threadIdx.x & (kWave - 1);
     if (row_at >= static_cast<int64_t>(a.B) * a.T * a.H) return;

@@ -641,8 +641,9 @@ typedef struct spec_cache {
  * counts as nothing), has out 0 and lse -inf.  Sums and products are taken in
  * 32 bits; for 16-bit types the weights are rounded to the type before their
  * product with the values.  out and lse overlap no input.  workspace: device,
- * spec_tree_attention_workspace_bytes (0 if the arguments are not valid),
- * 16-byte aligned; its contents on entry do not matter.
+ * spec_tree_attention_workspace_bytes (0, and then NULL will do, for tables of
+ * few positions; 0 too if the arguments are not valid), 16-byte aligned; its
+ * contents on entry do not matter.
  */
 size_t spec_tree_attention_workspace_bytes(const spec_cache *cache, int32_t nodes, int32_t heads);
 spec_status spec_tree_attention(const spec_cache *cache, const void *q, int64_t q_batch_stride,

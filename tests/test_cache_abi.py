@@ -73,7 +73,7 @@ def test_tree_attention_validates_on_host(L):
     for kw in (dict(T=129, parents=P(16)), dict(T=65537), dict(H=65540), dict(batch=2 ** 31 - 1),
                dict(sb=1 << 41)):
         assert call(**kw) == -2, kw
-    for kw in (dict(ws=None), dict(n=64)):
+    for kw in (dict(ws=None, table_width=65), dict(n=64, table_width=65)):
         assert call(**kw) == -3, kw
     assert call(batch=0, keys=None, values=None, table=None, lengths=None, q=None, out=None,
                 ws=None, n=0) == 0
@@ -82,8 +82,11 @@ def test_tree_attention_validates_on_host(L):
 def test_tree_workspace(L):
     def need(T=3, H=8, **kw):
         return L.spec_tree_attention_workspace_bytes(ctypes.byref(cache(**kw)), T, H)
-    assert need() > 0 and need() % 256 == 0
-    assert need(batch=0) == 0 and need(T=0) == 0 and need(H=6) == 0 and need(page_size=12) == 0
+    assert need() == 0  # sequences of at most 1024 positions are not cut
+    assert need(table_width=64) == 0
+    assert need(table_width=65) > 0 and need(table_width=65) % 256 == 0
+    for kw in (dict(batch=0), dict(T=0), dict(H=6), dict(page_size=12)):
+        assert need(table_width=65, **kw) == 0
     assert L.spec_tree_attention_workspace_bytes(None, 3, 8) == 0
 
 

@@ -181,6 +181,15 @@ def test_long_and_short_sequences_share_the_work(dt):
     check(both, call(on_gpu(both), lse=True))
 
 
+@pytest.mark.parametrize("T,G", [(3, 2), (6, 4), (9, 4), (9, 8)])
+def test_cut_and_whole_sequences_agree(T, G):
+    """A wider table row has the same sequence cut over workgroups and joined."""
+    c = make(T, BF16, 3, T, 2 * G, 2, 128, 16, 0, 900, tree=True, least=0)
+    check(c, call(on_gpu(c), lse=True))
+    c["table"] = torch.cat([c["table"], torch.full((3, 70), -1, dtype=torch.int32)], 1)
+    check(c, call(on_gpu(c), lse=True))
+
+
 def test_many_sequences():
     """More sequences than a workgroup has threads."""
     c = make(11, BF16, 700, 1, 2, 1, 64, 8, 0, 40, least=0)
@@ -309,7 +318,7 @@ def test_offsets_beyond_32_bits():
 
 
 def test_repeats_to_the_bit_and_with_any_workspace():
-    c = make(22, BF16, 5, 4, 8, 2, 128, 16, 0, 900, tree=True)
+    c = make(22, BF16, 5, 4, 8, 2, 128, 16, 1100, 1900, tree=True)
     d = on_gpu(c)
     a = call(d, lse=True)
     n = sv._tree_workspace_bytes(5, c["table"].shape[1], 16, 2, 128, sv.DTYPE_BF16, 4, 8)
@@ -321,7 +330,7 @@ def test_repeats_to_the_bit_and_with_any_workspace():
 
 
 def test_in_graphs_that_share_a_workspace_and_on_streams():
-    cs = [make(30 + i, BF16, 3, 4, 8, 2, 128, 16, 0, 700, tree=i == 1) for i in range(2)]
+    cs = [make(30 + i, BF16, 3, 4, 8, 2, 128, 16, 1100, 1700, tree=i == 1) for i in range(2)]
     ds = [on_gpu(c) for c in cs]
     want = [call(d, lse=True) for d in ds]
     n = max(sv._tree_workspace_bytes(3, c["table"].shape[1], 16, 2, 128, sv.DTYPE_BF16, 4, 8)
@@ -403,9 +412,10 @@ def test_refusals():
     refused(ValueError, num_nodes=torch.ones(3, dtype=torch.int32, device="cuda"))
     refused(ValueError, out=d["q"][:, :1].contiguous())
     for kw in (dict(scale=0.0), dict(scale=-1.0), dict(scale=math.inf), dict(scale=math.nan),
-               dict(out=d["q"]), dict(workspace=torch.empty(16, dtype=torch.uint8, device="cuda")),
-               dict(q=d["q"][:, :, :3].contiguous())):
+               dict(out=d["q"]), dict(q=d["q"][:, :, :3].contiguous())):
         refused(sv.SpecVerifyError, **kw)
+    refused(sv.SpecVerifyError, table=torch.full((2, 100), -1, dtype=torch.int32, device="cuda"),
+            workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     wide = torch.zeros(2, 2, 4, 68, dtype=BF16, device="cuda")[..., 2:66]  # 4 bytes off
     refused(sv.SpecVerifyError, q=wide)
     c = make(1, BF16, 1, 129, 1, 1, 64, 16, 5, 9, tree=True)
