@@ -118,7 +118,8 @@ spec_status check_tree(const spec_cache *c, int32_t nodes, int32_t heads, bool t
     if (c->batch > INT32_MAX / tiles) return SPEC_ERR_UNSUPPORTED;
     const int64_t rows = static_cast<int64_t>(c->batch) * nodes;
     if (rows > 0 && rows > (int64_t{1} << 40) / heads) return SPEC_ERR_UNSUPPORTED;
-    if (!grid_fits(rows * heads / kTreeWaves + 1, kTreeBlock)) return SPEC_ERR_UNSUPPORTED;
+    const int64_t joins = (static_cast<int64_t>(nodes) * heads / kTreeWaves + 1) * c->batch;
+    if (!grid_fits(joins, kTreeBlock)) return SPEC_ERR_UNSUPPORTED;
     return SPEC_OK;
 }
 
@@ -207,16 +208,29 @@ void launch_tree(const TreeArgs &a, const TreePlan &p, hipStream_t st) {
         launch_tree_dim<T, 256>(a, p, st);
 }
 
+// Four rows to a wave where there are rows for every wave that the chip holds.
+constexpr int64_t kJoinRows = 8192;
+
+template <typename T, int L>
+void launch_join_rows(const TreeArgs &a, const TreePlan &p, hipStream_t st) {
+    const int rows = a.T * a.H;
+    const bool four = static_cast<int64_t>(a.B) * rows >= kJoinRows && rows % 4 == 0;
+    const int per = kTreeWaves * (four ? 4 : 1), blocks = (rows + per - 1) / per;
+    const dim3 grid(static_cast<unsigned>(blocks * a.B)), block(kTreeBlock);
+    if (four)
+        tree_join_kernel<T, L, 4><<<grid, block, 0, st>>>(a, p.rows, blocks);
+    else
+        tree_join_kernel<T, L, 1><<<grid, block, 0, st>>>(a, p.rows, blocks);
+}
+
 template <typename T>
 void launch_join(const TreeArgs &a, const TreePlan &p, hipStream_t st) {
-    const int64_t rows = static_cast<int64_t>(a.B) * a.T * a.H;
-    const dim3 grid(static_cast<unsigned>((rows + kTreeWaves - 1) / kTreeWaves));
     if (p.dp == 64)
-        tree_join_kernel<T, 16><<<grid, dim3(kTreeBlock), 0, st>>>(a, p.rows);
+        launch_join_rows<T, 16>(a, p, st);
     else if (p.dp == 128)
-        tree_join_kernel<T, 32><<<grid, dim3(kTreeBlock), 0, st>>>(a, p.rows);
+        launch_join_rows<T, 32>(a, p, st);
     else
-        tree_join_kernel<T, 64><<<grid, dim3(kTreeBlock), 0, st>>>(a, p.rows);
+        launch_join_rows<T, 64>(a, p, st);
 }
 
 // ---------------------------------------------------------------------------

@@ -1238,85 +1238,106 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
     }
 }
 
-// Joins the parts of a row whose sequence was cut: a wave per row.  Its lanes
-// take the parts' references and sums, then 64 / L parts at a time, L lanes to
-// a part's dimensions.
-template <typename T, int L>
-__global__ __launch_bounds__(kTreeBlock) void tree_join_kernel(TreeArgs a, int rows16) {
+// Joins the parts of the rows of sequences that were cut.  A wave takes NR rows of
+// a sequence; its lanes take the parts' references and sums, then 64 / L parts at
+// a time, L lanes to a part's dimensions.  Everything that depends on nothing read
+// before is asked for at once: the launch is bound by how often it waits.
+template <typename T, int L, int NR>
+__global__ __launch_bounds__(kTreeBlock) void tree_join_kernel(TreeArgs a, int rows16,
+                                                               int blocks) {
     tree_touch(a);
-    const int64_t row_at = static_cast<int64_t>(blockIdx.x) * kTreeWaves + threadIdx.x / kWave;
+    constexpr int kAt = kWave / L, kAhead = NR == 1 ? 8 : 2;  // parts at a time, and ahead
+    const int b = blockIdx.x / blocks;
     const int lane = threadIdx.x & (kWave - 1);
-    if (row_at >= static_cast<int64_t>(a.B) * a.T * a.H) return;
-    const int head = static_cast<int>(row_at % a.H);
-    const int nd = static_cast<int>(row_at / a.H % a.T);
-    const int b = static_cast<int>(row_at / a.H / a.T);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int per = a.first[a.B], first = a.first[b];
     const TreeSpan span = tree_span(a, b);
     const int w0 = first / per, w1 = (first + tree_tiles(span.keys) - 1) / per;
-    if (w0 == w1) return;
-    T *out = static_cast<T *>(a.out) + row_at * a.D;
+    const int n = w1 - w0 + 1;
+    if (n == 1) return;
+    const int of = a.T * a.H;  // rows of the sequence
+    const int row0 = ((blockIdx.x % blocks) * kTreeWaves + wave) * NR;
+    if (row0 >= of) return;
     const int d = lane % L * 4;
-    if (nd >= span.live) {
-        if (lane < L && d < a.D)
-            for (int t = 0; t < 4; ++t) out[d + t] = static_cast<T>(0.0f);
-        if (lane == 0 && a.lse) a.lse[row_at] = -__builtin_inff();
-        return;
-    }
-    const int h = head / a.G;
-    const int row = nd * a.G + head % a.G;
-    const int64_t step = static_cast<int64_t>(a.KV) * 2 * rows16;  // from a slice's part to the next's
-    const int64_t at0 = (static_cast<int64_t>(row / rows16) * a.slices * a.KV + h) * 2 * rows16 +
-                        row % rows16;
-    auto at = [&](int w) { return at0 + w * step + (w == w0 ? rows16 : 0); };
-    auto ml_of = [&](int w) {
-        return w <= w1 ? *reinterpret_cast<const v4f32 *>(a.part_ml + at(w) * 4)
-                       : v4f32{-__builtin_inff(), 0.0f, 0.0f, 0.0f};
-    };
-    float top = -__builtin_inff();
-    for (int w = w0; w <= w1; w += kWave) top = fmaxf(top, ml_of(w + lane)[0]);
+    const int64_t step = static_cast<int64_t>(a.KV) * 2 * rows16;  // to the next slice's part
+    int64_t at0[NR];
+    bool on[NR];
+    v4f32 ml[NR], p[NR][kAhead];
 #pragma unroll
-    for (int o = 1; o < kWave; o <<= 1) top = fmaxf(top, __shfl_xor(top, o, kWave));
-    const float ref = top == -__builtin_inff() ? 0.0f : top;
-    float sum = 0.0f, norm = 0.0f;
-    v4f32 v = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int wb = w0; wb <= w1; wb += kWave) {
-        const v4f32 ml = ml_of(wb + lane);
-        const float f = hw_exp2(ml[0] - ref);
-        sum += f * ml[1];
-        norm += f * ml[2];
-        const int n = w1 - wb + 1 < kWave ? w1 - wb + 1 : kWave;
-        for (int k0 = 0; k0 < n; k0 += 4 * (kWave / L)) {
-            v4f32 p[4];
-            float fk[4];
+    for (int r = 0; r < NR; ++r) {
+        const int nd = (row0 + r) / a.H, head = (row0 + r) % a.H;
+        on[r] = nd < span.live;
+        const int h = head / a.G, row = nd * a.G + head - h * a.G;
+        // a slice's part 1 where the sequence begins in it, else 0
+        at0[r] = ((static_cast<int64_t>(row / rows16) * a.slices + w0) * a.KV + h) * 2 * rows16 +
+                 row % rows16;
+        ml[r] = v4f32{-__builtin_inff(), 0.0f, 0.0f, 0.0f};
+        if (on[r] && lane < n)
+            ml[r] = *reinterpret_cast<const v4f32 *>(
+                a.part_ml + (at0[r] + lane * step + (lane ? 0 : rows16)) * 4);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int k = k0 + u * (kWave / L) + lane / L;
-                fk[u] = __shfl(f, k & (kWave - 1), kWave);
-                p[u] = v4f32{0.0f, 0.0f, 0.0f, 0.0f};
-                if (k < n && d < a.D)
-                    p[u] = *reinterpret_cast<const v4f32 *>(a.part + at(wb + k) * a.D + d);
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) v += p[u] * fk[u];
+        for (int u = 0; u < kAhead; ++u) {
+            const int k = u * kAt + lane / L;
+            p[r][u] = v4f32{0.0f, 0.0f, 0.0f, 0.0f};
+            if (on[r] && k < n && d < a.D)
+                p[r][u] = *reinterpret_cast<const v4f32 *>(
+                    a.part + (at0[r] + k * step + (k ? 0 : rows16)) * a.D + d);
         }
     }
 #pragma unroll
-    for (int o = 1; o < kWave; o <<= 1) {
-        sum += __shfl_xor(sum, o, kWave);
-        norm += __shfl_xor(norm, o, kWave);
+    for (int r = 0; r < NR; ++r) {
+        if (row0 + r >= of) break;
+        const int64_t row_at = static_cast<int64_t>(b) * of + row0 + r;
+        T *out = static_cast<T *>(a.out) + row_at * a.D;
+        auto ml_of = [&](int k) {
+            return k < n ? *reinterpret_cast<const v4f32 *>(
+                               a.part_ml + (at0[r] + k * step + (k ? 0 : rows16)) * 4)
+                         : v4f32{-__builtin_inff(), 0.0f, 0.0f, 0.0f};
+        };
+        float top = ml[r][0];
+        if (on[r])
+            for (int k = kWave; k < n; k += kWave) top = fmaxf(top, ml_of(k + lane)[0]);
+#pragma unroll
+        for (int o = 1; o < kWave; o <<= 1) top = fmaxf(top, __shfl_xor(top, o, kWave));
+        const float ref = top == -__builtin_inff() ? 0.0f : top;
+        float f = hw_exp2(ml[r][0] - ref);
+        float sum = f * ml[r][1], norm = f * ml[r][2];
+        v4f32 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            v += p[r][u] * __shfl(f, (u * kAt + lane / L) & (kWave - 1), kWave);
+        if (on[r])
+            for (int k0 = kAhead * kAt; k0 < n; k0 += kAt) {
+                if (k0 % kWave == 0) {
+                    const v4f32 more = ml_of(k0 + lane);
+                    f = hw_exp2(more[0] - ref);
+                    sum += f * more[1];
+                    norm += f * more[2];
+                }
+                const int k = k0 + lane / L;
+                const float fk = __shfl(f, k & (kWave - 1), kWave);
+                if (k < n && d < a.D)
+                    v += *reinterpret_cast<const v4f32 *>(a.part + (at0[r] + k * step) * a.D + d) *
+                         fk;
+            }
+#pragma unroll
+        for (int o = 1; o < kWave; o <<= 1) {
+            sum += __shfl_xor(sum, o, kWave);
+            norm += __shfl_xor(norm, o, kWave);
+        }
+#pragma unroll
+        for (int o = L; o < kWave; o <<= 1)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) v[t] += __shfl_xor(v[t], o, kWave);
+        const bool some = on[r] && !(sum == 0.0f);
+        if (lane < L && d < a.D) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) out[d + t] = static_cast<T>(some ? v[t] / norm : 0.0f);
+        }
+        if (lane == 0 && a.lse)
+            a.lse[row_at] = some ? static_cast<float>(kLn2) * (ref + hw_log2(sum))
+                                 : -__builtin_inff();
     }
-#pragma unroll
-    for (int o = L; o < kWave; o <<= 1)
-#pragma unroll
-        for (int t = 0; t < 4; ++t) v[t] += __shfl_xor(v[t], o, kWave);
-    const bool some = !(sum == 0.0f);
-    if (lane < L && d < a.D) {
-#pragma unroll
-        for (int t = 0; t < 4; ++t) out[d + t] = static_cast<T>(some ? v[t] / norm : 0.0f);
-    }
-    if (lane == 0 && a.lse)
-        a.lse[row_at] = some ? static_cast<float>(kLn2) * (ref + hw_log2(sum))
-                             : -__builtin_inff();
 }
 
 }  // namespace sv
