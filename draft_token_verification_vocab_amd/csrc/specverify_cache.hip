@@ -129,8 +129,13 @@ TreePlan plan_tree(const spec_cache *c, int32_t nodes, int32_t heads) {
     const int64_t rows = static_cast<int64_t>(nodes) * (heads / c->kv_heads);
     const int64_t tiles16 = (rows + 15) / 16;
     const bool half = c->dtype != SPEC_DTYPE_F32;
-    // (the first addresses a few slots by 32 bits)
-    p.wide = half && tiles16 > (p.dp == 256 ? 1 : 3) && c->slot_stride <= (1 << 24);
+    const int64_t longest =
+        (static_cast<int64_t>(c->table_width) * c->page_size + kTreeTile - 1) / kTreeTile;
+    // 16-bit types take keys and values through shared memory, except for few rows
+    // of short sequences, where four waves that share out the keys are done sooner
+    // (and for slots further apart than the loads' 32-bit offsets reach)
+    p.wide = half && (longest > kTreeWhole || tiles16 > (p.dp == 256 ? 1 : 3)) &&
+             c->slot_stride <= (1 << 24);
     if (p.wide) {
         p.rt = tiles16 > 4 ? 2 : 1;
         p.rows = 64 * p.rt;
@@ -147,8 +152,6 @@ TreePlan plan_tree(const spec_cache *c, int32_t nodes, int32_t heads) {
     }
     p.mtiles = static_cast<int>((rows + p.rows - 1) / p.rows);
     const int64_t units = static_cast<int64_t>(p.mtiles) * c->kv_heads;
-    const int64_t longest =
-        (static_cast<int64_t>(c->table_width) * c->page_size + kTreeTile - 1) / kTreeTile;
     const int64_t tiles = c->batch * longest;
     // short sequences are not cut: no second launch
     p.whole = longest <= (p.wide ? kTreeWholeWide : kTreeWhole);
@@ -168,10 +171,12 @@ void launch_tree_rt(const TreeArgs &a, const TreePlan &p, hipStream_t st) {
     const dim3 grid(static_cast<unsigned>(p.slices * a.KV * p.mtiles)), block(kTreeBlock);
     if constexpr (sizeof(T) == 2) {
         if (p.wide) {
-            if (p.rt == 2)
-                tree_wide_kernel<T, DP, 2, FULL><<<grid, block, 0, st>>>(a);
+            if (p.mtiles > 1)
+                tree_wide_kernel<T, DP, 2, FULL, false><<<grid, block, 0, st>>>(a);
+            else if (p.rt == 2)
+                tree_wide_kernel<T, DP, 2, FULL, true><<<grid, block, 0, st>>>(a);
             else
-                tree_wide_kernel<T, DP, 1, FULL><<<grid, block, 0, st>>>(a);
+                tree_wide_kernel<T, DP, 1, FULL, true><<<grid, block, 0, st>>>(a);
             return;
         }
         if constexpr (DP <= 128) {

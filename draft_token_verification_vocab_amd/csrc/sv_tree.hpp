@@ -844,9 +844,16 @@ constexpr int kTreeArith = 0x406;
 // destination register and the compiler does not know of it, so that reading
 // another stage does not wait for it; tree_loads_done() does.  Nothing else in the
 // kernel uses m0 (shared memory needs none on this architecture).
+template <bool ONCE>
 __device__ __forceinline__ void tree_load_lds(const void *p, uint32_t at, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(at), "s"(p)
-                 : "memory");
+    if (ONCE)  // past the caches' usual order
+        asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(lds), "v"(at),
+                     "s"(p)
+                     : "memory");
+    else
+        asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(at),
+                     "s"(p)
+                     : "memory");
 }
 __device__ __forceinline__ void tree_loads_done() {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -872,7 +879,8 @@ struct TreeWideShared {
     int odd;
 };
 
-template <typename T, int DP, int R, bool FULL>
+// ONCE: no other workgroup reads the same keys.
+template <typename T, int DP, int R, bool FULL, bool ONCE>
 __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_kernel(TreeArgs a) {
     using E = TreeElem<T>;
     using Frag = typename E::Frag;
@@ -881,6 +889,8 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
     constexpr int kSteps = DP / 32, kCols = DP / 16, kRow = DP / 8;
     constexpr int kLoads = kKeys * kRow / kTreeBlock;  // chunks per thread and matrix
     constexpr int kTile = 64 * R;                      // rows of a workgroup
+    // few rows leave the time to follow every maximum
+    constexpr float kSlack = R == 1 ? 0.0f : kTreeSlack;
     static_assert(kTreeTile % kKeys == 0, "tiles are dealt out in whole ones");
     __shared__ TreeWideShared<DP> sh;
 
@@ -999,8 +1009,8 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
                 const int64_t at =
                     page * a.page_stride + ((p0 + key) & slot_mask) * slot_stride;
                 if (FULL || 8 * chunk[k] < a.D) {
-                    tree_load_lds(keys + at, lane_at[k], to_k + k * kTreeBlock * 16);
-                    tree_load_lds(values + at, lane_at[k], to_v + k * kTreeBlock * 16);
+                    tree_load_lds<ONCE>(keys + at, lane_at[k], to_k + k * kTreeBlock * 16);
+                    tree_load_lds<ONCE>(values + at, lane_at[k], to_v + k * kTreeBlock * 16);
                 }
             }
         };
@@ -1066,7 +1076,7 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
                 for (int j = 1; j < 8 * kBlocks; ++j)
                     t = fmaxf(t, z[j / 8][r][j / 4 % 2][j % 4]);
                 top[r] = t * a.scale2;
-                behind |= top[r] > m[r] + kTreeSlack;
+                behind |= top[r] > m[r] + kSlack;
             }
             if (__builtin_expect(__any(behind), 0)) {
 #pragma unroll
