@@ -1031,11 +1031,14 @@ def beam_reorder(parents: torch.Tensor, states, outs=None, *,
 _CACHE_DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
 
 
+_INT32 = torch.int32
+
+
 def _ints(t, name, index, shape):
     """Raise unless t is a contiguous int32 tensor of this shape on GPU index."""
-    if not (t.dtype is torch.int32 and t.get_device() == index and t.shape == shape
+    if not (t.dtype is _INT32 and t.shape == shape and t.get_device() == index
             and t.is_contiguous()):
-        _need_cuda(t, name, torch.device("cuda", index), torch.int32, shape)
+        _need_cuda(t, name, torch.device("cuda", index), _INT32, shape)
 
 
 def _strides(t):
@@ -1052,25 +1055,28 @@ def _same_layout(t, u):
 def _cache(keys, values, table, lengths):
     """(the checked _Cache of two pools [pages, heads, page, dim] and a table [B, P],
     the GPU's index)."""
-    index = keys.get_device()
+    index, shape, strides = keys.get_device(), keys.shape, keys.stride()
+    code = _CACHE_DTYPES.get(keys.dtype)
     if index < 0:
         raise ValueError("keys must be a GPU tensor")
-    if keys.dim() != 4 or keys.stride(3) != 1:
+    if len(shape) != 4 or strides[3] != 1:
         raise ValueError("keys must be [pages, heads, page, dim] with a contiguous last dimension")
-    if not _same_layout(values, keys):
+    if not (values.stride() == strides and values.shape == shape and values.dtype is keys.dtype
+            and values.get_device() == index) and not _same_layout(values, keys):
         raise ValueError("values must be laid out as keys, on the same device")
-    code = _CACHE_DTYPES.get(keys.dtype)
     if code is None:
         raise TypeError("keys and values must be float32, bfloat16 or float16, got %s" % keys.dtype)
-    if table.dim() != 2:
+    at = table.shape
+    if len(at) != 2:
         raise ValueError("table must be [B, pages of a sequence]")
-    B, P = shape = table.shape
-    _ints(table, "table", index, shape)
+    B, P = at
+    _ints(table, "table", index, at)
     _ints(lengths, "lengths", index, (B,))
-    N, kv, page, D = keys.shape
-    s = _strides(keys)
-    return _Cache(keys.data_ptr(), values.data_ptr(), s[0], s[1], s[2], table.data_ptr(),
-                  lengths.data_ptr(), B, N, page, P, kv, D, code, 0), index
+    N, kv, page, D = shape
+    if 1 in shape:
+        strides = _strides(keys)
+    return _Cache(keys.data_ptr(), values.data_ptr(), strides[0], strides[1], strides[2],
+                  table.data_ptr(), lengths.data_ptr(), B, N, page, P, kv, D, code, 0), index
 
 
 def _need_rows(t, name, index, keys, B, heads=None):
@@ -1079,14 +1085,14 @@ def _need_rows(t, name, index, keys, B, heads=None):
         raise ValueError("%s must be on cuda:%d" % (name, index))
     if t.dtype is not keys.dtype:
         raise ValueError("%s must be %s, not %s" % (name, keys.dtype, t.dtype))
-    shape = t.shape
+    shape, strides = t.shape, t.stride()
     if (len(shape) != 4 or shape[0] != B or shape[3] != keys.shape[3]
             or (heads is not None and shape[2] != heads)):
         raise ValueError("%s must have shape (%d, nodes, %s, %d), not %s"
                          % (name, B, heads or "heads", keys.shape[3], tuple(shape)))
-    if t.stride(3) != 1:
+    if strides[3] != 1:
         raise ValueError("%s must have a contiguous last dimension" % name)
-    return _strides(t)
+    return strides if 1 not in shape else _strides(t)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -1157,7 +1163,8 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, keys: torch.Tensor, values: t
     (keys, values), the pools written."""
     c, index = _cache(keys, values, table, lengths)
     strides = _need_rows(k, "k", index, keys, c.batch, c.kv_heads)
-    if not _same_layout(v, k):
+    if not (v.stride() == k.stride() and v.shape == k.shape and v.dtype is k.dtype
+            and v.get_device() == index) and not _same_layout(v, k):
         raise ValueError("v must be laid out as k")
     if num_nodes is not None:
         _ints(num_nodes, "num_nodes", index, (c.batch,))
@@ -1177,10 +1184,10 @@ def tree_accept(parents: torch.Tensor, tokens: torch.Tensor, chosen: torch.Tenso
     verification, or its own samples).  Returns path (int32 [B, T], the accepted
     nodes, then -1), count (int32 [B]) and tokens (int32 [B, T], what is emitted:
     count tokens, the last one the target's own)."""
-    if tokens.dim() != 2:
+    index, shape = tokens.get_device(), tokens.shape
+    if len(shape) != 2:
         raise ValueError("tokens must be [B, nodes]")
-    B, T = shape = tokens.shape
-    index = tokens.get_device()
+    B, T = shape
     if index < 0:
         raise ValueError("tokens must be a GPU tensor")
     _ints(tokens, "tokens", index, shape)
@@ -1208,21 +1215,22 @@ def _pools(pools, index):
     first = pools[0]
     if first.get_device() != index:
         raise ValueError("pools[0] must be on cuda:%d" % index)
-    if first.dim() != 4 or first.stride(3) != 1:
+    dtype, shape, stride = first.dtype, first.shape, first.stride()
+    if len(shape) != 4 or stride[3] != 1:
         raise ValueError("pools[0] must be [pages, heads, page, dim] with a contiguous last "
                          "dimension")
-    dtype, shape, stride = first.dtype, first.shape, first.stride()
-    for i, t in enumerate(pools):
-        if not (t.dtype is dtype and t.shape == shape and t.get_device() == index
-                and t.stride() == stride) and not _same_layout(t, first):
-            raise ValueError("pools[%d] must be laid out as pools[0], on the same device" % i)
+    for t in pools:
+        if not (t.stride() == stride and t.shape == shape and t.dtype is dtype
+                and t.get_device() == index) and not _same_layout(t, first):
+            raise ValueError("every tensor of pools must be laid out as pools[0], on its device")
     n = len(pools)
     bases = _address_array(n)(*[t.data_ptr() for t in pools])
     e = first.element_size()
-    s = _strides(first)
+    if 1 in shape:
+        stride = _strides(first)
     N, kv, page, D = shape
-    return _CachePools(ctypes.addressof(bases), n, N, page, kv, s[0] * e, s[1] * e, s[2] * e,
-                       D * e), bases
+    return _CachePools(ctypes.addressof(bases), n, N, page, kv, stride[0] * e, stride[1] * e,
+                       stride[2] * e, D * e), bases
 
 
 def cache_keep(pools, table: torch.Tensor, lengths: torch.Tensor, path: torch.Tensor,
@@ -1232,17 +1240,16 @@ def cache_keep(pools, table: torch.Tensor, lengths: torch.Tensor, path: torch.Te
     lengths[b] + path[b, i] to lengths[b] + i for i < count[b] (path and count as
     tree_accept gives them).  Returns the new lengths, int32 [B]."""
     pools = list(pools)
-    index = table.get_device()
+    index, shape, at = table.get_device(), path.shape, table.shape
     if index < 0:
         raise ValueError("table must be a GPU tensor")
-    if path.dim() != 2 or table.dim() != 2:
+    if len(shape) != 2 or len(at) != 2 or at[0] != shape[0]:
         raise ValueError("path must be [B, nodes] and table [B, pages of a sequence]")
-    B, T = path.shape
-    P = table.shape[1]
-    _ints(path, "path", index, (B, T))
-    _ints(table, "table", index, (B, P))
-    _ints(lengths, "lengths", index, (B,))
-    _ints(count, "count", index, (B,))
+    (B, T), P, one = shape, at[1], (shape[0],)
+    _ints(path, "path", index, shape)
+    _ints(table, "table", index, at)
+    _ints(lengths, "lengths", index, one)
+    _ints(count, "count", index, one)
     p, _bases = _pools(pools, index)
     new = torch.empty_like(lengths)
     _enqueue("spec_cache_keep", table.device, load().spec_cache_keep, ctypes.byref(p),
@@ -1255,13 +1262,13 @@ def cache_keep(pools, table: torch.Tensor, lengths: torch.Tensor, path: torch.Te
 def _table_on(table, refs, dims, what):
     """The GPU's index of a table [..., P] with dims dimensions (0: any from two on)
     beside refs [pages]."""
-    index = table.get_device()
+    index, shape, pages = table.get_device(), table.shape, refs.shape
     if index < 0:
         raise ValueError("table must be a GPU tensor")
-    if table.dim() < 2 or (dims and table.dim() != dims) or refs.dim() != 1:
+    if len(shape) < 2 or (dims and len(shape) != dims) or len(pages) != 1:
         raise ValueError("table must be %s and refs [pages]" % what)
-    _ints(table, "table", index, table.shape)
-    _ints(refs, "refs", index, refs.shape)
+    _ints(table, "table", index, shape)
+    _ints(refs, "refs", index, pages)
     return index
 
 
