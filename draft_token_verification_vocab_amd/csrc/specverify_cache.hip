@@ -123,6 +123,13 @@ spec_status check_tree(const spec_cache *c, int32_t nodes, int32_t heads, bool t
     return SPEC_OK;
 }
 
+template <typename T>
+int tree_waves_of(int dp, int rt) {
+    return dp == 64    ? tree_waves<T, 64>(rt)
+           : dp == 128 ? tree_waves<T, 128>(rt)
+                       : tree_waves<T, 256>(rt);
+}
+
 TreePlan plan_tree(const spec_cache *c, int32_t nodes, int32_t heads) {
     TreePlan p;
     p.dp = c->dim <= 64 ? 64 : (c->dim <= 128 ? 128 : 256);
@@ -141,14 +148,11 @@ TreePlan plan_tree(const spec_cache *c, int32_t nodes, int32_t heads) {
         p.rows = 64 * p.rt;
         p.waves = p.dp == 256 ? 1 : 2;
     } else {
-        const int most = half ? (p.dp == 256 ? 1 : 3) : 2;
+        const int most = p.dp == 256 ? 1 : (half ? 3 : 2);
         const int64_t splits = (tiles16 + most - 1) / most;
         p.rt = static_cast<int>((tiles16 + splits - 1) / splits);
         p.rows = 16 * p.rt;
-        p.waves = !half         ? 1
-                  : p.dp == 64  ? tree_waves<__bf16, 64>(p.rt)
-                  : p.dp == 128 ? tree_waves<__bf16, 128>(p.rt)
-                                : tree_waves<__bf16, 256>(p.rt);
+        p.waves = half ? tree_waves_of<__bf16>(p.dp, p.rt) : tree_waves_of<float>(p.dp, p.rt);
     }
     p.mtiles = static_cast<int>((rows + p.rows - 1) / p.rows);
     const int64_t units = static_cast<int64_t>(p.mtiles) * c->kv_heads;
@@ -186,7 +190,7 @@ void launch_tree_rt(const TreeArgs &a, const TreePlan &p, hipStream_t st) {
             }
         }
     }
-    if constexpr (DP <= 128 || sizeof(T) == 4) {
+    if constexpr (DP <= 128) {
         if (p.rt == 2) {
             tree_attention_kernel<T, DP, 2, FULL><<<grid, block, 0, st>>>(a);
             return;

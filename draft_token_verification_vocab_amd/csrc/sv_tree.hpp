@@ -444,9 +444,10 @@ __device__ __forceinline__ void tree_add_odd(const TreeArgs &a, const uint64_t (
 // need (an accumulator takes DP/4 of them, a block's keys and values DP/2).
 template <typename T, int DP>
 constexpr int tree_waves(int R) {
-    if (DP == 256 || sizeof(T) == 4) return 1;
-    if (DP == 64) return R <= 2 ? 4 : (R <= 4 ? 2 : 1);
-    return R == 1 ? 3 : (R <= 3 ? 2 : 1);
+    if (sizeof(T) == 4) return DP == 64 ? 2 : 1;
+    if (DP == 256) return 1;
+    if (DP == 64) return R <= 2 ? 4 : 2;
+    return R == 1 ? 3 : 2;
 }
 
 // FULL: a slot has DP elements and the next one follows it, so that the loads of
