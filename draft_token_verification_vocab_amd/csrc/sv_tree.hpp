@@ -824,10 +824,10 @@ __global__ __launch_bounds__(kTreeBlock, (tree_waves<T, DP>(R))) void tree_atten
 // cross the vector registers' load path once for 64 R rows.
 //
 // A tile of keys is in shared memory while the next one is on its way there,
-// past the registers.  Rows lie 16-byte chunk by chunk, chunk c of key k at c xor
-// tree_swizzle(k): the 16 keys that one operand of K Q^T takes, and the 16 that
-// one transposing read of V takes, then lie on different banks.  For V^T P^T
-// that read gives a lane four keys' elements of its dimension.
+// past the registers.  Rows lie 16-byte chunk by chunk, chunk c of key k at c xor a
+// function of k, so that what is read at once lies on different banks: of the
+// keys, a chunk of 16 rows; of the values, two chunks of eight rows, by a
+// transposing read that gives a lane four keys' elements of its dimension.
 //
 // The weights' reference moves only when a score passes it by 2^6: they stay
 // below 2^6 and sums of 2^30 of them far from a float's end.  As the largest
@@ -866,8 +866,13 @@ constexpr int tree_wide_keys() {
 }
 
 template <int DP>
-__device__ __forceinline__ int tree_swizzle(int key) {
+__device__ __forceinline__ int tree_swizzle_k(int key) {
     return DP >= 128 ? (key & 3) | (key >> 1 & 12) : (key >> 1 & 1) | (key >> 2 & 6);
+}
+template <int DP>
+__device__ __forceinline__ int tree_swizzle_v(int key) {
+    return DP >= 128 ? (key << 1 & 6) | (key & 8) | (key >> 4 & 1)
+                     : (key & 2) | (key >> 1 & 4) | (key >> 4 & 1);
 }
 
 typedef short v4i16 __attribute__((ext_vector_type(4)));
@@ -924,12 +929,15 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
     constexpr int kKeyStep = kTreeBlock / kRow, kWaveKeys = kWave / kRow;
     static_assert(kWaveKeys <= 8, "a wave's load stays in a page");
     // key0 lies below a load's step, so the swizzles of the two xor
-    int chunk[kLoads];
-    uint32_t lane_at[kLoads];
+    int chunk_k[kLoads], chunk_v[kLoads];
+    uint32_t k_at[kLoads], v_at[kLoads];
 #pragma unroll
     for (int k = 0; k < kLoads; ++k) {
-        chunk[k] = (tid % kRow) ^ tree_swizzle<DP>(key0) ^ tree_swizzle<DP>(k * kKeyStep);
-        lane_at[k] = static_cast<uint32_t>((lane / kRow * slot_stride + 8 * chunk[k]) * sizeof(T));
+        const int64_t row = lane / kRow * slot_stride;
+        chunk_k[k] = (tid % kRow) ^ tree_swizzle_k<DP>(key0) ^ tree_swizzle_k<DP>(k * kKeyStep);
+        chunk_v[k] = (tid % kRow) ^ tree_swizzle_v<DP>(key0) ^ tree_swizzle_v<DP>(k * kKeyStep);
+        k_at[k] = static_cast<uint32_t>((row + 8 * chunk_k[k]) * sizeof(T));
+        v_at[k] = static_cast<uint32_t>((row + 8 * chunk_v[k]) * sizeof(T));
     }
     // and its operands' addresses: chunk 4s + g of key i16's in the instruction's
     // order, and four dimensions of key 8g + i16/4
@@ -937,8 +945,8 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(
         reinterpret_cast<size_t>((__attribute__((address_space(3))) v4u32 *)&sh.tile[0][0][0]) +
         wave * kWave * 16));
-    const int fk = tree_swizzle<DP>(8 * (i16 >> 2) + (i16 & 3));
-    const int fv = tree_swizzle<DP>(8 * g + (i16 >> 2));
+    const int fk = tree_swizzle_k<DP>(8 * (i16 >> 2) + (i16 & 3));
+    const int fv = tree_swizzle_v<DP>(8 * g + (i16 >> 2));
 
     while (tile < end) {
         const int nt = tree_tiles(span.keys);
@@ -1009,10 +1017,10 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
                 if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.pages)) page = 0;
                 const int64_t at =
                     page * a.page_stride + ((p0 + key) & slot_mask) * slot_stride;
-                if (FULL || 8 * chunk[k] < a.D) {
-                    tree_load_lds<ONCE>(keys + at, lane_at[k], to_k + k * kTreeBlock * 16);
-                    tree_load_lds<ONCE>(values + at, lane_at[k], to_v + k * kTreeBlock * 16);
-                }
+                if (FULL || 8 * chunk_k[k] < a.D)
+                    tree_load_lds<ONCE>(keys + at, k_at[k], to_k + k * kTreeBlock * 16);
+                if (FULL || 8 * chunk_v[k] < a.D)
+                    tree_load_lds<ONCE>(values + at, v_at[k], to_v + k * kTreeBlock * 16);
             }
         };
         // Values of positions that are not there become 0, and of nodes lose their
