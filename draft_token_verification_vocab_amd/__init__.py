@@ -24,6 +24,7 @@ __all__ = [
     "beam_select", "beam_reorder",
     "tree_attention", "tree_accept", "cache_append", "cache_keep",
     "pages_fork", "pages_release", "pages_reserve", "pages_copy",
+    "tree_workspace_bytes", "reserve_workspace_bytes",
     "workspace_bytes", "draft_stats_bytes", "MODE_LOSSLESS", "MODE_FLY",
 ]
 
@@ -1103,6 +1104,16 @@ def _tree_workspace_bytes(B: int, P: int, page: int, kv: int, dim: int, dtype: i
     return int(load().spec_tree_attention_workspace_bytes(ctypes.byref(c), T, H))
 
 
+def tree_workspace_bytes(q: torch.Tensor, keys: torch.Tensor, table: torch.Tensor) -> int:
+    """The bytes that tree_attention's workspace has to have for arguments of these
+    shapes, types and strides (0: none), whatever the lengths.  Calls that may run at
+    the same time need workspaces of their own; those in stream order may share one."""
+    N, kv, page, D = keys.shape
+    return _tree_workspace_bytes(table.shape[0], table.shape[1], page, kv, D,
+                                 _CACHE_DTYPES[keys.dtype], q.shape[1], q.shape[2],
+                                 _strides(keys)[2])
+
+
 def tree_attention(q: torch.Tensor, keys: torch.Tensor, values: torch.Tensor, table: torch.Tensor,
                    lengths: torch.Tensor, parents: Optional[torch.Tensor] = None, *,
                    num_nodes: Optional[torch.Tensor] = None, scale: Optional[float] = None,
@@ -1116,6 +1127,7 @@ def tree_attention(q: torch.Tensor, keys: torch.Tensor, values: torch.Tensor, ta
     node follows (-1: none), for a tree of at most 128 nodes; None: a chain.
     Node i sees the cached positions, itself and its ancestors.  num_nodes int32
     [B]: nodes in use; the others' outputs are 0.  scale: None is dim ** -0.5.
+    workspace: a uint8 tensor of tree_workspace_bytes (None: a new one).
     Returns out [B, T, H, dim], with lse also the log-sum-exp of the scores
     (float32 [B, T, H], -inf where a node sees nothing).  q and the pools may be
     strided views with contiguous last dimensions.  Autograd does not record the
@@ -1250,7 +1262,9 @@ def cache_keep(pools, table: torch.Tensor, lengths: torch.Tensor, path: torch.Te
     _ints(table, "table", index, at)
     _ints(lengths, "lengths", index, one)
     _ints(count, "count", index, one)
-    p, _bases = _pools(pools, index)
+    p, bases = _pools(pools, index)
+    if len(set(bases)) < len(pools):
+        raise ValueError("pools must be different tensors")
     new = torch.empty_like(lengths)
     _enqueue("spec_cache_keep", table.device, load().spec_cache_keep, ctypes.byref(p),
              table.data_ptr(), P, lengths.data_ptr(), path.data_ptr(), count.data_ptr(), B, T,
@@ -1316,6 +1330,12 @@ def _reserve_workspace_bytes(rows: int, pages: int) -> int:
     return int(load().spec_pages_reserve_workspace_bytes(rows, pages))
 
 
+def reserve_workspace_bytes(table: torch.Tensor, refs: torch.Tensor) -> int:
+    """The bytes that pages_reserve's workspace has to have for arguments of these
+    shapes."""
+    return _reserve_workspace_bytes(math.prod(table.shape[:-1]), refs.shape[0])
+
+
 def pages_reserve(table: torch.Tensor, lengths: torch.Tensor, refs: torch.Tensor, page_size: int,
                   new: torch.Tensor, *, workspace: Optional[torch.Tensor] = None) -> dict:
     """Give each row of table (int32 [..., P]) pages of its own for the new
@@ -1323,7 +1343,8 @@ def pages_reserve(table: torch.Tensor, lengths: torch.Tensor, refs: torch.Tensor
     entries without one and in place of shared ones.  Returns copies (int32
     [rows, 3]: page, its replacement, positions that pages_copy is to move; -1, -1
     and 0 for none) and missing (int32 [1]: 0; the pages that lack, or -1 where
-    positions pass a table row, and then nothing changed)."""
+    positions pass a table row, and then nothing changed).  workspace: a uint8
+    tensor of reserve_workspace_bytes (None: a new one)."""
     index = _table_on(table, refs, 0, "[..., P]")
     lead, P = table.shape[:-1], table.shape[-1]
     rows, pages = math.prod(lead), refs.shape[0]

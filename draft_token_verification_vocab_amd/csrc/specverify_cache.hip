@@ -402,6 +402,7 @@ spec_status spec_cache_append(const spec_cache *cache, const void *k, const void
         return SPEC_ERR_ARG;
     if (cache->batch == 0 || nodes == 0) return SPEC_OK;
     if (!pools_ok(cache) || !k || !v || !aligned16(k) || !aligned16(v)) return SPEC_ERR_ARG;
+    if (cache->keys == cache->values) return SPEC_ERR_ARG;  // two writers to an element
     const int64_t span = ((cache->batch - 1) * batch_stride + (nodes - 1) * node_stride +
                           (cache->kv_heads - 1) * head_stride + cache->dim) *
                          e;

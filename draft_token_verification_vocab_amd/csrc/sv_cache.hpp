@@ -273,13 +273,14 @@ __global__ __launch_bounds__(kCacheBlock) void pages_release_kernel(ReleaseArgs 
 //
 // Where the rows fit the workgroup, an entry to a thread (a step of decoding),
 // entries stay in registers; otherwise shared ones are marked in the table
-// (-2 - page) until they are settled.
+// (kSharedMark + page) until they are settled.
 // ---------------------------------------------------------------------------
 constexpr int kReserveBlock = 1024;
 constexpr int kPageChunk = 1024;                   // pages to a count
 constexpr int kChunkWords = kPageChunk / kWave;
 constexpr int kMaxReservePages = 1 << 22;
 constexpr int kKeeper = 1 << 30;
+constexpr int kSharedMark = -2147483647 - 1;
 constexpr int kReserveAlone = 32;  // chunks that the workgroup looks through by itself
 
 struct ReserveArgs {
@@ -415,6 +416,7 @@ __global__ __launch_bounds__(kReserveBlock) void pages_reserve_kernel(ReserveArg
         c[2] = n;
     };
     auto is_page = [&](int e) { return static_cast<uint32_t>(e) < static_cast<uint32_t>(a.pages); };
+    auto is_mark = [&](int e) { return e < kSharedMark + a.pages; };
 
     if (a.rows <= batch && sh_widest <= group) {
         const int r = tid / group;
@@ -475,17 +477,17 @@ __global__ __launch_bounds__(kReserveBlock) void pages_reserve_kernel(ReserveArg
                 const int e = row[i];
                 if (phase == 0) {
                     if (is_page(e)) {
-                        if (a.refs[e] > 1) row[i] = -2 - e;
-                    } else if (e != -1) {
-                        row[i] = -1;  // lists nothing
+                        if (a.refs[e] > 1) row[i] = kSharedMark + e;
+                    } else if (is_mark(e)) {
+                        row[i] = -1;  // lists nothing, and must not be taken for a mark
                     }
-                } else if (e < -1) {
-                    int *ref = &a.refs[-2 - e];
+                } else if (is_mark(e)) {
+                    int *ref = &a.refs[e - kSharedMark];
                     if (phase == 1) atomicSub(ref, 1);
                     if (phase == 2 && atomicAdd(ref, 0) <= 0) atomicMin(ref, r - kKeeper);
                     if (phase == 3) need += atomicAdd(ref, 0) + kKeeper != r;
                 } else if (phase == 3) {
-                    need += e == -1;
+                    need += !is_page(e);
                 }
             }
         }
@@ -507,13 +509,13 @@ __global__ __launch_bounds__(kReserveBlock) void pages_reserve_kernel(ReserveArg
                 int32_t *row = a.table + static_cast<int64_t>(r) * a.P;
                 for (int i = lo + in; i < hi && !over; i += group) {
                     const int e = row[i];
-                    if (e >= -1) continue;
-                    int *ref = &a.refs[-2 - e];
+                    if (!is_mark(e)) continue;
+                    int *ref = &a.refs[e - kSharedMark];
                     if (phase == 0) {
                         if (atomicAdd(ref, 0) + kKeeper == r) atomicExch(ref, 0);
                     } else {
                         atomicAdd(ref, 1);
-                        row[i] = -2 - e;
+                        row[i] = e - kSharedMark;
                     }
                 }
             }
@@ -530,9 +532,8 @@ __global__ __launch_bounds__(kReserveBlock) void pages_reserve_kernel(ReserveArg
         int32_t *row = a.table + static_cast<int64_t>(r) * a.P;
         auto fresh = [&](int i, int &e) {
             e = i < hi ? row[i] : 0;
-            if (e == -1) return true;
-            if (e >= 0) return false;
-            return atomicAdd(&a.refs[-2 - e], 0) + kKeeper != r;
+            if (is_mark(e)) return atomicAdd(&a.refs[e - kSharedMark], 0) + kKeeper != r;
+            return !is_page(e);
         };
         int mine = 0, e;
         for (int i = lo + in; i < hi; i += group) mine += fresh(i, e);
@@ -550,8 +551,8 @@ __global__ __launch_bounds__(kReserveBlock) void pages_reserve_kernel(ReserveArg
                     free_page(a, sh_before, before + done + __popcll(who & ((1ull << lane) - 1)));
                 row[i] = page;
                 a.refs[page] = 1;
-                if (e < -1 && i == lo && (length & (page_size - 1))) {
-                    copy_from = -2 - e;
+                if (is_mark(e) && i == lo && (length & (page_size - 1))) {
+                    copy_from = e - kSharedMark;
                     copy_to = page;
                     copy_n = length & (page_size - 1);
                 }
@@ -571,9 +572,9 @@ __global__ __launch_bounds__(kReserveBlock) void pages_reserve_kernel(ReserveArg
         int32_t *row = a.table + static_cast<int64_t>(r) * a.P;
         for (int i = lo + in; i < hi; i += group) {
             const int e = row[i];
-            if (e < -1) {
-                row[i] = -2 - e;
-                atomicExch(&a.refs[-2 - e], 1);
+            if (is_mark(e)) {
+                row[i] = e - kSharedMark;
+                atomicExch(&a.refs[e - kSharedMark], 1);
             }
         }
     }

@@ -656,8 +656,8 @@ spec_status spec_tree_attention(const spec_cache *cache, const void *q, int64_t 
  * spec_cache_append -- writes the nodes' keys and values to their positions.
  * k, v: device, elements of cache->dtype, node j's key head h of sequence b at
  * b*batch_stride + j*node_stride + h*head_stride of each (elements; multiples
- * of 16 bytes, >= 0; 16-byte aligned).  Positions past the table row are
- * dropped.  Rows of a table that share a page must not both write to it
+ * of 16 bytes, >= 0; 16-byte aligned; outside the pools).  The pools of keys
+ * and values are different ones.  Positions past the table row are dropped.  Rows of a table that share a page must not both write to it
  * (spec_pages_reserve sees to that).
  */
 spec_status spec_cache_append(const spec_cache *cache, const void *k, const void *v,
@@ -701,13 +701,14 @@ typedef struct spec_cache_pools {
 
 /*
  * spec_cache_keep -- after verification: moves the accepted nodes' positions
- * together, in every pool: position lengths[b] + path[b][i] goes to
- * lengths[b] + i for i < count[b].  path: device int32 [batch][nodes],
+ * together, in every pool (all different): position lengths[b] + path[b][i] goes
+ * to lengths[b] + i for i < count[b].  path: device int32 [batch][nodes],
  * ascending within [0, nodes) as spec_tree_accept gives it (the first entry
  * that is not ends the list); count: device int32 [batch].  new_lengths
  * (device int32 [batch], apart from the inputs): lengths[b] plus the entries
- * kept, at most what the table row can hold.  A move from or to a position without a page is left out.  Rows of a
- * table that share a page must not both move into it.  nodes <= 1024.
+ * kept, at most what the table row can hold.  A move from or to a position
+ * without a page is left out.  Rows of a table that share a page must not both
+ * move into it.  nodes <= 1024.
  */
 spec_status spec_cache_keep(const spec_cache_pools *pools, const int32_t *table,
                             int32_t table_width, const int32_t *lengths, const int32_t *path,
@@ -755,7 +756,8 @@ spec_status spec_pages_release(int32_t *table, const int32_t *lengths, int32_t r
  * spec_pages_copy); (-1, -1, 0) otherwise.  missing (device int32 [1]): 0, or,
  * where the free pages do not suffice, how many lack, or -1 where a row's
  * positions pass its table row; then nothing is taken or changed and copies
- * are (-1, -1, 0).  workspace: device, spec_pages_reserve_workspace_bytes,
+ * are (-1, -1, 0), but that an entry below -2^31 + num_pages may become -1.
+ * workspace: device, spec_pages_reserve_workspace_bytes,
  * 16-byte aligned; its contents on entry do not matter.  rows <= 65536, else
  * SPEC_ERR_UNSUPPORTED.
  */

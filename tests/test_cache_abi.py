@@ -90,6 +90,21 @@ def test_tree_workspace(L):
     assert L.spec_tree_attention_workspace_bytes(None, 3, 8) == 0
 
 
+def test_public_workspace_sizes():
+    keys = torch.empty(4, 2, 16, 64, dtype=torch.bfloat16)
+    table = torch.empty(3, 65, dtype=torch.int32)
+    q = torch.empty(3, 5, 8, 64, dtype=torch.bfloat16)
+    n = sv.tree_workspace_bytes(q, keys, table)
+    assert n > 0
+    # strides do not matter to it but for rows that are far apart
+    assert sv.tree_workspace_bytes(q, keys.transpose(1, 2).contiguous().transpose(1, 2),
+                                   table) == n
+    assert sv.tree_workspace_bytes(q, keys, table[:, :64]) == 0
+    refs = torch.empty(5000, dtype=torch.int32)
+    assert sv.reserve_workspace_bytes(table, refs) == \
+        sv.load().spec_pages_reserve_workspace_bytes(3, 5000) > 0
+
+
 @host_only
 def test_append_validates_on_host(L):
     def call(k=P(16), v=P(16), sb=1024, sn=512, sh=64, T=3, null=False, **kw):
@@ -98,7 +113,7 @@ def test_append_validates_on_host(L):
                                    None)
     for kw in (dict(null=True), dict(k=None), dict(v=None), dict(k=P(8)), dict(v=P(24)),
                dict(T=-1), dict(sb=4), dict(sn=-8), dict(sh=1), dict(k=P(FAR + 64)),
-               dict(v=P(2 * FAR))):
+               dict(v=P(2 * FAR)), dict(values=FAR)):
         assert call(**kw) == -1, kw
     assert call(T=1 << 30, batch=1 << 20) == -2
     assert call(sn=1 << 41) == -2

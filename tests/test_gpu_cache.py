@@ -267,6 +267,33 @@ def test_reserve_all_or_nothing():
     assert got[3] == 0
 
 
+@pytest.mark.parametrize("rows,P,news", [(3, 4, [9, 20, 8]),        # an entry to a thread
+                                         (3, 2000, [9, 15000, 8]),  # a row of many entries
+                                         (1500, 4, [9, 20, 8] + 1497 * [0])])
+@pytest.mark.parametrize("enough", [True, False])
+def test_reserve_of_entries_that_are_no_pages(rows, P, news, enough):
+    """Whatever lists nothing takes a page, or stays as it is where pages lack."""
+    page, N = 8, 2100
+    table = np.full((rows, P), -7)
+    table[0, :3] = [5, 3, -2]
+    table[1, :4] = [5, 3, N, 2 ** 31 - 1]
+    table[2, :3] = [-2 ** 31 + N, 4, -5]
+    refs = np.zeros(N, dtype=int) if enough else np.ones(N, dtype=int)
+    refs[[5, 3, 4]] = [2, 2, 1]
+    got = check_reserve(table, [12, 12, 9] + (rows - 3) * [0], refs, page, news)
+    assert (got[3] == 0) == enough
+    if not enough:
+        assert (got[0] == table).all() and (got[1] == refs).all()
+
+
+def test_keep_refuses_a_pool_twice():
+    pool = torch.zeros(4, 1, 8, 8, device="cuda")
+    one = torch.zeros(1, 2, dtype=torch.int32, device="cuda")
+    n = torch.zeros(1, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="different"):
+        sv.cache_keep([pool, pool.clone(), pool], one, n, one, n)
+
+
 def test_reserve_takes_its_workspace_as_it_is():
     rng = np.random.default_rng(5)
     table, lengths, refs = random_tables(rng, 30, 8, 5000, 16, 0.5)
