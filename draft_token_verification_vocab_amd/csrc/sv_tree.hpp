@@ -73,12 +73,6 @@ struct TreeArgs {
     float scale2;            // scale * log2(e)
 };
 
-// Asks for every 64 bytes of the arguments at once: they come from far, and each
-// part that is first read later would be waited for again.
-__device__ __forceinline__ void tree_touch(const TreeArgs &a) {
-    asm volatile("" ::"s"(a.keys), "s"(a.parents), "s"(a.q_node), "s"(a.scale2));
-}
-
 // Types of keys and values.  Frag: a matrix operand's 8 elements along the
 // summed dimension; load8: 8 consecutive elements.
 template <typename T>
@@ -465,7 +459,6 @@ __global__ __launch_bounds__(kTreeBlock, (tree_waves<T, DP>(R))) void tree_atten
     using Shared = TreeShared<T, DP, R>;
     __shared__ Shared sh;
 
-    tree_touch(a);
     const int units = a.slices * a.KV;
     const int mt = blockIdx.x / units;
     const int slice = (blockIdx.x % units) / a.KV;
@@ -900,7 +893,6 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
     static_assert(kTreeTile % kKeys == 0, "tiles are dealt out in whole ones");
     __shared__ TreeWideShared<DP> sh;
 
-    tree_touch(a);
     const int units = a.slices * a.KV;
     const int mt = blockIdx.x / units;
     const int slice = (blockIdx.x % units) / a.KV;
@@ -1268,7 +1260,6 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
 template <typename T, int L, int NR>
 __global__ __launch_bounds__(kTreeBlock) void tree_join_kernel(TreeArgs a, int rows16,
                                                                int blocks) {
-    tree_touch(a);
     constexpr int kAt = kWave / L, kAhead = NR == 1 ? 8 : 2;  // parts at a time, and ahead
     const int b = blockIdx.x / blocks;
     const int lane = threadIdx.x & (kWave - 1);

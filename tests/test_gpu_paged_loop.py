@@ -193,3 +193,104 @@ def test_serving_loop(dt):
     count[:] = 0
     count[::3] = 1
     assert torch.equal(refs.cpu(), count)
+
+
+class Step:
+    """A step of given sequences over two layers: branch, reserve, copy, append, attend,
+    accept, keep and release, all of it on the stream that run() finds."""
+
+    def __init__(self, seed, dt=torch.bfloat16):
+        g = torch.Generator().manual_seed(seed)
+        self.B, self.W, self.T, P, N = 3, 2, 7, 200, 700
+        self.pools = [torch.randn(N, KV, PAGE, DIM, generator=g).to(dt).cuda() for _ in range(4)]
+
+        def ints(x):
+            return torch.as_tensor(x, dtype=torch.int32).cuda()
+
+        B, W, T = self.B, self.W, self.T
+        self.lengths = ints(torch.randint(1, (P - 2) * PAGE, (B, 1), generator=g))
+        self.table = torch.full((B, 1, P), -1, dtype=torch.int32, device="cuda")
+        self.refs = torch.zeros(N, dtype=torch.int32, device="cuda")
+        zero = torch.zeros(B, 1, dtype=torch.int32, device="cuda")
+        sv.pages_reserve(self.table, zero, self.refs, PAGE, self.lengths)
+        self.branches = torch.zeros(B, W, dtype=torch.int32, device="cuda")
+        self.new = ints(torch.randint(1, T + 1, (B, W), generator=g))
+        self.parents = ints(torch.stack([torch.arange(T) // 2 - (torch.arange(T) == 0).long()
+                                         for _ in range(B * W)]))
+        self.tokens = ints(torch.randint(0, 2, (B * W, T), generator=g))
+        self.chosen = ints(torch.randint(0, 2, (B * W, T), generator=g))
+        self.q = torch.randn(B * W, T, HEADS, DIM, generator=g).to(dt).cuda()
+        self.k, self.v = (torch.randn(B * W, T, KV, DIM, generator=g).to(dt).cuda()
+                          for _ in range(2))
+        self.rows = torch.full((B, W, P), -1, dtype=torch.int32, device="cuda")
+        self.start = [t.clone() for t in self.state()]
+
+    def state(self):
+        return [*self.pools, self.refs, self.rows]
+
+    def reset(self):
+        for t, u in zip(self.state(), self.start):
+            t.copy_(u)
+
+    def run(self):
+        rows, nodes = self.rows, self.new.view(-1)
+        used = sv.pages_fork(self.table, self.lengths, self.branches, self.refs, PAGE, out=rows)
+        r = sv.pages_reserve(rows, used, self.refs, PAGE, self.new)
+        sv.pages_copy(self.pools, r["copies"])
+        flat, at, outs = rows.view(self.B * self.W, -1), used.view(-1), []
+        for i in range(0, 4, 2):
+            sv.cache_append(self.k, self.v, *self.pools[i:i + 2], flat, at, num_nodes=nodes)
+            outs += sv.tree_attention(self.q, *self.pools[i:i + 2], flat, at, self.parents,
+                                      num_nodes=nodes, lse=True)
+        path = sv.tree_accept(self.parents, self.tokens, self.chosen, num_nodes=nodes)
+        used = sv.cache_keep(self.pools, flat, at, path["path"], path["count"])
+        sv.pages_release(rows, self.refs, PAGE, used.view(self.B, self.W))
+        return [*outs, path["path"], path["tokens"], path["count"], used, r["copies"],
+                r["missing"]]
+
+
+def test_captured_steps_and_other_streams():
+    steps = [Step(s) for s in (1, 2)]
+    want = []
+    for s in steps:
+        got = s.run()
+        assert got[-1].item() == 0 and (got[-2][:, 2] > 0).any()
+        want.append([t.clone() for t in got + s.state()])
+        s.reset()
+    torch.cuda.synchronize()
+    graphs, got = [], []
+    for s in steps:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got.append(s.run())
+        graphs.append(g)
+    for turn in range(3):
+        for s in steps:
+            s.reset()
+        if turn == 2:       # both at once, on streams of their own
+            streams = [torch.cuda.Stream() for _ in steps]
+            for t, g in zip(streams, graphs):
+                t.wait_stream(torch.cuda.current_stream())
+                with torch.cuda.stream(t):
+                    g.replay()
+        else:
+            for g in graphs:
+                g.replay()
+        torch.cuda.synchronize()
+        for s, g, w in zip(steps, got, want):
+            for a, b in zip(g + s.state(), w):
+                assert torch.equal(a, b)
+        (steps[0].k + 1).sum().item()      # eager work between the replays
+    # eager calls of two streams side by side
+    torch.cuda.synchronize()
+    for s in steps:
+        s.reset()
+    streams, got = [torch.cuda.Stream() for _ in steps], []
+    for s, t in zip(steps, streams):
+        t.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(t):
+            got.append(s.run())
+    torch.cuda.synchronize()
+    for s, g, w in zip(steps, got, want):
+        for a, b in zip(g + s.state(), w):
+            assert torch.equal(a, b)
