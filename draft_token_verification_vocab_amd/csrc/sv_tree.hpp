@@ -870,6 +870,11 @@ __device__ __forceinline__ int tree_swizzle_v(int key) {
 
 typedef short v4i16 __attribute__((ext_vector_type(4)));
 
+template <int N>
+struct Tiles {
+    static constexpr int value = N;
+};
+
 template <int DP>
 struct TreeWideShared {
     v4u32 tile[2][2][tree_wide_keys<DP>() * DP / 8];  // [stage][keys, values]
@@ -1037,10 +1042,13 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
             if (odd) sh.odd = 1;
         };
         constexpr int kBlocks = kKeys / kTreeKeys;
-        // a wave whose rows are not in use only loads
+        // a wave whose rows are not in use only loads, and one that has only its
+        // first tile's works on that alone
         const bool mine = mt * kTile + 16 * wave < span.live * a.G;
+        const bool all = mt * kTile + 16 * (4 * (R - 1) + wave) < span.live * a.G;
         v4f32 z[kBlocks][R][2];
-        auto score = [&](int stage) {
+        auto score = [&](auto tiles, int stage) {
+            constexpr int N = decltype(tiles)::value;
             const v4u32 *kt = sh.tile[stage][0];
             // operands are read kAhead products before they are needed; the
             // barriers keep reads and products in this order
@@ -1058,7 +1066,7 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
                 const int c = i % 2, s = i / 2 % kSteps, kb = i / 2 / kSteps;
                 __builtin_amdgcn_sched_barrier(kTreeArith);
 #pragma unroll
-                for (int r = 0; r < R; ++r)
+                for (int r = 0; r < N; ++r)
                     z[kb][r][c] =
                         E::mma(E::frag(kf[i % kAhead]), qf[r][s],
                                s == 0 ? v4f32{0.0f, 0.0f, 0.0f, 0.0f} : z[kb][r][c]);
@@ -1066,12 +1074,13 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
                 if (i + kAhead < kAll) operand(i + kAhead);
             }
         };
-        auto add_values = [&](int stage) {
+        auto add_values = [&](auto tiles, int stage) {
+            constexpr int N = decltype(tiles)::value;
             const char *vt = reinterpret_cast<const char *>(sh.tile[stage][1]);
-            float top[R];
+            float top[N];
             bool behind = false;
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
+            for (int r = 0; r < N; ++r) {
                 float t = z[0][r][0][0];
 #pragma unroll
                 for (int j = 1; j < 8 * kBlocks; ++j)
@@ -1081,7 +1090,7 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
             }
             if (__builtin_expect(__any(behind), 0)) {
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
+                for (int r = 0; r < N; ++r) {
                     const float up = fmaxf(m[r], across_groups_max(top[r]));
                     const float f = up == -__builtin_inff() ? 1.0f : hw_exp2(m[r] - up);
                     l[r] *= f;
@@ -1109,12 +1118,12 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
             };
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) operand(i);
-            float shift[R], w[kBlocks][R][8];
+            float shift[N], w[kBlocks][N][8];
 #pragma unroll
-            for (int r = 0; r < R; ++r) shift[r] = m[r] == -__builtin_inff() ? 0.0f : m[r];
+            for (int r = 0; r < N; ++r) shift[r] = m[r] == -__builtin_inff() ? 0.0f : m[r];
             auto weigh = [&](int kb, int j) {
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
+                for (int r = 0; r < N; ++r) {
                     w[kb][r][j] =
                         hw_exp2(__builtin_fmaf(z[kb][r][j / 4][j % 4], a.scale2, -shift[r]));
                     l[r] += w[kb][r][j];
@@ -1122,19 +1131,19 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
             };
 #pragma unroll
             for (int j = 0; j < 8; ++j) weigh(0, j);
-            Frag pf[R];
+            Frag pf[N];
 #pragma unroll
             for (int i = 0; i < kAll; ++i) {
                 const int kb = i / kCols, t = i % kCols;
                 if (t == 0) {
 #pragma unroll
-                    for (int r = 0; r < R; ++r) {
+                    for (int r = 0; r < N; ++r) {
                         pf[r] = E::from(w[kb][r]);
                         n[r] = E::mma(E::ones(), pf[r], n[r]);
                     }
                 }
 #pragma unroll
-                for (int r = 0; r < R; ++r) o[r][t] = E::mma(vf[i % kAhead], pf[r], o[r][t]);
+                for (int r = 0; r < N; ++r) o[r][t] = E::mma(vf[i % kAhead], pf[r], o[r][t]);
                 __builtin_amdgcn_sched_barrier(kTreeArith);
                 if (i + kAhead < kAll) operand(i + kAhead);
                 // the next block's weights between this one's products
@@ -1161,27 +1170,35 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
         // while every row sees every key and a tile follows, which is on its way
         // meanwhile; then the rest: the last tile, the nodes, and everything behind
         // a page that is missing
-        while (p0 + kKeys < keys_end && p0 + kKeys <= span.cached && ~held == 0) {
-            load(stage ^ 1, p0 + kKeys, entry_next);
-            held = held_of(p0 + kKeys, entry_next);
-            entry_next = entry_of(p0 + 2 * kKeys);
-            if (mine) {
-                score(stage);
-                // the compute unit's other workgroup scores meanwhile: wide trees
-                // 350 -> 327 us, two caches of 131072 184.7 -> 176.7
-                __builtin_amdgcn_s_setprio(1);
-                add_values(stage);
-                __builtin_amdgcn_s_setprio(0);
+        auto plain = [&](auto tiles) {
+            while (p0 + kKeys < keys_end && p0 + kKeys <= span.cached && ~held == 0) {
+                load(stage ^ 1, p0 + kKeys, entry_next);
+                held = held_of(p0 + kKeys, entry_next);
+                entry_next = entry_of(p0 + 2 * kKeys);
+                if (mine) {
+                    score(tiles, stage);
+                    // the compute unit's other workgroup scores meanwhile: wide trees
+                    // 350 -> 327 us, two caches of 131072 184.7 -> 176.7
+                    __builtin_amdgcn_s_setprio(1);
+                    add_values(tiles, stage);
+                    __builtin_amdgcn_s_setprio(0);
+                }
+                p0 += kKeys;
+                stage ^= 1;
+                tree_loads_done();
+                lds_barrier();
             }
-            p0 += kKeys;
-            stage ^= 1;
-            tree_loads_done();
-            lds_barrier();
-        }
+        };
+        // a wave with one row tile in use runs a loop of its own (wide trees 321 ->
+        // 314 us); a branch within one loop spills registers (351 to 403)
+        if (all)
+            plain(Tiles<R>{});
+        else
+            plain(Tiles<1>{});
         while (p0 < keys_end) {
             clean(stage, p0, held);
             lds_barrier();
-            if (mine) score(stage);
+            if (mine) score(Tiles<R>{}, stage);
 #pragma unroll
             for (int kb = 0; kb < kBlocks; ++kb) {
                 const uint32_t there = static_cast<uint32_t>(held >> (32 * kb + 8 * g)) & 0xFFu;
@@ -1195,7 +1212,7 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
                         if (!(see >> j & 1)) z[kb][r][j / 4][j % 4] = -__builtin_inff();
                 }
             }
-            if (mine) add_values(stage);
+            if (mine) add_values(Tiles<R>{}, stage);
             p0 += kKeys;
             if (p0 < keys_end) {
                 stage ^= 1;  // free since the last barrier
