@@ -93,7 +93,13 @@ bool pools_ok(const spec_cache *c) {
 // ---------------------------------------------------------------------------
 // Tree attention
 // ---------------------------------------------------------------------------
-constexpr int kTreeWhole = 8, kTreeWholeWide = 4;  // tiles of the longest sequence
+// Slots of 16-bit types: eight of them have offsets below 2^32 bytes.
+constexpr int64_t kMaxWideSlot = int64_t{1} << 28;
+// Tiles of the longest sequence that is not cut, and so needs no second launch: one
+// of float32 (one sequence of two tiles 19.0 us whole, 17.5 cut), four of 16-bit
+// types, where five nodes of 64 sequences take 24.2 us whole and 26.7 cut, of one
+// sequence 13.1 and 14.0 (11.4 in a graph); of eight tiles one takes 21.3 and 13.8.
+constexpr int kTreeWhole = 4;
 
 struct TreePlan {
     int dp;      // dimensions, rounded up to what a kernel takes
@@ -113,6 +119,7 @@ spec_status check_tree(const spec_cache *c, int32_t nodes, int32_t heads, bool t
     if (nodes < 1 || heads < 1 || heads % c->kv_heads != 0) return SPEC_ERR_ARG;
     if (nodes > (tree ? kMaxTreeNodes : kMaxChainNodes) || heads > kMaxHeads)
         return SPEC_ERR_UNSUPPORTED;
+    if (c->dtype != SPEC_DTYPE_F32 && c->slot_stride > kMaxWideSlot) return SPEC_ERR_UNSUPPORTED;
     const int64_t tiles =
         (static_cast<int64_t>(c->table_width) * c->page_size + kTreeTile - 1) / kTreeTile;
     if (c->batch > INT32_MAX / tiles) return SPEC_ERR_UNSUPPORTED;
@@ -123,42 +130,33 @@ spec_status check_tree(const spec_cache *c, int32_t nodes, int32_t heads, bool t
     return SPEC_OK;
 }
 
-template <typename T>
-int tree_waves_of(int dp, int rt) {
-    return dp == 64    ? tree_waves<T, 64>(rt)
-           : dp == 128 ? tree_waves<T, 128>(rt)
-                       : tree_waves<T, 256>(rt);
-}
-
 TreePlan plan_tree(const spec_cache *c, int32_t nodes, int32_t heads) {
     TreePlan p;
     p.dp = c->dim <= 64 ? 64 : (c->dim <= 128 ? 128 : 256);
     const int64_t rows = static_cast<int64_t>(nodes) * (heads / c->kv_heads);
     const int64_t tiles16 = (rows + 15) / 16;
-    const bool half = c->dtype != SPEC_DTYPE_F32;
     const int64_t longest =
         (static_cast<int64_t>(c->table_width) * c->page_size + kTreeTile - 1) / kTreeTile;
-    // 16-bit types take keys and values through shared memory, except for few rows
-    // of short sequences, where four waves that share out the keys are done sooner
-    // (and for slots further apart than the loads' 32-bit offsets reach)
-    p.wide = half && (longest > kTreeWhole || tiles16 > (p.dp == 256 ? 1 : 3)) &&
-             c->slot_stride <= (1 << 24);
+    // 16-bit types' keys and values go through shared memory, float32's straight into
+    // registers: of 16 bits those were never sooner by more than 2 us (one sequence of
+    // 512 positions, 10.8 us against 12.7) and up to 2.3 times slower (rows of 64)
+    p.wide = c->dtype != SPEC_DTYPE_F32;
     if (p.wide) {
         p.rt = tiles16 > 4 ? 2 : 1;
         p.rows = 64 * p.rt;
         p.waves = p.dp == 256 ? 1 : 2;
     } else {
-        const int most = p.dp == 256 ? 1 : (half ? 3 : 2);
+        const int most = p.dp == 256 ? 1 : 2;
         const int64_t splits = (tiles16 + most - 1) / most;
         p.rt = static_cast<int>((tiles16 + splits - 1) / splits);
         p.rows = 16 * p.rt;
-        p.waves = half ? tree_waves_of<__bf16>(p.dp, p.rt) : tree_waves_of<float>(p.dp, p.rt);
+        p.waves = tree_waves(p.dp);
     }
     p.mtiles = static_cast<int>((rows + p.rows - 1) / p.rows);
     const int64_t units = static_cast<int64_t>(p.mtiles) * c->kv_heads;
     const int64_t tiles = c->batch * longest;
     // short sequences are not cut: no second launch
-    p.whole = longest <= (p.wide ? kTreeWholeWide : kTreeWhole);
+    p.whole = longest <= (p.wide ? kTreeWhole : 1);
     int64_t slices = (p.waves * kUnits + units - 1) / units;
     if (slices > tiles) slices = tiles;
     p.slices = p.whole ? c->batch : static_cast<int>(slices < 1 ? 1 : slices);
@@ -174,29 +172,21 @@ template <typename T, int DP, bool FULL>
 void launch_tree_rt(const TreeArgs &a, const TreePlan &p, hipStream_t st) {
     const dim3 grid(static_cast<unsigned>(p.slices * a.KV * p.mtiles)), block(kTreeBlock);
     if constexpr (sizeof(T) == 2) {
-        if (p.wide) {
-            if (p.mtiles > 1)
-                tree_wide_kernel<T, DP, 2, FULL, false><<<grid, block, 0, st>>>(a);
-            else if (p.rt == 2)
-                tree_wide_kernel<T, DP, 2, FULL, true><<<grid, block, 0, st>>>(a);
-            else
-                tree_wide_kernel<T, DP, 1, FULL, true><<<grid, block, 0, st>>>(a);
-            return;
-        }
+        if (p.mtiles > 1)
+            tree_wide_kernel<T, DP, 2, FULL, false><<<grid, block, 0, st>>>(a);
+        else if (p.rt == 2)
+            tree_wide_kernel<T, DP, 2, FULL, true><<<grid, block, 0, st>>>(a);
+        else
+            tree_wide_kernel<T, DP, 1, FULL, true><<<grid, block, 0, st>>>(a);
+    } else {
         if constexpr (DP <= 128) {
-            if (p.rt == 3) {
-                tree_attention_kernel<T, DP, 3, FULL><<<grid, block, 0, st>>>(a);
+            if (p.rt == 2) {
+                tree_attention_kernel<DP, 2, FULL><<<grid, block, 0, st>>>(a);
                 return;
             }
         }
+        tree_attention_kernel<DP, 1, FULL><<<grid, block, 0, st>>>(a);
     }
-    if constexpr (DP <= 128) {
-        if (p.rt == 2) {
-            tree_attention_kernel<T, DP, 2, FULL><<<grid, block, 0, st>>>(a);
-            return;
-        }
-    }
-    tree_attention_kernel<T, DP, 1, FULL><<<grid, block, 0, st>>>(a);
 }
 
 template <typename T, int DP>
@@ -217,7 +207,9 @@ void launch_tree(const TreeArgs &a, const TreePlan &p, hipStream_t st) {
         launch_tree_dim<T, 256>(a, p, st);
 }
 
-// Four rows to a wave where there are rows for every wave that the chip holds.
+// Four rows to a wave where there are rows for every wave that the chip holds: wide
+// trees 317 us against 325, 64 chains of nine 211.7 against 212.9; with four, 64
+// single tokens' 2048 rows take 169 against 162.
 constexpr int64_t kJoinRows = 8192;
 
 template <typename T, int L>

@@ -7,29 +7,39 @@
 // over the cached positions p < L, which every row sees, and the row's own node
 // and its ancestors among the n - L nodes behind them.
 //
-// One pass over the keys with a running maximum and sum per row.  A wave takes
-// 32 keys at a time straight from memory into the matrix instructions'
-// registers, without shared memory:
-//   S^T = K Q^T   a lane's operand is 8 consecutive elements of a key's row, a
-//                 16-byte load.  The instruction's 16 rows are given keys in
-//                 the order that leaves lane group g (of four) with the scores
-//                 of keys 8g..8g+7, all of one query row.
+// One pass over the keys with a running maximum and sum per row:
+//   S^T = K Q^T   a lane's operand is 8 consecutive elements of a key's row.  The
+//                 instruction's 16 rows are given keys in the order that leaves
+//                 lane group g (of four) with the scores of keys 8g..8g+7, all of
+//                 one query row.
 //   O^T = V^T P^T those 8 weights are the lane's operand as they stand; the
-//                 other one is 8 keys' values of one dimension, which the lane
-//                 picks from its own 8 loads (a load: 8 consecutive dimensions
-//                 of one key), for 16-bit types two at a time by a byte
-//                 permutation.
+//                 other one is 8 keys' values of one dimension.
 // A query row is a column throughout, so its maximum, sum and rescaling stay in
-// its lanes.  Products are added in 32 bits.  The weights are rounded to the
-// values' type before the second product, as the matrix instructions of 16-bit
-// types take them (a relative 2^-9 or 2^-12 of each, with independent signs);
-// their sum is taken before that rounding, in 32 bits, so that lse is good to
-// 32 bits.
+// its lanes.  Products are added in 32 bits.  For 16-bit types the weights are
+// rounded to the type before the second product, as its matrix instructions take
+// them (a relative 2^-9 or 2^-12 of each, with independent signs).  lse comes from
+// their sum before that rounding, in 32 bits.
 //
-// The keys of all sequences are cut into tiles and the tiles dealt out evenly:
-// a workgroup takes a run of tiles, which may end inside a sequence and hold
-// several short ones, so ragged batches load every workgroup alike.  A
-// sequence whose tiles are in several workgroups is joined by a second launch.
+// Two kernels: tree_wide_kernel for 16-bit types, where rows are shared out to the
+// waves and keys come through shared memory, and tree_attention_kernel for
+// float32, where keys are shared out to the waves and come straight into
+// registers (a tile of float32 keys and values takes twice the shared memory, and
+// its products a 16th of the rate, so nothing waits for loads).
+//
+// The keys of all sequences are cut into tiles of 128 and the tiles dealt out
+// evenly to as many workgroups as the chip holds: a workgroup takes a run of
+// tiles, which may end inside a sequence and hold several short ones, so ragged
+// batches load every workgroup alike.  More, smaller runs were slower (1.5, 2 and 3
+// times as many).  A sequence whose tiles are in several workgroups is joined by a
+// second launch.  Where every sequence is short, a workgroup takes a whole one
+// and there is none.
+//
+// Measured (kernel + join): 64 single tokens over up to 4000 positions, 552 MB,
+// 88.7 + 4.8 us (6.2 TB/s); 64 chains of nine over up to 8000, 1.19 GB, 201 + 11
+// (5.9 TB/s); two caches of 131072, 1.03 GB, 167 + 8.7 (6.2 TB/s): memory.  16
+// trees of 64 nodes, 64 heads, over up to 12000 positions, 225 GFLOP, 290 + 26
+// (776 TFLOP/s in the main kernel): the exponentials' and conversions' issue
+// beside the products.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -142,55 +152,28 @@ template <typename T>
 __device__ __forceinline__ typename TreeElem<T>::Raw tree_load8(const T *p) {
     return *reinterpret_cast<const typename TreeElem<T>::Raw *>(p);
 }
-// Keys and values are read once, so past the caches' usual order.
-template <typename T>
-__device__ __forceinline__ typename TreeElem<T>::Raw tree_stream8(const T *p) {
-    typename TreeElem<T>::Raw r;
-    using V = decltype(r.w);
-    r.w = __builtin_nontemporal_load(reinterpret_cast<const V *>(p));
-    return r;
+// float32 keys and values are read once, so past the caches' usual order.
+__device__ __forceinline__ v8f32 tree_stream8(const float *p) {
+    return __builtin_nontemporal_load(reinterpret_cast<const v8f32 *>(p));
 }
 
-// Words of 32 bits that C elements take.
-template <typename T, int C>
-constexpr int tree_words() {
-    return C * static_cast<int>(sizeof(T)) / 4;
-}
-
-template <typename T, int C>
-__device__ __forceinline__ void tree_load_row(const T *p, uint32_t *w) {
-    constexpr int n = tree_words<T, C>();
-    if constexpr (n == 2) {
-        const v2u32 v = __builtin_nontemporal_load(reinterpret_cast<const v2u32 *>(p));
-        w[0] = v.x;
-        w[1] = v.y;
-    } else {
+template <int C>
+__device__ __forceinline__ void tree_load_row(const float *p, uint32_t *w) {
 #pragma unroll
-        for (int i = 0; i < n / 4; ++i) {
-            const v4u32 v = __builtin_nontemporal_load(reinterpret_cast<const v4u32 *>(p) + i);
+    for (int i = 0; i < C / 4; ++i) {
+        const v4u32 v = __builtin_nontemporal_load(reinterpret_cast<const v4u32 *>(p) + i);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) w[4 * i + k] = v[k];
-        }
+        for (int k = 0; k < 4; ++k) w[4 * i + k] = v[k];
     }
 }
 
 // Element t of 8 keys' rows as an operand.
-template <typename T, int C>
-__device__ __forceinline__ typename TreeElem<T>::Frag tree_column(
-    const uint32_t (&w)[8][tree_words<T, C>()], int t) {
-    if constexpr (sizeof(T) == 4) {
-        v8f32 v;
+template <int C>
+__device__ __forceinline__ v8f32 tree_column(const uint32_t (&w)[8][C], int t) {
+    v8f32 v;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(w[j][t]);
-        return v;
-    } else {
-        v4u32 v;
-        const uint32_t pick = t % 2 ? 0x07060302u : 0x05040100u;
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-            v[m] = __builtin_amdgcn_perm(w[2 * m + 1][t / 2], w[2 * m][t / 2], pick);
-        return __builtin_bit_cast(typename TreeElem<T>::Frag, v);
-    }
+    for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(w[j][t]);
+    return v;
 }
 
 // A word with its infinities and NaNs taken out.
@@ -265,7 +248,7 @@ __device__ __forceinline__ uint32_t tree_sees8(const uint64_t (*mask)[2], bool c
 }
 
 // Queries and joined sums are not needed at the same time.
-template <typename T, int DP, int R>
+template <int DP, int R>
 struct TreeShared {
     static constexpr int kPitch = DP + 4;  // 16 rows' starts on different banks
     // row tiles that are joined at a time, by what shared memory holds beside
@@ -273,7 +256,7 @@ struct TreeShared {
     static constexpr int kJoin = R == 2 && DP <= 128 ? 2 : 1;
     union {
         float merge[kJoin][kTreeWaves][16][kPitch];
-        typename TreeElem<T>::Raw q[R][DP / 32][kWave];
+        v8f32 q[R][DP / 32][kWave];
     };
     float ml[kTreeWaves][16 * R][2];
     int node[16 * R];  // a row's node
@@ -434,20 +417,15 @@ __device__ __forceinline__ void tree_add_odd(const TreeArgs &a, const uint64_t (
     }
 }
 
-// Waves that a compute unit's SIMD holds, by the registers that R row tiles
-// need (an accumulator takes DP/4 of them, a block's keys and values DP/2).
-template <typename T, int DP>
-constexpr int tree_waves(int R) {
-    if (sizeof(T) == 4) return DP == 64 ? 2 : 1;
-    if (DP == 256) return 1;
-    if (DP == 64) return R <= 2 ? 4 : 2;
-    return R == 1 ? 3 : 2;
-}
+// Waves that a compute unit's SIMD holds, by the registers that R row tiles need
+// (an accumulator takes DP/4 of them, a block's keys and values DP).
+constexpr int tree_waves(int dp) { return dp == 64 ? 2 : 1; }
 
-// FULL: a slot has DP elements and the next one follows it, so that the loads of
-// a block share their addresses; otherwise fewer than DP or further apart.
-template <typename T, int DP, int R, bool FULL>
-__global__ __launch_bounds__(kTreeBlock, (tree_waves<T, DP>(R))) void tree_attention_kernel(TreeArgs a) {
+// float32.  FULL: a slot has DP elements and the next one follows it, so that the
+// loads of a block share their addresses; otherwise fewer than DP or further apart.
+template <int DP, int R, bool FULL>
+__global__ __launch_bounds__(kTreeBlock, tree_waves(DP)) void tree_attention_kernel(TreeArgs a) {
+    using T = float;
     using E = TreeElem<T>;
     using Frag = typename E::Frag;
     using Raw = typename E::Raw;
@@ -455,8 +433,7 @@ __global__ __launch_bounds__(kTreeBlock, (tree_waves<T, DP>(R))) void tree_atten
     constexpr int kCols = DP / 16;              // along the output's dimensions
     constexpr int kChunk = kCols < 8 ? kCols : 8;   // elements of a value load
     constexpr int kChunks = kCols / kChunk;
-    constexpr int kWords = tree_words<T, kChunk>();
-    using Shared = TreeShared<T, DP, R>;
+    using Shared = TreeShared<DP, R>;
     __shared__ Shared sh;
 
     const int units = a.slices * a.KV;
@@ -533,7 +510,7 @@ __global__ __launch_bounds__(kTreeBlock, (tree_waves<T, DP>(R))) void tree_atten
             return static_cast<uint32_t>(e) < static_cast<uint32_t>(a.pages);
         };
         Frag kf[2][kSteps];
-        uint32_t vw[kChunks][8][kWords];
+        uint32_t vw[kChunks][8][kChunk];
         auto load_keys = [&](int p0, int page) {
             if (!is_page(page)) page = 0;
             const T *kp = keys + page * a.page_stride +
@@ -542,7 +519,7 @@ __global__ __launch_bounds__(kTreeBlock, (tree_waves<T, DP>(R))) void tree_atten
             for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int s = 0; s < kSteps; ++s)
-                    kf[c][s] = E::frag(tree_stream8<T>(kp + 4 * c * slot_stride + dk[s]));
+                    kf[c][s] = tree_stream8(kp + 4 * c * slot_stride + dk[s]);
         };
         auto load_values = [&](int p0, int page) {
             if (!is_page(page)) page = 0;
@@ -552,7 +529,7 @@ __global__ __launch_bounds__(kTreeBlock, (tree_waves<T, DP>(R))) void tree_atten
             for (int j = 0; j < 8; ++j)
 #pragma unroll
                 for (int c = 0; c < kChunks; ++c)
-                    tree_load_row<T, kChunk>(vp + j * slot_stride + dv[c], vw[c][j]);
+                    tree_load_row<kChunk>(vp + j * slot_stride + dv[c], vw[c][j]);
         };
         int p0 = from * kTreeTile + wave * kTreeKeys;
         int page_k = -1, page_v = -1, next_k = -1, next_v = -1;
@@ -570,7 +547,7 @@ __global__ __launch_bounds__(kTreeBlock, (tree_waves<T, DP>(R))) void tree_atten
 #pragma unroll
         for (int k = 0; k < kQueries; ++k)
             if (k * kTreeBlock + qt < R * kSteps * kWave)
-                (&sh.q[0][0][0])[k * kTreeBlock + qt] = queries[k];
+                (&sh.q[0][0][0])[k * kTreeBlock + qt] = queries[k].w;
         if (qt < 16 * R) sh.node[qt] = mine;
         if (qt == 0) sh.odd = 0;
         lds_barrier();
@@ -598,7 +575,7 @@ __global__ __launch_bounds__(kTreeBlock, (tree_waves<T, DP>(R))) void tree_atten
                 z[r][0] = z[r][1] = v4f32{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int s = 0; s < kSteps; ++s) {
-                    const Frag qf = E::frag(sh.q[r][s][lane]);
+                    const Frag qf = sh.q[r][s][lane];
                     z[r][0] = E::mma(kf[0][s], qf, z[r][0]);
                     z[r][1] = E::mma(kf[1][s], qf, z[r][1]);
                 }
@@ -644,7 +621,7 @@ __global__ __launch_bounds__(kTreeBlock, (tree_waves<T, DP>(R))) void tree_atten
             for (int c = 0; c < kChunks; ++c)
 #pragma unroll
                 for (int t = 0; t < kChunk; ++t) {
-                    const Frag vf = tree_column<T, kChunk>(vw[c], t);
+                    const Frag vf = tree_column<kChunk>(vw[c], t);
 #pragma unroll
                     for (int r = 0; r < R; ++r)
                         o[r][c * kChunk + t] = E::mma(vf, pf[r], o[r][c * kChunk + t]);
@@ -684,7 +661,7 @@ __global__ __launch_bounds__(kTreeBlock, (tree_waves<T, DP>(R))) void tree_atten
 #pragma unroll
                 for (int c = 0; c < kChunks; ++c)
 #pragma unroll
-                    for (int k = 0; k < kWords; ++k) {
+                    for (int k = 0; k < kChunk; ++k) {
                         const uint32_t w = vw[c][j][k] & there;
                         const uint32_t out = (w ^ tree_finite<T>(w)) & node;
                         odd |= out;
@@ -840,7 +817,7 @@ constexpr int kTreeArith = 0x406;
 // kernel uses m0 (shared memory needs none on this architecture).
 template <bool ONCE>
 __device__ __forceinline__ void tree_load_lds(const void *p, uint32_t at, uint32_t lds) {
-    if (ONCE)  // past the caches' usual order
+    if (ONCE)  // past the caches' usual order: 161 us against 180, 319 against 358
         asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(lds), "v"(at),
                      "s"(p)
                      : "memory");
@@ -893,7 +870,8 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
     constexpr int kSteps = DP / 32, kCols = DP / 16, kRow = DP / 8;
     constexpr int kLoads = kKeys * kRow / kTreeBlock;  // chunks per thread and matrix
     constexpr int kTile = 64 * R;                      // rows of a workgroup
-    // few rows leave the time to follow every maximum
+    // with few rows following every maximum costs nothing that shows (64 single
+    // tokens 161.1 us, 160.5 with slack)
     constexpr float kSlack = R == 1 ? 0.0f : kTreeSlack;
     static_assert(kTreeTile % kKeys == 0, "tiles are dealt out in whole ones");
     __shared__ TreeWideShared<DP> sh;

@@ -71,7 +71,7 @@ def test_tree_attention_validates_on_host(L):
                dict(lse=P(4 * FAR)), dict(lse=P(2 * FAR + 4))):
         assert call(**kw) == -1, kw
     for kw in (dict(T=129, parents=P(16)), dict(T=65537), dict(H=65540), dict(batch=2 ** 31 - 1),
-               dict(sb=1 << 41)):
+               dict(sb=1 << 41), dict(slot_stride=(1 << 28) + 8, page_stride=1 << 33)):
         assert call(**kw) == -2, kw
     for kw in (dict(ws=None, table_width=65), dict(n=64, table_width=65)):
         assert call(**kw) == -3, kw
@@ -82,9 +82,9 @@ def test_tree_attention_validates_on_host(L):
 def test_tree_workspace(L):
     def need(T=3, H=8, **kw):
         return L.spec_tree_attention_workspace_bytes(ctypes.byref(cache(**kw)), T, H)
-    assert need() == 0  # sequences of at most 1024 positions are not cut
-    assert need(table_width=64) == 0
-    assert need(table_width=65) > 0 and need(table_width=65) % 256 == 0
+    assert need() == 0  # sequences of at most 512 positions are not cut
+    assert need(table_width=32) == 0
+    assert need(table_width=33) > 0 and need(table_width=33) % 256 == 0
     for kw in (dict(batch=0), dict(T=0), dict(H=6), dict(page_size=12)):
         assert need(table_width=65, **kw) == 0
     assert L.spec_tree_attention_workspace_bytes(None, 3, 8) == 0
@@ -99,7 +99,7 @@ def test_public_workspace_sizes():
     # strides do not matter to it but for rows that are far apart
     assert sv.tree_workspace_bytes(q, keys.transpose(1, 2).contiguous().transpose(1, 2),
                                    table) == n
-    assert sv.tree_workspace_bytes(q, keys, table[:, :64]) == 0
+    assert sv.tree_workspace_bytes(q, keys, table[:, :32]) == 0
     refs = torch.empty(5000, dtype=torch.int32)
     assert sv.reserve_workspace_bytes(table, refs) == \
         sv.load().spec_pages_reserve_workspace_bytes(3, 5000) > 0

@@ -182,9 +182,11 @@ def test_long_and_short_sequences_share_the_work(dt):
 
 
 @pytest.mark.parametrize("T,G", [(3, 2), (6, 4), (9, 4), (9, 8)])
-def test_cut_and_whole_sequences_agree(T, G):
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("most", [480, 900])
+def test_cut_and_whole_sequences_agree(T, G, dt, most):
     """A wider table row has the same sequence cut over workgroups and joined."""
-    c = make(T, BF16, 3, T, 2 * G, 2, 128, 16, 0, 900, tree=True, least=0)
+    c = make(T, dt, 3, T, 2 * G, 2, 128, 16, 0, most, tree=True, least=0)
     check(c, call(on_gpu(c), lse=True))
     c["table"] = torch.cat([c["table"], torch.full((3, 70), -1, dtype=torch.int32)], 1)
     check(c, call(on_gpu(c), lse=True))
@@ -314,6 +316,20 @@ def test_offsets_beyond_32_bits():
         big[far] = d[k][d["table"][0, :2].long()]
         d[k] = big
     d["table"] = far.to(torch.int32)[None].contiguous()
+    check(c, call(d, lse=True))
+
+
+def test_slots_far_apart():
+    """All pages' first slots, then their second ones: a slot's neighbour in its page lies
+    half a gigabyte behind it, the furthest that 16-bit types may have."""
+    page, kv, D, apart = 8, 2, 64, 1 << 28
+    c = make(23, BF16, 2, 5, 4, kv, D, page, 30, 60, tree=True)
+    d, want = on_gpu(c), c["keys"].shape
+    for k in ("keys", "values"):
+        room = torch.empty(apart * (page - 1) + want[0] * kv * D, dtype=BF16, device="cuda")
+        far = room.as_strided(want, (kv * D, D, apart, 1))
+        far.copy_(d[k])
+        d[k] = far
     check(c, call(d, lse=True))
 
 
