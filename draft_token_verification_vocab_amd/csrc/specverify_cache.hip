@@ -58,8 +58,9 @@ Range range(const void *p, int64_t bytes) {
     return Range{c, c + bytes};
 }
 
-// The largest multiple of n that fits the address arithmetic.
-constexpr int64_t kMaxStride = int64_t{1} << 40;
+// Strides, and counts times them, that keep the address arithmetic far from 2^63.
+constexpr int64_t kMaxStride = int64_t{1} << 40, kMaxSpan = int64_t{1} << 56;
+bool span_ok(int64_t n, int64_t stride) { return stride < 1 || n <= kMaxSpan / stride; }
 
 spec_status check_cache(const spec_cache *c) {
     if (!c || c->batch < 0 || c->reserved != 0) return SPEC_ERR_ARG;
@@ -69,7 +70,8 @@ spec_status check_cache(const spec_cache *c) {
     const spec_status s = check_table(c->table_width, c->page_size, c->num_pages);
     if (s != SPEC_OK) return s;
     const int e = elem_size(c->dtype);
-    if (c->page_stride > kMaxStride || c->head_stride > kMaxStride || c->slot_stride > kMaxStride)
+    if (c->page_stride > kMaxStride || c->head_stride > kMaxStride ||
+        c->slot_stride > kMaxStride || !span_ok(c->num_pages, c->page_stride))
         return SPEC_ERR_UNSUPPORTED;
     if (!stride_ok(c->page_stride * e) || !stride_ok(c->head_stride * e) ||
         !stride_ok(c->slot_stride * e) || c->slot_stride < c->dim)
@@ -84,6 +86,14 @@ int64_t pool_bytes(const spec_cache *c) {
             (c->page_size - 1) * c->slot_stride + c->dim) *
            elem_size(c->dtype);
 }
+
+// Whether a pool that is written to has places of their own for its pages and heads.
+template <typename C>
+bool strides_apart(const C *c, int32_t heads) {
+    return (c->num_pages == 1 || c->page_stride > 0) && (heads == 1 || c->head_stride > 0);
+}
+bool pages_apart(const spec_cache *c) { return strides_apart(c, c->kv_heads); }
+bool pages_apart(const spec_cache_pools *p) { return strides_apart(p, p->heads); }
 
 bool pools_ok(const spec_cache *c) {
     return c->keys && c->values && aligned16(c->keys) && aligned16(c->values) && c->table &&
@@ -241,10 +251,11 @@ spec_status check_pools(const spec_cache_pools *p) {
     if (!p || p->num_pools < 0 || p->num_pages < 1 || p->page_size < 1 || p->heads < 1 ||
         p->slot_bytes < 1)
         return SPEC_ERR_ARG;
-    if (p->page_stride > kMaxStride || p->head_stride > kMaxStride || p->slot_stride > kMaxStride)
+    if (p->page_stride > kMaxStride || p->head_stride > kMaxStride ||
+        p->slot_stride > kMaxStride || !span_ok(p->num_pages, p->page_stride))
         return SPEC_ERR_UNSUPPORTED;
     if (!stride_ok(p->page_stride) || !stride_ok(p->head_stride) || !stride_ok(p->slot_stride) ||
-        p->slot_bytes % 16 != 0 || p->slot_stride < p->slot_bytes)
+        p->slot_bytes % 16 != 0 || p->slot_stride < p->slot_bytes || !pages_apart(p))
         return SPEC_ERR_ARG;
     if (!page_size_ok(p->page_size) || p->heads > kMaxHeads || p->slot_bytes > 65536)
         return SPEC_ERR_UNSUPPORTED;
@@ -304,7 +315,8 @@ spec_status spec_tree_attention(const spec_cache *cache, const void *q, int64_t 
     if (s != SPEC_OK) return s;
     if (!(scale > 0.0f) || !std::isfinite(scale)) return SPEC_ERR_ARG;
     const int e = elem_size(cache->dtype);
-    if (q_batch_stride > kMaxStride || q_node_stride > kMaxStride || q_head_stride > kMaxStride)
+    if (q_batch_stride > kMaxStride || q_node_stride > kMaxStride ||
+        q_head_stride > kMaxStride || !span_ok(cache->batch, q_batch_stride))
         return SPEC_ERR_UNSUPPORTED;
     if (!stride_ok(q_batch_stride * e) || !stride_ok(q_node_stride * e) ||
         !stride_ok(q_head_stride * e))
@@ -388,13 +400,14 @@ spec_status spec_cache_append(const spec_cache *cache, const void *k, const void
     const int e = elem_size(cache->dtype);
     if (nodes < 0) return SPEC_ERR_ARG;
     if (batch_stride > kMaxStride || node_stride > kMaxStride || head_stride > kMaxStride ||
-        nodes > kMaxRoom)
+        nodes > kMaxRoom || !span_ok(cache->batch, batch_stride) || !span_ok(nodes, node_stride))
         return SPEC_ERR_UNSUPPORTED;
     if (!stride_ok(batch_stride * e) || !stride_ok(node_stride * e) || !stride_ok(head_stride * e))
         return SPEC_ERR_ARG;
     if (cache->batch == 0 || nodes == 0) return SPEC_OK;
     if (!pools_ok(cache) || !k || !v || !aligned16(k) || !aligned16(v)) return SPEC_ERR_ARG;
-    if (cache->keys == cache->values) return SPEC_ERR_ARG;  // two writers to an element
+    // two writers to an element
+    if (cache->keys == cache->values || !pages_apart(cache)) return SPEC_ERR_ARG;
     const int64_t span = ((cache->batch - 1) * batch_stride + (nodes - 1) * node_stride +
                           (cache->kv_heads - 1) * head_stride + cache->dim) *
                          e;

@@ -42,7 +42,8 @@ BAD_CACHE = [
     (dict(page_size=0), -1), (dict(page_size=4), -2), (dict(page_size=12), -2),
     (dict(page_size=2048), -2), (dict(table_width=1 << 28), -2), (dict(slot_stride=63), -1),
     (dict(slot_stride=56), -1), (dict(page_stride=4100), -1), (dict(head_stride=-8), -1),
-    (dict(page_stride=1 << 41), -2), (dict(keys=None), -1), (dict(values=None), -1),
+    (dict(page_stride=1 << 41), -2),
+    (dict(page_stride=1 << 40, num_pages=1 << 20), -2), (dict(keys=None), -1), (dict(values=None), -1),
     (dict(keys=FAR + 8), -1), (dict(table=None), -1), (dict(lengths=None), -1)]
 
 
@@ -71,7 +72,7 @@ def test_tree_attention_validates_on_host(L):
                dict(lse=P(4 * FAR)), dict(lse=P(2 * FAR + 4))):
         assert call(**kw) == -1, kw
     for kw in (dict(T=129, parents=P(16)), dict(T=65537), dict(H=65540), dict(batch=2 ** 31 - 1),
-               dict(sb=1 << 41), dict(slot_stride=(1 << 28) + 8, page_stride=1 << 33)):
+               dict(sb=1 << 41), dict(sb=1 << 40, batch=1 << 20), dict(slot_stride=(1 << 28) + 8, page_stride=1 << 33)):
         assert call(**kw) == -2, kw
     for kw in (dict(ws=None, table_width=65), dict(n=64, table_width=65)):
         assert call(**kw) == -3, kw
@@ -113,10 +114,11 @@ def test_append_validates_on_host(L):
                                    None)
     for kw in (dict(null=True), dict(k=None), dict(v=None), dict(k=P(8)), dict(v=P(24)),
                dict(T=-1), dict(sb=4), dict(sn=-8), dict(sh=1), dict(k=P(FAR + 64)),
-               dict(v=P(2 * FAR)), dict(values=FAR)):
+               dict(v=P(2 * FAR)), dict(values=FAR), dict(page_stride=0), dict(head_stride=0)):
         assert call(**kw) == -1, kw
     assert call(T=1 << 30, batch=1 << 20) == -2
-    assert call(sn=1 << 41) == -2
+    assert call(sn=1 << 41) == -2 and call(sn=1 << 40, T=1 << 20) == -2
+    assert call(sb=1 << 40, batch=1 << 20) == -2
     assert call(T=0, k=None, v=None) == 0 and call(batch=0, k=None, v=None) == 0
 
 
@@ -149,6 +151,7 @@ BAD_POOLS = [
     (dict(page_size=24), -2), (dict(heads=0), -1), (dict(slot_bytes=0), -1),
     (dict(slot_bytes=120), -1), (dict(slot_bytes=144), -1), (dict(page_stride=4104), -1),
     (dict(head_stride=-16), -1), (dict(slot_bytes=65552, slot_stride=65552), -2),
+    (dict(page_stride=0), -1), (dict(head_stride=0), -1),
     (dict(page_stride=1 << 41), -2), (dict(bases=None), -1), (dict(bases=(FAR, None)), -1),
     (dict(bases=(FAR + 8,)), -1), (dict(heads=65536), -2)]
 

@@ -70,7 +70,7 @@ def test_example():
     want = np.full((B, P), -1)
     refs = np.zeros(N, dtype=int)
     for b in range(B):
-        want[b, :held[b]] = table[b, :held[b]]
+        want[b, :held[b]] = table[b, :held[b]].tolist()
         refs[want[b, :held[b]]] = 3
     assert (table.numpy() == want).all()
     assert (names["branches"].cpu().numpy() == want[:, None]).all()
