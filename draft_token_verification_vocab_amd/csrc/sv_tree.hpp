@@ -822,17 +822,22 @@ constexpr int kTreeArith = 0x406;
 // 16 bytes a lane, at bytes behind p, to the wave's 1024 bytes of shared memory at
 // lds, lane by lane; lanes that are off leave their places.  The load has no
 // destination register and the compiler does not know of it, so that reading
-// another stage does not wait for it; tree_loads_done() does.  Nothing else in the
-// kernel uses m0 (shared memory needs none on this architecture).
+// another stage does not wait for it; tree_loads_done() does.  Its base in shared
+// memory is m0, which a load may take one wait state after a scalar write at the
+// earliest; the compiler keeps no wait states within an asm block, so the s_nop does.
+// m0 is reserved and cannot be listed as overwritten: nothing else in the kernel uses
+// it (shared memory needs none on this architecture; tests/test_isa_hazards.py looks).
 template <bool ONCE>
 __device__ __forceinline__ void tree_load_lds(const void *p, uint32_t at, uint32_t lds) {
     if (ONCE)  // past the caches' usual order: 161 us against 180, 319 against 358
-        asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(lds), "v"(at),
-                     "s"(p)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt"
+                     :
+                     : "s"(lds), "v"(at), "s"(p)
                      : "memory");
     else
-        asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(at),
-                     "s"(p)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                     :
+                     : "s"(lds), "v"(at), "s"(p)
                      : "memory");
 }
 __device__ __forceinline__ void tree_loads_done() {
