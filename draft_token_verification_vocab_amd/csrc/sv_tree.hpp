@@ -17,8 +17,9 @@
 // A query row is a column throughout, so its maximum, sum and rescaling stay in
 // its lanes.  Products are added in 32 bits.  For 16-bit types the weights are
 // rounded to the type before the second product, as its matrix instructions take
-// them (a relative 2^-9 or 2^-12 of each, with independent signs).  lse comes from
-// their sum before that rounding, in 32 bits.
+// them: a relative 2^-9 (bfloat16) or 2^-12 (float16) of each, with independent signs;
+// float16 weights below 2^-23 of the row's largest keep an absolute 2^-34 of it instead
+// (see kLift).  lse comes from their sum before that rounding, in 32 bits.
 //
 // Two kernels: tree_wide_kernel for 16-bit types, where rows are shared out to the
 // waves and keys come through shared memory, and tree_attention_kernel for
@@ -84,7 +85,8 @@ struct TreeArgs {
 };
 
 // Types of keys and values.  Frag: a matrix operand's 8 elements along the
-// summed dimension; load8: 8 consecutive elements.
+// summed dimension; load8: 8 consecutive elements; kTop: the power of two that
+// weights may reach where the type's exponents are too few below 1 (else 0).
 template <typename T>
 struct TreeElem;
 
@@ -115,6 +117,7 @@ struct TreeElem<__bf16> : TreeElem16<v8bf16> {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
     }
     static constexpr uint32_t kExponent = 0x7F80u;
+    static constexpr float kTop = 0.0f;
 };
 
 template <>
@@ -123,6 +126,7 @@ struct TreeElem<_Float16> : TreeElem16<v8f16> {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
     }
     static constexpr uint32_t kExponent = 0x7C00u;
+    static constexpr float kTop = 15.0f;
 };
 
 template <>
@@ -809,10 +813,13 @@ __global__ __launch_bounds__(kTreeBlock, tree_waves(DP)) void tree_attention_ker
 // twice (half of shared memory's cycles, wide trees 327 us against 316).
 //
 // The weights' reference moves only when a score passes it by 2^6: they stay
-// below 2^6 and sums of 2^30 of them far from a float's end.  As the largest
-// weight is then not exactly 1, the output is divided by the sum of the rounded
-// weights, one more matrix product with a row of ones; lse takes the sum of
-// the unrounded ones.
+// below 2^6 and sums of 2^30 of them far from a float's end.  float16 has normal
+// numbers down to 2^-14 alone but up to 65504, so there the reference lies 2^9 (2^15
+// without slack) below the largest score and weights reach 2^15: a key that takes
+// nearly all of a row's weight and holds nothing leaves the others nine bits more.
+// As the largest weight is then not exactly 1, the output is divided by the sum of
+// the rounded weights, one more matrix product with a row of ones; lse takes the sum
+// of the unrounded ones.
 // ---------------------------------------------------------------------------
 constexpr float kTreeSlack = 6.0f;
 // What may be moved past a scheduling barrier: ordinary arithmetic, which then
@@ -887,6 +894,8 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
     // with few rows following every maximum costs nothing that shows (64 single
     // tokens 161.1 us, 160.5 with slack)
     constexpr float kSlack = R == 1 ? 0.0f : kTreeSlack;
+    // how far the reference lies below the largest score at the time
+    constexpr float kLift = E::kTop > 0.0f ? E::kTop - kSlack : 0.0f;
     static_assert(kTreeTile % kKeys == 0, "tiles are dealt out in whole ones");
     __shared__ TreeWideShared<DP> sh;
 
@@ -1078,12 +1087,12 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
                 for (int j = 1; j < 8 * kBlocks; ++j)
                     t = fmaxf(t, z[j / 8][r][j / 4 % 2][j % 4]);
                 top[r] = t * a.scale2;
-                behind |= top[r] > m[r] + kSlack;
+                behind |= top[r] > m[r] + (kSlack + kLift);
             }
             if (__builtin_expect(__any(behind), 0)) {
 #pragma unroll
                 for (int r = 0; r < N; ++r) {
-                    const float up = fmaxf(m[r], across_groups_max(top[r]));
+                    const float up = fmaxf(m[r], across_groups_max(top[r]) - kLift);
                     const float f = up == -__builtin_inff() ? 1.0f : hw_exp2(m[r] - up);
                     l[r] *= f;
                     n[r] *= f;

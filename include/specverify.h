@@ -641,7 +641,8 @@ typedef struct spec_cache {
  * A node that is not in use, or that sees nothing (its scores -inf throughout
  * counts as nothing), has out 0 and lse -inf.  Sums and products are taken in
  * 32 bits; for 16-bit types the weights are rounded to the type before their
- * product with the values.  out and lse overlap no input.  workspace: device,
+ * product with the values (float16: those below 2^-23 of a row's largest to a
+ * multiple of at most 2^-33 of it).  out and lse overlap no input.  workspace: device,
  * spec_tree_attention_workspace_bytes (0, and then NULL will do, for tables of
  * few positions; 0 too if the arguments are not valid), 16-byte aligned; its
  * contents on entry do not matter.
