@@ -46,7 +46,8 @@ spec_status check_table(int32_t table_width, int32_t page_size, int32_t num_page
     return SPEC_OK;
 }
 
-bool stride_ok(int64_t bytes) { return bytes >= 0 && bytes % 16 == 0; }
+// A stride of n elements of e bytes: looked at before it is multiplied, which may wrap.
+bool stride_ok(int64_t n, int e) { return n >= 0 && n % (16 / e) == 0; }
 
 // Addresses [from, to).
 struct Range {
@@ -73,8 +74,8 @@ spec_status check_cache(const spec_cache *c) {
     if (c->page_stride > kMaxStride || c->head_stride > kMaxStride ||
         c->slot_stride > kMaxStride || !span_ok(c->num_pages, c->page_stride))
         return SPEC_ERR_UNSUPPORTED;
-    if (!stride_ok(c->page_stride * e) || !stride_ok(c->head_stride * e) ||
-        !stride_ok(c->slot_stride * e) || c->slot_stride < c->dim)
+    if (!stride_ok(c->page_stride, e) || !stride_ok(c->head_stride, e) ||
+        !stride_ok(c->slot_stride, e) || c->slot_stride < c->dim)
         return SPEC_ERR_ARG;
     if (c->dim > 256 || c->kv_heads > kMaxHeads) return SPEC_ERR_UNSUPPORTED;
     return SPEC_OK;
@@ -254,7 +255,8 @@ spec_status check_pools(const spec_cache_pools *p) {
     if (p->page_stride > kMaxStride || p->head_stride > kMaxStride ||
         p->slot_stride > kMaxStride || !span_ok(p->num_pages, p->page_stride))
         return SPEC_ERR_UNSUPPORTED;
-    if (!stride_ok(p->page_stride) || !stride_ok(p->head_stride) || !stride_ok(p->slot_stride) ||
+    if (!stride_ok(p->page_stride, 1) || !stride_ok(p->head_stride, 1) ||
+        !stride_ok(p->slot_stride, 1) ||
         p->slot_bytes % 16 != 0 || p->slot_stride < p->slot_bytes || !pages_apart(p))
         return SPEC_ERR_ARG;
     if (!page_size_ok(p->page_size) || p->heads > kMaxHeads || p->slot_bytes > 65536)
@@ -318,8 +320,8 @@ spec_status spec_tree_attention(const spec_cache *cache, const void *q, int64_t 
     if (q_batch_stride > kMaxStride || q_node_stride > kMaxStride ||
         q_head_stride > kMaxStride || !span_ok(cache->batch, q_batch_stride))
         return SPEC_ERR_UNSUPPORTED;
-    if (!stride_ok(q_batch_stride * e) || !stride_ok(q_node_stride * e) ||
-        !stride_ok(q_head_stride * e))
+    if (!stride_ok(q_batch_stride, e) || !stride_ok(q_node_stride, e) ||
+        !stride_ok(q_head_stride, e))
         return SPEC_ERR_ARG;
     if (cache->batch == 0) return SPEC_OK;
     if (!pools_ok(cache) || !q || !aligned16(q) || !out || !aligned16(out)) return SPEC_ERR_ARG;
@@ -402,7 +404,7 @@ spec_status spec_cache_append(const spec_cache *cache, const void *k, const void
     if (batch_stride > kMaxStride || node_stride > kMaxStride || head_stride > kMaxStride ||
         nodes > kMaxRoom || !span_ok(cache->batch, batch_stride) || !span_ok(nodes, node_stride))
         return SPEC_ERR_UNSUPPORTED;
-    if (!stride_ok(batch_stride * e) || !stride_ok(node_stride * e) || !stride_ok(head_stride * e))
+    if (!stride_ok(batch_stride, e) || !stride_ok(node_stride, e) || !stride_ok(head_stride, e))
         return SPEC_ERR_ARG;
     if (cache->batch == 0 || nodes == 0) return SPEC_OK;
     if (!pools_ok(cache) || !k || !v || !aligned16(k) || !aligned16(v)) return SPEC_ERR_ARG;
