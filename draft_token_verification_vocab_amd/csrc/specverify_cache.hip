@@ -13,6 +13,7 @@
 #include "sv_cache.hpp"
 #include "sv_common.hpp"
 #include "sv_host.hpp"
+#include "sv_launch.hpp"
 #include "sv_tree.hpp"
 
 namespace {
@@ -24,11 +25,6 @@ constexpr int kMaxChainNodes = 65536;
 constexpr int kMaxHeads = 65535;
 constexpr int kMaxRoom = 1 << 30;      // positions that a table row can hold
 constexpr int kMaxReserveRows = 65536;
-
-// A grid's threads must stay below 2^32.
-bool grid_fits(int64_t blocks, int block) {
-    return blocks <= (int64_t{1} << 32) / block - 1 && blocks <= INT32_MAX;
-}
 
 int page_shift(int32_t page_size) {
     int s = 0;
@@ -497,18 +493,14 @@ spec_status spec_cache_keep(const spec_cache_pools *pools, const int32_t *table,
     a.T = nodes;
     a.P = table_width;
     const int64_t column = static_cast<int64_t>(pools->heads) * (pools->slot_bytes / 16);
-    int step = kMaxPools;
-    const int64_t most = (int64_t{1} << 30) / batch;  // workgroups per sequence
-    while (step > 1 && column * step / kCacheBlock + 1 > most) step /= 2;
-    if (column * step / kCacheBlock + 1 > most ||
-        !grid_fits((column * step / kCacheBlock + 1) * batch, kCacheBlock))
-        return SPEC_ERR_UNSUPPORTED;
+    // no pools: the lengths alone
+    const int step = pools->num_pools ? keep_pools_per_launch(column, batch, pools->num_pools) : 1;
+    if (step == 0 || !grid_fits(batch, kCacheBlock)) return SPEC_ERR_UNSUPPORTED;
     for (int first = 0; first == 0 || first < pools->num_pools; first += step) {
         const int n = pools->num_pools - first < step ? pools->num_pools - first : step;
         a.pool = pool_args(pools, first, n);
         a.new_lengths = first == 0 ? new_lengths : nullptr;
-        a.blocks = static_cast<int32_t>((column * n + kCacheBlock - 1) / kCacheBlock);
-        if (a.blocks < 1) a.blocks = 1;  // no pools: the lengths alone
+        a.blocks = static_cast<int32_t>(keep_blocks(column, n));
         cache_keep_kernel<<<dim3(static_cast<unsigned>(a.blocks * batch)), dim3(kCacheBlock), 0,
                             static_cast<hipStream_t>(stream)>>>(a);
         if ((s = launch_status()) != SPEC_OK) return s;
@@ -633,9 +625,8 @@ spec_status spec_pages_copy(const spec_cache_pools *pools, const int32_t *copies
     if (!copies) return SPEC_ERR_ARG;
     CopyArgs a{};
     a.copies = copies;
-    int step = kMaxPools;
-    while (step > 1 && !grid_fits(int64_t{rows} * pools->heads * step, kCacheBlock)) step /= 2;
-    if (!grid_fits(int64_t{rows} * pools->heads * step, kCacheBlock)) return SPEC_ERR_UNSUPPORTED;
+    const int step = copy_pools_per_launch(rows, pools->heads, pools->num_pools);
+    if (step == 0) return SPEC_ERR_UNSUPPORTED;
     for (int first = 0; first < pools->num_pools; first += step) {
         const int n = pools->num_pools - first < step ? pools->num_pools - first : step;
         a.pool = pool_args(pools, first, n);

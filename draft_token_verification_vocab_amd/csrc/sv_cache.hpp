@@ -12,11 +12,10 @@
 #include <cstdint>
 
 #include "sv_common.hpp"
+#include "sv_launch.hpp"
 
 namespace sv {
 
-constexpr int kCacheBlock = 256;
-constexpr int kMaxPools = 64;        // pools per launch
 constexpr int kMaxKeepNodes = 1024;  // entries of a path
 constexpr int kMaxAcceptNodes = 128;
 

@@ -602,7 +602,9 @@ spec_status spec_beam_reorder(const int32_t *parents, const int32_t *lengths, in
  * [0, nodes], and lengths to what the table row can hold.
  *
  * page_size is a power of two from 8 to 1024, kv_heads <= 65535, and table_width
- * * page_size <= 2^30, else SPEC_ERR_UNSUPPORTED.
+ * * page_size <= 2^30, else SPEC_ERR_UNSUPPORTED.  So is what a launch's grid does
+ * not hold, 2^24 workgroups of 256 threads: rows for forking and releasing, rows *
+ * heads for copying, and batch * heads * slot_bytes / 4096 for keeping.
  */
 typedef struct spec_cache {
     void *keys;           /* device, 16-byte aligned                          */
