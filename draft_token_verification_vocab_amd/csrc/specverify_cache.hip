@@ -14,6 +14,7 @@
 #include "sv_common.hpp"
 #include "sv_host.hpp"
 #include "sv_launch.hpp"
+#include "sv_layout.hpp"
 #include "sv_tree.hpp"
 
 namespace {
@@ -84,13 +85,17 @@ int64_t pool_bytes(const spec_cache *c) {
            elem_size(c->dtype);
 }
 
-// Whether a pool that is written to has places of their own for its pages and heads.
-template <typename C>
-bool strides_apart(const C *c, int32_t heads) {
-    return (c->num_pages == 1 || c->page_stride > 0) && (heads == 1 || c->head_stride > 0);
+// Whether every element of a pool that is written to has a place of its own: one that
+// pages, heads or slots share has two writers.
+bool elements_apart(const spec_cache *c, PoolLayout *p) {
+    const int64_t e = elem_size(c->dtype);
+    return lay_out({c->num_pages, c->kv_heads, c->page_size},
+                   {c->page_stride * e, c->head_stride * e, c->slot_stride * e}, c->dim * e, p);
 }
-bool pages_apart(const spec_cache *c) { return strides_apart(c, c->kv_heads); }
-bool pages_apart(const spec_cache_pools *p) { return strides_apart(p, p->heads); }
+bool elements_apart(const spec_cache_pools *c, PoolLayout *p) {
+    return lay_out({c->num_pages, c->heads, c->page_size},
+                   {c->page_stride, c->head_stride, c->slot_stride}, c->slot_bytes, p);
+}
 
 bool pools_ok(const spec_cache *c) {
     return c->keys && c->values && aligned16(c->keys) && aligned16(c->values) && c->table &&
@@ -252,11 +257,13 @@ spec_status check_pools(const spec_cache_pools *p) {
         p->slot_stride > kMaxStride || !span_ok(p->num_pages, p->page_stride))
         return SPEC_ERR_UNSUPPORTED;
     if (!stride_ok(p->page_stride, 1) || !stride_ok(p->head_stride, 1) ||
-        !stride_ok(p->slot_stride, 1) ||
-        p->slot_bytes % 16 != 0 || p->slot_stride < p->slot_bytes || !pages_apart(p))
+        !stride_ok(p->slot_stride, 1) || p->slot_bytes % 16 != 0 ||
+        p->slot_stride < p->slot_bytes)
         return SPEC_ERR_ARG;
     if (!page_size_ok(p->page_size) || p->heads > kMaxHeads || p->slot_bytes > 65536)
         return SPEC_ERR_UNSUPPORTED;
+    PoolLayout layout;
+    if (!elements_apart(p, &layout)) return SPEC_ERR_ARG;
     if (p->num_pools > 0 && !p->bases) return SPEC_ERR_ARG;
     for (int i = 0; i < p->num_pools; ++i)
         if (!p->bases[i] || !aligned16(p->bases[i])) return SPEC_ERR_ARG;
@@ -405,7 +412,8 @@ spec_status spec_cache_append(const spec_cache *cache, const void *k, const void
     if (cache->batch == 0 || nodes == 0) return SPEC_OK;
     if (!pools_ok(cache) || !k || !v || !aligned16(k) || !aligned16(v)) return SPEC_ERR_ARG;
     // two writers to an element
-    if (cache->keys == cache->values || !pages_apart(cache)) return SPEC_ERR_ARG;
+    PoolLayout layout;
+    if (cache->keys == cache->values || !elements_apart(cache, &layout)) return SPEC_ERR_ARG;
     const int64_t span = ((cache->batch - 1) * batch_stride + (nodes - 1) * node_stride +
                           (cache->kv_heads - 1) * head_stride + cache->dim) *
                          e;

@@ -661,8 +661,10 @@ spec_status spec_tree_attention(const spec_cache *cache, const void *q, int64_t 
  * k, v: device, elements of cache->dtype, node j's key head h of sequence b at
  * b*batch_stride + j*node_stride + h*head_stride of each (elements; multiples
  * of 16 bytes, >= 0; 16-byte aligned; outside the pools).  The pools of keys
- * and values are different ones, and their pages and heads lie apart (strides
- * above 0).  Positions past the table row are dropped.  Rows of a table that share a page must not both write to it
+ * and values are different ones, and each element has a place of its own: of the
+ * strides of pages, heads and slots (where there are more than one) each is at
+ * least what the smaller ones span.  Positions past the table row are dropped.
+ * Rows of a table that share a page must not both write to it
  * (spec_pages_reserve sees to that).
  */
 spec_status spec_cache_append(const spec_cache *cache, const void *k, const void *v,
@@ -691,7 +693,8 @@ spec_status spec_tree_accept(const int32_t *parents, const int32_t *tokens,
 
 /* Pools of one shape, for the calls that move positions or pages of all layers
  * at once.  Sizes and strides in bytes; bases, strides and slot_bytes are
- * multiples of 16; pages and heads lie apart (strides above 0). */
+ * multiples of 16; each element has a place of its own, as spec_cache_append
+ * asks. */
 typedef struct spec_cache_pools {
     void *const *bases;   /* host array of num_pools device addresses         */
     int32_t num_pools;    /* >= 0                                             */

@@ -1,6 +1,7 @@
 """Host-side limits of the paged-cache calls at their ends (no GPU needed): strides
 that wrap, counts past 32 bits, and memory that is given twice."""
 import ctypes
+import itertools
 import os
 import subprocess
 
@@ -73,3 +74,34 @@ def test_keep_takes_what_a_launch_holds(L):  # noqa: F811
                              None) not in (-1, -2)
     assert L.spec_cache_keep(ctypes.byref(p), a[0], 5, a[1], a[2], a[3], 1 << 22, 4, a[4],
                              None) == -2
+
+
+def span(n, stride, unit):
+    return {sum(i * s for i, s in zip(at, stride)) + k for at in itertools.product(*map(range, n))
+            for k in range(unit)}
+
+
+# page, head and slot strides in 16-byte units for 3 pages, 2 heads and 8 slots of 2 units
+STRIDES = [(32, 16, 2), (40, 16, 2), (32, 2, 4), (16, 48, 2), (2, 6, 12), (16, 1, 2), (15, 16, 2),
+           (32, 15, 2), (31, 16, 2), (0, 16, 2), (32, 0, 2), (1, 16, 2), (32, 2, 3), (34, 17, 2)]
+
+
+@host_only
+@pytest.mark.parametrize("strides", STRIDES, ids=str)
+def test_pools_that_are_written_have_a_place_for_every_element(L, strides):  # noqa: F811
+    """An element that two pages, heads or slots share would have two writers."""
+    apart = len(span((3, 2, 8), strides, 2)) == 3 * 2 * 8 * 2
+    page, head, slot = strides
+    p = pools(page_size=8, num_pages=3, heads=2, slot_bytes=32, page_stride=16 * page,
+              head_stride=16 * head, slot_stride=16 * slot)
+    c = cache(page_size=8, num_pages=3, kv_heads=2, dim=16, page_stride=8 * page,
+              head_stride=8 * head, slot_stride=8 * slot)
+    a = [P(n << 32) for n in range(1, 6)]
+    for status in (L.spec_cache_keep(ctypes.byref(p), a[0], 5, a[1], a[2], a[3], 2, 4, a[4], None),
+                   L.spec_pages_copy(ctypes.byref(p), a[0], 3, None),
+                   L.spec_cache_append(ctypes.byref(c), a[0], a[1], 1024, 512, 64, 3, None, None)):
+        assert (status not in (-1, -2)) if apart else status == -1
+    # axes of one element may have any stride
+    one = pools(page_size=8, num_pages=1, heads=1, slot_bytes=32, page_stride=0, head_stride=16,
+                slot_stride=32)
+    assert L.spec_pages_copy(ctypes.byref(one), a[0], 3, None) not in (-1, -2)
