@@ -249,7 +249,8 @@ void launch_join(const TreeArgs &a, const TreePlan &p, hipStream_t st) {
 // ---------------------------------------------------------------------------
 // Pools
 // ---------------------------------------------------------------------------
-spec_status check_pools(const spec_cache_pools *p) {
+// twice: whether a pool that is given twice counts as sharing its memory.
+spec_status check_pools(const spec_cache_pools *p, bool twice) {
     if (!p || p->num_pools < 0 || p->num_pages < 1 || p->page_size < 1 || p->heads < 1 ||
         p->slot_bytes < 1)
         return SPEC_ERR_ARG;
@@ -267,7 +268,7 @@ spec_status check_pools(const spec_cache_pools *p) {
     if (p->num_pools > 0 && !p->bases) return SPEC_ERR_ARG;
     for (int i = 0; i < p->num_pools; ++i)
         if (!p->bases[i] || !aligned16(p->bases[i])) return SPEC_ERR_ARG;
-    return SPEC_OK;
+    return any_pools_meet(layout, p->bases, p->num_pools, twice) ? SPEC_ERR_ARG : SPEC_OK;
 }
 
 // Pools [first, first + count) as a kernel takes them.
@@ -413,7 +414,9 @@ spec_status spec_cache_append(const spec_cache *cache, const void *k, const void
     if (!pools_ok(cache) || !k || !v || !aligned16(k) || !aligned16(v)) return SPEC_ERR_ARG;
     // two writers to an element
     PoolLayout layout;
-    if (cache->keys == cache->values || !elements_apart(cache, &layout)) return SPEC_ERR_ARG;
+    void *const both[] = {cache->keys, cache->values};
+    if (!elements_apart(cache, &layout) || any_pools_meet(layout, both, 2, true))
+        return SPEC_ERR_ARG;
     const int64_t span = ((cache->batch - 1) * batch_stride + (nodes - 1) * node_stride +
                           (cache->kv_heads - 1) * head_stride + cache->dim) *
                          e;
@@ -481,7 +484,7 @@ spec_status spec_cache_keep(const spec_cache_pools *pools, const int32_t *table,
                             int32_t table_width, const int32_t *lengths, const int32_t *path,
                             const int32_t *count, int32_t batch, int32_t nodes,
                             int32_t *new_lengths, void *stream) {
-    spec_status s = check_pools(pools);
+    spec_status s = check_pools(pools, true);
     if (s != SPEC_OK) return s;
     if ((s = check_table(table_width, pools->page_size, pools->num_pages)) != SPEC_OK) return s;
     if (batch < 0 || nodes < 1) return SPEC_ERR_ARG;
@@ -626,7 +629,7 @@ spec_status spec_pages_reserve(int32_t *table, const int32_t *lengths,
 
 spec_status spec_pages_copy(const spec_cache_pools *pools, const int32_t *copies, int32_t rows,
                             void *stream) {
-    spec_status s = check_pools(pools);
+    spec_status s = check_pools(pools, false);
     if (s != SPEC_OK) return s;
     if (rows < 0) return SPEC_ERR_ARG;
     if (rows == 0 || pools->num_pools == 0) return SPEC_OK;

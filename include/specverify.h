@@ -661,7 +661,7 @@ spec_status spec_tree_attention(const spec_cache *cache, const void *q, int64_t 
  * k, v: device, elements of cache->dtype, node j's key head h of sequence b at
  * b*batch_stride + j*node_stride + h*head_stride of each (elements; multiples
  * of 16 bytes, >= 0; 16-byte aligned; outside the pools).  The pools of keys
- * and values are different ones, and each element has a place of its own: of the
+ * and values share no element, and each element has a place of its own: of the
  * strides of pages, heads and slots (where there are more than one) each is at
  * least what the smaller ones span.  Positions past the table row are dropped.
  * Rows of a table that share a page must not both write to it
@@ -709,7 +709,7 @@ typedef struct spec_cache_pools {
 
 /*
  * spec_cache_keep -- after verification: moves the accepted nodes' positions
- * together, in every pool (all different): position lengths[b] + path[b][i] goes
+ * together, in every pool (no two share an element): position lengths[b] + path[b][i] goes
  * to lengths[b] + i for i < count[b].  path: device int32 [batch][nodes],
  * ascending within [0, nodes) as spec_tree_accept gives it (the first entry
  * that is not ends the list); count: device int32 [batch].  new_lengths
@@ -778,7 +778,8 @@ spec_status spec_pages_reserve(int32_t *table, const int32_t *lengths,
 
 /* spec_pages_copy -- in every pool, the first copies[r][2] positions of page
  * copies[r][0] to page copies[r][1] (device int32 [rows][3]), for all rows whose
- * pages lie in [0, num_pages).  No page is the destination of two rows, or of
+ * pages lie in [0, num_pages).  Pools share no element, but that one may be listed
+ * twice.  No page is the destination of two rows, or of
  * one and the source of another. */
 spec_status spec_pages_copy(const spec_cache_pools *pools, const int32_t *copies, int32_t rows,
                             void *stream);

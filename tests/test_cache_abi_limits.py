@@ -3,6 +3,7 @@ that wrap, counts past 32 bits, and memory that is given twice."""
 import ctypes
 import itertools
 import os
+import random
 import subprocess
 
 import pytest
@@ -105,3 +106,73 @@ def test_pools_that_are_written_have_a_place_for_every_element(L, strides):  # n
     one = pools(page_size=8, num_pages=1, heads=1, slot_bytes=32, page_stride=0, head_stride=16,
                 slot_stride=32)
     assert L.spec_pages_copy(ctypes.byref(one), a[0], 3, None) not in (-1, -2)
+
+
+LAYOUTS = [(32, 16, 2), (64, 16, 2), (64, 32, 4), (64, 2, 8), (512, 128, 16)]
+
+
+@host_only
+@pytest.mark.parametrize("strides", LAYOUTS, ids=str)
+def test_pools_that_share_memory_are_refused(L, strides):  # noqa: F811
+    """Pools of one layout, some of them between each other's elements, against their
+    elements listed."""
+    page, head, slot = strides
+    rng = random.Random(page)
+    mine = span((3, 2, 8), strides, 2)
+    a = [P(n << 32) for n in range(1, 6)]
+    layout = dict(page_size=8, num_pages=3, heads=2, slot_bytes=32, page_stride=16 * page,
+                  head_stride=16 * head, slot_stride=16 * slot)
+    seen = set()
+    # apart by every distance that matters
+    for d in list(range(0, max(mine) + 3)):
+        meet = any(x + d in mine for x in mine)
+        seen.add(meet)
+        for bases in ((FAR, FAR + 16 * d), (FAR + 16 * d, FAR)):
+            p = pools(bases=bases, **layout)
+            got = L.spec_cache_keep(ctypes.byref(p), a[0], 5, a[1], a[2], a[3], 2, 4, a[4], None)
+            assert got == -1 if meet else got not in (-1, -2), d
+            copy = L.spec_pages_copy(ctypes.byref(p), a[0], 3, None)
+            # a pool given twice is copied to twice, alike
+            assert copy == -1 if meet and d else copy not in (-1, -2), d
+            c = cache(keys=bases[0], values=bases[1], page_size=8, num_pages=3, kv_heads=2, dim=16,
+                      page_stride=8 * page, head_stride=8 * head, slot_stride=8 * slot)
+            got = L.spec_cache_append(ctypes.byref(c), a[0], a[1], 1024, 512, 64, 3, None, None)
+            assert got == -1 if meet else got not in (-1, -2), d
+    assert True in seen
+    # several at once, in any order
+    for _ in range(300):
+        at = [rng.randrange(0, 3 * max(mine)) for _ in range(rng.randint(2, 6))]
+        if rng.random() < 0.5:
+            at = [slot // 2 * 2 * rng.randrange(0, 64) + rng.choice((0, 0, 2)) for _ in at]
+        used = [x + b for b in at for x in mine]
+        p = pools(bases=[FAR + 16 * b for b in at], **layout)
+        got = L.spec_cache_keep(ctypes.byref(p), a[0], 5, a[1], a[2], a[3], 2, 4, a[4], None)
+        if len(set(used)) < len(used):
+            assert got == -1, at
+        else:
+            assert got not in (-1, -2), at
+
+
+@host_only
+@pytest.mark.parametrize("axis", ["apart", "pages", "slots"])
+def test_many_pools_of_one_tensor(L, axis):  # noqa: F811
+    """All layers' pools in one allocation: one behind the other, or within each page
+    or slot; then one of them once more."""
+    n, unit = 1500, 2 * 8 * 32
+    layout = dict(page_size=8, num_pages=3, heads=2, slot_bytes=32, head_stride=8 * 32, slot_stride=32)
+    if axis == "apart":
+        layout.update(page_stride=unit)
+        bases = [FAR + 3 * unit * i for i in range(n)]
+    elif axis == "pages":
+        layout.update(page_stride=unit * n)
+        bases = [FAR + unit * i for i in range(n)]
+    else:
+        layout.update(slot_stride=64 * n, head_stride=32, page_stride=8 * 64 * n)
+        bases = [FAR + 64 * i for i in range(n)]
+    random.Random(1).shuffle(bases)
+    a = [P(m << 32) for m in range(1, 6)]
+    for k in (2, 130, n):
+        for extra, bad in (((), False), ((bases[0],), True), ((bases[1] + 16,), True)):
+            p = pools(bases=tuple(bases[:k]) + extra, **layout)
+            got = L.spec_cache_keep(ctypes.byref(p), a[0], 5, a[1], a[2], a[3], 2, 4, a[4], None)
+            assert (got == -1) if bad else got not in (-1, -2), (k, extra)
