@@ -56,6 +56,21 @@ Range range(const void *p, int64_t bytes) {
     return Range{c, c + bytes};
 }
 
+Range ints(const int32_t *p, int64_t n) { return range(p, p ? n * 4 : 0); }
+
+// Whether something that is written meets something that is read, or another that is
+// written.
+template <int W, int R>
+bool writes_meet(const Range (&to)[W], const Range (&in)[R]) {
+    for (int i = 0; i < W; ++i) {
+        for (int j = 0; j < i; ++j)
+            if (to[i].meets(to[j])) return true;
+        for (const Range &r : in)
+            if (to[i].meets(r)) return true;
+    }
+    return false;
+}
+
 // Strides, and counts times them, that keep the address arithmetic far from 2^63.
 constexpr int64_t kMaxStride = int64_t{1} << 40, kMaxSpan = int64_t{1} << 56;
 bool span_ok(int64_t n, int64_t stride) { return stride < 1 || n <= kMaxSpan / stride; }
@@ -79,6 +94,10 @@ spec_status check_cache(const spec_cache *c) {
 }
 
 // The bytes from a pool's base to its last element's end.
+int64_t pool_bytes(const spec_cache_pools *p) {
+    return (p->num_pages - 1) * p->page_stride + (p->heads - 1) * p->head_stride +
+           (p->page_size - 1) * p->slot_stride + p->slot_bytes;
+}
 int64_t pool_bytes(const spec_cache *c) {
     return ((c->num_pages - 1) * c->page_stride + (c->kv_heads - 1) * c->head_stride +
             (c->page_size - 1) * c->slot_stride + c->dim) *
@@ -330,21 +349,22 @@ spec_status spec_tree_attention(const spec_cache *cache, const void *q, int64_t 
     if (cache->batch == 0) return SPEC_OK;
     if (!pools_ok(cache) || !q || !aligned16(q) || !out || !aligned16(out)) return SPEC_ERR_ARG;
     const int64_t rows = static_cast<int64_t>(cache->batch) * nodes * heads;
-    const Range to = range(out, rows * cache->dim * e);
-    const Range sums = range(lse, lse ? rows * static_cast<int64_t>(sizeof(float)) : 0);
-    const Range in[] = {
-        range(cache->keys, pool_bytes(cache)), range(cache->values, pool_bytes(cache)),
-        range(q, ((cache->batch - 1) * q_batch_stride + (nodes - 1) * q_node_stride +
-                  (heads - 1) * q_head_stride + cache->dim) *
-                     e)};
-    for (const Range &r : in)
-        if (to.meets(r) || (lse && sums.meets(r))) return SPEC_ERR_ARG;
-    if (lse && to.meets(sums)) return SPEC_ERR_ARG;
     const TreePlan p = plan_tree(cache, nodes, heads);
     if (!grid_fits(static_cast<int64_t>(p.slices) * cache->kv_heads * p.mtiles, kTreeBlock))
         return SPEC_ERR_UNSUPPORTED;
     if (p.total > 0 && (!workspace || workspace_bytes < p.total)) return SPEC_ERR_WORKSPACE;
     if (!aligned16(workspace)) return SPEC_ERR_ARG;
+    const int64_t batch = cache->batch;
+    const Range to[] = {range(out, rows * cache->dim * e), range(lse, lse ? rows * 4 : 0),
+                        range(workspace, static_cast<int64_t>(p.total))};
+    const Range in[] = {
+        range(cache->keys, pool_bytes(cache)), range(cache->values, pool_bytes(cache)),
+        range(q, ((batch - 1) * q_batch_stride + (nodes - 1) * q_node_stride +
+                  (heads - 1) * q_head_stride + cache->dim) *
+                     e),
+        ints(cache->table, batch * cache->table_width), ints(cache->lengths, batch),
+        ints(parents, batch * nodes), ints(num_nodes, batch)};
+    if (writes_meet(to, in)) return SPEC_ERR_ARG;
     char *w = static_cast<char *>(workspace);
     TreeArgs a{};
     a.keys = cache->keys;
@@ -422,8 +442,12 @@ spec_status spec_cache_append(const spec_cache *cache, const void *k, const void
                          e;
     const Range pools[] = {range(cache->keys, pool_bytes(cache)),
                            range(cache->values, pool_bytes(cache))};
-    for (const Range &r : pools)
-        if (r.meets(range(k, span)) || r.meets(range(v, span))) return SPEC_ERR_ARG;
+    const int64_t batch = cache->batch;
+    const Range in[] = {range(k, span), range(v, span),
+                        ints(cache->table, batch * cache->table_width),
+                        ints(cache->lengths, batch), ints(num_nodes, batch)};
+    for (const Range &r : in)
+        if (pools[0].meets(r) || pools[1].meets(r)) return SPEC_ERR_ARG;
     AppendArgs a{};
     a.k = static_cast<const char *>(k);
     a.v = static_cast<const char *>(v);
@@ -462,6 +486,17 @@ spec_status spec_tree_accept(const int32_t *parents, const int32_t *tokens,
     if (nodes > kMaxAcceptNodes) return SPEC_ERR_UNSUPPORTED;
     if (batch == 0) return SPEC_OK;
     if (!parents || !tokens || !chosen || !path || !count || !emitted) return SPEC_ERR_ARG;
+    // a sequence's row is read before it is written, so an output may be an input
+    const int64_t row = int64_t{batch} * nodes;
+    const Range to[] = {ints(path, row), ints(emitted, row), ints(count, batch)};
+    const Range in[] = {ints(parents, row), ints(tokens, row), ints(chosen, row),
+                        ints(num_nodes, batch)};
+    for (int i = 0; i < 3; ++i) {
+        for (int j = 0; j < i; ++j)
+            if (to[i].meets(to[j])) return SPEC_ERR_ARG;
+        for (const Range &r : in)
+            if (to[i].meets(r) && !(to[i].from == r.from && to[i].to == r.to)) return SPEC_ERR_ARG;
+    }
     AcceptArgs a{};
     a.parents = parents;
     a.tokens = tokens;
@@ -491,11 +526,16 @@ spec_status spec_cache_keep(const spec_cache_pools *pools, const int32_t *table,
     if (nodes > kMaxKeepNodes) return SPEC_ERR_UNSUPPORTED;
     if (batch == 0) return SPEC_OK;
     if (!table || !lengths || !path || !count || !new_lengths) return SPEC_ERR_ARG;
-    const Range to = range(new_lengths, int64_t{batch} * 4);
-    if (to.meets(range(lengths, int64_t{batch} * 4)) || to.meets(range(count, int64_t{batch} * 4)) ||
-        to.meets(range(path, int64_t{batch} * nodes * 4)) ||
-        to.meets(range(table, int64_t{batch} * table_width * 4)))
-        return SPEC_ERR_ARG;
+    const Range to[] = {ints(new_lengths, batch)};
+    const Range in[] = {ints(lengths, batch), ints(count, batch), ints(path, int64_t{batch} * nodes),
+                        ints(table, int64_t{batch} * table_width)};
+    if (writes_meet(to, in)) return SPEC_ERR_ARG;
+    for (int i = 0; i < pools->num_pools; ++i) {
+        const Range pool = range(pools->bases[i], pool_bytes(pools));
+        for (const Range &r : in)
+            if (pool.meets(r)) return SPEC_ERR_ARG;
+        if (pool.meets(to[0])) return SPEC_ERR_ARG;
+    }
     KeepArgs a{};
     a.table = table;
     a.lengths = lengths;
@@ -532,14 +572,10 @@ spec_status spec_pages_fork(const int32_t *table, const int32_t *lengths, const 
     const int64_t rows = static_cast<int64_t>(batch) * num_out;
     const int64_t from = static_cast<int64_t>(batch) * num_beams;
     if (!grid_fits(rows, kCacheBlock) || from > INT32_MAX) return SPEC_ERR_UNSUPPORTED;
-    const Range to[] = {range(out_table, rows * table_width * 4), range(out_lengths, rows * 4),
-                        range(refs, int64_t{num_pages} * 4)};
-    const Range in[] = {range(table, from * table_width * 4), range(lengths, from * 4),
-                        range(parents, rows * 4)};
-    for (const Range &t : to)
-        for (const Range &i : in)
-            if (t.meets(i)) return SPEC_ERR_ARG;
-    if (to[0].meets(to[1]) || to[0].meets(to[2]) || to[1].meets(to[2])) return SPEC_ERR_ARG;
+    const Range to[] = {ints(out_table, rows * table_width), ints(out_lengths, rows),
+                        ints(refs, num_pages)};
+    const Range in[] = {ints(table, from * table_width), ints(lengths, from), ints(parents, rows)};
+    if (writes_meet(to, in)) return SPEC_ERR_ARG;
     ForkArgs a{};
     a.table = table;
     a.lengths = lengths;
@@ -566,6 +602,9 @@ spec_status spec_pages_release(int32_t *table, const int32_t *lengths, int32_t r
     if (rows == 0) return SPEC_OK;
     if (!table || !refs) return SPEC_ERR_ARG;
     if (!grid_fits(rows, kCacheBlock)) return SPEC_ERR_UNSUPPORTED;
+    const Range to[] = {ints(table, int64_t{rows} * table_width), ints(refs, num_pages)};
+    const Range in[] = {ints(lengths, rows)};
+    if (writes_meet(to, in)) return SPEC_ERR_ARG;
     ReleaseArgs a{};
     a.table = table;
     a.refs = refs;
@@ -595,9 +634,14 @@ spec_status spec_pages_reserve(int32_t *table, const int32_t *lengths,
     if (rows > kMaxReserveRows || num_pages > kMaxReservePages) return SPEC_ERR_UNSUPPORTED;
     if (rows == 0) return SPEC_OK;
     if (!table || !lengths || !new_positions || !refs || !copies || !missing) return SPEC_ERR_ARG;
-    if (!workspace || workspace_bytes < plan_reserve(num_pages).total)
-        return SPEC_ERR_WORKSPACE;
+    const ReservePlan p = plan_reserve(num_pages);
+    if (!workspace || workspace_bytes < p.total) return SPEC_ERR_WORKSPACE;
     if (!aligned16(workspace)) return SPEC_ERR_ARG;
+    const Range to[] = {ints(table, int64_t{rows} * table_width), ints(refs, num_pages),
+                        ints(copies, int64_t{rows} * 3), ints(missing, 1),
+                        range(workspace, static_cast<int64_t>(p.total))};
+    const Range in[] = {ints(lengths, rows), ints(new_positions, rows)};
+    if (writes_meet(to, in)) return SPEC_ERR_ARG;
     char *w = static_cast<char *>(workspace);
     ReserveArgs a{};
     a.table = table;
@@ -606,7 +650,6 @@ spec_status spec_pages_reserve(int32_t *table, const int32_t *lengths,
     a.missing = missing;
     a.lengths = lengths;
     a.news = new_positions;
-    const ReservePlan p = plan_reserve(num_pages);
     a.words = reinterpret_cast<unsigned long long *>(w + p.words);
     a.before = reinterpret_cast<int32_t *>(w + p.before);
     a.counts = reinterpret_cast<int32_t *>(w + p.counts);
@@ -634,6 +677,9 @@ spec_status spec_pages_copy(const spec_cache_pools *pools, const int32_t *copies
     if (rows < 0) return SPEC_ERR_ARG;
     if (rows == 0 || pools->num_pools == 0) return SPEC_OK;
     if (!copies) return SPEC_ERR_ARG;
+    for (int i = 0; i < pools->num_pools; ++i)
+        if (range(pools->bases[i], pool_bytes(pools)).meets(ints(copies, int64_t{rows} * 3)))
+            return SPEC_ERR_ARG;
     CopyArgs a{};
     a.copies = copies;
     const int step = copy_pools_per_launch(rows, pools->heads, pools->num_pools);

@@ -605,6 +605,10 @@ spec_status spec_beam_reorder(const int32_t *parents, const int32_t *lengths, in
  * * page_size <= 2^30, else SPEC_ERR_UNSUPPORTED.  So is what a launch's grid does
  * not hold, 2^24 workgroups of 256 threads: rows for forking and releasing, rows *
  * heads for copying, and batch * heads * slot_bytes / 4096 for keeping.
+ *
+ * What a call writes, its workspace among it, overlaps nothing else that it is
+ * given, else SPEC_ERR_ARG (spec_tree_accept says what it allows).  A pool counts
+ * from its first element to its last.
  */
 typedef struct spec_cache {
     void *keys;           /* device, 16-byte aligned                          */
@@ -644,7 +648,7 @@ typedef struct spec_cache {
  * counts as nothing), has out 0 and lse -inf.  Sums and products are taken in
  * 32 bits; for 16-bit types the weights are rounded to the type before their
  * product with the values (float16: those below 2^-23 of a row's largest to a
- * multiple of at most 2^-33 of it).  out and lse overlap no input.  workspace: device,
+ * multiple of at most 2^-33 of it).  workspace: device,
  * spec_tree_attention_workspace_bytes (0, and then NULL will do, for tables of
  * few positions; 0 too if the arguments are not valid), 16-byte aligned; its
  * contents on entry do not matter.
@@ -684,6 +688,7 @@ spec_status spec_cache_append(const spec_cache *cache, const void *k, const void
  * ascending; count [batch], how many (0 for a sequence without nodes);
  * emitted [batch][nodes], the accepted children's tokens and then the target's
  * choice after the last one; path and emitted hold count[b] entries, then -1.
+ * An output may be an input of its shape itself (in place).
  * 1 <= nodes <= 128, else SPEC_ERR_UNSUPPORTED.
  */
 spec_status spec_tree_accept(const int32_t *parents, const int32_t *tokens,
@@ -713,7 +718,7 @@ typedef struct spec_cache_pools {
  * to lengths[b] + i for i < count[b].  path: device int32 [batch][nodes],
  * ascending within [0, nodes) as spec_tree_accept gives it (the first entry
  * that is not ends the list); count: device int32 [batch].  new_lengths
- * (device int32 [batch], apart from the inputs): lengths[b] plus the entries
+ * (device int32 [batch]): lengths[b] plus the entries
  * kept, at most what the table row can hold.  A move from or to a position
  * without a page is left out.  Rows of a table that share a page must not both
  * move into it.  nodes <= 1024.
@@ -735,7 +740,7 @@ spec_status spec_cache_keep(const spec_cache_pools *pools, const int32_t *table,
  * that hold its lengths[b][w] positions, then -1; their refs go up by one each;
  * out_lengths[b][i] = lengths[b][w].  A parent outside [0, num_beams) gives
  * an empty row of length 0.  What out_table's rows listed before is
- * overwritten, not released.  Outputs overlap no input.
+ * overwritten, not released.
  */
 spec_status spec_pages_fork(const int32_t *table, const int32_t *lengths, const int32_t *parents,
                             int32_t batch, int32_t num_beams, int32_t num_out,

@@ -176,3 +176,116 @@ def test_many_pools_of_one_tensor(L, axis):  # noqa: F811
             p = pools(bases=tuple(bases[:k]) + extra, **layout)
             got = L.spec_cache_keep(ctypes.byref(p), a[0], 5, a[1], a[2], a[3], 2, 4, a[4], None)
             assert (got == -1) if bad else got not in (-1, -2), (k, extra)
+
+
+def places(sizes, start=1 << 40):
+    """Addresses of buffers one behind the other, with no gap."""
+    at = {}
+    for name, size in sizes.items():
+        at[name] = start
+        start += -(-size // 256) * 256
+    return at
+
+
+def overlapping(call, sizes, written, allowed=()):
+    """call(addresses) is refused where a buffer that is written to overlaps another, by
+    its first byte or its last, and only there."""
+    at = places(sizes)
+    assert call(at) not in (-1, -2, -3)
+    for w in written:
+        for other in sizes:
+            if other == w or (w, other) in allowed or (other, w) in allowed:
+                continue
+            for move in (at[other] + sizes[other] // 16 * 16 - (sizes[other] % 16 == 0) * 16,
+                         at[other] - (sizes[w] - 1) // 16 * 16):
+                assert call(dict(at, **{w: move})) == -1, (w, other)
+
+
+@host_only
+def test_attention_writes_over_nothing(L):  # noqa: F811
+    B, T, H, width = 2, 3, 8, 65
+    pool = (9 * 4096 + 3 * 1024 + 15 * 64 + 64) * 2
+    need = L.spec_tree_attention_workspace_bytes(ctypes.byref(cache(table_width=width)), T, H)
+    sizes = dict(keys=pool, values=pool, table=B * width * 4, lengths=B * 4, q=B * T * H * 64 * 2,
+                 parents=B * T * 4, nodes=B * 4, out=B * T * H * 64 * 2, lse=B * T * H * 4,
+                 workspace=need)
+
+    def call(at):
+        c = cache(keys=at["keys"], values=at["values"], table=at["table"], lengths=at["lengths"],
+                  table_width=width)
+        return L.spec_tree_attention(ctypes.byref(c), P(at["q"]), T * H * 64, H * 64, 64, T, H,
+                                     P(at["parents"]), P(at["nodes"]), 1.0, P(at["out"]),
+                                     P(at["lse"]), P(at["workspace"]), need, None)
+    overlapping(call, sizes, ("out", "lse", "workspace"))
+
+
+@host_only
+def test_append_and_keep_and_copy_write_over_nothing(L):  # noqa: F811
+    B, T, width = 2, 3, 5
+    pool = (9 * 4096 + 3 * 1024 + 15 * 64 + 64) * 2
+    rows = (1024 + 2 * 512 + 3 * 64 + 64) * 2
+    sizes = dict(keys=pool, values=pool, table=B * width * 4, lengths=B * 4, nodes=B * 4, k=rows,
+                 v=rows)
+
+    def append(at):
+        c = cache(**{k: at[k] for k in ("keys", "values", "table", "lengths")})
+        return L.spec_cache_append(ctypes.byref(c), P(at["k"]), P(at["v"]), 1024, 512, 64, T,
+                                   P(at["nodes"]), None)
+    overlapping(append, sizes, ("keys", "values"), allowed=[("keys", "values")])
+
+    pool = 9 * 4096 + 2048 + 15 * 128 + 128
+    sizes = dict(a=pool, b=pool, table=B * width * 4, lengths=B * 4, path=B * T * 4, count=B * 4,
+                 new=B * 4)
+
+    def keep(at):
+        p = pools(bases=(at["a"], at["b"]))
+        return L.spec_cache_keep(ctypes.byref(p), P(at["table"]), width, P(at["lengths"]),
+                                 P(at["path"]), P(at["count"]), B, T, P(at["new"]), None)
+    overlapping(keep, sizes, ("a", "b", "new"), allowed=[("a", "b")])
+
+    def copy(at):
+        p = pools(bases=(at["a"], at["b"]))
+        return L.spec_pages_copy(ctypes.byref(p), P(at["copies"]), 7, None)
+    overlapping(copy, dict(a=pool, b=pool, copies=84), ("a", "b"), allowed=[("a", "b")])
+
+
+@host_only
+def test_accept_writes_over_nothing_but_in_place(L):  # noqa: F811
+    B, T = 3, 8
+    row = B * T * 4
+    sizes = dict(parents=row, tokens=row, chosen=row, nodes=B * 4, path=row, count=B * 4, emitted=row)
+
+    def call(at):
+        names = ("parents", "tokens", "chosen", "nodes")
+        return L.spec_tree_accept(*[P(at[n]) for n in names], B, T, P(at["path"]), P(at["count"]),
+                                  P(at["emitted"]), None)
+    overlapping(call, sizes, ("path", "count", "emitted"), allowed=[("count", "nodes")])
+    # a row is read as a whole before it is written
+    at = places(sizes)
+    for new in ("path", "emitted"):
+        for old in ("parents", "tokens", "chosen"):
+            assert call(dict(at, **{new: at[old]})) not in (-1, -2)
+    assert call(dict(at, count=at["nodes"])) not in (-1, -2)
+    assert call(dict(at, path=at["emitted"])) == -1
+
+
+@host_only
+def test_page_calls_write_over_nothing(L):  # noqa: F811
+    R, width, N = 3, 5, 40
+    sizes = dict(table=R * width * 4, refs=N * 4, lengths=R * 4)
+
+    def release(at):
+        return L.spec_pages_release(P(at["table"]), P(at["lengths"]), R, width, 16, N, P(at["refs"]),
+                                    None)
+    overlapping(release, sizes, ("table", "refs"))
+    need = L.spec_pages_reserve_workspace_bytes(R, N)
+    sizes.update(new=R * 4, copies=R * 12, missing=4, workspace=need)
+
+    def reserve(at):
+        return L.spec_pages_reserve(P(at["table"]), P(at["lengths"]), P(at["new"]), R, width, 16, N,
+                                    P(at["refs"]), P(at["copies"]), P(at["missing"]),
+                                    P(at["workspace"]), need, None)
+    overlapping(reserve, sizes, ("table", "refs", "copies", "missing", "workspace"))
+    # inputs may be one and the same
+    at = places(sizes)
+    assert reserve(dict(at, new=at["lengths"])) not in (-1, -2, -3)
