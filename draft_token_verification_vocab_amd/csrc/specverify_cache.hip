@@ -25,7 +25,6 @@ constexpr int kUnits = 256;            // compute units
 constexpr int kMaxChainNodes = 65536;
 constexpr int kMaxHeads = 65535;
 constexpr int kMaxRoom = 1 << 30;      // positions that a table row can hold
-constexpr int kMaxReserveRows = 65536;
 
 int page_shift(int32_t page_size) {
     int s = 0;

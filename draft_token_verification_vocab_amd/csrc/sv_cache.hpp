@@ -278,7 +278,8 @@ __global__ __launch_bounds__(kCacheBlock) void pages_release_kernel(ReleaseArgs 
 // many as the widest row needs.  Shared pages among them are settled in the
 // pages' own counts: every entry takes its reference off; a page that has none
 // left then has all its holders here, and the lowest row among them, found by a
-// minimum over row - 2^30, keeps it.
+// minimum over row - 2^30, keeps it, with the first entry that lists the page where
+// the row does so more than once.
 //
 // Where the rows fit the workgroup, an entry to a thread (a step of decoding),
 // entries stay in registers (four rows in 4096 pages 7.3 us, 512 rows in 40000 pages
@@ -290,6 +291,7 @@ constexpr int kReserveBlock = 1024;
 constexpr int kPageChunk = 1024;                   // pages to a count
 constexpr int kChunkWords = kPageChunk / kWave;
 constexpr int kMaxReservePages = 1 << 22;
+constexpr int kMaxReserveRows = 65536;
 constexpr int kKeeper = 1 << 30;
 constexpr int kSharedMark = -2147483647 - 1;
 // Chunks that the workgroup looks through by itself.  In a graph 4 take 6.2 us and 7.2
@@ -376,11 +378,12 @@ __device__ __forceinline__ int free_page(const ReserveArgs &a, const int *before
 __global__ __launch_bounds__(kReserveBlock) void pages_reserve_kernel(ReserveArgs a) {
     __shared__ int sh_before[kMaxReservePages / kPageChunk];
     __shared__ int sh_scan[kReserveBlock / kWave];
-    __shared__ int sh_widest, sh_over;
+    __shared__ int sh_widest, sh_over, sh_twice;
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     if (tid == 0) {
         sh_widest = 1;
         sh_over = 0;
+        sh_twice = 0;
     }
     const int room = a.P << a.shift, page_size = 1 << a.shift;
     // the table entries [lo, hi) that row r is about to write (hi -1: too many)
@@ -445,9 +448,10 @@ __global__ __launch_bounds__(kReserveBlock) void pages_reserve_kernel(ReserveArg
         if (__syncthreads_or(shared)) {
             if (shared) atomicSub(&a.refs[e], 1);
             __syncthreads();
-            if (shared && atomicAdd(&a.refs[e], 0) <= 0) atomicMin(&a.refs[e], r - kKeeper);
+            // threads are in the entries' order
+            if (shared && atomicAdd(&a.refs[e], 0) <= 0) atomicMin(&a.refs[e], tid - kKeeper);
             __syncthreads();
-            if (shared) stays = atomicAdd(&a.refs[e], 0) + kKeeper == r;
+            if (shared) stays = atomicAdd(&a.refs[e], 0) + kKeeper == tid;
         }
         const bool fresh = mine && (!held || (shared && !stays));
         int total;
@@ -478,6 +482,19 @@ __global__ __launch_bounds__(kReserveBlock) void pages_reserve_kernel(ReserveArg
 
     const uint64_t below = (group == kWave ? ~0ull : ((1ull << group) - 1))
                            << (lane & ~(group - 1));
+    // what a page's count says once row r is to keep it, and once an entry of it does
+    auto keeper = [](int r) { return r - kKeeper; };
+    auto claimed = [](int r) { return r - kKeeper - kMaxReserveRows; };
+    // whether the marked entry i of row r, which begins at lo, keeps its page (after
+    // phase 3)
+    auto keeps = [&](const int32_t *row, int lo, int i, int r) {
+        const int e = row[i];
+        if (atomicAdd(&a.refs[e - kSharedMark], 0) != claimed(r)) return false;
+        if (sh_twice)
+            for (int j = lo; j < i; ++j)
+                if (row[j] == e) return false;
+        return true;
+    };
     int need = 0;
     // phase 0 marks shared entries, 1 takes their references off, 2 finds who
     // keeps, 3 counts what is needed
@@ -498,8 +515,12 @@ __global__ __launch_bounds__(kReserveBlock) void pages_reserve_kernel(ReserveArg
                 } else if (is_mark(e)) {
                     int *ref = &a.refs[e - kSharedMark];
                     if (phase == 1) atomicSub(ref, 1);
-                    if (phase == 2 && atomicAdd(ref, 0) <= 0) atomicMin(ref, r - kKeeper);
-                    if (phase == 3) need += atomicAdd(ref, 0) + kKeeper != r;
+                    if (phase == 2 && atomicAdd(ref, 0) <= 0) atomicMin(ref, keeper(r));
+                    if (phase == 3) {
+                        const int v = atomicCAS(ref, keeper(r), claimed(r));
+                        if (v == claimed(r)) sh_twice = 1;  // the row lists it again
+                        need += v != keeper(r);
+                    }
                 } else if (phase == 3) {
                     need += !is_page(e);
                 }
@@ -526,7 +547,7 @@ __global__ __launch_bounds__(kReserveBlock) void pages_reserve_kernel(ReserveArg
                     if (!is_mark(e)) continue;
                     int *ref = &a.refs[e - kSharedMark];
                     if (phase == 0) {
-                        if (atomicAdd(ref, 0) + kKeeper == r) atomicExch(ref, 0);
+                        if (atomicAdd(ref, 0) == claimed(r)) atomicExch(ref, 0);
                     } else {
                         atomicAdd(ref, 1);
                         row[i] = e - kSharedMark;
@@ -546,7 +567,7 @@ __global__ __launch_bounds__(kReserveBlock) void pages_reserve_kernel(ReserveArg
         int32_t *row = a.table + static_cast<int64_t>(r) * a.P;
         auto fresh = [&](int i, int &e) {
             e = i < hi ? row[i] : 0;
-            if (is_mark(e)) return atomicAdd(&a.refs[e - kSharedMark], 0) + kKeeper != r;
+            if (is_mark(e)) return !keeps(row, lo, i, r);
             return !is_page(e);
         };
         int mine = 0, e;
