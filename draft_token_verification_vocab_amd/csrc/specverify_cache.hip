@@ -45,10 +45,12 @@ spec_status check_table(int32_t table_width, int32_t page_size, int32_t num_page
 // A stride of n elements of e bytes: looked at before it is multiplied, which may wrap.
 bool stride_ok(int64_t n, int e) { return n >= 0 && n % (16 / e) == 0; }
 
-// Addresses [from, to).
+// Addresses [from, to); an empty range meets nothing.
 struct Range {
     const char *from, *to;
-    bool meets(const Range &o) const { return from < o.to && o.from < to; }
+    bool meets(const Range &o) const {
+        return from < o.to && o.from < to && from < to && o.from < o.to;
+    }
 };
 Range range(const void *p, int64_t bytes) {
     const char *c = static_cast<const char *>(p);

@@ -289,3 +289,12 @@ def test_page_calls_write_over_nothing(L):  # noqa: F811
     # inputs may be one and the same
     at = places(sizes)
     assert reserve(dict(at, new=at["lengths"])) not in (-1, -2, -3)
+
+
+@host_only
+def test_an_empty_workspace_is_nowhere(L):  # noqa: F811
+    """A table of few positions needs none, whatever it points to."""
+    c = cache(keys=1 << 40, values=1 << 41)
+    for at in (None, P((1 << 42) + 16), P((1 << 40) + 16), P(FAR + 16)):
+        assert L.spec_tree_attention(ctypes.byref(c), P(1 << 42), 3 * 8 * 64, 8 * 64, 64, 3, 8, None,
+                                     None, 1.0, P(FAR), None, at, 0, None) not in (-1, -2, -3)
