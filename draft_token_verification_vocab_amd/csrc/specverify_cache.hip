@@ -339,7 +339,7 @@ spec_status spec_tree_attention(const spec_cache *cache, const void *q, int64_t 
                                 size_t workspace_bytes, void *stream) {
     const spec_status s = check_tree(cache, nodes, heads, parents != nullptr);
     if (s != SPEC_OK) return s;
-    if (!(scale > 0.0f) || !std::isfinite(scale)) return SPEC_ERR_ARG;
+    if (!(scale > 0.0f) || !std::isfinite(scale * kLog2e)) return SPEC_ERR_ARG;
     const int e = elem_size(cache->dtype);
     if (q_batch_stride > kMaxStride || q_node_stride > kMaxStride ||
         q_head_stride > kMaxStride || !span_ok(cache->batch, q_batch_stride))

@@ -640,7 +640,7 @@ typedef struct spec_cache {
  *            (elements; multiples of 16 bytes, >= 0; q 16-byte aligned).
  *   parents  device int32 [batch][nodes], or NULL for a chain.  A tree has at
  *            most 128 nodes, a chain at most 65536, else SPEC_ERR_UNSUPPORTED.
- *   scale    finite and > 0.
+ *   scale    > 0; it and scale / ln 2 are finite.
  *   16-bit slots lie at most 2^28 elements apart, else SPEC_ERR_UNSUPPORTED.
  *   out      device [batch][nodes][heads][dim], cache->dtype, 16-byte aligned.
  *   lse      device float [batch][nodes][heads] or NULL.

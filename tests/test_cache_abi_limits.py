@@ -298,3 +298,13 @@ def test_an_empty_workspace_is_nowhere(L):  # noqa: F811
     for at in (None, P((1 << 42) + 16), P((1 << 40) + 16), P(FAR + 16)):
         assert L.spec_tree_attention(ctypes.byref(c), P(1 << 42), 3 * 8 * 64, 8 * 64, 64, 3, 8, None,
                                      None, 1.0, P(FAR), None, at, 0, None) not in (-1, -2, -3)
+
+
+@host_only
+def test_scales_whose_powers_of_two_overflow_are_refused(L):  # noqa: F811
+    """The kernels take scale / ln 2, which has to be finite as well."""
+    c = cache(keys=1 << 40, values=1 << 41)
+    for scale, fine in ((2.3e38, True), (2.4e38, False), (3.4e38, False), (1e-45, True)):
+        got = L.spec_tree_attention(ctypes.byref(c), P(1 << 42), 3 * 8 * 64, 8 * 64, 64, 3, 8, None,
+                                    None, scale, P(FAR), None, None, 0, None)
+        assert (got not in (-1, -2, -3)) if fine else got == -1
