@@ -1053,6 +1053,10 @@ def _same_layout(t, u):
             and (t.stride() == u.stride() or list(_strides(t)) == list(_strides(u))))
 
 
+def _no_cache_dtype(keys):
+    raise TypeError("keys and values must be float32, bfloat16 or float16, got %s" % keys.dtype)
+
+
 def _cache(keys, values, table, lengths):
     """(the checked _Cache of two pools [pages, heads, page, dim] and a table [B, P],
     the GPU's index)."""
@@ -1066,7 +1070,7 @@ def _cache(keys, values, table, lengths):
             and values.get_device() == index) and not _same_layout(values, keys):
         raise ValueError("values must be laid out as keys, on the same device")
     if code is None:
-        raise TypeError("keys and values must be float32, bfloat16 or float16, got %s" % keys.dtype)
+        _no_cache_dtype(keys)
     at = table.shape
     if len(at) != 2:
         raise ValueError("table must be [B, pages of a sequence]")
@@ -1109,9 +1113,11 @@ def tree_workspace_bytes(q: torch.Tensor, keys: torch.Tensor, table: torch.Tenso
     shapes, types and strides (0: none), whatever the lengths.  Calls that may run at
     the same time need workspaces of their own; those in stream order may share one."""
     N, kv, page, D = keys.shape
-    return _tree_workspace_bytes(table.shape[0], table.shape[1], page, kv, D,
-                                 _CACHE_DTYPES[keys.dtype], q.shape[1], q.shape[2],
-                                 _strides(keys)[2])
+    code = _CACHE_DTYPES.get(keys.dtype)
+    if code is None:
+        _no_cache_dtype(keys)
+    return _tree_workspace_bytes(table.shape[0], table.shape[1], page, kv, D, code, q.shape[1],
+                                 q.shape[2], _strides(keys)[2])
 
 
 def tree_attention(q: torch.Tensor, keys: torch.Tensor, values: torch.Tensor, table: torch.Tensor,

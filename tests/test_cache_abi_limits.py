@@ -7,6 +7,7 @@ import random
 import subprocess
 
 import pytest
+import torch
 
 import draft_token_verification_vocab_amd as sv
 from test_cache_abi import FAR, L, P, cache, host_only, pools  # noqa: F401
@@ -308,3 +309,10 @@ def test_scales_whose_powers_of_two_overflow_are_refused(L):  # noqa: F811
         got = L.spec_tree_attention(ctypes.byref(c), P(1 << 42), 3 * 8 * 64, 8 * 64, 64, 3, 8, None,
                                     None, scale, P(FAR), None, None, 0, None)
         assert (got not in (-1, -2, -3)) if fine else got == -1
+
+
+def test_workspace_sizes_of_types_without_a_kernel():
+    keys = torch.empty(4, 2, 16, 64, dtype=torch.float64)
+    q = torch.empty(3, 5, 8, 64, dtype=torch.float64)
+    with pytest.raises(TypeError, match="float64"):
+        sv.tree_workspace_bytes(q, keys, torch.empty(3, 65, dtype=torch.int32))
