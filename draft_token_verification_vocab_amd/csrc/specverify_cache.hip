@@ -22,6 +22,7 @@ namespace {
 using namespace sv;
 
 constexpr int kUnits = 256;            // compute units
+constexpr int kMaxSlices = 2 * kUnits; // runs of tiles
 constexpr int kMaxChainNodes = 65536;
 constexpr int kMaxHeads = 65535;
 constexpr int kMaxRoom = 1 << 30;      // positions that a table row can hold
@@ -154,7 +155,8 @@ spec_status check_tree(const spec_cache *c, int32_t nodes, int32_t heads, bool t
     if (c->dtype != SPEC_DTYPE_F32 && c->slot_stride > kMaxWideSlot) return SPEC_ERR_UNSUPPORTED;
     const int64_t tiles =
         (static_cast<int64_t>(c->table_width) * c->page_size + kTreeTile - 1) / kTreeTile;
-    if (c->batch > INT32_MAX / tiles) return SPEC_ERR_UNSUPPORTED;
+    // counted in 32 bits, and rounded up to whole runs
+    if (c->batch > (INT32_MAX - kMaxSlices) / tiles) return SPEC_ERR_UNSUPPORTED;
     const int64_t rows = static_cast<int64_t>(c->batch) * nodes;
     if (rows > 0 && rows > (int64_t{1} << 40) / heads) return SPEC_ERR_UNSUPPORTED;
     const int64_t joins = (static_cast<int64_t>(nodes) * heads / kTreeWaves + 1) * c->batch;

@@ -641,7 +641,9 @@ typedef struct spec_cache {
  *   parents  device int32 [batch][nodes], or NULL for a chain.  A tree has at
  *            most 128 nodes, a chain at most 65536, else SPEC_ERR_UNSUPPORTED.
  *   scale    > 0; it and scale / ln 2 are finite.
- *   16-bit slots lie at most 2^28 elements apart, else SPEC_ERR_UNSUPPORTED.
+ *   16-bit slots lie at most 2^28 elements apart, batch * nodes * heads and batch
+ *   * table_width * page_size / 128 stay below about 2^26 and 2^31 - 512, else
+ *   SPEC_ERR_UNSUPPORTED.
  *   out      device [batch][nodes][heads][dim], cache->dtype, 16-byte aligned.
  *   lse      device float [batch][nodes][heads] or NULL.
  * A node that is not in use, or that sees nothing (its scores -inf throughout

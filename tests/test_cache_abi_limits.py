@@ -316,3 +316,16 @@ def test_workspace_sizes_of_types_without_a_kernel():
     q = torch.empty(3, 5, 8, 64, dtype=torch.float64)
     with pytest.raises(TypeError, match="float64"):
         sv.tree_workspace_bytes(q, keys, torch.empty(3, 65, dtype=torch.int32))
+
+
+def test_tiles_are_counted_in_32_bits_with_room_for_rounding(L):  # noqa: F811
+    """Tiles of 128 positions are dealt out in runs rounded up, over at most 512
+    workgroups: their count stays that far from 2^31."""
+    def need(tiles, batch):
+        c = cache(kv_heads=1, page_size=128, table_width=tiles, batch=batch)
+        return L.spec_tree_attention_workspace_bytes(ctypes.byref(c), 1, 1)
+    for tiles in (129, 1000, 1 << 23):
+        fits = (2 ** 31 - 1 - 512) // tiles
+        assert need(tiles, fits) > 0, tiles
+        if fits < (2 ** 31 - 1) // tiles:
+            assert need(tiles, fits + 1) == 0, tiles
