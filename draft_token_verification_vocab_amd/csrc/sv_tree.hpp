@@ -251,6 +251,19 @@ __device__ __forceinline__ uint32_t tree_sees8(const uint64_t (*mask)[2], bool c
     return static_cast<uint32_t>(w) & 0xFFu;
 }
 
+// Where values of nodes hold an infinity or a NaN: positions [from, to), as tiles.
+struct TreeOdd {
+    int from, to;
+    __device__ __forceinline__ void clear() {
+        from = 0x7FFFFFFF;
+        to = 0;
+    }
+    __device__ __forceinline__ void add(int at, int n) {
+        atomicMin(&from, at);
+        atomicMax(&to, at + n);
+    }
+};
+
 // Queries and joined sums are not needed at the same time.
 template <int DP, int R>
 struct TreeShared {
@@ -264,7 +277,7 @@ struct TreeShared {
     };
     float ml[kTreeWaves][16 * R][2];
     int node[16 * R];  // a row's node
-    int odd;           // a node's value holds an infinity or a NaN
+    TreeOdd odd;
     uint64_t mask[kMaxTreeNodes][2];
     int up[kMaxTreeNodes];
 };
@@ -388,36 +401,81 @@ __device__ __forceinline__ void tree_masks(const TreeArgs &a, Shared &sh, int b,
 // Adds the infinities and NaNs among the values of nodes, between positions
 // `from` and `to`, to the rows that see them: a weight above 0 times one is that
 // again.  The workgroup's rows row0 .. row0 + rows - 1 have been written, to out
-// (whole) or to its part.
+// (whole) or to its part.  A thread takes a dimension and a run of rows.  Of a chain
+// it walks along the positions once, as a row sees all up to its own: a running sum
+// goes to each row in turn.  Of a tree it keeps which nodes hold what, in bits, and
+// meets them with what a row sees.
 template <typename T>
 __device__ __forceinline__ void tree_add_odd(const TreeArgs &a, const uint64_t (*mask)[2],
-                                             const TreeSpan &span, int b, int h, int from, int to,
-                                             bool whole, int64_t slot, int row0, int rows) {
+                                             const TreeOdd &odd, const TreeSpan &span, int b,
+                                             int h, int from, int to, bool whole, int64_t slot,
+                                             int row0, int rows) {
     __threadfence_block();
     __syncthreads();
-    const int32_t *table = a.table + static_cast<int64_t>(b) * a.P;
-    for (int e = threadIdx.x; e < rows * a.D; e += kTreeBlock) {
-        const int in = e / a.D, d = e % a.D, row = row0 + in, node = row / a.G;
-        if (node >= span.live) break;
-        float sum = 0.0f;
-        for (int p = from > span.cached ? from : span.cached; p < to; ++p) {
-            const int page = table[p >> a.shift];
-            if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.pages) ||
-                !tree_sees(mask, a.parents == nullptr, node, p - span.cached))
-                continue;
-            const float v = static_cast<float>(static_cast<const T *>(
-                a.values)[page * a.page_stride + h * a.head_stride +
-                          (p & ((1 << a.shift) - 1)) * a.slot_stride + d]);
-            if (!(__builtin_fabsf(v) < __builtin_inff())) sum += v;
-        }
-        if (sum == 0.0f) continue;
+    const int threads = kTreeBlock / a.D, d = threadIdx.x % a.D, k = threadIdx.x / a.D;
+    if (k >= threads) return;
+    int in = rows * k / threads, end = rows * (k + 1) / threads;
+    if (end > span.live * a.G - row0) end = span.live * a.G - row0;  // rows in use
+    if (from < span.cached) from = span.cached;
+    if (from < odd.from) from = odd.from;
+    if (to > odd.to) to = odd.to;
+    // rows of nodes before the first of them
+    const int64_t before = static_cast<int64_t>(from - span.cached) * a.G - row0;
+    if (in < before) in = before < end ? static_cast<int>(before) : end;
+    if (in >= end) return;
+    const int last = (row0 + end - 1) / a.G;
+    if (to > span.cached + last + 1) to = span.cached + last + 1;
+
+    auto add = [&](int i, float sum) {
+        const int row = row0 + i;
         if (whole) {
-            T *out = static_cast<T *>(a.out) +
-                     ((static_cast<int64_t>(b) * a.T + node) * a.H + h * a.G + row % a.G) * a.D + d;
+            T *out = static_cast<T *>(a.out) + ((static_cast<int64_t>(b) * a.T + row / a.G) * a.H +
+                                                h * a.G + row % a.G) *
+                                                   a.D + d;
             *out = static_cast<T>(static_cast<float>(*out) + sum);
         } else {
-            a.part[(slot * rows + in) * a.D + d] += sum;
+            a.part[(slot * rows + i) * a.D + d] += sum;
         }
+    };
+    const bool chain = a.parents == nullptr;
+    const int32_t *table = a.table + static_cast<int64_t>(b) * a.P;
+    float sum = 0.0f;
+    int node = (row0 + in) / a.G;
+    uint64_t up[2] = {0, 0}, down[2] = {0, 0};  // nodes of +inf or NaN, of -inf or NaN
+    for (int p0 = from & ~7; p0 < to && in < end && !(sum != sum); p0 += 8) {
+        const int page = table[p0 >> a.shift];
+        const bool held = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.pages);
+        const T *at = static_cast<const T *>(a.values) + (held ? page : 0) * a.page_stride +
+                      h * a.head_stride + (p0 & ((1 << a.shift) - 1)) * a.slot_stride + d;
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = static_cast<float>(at[j * a.slot_stride]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int n = p0 + j - span.cached;
+            if (p0 + j < from || p0 + j >= to) continue;
+            if (held && !(__builtin_fabsf(v[j]) < __builtin_inff())) {
+                sum += v[j];
+                if (!chain) {
+                    const uint64_t bit = 1ull << (n & 63);
+                    if (!(v[j] < 0.0f)) up[n >> 6] |= bit;
+                    if (!(v[j] > 0.0f)) down[n >> 6] |= bit;
+                }
+            }
+            if (!chain) continue;
+            for (; in < end && node <= n; ++in, node = (row0 + in) / a.G)
+                if (!(sum == 0.0f)) add(in, sum);
+        }
+        if (!chain) sum = 0.0f;
+    }
+    for (; in < end; ++in) {
+        if (!chain) {
+            node = (row0 + in) / a.G;
+            sum = 0.0f;
+            if ((mask[node][0] & up[0]) | (mask[node][1] & up[1])) sum += __builtin_inff();
+            if ((mask[node][0] & down[0]) | (mask[node][1] & down[1])) sum -= __builtin_inff();
+        }
+        if (!(sum == 0.0f)) add(in, sum);
     }
 }
 
@@ -560,7 +618,7 @@ __global__ __launch_bounds__(kTreeBlock, tree_waves(DP)) void tree_attention_ker
             if (k * kTreeBlock + qt < R * kSteps * kWave)
                 (&sh.q[0][0][0])[k * kTreeBlock + qt] = queries[k].w;
         if (qt < 16 * R) sh.node[qt] = mine;
-        if (qt == 0) sh.odd = 0;
+        if (qt == 0) sh.odd.clear();
         lds_barrier();
 
         float m[R], l[R];  // a row's maximum, scaled to powers of two, and the lane's sum
@@ -679,7 +737,7 @@ __global__ __launch_bounds__(kTreeBlock, tree_waves(DP)) void tree_attention_ker
                         vw[c][j][k] = w ^ out;
                     }
             }
-            if (odd) sh.odd = 1;
+            if (odd) sh.odd.add(p0, kTreeKeys);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const int node = sh.node[16 * r + i16];
@@ -788,8 +846,8 @@ __global__ __launch_bounds__(kTreeBlock, tree_waves(DP)) void tree_attention_ker
             }
             if (r0 + kJoin < R) lds_barrier();
         }
-        if (__builtin_expect(sh.odd, 0))
-            tree_add_odd<T>(a, sh.mask, span, b, h, from * kTreeTile, keys_end, whole, slot,
+        if (__builtin_expect(sh.odd.to > 0, 0))
+            tree_add_odd<T>(a, sh.mask, sh.odd, span, b, h, from * kTreeTile, keys_end, whole, slot,
                             mt * 16 * R, 16 * R);
         tile += to - from;
         first += nt;
@@ -878,7 +936,7 @@ struct TreeWideShared {
     v4u32 tile[2][2][tree_wide_keys<DP>() * DP / 8];  // [stage][keys, values]
     uint64_t mask[kMaxTreeNodes][2];
     int up[kMaxTreeNodes];
-    int odd;
+    TreeOdd odd;
 };
 
 // ONCE: no other workgroup reads the same keys.
@@ -961,7 +1019,7 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
         const int begin = from * kTreeTile;
 
         lds_barrier();
-        if (tid == 0) sh.odd = 0;
+        if (tid == 0) sh.odd.clear();
         if (keys_end > span.cached && !chain) tree_masks(a, sh, b, span.live);
 
         // wave w's tile r is the workgroup's tile 4 r + w
@@ -1040,7 +1098,7 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
                 }
                 sh.tile[stage][1][k * kTreeBlock + tid] = v;
             }
-            if (odd) sh.odd = 1;
+            if (odd) sh.odd.add(p0, kKeys);
         };
         constexpr int kBlocks = kKeys / kTreeKeys;
         // a wave whose rows are not in use only loads, and one that has only its
@@ -1261,8 +1319,8 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
                                        : -__builtin_inff();
             }
         }
-        if (__builtin_expect(sh.odd, 0))
-            tree_add_odd<T>(a, sh.mask, span, b, h, begin, keys_end, whole, slot, mt * kTile,
+        if (__builtin_expect(sh.odd.to > 0, 0))
+            tree_add_odd<T>(a, sh.mask, sh.odd, span, b, h, begin, keys_end, whole, slot, mt * kTile,
                             kTile);
         tile += to - from;
         first += nt;

@@ -1,0 +1,105 @@
+"""Infinities and NaN among the new tokens' values: each reaches the nodes that see it
+and no other, along chains of any length, and costs a call little."""
+import pytest
+import torch
+
+import test_gpu_tree as tree
+from oracle import cache_ref as ref
+
+pytestmark = pytest.mark.gpu
+BF16, F16, F32 = tree.BF16, tree.F16, tree.F32
+INF, NAN = float("inf"), float("nan")
+
+
+def put(c, b, node, head, d, value):
+    p = int(c["lengths"][b]) + node
+    c["values"][c["table"][b, p // c["values"].shape[2]].item(), head,
+                p % c["values"].shape[2], d] = value
+
+
+def check(c):
+    clean = dict(c, values=torch.where(torch.isfinite(c["values"]), c["values"], 0.0))
+    good = ref.tree_attention(clean["q"], clean["keys"], clean["values"], clean["table"],
+                              clean["lengths"], clean["parents"], clean["num_nodes"])
+    want = ref.tree_attention(c["q"], c["keys"], c["values"], c["table"], c["lengths"],
+                              c["parents"], c["num_nodes"])[0]
+    t_out, _ = tree.tolerances(c["q"].dtype, c["q"].shape[3], *good)
+    out = tree.call(tree.on_gpu(c), lse=True)[0].cpu().double()
+    finite = torch.isfinite(want)
+    assert not finite.all() and finite.any()
+    assert torch.equal(torch.isfinite(out), finite)
+    assert torch.equal(out.isnan(), want.isnan())
+    inf = want.isinf()
+    assert torch.equal(out[inf], want[inf])
+    assert ((out - good[0]).abs() <= t_out)[finite].all()
+
+
+# T, H, kv, D, page, cached
+CHAINS = [(300, 2, 1, 64, 16, 3), (300, 3, 1, 128, 8, 200), (140, 10, 2, 80, 32, 61),
+          (70, 4, 4, 256, 16, 130), (40, 7, 1, 128, 16, 700), (200, 16, 1, 8, 64, 1000),
+          (9, 4, 1, 96, 16, 45)]
+
+
+@pytest.mark.parametrize("dt", [BF16, F16, F32])
+@pytest.mark.parametrize("T,H,kv,D,page,cached", CHAINS)
+def test_chains(dt, T, H, kv, D, page, cached):
+    """A NaN, infinities of one sign and of both, in different dimensions."""
+    c = tree.make(T + D, dt, 2, T, H, kv, D, page, cached, cached + 20, garbage=1.0)
+    c["num_nodes"] = torch.tensor([T, max(1, T - 5)], dtype=torch.int32)
+    for b in range(2):
+        put(c, b, T // 3, 0, 1, NAN)
+        put(c, b, T // 2, kv - 1, 2, INF)
+        put(c, b, T // 2, kv - 1, 5, -INF)
+        put(c, b, T // 4, 0, 3, INF)
+        put(c, b, T - 7, 0, 3, -INF)
+        put(c, b, 0, 0, 7, -INF)
+        put(c, b, T - 1, kv - 1, D - 1, INF)
+    check(c)
+
+
+@pytest.mark.parametrize("dt", [BF16, F16, F32])
+@pytest.mark.parametrize("cached", [20, 600])
+def test_trees(dt, cached):
+    c = tree.make(3, dt, 2, 100, 4, 2, 128, 16, cached, cached + 20, tree=True, garbage=1.0)
+    for b in range(2):
+        for node, head, d, value in ((3, 0, 1, NAN), (10, 1, 2, INF), (12, 1, 2, INF), (5, 0, 3, INF),
+                                     (40, 0, 3, -INF), (1, 0, 4, INF), (2, 0, 4, -INF),
+                                     (70, 1, 127, -INF), (99, 0, 6, INF)):
+            put(c, b, node, head, d, value)
+    check(c)
+
+
+def test_a_missing_page_holds_no_infinity():
+    c = tree.make(4, BF16, 1, 100, 2, 1, 64, 16, 40, 40, garbage=1.0)
+    put(c, 0, 50, 0, 1, INF)
+    put(c, 0, 3, 0, 2, INF)
+    c["table"][0, (40 + 50) // 16] = -1
+    check(c)
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("where", [(2048,), (0, 4095), range(4096)])
+def test_they_cost_a_long_chain_little(dt, where):
+    """Each node's value is looked at a few times, not once for every row: 4096 of them
+    took 17 ms that way, and should add less than 3."""
+    T, H, kv, D, page = 4096, 4, 2, 128, 16
+    g = torch.Generator().manual_seed(1)
+    keys, values = (torch.randn(T // page, kv, page, D, generator=g).to(dt).cuda() for _ in range(2))
+    q = torch.randn(1, T, H, D, generator=g).to(dt).cuda()
+    table = torch.arange(T // page, dtype=torch.int32)[None].cuda()
+    none = torch.zeros(1, dtype=torch.int32, device="cuda")
+    odd = values.clone()
+    for p in where:
+        odd[p // page, :, p % page] = INF
+
+    def best(v):
+        times = []
+        for _ in range(6):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            tree.sv.tree_attention(q, keys, v, table, none)
+            b.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(b))
+        return min(times)
+    assert best(odd) < best(values) + 3.0
