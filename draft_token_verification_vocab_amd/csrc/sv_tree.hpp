@@ -1329,6 +1329,18 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
     }
 }
 
+// A part times its factor.  A factor that is 0 only in 32 bits leaves infinities and
+// NaNs what they are, as a weight within a part does.
+__device__ __forceinline__ v4f32 tree_scaled(v4f32 p, float f) {
+    v4f32 v = p * f;
+    if (f == 0.0f) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            v[t] = __builtin_fabsf(p[t]) < __builtin_inff() ? 0.0f : p[t];
+    }
+    return v;
+}
+
 // Joins the parts of the rows of sequences that were cut.  A wave takes NR rows of
 // a sequence; its lanes take the parts' references and sums, then 64 / L parts at
 // a time, L lanes to a part's dimensions.  Everything that depends on nothing read
@@ -1411,6 +1423,20 @@ __global__ __launch_bounds__(kTreeBlock) void tree_join_kernel(TreeArgs a, int r
                     v += *reinterpret_cast<const v4f32 *>(a.part + (at0[r] + k * step) * a.D + d) *
                          fk;
             }
+        // a NaN may be an infinite part times a factor that is 0: once more, with care
+        const float all = v[0] + v[1] + v[2] + v[3];
+        if (__builtin_expect(__any(all != all), 0)) {
+            v = v4f32{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int k0 = 0; k0 < n; k0 += kAt) {
+                if (k0 % kWave == 0) f = hw_exp2(ml_of(k0 + lane)[0] - ref);
+                const int k = k0 + lane / L;
+                const float fk = __shfl(f, k & (kWave - 1), kWave);
+                if (k < n && d < a.D)
+                    v += tree_scaled(*reinterpret_cast<const v4f32 *>(
+                                         a.part + (at0[r] + k * step + (k ? 0 : rows16)) * a.D + d),
+                                     fk);
+            }
+        }
         for (int o = 1; o < n && o < kWave; o <<= 1) {
             sum += __shfl_xor(sum, o, kWave);
             norm += __shfl_xor(norm, o, kWave);

@@ -103,3 +103,21 @@ def test_they_cost_a_long_chain_little(dt, where):
             times.append(a.elapsed_time(b))
         return min(times)
     assert best(odd) < best(values) + 3.0
+
+
+@pytest.mark.parametrize("dt", [BF16, F16, F32])
+@pytest.mark.parametrize("cached", [100, 2560, 20480])
+@pytest.mark.parametrize("value", [INF, -INF, NAN])
+def test_of_a_weight_too_small_for_32_bits(dt, cached, value):
+    """The nodes' scores lie 300 below the cached positions', whole or in a part of their own
+    of a sequence that is cut: their weights are above 0 and stay so."""
+    c = tree.make(9, dt, 1, 2, 2, 1, 64, 16, cached, cached, garbage=1.0)
+    c["q"][:], c["keys"][:] = 0.0, 0.0
+    c["q"][..., 0] = 8.0
+    for p in range(cached):
+        c["keys"][c["table"][0, p // 16].item(), :, p % 16, 0] = 300.0
+    put(c, 0, 1, 0, 5, value)
+    out = tree.call(tree.on_gpu(c)).cpu().double()
+    assert torch.isfinite(out[0, 0]).all() and torch.isfinite(out[0, 1, :, :5]).all()
+    for got in out[0, 1, :, 5]:
+        assert got.isnan() if value != value else got == value
