@@ -22,8 +22,8 @@ constexpr int kMaxAcceptNodes = 128;
 // ---------------------------------------------------------------------------
 // Appending: a thread per 16 bytes of a node's head, keys and values together, so
 // that both matrices' loads are in flight at once and the page is looked up once.
-// Five nodes of a sequence 2.2 us (a launch), eight pieces of a prompt of 301 to
-// 512 nodes 5.8 us, 27 MB read and written (4.6 TB/s): memory.
+// Five nodes of a sequence 2.1 us (a launch), eight pieces of a prompt of 301 to
+// 512 nodes 5.7 us, 27 MB read and written (4.6 TB/s): memory.
 // ---------------------------------------------------------------------------
 struct AppendArgs {
     const char *k, *v;
@@ -61,7 +61,7 @@ __global__ __launch_bounds__(kCacheBlock) void cache_append_kernel(AppendArgs a)
 // Accepting a path: a wave per sequence, two nodes to a lane.  A step compares
 // every node's parent and token at once and takes the lowest that fits, so a
 // sequence costs its accepted length, not its nodes.  Eight nodes 1.5 us, 256 trees
-// of 64 nodes 3.4 us: a step's latency (a ballot and two lane reads).
+// of 64 nodes 3.2 us: a step's latency (a ballot and two lane reads).
 // ---------------------------------------------------------------------------
 struct AcceptArgs {
     const int32_t *parents, *tokens, *chosen, *nodes;
@@ -115,7 +115,7 @@ __global__ __launch_bounds__(kCacheBlock) void tree_accept_kernel(AcceptArgs a) 
 // Moving accepted positions together, in place.  The path ascends, so position
 // i is never the source of a later move than its own: a thread that owns 16
 // bytes of a head's slots moves them in order, four loads before their stores,
-// and no other thread touches them.  Four pools of a sequence 2.3 us, eight pools of
+// and no other thread touches them.  Four pools of a sequence 2.2 us, eight pools of
 // 256 trees of 64 nodes 6.8 us: four reads that wait for each other (path, lengths
 // and table, the slots' own) and then memory.
 // ---------------------------------------------------------------------------
@@ -192,7 +192,7 @@ __global__ __launch_bounds__(kCacheBlock) void cache_keep_kernel(KeepArgs a) {
 
 // ---------------------------------------------------------------------------
 // Copying pages: a workgroup per row, pool and head, whose slots lie together.  Four
-// branches 3.0 us, 512 in eight pools, 134 MB read and written, 23.4 us (5.7 TB/s):
+// branches 3.0 us, 512 in eight pools, 134 MB read and written, 23.7 us (5.7 TB/s):
 // memory.
 // ---------------------------------------------------------------------------
 struct CopyArgs {
@@ -219,8 +219,8 @@ __global__ __launch_bounds__(kCacheBlock) void pages_copy_kernel(CopyArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Sharing and releasing: a workgroup per table row, a thread per entry.  Four rows 2.2
-// us, 512 rows 4.9 us: the counts' atomics, which eight branches of a sequence
+// Sharing and releasing: a workgroup per table row, a thread per entry.  Four rows 2.1
+// us, 512 rows 3.6 to 4.2: the counts' atomics, which eight branches of a sequence
 // send to the same places.
 // ---------------------------------------------------------------------------
 struct ForkArgs {
@@ -282,10 +282,10 @@ __global__ __launch_bounds__(kCacheBlock) void pages_release_kernel(ReleaseArgs 
 // the row does so more than once.
 //
 // Where the rows fit the workgroup, an entry to a thread (a step of decoding),
-// entries stay in registers (four rows in 4096 pages 7.3 us, 512 rows in 40000 pages
-// 4.7 us for the first launch and 11.6: barriers and atomics that wait for each
-// other in one workgroup; through the table the same 512 rows took 23); otherwise shared ones are marked in the table
-// (kSharedMark + page) until they are settled.
+// entries stay in registers (four rows in 4096 pages 6.9 us, 512 rows in 40000 pages
+// 3.9 us for the first launch and 11.5: barriers and atomics that wait for each
+// other in one workgroup; through the table the same 512 rows took 23); otherwise
+// shared ones are marked in the table (kSharedMark + page) until they are settled.
 // ---------------------------------------------------------------------------
 constexpr int kReserveBlock = 1024;
 constexpr int kPageChunk = 1024;                   // pages to a count

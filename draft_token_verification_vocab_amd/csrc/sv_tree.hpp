@@ -24,23 +24,25 @@
 // Two kernels: tree_wide_kernel for 16-bit types, where rows are shared out to the
 // waves and keys come through shared memory, and tree_attention_kernel for
 // float32, where keys are shared out to the waves and come straight into
-// registers (a tile of float32 keys and values takes twice the shared memory, and
-// its products a 16th of the rate, so nothing waits for loads).
+// registers (a tile of float32 keys and values takes twice the shared memory, for
+// products of a 16th of the rate).
 //
 // The keys of all sequences are cut into tiles of 128 and the tiles dealt out
-// evenly to as many workgroups as the chip holds: a workgroup takes a run of
-// tiles, which may end inside a sequence and hold several short ones, so ragged
-// batches load every workgroup alike.  More, smaller runs were slower (1.5, 2 and 3
+// evenly to as many workgroups as the chip holds, rounded up: a workgroup takes a
+// run of tiles, which may end inside a sequence and hold several short ones, so
+// ragged batches load every workgroup alike.  More, smaller runs were slower (1.5, 2 and 3
 // times as many).  A sequence whose tiles are in several workgroups is joined by a
 // second launch.  Where every sequence is short, a workgroup takes a whole one
 // and there is none.
 //
-// Measured (kernel + join): 64 single tokens over up to 4000 positions, 552 MB,
-// 88.7 + 4.8 us (6.2 TB/s); 64 chains of nine over up to 8000, 1.19 GB, 201 + 11
-// (5.9 TB/s); two caches of 131072, 1.03 GB, 167 + 8.7 (6.2 TB/s): memory.  16
-// trees of 64 nodes, 64 heads, over up to 12000 positions, 225 GFLOP, 290 + 26
-// (776 TFLOP/s in the main kernel): the exponentials' and conversions' issue
-// beside the products.
+// Measured (kernel + join, medians of traces of 60 calls): 64 single tokens over up to
+// 4000 positions, 552 MB, 90.4 + 4.8 us (6.1 TB/s); 64 chains of nine over up to 8000,
+// 1.19 GB, 203 + 12 (5.9 TB/s); two caches of 131072, 1.03 GB, 173 + 10.8 (5.9 TB/s):
+// memory.  16 trees of 64 nodes, 64 heads, over up to 12000 positions, 225 GFLOP, 321 +
+// 28 (702 TFLOP/s in the main kernel; the fastest call 290 + 25, and 309 to 322 for both
+// without a trace): the exponentials' and conversions' issue beside the products, and
+// shared memory, of which each wave reads a whole tile for 32 rows: four waves' 128 KB
+// to 64 keys take as many cycles at 128 bytes as their products at the full rate.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -488,8 +490,12 @@ constexpr int tree_waves(int dp) { return dp == 64 ? 2 : 1; }
 // join through shared memory at the end.  Two row tiles to a wave halve what is
 // loaded for a row; at 256 dimensions their registers would leave nothing for loads
 // in flight (64 nodes, 774 us against 735 with one).  13 nodes of five sequences of
-// up to 1500 positions, 80 dimensions: 16.3 us (and 4.0 joined), latency; trees of
-// 64 nodes over 128 dimensions reach 76 TFLOP/s of the 137 of a large product.
+// up to 1500 positions, 80 dimensions: 16.6 us (and 4.0 joined), a chain of dependent
+// reads, products (80 dimensions computed as 128, 39 rows as 64) and the waves' join.
+// 16 trees of 64 nodes, 32 heads on 8, over 2000 to 4000 positions reach 71, 85 and 37
+// TFLOP/s at 64, 128 and 256 dimensions of the 137 of a large product: with one wave to
+// a SIMD (two at 64) nothing else fills the time of exponentials and late loads, and at
+// 256 a block of keys and values feeds 16 rows alone.
 // FULL: a slot has DP elements and the next one follows it, so that the
 // loads of a block share their addresses; otherwise fewer than DP or further apart.
 template <int DP, int R, bool FULL>
@@ -894,7 +900,9 @@ constexpr int kTreeArith = 0x406;
 // it (shared memory needs none on this architecture; tests/test_isa_hazards.py looks).
 template <bool ONCE>
 __device__ __forceinline__ void tree_load_lds(const void *p, uint32_t at, uint32_t lds) {
-    if (ONCE)  // past the caches' usual order: 161 us against 180, 319 against 358
+    // past the caches' usual order, the pass: 64 single tokens over up to 4000 positions
+    // 94.2 us against 108.4, two caches of 131072 175.5 against 195.0
+    if (ONCE)
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt"
                      :
                      : "s"(lds), "v"(at), "s"(p)
@@ -949,8 +957,8 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
     constexpr int kSteps = DP / 32, kCols = DP / 16, kRow = DP / 8;
     constexpr int kLoads = kKeys * kRow / kTreeBlock;  // chunks per thread and matrix
     constexpr int kTile = 64 * R;                      // rows of a workgroup
-    // with few rows following every maximum costs nothing that shows (64 single
-    // tokens 161.1 us, 160.5 with slack)
+    // with few rows following every maximum costs next to nothing (64 single tokens
+    // over up to 4000 positions 94.2 us, 93.8 with slack)
     constexpr float kSlack = R == 1 ? 0.0f : kTreeSlack;
     // how far the reference lies below the largest score at the time
     constexpr float kLift = E::kTop > 0.0f ? E::kTop - kSlack : 0.0f;
@@ -1320,8 +1328,8 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
             }
         }
         if (__builtin_expect(sh.odd.to > 0, 0))
-            tree_add_odd<T>(a, sh.mask, sh.odd, span, b, h, begin, keys_end, whole, slot, mt * kTile,
-                            kTile);
+            tree_add_odd<T>(a, sh.mask, sh.odd, span, b, h, begin, keys_end, whole, slot,
+                            mt * kTile, kTile);
         tile += to - from;
         first += nt;
         ++b;
@@ -1330,7 +1338,7 @@ __global__ __launch_bounds__(kTreeBlock, (DP <= 128 ? 2 : 1)) void tree_wide_ker
 }
 
 // A part times its factor.  A factor that is 0 only in 32 bits leaves infinities and
-// NaNs what they are, as a weight within a part does.
+// NaNs what they are, as a node's weight within a part does.
 __device__ __forceinline__ v4f32 tree_scaled(v4f32 p, float f) {
     v4f32 v = p * f;
     if (f == 0.0f) {

@@ -634,7 +634,8 @@ typedef struct spec_cache {
  *   out = sum_p e^(s_p - lse) v_p,  s_p = scale q.k_p,  lse = ln sum_p e^s_p
  * over key head g's cached positions and node i's own and its ancestors'
  * positions (spec_cache_append writes them first).  Keys, values or scores of
- * positions that a node does not see do not enter, whatever they hold.
+ * positions that a node does not see do not enter, whatever they hold; a value
+ * that is not finite makes the outputs of the nodes that see it not finite.
  *   q        device, elements of cache->dtype: node i's head h of sequence b
  *            starts at q + b*q_batch_stride + i*q_node_stride + h*q_head_stride
  *            (elements; multiples of 16 bytes, >= 0; q 16-byte aligned).
@@ -773,8 +774,8 @@ spec_status spec_pages_release(int32_t *table, const int32_t *lengths, int32_t r
  * positions pass its table row; then nothing is taken or changed and copies
  * are (-1, -1, 0), but that an entry below -2^31 + num_pages may become -1.
  * workspace: device, spec_pages_reserve_workspace_bytes,
- * 16-byte aligned; its contents on entry do not matter.  rows <= 65536, else
- * SPEC_ERR_UNSUPPORTED.
+ * 16-byte aligned; its contents on entry do not matter.  rows <= 65536 and
+ * num_pages <= 2^22, else SPEC_ERR_UNSUPPORTED.
  */
 size_t spec_pages_reserve_workspace_bytes(int32_t rows, int32_t num_pages);
 spec_status spec_pages_reserve(int32_t *table, const int32_t *lengths,
