@@ -1177,8 +1177,9 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, keys: torch.Tensor, values: t
                  num_nodes: Optional[torch.Tensor] = None):
     """Write the nodes' keys and values, k and v [B, T, heads, dim] (strided alike),
     to the positions lengths[b] + j of their sequences' pages, for the first
-    num_nodes[b] nodes (None: T).  Positions without a page are left out.  Returns
-    (keys, values), the pools written."""
+    num_nodes[b] nodes (None: T).  Positions without a page are left out.  The pools
+    share no memory with each other or with anything else given.  Returns (keys,
+    values), the pools written."""
     c, index = _cache(keys, values, table, lengths)
     strides = _need_rows(k, "k", index, keys, c.batch, c.kv_heads)
     if not (v.stride() == k.stride() and v.shape == k.shape and v.dtype is k.dtype
@@ -1254,7 +1255,8 @@ def _pools(pools, index):
 def cache_keep(pools, table: torch.Tensor, lengths: torch.Tensor, path: torch.Tensor,
                count: torch.Tensor) -> torch.Tensor:
     """Move the accepted nodes' positions together in every pool (tensors [pages,
-    heads, page, dim] of one layout, all layers' keys and values): position
+    heads, page, dim] of one layout that share no memory, all layers' keys and
+    values; views between each other's pages or slots will do): position
     lengths[b] + path[b, i] to lengths[b] + i for i < count[b] (path and count as
     tree_accept gives them).  Returns the new lengths, int32 [B]."""
     pools = list(pools)
