@@ -1,9 +1,12 @@
-"""The pages' bookkeeping where a table lists a page more than once in a row, against
-the plain definitions; results are equal."""
+"""The pages' bookkeeping where a table lists a page more than once in a row, and pools
+that lie in one tensor, against the plain definitions; results are equal."""
 import numpy as np
 import pytest
+import torch
 
-from test_gpu_cache import check_reserve
+import draft_token_verification_vocab_amd as sv
+from oracle import cache_ref as ref
+from test_gpu_cache import check_reserve, i32, paged
 
 pytestmark = pytest.mark.gpu
 
@@ -45,3 +48,30 @@ def test_reserve_of_one_page_in_two_entries():
     wide = [5, 5] + 1500 * [-1]
     got = check_reserve([wide], [3], [0] * 5 + [2] + [0] * 2000, page, [13 + 1400 * page])
     assert got[0][0, :3].tolist() == [5, 0, 1] and got[1][5] == 1
+
+
+@pytest.mark.parametrize("axis", [0, 1, 3])
+def test_pools_between_each_others_elements(axis):
+    """All layers' pools in one tensor: in turn, within each page, or within each slot.
+    Appending, keeping and copying move what they should and nothing else."""
+    g = torch.Generator().manual_seed(axis)
+    layers, N, kv, page, D, B, T = 6, 12, 2, 8, 16, 3, 5
+    pools = [torch.randn(N, kv, page, D, generator=g) for _ in range(layers)]
+    stacked = torch.stack(pools, dim=axis).cuda()
+    views = list(stacked.unbind(axis))
+    table, lengths = paged(g, B, N, 4, page, 25)
+    path, counts = i32([[0, 2, 3, -1, -1], [1, 4, -1, -1, -1], [0, 1, 2, 3, 4]]), i32([3, 2, 5])
+    k, v = (torch.randn(B, T, kv, D, generator=g) for _ in range(2))
+    pools[2], pools[3] = ref.cache_append(k, v, pools[2], pools[3], table, lengths)
+    sv.cache_append(k.cuda(), v.cuda(), views[2], views[3], table.cuda(), lengths.cuda())
+    pools, new = ref.cache_keep(pools, table, lengths, path, counts)
+    got = sv.cache_keep(views, table.cuda(), lengths.cuda(), path.cuda(), counts.cuda())
+    assert got.tolist() == new
+    copies = i32([[0, 1, 5], [2, 3, 8], [4, 5, 0]])
+    pools = ref.pages_copy(pools, copies)
+    sv.pages_copy(views, copies.cuda())
+    assert torch.equal(stacked.cpu(), torch.stack(pools, dim=axis))
+    # one of them once more, and one that reaches into the next
+    for more in (views[0], stacked.flatten()[16:].as_strided(views[0].shape, views[0].stride())):
+        with pytest.raises((ValueError, sv.SpecVerifyError)):
+            sv.cache_keep(views + [more], table.cuda(), lengths.cuda(), path.cuda(), counts.cuda())
